@@ -413,6 +413,134 @@ LMC_API int lmc_load_blocks_q8(const lmc_layout *layout, int64_t blocks_per_obje
 LMC_API int lmc_object_bytes_blocks_q8(const lmc_layout *layout, int64_t blocks_per_object, int32_t kda_mode,
                                        int64_t row_elems, int32_t object_group, int64_t *out);
 
+/* ---- token entries of paged layers ---------------------------------------- */
+
+/* The calls below read and write single tokens' entries of a paged (MLA or
+ * SWA) layer: entry t of a request lies in block position t / N of the
+ * layer's KV group, at row t % N of the layer's page ([VB] §4.2: the view
+ * (num_blocks, block_size, kv_lora_rank + qk_rope_head_dim)). An entry is
+ * entry_dim values of one of these types; entry_dim * (bytes per value) must
+ * equal the layer's token_bytes. */
+#define LMC_E_BF16 0 /* bfloat16 */
+#define LMC_E_F16 1  /* IEEE binary16 */
+#define LMC_E_E4M3 2 /* fp8 e4m3 (no infinities), value = code * scale */
+
+/* One paged layer's entries of a batch of requests. */
+typedef struct {
+    int32_t layer;         /* an MLA or SWA layer of the layout */
+    int32_t dtype;         /* LMC_E_*: how the pages hold the values */
+    int32_t entry_dim;     /* values per token */
+    int32_t num_requests;  /* rows of the block table */
+    float scale;           /* LMC_E_E4M3: finite and > 0; else 1 */
+    int32_t reserved;      /* set to 0 */
+    lmc_block_table table; /* device block table of the layer's KV group */
+} lmc_entries;
+
+/* Append: row i of `rows` becomes the entry at position positions[i] of
+ * request requests[i] (the new tokens of a prefill or a decode step). Rows
+ * are entry_dim values of rows_dtype (LMC_E_BF16 or LMC_E_F16), row_stride
+ * elements apart. 16-bit entries must have the rows' type and are copied;
+ * an LMC_E_E4M3 entry holds code = e4m3(clamp(value / scale, -448, 448)),
+ * quotient in binary32, rounded half to even (NaN stays NaN). A row whose
+ * request is -1 is skipped (padding of a fixed-size batch). Other bytes of
+ * the pool are left as they were. Rows of one call that name the same place
+ * race: that entry then mixes theirs.
+ * requests, positions: device int32 [num_rows]. Status: BAD_JOB (request or
+ * position out of range), NO_BLOCK, BLOCK_OOR; such rows are skipped.
+ * Errors: INVALID_ARG, ALIGN, CUDA. */
+LMC_API int lmc_append(const lmc_layout *layout, const lmc_entries *entries, void *pool, const int32_t *requests,
+                       const int32_t *positions, const void *rows, int32_t rows_dtype, int64_t row_stride,
+                       int64_t num_rows, uint32_t *status, void *stream);
+
+/* Attention of one new token per request over the layer's pages: the query's
+ * heads share one entry per token (the latent form of MLA), whose first
+ * value_dim values are also the value. For request r of length L = lengths[r]
+ * and head h, over the tokens t of [max(0, L - window), L) (window: the
+ * layer's, 0 for MLA):
+ *   x_t = softmax_scale * q[r][h] . entry_t,   p = softmax(x),
+ *   out[r][h] = sum_t p_t * entry_t[0 .. value_dim),
+ *   lse[r][h] = log(sum_t exp(x_t))            (if lse is not NULL),
+ *   weights[r][t] += sum_h p_t                 (if weights is not NULL).
+ * A request of length 0 gives out = 0 and lse = -inf. Tokens of a missing
+ * block are left out of the sums, with a status bit; a request whose tokens
+ * are all missing gives out = 0, lse = -inf. Nothing outside the range is
+ * read into a result, whatever its bytes. (out, lse) of disjoint parts of a
+ * cache can be joined by their lse. */
+typedef struct {
+    const int32_t *lengths;  /* device [num_requests] */
+    int64_t max_length;      /* no length is above it (>= 1); it sizes the work
+                                space, not the work */
+    const void *q;           /* device [num_requests][num_heads][entry_dim], 16-byte
+                                aligned, strides multiples of 8 elements */
+    int64_t q_request_stride; /* elements */
+    int64_t q_head_stride;
+    void *out;               /* device [num_requests][num_heads][value_dim], of q's type */
+    int64_t out_request_stride;
+    int64_t out_head_stride;
+    float *lse;              /* device [num_requests][num_heads], or NULL */
+    int64_t lse_request_stride;
+    float *weights;          /* device [num_requests][>= max_length], or NULL */
+    int64_t weights_request_stride;
+    int32_t q_dtype;         /* LMC_E_BF16 or LMC_E_F16; the entries' type where they
+                                are of 16 bits */
+    int32_t num_heads;       /* >= 1 */
+    int32_t value_dim;       /* a multiple of 8, <= entry_dim and <= 512 */
+    float softmax_scale;     /* finite */
+} lmc_attention;
+
+/* Entries: entry_dim a multiple of 16, at most 576; the layer's base, stride
+ * and the pool 16-byte aligned. `workspace` is device memory of at least
+ * lmc_attend_workspace bytes, 256-byte aligned; its content does not matter
+ * and calls that may run at the same time each need their own. Asynchronous
+ * on `stream`; results do not depend on anything but the arguments (repeated
+ * calls give the same bits). Status: BAD_JOB (a length below 0, above
+ * max_length or past the table: that request's rows of out, lse and weights
+ * are left as they were), NO_BLOCK, BLOCK_OOR, TIMEOUT.
+ * Errors: INVALID_ARG, ALIGN, OVERFLOW, CUDA. */
+LMC_API int lmc_attend(const lmc_layout *layout, const lmc_entries *entries, const void *pool,
+                       const lmc_attention *attention, void *workspace, int64_t workspace_bytes, uint32_t *status,
+                       void *stream);
+
+/* Bytes of lmc_attend's workspace for a batch (with_weights: the call is
+ * given a weights buffer). */
+LMC_API int lmc_attend_workspace(const lmc_layout *layout, int32_t layer, int32_t num_requests, int32_t num_heads,
+                                 int32_t value_dim, int64_t max_length, int with_weights, int64_t *out);
+
+/* Select: which tokens a request keeps when its cache is cut to `budget`
+ * tokens, by their accumulated attention weight (lmc_attend's weights). Per
+ * set s (a layer, or one set for all) and request r of length L: all L tokens
+ * where L <= budget; else the last `recent` tokens and, of the others, the
+ * budget - recent of the highest scores[s][r][t] (equal scores: the lowest t
+ * first; NaN below every number, -0 equal to 0). kept[s][r] gets their
+ * positions in increasing order, kept_scores[s][r] (if not NULL) their
+ * scores, kept_lengths[r] = min(L, budget); elements of kept past that are
+ * left as they were. scores: device, strides in elements between sets and
+ * requests (no length is above max_length); kept, kept_scores: device
+ * [num_sets][num_requests][budget], contiguous; 0 <= recent <= budget.
+ * Status: BAD_JOB (a length below 0 or above max_length: nothing is written
+ * for that request). Errors: INVALID_ARG, ALIGN, CUDA. */
+LMC_API int lmc_select_tokens(const float *scores, int64_t set_stride, int64_t request_stride, int32_t num_sets,
+                              int32_t num_requests, const int32_t *lengths, int64_t max_length, int64_t budget,
+                              int64_t recent, int32_t *kept, float *kept_scores, int32_t *kept_lengths,
+                              uint32_t *status, void *stream);
+
+/* Move: gathers the kept tokens of a paged KV group into other blocks. For
+ * every layer of the group, every request r and j < kept_lengths[r], the
+ * entry at position kept[s][r][j] under `src` is copied to position j under
+ * `dst` (s: the layer's index in the group where num_sets is the group's
+ * layer count, 0 where num_sets is 1). Strides of kept in elements;
+ * kept_lengths: device [num_requests], each at most max_kept. The blocks
+ * named by `dst` must not be among those read (a load's fresh blocks): a call
+ * given one table as both is refused (LMC_ERR_OVERLAP), other overlaps race.
+ * Other bytes are left as they were. Status: BAD_JOB (kept_lengths[r] outside
+ * [0, max_kept]: the request is skipped; a kept position or j outside its
+ * table), NO_BLOCK, BLOCK_OOR; such entries are skipped.
+ * Errors: INVALID_ARG, ALIGN, OVERLAP, CUDA. */
+LMC_API int lmc_move_tokens(const lmc_layout *layout, int32_t kv_group, void *pool, int32_t num_requests,
+                            const lmc_block_table *src, const lmc_block_table *dst, const int32_t *kept,
+                            int32_t num_sets, int64_t set_stride, int64_t request_stride, const int32_t *kept_lengths,
+                            int64_t max_kept, uint32_t *status, void *stream);
+
 /* ---- diagnostics ----------------------------------------------------------- */
 
 /* Self-test of the device-side failure reporting: launches one thread that

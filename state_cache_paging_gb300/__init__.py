@@ -48,6 +48,10 @@ LMC_BK_PACKED_STATE = 0x4
 LMC_KDA_LAST_BLOCK = 0
 LMC_KDA_EVERY_BLOCK = 1
 
+LMC_E_BF16 = 0
+LMC_E_F16 = 1
+LMC_E_E4M3 = 2
+
 LMC_LAYER = {"MLA": 0, "KDA": 1, "SWA": 2}
 LMC_LAYER_NAME = {v: k for k, v in LMC_LAYER.items()}
 LMC_MAX_LAYERS = 256
@@ -109,6 +113,21 @@ class lmc_batch(ctypes.Structure):
                 ("num_jobs", ctypes.POINTER(ctypes.c_int64))]
 
 
+class lmc_entries(ctypes.Structure):
+    _fields_ = [("layer", ctypes.c_int32), ("dtype", ctypes.c_int32), ("entry_dim", ctypes.c_int32),
+                ("num_requests", ctypes.c_int32), ("scale", ctypes.c_float), ("reserved", ctypes.c_int32),
+                ("table", lmc_block_table)]
+
+
+class lmc_attention(ctypes.Structure):
+    _fields_ = [("lengths", ctypes.c_void_p), ("max_length", ctypes.c_int64), ("q", ctypes.c_void_p),
+                ("q_request_stride", ctypes.c_int64), ("q_head_stride", ctypes.c_int64), ("out", ctypes.c_void_p),
+                ("out_request_stride", ctypes.c_int64), ("out_head_stride", ctypes.c_int64),
+                ("lse", ctypes.c_void_p), ("lse_request_stride", ctypes.c_int64), ("weights", ctypes.c_void_p),
+                ("weights_request_stride", ctypes.c_int64), ("q_dtype", ctypes.c_int32),
+                ("num_heads", ctypes.c_int32), ("value_dim", ctypes.c_int32), ("softmax_scale", ctypes.c_float)]
+
+
 _P = ctypes.POINTER
 _i64 = ctypes.c_int64
 
@@ -144,6 +163,18 @@ def _bind(so: ctypes.CDLL) -> ctypes.CDLL:
         getattr(so, name).argtypes = [ctypes.c_void_p, _i64, ctypes.c_int32, _i64, ctypes.c_void_p,
                                       _P(lmc_batch), ctypes.c_void_p, _i64, ctypes.c_void_p, ctypes.c_void_p]
     so.lmc_object_bytes_blocks_q8.argtypes = [ctypes.c_void_p, _i64, ctypes.c_int32, _i64, ctypes.c_int32, _P(_i64)]
+    so.lmc_append.argtypes = [ctypes.c_void_p, _P(lmc_entries), ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
+                              ctypes.c_void_p, ctypes.c_int32, _i64, _i64, ctypes.c_void_p, ctypes.c_void_p]
+    so.lmc_attend.argtypes = [ctypes.c_void_p, _P(lmc_entries), ctypes.c_void_p, _P(lmc_attention), ctypes.c_void_p,
+                              _i64, ctypes.c_void_p, ctypes.c_void_p]
+    so.lmc_attend_workspace.argtypes = [ctypes.c_void_p, ctypes.c_int32, ctypes.c_int32, ctypes.c_int32,
+                                        ctypes.c_int32, _i64, ctypes.c_int, _P(_i64)]
+    so.lmc_select_tokens.argtypes = [ctypes.c_void_p, _i64, _i64, ctypes.c_int32, ctypes.c_int32, ctypes.c_void_p,
+                                     _i64, _i64, _i64, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p,
+                                     ctypes.c_void_p, ctypes.c_void_p]
+    so.lmc_move_tokens.argtypes = [ctypes.c_void_p, ctypes.c_int32, ctypes.c_void_p, ctypes.c_int32,
+                                   _P(lmc_block_table), _P(lmc_block_table), ctypes.c_void_p, ctypes.c_int32, _i64,
+                                   _i64, ctypes.c_void_p, _i64, ctypes.c_void_p, ctypes.c_void_p]
     so.lmc_selftest_wait.argtypes = [ctypes.c_void_p, _i64, ctypes.c_void_p]
     so.lmc_selftest_row_scale.argtypes = [ctypes.c_void_p] * 4 + [_i64, ctypes.c_void_p]
     so.lmc_strerror.argtypes = [ctypes.c_int]
@@ -471,6 +502,176 @@ def lmc_load_blocks_q8(layout: Layout, blocks_per_object: int, kda_mode: int, ro
                                    pool.data_ptr(), ctypes.byref(b), arena.data_ptr(),
                                    arena.numel() * arena.element_size(), status.data_ptr(), strm),
            "lmc_load_blocks_q8")
+
+
+# ----------------------------------------------------------------------------
+# Token entries of paged layers
+# ----------------------------------------------------------------------------
+
+def _refuse(what: str):
+    raise LmcError(LMC_ERR_INVALID_ARG, what)
+
+
+def _value_type(t) -> int:
+    """LMC_E_* of a bfloat16 or float16 tensor."""
+    import torch
+    if t.dtype == torch.bfloat16:
+        return LMC_E_BF16
+    if t.dtype == torch.float16:
+        return LMC_E_F16
+    _refuse(f"values must be bfloat16 or float16, not {t.dtype}")
+
+
+def _table(name: str, t) -> lmc_block_table:
+    _visible(name, t)
+    if t.dim() != 2 or t.element_size() != 4 or t.is_floating_point() or (t.shape[1] > 1 and t.stride(1) != 1):
+        _refuse(f"{name} must be int32 [num_requests, cols] with unit column stride")
+    return lmc_block_table(t.data_ptr(), max(int(t.stride(0)), int(t.shape[1])), int(t.shape[1]))
+
+
+def _ints(name: str, t, *shape):
+    """An int32 tensor of `shape`, contiguous."""
+    _visible(name, t)
+    if t.element_size() != 4 or t.is_floating_point() or tuple(t.shape) != shape or not t.is_contiguous():
+        _refuse(f"{name} must be contiguous int32 {list(shape)}")
+    return t.data_ptr()
+
+
+def _status(t):
+    _visible("status", t)
+    if t.numel() * t.element_size() < 4:
+        _refuse("status holds at least 4 bytes")
+    return t.data_ptr()
+
+
+def _entries(layout: Layout, layer: int, pool, table, entry_dim: int, value_type: int, scale: float) -> lmc_entries:
+    """The layer's entries: of `value_type` where its token_bytes hold
+    entry_dim 16-bit values, fp8 e4m3 where they hold entry_dim bytes."""
+    if not 0 <= layer < layout.num_layers:
+        _refuse(f"layer {layer} of {layout.num_layers}")
+    _visible("pool", pool)
+    if pool.numel() * pool.element_size() < layout.pool_bytes or not pool.is_contiguous():
+        _refuse(f"pool must be contiguous and hold the {layout.pool_bytes} bytes the layout addresses")
+    dtype = LMC_E_E4M3 if layout.real_bytes[layer] == layout.block_size * entry_dim else value_type
+    return lmc_entries(layer, dtype, entry_dim, int(table.shape[0]), scale, 0, _table("block table", table))
+
+
+def lmc_append(layout: Layout, layer: int, pool, table, requests, positions, entries, status, scale: float = 1.0,
+               stream=None) -> None:
+    """Writes row i of `entries` ([rows, entry_dim], bfloat16 or float16, any
+    row stride) as the entry at position positions[i] of request requests[i]
+    (int32 device tensors; request -1: skipped) of a paged layer. A layer
+    whose token_bytes equal entry_dim holds fp8 e4m3 codes of value / scale."""
+    if entries.dim() != 2 or (entries.shape[1] > 1 and entries.stride(1) != 1):
+        _refuse("entries must be [rows, entry_dim] with unit column stride")
+    _visible("entries", entries)
+    vt = _value_type(entries)
+    n, dim = int(entries.shape[0]), int(entries.shape[1])
+    e = _entries(layout, layer, pool, table, dim, vt, scale)
+    req, pos = _ints("requests", requests, n), _ints("positions", positions, n)
+    strm = _stream_ptr(stream, pool, table, requests, positions, entries, status)
+    _check(_lib.lmc_append(layout.handle, ctypes.byref(e), pool.data_ptr(), req, pos, entries.data_ptr(), vt,
+                           max(int(entries.stride(0)), dim), n, _status(status), strm), "lmc_append")
+
+
+def lmc_attend_workspace(layout: Layout, layer: int, num_requests: int, num_heads: int, value_dim: int,
+                         max_length: int, weights: bool = False) -> int:
+    """Bytes of lmc_attend's workspace tensor (`weights`: the call is given one)."""
+    out = _i64(0)
+    _check(_lib.lmc_attend_workspace(layout.handle, int(layer), int(num_requests), int(num_heads), int(value_dim),
+                                     int(max_length), int(bool(weights)), ctypes.byref(out)), "lmc_attend_workspace")
+    return out.value
+
+
+def lmc_attend(layout: Layout, layer: int, pool, table, lengths, q, value_dim: int, softmax_scale: float, out,
+               workspace, status, max_length: int | None = None, scale: float = 1.0, lse=None, weights=None,
+               stream=None) -> None:
+    """Attention of one new token per request over a paged layer's entries:
+    q [requests, heads, entry_dim] -> out [requests, heads, value_dim] (both
+    bfloat16 or both float16; the last dimension contiguous). lengths: int32
+    [requests] device tensor, none above max_length (default: what the block
+    table holds). lse (float32 [requests, heads]) receives the log of the sum
+    of exponentials; weights (float32 [requests, >= max_length]) has the sum
+    over the heads of each token's probability added to it."""
+    if q.dim() != 3 or out.dim() != 3 or q.stride(2) != 1 or out.stride(2) != 1 or out.dtype != q.dtype:
+        _refuse("q and out must be [requests, heads, dim] of one type with a contiguous last dimension")
+    _visible("q", q)
+    _visible("out", out)
+    _visible("workspace", workspace)
+    R, H, dim = (int(n) for n in q.shape)
+    if tuple(out.shape) != (R, H, value_dim) or int(table.shape[0]) != R:
+        _refuse(f"out must be [{R}, {H}, {value_dim}] and the block table have {R} rows")
+    vt = _value_type(q)
+    e = _entries(layout, layer, pool, table, dim, vt, scale)
+    if max_length is None:
+        max_length = max(1, int(table.shape[1]) * layout.block_size)
+    a = lmc_attention(_ints("lengths", lengths, R), max_length, q.data_ptr(), q.stride(0), q.stride(1),
+                      out.data_ptr(), out.stride(0), out.stride(1), None, 0, None, 0, vt, H, value_dim,
+                      softmax_scale)
+    for name, t, cols in (("lse", lse, H), ("weights", weights, max_length)):
+        if t is None:
+            continue
+        _visible(name, t)
+        if t.dim() != 2 or not t.is_floating_point() or t.element_size() != 4 or t.shape[0] != R or \
+                t.shape[1] < cols or (t.shape[1] > 1 and t.stride(1) != 1):
+            _refuse(f"{name} must be float32 [{R}, {cols}] with unit column stride")
+    if lse is not None:
+        a.lse, a.lse_request_stride = lse.data_ptr(), max(lse.stride(0), H)
+    if weights is not None:
+        a.weights, a.weights_request_stride = weights.data_ptr(), max(weights.stride(0), max_length)
+    strm = _stream_ptr(stream, pool, table, lengths, q, out, workspace, status, lse, weights)
+    _check(_lib.lmc_attend(layout.handle, ctypes.byref(e), pool.data_ptr(), ctypes.byref(a), workspace.data_ptr(),
+                           workspace.numel() * workspace.element_size(), _status(status), strm), "lmc_attend")
+
+
+def lmc_select_tokens(scores, lengths, budget: int, recent: int, kept, kept_scores, kept_lengths, status,
+                      stream=None) -> None:
+    """Which tokens a request keeps when it is cut to `budget`: the last
+    `recent` and the highest scores of the others. scores: float32 [sets,
+    requests, >= longest length], lengths: int32 [requests]; kept (int32) and
+    kept_scores (float32, or None) [sets, requests, budget] receive the kept
+    positions in increasing order and their scores, kept_lengths (int32
+    [requests]) how many there are."""
+    if scores.dim() != 3 or not scores.is_floating_point() or scores.element_size() != 4 or \
+            (scores.shape[2] > 1 and scores.stride(2) != 1):
+        _refuse("scores must be float32 [sets, requests, tokens] with unit token stride")
+    _visible("scores", scores)
+    S, R, T = (int(n) for n in scores.shape)
+    kept_p = _ints("kept", kept, S, R, budget)
+    if kept_scores is not None:
+        _visible("kept_scores", kept_scores)
+        if not kept_scores.is_floating_point() or kept_scores.element_size() != 4 or \
+                tuple(kept_scores.shape) != (S, R, budget) or not kept_scores.is_contiguous():
+            _refuse(f"kept_scores must be contiguous float32 {[S, R, budget]}")
+    strm = _stream_ptr(stream, scores, lengths, kept, kept_scores, kept_lengths, status)
+    _check(_lib.lmc_select_tokens(scores.data_ptr(), scores.stride(0), scores.stride(1), S, R,
+                                  _ints("lengths", lengths, R), T, int(budget), int(recent), kept_p,
+                                  None if kept_scores is None else kept_scores.data_ptr(),
+                                  _ints("kept_lengths", kept_lengths, R), _status(status), strm),
+           "lmc_select_tokens")
+
+
+def lmc_move_tokens(layout: Layout, kv_group: int, pool, src_table, dst_table, kept, kept_lengths, status,
+                    stream=None) -> None:
+    """Copies, for every layer of a paged KV group, the entries at positions
+    kept[set, request, j] (j < kept_lengths[request]) under `src_table` to
+    positions j under `dst_table`, whose blocks must be others. kept: int32
+    [sets, requests, most], with one set for all layers or one per layer."""
+    _visible("pool", pool)
+    if pool.numel() * pool.element_size() < layout.pool_bytes or not pool.is_contiguous():
+        _refuse(f"pool must be contiguous and hold the {layout.pool_bytes} bytes the layout addresses")
+    _visible("kept", kept)
+    if kept.dim() != 3 or kept.element_size() != 4 or kept.is_floating_point() or \
+            (kept.shape[2] > 1 and kept.stride(2) != 1):
+        _refuse("kept must be int32 [sets, requests, most] with unit last stride")
+    S, R, K = (int(n) for n in kept.shape)
+    src, dst = _table("source table", src_table), _table("destination table", dst_table)
+    if int(src_table.shape[0]) != R or int(dst_table.shape[0]) != R:
+        _refuse(f"the block tables must have {R} rows")
+    strm = _stream_ptr(stream, pool, src_table, dst_table, kept, kept_lengths, status)
+    _check(_lib.lmc_move_tokens(layout.handle, int(kv_group), pool.data_ptr(), R, ctypes.byref(src),
+                                ctypes.byref(dst), kept.data_ptr(), S, kept.stride(0), max(kept.stride(1), K),
+                                _ints("kept_lengths", kept_lengths, R), K, _status(status), strm), "lmc_move_tokens")
 
 
 def lmc_selftest_wait(status, rounds: int, stream=None) -> None:

@@ -24,6 +24,7 @@ LIB_PATH = os.path.join(PKG, "liblmc.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC = os.environ.get("NVCC", "nvcc")
 HOST_UNITS = ("layout", "checks")  # host C++ translation units in csrc/
+CUDA_UNITS = ("paging", "tokens", "attend")  # CUDA translation units in csrc/
 CXX = os.environ.get("CXX", "g++")
 
 
@@ -45,18 +46,19 @@ def _stale(target: str) -> bool:
 
 def build_library(force: bool = False, extra_nvcc=(), out_path: str | None = None, verbose: bool = False) -> str:
     """Compiles and links liblmc.so; returns its path. `extra_nvcc` adds flags
-    (e.g. -D tuning constants) to the CUDA translation unit."""
+    (e.g. -D tuning constants) to the CUDA translation units."""
     out = out_path or LIB_PATH
     if not force and not extra_nvcc and out_path is None and not _stale(out):
         return out
     os.makedirs(BUILD_DIR, exist_ok=True)
     work = tempfile.mkdtemp(dir=BUILD_DIR)  # private per build (builds may run concurrently)
-    cu_obj = os.path.join(work, "paging.o")
+    cu_objs = [os.path.join(work, name + ".o") for name in CUDA_UNITS]
     cpp_objs = [os.path.join(work, name + ".o") for name in HOST_UNITS]
     ptxas_log = os.path.join(BUILD_DIR, "ptxas.log")
     cmds = [
-        [NVCC, "-O3", "-std=c++17", *ARCH, "-lineinfo", "-Xptxas", "-v", "-Xcompiler", "-fPIC,-fvisibility=hidden",
-         "-I", INCLUDE, "-I", CSRC, *extra_nvcc, "-c", os.path.join(CSRC, "paging.cu"), "-o", cu_obj],
+        *[[NVCC, "-O3", "-std=c++17", *ARCH, "-lineinfo", "-Xptxas", "-v", "-Xcompiler", "-fPIC,-fvisibility=hidden",
+           "-I", INCLUDE, "-I", CSRC, *extra_nvcc, "-c", os.path.join(CSRC, name + ".cu"), "-o", obj]
+          for name, obj in zip(CUDA_UNITS, cu_objs)],
         *[[CXX, "-O2", "-std=c++17", "-fPIC", "-fvisibility=hidden", "-Wall", "-Wextra", "-Werror", "-I", INCLUDE,
            "-I", CSRC, "-c", os.path.join(CSRC, name + ".cpp"), "-o", obj]
           for name, obj in zip(HOST_UNITS, cpp_objs)],
@@ -67,12 +69,12 @@ def build_library(force: bool = False, extra_nvcc=(), out_path: str | None = Non
         if p.returncode != 0:
             raise RuntimeError(f"compile failed: {' '.join(c)}\n{log}")
     with open(ptxas_log, "w") as f:
-        f.write(logs[0])
+        f.write("".join(logs[:len(CUDA_UNITS)]))
     if verbose:
-        print(logs[0])
+        print("".join(logs[:len(CUDA_UNITS)]))
     tmp = os.path.join(work, "liblmc.so")
     link = [NVCC, "-shared", *ARCH, "-Xlinker", "--version-script=" + os.path.join(CSRC, "liblmc.map"),
-            "-o", tmp, cu_obj, *cpp_objs]
+            "-o", tmp, *cu_objs, *cpp_objs]
     r = subprocess.run(link, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed: {' '.join(link)}\n{r.stdout}{r.stderr}")

@@ -38,4 +38,23 @@ inline bool add_ok(int64_t a, int64_t b, int64_t *out) { return !__builtin_add_o
 // count and pair counts are checked by the caller.
 int check_copy_pairs(const lmc_layout *L, const lmc_copy_batch *b);
 
+// SMs of the current device (cached per device); -1 when CUDA fails.
+int sm_count();
+
+// Bytes of one value of an entry type (LMC_E_*); 0 for an unknown one.
+inline int entry_elem_bytes(int32_t dtype) {
+    return dtype == LMC_E_BF16 || dtype == LMC_E_F16 ? 2 : dtype == LMC_E_E4M3 ? 1 : 0;
+}
+
+// The rules every call on a layer's token entries shares: the layer is a
+// paged one, its token_bytes hold entry_dim values of the type, the scale and
+// the block table are usable. LMC_OK or LMC_ERR_INVALID_ARG.
+int check_entries(const lmc_layout *L, const lmc_entries *e);
+
+// A block table's geometry, and its pointer where it will be read.
+inline bool table_ok(const lmc_block_table &t, int64_t num_requests) {
+    return t.num_cols >= 0 && t.num_cols <= INT32_MAX && t.row_stride >= t.num_cols &&
+           (num_requests == 0 || t.num_cols == 0 || (t.table != nullptr && ((uintptr_t)t.table & 3) == 0));
+}
+
 }  // namespace lmc

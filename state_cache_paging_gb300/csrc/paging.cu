@@ -65,6 +65,28 @@
 #define LMC_ST_HINT 0  // 0: .cs (evict-first), 1: plain write-back, 2: .L1::no_allocate
 #endif
 
+namespace lmc {
+
+int sm_count() {
+    static std::mutex mu;
+    static std::vector<int> cache;
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess)
+        return -1;
+    std::lock_guard<std::mutex> lock(mu);
+    if ((int)cache.size() <= dev)
+        cache.resize(dev + 1, 0);
+    if (cache[dev] == 0) {
+        int n = 0;
+        if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
+            return -1;
+        cache[dev] = n;
+    }
+    return cache[dev];
+}
+
+}  // namespace lmc
+
 namespace {
 
 constexpr int kMaxEntries = 2 * LMC_MAX_LAYERS;  // layer entries in one launch (a codec KDA layer takes two)
@@ -930,24 +952,6 @@ __global__ void __launch_bounds__(32) lmc_load_bulk_kernel(const __grid_constant
 // Host side
 // ---------------------------------------------------------------------------
 
-int sm_count() {
-    static std::mutex mu;
-    static std::vector<int> cache;
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess)
-        return -1;
-    std::lock_guard<std::mutex> lock(mu);
-    if ((int)cache.size() <= dev)
-        cache.resize(dev + 1, 0);
-    if (cache[dev] == 0) {
-        int n = 0;
-        if (cudaDeviceGetAttribute(&n, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess)
-            return -1;
-        cache[dev] = n;
-    }
-    return cache[dev];
-}
-
 bool aligned16(int64_t x) { return (x & 15) == 0; }
 
 // Appends a layer entry: `pages` pages of `d` per object. The pages lie back
@@ -1135,7 +1139,7 @@ int build_object_plan(const lmc_layout *L, const Shape &sh, const void *pool, co
 int launch_plan(const Plan &P, bool vec, void *stream) {
     if (P.total_tiles == 0)
         return LMC_OK;
-    const int sms = sm_count();
+    const int sms = lmc::sm_count();
     if (sms <= 0)
         return LMC_ERR_CUDA;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
@@ -1393,7 +1397,7 @@ extern "C" int lmc_selftest_row_scale(const float *amax, float *scale, float *in
         return LMC_ERR_ALIGN;
     if (n == 0)
         return LMC_OK;
-    const int sms = sm_count();
+    const int sms = lmc::sm_count();
     if (sms <= 0)
         return LMC_ERR_CUDA;
     const unsigned grid = (unsigned)std::min<int64_t>((n + 255) / 256, (int64_t)sms * 8);

@@ -1,0 +1,698 @@
+// tokens.cu -- single tokens' entries of paged attention layers: appending
+// new entries by block table, selecting the tokens a request keeps by their
+// accumulated attention weight, and moving the kept entries into other
+// blocks, for sm_103a.
+#include <cooperative_groups.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_fp8.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+
+#include "lmc_internal.h"
+
+namespace cg = cooperative_groups;
+
+namespace {
+
+struct TokenTable {
+    const int32_t *ptr;
+    int64_t row_stride;
+    int32_t num_cols;
+};
+
+// The layer pages a token position resolves into.
+struct Pages {
+    int64_t base;       // pool byte of the first layer's block 0
+    int64_t stride;     // bytes between blocks
+    int64_t num_blocks;
+    int32_t block_size;
+    int32_t token_bytes;
+};
+
+// Pool byte of the entry at `pos` of request `req` (in range) under the
+// table; -1 with the status bit to raise when it has none.
+__device__ __forceinline__ int64_t entry_offset(const Pages &G, const TokenTable &T, int64_t req, int32_t pos,
+                                                uint32_t &bad) {
+    const int32_t page = pos < 0 ? -1 : pos / G.block_size;
+    if (page < 0 || page >= T.num_cols) {
+        bad |= LMC_ST_BAD_JOB;
+        return -1;
+    }
+    const int32_t block = __ldg(T.ptr + req * T.row_stride + page);
+    if (block < 0 || block >= G.num_blocks) {
+        bad |= block == -1 ? LMC_ST_NO_BLOCK : LMC_ST_BLOCK_OOR;
+        return -1;
+    }
+    return G.base + (int64_t)block * G.stride + (int64_t)(pos - page * G.block_size) * G.token_bytes;
+}
+
+// A piece's row: n / d by a multiplication with m = ceil(2^32 / d), exact
+// while n * d < 2^32 (a CTA has at most 4096 pieces, or one row: m = 1 gives
+// 0). m = 0 stands for d = 1.
+struct Divider {
+    uint32_t d, m;
+};
+__device__ __forceinline__ uint32_t divide(uint32_t n, const Divider &D, uint32_t &rem) {
+    const uint32_t q = D.m == 0 ? n : __umulhi(n, D.m);
+    rem = n - q * D.d;
+    return q;
+}
+
+constexpr int kRowThreads = 256;
+constexpr int kMaxRows = 64;     // rows a CTA resolves at a time
+constexpr int kRowUnroll = 4;    // pieces in flight per thread
+
+// Copies `rows` rows of `pieces` pieces of V each from src[i] to dst[i] (a
+// null source skips the row): the CTA's threads take the pieces in order, so
+// neighbouring threads touch neighbouring bytes, kRowUnroll loads before the
+// matching stores.
+template <typename V>
+__device__ __forceinline__ void copy_rows(const uint8_t *const *src, uint8_t *const *dst, int rows,
+                                          const Divider &pieces) {
+    const uint32_t total = (uint32_t)rows * pieces.d;
+    for (uint32_t first = threadIdx.x; first < total; first += kRowThreads * kRowUnroll) {
+        V v[kRowUnroll];
+        V *to[kRowUnroll];
+#pragma unroll
+        for (int u = 0; u < kRowUnroll; u++) {
+            const uint32_t i = first + u * kRowThreads;
+            to[u] = nullptr;
+            if (i < total) {
+                uint32_t at;
+                const uint32_t row = divide(i, pieces, at);
+                if (src[row] != nullptr) {
+                    v[u] = __ldcs(reinterpret_cast<const V *>(src[row]) + at);
+                    to[u] = reinterpret_cast<V *>(dst[row]) + at;
+                }
+            }
+        }
+#pragma unroll
+        for (int u = 0; u < kRowUnroll; u++)
+            if (to[u] != nullptr)
+                __stcs(to[u], v[u]);
+    }
+}
+
+struct AppendPlan {
+    Pages pages;
+    TokenTable table;
+    const int32_t *requests;
+    const int32_t *positions;
+    const uint8_t *rows;
+    int64_t row_bytes;  // between rows
+    uint8_t *pool;
+    uint32_t *status;
+    int64_t num_rows;
+    int32_t num_requests;
+    int32_t rows_per_cta;
+    Divider pieces;  // pieces of one row
+    float scale;
+};
+
+// Source and destination of the CTA's rows.
+__device__ __forceinline__ int resolve_append(const AppendPlan &P, const uint8_t **src, uint8_t **dst) {
+    const int64_t first = (int64_t)blockIdx.x * P.rows_per_cta;
+    const int n = (int)min((int64_t)P.rows_per_cta, P.num_rows - first);
+    if ((int)threadIdx.x < n) {
+        const int64_t i = first + threadIdx.x;
+        const int32_t req = __ldg(P.requests + i);
+        const uint8_t *s = nullptr;
+        uint8_t *d = nullptr;
+        if (req != -1) {
+            uint32_t bad = 0;
+            int64_t off = -1;
+            if (req < 0 || req >= P.num_requests)
+                bad = LMC_ST_BAD_JOB;
+            else
+                off = entry_offset(P.pages, P.table, req, __ldg(P.positions + i), bad);
+            if (bad)
+                atomicOr(P.status, bad);
+            if (off >= 0) {
+                s = P.rows + i * P.row_bytes;
+                d = P.pool + off;
+            }
+        }
+        src[threadIdx.x] = s;
+        dst[threadIdx.x] = d;
+    }
+    __syncthreads();
+    return n;
+}
+
+template <typename V>
+__global__ void __launch_bounds__(kRowThreads) lmc_append_kernel(const __grid_constant__ AppendPlan P) {
+    __shared__ const uint8_t *src[kMaxRows];
+    __shared__ uint8_t *dst[kMaxRows];
+    const int n = resolve_append(P, src, dst);
+    copy_rows<V>(src, dst, n, P.pieces);
+}
+
+__device__ __forceinline__ float2 to_float2(__nv_bfloat162 v) { return __bfloat1622float2(v); }
+__device__ __forceinline__ float2 to_float2(__half2 v) { return __half22float2(v); }
+
+// Two values as fp8 codes: the IEEE quotient by the scale, saturated, half to
+// even. A quotient above 448 converts to 448 (satfinite), NaN to NaN.
+__device__ __forceinline__ uint32_t codes2(float2 v, float scale) {
+    return __nv_cvt_float2_to_fp8x2(make_float2(__fdiv_rn(v.x, scale), __fdiv_rn(v.y, scale)), __NV_SATFINITE,
+                                    __NV_E4M3);
+}
+
+// Rows of 16-bit values T2 (pairs) written as fp8 codes: each piece is 16
+// values where the addresses allow (kVec), else two.
+template <typename T2, bool kVec>
+__global__ void __launch_bounds__(kRowThreads) lmc_append_e4m3_kernel(const __grid_constant__ AppendPlan P) {
+    __shared__ const uint8_t *src[kMaxRows];
+    __shared__ uint8_t *dst[kMaxRows];
+    const int n = resolve_append(P, src, dst);
+    const uint32_t total = (uint32_t)n * P.pieces.d;
+    for (uint32_t i = threadIdx.x; i < total; i += kRowThreads) {
+        uint32_t at;
+        const uint32_t row = divide(i, P.pieces, at);
+        if (src[row] == nullptr)
+            continue;
+        if (kVec) {
+            uint4 in[2];
+            const uint4 *s = reinterpret_cast<const uint4 *>(src[row]) + 2 * (size_t)at;
+            in[0] = __ldcs(s);
+            in[1] = __ldcs(s + 1);
+            const T2 *x = reinterpret_cast<const T2 *>(in);
+            uint32_t w[4];
+#pragma unroll
+            for (int k = 0; k < 4; k++)
+                w[k] = codes2(to_float2(x[2 * k]), P.scale) | codes2(to_float2(x[2 * k + 1]), P.scale) << 16;
+            __stcs(reinterpret_cast<uint4 *>(dst[row]) + at, make_uint4(w[0], w[1], w[2], w[3]));
+        } else {
+            // a row may hold an odd number of values, on any 2-byte boundary
+            T2 x;
+            reinterpret_cast<uint16_t *>(&x)[0] = reinterpret_cast<const uint16_t *>(src[row])[at];
+            reinterpret_cast<uint16_t *>(&x)[1] = 0;
+            dst[row][at] = (uint8_t)codes2(to_float2(x), P.scale);
+        }
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Move
+// ---------------------------------------------------------------------------
+
+struct MovePlan {
+    Pages pages;            // of the group's first layer
+    int64_t layer_stride;   // pool bytes between the group's layers
+    TokenTable src, dst;
+    const int32_t *kept;
+    int64_t set_stride;     // 0: one set for all layers
+    int64_t request_stride;
+    const int32_t *kept_lengths;
+    int64_t max_kept;
+    uint8_t *pool;
+    uint32_t *status;
+    int32_t num_requests;
+    int32_t rows_per_cta;
+    int64_t ctas_per_request;
+    Divider pieces;
+};
+
+template <typename V>
+__global__ void __launch_bounds__(kRowThreads) lmc_move_kernel(const __grid_constant__ MovePlan P) {
+    __shared__ const uint8_t *src[kMaxRows];
+    __shared__ uint8_t *dst[kMaxRows];
+    const int64_t part = blockIdx.x % P.ctas_per_request;
+    const int64_t unit = blockIdx.x / P.ctas_per_request;
+    const int64_t req = unit % P.num_requests;
+    const int64_t layer = unit / P.num_requests;
+    const int64_t kept = __ldg(P.kept_lengths + req);
+    if (kept < 0 || kept > P.max_kept) {
+        if (threadIdx.x == 0)
+            atomicOr(P.status, LMC_ST_BAD_JOB);
+        return;
+    }
+    const int64_t first = part * P.rows_per_cta;
+    if (first >= kept)
+        return;
+    const int n = (int)min((int64_t)P.rows_per_cta, kept - first);
+    if ((int)threadIdx.x < n) {
+        const int64_t j = first + threadIdx.x;
+        uint32_t bad = 0;
+        const int64_t from = entry_offset(P.pages, P.src, req,
+                                          __ldg(P.kept + layer * P.set_stride + req * P.request_stride + j), bad);
+        const int64_t to = entry_offset(P.pages, P.dst, req, (int32_t)j, bad);
+        if (bad)
+            atomicOr(P.status, bad);
+        const bool ok = from >= 0 && to >= 0;
+        src[threadIdx.x] = ok ? P.pool + layer * P.layer_stride + from : nullptr;
+        dst[threadIdx.x] = P.pool + layer * P.layer_stride + to;
+    }
+    __syncthreads();
+    copy_rows<V>(src, dst, n, P.pieces);
+}
+
+// ---------------------------------------------------------------------------
+// Select
+// ---------------------------------------------------------------------------
+
+// The `take` highest of a row's candidates, found by their binary32 patterns
+// mapped to unsigned keys of the same order, eight bits at a time from the
+// top: a histogram of the keys that still match the threshold's known bits
+// gives its next eight. A row is shared by the CTAs of a cluster, which read
+// one another's histograms through distributed shared memory; each keeps its
+// part of the keys in its own shared memory (kCached), so the scores are read
+// from HBM once. The histogram has a column per lane: scores share few
+// exponents, and one counter per key prefix would serialise a warp's
+// increments. Then each warp walks its own run of tokens in order, and a
+// token's place among the kept is the number kept before it.
+constexpr int kSelThreads = 512;
+constexpr int kSelWarps = kSelThreads / 32;
+constexpr int kSelMaxCluster = 8;
+
+struct SelectPlan {
+    const float *scores;
+    int64_t set_stride, request_stride;
+    const int32_t *lengths;
+    int64_t max_length;
+    int32_t *kept;
+    float *kept_scores;
+    int32_t *kept_lengths;
+    uint32_t *status;
+    int32_t budget, recent;
+    int32_t num_requests;
+    int32_t cluster;
+    int32_t cap;  // keys a CTA can hold
+};
+
+__device__ __forceinline__ uint32_t order_key(float x) {
+    if (x != x)
+        return 0;  // below every number
+    const uint32_t u = __float_as_uint(x == 0.0f ? 0.0f : x);
+    return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+}
+
+struct SelectShared {
+    uint32_t hist[256 * 32];
+    uint32_t totals[2][256];       // this CTA's, read by the cluster
+    uint32_t all[256];             // the cluster's
+    uint32_t warp_above[kSelWarps];
+    uint32_t warp_equal[kSelWarps];
+    uint32_t counts[2];            // this CTA's kept-for-sure and threshold keys
+    uint32_t found[2];             // the pass's bin, and what is left to take in it
+};
+
+template <bool kCached>
+__global__ void __launch_bounds__(kSelThreads) lmc_select_kernel(const __grid_constant__ SelectPlan P) {
+    extern __shared__ __align__(16) uint8_t select_mem[];
+    SelectShared &S = *reinterpret_cast<SelectShared *>(select_mem);
+    uint32_t *const keys = reinterpret_cast<uint32_t *>(select_mem + sizeof(SelectShared));
+    cg::cluster_group cluster = cg::this_cluster();
+    const int rank = (int)cluster.block_rank();
+    const int64_t row = blockIdx.x / P.cluster;
+    const int64_t set = row / P.num_requests, req = row % P.num_requests;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+
+    // uniform over the cluster, so leaving here leaves no CTA waiting
+    const int64_t L = __ldg(P.lengths + req);
+    if (L < 0 || L > P.max_length) {
+        if (rank == 0 && tid == 0)
+            atomicOr(P.status, LMC_ST_BAD_JOB);
+        return;
+    }
+    if (set == 0 && rank == 0 && tid == 0)
+        P.kept_lengths[req] = (int32_t)min(L, (int64_t)P.budget);
+    const float *const score = P.scores + set * P.set_stride + req * P.request_stride;
+    int32_t *const kept = P.kept + row * P.budget;
+    float *const kept_scores = P.kept_scores == nullptr ? nullptr : P.kept_scores + row * P.budget;
+    const int64_t step = (int64_t)P.cluster * kSelThreads;
+    if (L <= P.budget) {
+        for (int64_t t = (int64_t)rank * kSelThreads + tid; t < L; t += step) {
+            kept[t] = (int32_t)t;
+            if (kept_scores != nullptr)
+                kept_scores[t] = score[t];
+        }
+        return;
+    }
+    const int32_t n = (int32_t)L - P.recent;      // candidates: [0, n)
+    const int32_t take = P.budget - P.recent;     // 0 <= take < n
+    for (int32_t j = rank * kSelThreads + tid; j < P.recent; j += (int32_t)step) {
+        kept[take + j] = n + j;
+        if (kept_scores != nullptr)
+            kept_scores[take + j] = score[n + j];
+    }
+    if (take == 0)
+        return;
+
+    // this CTA's candidates, and within them each warp's run
+    const int32_t part = (int32_t)(((int64_t)n + P.cluster - 1) / P.cluster);
+    const int32_t lo = (int32_t)min((int64_t)rank * part, (int64_t)n);
+    const int32_t mine = (int32_t)min((int64_t)lo + part, (int64_t)n) - lo;
+    if (kCached) {
+        for (int32_t i = tid; i < mine; i += kSelThreads)
+            keys[i] = order_key(__ldcs(score + lo + i));
+    }
+    auto key_at = [&](int32_t i) { return kCached ? keys[i] : order_key(__ldg(score + lo + i)); };
+
+    uint32_t prefix = 0, mask = 0, left = (uint32_t)take;
+    int buf = 0;
+    for (int shift = 24; shift >= 0; shift -= 8, buf ^= 1) {
+        for (int i = tid; i < 256 * 32; i += kSelThreads)
+            S.hist[i] = 0;
+        __syncthreads();
+        for (int32_t i = tid; i < mine; i += kSelThreads) {
+            const uint32_t k = key_at(i);
+            if ((k & mask) == prefix)
+                atomicAdd(&S.hist[((k >> shift) & 255u) * 32 + lane], 1u);
+        }
+        __syncthreads();
+        if (tid < 256) {
+            uint32_t sum = 0;
+#pragma unroll 8
+            for (int j = 0; j < 32; j++)
+                sum += S.hist[tid * 32 + ((j + tid) & 31)];
+            S.totals[buf][tid] = sum;
+        }
+        cluster.sync();  // also a barrier of this CTA
+        if (tid < 256) {
+            uint32_t sum = 0;
+            for (int c = 0; c < P.cluster; c++)
+                sum += cluster.map_shared_rank(&S.totals[buf][0], c)[tid];
+            S.all[tid] = sum;
+        }
+        __syncthreads();
+        if (warp == 0) {
+            // lane l holds bins [8 l', 8 l' + 8) counted from the top
+            const int top = 255 - 8 * lane;
+            uint32_t sum = 0;
+#pragma unroll
+            for (int j = 0; j < 8; j++)
+                sum += S.all[top - j];
+            uint32_t before = sum;
+            for (int o = 1; o < 32; o <<= 1) {
+                const uint32_t x = __shfl_up_sync(0xffffffffu, before, o);
+                if (lane >= o)
+                    before += x;
+            }
+            before -= sum;
+            if (before < left && left <= before + sum) {
+                for (int j = 0; j < 8; j++) {
+                    const uint32_t c = S.all[top - j];
+                    if (left <= before + c) {
+                        S.found[0] = (uint32_t)(top - j);
+                        S.found[1] = left - before;
+                        S.counts[0] = c;
+                        break;
+                    }
+                    before += c;
+                }
+            }
+        }
+        __syncthreads();
+        const uint32_t bin = S.found[0], in_bin = S.counts[0];
+        left = S.found[1];
+        prefix |= bin << shift;
+        mask |= 255u << shift;
+        __syncthreads();
+        if (in_bin == left)
+            break;  // the whole bin is taken: the lower bits do not matter (uniform over the cluster)
+    }
+
+    // keys above the threshold's bits are taken, and the first `left` of
+    // those that match them
+    const int32_t run = (mine + kSelWarps - 1) / kSelWarps;
+    const int32_t w0 = min(warp * run, mine), w1 = min(w0 + run, mine);
+    uint32_t above = 0, equal = 0;
+    for (int32_t i = w0 + lane; i < w1; i += 32) {
+        const uint32_t k = key_at(i) & mask;
+        above += k > prefix;
+        equal += k == prefix;
+    }
+    above = __reduce_add_sync(0xffffffffu, above);
+    equal = __reduce_add_sync(0xffffffffu, equal);
+    if (lane == 0) {
+        S.warp_above[warp] = above;
+        S.warp_equal[warp] = equal;
+    }
+    __syncthreads();
+    if (tid == 0) {
+        uint32_t a = 0, e = 0;
+        for (int w = 0; w < kSelWarps; w++) {
+            const uint32_t x = S.warp_above[w], y = S.warp_equal[w];
+            S.warp_above[w] = a;
+            S.warp_equal[w] = e;
+            a += x;
+            e += y;
+        }
+        S.counts[0] = a;
+        S.counts[1] = e;
+    }
+    cluster.sync();
+    uint32_t a_before = S.warp_above[warp], e_before = S.warp_equal[warp];
+    for (int c = 0; c < rank; c++) {
+        const uint32_t *other = cluster.map_shared_rank(&S.counts[0], c);
+        a_before += other[0];
+        e_before += other[1];
+    }
+    const uint32_t lanes_below = (1u << lane) - 1u;
+    for (int32_t i0 = w0; i0 < w1; i0 += 32) {
+        const int32_t i = i0 + lane;
+        uint32_t k = 0;
+        if (i < w1)
+            k = key_at(i) & mask;
+        const bool a = i < w1 && k > prefix, e = i < w1 && k == prefix;
+        const uint32_t va = __ballot_sync(0xffffffffu, a), ve = __ballot_sync(0xffffffffu, e);
+        const uint32_t e_at = e_before + __popc(ve & lanes_below);
+        if (a || (e && e_at < left)) {
+            const uint32_t at = a_before + __popc(va & lanes_below) + min(e_at, left);
+            kept[at] = lo + i;
+            if (kept_scores != nullptr)
+                kept_scores[at] = score[lo + i];
+        }
+        a_before += __popc(va);
+        e_before += __popc(ve);
+    }
+    cluster.sync();  // no CTA leaves while another may read its counts
+}
+
+// ---------------------------------------------------------------------------
+// Host side
+// ---------------------------------------------------------------------------
+
+TokenTable token_table(const lmc_block_table &t) { return TokenTable{t.table, t.row_stride, (int32_t)t.num_cols}; }
+
+// Rows a CTA takes (up to 16 pieces per thread), and the division by a row's
+// pieces.
+int rows_per_cta(int64_t pieces, Divider &D) {
+    const int rows = (int)std::max<int64_t>(1, std::min<int64_t>(kMaxRows, kRowThreads * 16 / pieces));
+    D.d = (uint32_t)pieces;
+    D.m = rows == 1 ? 1u : pieces == 1 ? 0u : (uint32_t)((((uint64_t)1 << 32) + D.d - 1) / D.d);
+    return rows;
+}
+
+int launched() { return cudaGetLastError() == cudaSuccess ? LMC_OK : LMC_ERR_CUDA; }
+
+// The widest piece (16, 4 or 1 bytes) that every one of the values is a multiple of.
+int piece_bytes(std::initializer_list<int64_t> values) {
+    int64_t all = 0;
+    for (int64_t v : values)
+        all |= v;
+    return (all & 15) == 0 ? 16 : (all & 3) == 0 ? 4 : 1;
+}
+
+}  // namespace
+
+namespace lmc {
+
+int check_entries(const lmc_layout *L, const lmc_entries *e) {
+    if (L == nullptr || e == nullptr || e->layer < 0 || (size_t)e->layer >= L->desc.size())
+        return LMC_ERR_INVALID_ARG;
+    const lmc_layer_spec &spec = L->specs[e->layer];
+    const int elem = entry_elem_bytes(e->dtype);
+    if (spec.kind == LMC_LAYER_KDA || elem == 0 || e->entry_dim <= 0 ||
+        spec.token_bytes != (int64_t)e->entry_dim * elem || e->num_requests < 0 || L->block_size > INT32_MAX ||
+        spec.token_bytes > INT32_MAX / 2)
+        return LMC_ERR_INVALID_ARG;
+    if (!std::isfinite(e->scale) || e->scale <= 0.0f || (e->dtype != LMC_E_E4M3 && e->scale != 1.0f))
+        return LMC_ERR_INVALID_ARG;
+    return table_ok(e->table, e->num_requests) ? LMC_OK : LMC_ERR_INVALID_ARG;
+}
+
+}  // namespace lmc
+
+extern "C" int lmc_append(const lmc_layout *L, const lmc_entries *e, void *pool, const int32_t *requests,
+                          const int32_t *positions, const void *rows, int32_t rows_dtype, int64_t row_stride,
+                          int64_t num_rows, uint32_t *status, void *stream) {
+    if (const int rc = lmc::check_entries(L, e); rc != LMC_OK)
+        return rc;
+    if (status == nullptr || num_rows < 0 || (rows_dtype != LMC_E_BF16 && rows_dtype != LMC_E_F16) ||
+        (e->dtype != LMC_E_E4M3 && e->dtype != rows_dtype) || row_stride < e->entry_dim ||
+        row_stride > INT64_MAX / 2)
+        return LMC_ERR_INVALID_ARG;
+    if (num_rows > 0 && (pool == nullptr || requests == nullptr || positions == nullptr || rows == nullptr))
+        return LMC_ERR_INVALID_ARG;
+    if ((((uintptr_t)status | (uintptr_t)requests | (uintptr_t)positions) & 3) != 0 || ((uintptr_t)rows & 1) != 0)
+        return LMC_ERR_ALIGN;
+    if (num_rows == 0)
+        return LMC_OK;
+    const lmc_layer_desc &d = L->desc[e->layer];
+    const int64_t tb = L->specs[e->layer].token_bytes;
+    AppendPlan P;
+    P.pages = Pages{d.base, d.stride, L->num_blocks, (int32_t)L->block_size, (int32_t)tb};
+    P.table = token_table(e->table);
+    P.requests = requests;
+    P.positions = positions;
+    P.rows = static_cast<const uint8_t *>(rows);
+    P.row_bytes = row_stride * 2;
+    P.pool = static_cast<uint8_t *>(pool);
+    P.status = status;
+    P.num_rows = num_rows;
+    P.num_requests = e->num_requests;
+    P.scale = e->scale;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const int wide = piece_bytes({(int64_t)(uintptr_t)pool, d.base, d.stride, tb, (int64_t)(uintptr_t)rows,
+                                  P.row_bytes});
+    if (e->dtype == LMC_E_E4M3) {
+        const bool vec = wide == 16 && e->entry_dim % 16 == 0;
+        const int64_t pieces = vec ? e->entry_dim / 16 : e->entry_dim;
+        P.rows_per_cta = rows_per_cta(pieces, P.pieces);
+        const int64_t grid = (num_rows + P.rows_per_cta - 1) / P.rows_per_cta;
+        if (grid > INT32_MAX)
+            return LMC_ERR_INVALID_ARG;
+        auto kern = rows_dtype == LMC_E_BF16
+                        ? (vec ? lmc_append_e4m3_kernel<__nv_bfloat162, true> : lmc_append_e4m3_kernel<__nv_bfloat162, false>)
+                        : (vec ? lmc_append_e4m3_kernel<__half2, true> : lmc_append_e4m3_kernel<__half2, false>);
+        kern<<<(unsigned)grid, kRowThreads, 0, s>>>(P);
+        return launched();
+    }
+    P.rows_per_cta = rows_per_cta(tb / wide, P.pieces);
+    const int64_t grid = (num_rows + P.rows_per_cta - 1) / P.rows_per_cta;
+    if (grid > INT32_MAX)
+        return LMC_ERR_INVALID_ARG;
+    auto kern = wide == 16 ? lmc_append_kernel<uint4> : wide == 4 ? lmc_append_kernel<uint32_t> : lmc_append_kernel<uint8_t>;
+    kern<<<(unsigned)grid, kRowThreads, 0, s>>>(P);
+    return launched();
+}
+
+extern "C" int lmc_move_tokens(const lmc_layout *L, int32_t kv_group, void *pool, int32_t num_requests,
+                               const lmc_block_table *src, const lmc_block_table *dst, const int32_t *kept,
+                               int32_t num_sets, int64_t set_stride, int64_t request_stride,
+                               const int32_t *kept_lengths, int64_t max_kept, uint32_t *status, void *stream) {
+    if (L == nullptr || kv_group < 0 || (size_t)kv_group >= L->kv_group_kind.size() ||
+        L->kv_group_kind[kv_group] == LMC_LAYER_KDA || src == nullptr || dst == nullptr || status == nullptr ||
+        num_requests < 0 || max_kept < 0 || max_kept > INT32_MAX)
+        return LMC_ERR_INVALID_ARG;
+    const int32_t layers = L->kv_group_size[kv_group];
+    if ((num_sets != 1 && num_sets != layers) || set_stride < 0 || request_stride < max_kept ||
+        !lmc::table_ok(*src, num_requests) || !lmc::table_ok(*dst, num_requests))
+        return LMC_ERR_INVALID_ARG;
+    if (((uintptr_t)status & 3) != 0 || (((uintptr_t)kept | (uintptr_t)kept_lengths) & 3) != 0)
+        return LMC_ERR_ALIGN;
+    if (num_requests == 0 || max_kept == 0)
+        return LMC_OK;
+    if (pool == nullptr || kept == nullptr || kept_lengths == nullptr)
+        return LMC_ERR_INVALID_ARG;
+    if (src->table != nullptr && src->table == dst->table)
+        return LMC_ERR_OVERLAP;
+    // the group's layers have one page size each and lie evenly spaced
+    // (padded: one slab apart; packed: one page apart)
+    int64_t first = -1, second = -1;
+    int32_t layer = -1;
+    for (size_t i = 0; i < L->desc.size(); i++)
+        if (L->desc[i].kv_group == kv_group) {
+            if (L->desc[i].slot == 0) {
+                first = L->desc[i].base;
+                layer = (int32_t)i;
+            } else if (L->desc[i].slot == 1) {
+                second = L->desc[i].base;
+            }
+        }
+    const lmc_layer_desc &d = L->desc[layer];
+    const int64_t tb = L->specs[layer].token_bytes;
+    if (L->block_size > INT32_MAX || tb > INT32_MAX / 2)
+        return LMC_ERR_INVALID_ARG;
+    MovePlan P;
+    P.pages = Pages{first, d.stride, L->num_blocks, (int32_t)L->block_size, (int32_t)tb};
+    P.layer_stride = layers > 1 ? second - first : 0;
+    P.src = token_table(*src);
+    P.dst = token_table(*dst);
+    P.kept = kept;
+    P.set_stride = num_sets == 1 ? 0 : set_stride;
+    P.request_stride = request_stride;
+    P.kept_lengths = kept_lengths;
+    P.max_kept = max_kept;
+    P.pool = static_cast<uint8_t *>(pool);
+    P.status = status;
+    P.num_requests = num_requests;
+    const int wide = piece_bytes({(int64_t)(uintptr_t)pool, first, d.stride, P.layer_stride, tb});
+    P.rows_per_cta = rows_per_cta(tb / wide, P.pieces);
+    P.ctas_per_request = (max_kept + P.rows_per_cta - 1) / P.rows_per_cta;
+    int64_t grid;
+    if (!lmc::mul_ok(P.ctas_per_request, (int64_t)num_requests * layers, &grid) || grid > INT32_MAX)
+        return LMC_ERR_INVALID_ARG;
+    auto kern = wide == 16 ? lmc_move_kernel<uint4> : wide == 4 ? lmc_move_kernel<uint32_t> : lmc_move_kernel<uint8_t>;
+    kern<<<(unsigned)grid, kRowThreads, 0, static_cast<cudaStream_t>(stream)>>>(P);
+    return launched();
+}
+
+extern "C" int lmc_select_tokens(const float *scores, int64_t set_stride, int64_t request_stride, int32_t num_sets,
+                                 int32_t num_requests, const int32_t *lengths, int64_t max_length, int64_t budget,
+                                 int64_t recent, int32_t *kept, float *kept_scores, int32_t *kept_lengths,
+                                 uint32_t *status, void *stream) {
+    if (num_sets < 0 || num_requests < 0 || max_length < 0 || max_length > INT32_MAX || budget < 0 ||
+        budget > INT32_MAX || recent < 0 || recent > budget || set_stride < 0 || request_stride < 0 ||
+        status == nullptr)
+        return LMC_ERR_INVALID_ARG;
+    if ((((uintptr_t)scores | (uintptr_t)lengths | (uintptr_t)kept | (uintptr_t)kept_scores | (uintptr_t)kept_lengths |
+          (uintptr_t)status) & 3) != 0)
+        return LMC_ERR_ALIGN;
+    if (num_sets == 0 || num_requests == 0)
+        return LMC_OK;
+    if (lengths == nullptr || kept_lengths == nullptr || (scores == nullptr && max_length > 0) ||
+        (kept == nullptr && budget > 0))
+        return LMC_ERR_INVALID_ARG;
+    const int sms = lmc::sm_count();
+    if (sms <= 0)
+        return LMC_ERR_CUDA;
+    SelectPlan P;
+    P.scores = scores;
+    P.set_stride = set_stride;
+    P.request_stride = request_stride;
+    P.lengths = lengths;
+    P.max_length = max_length;
+    P.kept = kept;
+    P.kept_scores = kept_scores;
+    P.kept_lengths = kept_lengths;
+    P.status = status;
+    P.budget = (int32_t)budget;
+    P.recent = (int32_t)recent;
+    P.num_requests = num_requests;
+    const int64_t rows = (int64_t)num_sets * num_requests;
+    // 16384 keys (64 KB) per CTA let two CTAs share an SM; fewer where there
+    // are not enough rows for all SMs
+    int c = 1;
+    while (c < kSelMaxCluster &&
+           (max_length > (int64_t)c * 16384 || (rows * c < sms && max_length > (int64_t)c * 2048)))
+        c *= 2;
+    P.cluster = c;
+    const int64_t most = 227 * 1024 - (int64_t)sizeof(SelectShared);
+    const int64_t want = (max_length + c - 1) / c * 4;
+    const bool cached = want <= most;
+    P.cap = cached ? (int32_t)(want / 4) : 0;
+    const size_t smem = sizeof(SelectShared) + (cached ? (size_t)(want + 15) / 16 * 16 : 0);
+    if (rows * c > INT32_MAX)
+        return LMC_ERR_INVALID_ARG;
+    auto kern = cached ? lmc_select_kernel<true> : lmc_select_kernel<false>;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+        return LMC_ERR_CUDA;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)c;
+    attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(rows * c));
+    cfg.blockDim = dim3(kSelThreads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = static_cast<cudaStream_t>(stream);
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, P) == cudaSuccess ? LMC_OK : LMC_ERR_CUDA;
+}
