@@ -1,5 +1,48 @@
 // attend.cu -- attention of one new token per request over the paged entries
 // of an MLA or SWA layer, for sm_103a.
+//
+// Mathematics. The query's heads share one entry k_t per token, whose first V
+// values are also the value: x_ht = c q_h . k_t, out_h = sum_t p_ht k_t[:V]
+// with p the softmax of x over t. One pass over the cache keeps, per head, a
+// reference m and the sums l = sum 2^(x - m), O = sum 2^(x - m) k[:V] (x in
+// units of log 2); parts of a cache are joined by scaling them to one m.
+//
+// Every token's entry is read from HBM once and used for two products per
+// head, so with H heads a byte of a 16-bit cache carries about 2 H operations
+// (576 values, 512 of them the value): 60 at 32 heads, 121 at 64. The copy
+// rate allows 270 per byte at the dense tensor rate, so the call is bound by
+// HBM, and the tensor cores have to run beside the loads. CUDA cores cannot
+// (4.3 ms against 45 us for 32 requests of 8192 tokens).
+//
+// Split. The cache is cut into tiles of up to 64 tokens of one page; all
+// requests' tiles in a row are shared out evenly over the CTAs (one per SM),
+// whatever the lengths, so a CTA works through a run of segments (request,
+// tiles). A request inside one CTA is finished there; one that spans several
+// leaves its (m, l, O) per CTA in the workspace and a second kernel joins
+// them. Above 64 heads, groups of heads take CTAs of their own, side by side.
+//
+// A CTA: a loader brings the tile's entries to shared memory (panels of 64
+// values, 128-byte swizzle), one warp issues the products on the tensor cores,
+// four warps do the softmax.
+//   S [64 heads x 64 tokens]   = Q . K^T    (A = Q, B = the tile, both with
+//                                            the summed axis contiguous)
+//   O^T [V values x heads]    += V^T . P^T  (A = the same tile read along its
+//                                            values, B = P)
+// The second product is taken transposed so that its 128 rows are values, of
+// which there are always enough, and its columns the heads, of which there may
+// be few: O^T takes V/128 x heads columns of tensor memory, and no row of the
+// tensor cores idles however few heads there are. P goes through shared memory
+// as bf16 or f16 (the entries' type; f16 for an fp8 cache): the only rounding
+// below 32 bits on the way, at most half a step of p (2^-8 bf16, 2^-11 f16)
+// per token. l is summed from p before it is rounded. The reference m only
+// moves when a logit exceeds it by 8 (p up to 2^8 fits either type), so O is
+// rarely rescaled.
+//
+// Entries of 16 bits come by TMA: a tensor map over (values, page rows,
+// blocks) needs no address arithmetic, and rows past a page's end read as
+// zero. fp8 entries are loaded to registers, widened to f16 (exact) and stored
+// to the same panels; q is brought to f16 with a power of two per head.
+#include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
@@ -15,190 +58,1090 @@ namespace {
 
 constexpr int kMaxEntry = 576;
 constexpr int kMaxValue = 512;
+constexpr int kTile = 64;             // tokens per tile
+constexpr int kMaxHeads = 64;         // heads per CTA
+constexpr int kPanel = kTile * 128;   // bytes of 64 values of a tile's rows
+constexpr int kMaxStages = 4;
+constexpr int kMaxCols = 160;         // CTAs along the cache's length (an SM each)
+constexpr int kSoftWarps = 4;
+constexpr int kMmaWarp = 4;
+constexpr int kFirstLoader = 5;
+constexpr int kFp8Loaders = 8;        // warps: two groups of four, a tile each
+constexpr float kLag = 8.0f;          // how far (log2) a logit may exceed the reference
+constexpr uint32_t kWaitLimit = 1u << 22;
+constexpr int kSmemLimit = 227 * 1024;
+
+// Shared memory that is not a tile: barriers and per-head numbers.
+struct Control {
+    uint64_t q_full, q_free;
+    uint64_t kv_full[kMaxStages], kv_free[kMaxStages];
+    uint64_t s_full[2], s_free[2];
+    uint64_t p_full, pv_done, o_free;
+    uint64_t valid[kMaxStages];  // a tile's rows that are attended
+    uint64_t zero[kMaxStages];   // and those to be cleared before they are values
+    uint32_t tmem;
+    uint32_t gave_up;            // a wait ran out: nothing waits any more
+    float factor[kMaxHeads];     // rescaling of a head's O
+    float inverse[kMaxHeads];    // 1 / l
+    float q_scale[kMaxHeads];    // fp8: what q was divided by
+};
 
 struct AttendPlan {
-    const uint8_t *pool;  // + the layer's base
+    CUtensorMap cache;  // 16-bit entries
+    CUtensorMap query;
+    const uint8_t *pool;  // fp8: the layer's block 0
     int64_t block_stride;
     int64_t num_blocks;
-    int32_t block_size;
-    int32_t token_bytes;
     const int32_t *table;
     int64_t row_stride;
     int64_t num_cols;
     const int32_t *lengths;
     int64_t max_length;
-    int64_t window;  // 0: none
     const uint16_t *q;
     int64_t q_request_stride, q_head_stride;
     uint16_t *out;
     int64_t out_request_stride, out_head_stride;
     float *lse;  // caller's, or NULL
     int64_t lse_request_stride;
-    float *weights;
+    float *weights;  // caller's, or NULL
     int64_t weights_request_stride;
-    float *lse_all;  // workspace [R][H]
+    // workspace
+    int2 *segment;   // [2 cols]: (request, tiles) a CTA left unfinished, or (-1, 0)
+    float2 *part_ml; // [2 cols][H]
+    float *part_o;   // [2 cols][H][V]
+    float *lse2;     // [R][H], log2
+    float *logits;   // [R][H][logit_stride], log2, or NULL
+    int64_t logit_stride;
     uint32_t *status;
-    float softmax_scale;
-    float scale;
-    int32_t E, V, H;
-    int32_t dtype, q_dtype;
+    int32_t R, H, E, V;
+    int32_t window;            // 0: none
+    int32_t block_size;        // N
+    int32_t token_bytes;
+    int32_t pages_per_tile;    // > 1 where several pages fit a tile
+    int32_t span;              // tokens of a page, or of a tile's pages
+    int32_t tiles_per_span;
+    int32_t cols;              // CTAs along the length
+    int32_t head_groups, group_heads;  // heads of a CTA
+    int32_t padded_heads;      // rounded up to 16
+    int32_t panels;            // of an entry in shared memory
+    int32_t value_tiles;       // of 128 values
+    int32_t stages;
+    int32_t q_bf16;            // q's and out's type
+    float scale;               // of fp8 entries
+    float log2_scale;          // softmax_scale * scale * log2(e)
 };
 
-__device__ __forceinline__ float load16(uint16_t bits, int32_t dtype) {
-    return dtype == LMC_E_BF16 ? __uint_as_float((uint32_t)bits << 16) : __half2float(__ushort_as_half(bits));
+// ---- requests and tiles ----------------------------------------------------
+
+struct Range {
+    int64_t lo, L;  // tokens [lo, L)
+    bool ok;        // a length that can be served
+};
+
+__device__ __forceinline__ Range range_of(const AttendPlan &P, int r) {
+    Range g;
+    g.L = __ldg(P.lengths + r);
+    g.ok = g.L >= 0 && g.L <= P.max_length && g.L <= P.num_cols * P.block_size;
+    g.lo = P.window > 0 ? max((int64_t)0, g.L - P.window) : 0;
+    return g;
 }
 
-__device__ __forceinline__ float load_entry(const uint8_t *e, int32_t i, const AttendPlan &P) {
-    if (P.dtype == LMC_E_E4M3)
-        return __half2float(__half(__nv_cvt_fp8_to_halfraw(e[i], __NV_E4M3))) * P.scale;
-    return load16(reinterpret_cast<const uint16_t *>(e)[i], P.dtype);
+__device__ __forceinline__ int first_tile(const AttendPlan &P, const Range &g) {
+    const int t = (int)g.lo, s = t / P.span;
+    return s * P.tiles_per_span + (t - s * P.span) / kTile;
 }
 
-// First token of the request's range; false when the request is not served.
-__device__ __forceinline__ bool token_range(const AttendPlan &P, int64_t r, int64_t &lo, int64_t &L) {
-    L = __ldg(P.lengths + r);
-    lo = P.window > 0 ? max((int64_t)0, L - P.window) : 0;
-    return L >= 0 && L <= P.max_length && L <= P.num_cols * P.block_size;
+__device__ __forceinline__ int tiles_of(const AttendPlan &P, const Range &g) {
+    if (!g.ok || g.L == 0)
+        return 0;
+    const int t = (int)(g.L - 1), s = t / P.span;
+    return s * P.tiles_per_span + (t - s * P.span) / kTile + 1 - first_tile(P, g);
 }
 
-__device__ __forceinline__ const uint8_t *entry_at(const AttendPlan &P, int64_t r, int64_t t, uint32_t &bad) {
-    const int64_t page = t / P.block_size;
-    const int32_t block = __ldg(P.table + r * P.row_stride + page);
-    if (block < 0 || block >= P.num_blocks) {
-        bad |= block == -1 ? LMC_ST_NO_BLOCK : LMC_ST_BLOCK_OOR;
-        return nullptr;
-    }
-    return P.pool + (int64_t)block * P.block_stride + (t - page * P.block_size) * P.token_bytes;
-}
+// A CTA's run of segments. Each warp walks it on its own: 32 requests at a
+// time, a lane each.
+struct Walk {
+    int64_t pos, end;    // the CTA's tiles still to come, of all requests' in a row
+    int64_t base;        // tiles before the 32 requests at hand
+    int64_t start, stop; // this lane's request's tiles
+    int r0, lane;
 
-constexpr int kWarps = 8;
-constexpr int kPer = kMaxEntry / 32;
-constexpr int kValPer = kMaxValue / 32;
+    // the current segment
+    int r, first, count;  // request, its first tile here (of the request's), tiles
+    bool begins, ends;    // the request begins / ends in this CTA
+    Range range;
 
-// One CTA per (head, request), a token per warp at a time: the entry's values
-// lie across the lanes, the running maximum and sum of each warp are joined
-// at the end.
-__global__ void __launch_bounds__(32 * kWarps) lmc_attend_kernel(const __grid_constant__ AttendPlan P) {
-    const int64_t r = blockIdx.y;
-    const int h = blockIdx.x, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    int64_t lo, L;
-    if (!token_range(P, r, lo, L)) {
-        if (threadIdx.x == 0)
-            atomicOr(P.status, LMC_ST_BAD_JOB);
-        return;
-    }
-    float q[kPer], acc[kValPer];
-#pragma unroll
-    for (int i = 0; i < kPer; i++)
-        q[i] = lane + 32 * i < P.E
-                   ? load16(P.q[r * P.q_request_stride + h * P.q_head_stride + lane + 32 * i], P.q_dtype)
-                   : 0.0f;
-#pragma unroll
-    for (int i = 0; i < kValPer; i++)
-        acc[i] = 0.0f;
-    float m = -INFINITY, sum = 0.0f;
-    uint32_t bad = 0;
-    for (int64_t t = lo + warp; t < L; t += kWarps) {
-        const uint8_t *e = entry_at(P, r, t, bad);
-        if (e == nullptr)
-            continue;
-        float v[kPer], dot = 0.0f;
-#pragma unroll
-        for (int i = 0; i < kPer; i++) {
-            v[i] = lane + 32 * i < P.E ? load_entry(e, lane + 32 * i, P) : 0.0f;
-            dot = fmaf(q[i], v[i], dot);
+    __device__ __forceinline__ void load(const AttendPlan &P) {
+        int n = 0;
+        if (r0 + lane < P.R)
+            n = tiles_of(P, range_of(P, r0 + lane));
+        int64_t sum = n;
+        for (int o = 1; o < 32; o <<= 1) {
+            const int64_t x = __shfl_up_sync(0xffffffffu, sum, o);
+            if (lane >= o)
+                sum += x;
         }
+        stop = base + sum;
+        start = stop - n;
+    }
+
+    __device__ __forceinline__ void init(const AttendPlan &P, int col) {
+        lane = threadIdx.x & 31;
+        int64_t total = 0;
+        for (int i = lane; i < P.R; i += 32)
+            total += tiles_of(P, range_of(P, i));
         for (int o = 16; o > 0; o >>= 1)
-            dot += __shfl_xor_sync(0xffffffffu, dot, o);
-        const float x = dot * P.softmax_scale;
-        const float top = fmaxf(m, x);
-        const float keep = m == top ? 1.0f : expf(m - top), p = expf(x - top);
-        m = top;
-        sum = sum * keep + p;
-#pragma unroll
-        for (int i = 0; i < kValPer; i++)
-            acc[i] = acc[i] * keep + p * v[i];
+            total += __shfl_xor_sync(0xffffffffu, total, o);
+        const int64_t each = (total + P.cols - 1) / P.cols;  // so only the last CTAs may have none
+        pos = min(col * each, total);
+        end = min(pos + each, total);
+        r0 = 0;
+        base = 0;
+        load(P);
+    }
+
+    __device__ __forceinline__ bool next(const AttendPlan &P) {
+        if (pos >= end)
+            return false;
+        uint32_t here;
+        while ((here = __ballot_sync(0xffffffffu, start <= pos && pos < stop)) == 0) {
+            base = __shfl_sync(0xffffffffu, stop, 31);
+            r0 += 32;
+            if (r0 >= P.R)
+                return false;  // the lengths changed under the call
+            load(P);
+        }
+        const int k = __ffs(here) - 1;
+        const int64_t s = __shfl_sync(0xffffffffu, start, k), e = __shfl_sync(0xffffffffu, stop, k);
+        r = r0 + k;
+        range = range_of(P, r);
+        begins = s == pos;
+        ends = e <= end;
+        first = (int)(pos - s) + first_tile(P, range);
+        count = (int)(min(e, end) - pos);
+        pos += count;
+        return true;
+    }
+};
+
+// A tile's tokens: [t0, t0 + rows) of one page, or of pages_per_tile pages.
+struct Tile {
+    int t0, rows, page, row0;
+};
+
+__device__ __forceinline__ Tile tile_at(const AttendPlan &P, int tile) {
+    Tile T;
+    const int s = tile / P.tiles_per_span;
+    T.row0 = (tile - s * P.tiles_per_span) * kTile;
+    T.t0 = s * P.span + T.row0;
+    T.rows = min(kTile, P.span - T.row0);
+    T.page = s * P.pages_per_tile;
+    return T;
+}
+
+__device__ __forceinline__ uint64_t bits(int lo, int hi) {  // [lo, hi) of 64
+    lo = max(lo, 0);
+    hi = min(hi, 64);
+    if (hi <= lo)
+        return 0;
+    return (hi - lo == 64 ? ~0ull : ((1ull << (hi - lo)) - 1)) << lo;
+}
+
+// ---- barriers, tensor cores ------------------------------------------------
+
+__device__ __forceinline__ uint32_t smem_addr(const void *p) {
+    return static_cast<uint32_t>(__cvta_generic_to_shared(p));
+}
+
+__device__ __forceinline__ void bar_init(uint64_t *bar, int count) {
+    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_addr(bar)), "r"(count) : "memory");
+}
+
+__device__ __forceinline__ void bar_arrive(uint64_t *bar) {
+    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
+}
+
+__device__ __forceinline__ void bar_expect(uint64_t *bar, uint32_t bytes) {
+    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_addr(bar)), "r"(bytes)
+                 : "memory");
+}
+
+__device__ __forceinline__ bool bar_try(uint64_t *bar, uint32_t parity) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(smem_addr(bar)), "r"(parity)
+        : "memory");
+    return done != 0;
+}
+
+// Waits for a phase. When the limit runs out the CTA gives up as a whole: no
+// later wait waits, every warp runs its loops to their end (so that the
+// barriers among threads stay matched) and the status word says so.
+__device__ __forceinline__ void bar_wait(Control &C, uint64_t *bar, uint32_t parity, uint32_t *status) {
+    if (bar_try(bar, parity))
+        return;
+    for (uint32_t k = 0; k < kWaitLimit; k++) {
+        if (bar_try(bar, parity))
+            return;
+        if ((k & 255u) == 255u && *(volatile uint32_t *)&C.gave_up)
+            return;
+    }
+    *(volatile uint32_t *)&C.gave_up = 1;
+    atomicOr(status, LMC_ST_TIMEOUT);
+}
+
+__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+__device__ __forceinline__ void soft_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+
+__device__ __forceinline__ bool soft_any(bool x) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.u32 p, %1, 0;\n\t"
+        "barrier.cta.red.or.pred q, 1, 128, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"((uint32_t)x)
+        : "memory");
+    return r != 0;
+}
+
+__device__ __forceinline__ void tma_3d(const CUtensorMap *map, void *dst, int x, int y, int z, uint64_t *bar) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
+        "[%5];" ::"r"(smem_addr(dst)),
+        "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_addr(bar))
+        : "memory");
+}
+
+// Shared-memory matrix descriptor: 128-byte swizzle, 8-row groups `stride`
+// bytes apart, and (where the summed axis is not the contiguous one) 64-value
+// blocks of the other axis `leading` bytes apart.
+__device__ __forceinline__ uint64_t matrix(uint32_t addr, uint32_t leading, uint32_t stride) {
+    return (uint64_t)((addr >> 4) & 0x3FFF) | (uint64_t)(leading >> 4) << 16 | (uint64_t)(stride >> 4) << 32 |
+           (uint64_t)1 << 46 | (uint64_t)2 << 61;
+}
+
+// f32 accumulators; A and B both f16 or both bf16; `turned`: A is read with
+// its rows' axis contiguous.
+__device__ __forceinline__ uint32_t instruction(bool bf16, bool turned, int m, int n) {
+    const uint32_t t = bf16 ? 1u : 0u;
+    return 1u << 4 | t << 7 | t << 10 | (turned ? 1u << 15 : 0u) | (uint32_t)(n >> 3) << 17 | (uint32_t)(m >> 4) << 24;
+}
+
+__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.u32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
+        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+        : "memory");
+}
+
+__device__ __forceinline__ void commit(uint64_t *bar) {
+    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar))
+                 : "memory");
+}
+
+// 16 lanes x 64 columns: lane l of the warp holds rows l / 4 (s[4j], s[4j+1])
+// and l / 4 + 8 (s[4j+2], s[4j+3]), columns 8j + 2 (l % 4) and the next.
+__device__ __forceinline__ void load_s(uint32_t (&s)[32], uint32_t addr) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x8.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        : "=r"(s[0]), "=r"(s[1]), "=r"(s[2]), "=r"(s[3]), "=r"(s[4]), "=r"(s[5]), "=r"(s[6]), "=r"(s[7]), "=r"(s[8]),
+          "=r"(s[9]), "=r"(s[10]), "=r"(s[11]), "=r"(s[12]), "=r"(s[13]), "=r"(s[14]), "=r"(s[15]), "=r"(s[16]),
+          "=r"(s[17]), "=r"(s[18]), "=r"(s[19]), "=r"(s[20]), "=r"(s[21]), "=r"(s[22]), "=r"(s[23]), "=r"(s[24]),
+          "=r"(s[25]), "=r"(s[26]), "=r"(s[27]), "=r"(s[28]), "=r"(s[29]), "=r"(s[30]), "=r"(s[31])
+        : "r"(addr)
+        : "memory");
+}
+
+// 32 lanes x 16 columns: a lane's row.
+__device__ __forceinline__ void load_o(uint32_t (&o)[16], uint32_t addr) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
+        : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3]), "=r"(o[4]), "=r"(o[5]), "=r"(o[6]), "=r"(o[7]), "=r"(o[8]),
+          "=r"(o[9]), "=r"(o[10]), "=r"(o[11]), "=r"(o[12]), "=r"(o[13]), "=r"(o[14]), "=r"(o[15])
+        : "r"(addr)
+        : "memory");
+}
+
+__device__ __forceinline__ void store_o(const uint32_t (&o)[16], uint32_t addr) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15};" ::"r"(o[0]),
+        "r"(o[1]), "r"(o[2]), "r"(o[3]), "r"(o[4]), "r"(o[5]), "r"(o[6]), "r"(o[7]), "r"(o[8]), "r"(o[9]), "r"(o[10]),
+        "r"(o[11]), "r"(o[12]), "r"(o[13]), "r"(o[14]), "r"(o[15]), "r"(addr)
+        : "memory");
+}
+
+__device__ __forceinline__ float exp2_fast(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+template <bool kBf16>
+__device__ __forceinline__ uint32_t pack(float lo, float hi) {
+    uint32_t r;
+    if (kBf16)
+        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    else
+        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+
+__device__ __forceinline__ uint16_t to_out(float x, bool bf16) {
+    return bf16 ? __bfloat16_as_ushort(__float2bfloat16_rn(x)) : __half_as_ushort(__float2half_rn(x));
+}
+
+__device__ __forceinline__ float from_q(uint32_t h, bool bf16) {
+    return bf16 ? __uint_as_float(h << 16) : __half2float(__ushort_as_half((unsigned short)h));
+}
+
+// ---- the CTA's roles ---------------------------------------------------------
+
+struct Memory {
+    uint8_t *q, *kv, *p;
+    int stage_bytes;
+};
+
+// The block ids of a tile's pages, one per lane, and which rows they and the
+// range leave: a bad page's status bit is raised here.
+__device__ __forceinline__ int resolve(const AttendPlan &P, const Walk &W, const Tile &T, uint64_t &valid, uint32_t &bad) {
+    int block = -1;
+    const int lane = threadIdx.x & 31;
+    const int64_t first = (int64_t)T.page * P.block_size;
+    bool ok = false;
+    if (lane < P.pages_per_tile) {
+        const int64_t p0 = first + (int64_t)lane * P.block_size;  // the page's tokens
+        if (p0 < W.range.L && p0 + P.block_size > W.range.lo) {
+            block = __ldg(P.table + W.r * P.row_stride + T.page + lane);
+            ok = block >= 0 && block < P.num_blocks;
+            if (!ok)
+                bad |= block == -1 ? LMC_ST_NO_BLOCK : LMC_ST_BLOCK_OOR;
+        }
+    }
+    if (!ok)
+        block = -1;
+    const uint32_t pages = __ballot_sync(0xffffffffu, ok);
+    valid = bits((int)(W.range.lo - T.t0 > 64 ? 64 : W.range.lo - T.t0), (int)min((int64_t)T.rows, W.range.L - T.t0));
+    if (P.pages_per_tile == 1) {
+        if (pages == 0)
+            valid = 0;
+    } else {
+        uint64_t have = 0;
+        for (int k = 0; k < P.pages_per_tile; k++)
+            if (pages >> k & 1)
+                have |= bits(k * P.block_size, (k + 1) * P.block_size);
+        valid &= have;
+    }
+    return block;
+}
+
+// One warp: queries and 16-bit entries by TMA.
+__device__ __forceinline__ void load_by_tma(const AttendPlan &P, Control &C, const Memory &M, Walk &W, int group) {
+    const int lane = threadIdx.x & 31;
+    uint32_t bad = 0, n = 0, segments = 0;
+    while (W.next(P)) {
+        if (segments > 0)
+            bar_wait(C, &C.q_free, (segments - 1) & 1, P.status);
+        const int row_panels = (P.E + 63) / 64;
+        if (lane == 0) {
+            bar_expect(&C.q_full, (uint32_t)(row_panels * P.padded_heads * 128));
+            for (int i = 0; i < row_panels; i++)
+                tma_3d(&P.query, M.q + i * P.padded_heads * 128, i * 64, group * P.group_heads, W.r, &C.q_full);
+        }
+        segments++;
+        for (int j = 0; j < W.count; j++, n++) {
+            const int st = n % P.stages;
+            const Tile T = tile_at(P, W.first + j);
+            uint64_t valid;
+            const int block = resolve(P, W, T, valid, bad);
+            const uint32_t pages = __ballot_sync(0xffffffffu, block >= 0);
+            if (n >= (uint32_t)P.stages)
+                bar_wait(C, &C.kv_free[st], (n / P.stages - 1) & 1, P.status);
+            uint8_t *to = M.kv + (size_t)st * M.stage_bytes;
+            if (lane == 0) {
+                C.valid[st] = valid;
+                // rows behind a page's end were filled with zeros, others hold what lies there
+                uint64_t zero = ~valid;
+                if (P.pages_per_tile == 1 && pages != 0)
+                    zero &= bits(0, T.rows);
+                C.zero[st] = zero;
+                const int box = P.pages_per_tile == 1 ? kTile : P.block_size;
+                bar_expect(&C.kv_full[st], (uint32_t)(__popc(pages) * row_panels * box * 128));
+            }
+            __syncwarp();
+            for (int k = 0; k < P.pages_per_tile; k++) {
+                const int b = __shfl_sync(0xffffffffu, block, k);
+                if (lane == 0 && b >= 0)
+                    for (int i = 0; i < row_panels; i++)
+                        tma_3d(&P.cache, to + i * kPanel + k * P.block_size * 128, i * 64,
+                               P.pages_per_tile == 1 ? T.row0 : 0, b, &C.kv_full[st]);
+            }
+        }
     }
     if (bad)
         atomicOr(P.status, bad);
-    __shared__ float s_m[kWarps], s_sum[kWarps], s_acc[kWarps][kMaxValue];
-    if (lane == 0) {
-        s_m[warp] = m;
-        s_sum[warp] = sum;
+    // a CTA that gave up leaves no copy of its own in flight
+    if (*(volatile uint32_t *)&C.gave_up) {
+        for (uint32_t k = n > (uint32_t)P.stages ? n - P.stages : 0; k < n; k++)
+            for (uint32_t i = 0; i < kWaitLimit && !bar_try(&C.kv_full[k % P.stages], (k / P.stages) & 1); i++) {
+            }
+        for (uint32_t i = 0; segments > 0 && i < kWaitLimit && !bar_try(&C.q_full, (segments - 1) & 1); i++) {
+        }
     }
-    for (int i = 0; i < kValPer; i++)
-        s_acc[warp][lane + 32 * i] = acc[i];
+}
+
+// Eight warps: queries to f16 (each head times a power of two that brings its
+// largest value to [2^14, 2^15): exact for values within 2^27 of it), and
+// entries from fp8 to f16. Two groups of four warps take a tile each, so that
+// one group's loads are in flight while the other stores.
+__device__ __forceinline__ void load_fp8(const AttendPlan &P, Control &C, const Memory &M, Walk &W, int group) {
+    const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) - kFirstLoader;
+    const int half = warp >> 2, tid = threadIdx.x - (kFirstLoader + 4 * half) * 32;
+    uint32_t bad = 0, n = 0, segments = 0;
+    const int chunks = P.E / 16;  // of an entry: 16 codes each
+    const uint32_t magic = chunks == 1 ? 0u : (uint32_t)((0x100000000ull + chunks - 1) / chunks);
+    const int total = kTile * chunks;
+    while (W.next(P)) {
+        if (segments > 0)
+            bar_wait(C, &C.q_free, (segments - 1) & 1, P.status);
+        segments++;
+        for (int h = warp; h < P.padded_heads; h += kFp8Loaders) {
+            const int head = group * P.group_heads + h;
+            const bool real = h < P.group_heads && head < P.H;
+            const uint16_t *src = P.q + W.r * P.q_request_stride + head * P.q_head_stride;
+            uint4 v[3];
+            float top = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 3; i++) {
+                const int c = lane + 32 * i;
+                v[i] = make_uint4(0, 0, 0, 0);
+                if (real && c < P.E / 8)
+                    v[i] = __ldg(reinterpret_cast<const uint4 *>(src) + c);
+                const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+                for (int k = 0; k < 4; k++)
+                    top = fmaxf(top, fmaxf(fabsf(from_q(w[k] & 0xffff, P.q_bf16)), fabsf(from_q(w[k] >> 16, P.q_bf16))));
+            }
+            for (int o = 16; o > 0; o >>= 1)
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+            // 2^(14 - exponent of top), kept within what one float holds
+            const int e = top > 0.0f && top < INFINITY ? max(-100, min(100, 14 - ilogbf(top))) : 0;
+            const float up = ldexpf(1.0f, e);
+            if (lane == 0)
+                C.q_scale[h] = ldexpf(1.0f, -e);
+#pragma unroll
+            for (int i = 0; i < 3; i++) {
+                const int c = lane + 32 * i;
+                if (c < P.E / 8) {
+                    const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+                    uint32_t o[4];
+#pragma unroll
+                    for (int k = 0; k < 4; k++)
+                        o[k] = pack<false>(from_q(w[k] & 0xffff, P.q_bf16) * up, from_q(w[k] >> 16, P.q_bf16) * up);
+                    *reinterpret_cast<uint4 *>(M.q + (c >> 3) * P.padded_heads * 128 + h * 128 +
+                                               (((c & 7) ^ (h & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+                }
+            }
+        }
+        fence_async();
+        __syncwarp();
+        if (lane == 0)
+            bar_arrive(&C.q_full);
+        for (int j = 0; j < W.count; j++, n++) {
+            if ((int)(n & 1) != half)
+                continue;
+            const int st = n % P.stages;
+            const Tile T = tile_at(P, W.first + j);
+            uint64_t valid;
+            const int block = resolve(P, W, T, valid, bad);
+            // up to 64 * 36 chunks over 128 threads
+            uint4 v[18];
+#pragma unroll
+            for (int i = 0; i < 18; i++) {
+                const int c = tid + 128 * i;
+                v[i] = make_uint4(0, 0, 0, 0);
+                const int row = chunks == 1 ? c : (int)__umulhi((uint32_t)c, magic);
+                const int k = P.pages_per_tile == 1 ? 0 : row / P.block_size;
+                const int b = __shfl_sync(0xffffffffu, block, k & 31);
+                if (c < total && (valid >> (row & 63) & 1)) {
+                    const int64_t in_page = T.row0 + row - k * P.block_size;
+                    const uint8_t *src = P.pool + (int64_t)b * P.block_stride + in_page * P.token_bytes +
+                                         (c - row * chunks) * 16;
+                    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+                                 : "=r"(v[i].x), "=r"(v[i].y), "=r"(v[i].z), "=r"(v[i].w)
+                                 : "l"(src));
+                }
+            }
+            if (n >= (uint32_t)P.stages)
+                bar_wait(C, &C.kv_free[st], (n / P.stages - 1) & 1, P.status);
+            uint8_t *to = M.kv + (size_t)st * M.stage_bytes;
+#pragma unroll
+            for (int i = 0; i < 18; i++) {
+                const int c = tid + 128 * i;
+                const int row = chunks == 1 ? c : (int)__umulhi((uint32_t)c, magic);
+                const int ch = c - row * chunks;
+                if (c < total) {
+                    const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+                    uint32_t o[8];
+#pragma unroll
+                    for (int k = 0; k < 8; k++)
+                        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(o[k]) : "h"((unsigned short)(w[k >> 1] >> (16 * (k & 1)))));
+                    uint8_t *at = to + (ch >> 2) * kPanel + row * 128;
+                    const int c0 = (ch & 3) * 2, x = row & 7;
+                    *reinterpret_cast<uint4 *>(at + ((c0 ^ x) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
+                    *reinterpret_cast<uint4 *>(at + (((c0 + 1) ^ x) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
+                }
+            }
+            if (tid == 0) {
+                C.valid[st] = valid;
+                C.zero[st] = 0;  // the rows left out hold zeros
+            }
+            fence_async();
+            __syncwarp();
+            if (lane == 0)
+                bar_arrive(&C.kv_full[st]);
+        }
+    }
+    if (bad)
+        atomicOr(P.status, bad);
+}
+
+// One warp: issues the products.
+template <bool kBf16>
+__device__ __forceinline__ void multiply(const AttendPlan &P, Control &C, const Memory &M, Walk &W) {
+    const int lane = threadIdx.x & 31;
+    const uint32_t tmem = C.tmem;
+    const uint32_t qk = instruction(kBf16, false, 64, kTile);
+    const uint32_t pv = instruction(kBf16, true, 128, P.padded_heads);
+    const uint32_t q = smem_addr(M.q), p = smem_addr(M.p);
+    uint32_t n = 0, segments = 0;
+
+    auto values = [&](uint32_t k, bool begins) {  // O^T += V^T P^T of the CTA's k-th tile
+        if (begins && segments > 0)
+            bar_wait(C, &C.o_free, (segments - 1) & 1, P.status);
+        bar_wait(C, &C.p_full, k & 1, P.status);
+        fence_after();
+        const int st = k % P.stages;
+        if (lane == 0) {
+            const uint32_t kv = smem_addr(M.kv) + st * M.stage_bytes;
+            for (int t = 0; t < P.value_tiles; t++)
+#pragma unroll
+                for (int s = 0; s < kTile / 16; s++)
+                    mma(tmem + 128 + t * P.padded_heads, matrix(kv + 2 * t * kPanel + s * 2048, kPanel, 1024),
+                        matrix(p + s * 32, 16, 1024), pv, !(begins && s == 0));
+            commit(&C.kv_free[st]);
+            commit(&C.pv_done);
+        }
+        __syncwarp();
+    };
+
+    while (W.next(P)) {
+        bar_wait(C, &C.q_full, segments & 1, P.status);
+        bool pending = false;
+        for (int j = 0; j < W.count; j++, n++) {
+            const int st = n % P.stages;
+            // whichever is ready first: this tile, or the last one's values
+            if (pending) {
+                for (uint32_t k = 0; k < kWaitLimit; k++) {
+                    const bool full = __shfl_sync(0xffffffffu, (int)bar_try(&C.kv_full[st], (n / P.stages) & 1), 0);
+                    if (full)
+                        break;
+                    const bool ready = __shfl_sync(0xffffffffu, (int)bar_try(&C.p_full, (n - 1) & 1), 0);
+                    if (ready) {
+                        values(n - 1, j == 1);
+                        pending = false;
+                        break;
+                    }
+                    if ((k & 255u) == 255u && __shfl_sync(0xffffffffu, (int)*(volatile uint32_t *)&C.gave_up, 0))
+                        break;
+                }
+            }
+            bar_wait(C, &C.kv_full[st], (n / P.stages) & 1, P.status);
+            if (n >= 2)
+                bar_wait(C, &C.s_free[n & 1], (n / 2 - 1) & 1, P.status);
+            fence_after();
+            if (lane == 0) {
+                const uint32_t kv = smem_addr(M.kv) + st * M.stage_bytes;
+                for (int s = 0; s < P.E / 16; s++)
+                    mma(tmem + (n & 1) * 64, matrix(q + (s >> 2) * P.padded_heads * 128 + (s & 3) * 32, 16, 1024),
+                        matrix(kv + (s >> 2) * kPanel + (s & 3) * 32, 16, 1024), qk, s > 0);
+                commit(&C.s_full[n & 1]);
+                if (j == W.count - 1)
+                    commit(&C.q_free);
+            }
+            __syncwarp();
+            if (pending)
+                values(n - 1, j == 1);
+            pending = true;
+        }
+        values(n - 1, W.count == 1);
+        segments++;
+    }
+}
+
+// Four warps: the softmax, P, and the results. Warp w holds heads 16 w ..
+// 16 w + 15 of S, and values 32 w .. 32 w + 31 of each 128 of O^T.
+template <bool kBf16, bool kFp8>
+__device__ __forceinline__ void soften(const AttendPlan &P, Control &C, const Memory &M, Walk &W, int col, int group) {
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const uint32_t lanes = C.tmem + ((uint32_t)(warp * 32) << 16);
+    const int ra = warp * 16 + lane / 4, rb = ra + 8;  // this thread's heads
+    const bool active = warp * 16 < P.padded_heads;
+    const int head0 = group * P.group_heads;
+    const int heads = min(P.group_heads, P.H - head0);
+    uint32_t n = 0, segments = 0;
+    int2 left[2] = {make_int2(-1, 0), make_int2(-1, 0)};  // what the CTA leaves unfinished
+
+    while (W.next(P)) {
+        float ma = -INFINITY, mb = -INFINITY, la = 0.0f, lb = 0.0f;
+        float ca = P.log2_scale, cb = P.log2_scale;
+        for (int j = 0; j < W.count; j++, n++) {
+            const int st = n % P.stages;
+            const Tile T = tile_at(P, W.first + j);
+            bar_wait(C, &C.kv_full[st], (n / P.stages) & 1, P.status);
+            if (kFp8 && j == 0) {
+                bar_wait(C, &C.q_full, segments & 1, P.status);
+                if (active) {
+                    ca = P.log2_scale * C.q_scale[ra];
+                    cb = P.log2_scale * C.q_scale[rb];
+                }
+                __syncwarp();
+                if (lane == 0)
+                    bar_arrive(&C.q_free);
+            }
+            const uint64_t valid = C.valid[st], zero = C.zero[st];
+            bar_wait(C, &C.s_full[n & 1], (n >> 1) & 1, P.status);
+            fence_after();
+            uint32_t raw[32];
+            float *s = reinterpret_cast<float *>(raw);
+            float xa = -INFINITY, xb = -INFINITY;
+            if (active) {
+                load_s(raw, lanes + (n & 1) * 64);
+                wait_ld();
+            }
+            fence_before();
+            __syncwarp();
+            if (lane == 0)
+                bar_arrive(&C.s_free[n & 1]);
+            if (active) {
+#pragma unroll
+                for (int i = 0; i < 32; i++)
+                    s[i] *= (i & 2) ? cb : ca;
+                if (valid != ~0ull) {
+                    const uint64_t mine = valid >> (2 * (lane & 3));
+#pragma unroll
+                    for (int i = 0; i < 32; i++)
+                        if (!(mine >> (8 * (i >> 2) + (i & 1)) & 1))
+                            s[i] = -INFINITY;
+                }
+#pragma unroll
+                for (int i = 0; i < 32; i += 4) {
+                    xa = fmaxf(xa, fmaxf(s[i], s[i + 1]));
+                    xb = fmaxf(xb, fmaxf(s[i + 2], s[i + 3]));
+                }
+                xa = fmaxf(xa, __shfl_xor_sync(0xffffffffu, xa, 1));
+                xb = fmaxf(xb, __shfl_xor_sync(0xffffffffu, xb, 1));
+                xa = fmaxf(xa, __shfl_xor_sync(0xffffffffu, xa, 2));
+                xb = fmaxf(xb, __shfl_xor_sync(0xffffffffu, xb, 2));
+                if (P.logits != nullptr) {
+                    const int64_t base = W.range.lo & ~(int64_t)1;
+                    float *to = P.logits + ((int64_t)W.r * P.H + head0) * P.logit_stride + (T.t0 - base);
+                    const uint64_t inside = bits((int)max((int64_t)0, W.range.lo - T.t0),
+                                                 (int)min((int64_t)T.rows, W.range.L - T.t0));
+#pragma unroll
+                    for (int i = 0; i < 32; i++) {
+                        const int c = 8 * (i >> 2) + 2 * (lane & 3) + (i & 1), row = (i & 2) ? rb : ra;
+                        if ((inside >> c & 1) && row < heads)
+                            to[row * P.logit_stride + c] = s[i];
+                    }
+                }
+            }
+            if (soft_any(xa > ma + kLag || xb > mb + kLag)) {
+                float fa = 1.0f, fb = 1.0f;
+                if (xa > ma + kLag) {
+                    fa = exp2_fast(ma - xa);
+                    ma = xa;
+                }
+                if (xb > mb + kLag) {
+                    fb = exp2_fast(mb - xb);
+                    mb = xb;
+                }
+                la *= fa;
+                lb *= fb;
+                if (j > 0) {
+                    if (active && (lane & 3) == 0) {
+                        C.factor[ra] = fa;
+                        C.factor[rb] = fb;
+                    }
+                    soft_sync();
+                    bar_wait(C, &C.pv_done, (n - 1) & 1, P.status);
+                    fence_after();
+                    for (int t = 0; t < P.value_tiles; t++)
+                        for (int c = 0; c < P.padded_heads; c += 16) {
+                            uint32_t o[16];
+                            const uint32_t at = lanes + 128 + t * P.padded_heads + c;
+                            load_o(o, at);
+                            wait_ld();
+#pragma unroll
+                            for (int k = 0; k < 16; k++)
+                                o[k] = __float_as_uint(__uint_as_float(o[k]) * C.factor[c + k]);
+                            store_o(o, at);
+                        }
+                    wait_st();
+                    fence_before();
+                    soft_sync();  // the factors may be written again
+                }
+            }
+            // P and the cleared rows go where the last tile's product read
+            if (n > 0)
+                bar_wait(C, &C.pv_done, (n - 1) & 1, P.status);
+            if (active) {
+                const float na = ma == -INFINITY ? 0.0f : ma, nb = mb == -INFINITY ? 0.0f : mb;
+                uint8_t *const pa = M.p + ra * 128 + 4 * (lane & 3), *const pb = M.p + rb * 128 + 4 * (lane & 3);
+                const int x = ra & 7;  // rb & 7 is the same
+#pragma unroll
+                for (int i = 0; i < 8; i++) {
+                    const float p0 = exp2_fast(s[4 * i] - na), p1 = exp2_fast(s[4 * i + 1] - na);
+                    const float p2 = exp2_fast(s[4 * i + 2] - nb), p3 = exp2_fast(s[4 * i + 3] - nb);
+                    la += p0 + p1;
+                    lb += p2 + p3;
+                    *reinterpret_cast<uint32_t *>(pa + ((i ^ x) << 4)) = pack<kBf16>(p0, p1);
+                    *reinterpret_cast<uint32_t *>(pb + ((i ^ x) << 4)) = pack<kBf16>(p2, p3);
+                }
+            }
+            if (!kFp8 && zero != 0) {
+                // tokens that are not attended take part with p = 0: their
+                // values must not be infinite or NaN
+                uint8_t *kv = M.kv + (size_t)st * M.stage_bytes;
+                const int row = threadIdx.x & 63;
+                if (zero >> row & 1)
+                    for (int i = threadIdx.x >> 6; i < 2 * P.value_tiles; i += 2)
+                        for (int c = 0; c < 8; c++)
+                            *reinterpret_cast<uint4 *>(kv + i * kPanel + row * 128 + c * 16) = make_uint4(0, 0, 0, 0);
+            }
+            fence_async();
+            __syncwarp();
+            if (lane == 0)
+                bar_arrive(&C.p_full);
+        }
+
+        // the segment's end
+        la += __shfl_xor_sync(0xffffffffu, la, 1);
+        lb += __shfl_xor_sync(0xffffffffu, lb, 1);
+        la += __shfl_xor_sync(0xffffffffu, la, 2);
+        lb += __shfl_xor_sync(0xffffffffu, lb, 2);
+        const bool whole = W.begins && W.ends;
+        const int slot = 2 * col + (W.begins ? 1 : 0);
+        if (active && (lane & 3) == 0) {
+            const float na = ma == -INFINITY ? 0.0f : ma, nb = mb == -INFINITY ? 0.0f : mb;
+            C.inverse[ra] = whole ? (la == 0.0f ? 0.0f : P.scale / la) : P.scale;
+            C.inverse[rb] = whole ? (lb == 0.0f ? 0.0f : P.scale / lb) : P.scale;
+            for (int k = 0; k < 2; k++) {
+                const int row = k ? rb : ra;
+                const float m = k ? nb : na, l = k ? lb : la;
+                if (row >= heads)
+                    continue;
+                const int h = head0 + row;
+                if (whole) {
+                    const float lse = l == 0.0f ? -INFINITY : m + log2f(l);
+                    P.lse2[(int64_t)W.r * P.H + h] = lse;
+                    if (P.lse != nullptr)
+                        P.lse[W.r * P.lse_request_stride + h] = lse * 0.693147180559945309f;
+                } else {
+                    P.part_ml[(int64_t)slot * P.H + h] = make_float2(m, l);
+                }
+            }
+        }
+        if (!whole)
+            left[slot & 1] = make_int2(W.r, W.count);
+        soft_sync();
+        bar_wait(C, &C.pv_done, (n - 1) & 1, P.status);
+        fence_after();
+        for (int t = 0; t < P.value_tiles; t++) {
+            const int v = t * 128 + warp * 32 + lane;
+            for (int c = 0; c < P.padded_heads; c += 16) {
+                uint32_t o[16];
+                load_o(o, lanes + 128 + t * P.padded_heads + c);
+                wait_ld();
+                if (v < P.V) {
+                    if (whole) {
+                        uint16_t *to = P.out + W.r * P.out_request_stride + (int64_t)(head0 + c) * P.out_head_stride + v;
+#pragma unroll
+                        for (int k = 0; k < 16; k++)
+                            if (c + k < heads)
+                                to[k * P.out_head_stride] =
+                                    to_out(__uint_as_float(o[k]) * C.inverse[c + k], P.q_bf16);
+                    } else {
+                        float *to = P.part_o + ((int64_t)slot * P.H + head0 + c) * P.V + v;
+#pragma unroll
+                        for (int k = 0; k < 16; k++)
+                            if (c + k < heads)
+                                to[k * P.V] = __uint_as_float(o[k]) * C.inverse[c + k];
+                    }
+                }
+            }
+        }
+        fence_before();
+        soft_sync();  // the inverses may be written again
+        if (lane == 0)
+            bar_arrive(&C.o_free);
+        segments++;
+    }
+    if (threadIdx.x == 0 && group == 0) {
+        P.segment[2 * col] = left[0];
+        P.segment[2 * col + 1] = left[1];
+    }
+}
+
+template <bool kBf16, bool kFp8>
+__global__ void __launch_bounds__((kFirstLoader + (kFp8 ? kFp8Loaders : 1)) * 32, 1) lmc_attend_kernel(const __grid_constant__ AttendPlan P) {
+    extern __shared__ __align__(1024) uint8_t attend_mem[];
+    __shared__ Control C;
+    const int warp = threadIdx.x >> 5;
+    const int group = blockIdx.x % P.head_groups, col = blockIdx.x / P.head_groups;
+    Memory M;
+    M.q = attend_mem;
+    M.stage_bytes = P.panels * kPanel;
+    M.kv = M.q + (size_t)((P.E + 63) / 64) * P.padded_heads * 128;
+    M.p = M.kv + (size_t)P.stages * M.stage_bytes;
+    if (threadIdx.x == 0) {
+        bar_init(&C.q_full, kFp8 ? kFp8Loaders : 1);
+        bar_init(&C.q_free, kFp8 ? 1 + kSoftWarps : 1);  // the products', and the readers of q_scale
+        for (int i = 0; i < P.stages; i++) {
+            bar_init(&C.kv_full[i], kFp8 ? 4 : 1);
+            bar_init(&C.kv_free[i], 1);
+        }
+        for (int i = 0; i < 2; i++) {
+            bar_init(&C.s_full[i], 1);
+            bar_init(&C.s_free[i], kSoftWarps);
+        }
+        bar_init(&C.p_full, kSoftWarps);
+        bar_init(&C.pv_done, 1);
+        bar_init(&C.o_free, kSoftWarps);
+        C.gave_up = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+        fence_async();
+    }
+    if (warp == kMmaWarp) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(&C.tmem))
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
+    fence_before();
     __syncthreads();
-    float top = -INFINITY, total = 0.0f;
-    for (int w = 0; w < kWarps; w++)
-        top = fmaxf(top, s_m[w]);
-    for (int w = 0; w < kWarps; w++)
-        total += s_sum[w] == 0.0f ? 0.0f : s_sum[w] * expf(s_m[w] - top);
-    for (int v = threadIdx.x; v < P.V; v += blockDim.x) {
-        float x = 0.0f;
-        for (int w = 0; w < kWarps; w++)
-            x += s_sum[w] == 0.0f ? 0.0f : s_acc[w][v] * expf(s_m[w] - top);
-        x = total == 0.0f ? 0.0f : x / total;
-        P.out[r * P.out_request_stride + h * P.out_head_stride + v] =
-            P.q_dtype == LMC_E_BF16 ? __bfloat16_as_ushort(__float2bfloat16_rn(x)) : __half_as_ushort(__float2half_rn(x));
+    fence_after();
+
+    Walk W;
+    W.init(P, col);
+    if (warp < kSoftWarps)
+        soften<kBf16, kFp8>(P, C, M, W, col, group);
+    else if (warp == kMmaWarp)
+        multiply<kBf16>(P, C, M, W);
+    else if (kFp8)
+        load_fp8(P, C, M, W, group);
+    else
+        load_by_tma(P, C, M, W, group);
+    // lengths that cannot be served
+    if (blockIdx.x == 0)
+        for (int r = threadIdx.x; r < P.R; r += blockDim.x)
+            if (!range_of(P, r).ok)
+                atomicOr(P.status, LMC_ST_BAD_JOB);
+    fence_before();
+    __syncthreads();
+    fence_after();
+    if (warp == kMmaWarp)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(C.tmem));
+}
+
+// ---- joining -------------------------------------------------------------------
+
+constexpr int kJoinThreads = 128;
+
+// Block (c, h): if a request that spans several CTAs begins in CTA column c,
+// joins its parts for head h; and writes the rows of requests without tokens
+// (r = c, c + cols, ...).
+__global__ void __launch_bounds__(kJoinThreads) lmc_attend_join_kernel(const __grid_constant__ AttendPlan P) {
+    const int col = blockIdx.x, h = blockIdx.y;
+    for (int r = col; r < P.R; r += P.cols) {
+        const Range g = range_of(P, r);
+        if (!g.ok || g.L != 0)
+            continue;
+        for (int v = threadIdx.x; v < P.V; v += kJoinThreads)
+            P.out[r * P.out_request_stride + h * P.out_head_stride + v] = 0;
+        if (threadIdx.x == 0 && P.lse != nullptr)
+            P.lse[r * P.lse_request_stride + h] = -INFINITY;
+    }
+    const int r = P.segment[2 * col + 1].x;
+    if (r < 0)
+        return;
+    // parts: slot 2 col + 1, then 2 (col + 1), ...; all CTAs but the last have
+    // as many tiles as the next one
+    const int rest = tiles_of(P, range_of(P, r)) - P.segment[2 * col + 1].y;
+    int last = col + 1;
+    if (rest > 0 && last < P.cols && P.segment[2 * last].x == r) {
+        const int each = max(1, P.segment[2 * last].y);
+        last = min(P.cols, last + (rest + each - 1) / each);
+    }
+    float top = -INFINITY;
+    for (int c = col; c < last; c++) {
+        const float2 ml = P.part_ml[(int64_t)(2 * c + (c == col)) * P.H + h];
+        if (ml.y != 0.0f)
+            top = fmaxf(top, ml.x);
+    }
+    float sum = 0.0f, acc[kMaxValue / kJoinThreads] = {};
+    for (int c = col; c < last; c++) {
+        const int64_t at = (int64_t)(2 * c + (c == col)) * P.H + h;
+        const float2 ml = P.part_ml[at];
+        if (ml.y == 0.0f)
+            continue;
+        const float f = exp2_fast(ml.x - top);
+        sum += ml.y * f;
+#pragma unroll
+        for (int i = 0; i < kMaxValue / kJoinThreads; i++) {
+            const int v = threadIdx.x + i * kJoinThreads;
+            if (v < P.V)
+                acc[i] += P.part_o[at * P.V + v] * f;
+        }
+    }
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+#pragma unroll
+    for (int i = 0; i < kMaxValue / kJoinThreads; i++) {
+        const int v = threadIdx.x + i * kJoinThreads;
+        if (v < P.V)
+            P.out[r * P.out_request_stride + h * P.out_head_stride + v] = to_out(acc[i] * inv, P.q_bf16);
     }
     if (threadIdx.x == 0) {
-        const float lse = total == 0.0f ? -INFINITY : top + logf(total);
-        P.lse_all[r * P.H + h] = lse;
+        const float lse = sum == 0.0f ? -INFINITY : top + log2f(sum);
+        P.lse2[(int64_t)r * P.H + h] = lse;
         if (P.lse != nullptr)
-            P.lse[r * P.lse_request_stride + h] = lse;
+            P.lse[r * P.lse_request_stride + h] = lse * 0.693147180559945309f;
     }
 }
 
-// One warp per token: the sum over the heads of its probability.
-__global__ void __launch_bounds__(32 * kWarps) lmc_attend_weights_kernel(const __grid_constant__ AttendPlan P) {
-    const int64_t r = blockIdx.y;
-    const int lane = threadIdx.x & 31;
-    int64_t lo, L;
-    if (!token_range(P, r, lo, L))
+constexpr int kWeightThreads = 256;
+
+// A thread per token: the sum over the heads of 2^(logit - lse).
+__global__ void __launch_bounds__(kWeightThreads) lmc_attend_weights_kernel(const __grid_constant__ AttendPlan P) {
+    const int r = blockIdx.y;
+    const Range g = range_of(P, r);
+    if (!g.ok)
         return;
-    for (int64_t t = lo + blockIdx.x * (int64_t)kWarps + (threadIdx.x >> 5); t < L; t += (int64_t)gridDim.x * kWarps) {
-        uint32_t bad = 0;
-        const uint8_t *e = entry_at(P, r, t, bad);
-        if (e == nullptr)
-            continue;
-        float v[kPer];
-#pragma unroll
-        for (int i = 0; i < kPer; i++)
-            v[i] = lane + 32 * i < P.E ? load_entry(e, lane + 32 * i, P) : 0.0f;
-        float w = 0.0f;
-        for (int h = 0; h < P.H; h++) {
-            const uint16_t *q = P.q + r * P.q_request_stride + h * P.q_head_stride;
-            float dot = 0.0f;
-#pragma unroll
-            for (int i = 0; i < kPer; i++)
-                if (lane + 32 * i < P.E)
-                    dot = fmaf(load16(q[lane + 32 * i], P.q_dtype), v[i], dot);
-            for (int o = 16; o > 0; o >>= 1)
-                dot += __shfl_xor_sync(0xffffffffu, dot, o);
-            w += expf(dot * P.softmax_scale - P.lse_all[r * P.H + h]);
-        }
-        if (lane == 0)
-            P.weights[r * P.weights_request_stride + t] += w;
+    const int64_t t = g.lo + blockIdx.x * (int64_t)kWeightThreads + threadIdx.x;
+    if (t >= g.L)
+        return;
+    const float *x = P.logits + (int64_t)r * P.H * P.logit_stride + (t - (g.lo & ~(int64_t)1));
+    const float *lse = P.lse2 + (int64_t)r * P.H;
+    float w = 0.0f;
+#pragma unroll 4
+    for (int h = 0; h < P.H; h++) {
+        const float top = __ldg(lse + h);
+        const float p = exp2_fast(__ldcs(x + h * P.logit_stride) - top);
+        w += top == -INFINITY ? 0.0f : p;
     }
+    P.weights[r * P.weights_request_stride + t] += w;
 }
+
+// ---- host ------------------------------------------------------------------------
 
 bool aligned16(int64_t x) { return (x & 15) == 0; }
+
+struct Work {
+    int32_t cols, head_groups, group_heads;
+    int64_t logit_stride;
+    int64_t segment, part_ml, part_o, lse2, logits, bytes;  // offsets
+};
+
+int work_space(const lmc_layout *L, int32_t layer, int64_t R, int64_t H, int64_t V, int64_t max_length, bool weights,
+               Work &W) {
+    if (L == nullptr || layer < 0 || (size_t)layer >= L->desc.size() || L->specs[layer].kind == LMC_LAYER_KDA ||
+        R < 0 || R > 65535 || H <= 0 || H > 65535 || V <= 0 || V > kMaxValue || max_length <= 0 ||
+        max_length > INT32_MAX)
+        return LMC_ERR_INVALID_ARG;
+    W.head_groups = (int32_t)((H + kMaxHeads - 1) / kMaxHeads);
+    W.group_heads = (int32_t)((H + W.head_groups - 1) / W.head_groups);
+    W.cols = std::max(1, kMaxCols / W.head_groups);
+    const int64_t window = L->specs[layer].window;
+    const int64_t tokens = window > 0 ? std::min(max_length, window) : max_length;
+    W.logit_stride = (tokens + 1 + 3) / 4 * 4;
+    int64_t at = 0;
+    auto take = [&](int64_t bytes) {
+        const int64_t here = at;
+        at += (bytes + 255) / 256 * 256;
+        return here;
+    };
+    W.segment = take(2 * W.cols * 8);
+    W.part_ml = take(2 * W.cols * H * 8);
+    W.part_o = take(2 * W.cols * H * V * 4);
+    W.lse2 = take(R * H * 4);
+    int64_t logits = 0;
+    if (weights && (!lmc::mul_ok(R * H, W.logit_stride, &logits) || !lmc::mul_ok(logits, 4, &logits) ||
+                    logits > INT64_MAX / 2))
+        return LMC_ERR_OVERFLOW;
+    W.logits = take(logits);
+    W.bytes = at;
+    return LMC_OK;
+}
+
+using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
+                                 const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
+                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+
+EncodeTiled encoder() {
+    static const EncodeTiled fn = [] {
+        void *p = nullptr;
+        cudaDriverEntryPointQueryResult found;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &found) !=
+                cudaSuccess ||
+            found != cudaDriverEntryPointSuccess)
+            p = nullptr;
+        return reinterpret_cast<EncodeTiled>(p);
+    }();
+    return fn;
+}
+
+// (values, rows, slices) of 16 bits each, read in boxes of 64 x `box` x 1.
+bool tensor_map(CUtensorMap *map, bool bf16, const void *base, int64_t values, int64_t rows, int64_t slices,
+                int64_t row_bytes, int64_t slice_bytes, int box) {
+    const EncodeTiled fn = encoder();
+    if (fn == nullptr)
+        return false;
+    const cuuint64_t dims[3] = {(cuuint64_t)values, (cuuint64_t)rows, (cuuint64_t)slices};
+    const cuuint64_t strides[2] = {(cuuint64_t)row_bytes, (cuuint64_t)slice_bytes};
+    const cuuint32_t boxes[3] = {64, (cuuint32_t)box, 1};
+    const cuuint32_t steps[3] = {1, 1, 1};
+    return fn(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
+              const_cast<void *>(base), dims, strides, boxes, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
 
 }  // namespace
 
 extern "C" int lmc_attend_workspace(const lmc_layout *L, int32_t layer, int32_t num_requests, int32_t num_heads,
                                     int32_t value_dim, int64_t max_length, int with_weights, int64_t *out) {
-    (void)with_weights;
-    if (L == nullptr || out == nullptr || layer < 0 || (size_t)layer >= L->desc.size() ||
-        L->specs[layer].kind == LMC_LAYER_KDA || num_requests < 0 || num_heads <= 0 || value_dim <= 0 ||
-        value_dim > kMaxValue || max_length <= 0 || max_length > INT32_MAX)
+    Work W;
+    if (out == nullptr)
         return LMC_ERR_INVALID_ARG;
-    int64_t n;
-    if (!lmc::mul_ok((int64_t)num_requests * 4, num_heads, &n))
-        return LMC_ERR_OVERFLOW;
-    *out = n;
-    return LMC_OK;
+    const int rc = work_space(L, layer, num_requests, num_heads, value_dim, max_length, with_weights != 0, W);
+    if (rc == LMC_OK)
+        *out = W.bytes;
+    return rc;
 }
 
 extern "C" int lmc_attend(const lmc_layout *L, const lmc_entries *e, const void *pool, const lmc_attention *a,
@@ -208,22 +1151,21 @@ extern "C" int lmc_attend(const lmc_layout *L, const lmc_entries *e, const void 
     if (a == nullptr || status == nullptr || (a->q_dtype != LMC_E_BF16 && a->q_dtype != LMC_E_F16) ||
         (e->dtype != LMC_E_E4M3 && e->dtype != a->q_dtype) || e->entry_dim % 16 != 0 || e->entry_dim > kMaxEntry ||
         a->num_heads <= 0 || a->value_dim <= 0 || a->value_dim % 8 != 0 || a->value_dim > e->entry_dim ||
-        a->value_dim > kMaxValue || !std::isfinite(a->softmax_scale) || a->max_length <= 0 ||
-        a->max_length > INT32_MAX)
+        a->value_dim > kMaxValue || !std::isfinite(a->softmax_scale))
         return LMC_ERR_INVALID_ARG;
     const int64_t R = e->num_requests, H = a->num_heads;
     if (a->q_request_stride < 0 || a->q_head_stride < 0 || a->out_request_stride < 0 || a->out_head_stride < 0 ||
-        a->q_request_stride % 8 != 0 || a->q_head_stride % 8 != 0 || (H > 1 && a->out_head_stride < a->value_dim) ||
-        (R > 1 && a->out_request_stride < a->value_dim) ||
-        (a->lse != nullptr && a->lse_request_stride < H) ||
+        a->q_request_stride % 8 != 0 || a->q_head_stride % 8 != 0 || (H > 1 && a->q_head_stride == 0) ||
+        (R > 1 && a->q_request_stride == 0) || (H > 1 && a->out_head_stride < a->value_dim) ||
+        (R > 1 && a->out_request_stride < a->value_dim) || (a->lse != nullptr && a->lse_request_stride < H) ||
         (a->weights != nullptr && a->weights_request_stride < a->max_length))
         return LMC_ERR_INVALID_ARG;
-    int64_t need;
-    if (const int rc = lmc_attend_workspace(L, e->layer, e->num_requests, a->num_heads, a->value_dim, a->max_length,
-                                            a->weights != nullptr, &need); rc != LMC_OK)
+    Work W;
+    if (const int rc = work_space(L, e->layer, R, H, a->value_dim, a->max_length, a->weights != nullptr, W);
+        rc != LMC_OK)
         return rc;
     if (R > 0 && (pool == nullptr || a->lengths == nullptr || a->q == nullptr || a->out == nullptr ||
-                  workspace == nullptr || workspace_bytes < need))
+                  workspace == nullptr || workspace_bytes < W.bytes))
         return LMC_ERR_INVALID_ARG;
     const lmc_layer_desc &d = L->desc[e->layer];
     if ((((uintptr_t)status | (uintptr_t)a->lengths | (uintptr_t)a->lse | (uintptr_t)a->weights) & 3) != 0 ||
@@ -232,18 +1174,20 @@ extern "C" int lmc_attend(const lmc_layout *L, const lmc_entries *e, const void 
         return LMC_ERR_ALIGN;
     if (R == 0)
         return LMC_OK;
+    const int sms = lmc::sm_count();
+    if (sms <= 0)
+        return LMC_ERR_CUDA;
+    const bool fp8 = e->dtype == LMC_E_E4M3, bf16 = a->q_dtype == LMC_E_BF16;
+    const int64_t N = L->block_size;
     AttendPlan P = {};
     P.pool = static_cast<const uint8_t *>(pool) + d.base;
     P.block_stride = d.stride;
     P.num_blocks = L->num_blocks;
-    P.block_size = (int32_t)L->block_size;
-    P.token_bytes = (int32_t)L->specs[e->layer].token_bytes;
     P.table = e->table.table;
     P.row_stride = e->table.row_stride;
     P.num_cols = e->table.num_cols;
     P.lengths = a->lengths;
     P.max_length = a->max_length;
-    P.window = L->specs[e->layer].kind == LMC_LAYER_SWA ? L->specs[e->layer].window : 0;
     P.q = static_cast<const uint16_t *>(a->q);
     P.q_request_stride = a->q_request_stride;
     P.q_head_stride = a->q_head_stride;
@@ -254,22 +1198,60 @@ extern "C" int lmc_attend(const lmc_layout *L, const lmc_entries *e, const void 
     P.lse_request_stride = a->lse_request_stride;
     P.weights = a->weights;
     P.weights_request_stride = a->weights_request_stride;
-    P.lse_all = static_cast<float *>(workspace);
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    P.segment = reinterpret_cast<int2 *>(ws + W.segment);
+    P.part_ml = reinterpret_cast<float2 *>(ws + W.part_ml);
+    P.part_o = reinterpret_cast<float *>(ws + W.part_o);
+    P.lse2 = reinterpret_cast<float *>(ws + W.lse2);
+    P.logits = a->weights != nullptr ? reinterpret_cast<float *>(ws + W.logits) : nullptr;
+    P.logit_stride = W.logit_stride;
     P.status = status;
-    P.softmax_scale = a->softmax_scale;
-    P.scale = e->scale;
+    P.R = (int32_t)R;
+    P.H = (int32_t)H;
     P.E = e->entry_dim;
     P.V = a->value_dim;
-    P.H = a->num_heads;
-    P.dtype = e->dtype;
-    P.q_dtype = a->q_dtype;
-    if (R > 65535 || H > 65535)
-        return LMC_ERR_INVALID_ARG;
+    P.window = L->specs[e->layer].kind == LMC_LAYER_SWA ? L->specs[e->layer].window : 0;
+    P.block_size = (int32_t)N;
+    P.token_bytes = (int32_t)L->specs[e->layer].token_bytes;
+    // several small pages share a tile where each fills whole 8-row groups of it
+    P.pages_per_tile = N < kTile && N % 8 == 0 ? (int32_t)(kTile / N) : 1;
+    P.span = (int32_t)N * P.pages_per_tile;
+    P.tiles_per_span = (P.span + kTile - 1) / kTile;
+    P.head_groups = W.head_groups;
+    P.group_heads = W.group_heads;
+    P.cols = std::max(1, std::min(W.cols, sms / W.head_groups));
+    P.padded_heads = (P.group_heads + 15) / 16 * 16;
+    P.value_tiles = (P.V + 127) / 128;
+    P.panels = std::max((P.E + 63) / 64, 2 * P.value_tiles);
+    P.q_bf16 = bf16;
+    P.scale = e->scale;
+    P.log2_scale = (float)((double)a->softmax_scale * e->scale * 1.4426950408889634);
+    const int64_t fixed = (int64_t)((P.E + 63) / 64) * P.padded_heads * 128 + P.padded_heads * 128 + sizeof(Control) + 1024;
+    P.stages = (int32_t)std::min<int64_t>(kMaxStages, (kSmemLimit - fixed) / ((int64_t)P.panels * kPanel));
+    const size_t smem = std::max<size_t>((size_t)((P.E + 63) / 64) * P.padded_heads * 128 + (size_t)P.padded_heads * 128 +
+                                             (size_t)P.stages * P.panels * kPanel,
+                                         120 * 1024);  // one CTA per SM: each takes the whole tensor memory
+    if (!fp8) {
+        if (d.stride >= (int64_t)1 << 40 || L->num_blocks > INT32_MAX || a->q_request_stride >= (int64_t)1 << 38 ||
+            a->q_head_stride >= (int64_t)1 << 38)
+            return LMC_ERR_INVALID_ARG;
+        const int64_t head_bytes = H > 1 ? a->q_head_stride * 2 : (int64_t)P.E * 2;
+        const int64_t request_bytes = R > 1 ? a->q_request_stride * 2 : head_bytes * H;
+        if (!tensor_map(&P.cache, bf16, P.pool, P.E, N, L->num_blocks, P.token_bytes, d.stride,
+                        P.pages_per_tile == 1 ? kTile : (int)N) ||
+            !tensor_map(&P.query, bf16, a->q, P.E, H, R, head_bytes, request_bytes, P.padded_heads))
+            return LMC_ERR_CUDA;
+    }
+    auto kern = fp8 ? lmc_attend_kernel<false, true> : bf16 ? lmc_attend_kernel<true, false> : lmc_attend_kernel<false, false>;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+        return LMC_ERR_CUDA;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    lmc_attend_kernel<<<dim3((unsigned)H, (unsigned)R), 32 * kWarps, 0, s>>>(P);
-    if (a->weights != nullptr) {
-        const unsigned n = (unsigned)std::min<int64_t>(512, (a->max_length + kWarps - 1) / kWarps);
-        lmc_attend_weights_kernel<<<dim3(n, (unsigned)R), 32 * kWarps, 0, s>>>(P);
+    kern<<<(unsigned)(P.cols * P.head_groups), (kFirstLoader + (fp8 ? kFp8Loaders : 1)) * 32, smem, s>>>(P);
+    lmc_attend_join_kernel<<<dim3((unsigned)P.cols, (unsigned)H), kJoinThreads, 0, s>>>(P);
+    if (P.weights != nullptr) {
+        const int64_t tokens = P.window > 0 ? std::min<int64_t>(P.max_length, P.window) : P.max_length;
+        lmc_attend_weights_kernel<<<dim3((unsigned)((tokens + kWeightThreads - 1) / kWeightThreads), (unsigned)R),
+                                    kWeightThreads, 0, s>>>(P);
     }
     return cudaGetLastError() == cudaSuccess ? LMC_OK : LMC_ERR_CUDA;
 }
