@@ -64,9 +64,14 @@ constexpr int kPanel = kTile * 128;   // bytes of 64 values of a tile's rows
 constexpr int kMaxStages = 4;
 constexpr int kMaxCols = 160;         // CTAs along the cache's length (an SM each)
 constexpr int kSoftWarps = 4;
-constexpr int kMmaWarp = 4;
-constexpr int kFirstLoader = 5;
-constexpr int kFp8Loaders = 8;        // warps: two groups of four, a tile each
+constexpr int kScoreWarp = 4;          // issues S = Q K^T
+constexpr int kValueWarp = 5;          // issues O^T += V^T P^T
+constexpr int kFirstLoader = 6;
+constexpr int kFp8Loaders = 8;        // warps, eight of a tile's rows each
+#ifndef LMC_AHEAD
+#define LMC_AHEAD 2
+#endif
+constexpr int kAhead = LMC_AHEAD;     // tiles
 constexpr float kLag = 8.0f;          // how far (log2) a logit may exceed the reference
 constexpr uint32_t kWaitLimit = 1u << 22;
 constexpr int kSmemLimit = 227 * 1024;
@@ -77,12 +82,12 @@ struct Control {
     uint64_t kv_full[kMaxStages], kv_free[kMaxStages];
     uint64_t s_full[2], s_free[2];
     uint64_t p_full, pv_done, o_free;
-    uint64_t valid[kMaxStages];  // a tile's rows that are attended
-    uint64_t zero[kMaxStages];   // and those to be cleared before they are values
+    uint64_t valid[2 * kMaxStages];  // a tile's rows that are attended
+    uint64_t zero[2 * kMaxStages];   // and those to be cleared before they are values
     uint32_t tmem;
     uint32_t gave_up;            // a wait ran out: nothing waits any more
     float factor[kMaxHeads];     // rescaling of a head's O
-    float inverse[kMaxHeads];    // 1 / l
+    alignas(16) float inverse[kMaxHeads];  // 1 / l
     float q_scale[kMaxHeads];    // fp8: what q was divided by
 };
 
@@ -126,6 +131,7 @@ struct AttendPlan {
     int32_t panels;            // of an entry in shared memory
     int32_t value_tiles;       // of 128 values
     int32_t stages;
+    int32_t cache_copies, query_copies;  // TMA copies for all panels of a box
     int32_t q_bf16;            // q's and out's type
     float scale;               // of fp8 entries
     float log2_scale;          // softmax_scale * scale * log2(e)
@@ -294,6 +300,23 @@ __device__ __forceinline__ void bar_wait(Control &C, uint64_t *bar, uint32_t par
     atomicOr(status, LMC_ST_TIMEOUT);
 }
 
+// One lane of a converged warp. The products are issued behind this, not
+// behind a lane number: the compiler then knows that one thread runs and keeps
+// the descriptors in uniform registers (115 cycles an instruction otherwise).
+__device__ __forceinline__ bool elect() {
+    uint32_t one;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "elect.sync _|p, 0xffffffff;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(one));
+    return one != 0;
+}
+
+// The same value in every lane, said so that the compiler may keep it in a
+// uniform register.
+__device__ __forceinline__ uint32_t uniform(uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); }
+
 __device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
@@ -315,12 +338,19 @@ __device__ __forceinline__ bool soft_any(bool x) {
     return r != 0;
 }
 
-__device__ __forceinline__ void tma_3d(const CUtensorMap *map, void *dst, int x, int y, int z, uint64_t *bar) {
+// One copy of a box of rows: (64 values, rows, panels, a block or request).
+__device__ __forceinline__ void tma_box(const CUtensorMap *map, void *dst, int x, int y, int w, uint64_t *bar) {
     asm volatile(
-        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], "
-        "[%5];" ::"r"(smem_addr(dst)),
-        "l"(map), "r"(x), "r"(y), "r"(z), "r"(smem_addr(bar))
+        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
+        "[%6];" ::"r"(smem_addr(dst)),
+        "l"(map), "r"(x), "r"(y), "r"(0), "r"(w), "r"(smem_addr(bar))
         : "memory");
+}
+
+__device__ __forceinline__ void tma_prefetch(const CUtensorMap *map, int x, int y, int w) {
+    asm volatile("cp.async.bulk.prefetch.tensor.4d.L2.global.tile [%0, {%1, %2, %3, %4}];" ::"l"(map), "r"(x), "r"(y),
+                 "r"(0), "r"(w)
+                 : "memory");
 }
 
 // Shared-memory matrix descriptor: 128-byte swizzle, 8-row groups `stride`
@@ -387,6 +417,15 @@ __device__ __forceinline__ void store_o(const uint32_t (&o)[16], uint32_t addr) 
         : "memory");
 }
 
+// o[k] for a k known at run time, without an indexed (local memory) array.
+__device__ __forceinline__ uint32_t at16(const uint32_t (&o)[16], int k) {
+    uint32_t x = o[0];
+#pragma unroll
+    for (int i = 1; i < 16; i++)
+        x = k == i ? o[i] : x;
+    return x;
+}
+
 __device__ __forceinline__ float exp2_fast(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
@@ -411,6 +450,15 @@ __device__ __forceinline__ float from_q(uint32_t h, bool bf16) {
     return bf16 ? __uint_as_float(h << 16) : __half2float(__ushort_as_half((unsigned short)h));
 }
 
+// Kernels of this file are launched so that each may start while the one
+// before it in the stream still runs. This waits for that one to be done and
+// its writes to be seen; nothing in global memory is touched before it. Then
+// the next one may be brought in.
+__device__ __forceinline__ void wait_for_launch() {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+}
+
 // ---- the CTA's roles ---------------------------------------------------------
 
 struct Memory {
@@ -418,36 +466,48 @@ struct Memory {
     int stage_bytes;
 };
 
+// The page a warp resolved last: the tiles of a page follow one another, and
+// the block table's latency would be paid for each.
+struct LastPage {
+    int r = -1, page = -1, block = -1;
+};
+
 // The block ids of a tile's pages, one per lane, and which rows they and the
 // range leave: a bad page's status bit is raised here.
-__device__ __forceinline__ int resolve(const AttendPlan &P, const Walk &W, const Tile &T, uint64_t &valid, uint32_t &bad) {
-    int block = -1;
+__device__ __forceinline__ int resolve(const AttendPlan &P, const Walk &W, const Tile &T, uint64_t &valid, uint32_t &bad,
+                                       LastPage &last) {
     const int lane = threadIdx.x & 31;
-    const int64_t first = (int64_t)T.page * P.block_size;
-    bool ok = false;
-    if (lane < P.pages_per_tile) {
-        const int64_t p0 = first + (int64_t)lane * P.block_size;  // the page's tokens
-        if (p0 < W.range.L && p0 + P.block_size > W.range.lo) {
-            block = __ldg(P.table + W.r * P.row_stride + T.page + lane);
-            ok = block >= 0 && block < P.num_blocks;
-            if (!ok)
-                bad |= block == -1 ? LMC_ST_NO_BLOCK : LMC_ST_BLOCK_OOR;
-        }
-    }
-    if (!ok)
-        block = -1;
-    const uint32_t pages = __ballot_sync(0xffffffffu, ok);
     valid = bits((int)(W.range.lo - T.t0 > 64 ? 64 : W.range.lo - T.t0), (int)min((int64_t)T.rows, W.range.L - T.t0));
     if (P.pages_per_tile == 1) {
-        if (pages == 0)
+        if (W.r != last.r || T.page != last.page) {
+            int block = __ldg(P.table + W.r * P.row_stride + T.page);
+            if (block < 0 || block >= P.num_blocks) {
+                bad |= block == -1 ? LMC_ST_NO_BLOCK : LMC_ST_BLOCK_OOR;
+                block = -1;
+            }
+            last.r = W.r;
+            last.page = T.page;
+            last.block = block;
+        }
+        if (last.block < 0)
             valid = 0;
-    } else {
-        uint64_t have = 0;
-        for (int k = 0; k < P.pages_per_tile; k++)
-            if (pages >> k & 1)
-                have |= bits(k * P.block_size, (k + 1) * P.block_size);
-        valid &= have;
+        return last.block;
     }
+    int block = -1;
+    const int64_t p0 = ((int64_t)T.page + lane) * P.block_size;  // the page's tokens
+    if (lane < P.pages_per_tile && p0 < W.range.L && p0 + P.block_size > W.range.lo) {
+        block = __ldg(P.table + W.r * P.row_stride + T.page + lane);
+        if (block < 0 || block >= P.num_blocks) {
+            bad |= block == -1 ? LMC_ST_NO_BLOCK : LMC_ST_BLOCK_OOR;
+            block = -1;
+        }
+    }
+    const uint32_t pages = __ballot_sync(0xffffffffu, block >= 0);
+    uint64_t have = 0;
+    for (int k = 0; k < P.pages_per_tile; k++)
+        if (pages >> k & 1)
+            have |= bits(k * P.block_size, (k + 1) * P.block_size);
+    valid &= have;
     return block;
 }
 
@@ -455,42 +515,75 @@ __device__ __forceinline__ int resolve(const AttendPlan &P, const Walk &W, const
 __device__ __forceinline__ void load_by_tma(const AttendPlan &P, Control &C, const Memory &M, Walk &W, int group) {
     const int lane = threadIdx.x & 31;
     uint32_t bad = 0, n = 0, segments = 0;
+    LastPage last, last_ahead;
+    if (elect()) {
+        asm volatile("prefetch.tensormap [%0];" ::"l"(&P.cache) : "memory");
+        asm volatile("prefetch.tensormap [%0];" ::"l"(&P.query) : "memory");
+    }
     while (W.next(P)) {
         if (segments > 0)
             bar_wait(C, &C.q_free, (segments - 1) & 1, P.status);
         const int row_panels = (P.E + 63) / 64;
-        if (lane == 0) {
+        const int r = (int)uniform(W.r);
+        if (elect()) {
             bar_expect(&C.q_full, (uint32_t)(row_panels * P.padded_heads * 128));
-            for (int i = 0; i < row_panels; i++)
-                tma_3d(&P.query, M.q + i * P.padded_heads * 128, i * 64, group * P.group_heads, W.r, &C.q_full);
+            for (int i = 0; i < P.query_copies; i++)
+                tma_box(&P.query, M.q + i * P.padded_heads * 128, i * 64, group * P.group_heads, r, &C.q_full);
         }
+        __syncwarp();
         segments++;
         for (int j = 0; j < W.count; j++, n++) {
-            const int st = n % P.stages;
+            const int st = (int)uniform(n % P.stages);
             const Tile T = tile_at(P, W.first + j);
             uint64_t valid;
-            const int block = resolve(P, W, T, valid, bad);
-            const uint32_t pages = __ballot_sync(0xffffffffu, block >= 0);
+            const int block = resolve(P, W, T, valid, bad, last);
+            // pages there are: one held by every lane, or one per lane
+            const uint32_t pages = __ballot_sync(0xffffffffu, block >= 0) & (P.pages_per_tile == 1 ? 1u : ~0u);
+            const int row0 = (int)uniform(T.row0);
+            uint8_t *to = M.kv + (size_t)st * M.stage_bytes;
+            const uint32_t bytes =
+                uniform(__popc(pages) * row_panels * (P.pages_per_tile == 1 ? kTile : P.block_size) * 128);
+            if (lane == 0) {
+                // rows behind a page's end are filled with zeros, others hold what lies there
+                C.valid[n % (2 * kMaxStages)] = valid;
+                C.zero[n % (2 * kMaxStages)] =
+                    ~valid & (P.pages_per_tile == 1 && pages != 0 ? bits(0, T.rows) : ~0ull);
+            }
+            const int block0 = (int)uniform(block);
             if (n >= (uint32_t)P.stages)
                 bar_wait(C, &C.kv_free[st], (n / P.stages - 1) & 1, P.status);
-            uint8_t *to = M.kv + (size_t)st * M.stage_bytes;
-            if (lane == 0) {
-                C.valid[st] = valid;
-                // rows behind a page's end were filled with zeros, others hold what lies there
-                uint64_t zero = ~valid;
-                if (P.pages_per_tile == 1 && pages != 0)
-                    zero &= bits(0, T.rows);
-                C.zero[st] = zero;
-                const int box = P.pages_per_tile == 1 ? kTile : P.block_size;
-                bar_expect(&C.kv_full[st], (uint32_t)(__popc(pages) * row_panels * box * 128));
+            __syncwarp();
+            if (P.pages_per_tile == 1) {
+                if (elect()) {
+                    bar_expect(&C.kv_full[st], bytes);
+                    if (block0 >= 0)
+                        for (int i = 0; i < P.cache_copies; i++)
+                            tma_box(&P.cache, to + i * kPanel, i * 64, row0, block0, &C.kv_full[st]);
+                }
+            } else {
+                if (elect())
+                    bar_expect(&C.kv_full[st], bytes);
+                for (int k = 0; k < P.pages_per_tile; k++) {
+                    const int b = (int)__shfl_sync(0xffffffffu, block, k);
+                    if (b >= 0 && elect())
+                        for (int i = 0; i < P.cache_copies; i++)
+                            tma_box(&P.cache, to + i * kPanel + k * P.block_size * 128, i * 64, 0, b, &C.kv_full[st]);
+                }
             }
             __syncwarp();
-            for (int k = 0; k < P.pages_per_tile; k++) {
-                const int b = __shfl_sync(0xffffffffu, block, k);
-                if (lane == 0 && b >= 0)
-                    for (int i = 0; i < row_panels; i++)
-                        tma_3d(&P.cache, to + i * kPanel + k * P.block_size * 128, i * 64,
-                               P.pages_per_tile == 1 ? T.row0 : 0, b, &C.kv_full[st]);
+            if (j + kAhead < W.count) {
+                const Tile A = tile_at(P, W.first + j + kAhead);
+                uint64_t unused;
+                uint32_t later = 0;  // raised when the tile itself is loaded
+                const int ahead = resolve(P, W, A, unused, later, last_ahead);
+                const int arow = (int)uniform(A.row0);
+                for (int k = 0; k < P.pages_per_tile; k++) {
+                    const int b = __shfl_sync(0xffffffffu, ahead, k);
+                    if (b >= 0 && elect())
+                        for (int i = 0; i < P.cache_copies; i++)
+                            tma_prefetch(&P.cache, i * 64, arow, b);
+                    __syncwarp();
+                }
             }
         }
     }
@@ -506,191 +599,207 @@ __device__ __forceinline__ void load_by_tma(const AttendPlan &P, Control &C, con
     }
 }
 
-// Eight warps: queries to f16 (each head times a power of two that brings its
-// largest value to [2^14, 2^15): exact for values within 2^27 of it), and
-// entries from fp8 to f16. Two groups of four warps take a tile each, so that
-// one group's loads are in flight while the other stores.
+// A row of q to f16, times a power of two that brings its largest value to
+// [2^14, 2^15): exact for values within 2^27 of it. One warp.
+__device__ __forceinline__ void load_query_row(const AttendPlan &P, Control &C, const Memory &M, int r, int head, int h,
+                                               bool real) {
+    const int lane = threadIdx.x & 31;
+    const uint16_t *src = P.q + r * P.q_request_stride + head * P.q_head_stride;
+    uint4 v[3];
+    float top = 0.0f;
+#pragma unroll
+    for (int i = 0; i < 3; i++) {
+        const int c = lane + 32 * i;
+        v[i] = make_uint4(0, 0, 0, 0);
+        if (real && c < P.E / 8)
+            v[i] = __ldg(reinterpret_cast<const uint4 *>(src) + c);
+        const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+#pragma unroll
+        for (int k = 0; k < 4; k++)
+            top = fmaxf(top, fmaxf(fabsf(from_q(w[k] & 0xffff, P.q_bf16)), fabsf(from_q(w[k] >> 16, P.q_bf16))));
+    }
+    for (int o = 16; o > 0; o >>= 1)
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    // 2^(14 - exponent of top), kept within what one float holds
+    const int e = top > 0.0f && top < INFINITY ? max(-100, min(100, 14 - ilogbf(top))) : 0;
+    const float up = ldexpf(1.0f, e);
+    if (lane == 0)
+        C.q_scale[h] = ldexpf(1.0f, -e);
+#pragma unroll
+    for (int i = 0; i < 3; i++) {
+        const int c = lane + 32 * i;
+        if (c < P.E / 8) {
+            const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+            uint32_t o[4];
+#pragma unroll
+            for (int k = 0; k < 4; k++)
+                o[k] = pack<false>(from_q(w[k] & 0xffff, P.q_bf16) * up, from_q(w[k] >> 16, P.q_bf16) * up);
+            *reinterpret_cast<uint4 *>(M.q + (c >> 3) * P.padded_heads * 128 + h * 128 + (((c & 7) ^ (h & 7)) << 4)) =
+                make_uint4(o[0], o[1], o[2], o[3]);
+        }
+    }
+}
+
+// Eight warps: queries and fp8 entries, widened to f16 on the way. A warp
+// holds eight of a tile's rows, four lanes to a row: a lane takes 16 codes of
+// each panel, so a panel's codes are read as 64-byte pieces and its two
+// 16-byte halves are stored without bank conflicts, at offsets that do not
+// change from tile to tile. Two tiles are in flight in registers.
 __device__ __forceinline__ void load_fp8(const AttendPlan &P, Control &C, const Memory &M, Walk &W, int group) {
+    constexpr int kPanels = kMaxEntry / 64;
     const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) - kFirstLoader;
-    const int half = warp >> 2, tid = threadIdx.x - (kFirstLoader + 4 * half) * 32;
+    const int row = warp * 8 + lane / 4, piece = lane & 3;
+    const int chunks = P.E / 16;  // of an entry
+    const uint32_t at0 = row * 128 + (((2 * piece) ^ (row & 7)) << 4), at1 = row * 128 + (((2 * piece + 1) ^ (row & 7)) << 4);
     uint32_t bad = 0, n = 0, segments = 0;
-    const int chunks = P.E / 16;  // of an entry: 16 codes each
-    const uint32_t magic = chunks == 1 ? 0u : (uint32_t)((0x100000000ull + chunks - 1) / chunks);
-    const int total = kTile * chunks;
+    uint4 v[2][kPanels];
+    uint64_t valid[2];
+    LastPage last;
+    const int my_page = P.pages_per_tile == 1 ? 0 : row / P.block_size;
+    const int my_row = row - my_page * P.block_size;
+
+    auto load = [&](uint4(&x)[kPanels], uint64_t &rows, int j) {
+        const Tile T = tile_at(P, W.first + j);
+        const int block = resolve(P, W, T, rows, bad, last);
+        const int64_t b = __shfl_sync(0xffffffffu, block, my_page & 31);
+        const bool mine = rows >> row & 1;
+        const uint8_t *src = P.pool + b * P.block_stride + (int64_t)(T.row0 + my_row) * P.token_bytes + piece * 16;
+#pragma unroll
+        for (int i = 0; i < kPanels; i++) {
+            x[i] = make_uint4(0, 0, 0, 0);
+            if (mine && i * 4 + piece < chunks)
+                asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+                             : "=r"(x[i].x), "=r"(x[i].y), "=r"(x[i].z), "=r"(x[i].w)
+                             : "l"(src + i * 64));
+        }
+    };
+    auto store = [&](const uint4(&x)[kPanels], uint64_t rows) {
+        const int st = n % P.stages;
+        if (n >= (uint32_t)P.stages)
+            bar_wait(C, &C.kv_free[st], (n / P.stages - 1) & 1, P.status);
+        uint8_t *to = M.kv + (size_t)st * M.stage_bytes;
+#pragma unroll
+        for (int i = 0; i < kPanels; i++)
+            if (i * 4 + piece < chunks) {
+                const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
+                uint32_t o[8];
+#pragma unroll
+                for (int k = 0; k < 8; k++)
+                    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(o[k]) : "h"((unsigned short)(w[k >> 1] >> (16 * (k & 1)))));
+                *reinterpret_cast<uint4 *>(to + i * kPanel + at0) = make_uint4(o[0], o[1], o[2], o[3]);
+                *reinterpret_cast<uint4 *>(to + i * kPanel + at1) = make_uint4(o[4], o[5], o[6], o[7]);
+            }
+        if (warp == 0 && lane == 0) {
+            C.valid[n % (2 * kMaxStages)] = rows;
+            C.zero[n % (2 * kMaxStages)] = 0;  // the rows left out hold zeros
+        }
+        fence_async();
+        __syncwarp();
+        if (lane == 0)
+            bar_arrive(&C.kv_full[st]);
+        n++;
+    };
+
     while (W.next(P)) {
+        load(v[0], valid[0], 0);
+        if (W.count > 1)
+            load(v[1], valid[1], 1);
         if (segments > 0)
             bar_wait(C, &C.q_free, (segments - 1) & 1, P.status);
         segments++;
         for (int h = warp; h < P.padded_heads; h += kFp8Loaders) {
             const int head = group * P.group_heads + h;
-            const bool real = h < P.group_heads && head < P.H;
-            const uint16_t *src = P.q + W.r * P.q_request_stride + head * P.q_head_stride;
-            uint4 v[3];
-            float top = 0.0f;
-#pragma unroll
-            for (int i = 0; i < 3; i++) {
-                const int c = lane + 32 * i;
-                v[i] = make_uint4(0, 0, 0, 0);
-                if (real && c < P.E / 8)
-                    v[i] = __ldg(reinterpret_cast<const uint4 *>(src) + c);
-                const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-#pragma unroll
-                for (int k = 0; k < 4; k++)
-                    top = fmaxf(top, fmaxf(fabsf(from_q(w[k] & 0xffff, P.q_bf16)), fabsf(from_q(w[k] >> 16, P.q_bf16))));
-            }
-            for (int o = 16; o > 0; o >>= 1)
-                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-            // 2^(14 - exponent of top), kept within what one float holds
-            const int e = top > 0.0f && top < INFINITY ? max(-100, min(100, 14 - ilogbf(top))) : 0;
-            const float up = ldexpf(1.0f, e);
-            if (lane == 0)
-                C.q_scale[h] = ldexpf(1.0f, -e);
-#pragma unroll
-            for (int i = 0; i < 3; i++) {
-                const int c = lane + 32 * i;
-                if (c < P.E / 8) {
-                    const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-                    uint32_t o[4];
-#pragma unroll
-                    for (int k = 0; k < 4; k++)
-                        o[k] = pack<false>(from_q(w[k] & 0xffff, P.q_bf16) * up, from_q(w[k] >> 16, P.q_bf16) * up);
-                    *reinterpret_cast<uint4 *>(M.q + (c >> 3) * P.padded_heads * 128 + h * 128 +
-                                               (((c & 7) ^ (h & 7)) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
-                }
-            }
+            load_query_row(P, C, M, W.r, head, h, h < P.group_heads && head < P.H);
         }
         fence_async();
         __syncwarp();
         if (lane == 0)
             bar_arrive(&C.q_full);
-        for (int j = 0; j < W.count; j++, n++) {
-            if ((int)(n & 1) != half)
-                continue;
-            const int st = n % P.stages;
-            const Tile T = tile_at(P, W.first + j);
-            uint64_t valid;
-            const int block = resolve(P, W, T, valid, bad);
-            // up to 64 * 36 chunks over 128 threads
-            uint4 v[18];
-#pragma unroll
-            for (int i = 0; i < 18; i++) {
-                const int c = tid + 128 * i;
-                v[i] = make_uint4(0, 0, 0, 0);
-                const int row = chunks == 1 ? c : (int)__umulhi((uint32_t)c, magic);
-                const int k = P.pages_per_tile == 1 ? 0 : row / P.block_size;
-                const int b = __shfl_sync(0xffffffffu, block, k & 31);
-                if (c < total && (valid >> (row & 63) & 1)) {
-                    const int64_t in_page = T.row0 + row - k * P.block_size;
-                    const uint8_t *src = P.pool + (int64_t)b * P.block_stride + in_page * P.token_bytes +
-                                         (c - row * chunks) * 16;
-                    asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-                                 : "=r"(v[i].x), "=r"(v[i].y), "=r"(v[i].z), "=r"(v[i].w)
-                                 : "l"(src));
-                }
+        for (int j = 0; j < W.count; j += 2) {
+            store(v[0], valid[0]);
+            if (j + 2 < W.count)
+                load(v[0], valid[0], j + 2);
+            if (j + 1 < W.count) {
+                store(v[1], valid[1]);
+                if (j + 3 < W.count)
+                    load(v[1], valid[1], j + 3);
             }
-            if (n >= (uint32_t)P.stages)
-                bar_wait(C, &C.kv_free[st], (n / P.stages - 1) & 1, P.status);
-            uint8_t *to = M.kv + (size_t)st * M.stage_bytes;
-#pragma unroll
-            for (int i = 0; i < 18; i++) {
-                const int c = tid + 128 * i;
-                const int row = chunks == 1 ? c : (int)__umulhi((uint32_t)c, magic);
-                const int ch = c - row * chunks;
-                if (c < total) {
-                    const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-                    uint32_t o[8];
-#pragma unroll
-                    for (int k = 0; k < 8; k++)
-                        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(o[k]) : "h"((unsigned short)(w[k >> 1] >> (16 * (k & 1)))));
-                    uint8_t *at = to + (ch >> 2) * kPanel + row * 128;
-                    const int c0 = (ch & 3) * 2, x = row & 7;
-                    *reinterpret_cast<uint4 *>(at + ((c0 ^ x) << 4)) = make_uint4(o[0], o[1], o[2], o[3]);
-                    *reinterpret_cast<uint4 *>(at + (((c0 + 1) ^ x) << 4)) = make_uint4(o[4], o[5], o[6], o[7]);
-                }
-            }
-            if (tid == 0) {
-                C.valid[st] = valid;
-                C.zero[st] = 0;  // the rows left out hold zeros
-            }
-            fence_async();
-            __syncwarp();
-            if (lane == 0)
-                bar_arrive(&C.kv_full[st]);
         }
     }
     if (bad)
         atomicOr(P.status, bad);
 }
 
-// One warp: issues the products.
+// One warp: S = Q K^T of each tile, as soon as it is there. (The two products
+// are issued by two warps, so that neither waits behind the other's barriers.)
 template <bool kBf16>
-__device__ __forceinline__ void multiply(const AttendPlan &P, Control &C, const Memory &M, Walk &W) {
-    const int lane = threadIdx.x & 31;
-    const uint32_t tmem = C.tmem;
+__device__ __forceinline__ void multiply_scores(const AttendPlan &P, Control &C, const Memory &M, Walk &W) {
+    const uint32_t tmem = uniform(C.tmem);
     const uint32_t qk = instruction(kBf16, false, 64, kTile);
-    const uint32_t pv = instruction(kBf16, true, 128, P.padded_heads);
-    const uint32_t q = smem_addr(M.q), p = smem_addr(M.p);
+    // descriptors hold addresses in units of 16 bytes: steps are added to them
+    const uint64_t q0 = matrix(smem_addr(M.q), 16, 1024);
+    const uint32_t q_panel = P.padded_heads * 128 >> 4;
+    const int steps = P.E / 16, panels = steps / 4;
     uint32_t n = 0, segments = 0;
-
-    auto values = [&](uint32_t k, bool begins) {  // O^T += V^T P^T of the CTA's k-th tile
-        if (begins && segments > 0)
-            bar_wait(C, &C.o_free, (segments - 1) & 1, P.status);
-        bar_wait(C, &C.p_full, k & 1, P.status);
-        fence_after();
-        const int st = k % P.stages;
-        if (lane == 0) {
-            const uint32_t kv = smem_addr(M.kv) + st * M.stage_bytes;
-            for (int t = 0; t < P.value_tiles; t++)
-#pragma unroll
-                for (int s = 0; s < kTile / 16; s++)
-                    mma(tmem + 128 + t * P.padded_heads, matrix(kv + 2 * t * kPanel + s * 2048, kPanel, 1024),
-                        matrix(p + s * 32, 16, 1024), pv, !(begins && s == 0));
-            commit(&C.kv_free[st]);
-            commit(&C.pv_done);
-        }
-        __syncwarp();
-    };
-
     while (W.next(P)) {
         bar_wait(C, &C.q_full, segments & 1, P.status);
-        bool pending = false;
         for (int j = 0; j < W.count; j++, n++) {
-            const int st = n % P.stages;
-            // whichever is ready first: this tile, or the last one's values
-            if (pending) {
-                for (uint32_t k = 0; k < kWaitLimit; k++) {
-                    const bool full = __shfl_sync(0xffffffffu, (int)bar_try(&C.kv_full[st], (n / P.stages) & 1), 0);
-                    if (full)
-                        break;
-                    const bool ready = __shfl_sync(0xffffffffu, (int)bar_try(&C.p_full, (n - 1) & 1), 0);
-                    if (ready) {
-                        values(n - 1, j == 1);
-                        pending = false;
-                        break;
-                    }
-                    if ((k & 255u) == 255u && __shfl_sync(0xffffffffu, (int)*(volatile uint32_t *)&C.gave_up, 0))
-                        break;
-                }
-            }
-            bar_wait(C, &C.kv_full[st], (n / P.stages) & 1, P.status);
+            const int st = (int)uniform(n % P.stages);
+            const uint32_t d = tmem + uniform(n & 1) * 64;
+            const uint64_t k0 = matrix(smem_addr(M.kv) + st * M.stage_bytes, 16, 1024);
             if (n >= 2)
                 bar_wait(C, &C.s_free[n & 1], (n / 2 - 1) & 1, P.status);
+            bar_wait(C, &C.kv_full[st], (n / P.stages) & 1, P.status);
+            __syncwarp();
             fence_after();
-            if (lane == 0) {
-                const uint32_t kv = smem_addr(M.kv) + st * M.stage_bytes;
-                for (int s = 0; s < P.E / 16; s++)
-                    mma(tmem + (n & 1) * 64, matrix(q + (s >> 2) * P.padded_heads * 128 + (s & 3) * 32, 16, 1024),
-                        matrix(kv + (s >> 2) * kPanel + (s & 3) * 32, 16, 1024), qk, s > 0);
+            if (elect()) {
+                for (int i = 0; i < panels; i++)
+#pragma unroll
+                    for (int s = 0; s < 4; s++)
+                        mma(d, q0 + i * q_panel + s * (32 >> 4), k0 + i * (kPanel >> 4) + s * (32 >> 4), qk, i + s > 0);
+                for (int s = 4 * panels; s < steps; s++)
+                    mma(d, q0 + panels * q_panel + (s & 3) * (32 >> 4), k0 + panels * (kPanel >> 4) + (s & 3) * (32 >> 4),
+                        qk, s > 0);
                 commit(&C.s_full[n & 1]);
                 if (j == W.count - 1)
                     commit(&C.q_free);
             }
             __syncwarp();
-            if (pending)
-                values(n - 1, j == 1);
-            pending = true;
         }
-        values(n - 1, W.count == 1);
+        segments++;
+    }
+}
+
+// One warp: O^T += V^T P^T of each tile, once its P is written.
+template <bool kBf16>
+__device__ __forceinline__ void multiply_values(const AttendPlan &P, Control &C, const Memory &M, Walk &W) {
+    const uint32_t o = uniform(C.tmem) + 128;
+    const uint32_t pv = instruction(kBf16, true, 128, P.padded_heads);
+    const uint64_t p0 = matrix(smem_addr(M.p), 16, 1024);
+    uint32_t n = 0, segments = 0;
+    while (W.next(P)) {
+        for (int j = 0; j < W.count; j++, n++) {
+            const int st = (int)uniform(n % P.stages);
+            const uint64_t v0 = matrix(smem_addr(M.kv) + st * M.stage_bytes, kPanel, 1024);
+            if (j == 0 && segments > 0)
+                bar_wait(C, &C.o_free, (segments - 1) & 1, P.status);
+            bar_wait(C, &C.p_full, n & 1, P.status);
+            __syncwarp();
+            fence_after();
+            if (elect()) {
+#pragma unroll
+                for (int t = 0; t < kMaxValue / 128; t++)
+                    if (t < P.value_tiles) {
+#pragma unroll
+                        for (int s = 0; s < kTile / 16; s++)
+                            mma(o + t * P.padded_heads, v0 + t * (2 * kPanel >> 4) + s * (2048 >> 4), p0 + s * (32 >> 4),
+                                pv, j > 0 || s > 0);
+                    }
+                commit(&C.kv_free[st]);
+                commit(&C.pv_done);
+            }
+            __syncwarp();
+        }
         segments++;
     }
 }
@@ -725,7 +834,7 @@ __device__ __forceinline__ void soften(const AttendPlan &P, Control &C, const Me
                 if (lane == 0)
                     bar_arrive(&C.q_free);
             }
-            const uint64_t valid = C.valid[st], zero = C.zero[st];
+            const uint64_t valid = C.valid[n % (2 * kMaxStages)], zero = C.zero[n % (2 * kMaxStages)];
             bar_wait(C, &C.s_full[n & 1], (n >> 1) & 1, P.status);
             fence_after();
             uint32_t raw[32];
@@ -878,21 +987,34 @@ __device__ __forceinline__ void soften(const AttendPlan &P, Control &C, const Me
             for (int c = 0; c < P.padded_heads; c += 16) {
                 uint32_t o[16];
                 load_o(o, lanes + 128 + t * P.padded_heads + c);
+                float inv[16];
+#pragma unroll
+                for (int k = 0; k < 16; k += 4)
+                    *reinterpret_cast<float4 *>(inv + k) = *reinterpret_cast<const float4 *>(C.inverse + c + k);
                 wait_ld();
-                if (v < P.V) {
-                    if (whole) {
-                        uint16_t *to = P.out + W.r * P.out_request_stride + (int64_t)(head0 + c) * P.out_head_stride + v;
+                if (v >= P.V)
+                    continue;
+                // 16 heads without a test each where there are as many (a
+                // test per store costs three times the store)
+                if (whole) {
+                    uint16_t *to = P.out + W.r * P.out_request_stride + (head0 + c) * P.out_head_stride + v;
+                    if (c + 16 <= heads) {
 #pragma unroll
-                        for (int k = 0; k < 16; k++)
-                            if (c + k < heads)
-                                to[k * P.out_head_stride] =
-                                    to_out(__uint_as_float(o[k]) * C.inverse[c + k], P.q_bf16);
+                        for (int k = 0; k < 16; k++, to += P.out_head_stride)
+                            *to = to_out(__uint_as_float(o[k]) * inv[k], P.q_bf16);
                     } else {
-                        float *to = P.part_o + ((int64_t)slot * P.H + head0 + c) * P.V + v;
+                        for (int k = 0; c + k < heads; k++, to += P.out_head_stride)
+                            *to = to_out(__uint_as_float(at16(o, k)) * C.inverse[c + k], P.q_bf16);
+                    }
+                } else {
+                    float *to = P.part_o + ((int64_t)slot * P.H + head0 + c) * P.V + v;
+                    if (c + 16 <= heads) {
 #pragma unroll
-                        for (int k = 0; k < 16; k++)
-                            if (c + k < heads)
-                                to[k * P.V] = __uint_as_float(o[k]) * C.inverse[c + k];
+                        for (int k = 0; k < 16; k++, to += P.V)
+                            *to = __uint_as_float(o[k]) * inv[k];
+                    } else {
+                        for (int k = 0; c + k < heads; k++, to += P.V)
+                            *to = __uint_as_float(at16(o, k)) * C.inverse[c + k];
                     }
                 }
             }
@@ -924,7 +1046,7 @@ __global__ void __launch_bounds__((kFirstLoader + (kFp8 ? kFp8Loaders : 1)) * 32
         bar_init(&C.q_full, kFp8 ? kFp8Loaders : 1);
         bar_init(&C.q_free, kFp8 ? 1 + kSoftWarps : 1);  // the products', and the readers of q_scale
         for (int i = 0; i < P.stages; i++) {
-            bar_init(&C.kv_full[i], kFp8 ? 4 : 1);
+            bar_init(&C.kv_full[i], kFp8 ? kFp8Loaders : 1);
             bar_init(&C.kv_free[i], 1);
         }
         for (int i = 0; i < 2; i++) {
@@ -938,7 +1060,7 @@ __global__ void __launch_bounds__((kFirstLoader + (kFp8 ? kFp8Loaders : 1)) * 32
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         fence_async();
     }
-    if (warp == kMmaWarp) {
+    if (warp == kScoreWarp) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(&C.tmem))
                      : "memory");
         asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
@@ -946,13 +1068,16 @@ __global__ void __launch_bounds__((kFirstLoader + (kFp8 ? kFp8Loaders : 1)) * 32
     fence_before();
     __syncthreads();
     fence_after();
+    wait_for_launch();
 
     Walk W;
     W.init(P, col);
     if (warp < kSoftWarps)
         soften<kBf16, kFp8>(P, C, M, W, col, group);
-    else if (warp == kMmaWarp)
-        multiply<kBf16>(P, C, M, W);
+    else if (warp == kScoreWarp)
+        multiply_scores<kBf16>(P, C, M, W);
+    else if (warp == kValueWarp)
+        multiply_values<kBf16>(P, C, M, W);
     else if (kFp8)
         load_fp8(P, C, M, W, group);
     else
@@ -965,68 +1090,93 @@ __global__ void __launch_bounds__((kFirstLoader + (kFp8 ? kFp8Loaders : 1)) * 32
     fence_before();
     __syncthreads();
     fence_after();
-    if (warp == kMmaWarp)
+    if (warp == kScoreWarp)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(C.tmem));
 }
 
 // ---- joining -------------------------------------------------------------------
 
-constexpr int kJoinThreads = 128;
+constexpr int kJoinWarps = 4;
 
-// Block (c, h): if a request that spans several CTAs begins in CTA column c,
-// joins its parts for head h; and writes the rows of requests without tokens
-// (r = c, c + cols, ...).
-__global__ void __launch_bounds__(kJoinThreads) lmc_attend_join_kernel(const __grid_constant__ AttendPlan P) {
-    const int col = blockIdx.x, h = blockIdx.y;
+// Block (c, y), a warp per head: if a request that spans several CTAs begins
+// in CTA column c, joins its parts; and writes the rows of requests without
+// tokens (r = c, c + cols, ...).
+__global__ void __launch_bounds__(kJoinWarps * 32) lmc_attend_join_kernel(const __grid_constant__ AttendPlan P) {
+    __shared__ float factors[kJoinWarps][kMaxCols];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int col = blockIdx.x, h = blockIdx.y * kJoinWarps + warp;
+    wait_for_launch();
+    if (h >= P.H)
+        return;
     for (int r = col; r < P.R; r += P.cols) {
         const Range g = range_of(P, r);
         if (!g.ok || g.L != 0)
             continue;
-        for (int v = threadIdx.x; v < P.V; v += kJoinThreads)
+        for (int v = lane; v < P.V; v += 32)
             P.out[r * P.out_request_stride + h * P.out_head_stride + v] = 0;
-        if (threadIdx.x == 0 && P.lse != nullptr)
+        if (lane == 0 && P.lse != nullptr)
             P.lse[r * P.lse_request_stride + h] = -INFINITY;
     }
-    const int r = P.segment[2 * col + 1].x;
+    const int2 head = P.segment[2 * col + 1];
+    const int r = head.x;
     if (r < 0)
         return;
     // parts: slot 2 col + 1, then 2 (col + 1), ...; all CTAs but the last have
     // as many tiles as the next one
-    const int rest = tiles_of(P, range_of(P, r)) - P.segment[2 * col + 1].y;
-    int last = col + 1;
-    if (rest > 0 && last < P.cols && P.segment[2 * last].x == r) {
-        const int each = max(1, P.segment[2 * last].y);
-        last = min(P.cols, last + (rest + each - 1) / each);
+    const int rest = tiles_of(P, range_of(P, r)) - head.y;
+    int parts = 1;
+    if (rest > 0 && col + 1 < P.cols && P.segment[2 * col + 2].x == r) {
+        const int each = max(1, P.segment[2 * col + 2].y);
+        parts = min(P.cols - col, 1 + (rest + each - 1) / each);
     }
     float top = -INFINITY;
-    for (int c = col; c < last; c++) {
-        const float2 ml = P.part_ml[(int64_t)(2 * c + (c == col)) * P.H + h];
+    for (int i = lane; i < parts; i += 32) {
+        const float2 ml = P.part_ml[(int64_t)(2 * (col + i) + (i == 0)) * P.H + h];
         if (ml.y != 0.0f)
             top = fmaxf(top, ml.x);
     }
-    float sum = 0.0f, acc[kMaxValue / kJoinThreads] = {};
-    for (int c = col; c < last; c++) {
-        const int64_t at = (int64_t)(2 * c + (c == col)) * P.H + h;
-        const float2 ml = P.part_ml[at];
-        if (ml.y == 0.0f)
-            continue;
-        const float f = exp2_fast(ml.x - top);
-        sum += ml.y * f;
+    for (int o = 16; o > 0; o >>= 1)
+        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    float sum = 0.0f;
+    for (int i = lane; i < parts; i += 32) {
+        const float2 ml = P.part_ml[(int64_t)(2 * (col + i) + (i == 0)) * P.H + h];
+        const float f = ml.y == 0.0f ? 0.0f : exp2_fast(ml.x - top);
+        factors[warp][i] = f;
+        sum += ml.y == 0.0f ? 0.0f : ml.y * f;
+    }
+    for (int o = 16; o > 0; o >>= 1)
+        sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    __syncwarp();
+    float4 acc[kMaxValue / 128] = {};
+    const float *part = P.part_o + ((int64_t)(2 * col + 1) * P.H + h) * P.V;
+    const int64_t step = (int64_t)2 * P.H * P.V;
+#pragma unroll 4
+    for (int i = 0; i < parts; i++) {
+        const float f = factors[warp][i];
+        const float4 *o = reinterpret_cast<const float4 *>(part + i * step - (i > 0 ? (int64_t)P.H * P.V : 0));
 #pragma unroll
-        for (int i = 0; i < kMaxValue / kJoinThreads; i++) {
-            const int v = threadIdx.x + i * kJoinThreads;
-            if (v < P.V)
-                acc[i] += P.part_o[at * P.V + v] * f;
-        }
+        for (int k = 0; k < kMaxValue / 128; k++)
+            if (4 * (lane + 32 * k) < P.V) {
+                const float4 x = __ldcs(o + lane + 32 * k);
+                acc[k].x += x.x * f;
+                acc[k].y += x.y * f;
+                acc[k].z += x.z * f;
+                acc[k].w += x.w * f;
+            }
     }
     const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+    uint16_t *to = P.out + r * P.out_request_stride + h * P.out_head_stride;
 #pragma unroll
-    for (int i = 0; i < kMaxValue / kJoinThreads; i++) {
-        const int v = threadIdx.x + i * kJoinThreads;
-        if (v < P.V)
-            P.out[r * P.out_request_stride + h * P.out_head_stride + v] = to_out(acc[i] * inv, P.q_bf16);
+    for (int k = 0; k < kMaxValue / 128; k++) {
+        const int v = 4 * (lane + 32 * k);
+        if (v < P.V) {
+            to[v] = to_out(acc[k].x * inv, P.q_bf16);
+            to[v + 1] = to_out(acc[k].y * inv, P.q_bf16);
+            to[v + 2] = to_out(acc[k].z * inv, P.q_bf16);
+            to[v + 3] = to_out(acc[k].w * inv, P.q_bf16);
+        }
     }
-    if (threadIdx.x == 0) {
+    if (lane == 0) {
         const float lse = sum == 0.0f ? -INFINITY : top + log2f(sum);
         P.lse2[(int64_t)r * P.H + h] = lse;
         if (P.lse != nullptr)
@@ -1039,6 +1189,7 @@ constexpr int kWeightThreads = 256;
 // A thread per token: the sum over the heads of 2^(logit - lse).
 __global__ void __launch_bounds__(kWeightThreads) lmc_attend_weights_kernel(const __grid_constant__ AttendPlan P) {
     const int r = blockIdx.y;
+    wait_for_launch();
     const Range g = range_of(P, r);
     if (!g.ok)
         return;
@@ -1115,20 +1266,39 @@ EncodeTiled encoder() {
     return fn;
 }
 
-// (values, rows, slices) of 16 bits each, read in boxes of 64 x `box` x 1.
+// (values, rows, slices) of 16 bits each, read in boxes of `box` rows of one
+// slice: of all panels of 64 values at once (`whole`; the values are a
+// multiple of 64 then), or of one.
 bool tensor_map(CUtensorMap *map, bool bf16, const void *base, int64_t values, int64_t rows, int64_t slices,
-                int64_t row_bytes, int64_t slice_bytes, int box) {
+                int64_t row_bytes, int64_t slice_bytes, int box, bool whole) {
     const EncodeTiled fn = encoder();
     if (fn == nullptr)
         return false;
-    const cuuint64_t dims[3] = {(cuuint64_t)values, (cuuint64_t)rows, (cuuint64_t)slices};
-    const cuuint64_t strides[2] = {(cuuint64_t)row_bytes, (cuuint64_t)slice_bytes};
-    const cuuint32_t boxes[3] = {64, (cuuint32_t)box, 1};
-    const cuuint32_t steps[3] = {1, 1, 1};
-    return fn(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 3,
+    const cuuint64_t panels = whole ? (cuuint64_t)values / 64 : 1;
+    const cuuint64_t dims[4] = {whole ? 64 : (cuuint64_t)values, (cuuint64_t)rows, panels, (cuuint64_t)slices};
+    const cuuint64_t strides[3] = {(cuuint64_t)row_bytes, 128, (cuuint64_t)slice_bytes};
+    const cuuint32_t boxes[4] = {64, (cuuint32_t)box, (cuuint32_t)panels, 1};
+    const cuuint32_t steps[4] = {1, 1, 1, 1};
+    return fn(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
               const_cast<void *>(base), dims, strides, boxes, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
               CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Launches a kernel that may start while the one before it in the stream still
+// runs (it waits for that one itself): its start-up costs no gap.
+bool follow(void (*kern)(AttendPlan), dim3 grid, int threads, size_t smem, cudaStream_t s, const AttendPlan &P) {
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = grid;
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, kern, P) == cudaSuccess;
 }
 
 }  // namespace
@@ -1237,21 +1407,30 @@ extern "C" int lmc_attend(const lmc_layout *L, const lmc_entries *e, const void 
             return LMC_ERR_INVALID_ARG;
         const int64_t head_bytes = H > 1 ? a->q_head_stride * 2 : (int64_t)P.E * 2;
         const int64_t request_bytes = R > 1 ? a->q_request_stride * 2 : head_bytes * H;
+        const int row_panels = (P.E + 63) / 64;
+        const bool whole = P.E % 64 == 0, tile = P.pages_per_tile == 1;
+        P.cache_copies = whole && tile ? 1 : row_panels;
+        P.query_copies = whole ? 1 : row_panels;
         if (!tensor_map(&P.cache, bf16, P.pool, P.E, N, L->num_blocks, P.token_bytes, d.stride,
-                        P.pages_per_tile == 1 ? kTile : (int)N) ||
-            !tensor_map(&P.query, bf16, a->q, P.E, H, R, head_bytes, request_bytes, P.padded_heads))
+                        tile ? kTile : (int)N, whole && tile) ||
+            !tensor_map(&P.query, bf16, a->q, P.E, H, R, head_bytes, request_bytes, P.padded_heads, whole))
             return LMC_ERR_CUDA;
     }
     auto kern = fp8 ? lmc_attend_kernel<false, true> : bf16 ? lmc_attend_kernel<true, false> : lmc_attend_kernel<false, false>;
     if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
         return LMC_ERR_CUDA;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    kern<<<(unsigned)(P.cols * P.head_groups), (kFirstLoader + (fp8 ? kFp8Loaders : 1)) * 32, smem, s>>>(P);
-    lmc_attend_join_kernel<<<dim3((unsigned)P.cols, (unsigned)H), kJoinThreads, 0, s>>>(P);
+    if (!follow(kern, dim3((unsigned)(P.cols * P.head_groups)), (kFirstLoader + (fp8 ? kFp8Loaders : 1)) * 32, smem, s,
+                P) ||
+        !follow(lmc_attend_join_kernel, dim3((unsigned)P.cols, (unsigned)((H + kJoinWarps - 1) / kJoinWarps)),
+                kJoinWarps * 32, 0, s, P))
+        return LMC_ERR_CUDA;
     if (P.weights != nullptr) {
         const int64_t tokens = P.window > 0 ? std::min<int64_t>(P.max_length, P.window) : P.max_length;
-        lmc_attend_weights_kernel<<<dim3((unsigned)((tokens + kWeightThreads - 1) / kWeightThreads), (unsigned)R),
-                                    kWeightThreads, 0, s>>>(P);
+        if (!follow(lmc_attend_weights_kernel,
+                    dim3((unsigned)((tokens + kWeightThreads - 1) / kWeightThreads), (unsigned)R), kWeightThreads, 0, s,
+                    P))
+            return LMC_ERR_CUDA;
     }
     return cudaGetLastError() == cudaSuccess ? LMC_OK : LMC_ERR_CUDA;
 }
