@@ -72,6 +72,10 @@ constexpr int kFp8Loaders = 8;        // warps, eight of a tile's rows each
 #define LMC_AHEAD 2
 #endif
 constexpr int kAhead = LMC_AHEAD;     // tiles
+#ifndef LMC_FP8_AHEAD
+#define LMC_FP8_AHEAD 2
+#endif
+constexpr int kFp8Ahead = LMC_FP8_AHEAD;
 constexpr float kLag = 8.0f;          // how far (log2) a logit may exceed the reference
 constexpr uint32_t kWaitLimit = 1u << 22;
 constexpr int kSmemLimit = 227 * 1024;
@@ -99,9 +103,7 @@ struct AttendPlan {
     int64_t num_blocks;
     const int32_t *table;
     int64_t row_stride;
-    int64_t num_cols;
     const int32_t *lengths;
-    int64_t max_length;
     const uint16_t *q;
     int64_t q_request_stride, q_head_stride;
     uint16_t *out;
@@ -119,6 +121,7 @@ struct AttendPlan {
     int64_t logit_stride;
     uint32_t *status;
     int32_t R, H, E, V;
+    int32_t max_length;        // the caller's, and what the table holds
     int32_t window;            // 0: none
     int32_t block_size;        // N
     int32_t token_bytes;
@@ -140,50 +143,45 @@ struct AttendPlan {
 // ---- requests and tiles ----------------------------------------------------
 
 struct Range {
-    int64_t lo, L;  // tokens [lo, L)
-    bool ok;        // a length that can be served
+    int lo, L;  // tokens [lo, L)
+    bool ok;    // a length that can be served
 };
 
 __device__ __forceinline__ Range range_of(const AttendPlan &P, int r) {
     Range g;
     g.L = __ldg(P.lengths + r);
-    g.ok = g.L >= 0 && g.L <= P.max_length && g.L <= P.num_cols * P.block_size;
-    g.lo = P.window > 0 ? max((int64_t)0, g.L - P.window) : 0;
+    g.ok = g.L >= 0 && g.L <= P.max_length;
+    g.lo = P.window > 0 ? max(0, g.L - P.window) : 0;
     return g;
 }
 
-__device__ __forceinline__ int first_tile(const AttendPlan &P, const Range &g) {
-    const int t = (int)g.lo, s = t / P.span;
+__device__ __forceinline__ int tile_of(const AttendPlan &P, int t) {
+    const int s = t / P.span;
     return s * P.tiles_per_span + (t - s * P.span) / kTile;
 }
 
 __device__ __forceinline__ int tiles_of(const AttendPlan &P, const Range &g) {
-    if (!g.ok || g.L == 0)
-        return 0;
-    const int t = (int)(g.L - 1), s = t / P.span;
-    return s * P.tiles_per_span + (t - s * P.span) / kTile + 1 - first_tile(P, g);
+    return !g.ok || g.L == 0 ? 0 : tile_of(P, g.L - 1) + 1 - tile_of(P, g.lo);
 }
 
 // A CTA's run of segments. Each warp walks it on its own: 32 requests at a
-// time, a lane each.
+// time, a lane each. (All requests' tiles together number less than 2^31.)
 struct Walk {
-    int64_t pos, end;    // the CTA's tiles still to come, of all requests' in a row
-    int64_t base;        // tiles before the 32 requests at hand
-    int64_t start, stop; // this lane's request's tiles
-    int r0, lane;
+    int pos, end;     // the CTA's tiles still to come, of all requests' in a row
+    int start, stop;  // this lane's request's tiles
+    int r0;           // the first of the 32 requests at hand
 
     // the current segment
     int r, first, count;  // request, its first tile here (of the request's), tiles
     bool begins, ends;    // the request begins / ends in this CTA
     Range range;
 
-    __device__ __forceinline__ void load(const AttendPlan &P) {
-        int n = 0;
-        if (r0 + lane < P.R)
-            n = tiles_of(P, range_of(P, r0 + lane));
-        int64_t sum = n;
+    __device__ __forceinline__ void load(const AttendPlan &P, int base) {
+        const int lane = threadIdx.x & 31;
+        const int n = r0 + lane < P.R ? tiles_of(P, range_of(P, r0 + lane)) : 0;
+        int sum = n;
         for (int o = 1; o < 32; o <<= 1) {
-            const int64_t x = __shfl_up_sync(0xffffffffu, sum, o);
+            const int x = __shfl_up_sync(0xffffffffu, sum, o);
             if (lane >= o)
                 sum += x;
         }
@@ -192,18 +190,17 @@ struct Walk {
     }
 
     __device__ __forceinline__ void init(const AttendPlan &P, int col) {
-        lane = threadIdx.x & 31;
-        int64_t total = 0;
-        for (int i = lane; i < P.R; i += 32)
+        int total = 0;
+        for (int i = threadIdx.x & 31; i < P.R; i += 32)
             total += tiles_of(P, range_of(P, i));
-        for (int o = 16; o > 0; o >>= 1)
-            total += __shfl_xor_sync(0xffffffffu, total, o);
-        const int64_t each = (total + P.cols - 1) / P.cols;  // so only the last CTAs may have none
-        pos = min(col * each, total);
-        end = min(pos + each, total);
+        total = __reduce_add_sync(0xffffffffu, total);
+        // equal shares, so only the last CTAs may have none (in 64 bits: a
+        // share times a CTA's number may pass the total)
+        const int64_t each = (total + P.cols - 1) / P.cols;
+        pos = (int)min(col * each, (int64_t)total);
+        end = (int)min(pos + each, (int64_t)total);
         r0 = 0;
-        base = 0;
-        load(P);
+        load(P, 0);
     }
 
     __device__ __forceinline__ bool next(const AttendPlan &P) {
@@ -211,20 +208,19 @@ struct Walk {
             return false;
         uint32_t here;
         while ((here = __ballot_sync(0xffffffffu, start <= pos && pos < stop)) == 0) {
-            base = __shfl_sync(0xffffffffu, stop, 31);
             r0 += 32;
             if (r0 >= P.R)
                 return false;  // the lengths changed under the call
-            load(P);
+            load(P, __shfl_sync(0xffffffffu, stop, 31));
         }
         const int k = __ffs(here) - 1;
-        const int64_t s = __shfl_sync(0xffffffffu, start, k), e = __shfl_sync(0xffffffffu, stop, k);
+        const int s = __shfl_sync(0xffffffffu, start, k), e = __shfl_sync(0xffffffffu, stop, k);
         r = r0 + k;
         range = range_of(P, r);
         begins = s == pos;
         ends = e <= end;
-        first = (int)(pos - s) + first_tile(P, range);
-        count = (int)(min(e, end) - pos);
+        first = pos - s + tile_of(P, range.lo);
+        count = min(e, end) - pos;
         pos += count;
         return true;
     }
@@ -451,13 +447,14 @@ __device__ __forceinline__ float from_q(uint32_t h, bool bf16) {
 }
 
 // Kernels of this file are launched so that each may start while the one
-// before it in the stream still runs. This waits for that one to be done and
-// its writes to be seen; nothing in global memory is touched before it. Then
-// the next one may be brought in.
-__device__ __forceinline__ void wait_for_launch() {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-}
+// before it in the stream still runs. The first waits for that one to be done
+// and its writes to be seen; nothing in global memory is touched before it.
+// The second lets the next one be brought in (the short kernels do; blocks
+// that only wait slow the long one down: 161 -> 173 us at four fp8 requests of
+// 131072 tokens).
+__device__ __forceinline__ void wait_for_launch() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
+__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
+
 
 // ---- the CTA's roles ---------------------------------------------------------
 
@@ -477,7 +474,7 @@ struct LastPage {
 __device__ __forceinline__ int resolve(const AttendPlan &P, const Walk &W, const Tile &T, uint64_t &valid, uint32_t &bad,
                                        LastPage &last) {
     const int lane = threadIdx.x & 31;
-    valid = bits((int)(W.range.lo - T.t0 > 64 ? 64 : W.range.lo - T.t0), (int)min((int64_t)T.rows, W.range.L - T.t0));
+    valid = bits(W.range.lo - T.t0, min(T.rows, W.range.L - T.t0));
     if (P.pages_per_tile == 1) {
         if (W.r != last.r || T.page != last.page) {
             int block = __ldg(P.table + W.r * P.row_stride + T.page);
@@ -599,43 +596,60 @@ __device__ __forceinline__ void load_by_tma(const AttendPlan &P, Control &C, con
     }
 }
 
-// A row of q to f16, times a power of two that brings its largest value to
-// [2^14, 2^15): exact for values within 2^27 of it. One warp.
-__device__ __forceinline__ void load_query_row(const AttendPlan &P, Control &C, const Memory &M, int r, int head, int h,
-                                               bool real) {
+// kRows rows of q (h, h + step, ...) to f16, each times a power of two that
+// brings its largest value to [2^14, 2^15): exact for values within 2^27 of
+// it. One warp; all rows' loads are issued before the first is used. Not
+// inlined: its registers would push the entries' loop into spilling.
+template <int kRows>
+__device__ __noinline__ void load_query_rows(const AttendPlan &P, Control &C, const Memory &M, int r, int group, int h0,
+                                                int step) {
+    constexpr int kPieces = (kMaxEntry / 8 + 31) / 32;
     const int lane = threadIdx.x & 31;
-    const uint16_t *src = P.q + r * P.q_request_stride + head * P.q_head_stride;
-    uint4 v[3];
-    float top = 0.0f;
+    uint4 v[kRows][kPieces];
 #pragma unroll
-    for (int i = 0; i < 3; i++) {
-        const int c = lane + 32 * i;
-        v[i] = make_uint4(0, 0, 0, 0);
-        if (real && c < P.E / 8)
-            v[i] = __ldg(reinterpret_cast<const uint4 *>(src) + c);
-        const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+    for (int m = 0; m < kRows; m++) {
+        const int h = h0 + m * step, head = group * P.group_heads + h;
+        const bool real = h < P.group_heads && head < P.H;
+        const uint4 *src = reinterpret_cast<const uint4 *>(P.q + r * P.q_request_stride + head * P.q_head_stride);
 #pragma unroll
-        for (int k = 0; k < 4; k++)
-            top = fmaxf(top, fmaxf(fabsf(from_q(w[k] & 0xffff, P.q_bf16)), fabsf(from_q(w[k] >> 16, P.q_bf16))));
+        for (int i = 0; i < kPieces; i++) {
+            v[m][i] = make_uint4(0, 0, 0, 0);
+            if (real && lane + 32 * i < P.E / 8)
+                v[m][i] = __ldg(src + lane + 32 * i);
+        }
     }
-    for (int o = 16; o > 0; o >>= 1)
-        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    // 2^(14 - exponent of top), kept within what one float holds
-    const int e = top > 0.0f && top < INFINITY ? max(-100, min(100, 14 - ilogbf(top))) : 0;
-    const float up = ldexpf(1.0f, e);
-    if (lane == 0)
-        C.q_scale[h] = ldexpf(1.0f, -e);
 #pragma unroll
-    for (int i = 0; i < 3; i++) {
-        const int c = lane + 32 * i;
-        if (c < P.E / 8) {
-            const uint32_t w[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-            uint32_t o[4];
+    for (int m = 0; m < kRows; m++) {
+        const int h = h0 + m * step;
+        float top = 0.0f;
+#pragma unroll
+        for (int i = 0; i < kPieces; i++) {
+            const uint32_t w[4] = {v[m][i].x, v[m][i].y, v[m][i].z, v[m][i].w};
 #pragma unroll
             for (int k = 0; k < 4; k++)
-                o[k] = pack<false>(from_q(w[k] & 0xffff, P.q_bf16) * up, from_q(w[k] >> 16, P.q_bf16) * up);
-            *reinterpret_cast<uint4 *>(M.q + (c >> 3) * P.padded_heads * 128 + h * 128 + (((c & 7) ^ (h & 7)) << 4)) =
-                make_uint4(o[0], o[1], o[2], o[3]);
+                top = fmaxf(top, fmaxf(fabsf(from_q(w[k] & 0xffff, P.q_bf16)), fabsf(from_q(w[k] >> 16, P.q_bf16))));
+        }
+        for (int o = 16; o > 0; o >>= 1)
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+        // 2^e with e = 14 - floor(log2(top)), kept within what one float
+        // holds; 1 where there is nothing to scale (zero, infinity)
+        const int exponent = (int)(__float_as_uint(top) >> 23) - 127;
+        const int e = top == 0.0f || exponent == 128 ? 0 : max(-100, min(100, 14 - exponent));
+        const float up = __uint_as_float((uint32_t)(127 + e) << 23);
+        if (lane == 0 && h < P.padded_heads)
+            C.q_scale[h] = __uint_as_float((uint32_t)(127 - e) << 23);
+#pragma unroll
+        for (int i = 0; i < kPieces; i++) {
+            const int c = lane + 32 * i;
+            if (h < P.padded_heads && c < P.E / 8) {
+                const uint32_t w[4] = {v[m][i].x, v[m][i].y, v[m][i].z, v[m][i].w};
+                uint32_t o[4];
+#pragma unroll
+                for (int k = 0; k < 4; k++)
+                    o[k] = pack<false>(from_q(w[k] & 0xffff, P.q_bf16) * up, from_q(w[k] >> 16, P.q_bf16) * up);
+                *reinterpret_cast<uint4 *>(M.q + (c >> 3) * P.padded_heads * 128 + h * 128 + (((c & 7) ^ (h & 7)) << 4)) =
+                    make_uint4(o[0], o[1], o[2], o[3]);
+            }
         }
     }
 }
@@ -654,7 +668,7 @@ __device__ __forceinline__ void load_fp8(const AttendPlan &P, Control &C, const 
     uint32_t bad = 0, n = 0, segments = 0;
     uint4 v[2][kPanels];
     uint64_t valid[2];
-    LastPage last;
+    LastPage last, last_ahead;
     const int my_page = P.pages_per_tile == 1 ? 0 : row / P.block_size;
     const int my_row = row - my_page * P.block_size;
 
@@ -671,6 +685,19 @@ __device__ __forceinline__ void load_fp8(const AttendPlan &P, Control &C, const 
                 asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
                              : "=r"(x[i].x), "=r"(x[i].y), "=r"(x[i].z), "=r"(x[i].w)
                              : "l"(src + i * 64));
+        }
+        // a later tile of one page is a run of bytes: on its way to L2
+        if (warp == 0 && P.pages_per_tile == 1 && j + kFp8Ahead < W.count) {
+            const Tile A = tile_at(P, W.first + j + kFp8Ahead);
+            uint64_t unused;
+            uint32_t later = 0;  // raised when the tile itself is loaded
+            const int64_t ahead = resolve(P, W, A, unused, later, last_ahead);
+            if (ahead >= 0 && elect())
+                asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(
+                                 P.pool + ahead * P.block_stride + (int64_t)A.row0 * P.token_bytes),
+                             "r"(A.rows * P.token_bytes)
+                             : "memory");
+            __syncwarp();
         }
     };
     auto store = [&](const uint4(&x)[kPanels], uint64_t rows) {
@@ -701,20 +728,18 @@ __device__ __forceinline__ void load_fp8(const AttendPlan &P, Control &C, const 
     };
 
     while (W.next(P)) {
-        load(v[0], valid[0], 0);
-        if (W.count > 1)
-            load(v[1], valid[1], 1);
         if (segments > 0)
             bar_wait(C, &C.q_free, (segments - 1) & 1, P.status);
         segments++;
-        for (int h = warp; h < P.padded_heads; h += kFp8Loaders) {
-            const int head = group * P.group_heads + h;
-            load_query_row(P, C, M, W.r, head, h, h < P.group_heads && head < P.H);
-        }
+        for (int h = warp; h < P.padded_heads; h += 4 * kFp8Loaders)
+            load_query_rows<4>(P, C, M, W.r, group, h, kFp8Loaders);
         fence_async();
         __syncwarp();
         if (lane == 0)
             bar_arrive(&C.q_full);
+        load(v[0], valid[0], 0);
+        if (W.count > 1)
+            load(v[1], valid[1], 1);
         for (int j = 0; j < W.count; j += 2) {
             store(v[0], valid[0]);
             if (j + 2 < W.count)
@@ -804,6 +829,33 @@ __device__ __forceinline__ void multiply_values(const AttendPlan &P, Control &C,
     }
 }
 
+// A tile's logits (log2) to the workspace, for the token weights: pairs of
+// tokens where the whole tile is attended and its first token lies on an even
+// place, else one by one.
+__device__ __forceinline__ void keep_logits(const AttendPlan &P, const Walk &W, const Tile &T, const float *s, int head0,
+                                            int heads, int ra) {
+    const int at = T.t0 - (W.range.lo & ~1), c0 = 2 * (threadIdx.x & 3);
+    const uint64_t inside = bits(W.range.lo - T.t0, min(T.rows, W.range.L - T.t0));
+    float *a = P.logits + ((int64_t)W.r * P.H + head0 + ra) * P.logit_stride + at + c0, *b = a + 8 * P.logit_stride;
+    if (inside == ~0ull && (at & 1) == 0) {
+        if (ra < heads)
+#pragma unroll
+            for (int i = 0; i < 8; i++)
+                *reinterpret_cast<float2 *>(a + 8 * i) = make_float2(s[4 * i], s[4 * i + 1]);
+        if (ra + 8 < heads)
+#pragma unroll
+            for (int i = 0; i < 8; i++)
+                *reinterpret_cast<float2 *>(b + 8 * i) = make_float2(s[4 * i + 2], s[4 * i + 3]);
+        return;
+    }
+#pragma unroll
+    for (int i = 0; i < 32; i++) {
+        const int c = 8 * (i >> 2) + (i & 1);
+        if ((inside >> (c + c0) & 1) && ((i & 2) ? ra + 8 : ra) < heads)
+            ((i & 2) ? b : a)[c] = s[i];
+    }
+}
+
 // Four warps: the softmax, P, and the results. Warp w holds heads 16 w ..
 // 16 w + 15 of S, and values 32 w .. 32 w + 31 of each 128 of O^T.
 template <bool kBf16, bool kFp8>
@@ -868,18 +920,8 @@ __device__ __forceinline__ void soften(const AttendPlan &P, Control &C, const Me
                 xb = fmaxf(xb, __shfl_xor_sync(0xffffffffu, xb, 1));
                 xa = fmaxf(xa, __shfl_xor_sync(0xffffffffu, xa, 2));
                 xb = fmaxf(xb, __shfl_xor_sync(0xffffffffu, xb, 2));
-                if (P.logits != nullptr) {
-                    const int64_t base = W.range.lo & ~(int64_t)1;
-                    float *to = P.logits + ((int64_t)W.r * P.H + head0) * P.logit_stride + (T.t0 - base);
-                    const uint64_t inside = bits((int)max((int64_t)0, W.range.lo - T.t0),
-                                                 (int)min((int64_t)T.rows, W.range.L - T.t0));
-#pragma unroll
-                    for (int i = 0; i < 32; i++) {
-                        const int c = 8 * (i >> 2) + 2 * (lane & 3) + (i & 1), row = (i & 2) ? rb : ra;
-                        if ((inside >> c & 1) && row < heads)
-                            to[row * P.logit_stride + c] = s[i];
-                    }
-                }
+                if (P.logits != nullptr)
+                    keep_logits(P, W, T, s, head0, heads, ra);
             }
             if (soft_any(xa > ma + kLag || xb > mb + kLag)) {
                 float fa = 1.0f, fb = 1.0f;
@@ -1096,31 +1138,41 @@ __global__ void __launch_bounds__((kFirstLoader + (kFp8 ? kFp8Loaders : 1)) * 32
 
 // ---- joining -------------------------------------------------------------------
 
-constexpr int kJoinWarps = 4;
+constexpr int kJoinWarps = kMaxValue / 128;  // a warp for 128 values each
 
-// Block (c, y), a warp per head: if a request that spans several CTAs begins
-// in CTA column c, joins its parts; and writes the rows of requests without
-// tokens (r = c, c + cols, ...).
+// Block (x, h): joins head h of the x-th request that spans several CTAs (each
+// begins in a CTA of its own, so there are at most as many as requests and
+// CTAs); and writes the rows of requests without tokens (r = x, x + blocks,
+// ...).
 __global__ void __launch_bounds__(kJoinWarps * 32) lmc_attend_join_kernel(const __grid_constant__ AttendPlan P) {
     __shared__ float factors[kJoinWarps][kMaxCols];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int col = blockIdx.x, h = blockIdx.y * kJoinWarps + warp;
+    const int h = blockIdx.y, v = threadIdx.x * 4;
     wait_for_launch();
-    if (h >= P.H)
-        return;
-    for (int r = col; r < P.R; r += P.cols) {
+    let_next_start();
+    for (int r = blockIdx.x; r < P.R; r += gridDim.x) {
         const Range g = range_of(P, r);
         if (!g.ok || g.L != 0)
             continue;
-        for (int v = lane; v < P.V; v += 32)
-            P.out[r * P.out_request_stride + h * P.out_head_stride + v] = 0;
-        if (lane == 0 && P.lse != nullptr)
+        for (int i = threadIdx.x; i < P.V; i += kJoinWarps * 32)
+            P.out[r * P.out_request_stride + h * P.out_head_stride + i] = 0;
+        if (threadIdx.x == 0 && P.lse != nullptr)
             P.lse[r * P.lse_request_stride + h] = -INFINITY;
     }
+    int col = -1, seen = 0;
+    for (int c0 = 0; c0 < P.cols; c0 += 32) {
+        const bool begins = c0 + lane < P.cols && P.segment[2 * (c0 + lane) + 1].x >= 0;
+        const uint32_t here = __ballot_sync(0xffffffffu, begins);
+        const int rank = seen + __popc(here & ((1u << lane) - 1u));
+        const uint32_t mine = __ballot_sync(0xffffffffu, begins && rank == (int)blockIdx.x);
+        if (mine != 0)
+            col = c0 + __ffs(mine) - 1;
+        seen += __popc(here);
+    }
+    if (col < 0)
+        return;
     const int2 head = P.segment[2 * col + 1];
     const int r = head.x;
-    if (r < 0)
-        return;
     // parts: slot 2 col + 1, then 2 (col + 1), ...; all CTAs but the last have
     // as many tiles as the next one
     const int rest = tiles_of(P, range_of(P, r)) - head.y;
@@ -1129,59 +1181,52 @@ __global__ void __launch_bounds__(kJoinWarps * 32) lmc_attend_join_kernel(const 
         const int each = max(1, P.segment[2 * col + 2].y);
         parts = min(P.cols - col, 1 + (rest + each - 1) / each);
     }
+    // each warp has the factors for itself: no barrier
+    const float2 *ml = P.part_ml + (int64_t)2 * col * P.H + h;
     float top = -INFINITY;
     for (int i = lane; i < parts; i += 32) {
-        const float2 ml = P.part_ml[(int64_t)(2 * (col + i) + (i == 0)) * P.H + h];
-        if (ml.y != 0.0f)
-            top = fmaxf(top, ml.x);
+        const float2 x = ml[(int64_t)(2 * i + (i == 0)) * P.H];
+        if (x.y != 0.0f)
+            top = fmaxf(top, x.x);
     }
     for (int o = 16; o > 0; o >>= 1)
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
     float sum = 0.0f;
     for (int i = lane; i < parts; i += 32) {
-        const float2 ml = P.part_ml[(int64_t)(2 * (col + i) + (i == 0)) * P.H + h];
-        const float f = ml.y == 0.0f ? 0.0f : exp2_fast(ml.x - top);
+        const float2 x = ml[(int64_t)(2 * i + (i == 0)) * P.H];
+        const float f = x.y == 0.0f ? 0.0f : exp2_fast(x.x - top);
         factors[warp][i] = f;
-        sum += ml.y == 0.0f ? 0.0f : ml.y * f;
+        sum += x.y == 0.0f ? 0.0f : x.y * f;
     }
     for (int o = 16; o > 0; o >>= 1)
         sum += __shfl_xor_sync(0xffffffffu, sum, o);
     __syncwarp();
-    float4 acc[kMaxValue / 128] = {};
-    const float *part = P.part_o + ((int64_t)(2 * col + 1) * P.H + h) * P.V;
-    const int64_t step = (int64_t)2 * P.H * P.V;
-#pragma unroll 4
-    for (int i = 0; i < parts; i++) {
-        const float f = factors[warp][i];
-        const float4 *o = reinterpret_cast<const float4 *>(part + i * step - (i > 0 ? (int64_t)P.H * P.V : 0));
-#pragma unroll
-        for (int k = 0; k < kMaxValue / 128; k++)
-            if (4 * (lane + 32 * k) < P.V) {
-                const float4 x = __ldcs(o + lane + 32 * k);
-                acc[k].x += x.x * f;
-                acc[k].y += x.y * f;
-                acc[k].z += x.z * f;
-                acc[k].w += x.w * f;
-            }
-    }
-    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-    uint16_t *to = P.out + r * P.out_request_stride + h * P.out_head_stride;
-#pragma unroll
-    for (int k = 0; k < kMaxValue / 128; k++) {
-        const int v = 4 * (lane + 32 * k);
-        if (v < P.V) {
-            to[v] = to_out(acc[k].x * inv, P.q_bf16);
-            to[v + 1] = to_out(acc[k].y * inv, P.q_bf16);
-            to[v + 2] = to_out(acc[k].z * inv, P.q_bf16);
-            to[v + 3] = to_out(acc[k].w * inv, P.q_bf16);
-        }
-    }
-    if (lane == 0) {
+    if (threadIdx.x == 0) {
         const float lse = sum == 0.0f ? -INFINITY : top + log2f(sum);
         P.lse2[(int64_t)r * P.H + h] = lse;
         if (P.lse != nullptr)
             P.lse[r * P.lse_request_stride + h] = lse * 0.693147180559945309f;
     }
+    if (v >= P.V)
+        return;
+    float4 acc = {};
+    const float *part = P.part_o + ((int64_t)2 * col * P.H + h) * P.V + v;
+    const int64_t step = (int64_t)P.H * P.V;
+#pragma unroll 8
+    for (int i = 0; i < parts; i++) {
+        const float f = factors[warp][i];
+        const float4 x = __ldcs(reinterpret_cast<const float4 *>(part + (2 * i + (i == 0)) * step));
+        acc.x += x.x * f;
+        acc.y += x.y * f;
+        acc.z += x.z * f;
+        acc.w += x.w * f;
+    }
+    const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+    uint16_t *to = P.out + r * P.out_request_stride + h * P.out_head_stride + v;
+    to[0] = to_out(acc.x * inv, P.q_bf16);
+    to[1] = to_out(acc.y * inv, P.q_bf16);
+    to[2] = to_out(acc.z * inv, P.q_bf16);
+    to[3] = to_out(acc.w * inv, P.q_bf16);
 }
 
 constexpr int kWeightThreads = 256;
@@ -1190,16 +1235,17 @@ constexpr int kWeightThreads = 256;
 __global__ void __launch_bounds__(kWeightThreads) lmc_attend_weights_kernel(const __grid_constant__ AttendPlan P) {
     const int r = blockIdx.y;
     wait_for_launch();
+    let_next_start();
     const Range g = range_of(P, r);
     if (!g.ok)
         return;
     const int64_t t = g.lo + blockIdx.x * (int64_t)kWeightThreads + threadIdx.x;
     if (t >= g.L)
         return;
-    const float *x = P.logits + (int64_t)r * P.H * P.logit_stride + (t - (g.lo & ~(int64_t)1));
+    const float *x = P.logits + (int64_t)r * P.H * P.logit_stride + (t - (g.lo & ~1));
     const float *lse = P.lse2 + (int64_t)r * P.H;
     float w = 0.0f;
-#pragma unroll 4
+#pragma unroll 16
     for (int h = 0; h < P.H; h++) {
         const float top = __ldg(lse + h);
         const float p = exp2_fast(__ldcs(x + h * P.logit_stride) - top);
@@ -1355,9 +1401,8 @@ extern "C" int lmc_attend(const lmc_layout *L, const lmc_entries *e, const void 
     P.num_blocks = L->num_blocks;
     P.table = e->table.table;
     P.row_stride = e->table.row_stride;
-    P.num_cols = e->table.num_cols;
     P.lengths = a->lengths;
-    P.max_length = a->max_length;
+    P.max_length = (int32_t)std::min(a->max_length, (int64_t)std::min<int64_t>(e->table.num_cols, INT32_MAX / N) * N);
     P.q = static_cast<const uint16_t *>(a->q);
     P.q_request_stride = a->q_request_stride;
     P.q_head_stride = a->q_head_stride;
@@ -1387,6 +1432,8 @@ extern "C" int lmc_attend(const lmc_layout *L, const lmc_entries *e, const void 
     P.pages_per_tile = N < kTile && N % 8 == 0 ? (int32_t)(kTile / N) : 1;
     P.span = (int32_t)N * P.pages_per_tile;
     P.tiles_per_span = (P.span + kTile - 1) / kTile;
+    if (R * (P.max_length / P.span + 1) * P.tiles_per_span > INT32_MAX)
+        return LMC_ERR_OVERFLOW;
     P.head_groups = W.head_groups;
     P.group_heads = W.group_heads;
     P.cols = std::max(1, std::min(W.cols, sms / W.head_groups));
@@ -1422,11 +1469,11 @@ extern "C" int lmc_attend(const lmc_layout *L, const lmc_entries *e, const void 
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (!follow(kern, dim3((unsigned)(P.cols * P.head_groups)), (kFirstLoader + (fp8 ? kFp8Loaders : 1)) * 32, smem, s,
                 P) ||
-        !follow(lmc_attend_join_kernel, dim3((unsigned)P.cols, (unsigned)((H + kJoinWarps - 1) / kJoinWarps)),
-                kJoinWarps * 32, 0, s, P))
+        !follow(lmc_attend_join_kernel, dim3((unsigned)std::min<int64_t>(P.cols, R), (unsigned)H), kJoinWarps * 32, 0,
+                s, P))
         return LMC_ERR_CUDA;
     if (P.weights != nullptr) {
-        const int64_t tokens = P.window > 0 ? std::min<int64_t>(P.max_length, P.window) : P.max_length;
+        const int64_t tokens = P.window > 0 ? std::min(P.max_length, P.window) : std::max(P.max_length, 1);
         if (!follow(lmc_attend_weights_kernel,
                     dim3((unsigned)((tokens + kWeightThreads - 1) / kWeightThreads), (unsigned)R), kWeightThreads, 0, s,
                     P))
