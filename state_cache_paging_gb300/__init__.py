@@ -374,8 +374,9 @@ def _stream_ptr(stream, *buffers):
     call's kernels have read or written it."""
     import torch
     if stream is None:
-        stream = torch.cuda.current_stream()
-    elif stream != torch.cuda.current_stream(stream.device):
+        # the handle alone: a Stream object costs more than some calls' kernels
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    if stream != torch.cuda.current_stream(stream.device):
         todo = list(buffers)
         while todo:
             t = todo.pop()
@@ -512,29 +513,37 @@ def _refuse(what: str):
     raise LmcError(LMC_ERR_INVALID_ARG, what)
 
 
-def _value_type(t) -> int:
-    """LMC_E_* of a bfloat16 or float16 tensor."""
-    import torch
-    if t.dtype == torch.bfloat16:
-        return LMC_E_BF16
-    if t.dtype == torch.float16:
-        return LMC_E_F16
-    _refuse(f"values must be bfloat16 or float16, not {t.dtype}")
-
+# Decode steps make these calls with little work each, so their checks are kept
+# to a few attribute reads per tensor.
 
 def _table(name: str, t) -> lmc_block_table:
+    import torch
     _visible(name, t)
-    if t.dim() != 2 or t.element_size() != 4 or t.is_floating_point() or (t.shape[1] > 1 and t.stride(1) != 1):
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 2 or t.dtype != torch.int32 or (stride[1] != 1 and shape[1] > 1):
         _refuse(f"{name} must be int32 [num_requests, cols] with unit column stride")
-    return lmc_block_table(t.data_ptr(), max(int(t.stride(0)), int(t.shape[1])), int(t.shape[1]))
+    cols = shape[1]
+    return lmc_block_table(t.data_ptr(), stride[0] if stride[0] > cols else cols, cols)
 
 
 def _ints(name: str, t, *shape):
-    """An int32 tensor of `shape`, contiguous."""
+    """The address of an int32 tensor of `shape`, contiguous."""
+    import torch
     _visible(name, t)
-    if t.element_size() != 4 or t.is_floating_point() or tuple(t.shape) != shape or not t.is_contiguous():
+    if t.dtype != torch.int32 or t.shape != shape or not t.is_contiguous():
         _refuse(f"{name} must be contiguous int32 {list(shape)}")
     return t.data_ptr()
+
+
+def _floats(name: str, t, rows: int, cols: int):
+    """(address, row stride) of a float32 [rows, >= cols] tensor."""
+    import torch
+    _visible(name, t)
+    shape, stride = t.shape, t.stride()
+    if len(shape) != 2 or t.dtype != torch.float32 or shape[0] != rows or shape[1] < cols or \
+            (stride[1] != 1 and shape[1] > 1):
+        _refuse(f"{name} must be float32 [{rows}, {cols}] with unit column stride")
+    return t.data_ptr(), stride[0] if stride[0] > cols else cols
 
 
 def _status(t):
@@ -544,16 +553,32 @@ def _status(t):
     return t.data_ptr()
 
 
-def _entries(layout: Layout, layer: int, pool, table, entry_dim: int, value_type: int, scale: float) -> lmc_entries:
+def _pool(layout: Layout, pool):
+    _visible("pool", pool)
+    if pool.nbytes < layout.pool_bytes or not pool.is_contiguous():
+        _refuse(f"pool must be contiguous and hold the {layout.pool_bytes} bytes the layout addresses")
+    return pool.data_ptr()
+
+
+def _value_type(t) -> int:
+    """LMC_E_* of a bfloat16 or float16 tensor."""
+    import torch
+    dtype = t.dtype
+    if dtype == torch.bfloat16:
+        return LMC_E_BF16
+    if dtype == torch.float16:
+        return LMC_E_F16
+    _refuse(f"values must be bfloat16 or float16, not {dtype}")
+
+
+def _entries(layout: Layout, layer: int, table, entry_dim: int, value_type: int, scale: float) -> lmc_entries:
     """The layer's entries: of `value_type` where its token_bytes hold
     entry_dim 16-bit values, fp8 e4m3 where they hold entry_dim bytes."""
     if not 0 <= layer < layout.num_layers:
         _refuse(f"layer {layer} of {layout.num_layers}")
-    _visible("pool", pool)
-    if pool.numel() * pool.element_size() < layout.pool_bytes or not pool.is_contiguous():
-        _refuse(f"pool must be contiguous and hold the {layout.pool_bytes} bytes the layout addresses")
-    dtype = LMC_E_E4M3 if layout.real_bytes[layer] == layout.block_size * entry_dim else value_type
-    return lmc_entries(layer, dtype, entry_dim, int(table.shape[0]), scale, 0, _table("block table", table))
+    if layout.real_bytes[layer] == layout.block_size * entry_dim:
+        value_type = LMC_E_E4M3
+    return lmc_entries(layer, value_type, entry_dim, table.shape[0], scale, 0, _table("block table", table))
 
 
 def lmc_append(layout: Layout, layer: int, pool, table, requests, positions, entries, status, scale: float = 1.0,
@@ -562,16 +587,19 @@ def lmc_append(layout: Layout, layer: int, pool, table, requests, positions, ent
     row stride) as the entry at position positions[i] of request requests[i]
     (int32 device tensors; request -1: skipped) of a paged layer. A layer
     whose token_bytes equal entry_dim holds fp8 e4m3 codes of value / scale."""
-    if entries.dim() != 2 or (entries.shape[1] > 1 and entries.stride(1) != 1):
-        _refuse("entries must be [rows, entry_dim] with unit column stride")
     _visible("entries", entries)
+    shape, stride = entries.shape, entries.stride()
+    if len(shape) != 2 or (stride[1] != 1 and shape[1] > 1):
+        _refuse("entries must be [rows, entry_dim] with unit column stride")
+    n, dim = shape
     vt = _value_type(entries)
-    n, dim = int(entries.shape[0]), int(entries.shape[1])
-    e = _entries(layout, layer, pool, table, dim, vt, scale)
-    req, pos = _ints("requests", requests, n), _ints("positions", positions, n)
-    strm = _stream_ptr(stream, pool, table, requests, positions, entries, status)
-    _check(_lib.lmc_append(layout.handle, ctypes.byref(e), pool.data_ptr(), req, pos, entries.data_ptr(), vt,
-                           max(int(entries.stride(0)), dim), n, _status(status), strm), "lmc_append")
+    e = _entries(layout, layer, table, dim, vt, scale)
+    rc = _lib.lmc_append(layout.handle, e, _pool(layout, pool), _ints("requests", requests, n),
+                         _ints("positions", positions, n), entries.data_ptr(), vt,
+                         stride[0] if stride[0] > dim else dim, n, _status(status),
+                         _stream_ptr(stream, pool, table, requests, positions, entries, status))
+    if rc != LMC_OK:
+        raise LmcError(rc, "lmc_append")
 
 
 def lmc_attend_workspace(layout: Layout, layer: int, num_requests: int, num_heads: int, value_dim: int,
@@ -593,35 +621,28 @@ def lmc_attend(layout: Layout, layer: int, pool, table, lengths, q, value_dim: i
     table holds). lse (float32 [requests, heads]) receives the log of the sum
     of exponentials; weights (float32 [requests, >= max_length]) has the sum
     over the heads of each token's probability added to it."""
-    if q.dim() != 3 or out.dim() != 3 or q.stride(2) != 1 or out.stride(2) != 1 or out.dtype != q.dtype:
-        _refuse("q and out must be [requests, heads, dim] of one type with a contiguous last dimension")
     _visible("q", q)
     _visible("out", out)
     _visible("workspace", workspace)
-    R, H, dim = (int(n) for n in q.shape)
-    if tuple(out.shape) != (R, H, value_dim) or int(table.shape[0]) != R:
+    shape, qs, os_ = q.shape, q.stride(), out.stride()
+    if len(shape) != 3 or len(os_) != 3 or qs[2] != 1 or os_[2] != 1 or out.dtype != q.dtype:
+        _refuse("q and out must be [requests, heads, dim] of one type with a contiguous last dimension")
+    R, H, dim = shape
+    if out.shape != (R, H, value_dim) or table.shape[0] != R:
         _refuse(f"out must be [{R}, {H}, {value_dim}] and the block table have {R} rows")
     vt = _value_type(q)
-    e = _entries(layout, layer, pool, table, dim, vt, scale)
+    e = _entries(layout, layer, table, dim, vt, scale)
     if max_length is None:
-        max_length = max(1, int(table.shape[1]) * layout.block_size)
-    a = lmc_attention(_ints("lengths", lengths, R), max_length, q.data_ptr(), q.stride(0), q.stride(1),
-                      out.data_ptr(), out.stride(0), out.stride(1), None, 0, None, 0, vt, H, value_dim,
-                      softmax_scale)
-    for name, t, cols in (("lse", lse, H), ("weights", weights, max_length)):
-        if t is None:
-            continue
-        _visible(name, t)
-        if t.dim() != 2 or not t.is_floating_point() or t.element_size() != 4 or t.shape[0] != R or \
-                t.shape[1] < cols or (t.shape[1] > 1 and t.stride(1) != 1):
-            _refuse(f"{name} must be float32 [{R}, {cols}] with unit column stride")
-    if lse is not None:
-        a.lse, a.lse_request_stride = lse.data_ptr(), max(lse.stride(0), H)
-    if weights is not None:
-        a.weights, a.weights_request_stride = weights.data_ptr(), max(weights.stride(0), max_length)
-    strm = _stream_ptr(stream, pool, table, lengths, q, out, workspace, status, lse, weights)
-    _check(_lib.lmc_attend(layout.handle, ctypes.byref(e), pool.data_ptr(), ctypes.byref(a), workspace.data_ptr(),
-                           workspace.numel() * workspace.element_size(), _status(status), strm), "lmc_attend")
+        max_length = max(1, e.table.num_cols * layout.block_size)
+    lse_p, lse_s = (None, 0) if lse is None else _floats("lse", lse, R, H)
+    w_p, w_s = (None, 0) if weights is None else _floats("weights", weights, R, max_length)
+    a = lmc_attention(_ints("lengths", lengths, R), max_length, q.data_ptr(), qs[0], qs[1], out.data_ptr(), os_[0],
+                      os_[1], lse_p, lse_s, w_p, w_s, vt, H, value_dim, softmax_scale)
+    rc = _lib.lmc_attend(layout.handle, e, _pool(layout, pool), a, workspace.data_ptr(), workspace.nbytes,
+                         _status(status),
+                         _stream_ptr(stream, pool, table, lengths, q, out, workspace, status, lse, weights))
+    if rc != LMC_OK:
+        raise LmcError(rc, "lmc_attend")
 
 
 def lmc_select_tokens(scores, lengths, budget: int, recent: int, kept, kept_scores, kept_lengths, status,
@@ -632,23 +653,24 @@ def lmc_select_tokens(scores, lengths, budget: int, recent: int, kept, kept_scor
     kept_scores (float32, or None) [sets, requests, budget] receive the kept
     positions in increasing order and their scores, kept_lengths (int32
     [requests]) how many there are."""
-    if scores.dim() != 3 or not scores.is_floating_point() or scores.element_size() != 4 or \
-            (scores.shape[2] > 1 and scores.stride(2) != 1):
-        _refuse("scores must be float32 [sets, requests, tokens] with unit token stride")
+    import torch
     _visible("scores", scores)
-    S, R, T = (int(n) for n in scores.shape)
-    kept_p = _ints("kept", kept, S, R, budget)
+    shape, stride = scores.shape, scores.stride()
+    if len(shape) != 3 or scores.dtype != torch.float32 or (stride[2] != 1 and shape[2] > 1):
+        _refuse("scores must be float32 [sets, requests, tokens] with unit token stride")
+    S, R, T = shape
+    scores_out = None
     if kept_scores is not None:
         _visible("kept_scores", kept_scores)
-        if not kept_scores.is_floating_point() or kept_scores.element_size() != 4 or \
-                tuple(kept_scores.shape) != (S, R, budget) or not kept_scores.is_contiguous():
+        if kept_scores.dtype != torch.float32 or kept_scores.shape != (S, R, budget) or not kept_scores.is_contiguous():
             _refuse(f"kept_scores must be contiguous float32 {[S, R, budget]}")
-    strm = _stream_ptr(stream, scores, lengths, kept, kept_scores, kept_lengths, status)
-    _check(_lib.lmc_select_tokens(scores.data_ptr(), scores.stride(0), scores.stride(1), S, R,
-                                  _ints("lengths", lengths, R), T, int(budget), int(recent), kept_p,
-                                  None if kept_scores is None else kept_scores.data_ptr(),
-                                  _ints("kept_lengths", kept_lengths, R), _status(status), strm),
-           "lmc_select_tokens")
+        scores_out = kept_scores.data_ptr()
+    rc = _lib.lmc_select_tokens(scores.data_ptr(), stride[0], stride[1], S, R, _ints("lengths", lengths, R), T, budget,
+                                recent, _ints("kept", kept, S, R, budget), scores_out,
+                                _ints("kept_lengths", kept_lengths, R), _status(status),
+                                _stream_ptr(stream, scores, lengths, kept, kept_scores, kept_lengths, status))
+    if rc != LMC_OK:
+        raise LmcError(rc, "lmc_select_tokens")
 
 
 def lmc_move_tokens(layout: Layout, kv_group: int, pool, src_table, dst_table, kept, kept_lengths, status,
@@ -657,21 +679,21 @@ def lmc_move_tokens(layout: Layout, kv_group: int, pool, src_table, dst_table, k
     kept[set, request, j] (j < kept_lengths[request]) under `src_table` to
     positions j under `dst_table`, whose blocks must be others. kept: int32
     [sets, requests, most], with one set for all layers or one per layer."""
-    _visible("pool", pool)
-    if pool.numel() * pool.element_size() < layout.pool_bytes or not pool.is_contiguous():
-        _refuse(f"pool must be contiguous and hold the {layout.pool_bytes} bytes the layout addresses")
+    import torch
     _visible("kept", kept)
-    if kept.dim() != 3 or kept.element_size() != 4 or kept.is_floating_point() or \
-            (kept.shape[2] > 1 and kept.stride(2) != 1):
+    shape, stride = kept.shape, kept.stride()
+    if len(shape) != 3 or kept.dtype != torch.int32 or (stride[2] != 1 and shape[2] > 1):
         _refuse("kept must be int32 [sets, requests, most] with unit last stride")
-    S, R, K = (int(n) for n in kept.shape)
+    S, R, K = shape
     src, dst = _table("source table", src_table), _table("destination table", dst_table)
-    if int(src_table.shape[0]) != R or int(dst_table.shape[0]) != R:
+    if src_table.shape[0] != R or dst_table.shape[0] != R:
         _refuse(f"the block tables must have {R} rows")
-    strm = _stream_ptr(stream, pool, src_table, dst_table, kept, kept_lengths, status)
-    _check(_lib.lmc_move_tokens(layout.handle, int(kv_group), pool.data_ptr(), R, ctypes.byref(src),
-                                ctypes.byref(dst), kept.data_ptr(), S, kept.stride(0), max(kept.stride(1), K),
-                                _ints("kept_lengths", kept_lengths, R), K, _status(status), strm), "lmc_move_tokens")
+    rc = _lib.lmc_move_tokens(layout.handle, kv_group, _pool(layout, pool), R, src, dst, kept.data_ptr(), S, stride[0],
+                              stride[1] if stride[1] > K else K, _ints("kept_lengths", kept_lengths, R), K,
+                              _status(status),
+                              _stream_ptr(stream, pool, src_table, dst_table, kept, kept_lengths, status))
+    if rc != LMC_OK:
+        raise LmcError(rc, "lmc_move_tokens")
 
 
 def lmc_selftest_wait(status, rounds: int, stream=None) -> None:

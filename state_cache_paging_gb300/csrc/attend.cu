@@ -51,6 +51,8 @@
 #include <algorithm>
 #include <cmath>
 #include <cstdint>
+#include <mutex>
+#include <vector>
 
 #include "lmc_internal.h"
 
@@ -1331,6 +1333,26 @@ bool tensor_map(CUtensorMap *map, bool bf16, const void *base, int64_t values, i
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
+// Lets the attention kernels take a whole SM's shared memory (once per kernel
+// and device: the call costs as much as a launch).
+bool allow_shared_memory(int which, void (*kern)(AttendPlan)) {
+    static std::mutex mu;
+    static std::vector<int> done[3];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess)
+        return false;
+    std::lock_guard<std::mutex> lock(mu);
+    if ((int)done[which].size() <= dev)
+        done[which].resize(dev + 1, 0);
+    if (!done[which][dev]) {
+        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 kSmemLimit - (int)((sizeof(Control) + 1023) / 1024 * 1024)) != cudaSuccess)
+            return false;
+        done[which][dev] = 1;
+    }
+    return true;
+}
+
 // Launches a kernel that may start while the one before it in the stream still
 // runs (it waits for that one itself): its start-up costs no gap.
 bool follow(void (*kern)(AttendPlan), dim3 grid, int threads, size_t smem, cudaStream_t s, const AttendPlan &P) {
@@ -1464,7 +1486,7 @@ extern "C" int lmc_attend(const lmc_layout *L, const lmc_entries *e, const void 
             return LMC_ERR_CUDA;
     }
     auto kern = fp8 ? lmc_attend_kernel<false, true> : bf16 ? lmc_attend_kernel<true, false> : lmc_attend_kernel<false, false>;
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+    if (!allow_shared_memory(fp8 ? 2 : bf16 ? 1 : 0, kern))
         return LMC_ERR_CUDA;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (!follow(kern, dim3((unsigned)(P.cols * P.head_groups)), (kFirstLoader + (fp8 ? kFp8Loaders : 1)) * 32, smem, s,
