@@ -260,13 +260,22 @@ __global__ void __launch_bounds__(kRowThreads) lmc_move_kernel(const __grid_cons
 // gives its next eight. A row is shared by the CTAs of a cluster, which read
 // one another's histograms through distributed shared memory; each keeps its
 // part of the keys in its own shared memory (kCached), so the scores are read
-// from HBM once. The histogram has a column per lane: scores share few
-// exponents, and one counter per key prefix would serialise a warp's
-// increments. Then each warp walks its own run of tokens in order, and a
-// token's place among the kept is the number kept before it.
+// from HBM once. The floor is that read (75 MB for 96 rows of 131072 with what
+// is written: 11 us); the work is bound by instructions, so keys are taken
+// four at a time, the first histogram is made while they are loaded, and a
+// pass stops the search as soon as a bin is taken whole. The histogram has
+// eight columns, by lane: scores share few exponents, and one counter per bin
+// would serialise a warp's increments. Then each warp walks its own run of
+// tokens in order, and a token's place among the kept is the number kept
+// before it.
 constexpr int kSelThreads = 512;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kSelMaxCluster = 8;
+constexpr int kSelColumns = 8;
+#ifndef LMC_SEL_PER_SM
+#define LMC_SEL_PER_SM 3
+#endif
+constexpr int kSelPerSm = LMC_SEL_PER_SM;
 
 struct SelectPlan {
     const float *scores;
@@ -280,9 +289,9 @@ struct SelectPlan {
     int32_t budget, recent;
     int32_t num_requests;
     int32_t cluster;
-    int32_t cap;  // keys a CTA can hold
 };
 
+// Keeps the order of the scores; NaN below every number, -0 as 0.
 __device__ __forceinline__ uint32_t order_key(float x) {
     if (x != x)
         return 0;  // below every number
@@ -290,18 +299,42 @@ __device__ __forceinline__ uint32_t order_key(float x) {
     return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
 }
 
-struct SelectShared {
-    uint32_t hist[256 * 32];
-    uint32_t totals[2][256];       // this CTA's, read by the cluster
-    uint32_t all[256];             // the cluster's
+// The score of a key, but for the two that more than one pattern maps to.
+__device__ __forceinline__ bool key_score(uint32_t key, float &x) {
+    x = __uint_as_float((key & 0x80000000u) ? key & 0x7fffffffu : ~key);
+    return key != 0u && key != 0x80000000u;
+}
+
+struct alignas(16) SelectShared {
+    union {
+        uint32_t hist[256 * kSelColumns];
+        uint32_t all[256];                // the cluster's totals, once hist is summed
+        uint32_t picked[kSelWarps][128];  // at the end: positions a warp takes of 128
+    };
+    uint32_t totals[2][256];              // this CTA's, read by the cluster
     uint32_t warp_above[kSelWarps];
     uint32_t warp_equal[kSelWarps];
     uint32_t counts[2];            // this CTA's kept-for-sure and threshold keys
-    uint32_t found[2];             // the pass's bin, and what is left to take in it
+    uint32_t found[3];             // the pass's bin, what is left to take in it, its keys
 };
 
+// Four keys of a thread: positions 4 i .. 4 i + 3 of the CTA's part (what lies
+// past its end is not looked at).
 template <bool kCached>
-__global__ void __launch_bounds__(kSelThreads) lmc_select_kernel(const __grid_constant__ SelectPlan P) {
+__device__ __forceinline__ uint4 keys_at(const uint32_t *keys, const float *score, int32_t i, int32_t mine) {
+    if constexpr (kCached) {
+        return reinterpret_cast<const uint4 *>(keys)[i];
+    } else {
+        uint32_t k[4];
+#pragma unroll
+        for (int j = 0; j < 4; j++)
+            k[j] = 4 * i + j < mine ? order_key(__ldg(score + 4 * i + j)) : 0u;
+        return make_uint4(k[0], k[1], k[2], k[3]);
+    }
+}
+
+template <bool kCached>
+__global__ void __launch_bounds__(kSelThreads, kSelPerSm) lmc_select_kernel(const __grid_constant__ SelectPlan P) {
     extern __shared__ __align__(16) uint8_t select_mem[];
     SelectShared &S = *reinterpret_cast<SelectShared *>(select_mem);
     uint32_t *const keys = reinterpret_cast<uint32_t *>(select_mem + sizeof(SelectShared));
@@ -342,33 +375,60 @@ __global__ void __launch_bounds__(kSelThreads) lmc_select_kernel(const __grid_co
     if (take == 0)
         return;
 
-    // this CTA's candidates, and within them each warp's run
-    const int32_t part = (int32_t)(((int64_t)n + P.cluster - 1) / P.cluster);
+    // this CTA's candidates (a multiple of four but for the last), in fours
+    const int32_t part = (int32_t)((((int64_t)n + P.cluster - 1) / P.cluster + 3) / 4 * 4);
     const int32_t lo = (int32_t)min((int64_t)rank * part, (int64_t)n);
     const int32_t mine = (int32_t)min((int64_t)lo + part, (int64_t)n) - lo;
-    if (kCached) {
-        for (int32_t i = tid; i < mine; i += kSelThreads)
-            keys[i] = order_key(__ldcs(score + lo + i));
-    }
-    auto key_at = [&](int32_t i) { return kCached ? keys[i] : order_key(__ldg(score + lo + i)); };
+    const int32_t fours = (mine + 3) / 4;
+    const bool wide = (((uintptr_t)(score + lo)) & 15) == 0;
+    const int column = lane & (kSelColumns - 1);
 
     uint32_t prefix = 0, mask = 0, left = (uint32_t)take;
-    int buf = 0;
-    for (int shift = 24; shift >= 0; shift -= 8, buf ^= 1) {
-        for (int i = tid; i < 256 * 32; i += kSelThreads)
-            S.hist[i] = 0;
+    bool whole = false;
+    for (int pass = 0; pass < 4; pass++) {
+        const int shift = 24 - 8 * pass, buf = pass & 1;
+        for (int i = tid; i < 64 * kSelColumns; i += kSelThreads)
+            reinterpret_cast<uint4 *>(S.hist)[i] = make_uint4(0, 0, 0, 0);
         __syncthreads();
-        for (int32_t i = tid; i < mine; i += kSelThreads) {
-            const uint32_t k = key_at(i);
-            if ((k & mask) == prefix)
-                atomicAdd(&S.hist[((k >> shift) & 255u) * 32 + lane], 1u);
+        auto count = [&](uint32_t k, bool real) {
+            if (real && (k & mask) == prefix)
+                atomicAdd(&S.hist[((k >> shift) & 255u) * kSelColumns + column], 1u);
+        };
+#pragma unroll 4
+        for (int32_t i = tid; i < fours; i += kSelThreads) {
+            uint4 k;
+            if (kCached && pass == 0) {
+                float4 x = {};
+                if (wide && 4 * i + 4 <= mine) {
+                    x = __ldcs(reinterpret_cast<const float4 *>(score + lo) + i);
+                } else {
+                    x.x = score[lo + 4 * i];
+                    if (4 * i + 1 < mine)
+                        x.y = score[lo + 4 * i + 1];
+                    if (4 * i + 2 < mine)
+                        x.z = score[lo + 4 * i + 2];
+                    if (4 * i + 3 < mine)
+                        x.w = score[lo + 4 * i + 3];
+                }
+                k = make_uint4(order_key(x.x), order_key(x.y), order_key(x.z), order_key(x.w));
+                reinterpret_cast<uint4 *>(keys)[i] = k;
+            } else {
+                k = keys_at<kCached>(keys, score + lo, i, mine);
+            }
+            count(k.x, true);
+            count(k.y, 4 * i + 1 < mine);
+            count(k.z, 4 * i + 2 < mine);
+            count(k.w, 4 * i + 3 < mine);
         }
         __syncthreads();
         if (tid < 256) {
+            const uint4 *h = reinterpret_cast<const uint4 *>(S.hist + tid * kSelColumns);
             uint32_t sum = 0;
-#pragma unroll 8
-            for (int j = 0; j < 32; j++)
-                sum += S.hist[tid * 32 + ((j + tid) & 31)];
+#pragma unroll
+            for (int j = 0; j < kSelColumns / 4; j++) {
+                const uint4 x = h[(j + (tid >> 2)) & (kSelColumns / 4 - 1)];
+                sum += x.x + x.y + x.z + x.w;
+            }
             S.totals[buf][tid] = sum;
         }
         cluster.sync();  // also a barrier of this CTA
@@ -399,7 +459,7 @@ __global__ void __launch_bounds__(kSelThreads) lmc_select_kernel(const __grid_co
                     if (left <= before + c) {
                         S.found[0] = (uint32_t)(top - j);
                         S.found[1] = left - before;
-                        S.counts[0] = c;
+                        S.found[2] = c;
                         break;
                     }
                     before += c;
@@ -407,43 +467,58 @@ __global__ void __launch_bounds__(kSelThreads) lmc_select_kernel(const __grid_co
             }
         }
         __syncthreads();
-        const uint32_t bin = S.found[0], in_bin = S.counts[0];
+        const uint32_t bin = S.found[0], in_bin = S.found[2];
         left = S.found[1];
         prefix |= bin << shift;
         mask |= 255u << shift;
-        __syncthreads();
-        if (in_bin == left)
-            break;  // the whole bin is taken: the lower bits do not matter (uniform over the cluster)
+        whole = in_bin == left;
+        if (whole)
+            break;  // the lower bits do not matter (uniform over the cluster)
     }
 
-    // keys above the threshold's bits are taken, and the first `left` of
-    // those that match them
-    const int32_t run = (mine + kSelWarps - 1) / kSelWarps;
-    const int32_t w0 = min(warp * run, mine), w1 = min(w0 + run, mine);
+    // Keys above `high` are taken. Where the last bin was taken whole that is
+    // all; else (equal scores at the border) also the first `left` of the keys
+    // from `prefix` to `high`.
+    const uint32_t high = whole ? prefix - 1u : prefix | ~mask;
+    const int32_t run = (fours + kSelWarps - 1) / kSelWarps;
+    const int32_t w0 = min(warp * run, fours), w1 = min(w0 + run, fours);
     uint32_t above = 0, equal = 0;
+#pragma unroll 4
     for (int32_t i = w0 + lane; i < w1; i += 32) {
-        const uint32_t k = key_at(i) & mask;
-        above += k > prefix;
-        equal += k == prefix;
+        const uint4 k = keys_at<kCached>(keys, score + lo, i, mine);
+        const uint32_t v[4] = {k.x, k.y, k.z, k.w};
+#pragma unroll
+        for (int j = 0; j < 4; j++)
+            if (4 * i + j < mine) {
+                above += v[j] > high;
+                equal += v[j] >= prefix;
+            }
     }
     above = __reduce_add_sync(0xffffffffu, above);
-    equal = __reduce_add_sync(0xffffffffu, equal);
+    equal = __reduce_add_sync(0xffffffffu, equal) - above;
     if (lane == 0) {
         S.warp_above[warp] = above;
         S.warp_equal[warp] = equal;
     }
     __syncthreads();
-    if (tid == 0) {
-        uint32_t a = 0, e = 0;
-        for (int w = 0; w < kSelWarps; w++) {
-            const uint32_t x = S.warp_above[w], y = S.warp_equal[w];
-            S.warp_above[w] = a;
-            S.warp_equal[w] = e;
-            a += x;
-            e += y;
+    if (warp == 0) {
+        const uint32_t x = lane < kSelWarps ? S.warp_above[lane] : 0u, y = lane < kSelWarps ? S.warp_equal[lane] : 0u;
+        uint32_t a = x, e = y;
+        for (int o = 1; o < kSelWarps; o <<= 1) {
+            const uint32_t u = __shfl_up_sync(0xffffffffu, a, o), w = __shfl_up_sync(0xffffffffu, e, o);
+            if (lane >= o) {
+                a += u;
+                e += w;
+            }
         }
-        S.counts[0] = a;
-        S.counts[1] = e;
+        if (lane < kSelWarps) {
+            S.warp_above[lane] = a - x;
+            S.warp_equal[lane] = e - y;
+        }
+        if (lane == kSelWarps - 1) {
+            S.counts[0] = a;
+            S.counts[1] = e;
+        }
     }
     cluster.sync();
     uint32_t a_before = S.warp_above[warp], e_before = S.warp_equal[warp];
@@ -455,20 +530,60 @@ __global__ void __launch_bounds__(kSelThreads) lmc_select_kernel(const __grid_co
     const uint32_t lanes_below = (1u << lane) - 1u;
     for (int32_t i0 = w0; i0 < w1; i0 += 32) {
         const int32_t i = i0 + lane;
-        uint32_t k = 0;
+        uint4 k = {};
         if (i < w1)
-            k = key_at(i) & mask;
-        const bool a = i < w1 && k > prefix, e = i < w1 && k == prefix;
-        const uint32_t va = __ballot_sync(0xffffffffu, a), ve = __ballot_sync(0xffffffffu, e);
-        const uint32_t e_at = e_before + __popc(ve & lanes_below);
-        if (a || (e && e_at < left)) {
-            const uint32_t at = a_before + __popc(va & lanes_below) + min(e_at, left);
-            kept[at] = lo + i;
-            if (kept_scores != nullptr)
-                kept_scores[at] = score[lo + i];
+            k = keys_at<kCached>(keys, score + lo, i, mine);
+        const uint32_t v[4] = {k.x, k.y, k.z, k.w};
+        const int32_t real = i < w1 ? mine - 4 * i : 0;
+        // the warp's picks, close together, then written as one run
+        const uint32_t first = a_before + min(e_before, left);
+        uint32_t *const picked = S.picked[warp];
+        if (whole) {
+            uint32_t at = 0, picks = 0;
+#pragma unroll
+            for (int j = 0; j < 4; j++) {
+                const uint32_t va = __ballot_sync(0xffffffffu, j < real && v[j] > high);
+                at += __popc(va & lanes_below);
+                picks += __popc(va);
+            }
+            a_before += picks;
+#pragma unroll
+            for (int j = 0; j < 4; j++)
+                if (j < real && v[j] > high)
+                    picked[at++] = (uint32_t)(4 * i + j);
+        } else {
+            uint32_t a_at = a_before, e_at = e_before;
+#pragma unroll
+            for (int j = 0; j < 4; j++) {
+                const bool a = j < real && v[j] > high, e = j < real && v[j] >= prefix && !a;
+                const uint32_t va = __ballot_sync(0xffffffffu, a), ve = __ballot_sync(0xffffffffu, e);
+                a_at += __popc(va & lanes_below);
+                e_at += __popc(ve & lanes_below);
+                a_before += __popc(va);
+                e_before += __popc(ve);
+            }
+#pragma unroll
+            for (int j = 0; j < 4; j++) {
+                const bool a = j < real && v[j] > high, e = j < real && v[j] >= prefix && !a;
+                if (a || (e && e_at < left))
+                    picked[a_at + min(e_at, left) - first] = (uint32_t)(4 * i + j);
+                a_at += a;
+                e_at += e;
+            }
         }
-        a_before += __popc(va);
-        e_before += __popc(ve);
+        __syncwarp();
+        const int32_t picks = (int32_t)(a_before + min(e_before, left) - first);
+        for (int32_t q = lane; q < picks; q += 32) {
+            const uint32_t at = picked[q];
+            kept[first + q] = lo + (int32_t)at;
+            if (kept_scores != nullptr) {
+                float x = 0.0f;
+                if (!kCached || !key_score(keys[at], x))
+                    x = score[lo + at];
+                kept_scores[first + q] = x;
+            }
+        }
+        __syncwarp();
     }
     cluster.sync();  // no CTA leaves while another may read its counts
 }
@@ -674,9 +789,8 @@ extern "C" int lmc_select_tokens(const float *scores, int64_t set_stride, int64_
         c *= 2;
     P.cluster = c;
     const int64_t most = 227 * 1024 - (int64_t)sizeof(SelectShared);
-    const int64_t want = (max_length + c - 1) / c * 4;
+    const int64_t want = ((max_length + c - 1) / c + 7) / 4 * 16;  // a part is rounded up to fours
     const bool cached = want <= most;
-    P.cap = cached ? (int32_t)(want / 4) : 0;
     const size_t smem = sizeof(SelectShared) + (cached ? (size_t)(want + 15) / 16 * 16 : 0);
     if (rows * c > INT32_MAX)
         return LMC_ERR_INVALID_ARG;
