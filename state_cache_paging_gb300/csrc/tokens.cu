@@ -318,8 +318,10 @@ struct alignas(16) SelectShared {
     uint32_t found[3];             // the pass's bin, what is left to take in it, its keys
 };
 
-// Four keys of a thread: positions 4 i .. 4 i + 3 of the CTA's part (what lies
-// past its end is not looked at).
+// Four keys of a thread: positions 4 i .. 4 i + 3 of the CTA's part. Past its
+// end a key reads 0, the lowest there is: such keys take part in the search
+// (only the row's last part has any, so they come after every real one; take
+// is less than the real ones' number, so none is ever reached).
 template <bool kCached>
 __device__ __forceinline__ uint4 keys_at(const uint32_t *keys, const float *score, int32_t i, int32_t mine) {
     if constexpr (kCached) {
@@ -390,35 +392,38 @@ __global__ void __launch_bounds__(kSelThreads, kSelPerSm) lmc_select_kernel(cons
         for (int i = tid; i < 64 * kSelColumns; i += kSelThreads)
             reinterpret_cast<uint4 *>(S.hist)[i] = make_uint4(0, 0, 0, 0);
         __syncthreads();
-        auto count = [&](uint32_t k, bool real) {
-            if (real && (k & mask) == prefix)
-                atomicAdd(&S.hist[((k >> shift) & 255u) * kSelColumns + column], 1u);
+        uint32_t *const bins = S.hist + column;
+        auto count = [&](uint32_t k) {
+            if ((k & mask) == prefix)
+                atomicAdd(bins + ((k >> shift) & 255u) * kSelColumns, 1u);
         };
+        if (kCached && pass == 0) {
+            const float4 *const four = reinterpret_cast<const float4 *>(score + lo);
+            const int32_t full = wide ? mine / 4 : 0;
 #pragma unroll 4
-        for (int32_t i = tid; i < fours; i += kSelThreads) {
-            uint4 k;
-            if (kCached && pass == 0) {
-                float4 x = {};
-                if (wide && 4 * i + 4 <= mine) {
-                    x = __ldcs(reinterpret_cast<const float4 *>(score + lo) + i);
-                } else {
-                    x.x = score[lo + 4 * i];
-                    if (4 * i + 1 < mine)
-                        x.y = score[lo + 4 * i + 1];
-                    if (4 * i + 2 < mine)
-                        x.z = score[lo + 4 * i + 2];
-                    if (4 * i + 3 < mine)
-                        x.w = score[lo + 4 * i + 3];
-                }
-                k = make_uint4(order_key(x.x), order_key(x.y), order_key(x.z), order_key(x.w));
+            for (int32_t i = tid; i < full; i += kSelThreads) {
+                const float4 x = __ldcs(four + i);
+                const uint4 k = make_uint4(order_key(x.x), order_key(x.y), order_key(x.z), order_key(x.w));
                 reinterpret_cast<uint4 *>(keys)[i] = k;
-            } else {
-                k = keys_at<kCached>(keys, score + lo, i, mine);
+                atomicAdd(bins + (k.x >> 24) * kSelColumns, 1u);
+                atomicAdd(bins + (k.y >> 24) * kSelColumns, 1u);
+                atomicAdd(bins + (k.z >> 24) * kSelColumns, 1u);
+                atomicAdd(bins + (k.w >> 24) * kSelColumns, 1u);
             }
-            count(k.x, true);
-            count(k.y, 4 * i + 1 < mine);
-            count(k.z, 4 * i + 2 < mine);
-            count(k.w, 4 * i + 3 < mine);
+            for (int32_t i = 4 * full + tid; i < 4 * fours; i += kSelThreads) {
+                const uint32_t k = i < mine ? order_key(score[lo + i]) : 0u;
+                keys[i] = k;
+                atomicAdd(bins + (k >> 24) * kSelColumns, 1u);
+            }
+        } else {
+#pragma unroll 4
+            for (int32_t i = tid; i < fours; i += kSelThreads) {
+                const uint4 k = keys_at<kCached>(keys, score + lo, i, mine);
+                count(k.x);
+                count(k.y);
+                count(k.z);
+                count(k.w);
+            }
         }
         __syncthreads();
         if (tid < 256) {
@@ -488,14 +493,14 @@ __global__ void __launch_bounds__(kSelThreads, kSelPerSm) lmc_select_kernel(cons
         const uint4 k = keys_at<kCached>(keys, score + lo, i, mine);
         const uint32_t v[4] = {k.x, k.y, k.z, k.w};
 #pragma unroll
-        for (int j = 0; j < 4; j++)
-            if (4 * i + j < mine) {
-                above += v[j] > high;
+        for (int j = 0; j < 4; j++) {
+            above += v[j] > high;
+            if (!whole)
                 equal += v[j] >= prefix;
-            }
+        }
     }
     above = __reduce_add_sync(0xffffffffu, above);
-    equal = __reduce_add_sync(0xffffffffu, equal) - above;
+    equal = whole ? 0u : __reduce_add_sync(0xffffffffu, equal) - above;
     if (lane == 0) {
         S.warp_above[warp] = above;
         S.warp_equal[warp] = equal;
@@ -534,7 +539,7 @@ __global__ void __launch_bounds__(kSelThreads, kSelPerSm) lmc_select_kernel(cons
         if (i < w1)
             k = keys_at<kCached>(keys, score + lo, i, mine);
         const uint32_t v[4] = {k.x, k.y, k.z, k.w};
-        const int32_t real = i < w1 ? mine - 4 * i : 0;
+        const bool real = i < w1;
         // the warp's picks, close together, then written as one run
         const uint32_t first = a_before + min(e_before, left);
         uint32_t *const picked = S.picked[warp];
@@ -542,20 +547,20 @@ __global__ void __launch_bounds__(kSelThreads, kSelPerSm) lmc_select_kernel(cons
             uint32_t at = 0, picks = 0;
 #pragma unroll
             for (int j = 0; j < 4; j++) {
-                const uint32_t va = __ballot_sync(0xffffffffu, j < real && v[j] > high);
+                const uint32_t va = __ballot_sync(0xffffffffu, v[j] > high);
                 at += __popc(va & lanes_below);
                 picks += __popc(va);
             }
             a_before += picks;
 #pragma unroll
             for (int j = 0; j < 4; j++)
-                if (j < real && v[j] > high)
+                if (v[j] > high)
                     picked[at++] = (uint32_t)(4 * i + j);
         } else {
             uint32_t a_at = a_before, e_at = e_before;
 #pragma unroll
             for (int j = 0; j < 4; j++) {
-                const bool a = j < real && v[j] > high, e = j < real && v[j] >= prefix && !a;
+                const bool a = v[j] > high, e = real && v[j] >= prefix && !a;
                 const uint32_t va = __ballot_sync(0xffffffffu, a), ve = __ballot_sync(0xffffffffu, e);
                 a_at += __popc(va & lanes_below);
                 e_at += __popc(ve & lanes_below);
@@ -564,7 +569,7 @@ __global__ void __launch_bounds__(kSelThreads, kSelPerSm) lmc_select_kernel(cons
             }
 #pragma unroll
             for (int j = 0; j < 4; j++) {
-                const bool a = j < real && v[j] > high, e = j < real && v[j] >= prefix && !a;
+                const bool a = v[j] > high, e = real && v[j] >= prefix && !a;
                 if (a || (e && e_at < left))
                     picked[a_at + min(e_at, left) - first] = (uint32_t)(4 * i + j);
                 a_at += a;
