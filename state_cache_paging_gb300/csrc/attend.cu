@@ -85,6 +85,7 @@ constexpr int kSmemLimit = 227 * 1024;
 // Shared memory that is not a tile: barriers and per-head numbers.
 struct Control {
     uint64_t q_full, q_free;
+    uint64_t q_raw;              // fp8: queries as they came
     uint64_t kv_full[kMaxStages], kv_free[kMaxStages];
     uint64_t s_full[2], s_free[2];
     uint64_t p_full, pv_done, o_free;
@@ -598,60 +599,46 @@ __device__ __forceinline__ void load_by_tma(const AttendPlan &P, Control &C, con
     }
 }
 
-// kRows rows of q (h, h + step, ...) to f16, each times a power of two that
-// brings its largest value to [2^14, 2^15): exact for values within 2^27 of
-// it. One warp; all rows' loads are issued before the first is used. Not
-// inlined: its registers would push the entries' loop into spilling.
-template <int kRows>
-__device__ __noinline__ void load_query_rows(const AttendPlan &P, Control &C, const Memory &M, int r, int group, int h0,
-                                                int step) {
-    constexpr int kPieces = (kMaxEntry / 8 + 31) / 32;
-    const int lane = threadIdx.x & 31;
-    uint4 v[kRows][kPieces];
-#pragma unroll
-    for (int m = 0; m < kRows; m++) {
-        const int h = h0 + m * step, head = group * P.group_heads + h;
-        const bool real = h < P.group_heads && head < P.H;
-        const uint4 *src = reinterpret_cast<const uint4 *>(P.q + r * P.q_request_stride + head * P.q_head_stride);
-#pragma unroll
-        for (int i = 0; i < kPieces; i++) {
-            v[m][i] = make_uint4(0, 0, 0, 0);
-            if (real && lane + 32 * i < P.E / 8)
-                v[m][i] = __ldg(src + lane + 32 * i);
-        }
-    }
-#pragma unroll
-    for (int m = 0; m < kRows; m++) {
-        const int h = h0 + m * step;
+// Queries to f16 where they lie in shared memory, each head's times a power of
+// two that brings its largest value to [2^14, 2^15): exact for values within
+// 2^27 of it. Eight warps, four rows at a time each, eight lanes to a row.
+// (Read from global memory instead, at this point all CTAs ask for the same
+// few lines: 24,000 cycles a segment.)
+__device__ __forceinline__ void query_to_f16(const AttendPlan &P, Control &C, const Memory &M, int warp) {
+    const int lane = threadIdx.x & 31, piece = lane & 7, pieces = P.E / 8;
+#pragma unroll 1
+    for (int h = warp * 4 + lane / 8; h < P.padded_heads; h += 4 * kFp8Loaders) {
+        // padded_heads is a multiple of 16, so a warp's lanes are here together
+        uint8_t *const row = M.q + h * 128;
+        const int panel = P.padded_heads * 128, x = h & 7;
         float top = 0.0f;
-#pragma unroll
-        for (int i = 0; i < kPieces; i++) {
-            const uint32_t w[4] = {v[m][i].x, v[m][i].y, v[m][i].z, v[m][i].w};
+#pragma unroll 3
+        for (int c = piece; c < pieces; c += 8) {
+            const uint4 v = *reinterpret_cast<const uint4 *>(row + (c >> 3) * panel + ((piece ^ x) << 4));
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
 #pragma unroll
             for (int k = 0; k < 4; k++)
                 top = fmaxf(top, fmaxf(fabsf(from_q(w[k] & 0xffff, P.q_bf16)), fabsf(from_q(w[k] >> 16, P.q_bf16))));
         }
-        for (int o = 16; o > 0; o >>= 1)
+        for (int o = 4; o > 0; o >>= 1)
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
         // 2^e with e = 14 - floor(log2(top)), kept within what one float
         // holds; 1 where there is nothing to scale (zero, infinity)
         const int exponent = (int)(__float_as_uint(top) >> 23) - 127;
         const int e = top == 0.0f || exponent == 128 ? 0 : max(-100, min(100, 14 - exponent));
         const float up = __uint_as_float((uint32_t)(127 + e) << 23);
-        if (lane == 0 && h < P.padded_heads)
+        if (piece == 0)
             C.q_scale[h] = __uint_as_float((uint32_t)(127 - e) << 23);
+#pragma unroll 3
+        for (int c = piece; c < pieces; c += 8) {
+            uint4 *const at = reinterpret_cast<uint4 *>(row + (c >> 3) * panel + ((piece ^ x) << 4));
+            const uint4 v = *at;
+            const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+            uint32_t o[4];
 #pragma unroll
-        for (int i = 0; i < kPieces; i++) {
-            const int c = lane + 32 * i;
-            if (h < P.padded_heads && c < P.E / 8) {
-                const uint32_t w[4] = {v[m][i].x, v[m][i].y, v[m][i].z, v[m][i].w};
-                uint32_t o[4];
-#pragma unroll
-                for (int k = 0; k < 4; k++)
-                    o[k] = pack<false>(from_q(w[k] & 0xffff, P.q_bf16) * up, from_q(w[k] >> 16, P.q_bf16) * up);
-                *reinterpret_cast<uint4 *>(M.q + (c >> 3) * P.padded_heads * 128 + h * 128 + (((c & 7) ^ (h & 7)) << 4)) =
-                    make_uint4(o[0], o[1], o[2], o[3]);
-            }
+            for (int k = 0; k < 4; k++)
+                o[k] = pack<false>(from_q(w[k] & 0xffff, P.q_bf16) * up, from_q(w[k] >> 16, P.q_bf16) * up);
+            *at = make_uint4(o[0], o[1], o[2], o[3]);
         }
     }
 }
@@ -668,12 +655,29 @@ __device__ __forceinline__ void load_fp8(const AttendPlan &P, Control &C, const 
     const int chunks = P.E / 16;  // of an entry
     const uint32_t at0 = row * 128 + (((2 * piece) ^ (row & 7)) << 4), at1 = row * 128 + (((2 * piece + 1) ^ (row & 7)) << 4);
     uint32_t bad = 0, n = 0, segments = 0;
+    if (warp == 0 && elect())
+        asm volatile("prefetch.tensormap [%0];" ::"l"(&P.query) : "memory");
     uint4 v[2][kPanels];
     uint64_t valid[2];
     LastPage last, last_ahead;
     const int my_page = P.pages_per_tile == 1 ? 0 : row / P.block_size;
     const int my_row = row - my_page * P.block_size;
 
+    // a tile of one page is a run of bytes: sent on its way to L2
+    auto prefetch = [&](int j) {
+        if (warp == 0 && P.pages_per_tile == 1 && j < W.count) {
+            const Tile A = tile_at(P, W.first + j);
+            uint64_t unused;
+            uint32_t later = 0;  // raised when the tile itself is loaded
+            const int64_t ahead = resolve(P, W, A, unused, later, last_ahead);
+            if (ahead >= 0 && elect())
+                asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(
+                                 P.pool + ahead * P.block_stride + (int64_t)A.row0 * P.token_bytes),
+                             "r"(A.rows * P.token_bytes)
+                             : "memory");
+            __syncwarp();
+        }
+    };
     auto load = [&](uint4(&x)[kPanels], uint64_t &rows, int j) {
         const Tile T = tile_at(P, W.first + j);
         const int block = resolve(P, W, T, rows, bad, last);
@@ -687,19 +691,6 @@ __device__ __forceinline__ void load_fp8(const AttendPlan &P, Control &C, const 
                 asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
                              : "=r"(x[i].x), "=r"(x[i].y), "=r"(x[i].z), "=r"(x[i].w)
                              : "l"(src + i * 64));
-        }
-        // a later tile of one page is a run of bytes: on its way to L2
-        if (warp == 0 && P.pages_per_tile == 1 && j + kFp8Ahead < W.count) {
-            const Tile A = tile_at(P, W.first + j + kFp8Ahead);
-            uint64_t unused;
-            uint32_t later = 0;  // raised when the tile itself is loaded
-            const int64_t ahead = resolve(P, W, A, unused, later, last_ahead);
-            if (ahead >= 0 && elect())
-                asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(
-                                 P.pool + ahead * P.block_stride + (int64_t)A.row0 * P.token_bytes),
-                             "r"(A.rows * P.token_bytes)
-                             : "memory");
-            __syncwarp();
         }
     };
     auto store = [&](const uint4(&x)[kPanels], uint64_t rows) {
@@ -732,29 +723,44 @@ __device__ __forceinline__ void load_fp8(const AttendPlan &P, Control &C, const 
     while (W.next(P)) {
         if (segments > 0)
             bar_wait(C, &C.q_free, (segments - 1) & 1, P.status);
+#pragma unroll 1
+        for (int j = 0; j < kFp8Ahead; j++)
+            prefetch(j);
+        const int r = (int)uniform(W.r);
+        if (warp == 0 && elect()) {
+            bar_expect(&C.q_raw, (uint32_t)((P.E + 63) / 64 * P.padded_heads * 128));
+            for (int i = 0; i < P.query_copies; i++)
+                tma_box(&P.query, M.q + i * P.padded_heads * 128, i * 64, group * P.group_heads, r, &C.q_raw);
+        }
+        __syncwarp();
+        bar_wait(C, &C.q_raw, segments & 1, P.status);
         segments++;
-        for (int h = warp; h < P.padded_heads; h += 4 * kFp8Loaders)
-            load_query_rows<4>(P, C, M, W.r, group, h, kFp8Loaders);
+        query_to_f16(P, C, M, warp);
         fence_async();
         __syncwarp();
         if (lane == 0)
             bar_arrive(&C.q_full);
-        load(v[0], valid[0], 0);
-        if (W.count > 1)
-            load(v[1], valid[1], 1);
-        for (int j = 0; j < W.count; j += 2) {
-            store(v[0], valid[0]);
+        // each half once in the code: a tile is loaded two turns ahead
+#pragma unroll 1
+        for (int j = -2; j < W.count; j += 2) {
+            if (j >= 0)
+                store(v[0], valid[0]);
             if (j + 2 < W.count)
                 load(v[0], valid[0], j + 2);
-            if (j + 1 < W.count) {
+            prefetch(j + 2 + kFp8Ahead);
+            if (j >= 0 && j + 1 < W.count)
                 store(v[1], valid[1]);
-                if (j + 3 < W.count)
-                    load(v[1], valid[1], j + 3);
-            }
+            if (j + 3 < W.count)
+                load(v[1], valid[1], j + 3);
+            prefetch(j + 3 + kFp8Ahead);
         }
     }
     if (bad)
         atomicOr(P.status, bad);
+    // a CTA that gave up leaves no copy of its own in flight
+    if (warp == 0 && *(volatile uint32_t *)&C.gave_up)
+        for (uint32_t i = 0; segments > 0 && i < kWaitLimit && !bar_try(&C.q_raw, (segments - 1) & 1); i++) {
+        }
 }
 
 // One warp: S = Q K^T of each tile, as soon as it is there. (The two products
@@ -1088,6 +1094,7 @@ __global__ void __launch_bounds__((kFirstLoader + (kFp8 ? kFp8Loaders : 1)) * 32
     M.p = M.kv + (size_t)P.stages * M.stage_bytes;
     if (threadIdx.x == 0) {
         bar_init(&C.q_full, kFp8 ? kFp8Loaders : 1);
+        bar_init(&C.q_raw, 1);
         bar_init(&C.q_free, kFp8 ? 1 + kSoftWarps : 1);  // the products', and the readers of q_scale
         for (int i = 0; i < P.stages; i++) {
             bar_init(&C.kv_full[i], kFp8 ? kFp8Loaders : 1);
@@ -1470,21 +1477,19 @@ extern "C" int lmc_attend(const lmc_layout *L, const lmc_entries *e, const void 
     const size_t smem = std::max<size_t>((size_t)((P.E + 63) / 64) * P.padded_heads * 128 + (size_t)P.padded_heads * 128 +
                                              (size_t)P.stages * P.panels * kPanel,
                                          120 * 1024);  // one CTA per SM: each takes the whole tensor memory
-    if (!fp8) {
-        if (d.stride >= (int64_t)1 << 40 || L->num_blocks > INT32_MAX || a->q_request_stride >= (int64_t)1 << 38 ||
-            a->q_head_stride >= (int64_t)1 << 38)
-            return LMC_ERR_INVALID_ARG;
-        const int64_t head_bytes = H > 1 ? a->q_head_stride * 2 : (int64_t)P.E * 2;
-        const int64_t request_bytes = R > 1 ? a->q_request_stride * 2 : head_bytes * H;
-        const int row_panels = (P.E + 63) / 64;
-        const bool whole = P.E % 64 == 0, tile = P.pages_per_tile == 1;
-        P.cache_copies = whole && tile ? 1 : row_panels;
-        P.query_copies = whole ? 1 : row_panels;
-        if (!tensor_map(&P.cache, bf16, P.pool, P.E, N, L->num_blocks, P.token_bytes, d.stride,
-                        tile ? kTile : (int)N, whole && tile) ||
-            !tensor_map(&P.query, bf16, a->q, P.E, H, R, head_bytes, request_bytes, P.padded_heads, whole))
-            return LMC_ERR_CUDA;
-    }
+    if (d.stride >= (int64_t)1 << 40 || L->num_blocks > INT32_MAX || a->q_request_stride >= (int64_t)1 << 38 ||
+        a->q_head_stride >= (int64_t)1 << 38)
+        return LMC_ERR_INVALID_ARG;
+    const int row_panels = (P.E + 63) / 64;
+    const bool whole = P.E % 64 == 0, tile = P.pages_per_tile == 1;
+    const int64_t head_bytes = H > 1 ? a->q_head_stride * 2 : (int64_t)P.E * 2;
+    const int64_t request_bytes = R > 1 ? a->q_request_stride * 2 : head_bytes * H;
+    P.cache_copies = whole && tile ? 1 : row_panels;
+    P.query_copies = whole ? 1 : row_panels;
+    if (!tensor_map(&P.query, bf16, a->q, P.E, H, R, head_bytes, request_bytes, P.padded_heads, whole) ||
+        (!fp8 && !tensor_map(&P.cache, bf16, P.pool, P.E, N, L->num_blocks, P.token_bytes, d.stride,
+                             tile ? kTile : (int)N, whole && tile)))
+        return LMC_ERR_CUDA;
     auto kern = fp8 ? lmc_attend_kernel<false, true> : bf16 ? lmc_attend_kernel<true, false> : lmc_attend_kernel<false, false>;
     if (!allow_shared_memory(fp8 ? 2 : bf16 ? 1 : 0, kern))
         return LMC_ERR_CUDA;
