@@ -68,7 +68,8 @@ constexpr int kMaxCols = 160;         // CTAs along the cache's length (an SM ea
 constexpr int kSoftWarps = 4;
 constexpr int kScoreWarp = 4;          // issues S = Q K^T
 constexpr int kValueWarp = 5;          // issues O^T += V^T P^T
-constexpr int kFirstLoader = 6;
+constexpr int kFirstLoader = 6;        // 16-bit entries: one warp
+constexpr int kFirstFp8Loader = 8;     // fp8: eight, two whole warpgroups
 constexpr int kFp8Loaders = 8;        // warps, eight of a tile's rows each
 #ifndef LMC_AHEAD
 #define LMC_AHEAD 2
@@ -78,6 +79,8 @@ constexpr int kAhead = LMC_AHEAD;     // tiles
 #define LMC_FP8_AHEAD 2
 #endif
 constexpr int kFp8Ahead = LMC_FP8_AHEAD;
+template <bool kFp8>
+constexpr int kThreads = (kFp8 ? kFirstFp8Loader + kFp8Loaders : kFirstLoader + 1) * 32;
 constexpr float kLag = 8.0f;          // how far (log2) a logit may exceed the reference
 constexpr uint32_t kWaitLimit = 1u << 22;
 constexpr int kSmemLimit = 227 * 1024;
@@ -647,18 +650,21 @@ __device__ __forceinline__ void query_to_f16(const AttendPlan &P, Control &C, co
 // holds eight of a tile's rows, four lanes to a row: a lane takes 16 codes of
 // each panel, so a panel's codes are read as 64-byte pieces and its two
 // 16-byte halves are stored without bank conflicts, at offsets that do not
-// change from tile to tile. Two tiles are in flight in registers.
+// change from tile to tile. A tile is widened in registers before its stage is
+// free (only the stores wait for that) while the next one's codes are in
+// flight from L2.
 __device__ __forceinline__ void load_fp8(const AttendPlan &P, Control &C, const Memory &M, Walk &W, int group) {
     constexpr int kPanels = kMaxEntry / 64;
-    const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) - kFirstLoader;
+    const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) - kFirstFp8Loader;
     const int row = warp * 8 + lane / 4, piece = lane & 3;
     const int chunks = P.E / 16;  // of an entry
     const uint32_t at0 = row * 128 + (((2 * piece) ^ (row & 7)) << 4), at1 = row * 128 + (((2 * piece + 1) ^ (row & 7)) << 4);
     uint32_t bad = 0, n = 0, segments = 0;
     if (warp == 0 && elect())
         asm volatile("prefetch.tensormap [%0];" ::"l"(&P.query) : "memory");
-    uint4 v[2][kPanels];
-    uint64_t valid[2];
+    uint4 codes[kPanels];
+    uint32_t wide[kPanels][8];
+    uint64_t next_valid = 0;
     LastPage last, last_ahead;
     const int my_page = P.pages_per_tile == 1 ? 0 : row / P.block_size;
     const int my_row = row - my_page * P.block_size;
@@ -678,46 +684,20 @@ __device__ __forceinline__ void load_fp8(const AttendPlan &P, Control &C, const 
             __syncwarp();
         }
     };
-    auto load = [&](uint4(&x)[kPanels], uint64_t &rows, int j) {
+    auto load = [&](int j) {
         const Tile T = tile_at(P, W.first + j);
-        const int block = resolve(P, W, T, rows, bad, last);
+        const int block = resolve(P, W, T, next_valid, bad, last);
         const int64_t b = __shfl_sync(0xffffffffu, block, my_page & 31);
-        const bool mine = rows >> row & 1;
+        const bool mine = next_valid >> row & 1;
         const uint8_t *src = P.pool + b * P.block_stride + (int64_t)(T.row0 + my_row) * P.token_bytes + piece * 16;
 #pragma unroll
         for (int i = 0; i < kPanels; i++) {
-            x[i] = make_uint4(0, 0, 0, 0);
+            codes[i] = make_uint4(0, 0, 0, 0);
             if (mine && i * 4 + piece < chunks)
                 asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-                             : "=r"(x[i].x), "=r"(x[i].y), "=r"(x[i].z), "=r"(x[i].w)
+                             : "=r"(codes[i].x), "=r"(codes[i].y), "=r"(codes[i].z), "=r"(codes[i].w)
                              : "l"(src + i * 64));
         }
-    };
-    auto store = [&](const uint4(&x)[kPanels], uint64_t rows) {
-        const int st = n % P.stages;
-        if (n >= (uint32_t)P.stages)
-            bar_wait(C, &C.kv_free[st], (n / P.stages - 1) & 1, P.status);
-        uint8_t *to = M.kv + (size_t)st * M.stage_bytes;
-#pragma unroll
-        for (int i = 0; i < kPanels; i++)
-            if (i * 4 + piece < chunks) {
-                const uint32_t w[4] = {x[i].x, x[i].y, x[i].z, x[i].w};
-                uint32_t o[8];
-#pragma unroll
-                for (int k = 0; k < 8; k++)
-                    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(o[k]) : "h"((unsigned short)(w[k >> 1] >> (16 * (k & 1)))));
-                *reinterpret_cast<uint4 *>(to + i * kPanel + at0) = make_uint4(o[0], o[1], o[2], o[3]);
-                *reinterpret_cast<uint4 *>(to + i * kPanel + at1) = make_uint4(o[4], o[5], o[6], o[7]);
-            }
-        if (warp == 0 && lane == 0) {
-            C.valid[n % (2 * kMaxStages)] = rows;
-            C.zero[n % (2 * kMaxStages)] = 0;  // the rows left out hold zeros
-        }
-        fence_async();
-        __syncwarp();
-        if (lane == 0)
-            bar_arrive(&C.kv_full[st]);
-        n++;
     };
 
     while (W.next(P)) {
@@ -740,19 +720,42 @@ __device__ __forceinline__ void load_fp8(const AttendPlan &P, Control &C, const 
         __syncwarp();
         if (lane == 0)
             bar_arrive(&C.q_full);
-        // each half once in the code: a tile is loaded two turns ahead
+        load(0);
 #pragma unroll 1
-        for (int j = -2; j < W.count; j += 2) {
-            if (j >= 0)
-                store(v[0], valid[0]);
-            if (j + 2 < W.count)
-                load(v[0], valid[0], j + 2);
-            prefetch(j + 2 + kFp8Ahead);
-            if (j >= 0 && j + 1 < W.count)
-                store(v[1], valid[1]);
-            if (j + 3 < W.count)
-                load(v[1], valid[1], j + 3);
-            prefetch(j + 3 + kFp8Ahead);
+        for (int j = 0; j < W.count; j++, n++) {
+#pragma unroll
+            for (int i = 0; i < kPanels; i++) {
+                const uint32_t w[4] = {codes[i].x, codes[i].y, codes[i].z, codes[i].w};
+#pragma unroll
+                for (int k = 0; k < 8; k++)
+                    asm volatile("cvt.rn.f16x2.e4m3x2 %0, %1;"
+                                 : "=r"(wide[i][k])
+                                 : "h"((unsigned short)(w[k >> 1] >> (16 * (k & 1)))));
+            }
+            const uint64_t valid = next_valid;
+            if (j + 1 < W.count)
+                load(j + 1);
+            prefetch(j + kFp8Ahead);
+            const int st = n % P.stages;
+            if (n >= (uint32_t)P.stages)
+                bar_wait(C, &C.kv_free[st], (n / P.stages - 1) & 1, P.status);
+            uint8_t *to = M.kv + (size_t)st * M.stage_bytes;
+#pragma unroll
+            for (int i = 0; i < kPanels; i++)
+                if (i * 4 + piece < chunks) {
+                    *reinterpret_cast<uint4 *>(to + i * kPanel + at0) =
+                        make_uint4(wide[i][0], wide[i][1], wide[i][2], wide[i][3]);
+                    *reinterpret_cast<uint4 *>(to + i * kPanel + at1) =
+                        make_uint4(wide[i][4], wide[i][5], wide[i][6], wide[i][7]);
+                }
+            if (warp == 0 && lane == 0) {
+                C.valid[n % (2 * kMaxStages)] = valid;
+                C.zero[n % (2 * kMaxStages)] = 0;  // the rows left out hold zeros
+            }
+            fence_async();
+            __syncwarp();
+            if (lane == 0)
+                bar_arrive(&C.kv_full[st]);
         }
     }
     if (bad)
@@ -1082,7 +1085,7 @@ __device__ __forceinline__ void soften(const AttendPlan &P, Control &C, const Me
 }
 
 template <bool kBf16, bool kFp8>
-__global__ void __launch_bounds__((kFirstLoader + (kFp8 ? kFp8Loaders : 1)) * 32, 1) lmc_attend_kernel(const __grid_constant__ AttendPlan P) {
+__global__ void __launch_bounds__(kThreads<kFp8>, 1) lmc_attend_kernel(const __grid_constant__ AttendPlan P) {
     extern __shared__ __align__(1024) uint8_t attend_mem[];
     __shared__ Control C;
     const int warp = threadIdx.x >> 5;
@@ -1123,16 +1126,23 @@ __global__ void __launch_bounds__((kFirstLoader + (kFp8 ? kFp8Loaders : 1)) * 32
 
     Walk W;
     W.init(P, col);
-    if (warp < kSoftWarps)
+    if (warp < kSoftWarps) {
         soften<kBf16, kFp8>(P, C, M, W, col, group);
-    else if (warp == kScoreWarp)
-        multiply_scores<kBf16>(P, C, M, W);
-    else if (warp == kValueWarp)
-        multiply_values<kBf16>(P, C, M, W);
-    else if (kFp8)
+    } else if (kFp8 && warp >= kFirstFp8Loader) {
+        // registers for a tile as f16 and the next one's codes, from the
+        // warpgroup that issues the products: 128 + 40 + 2 x 168 of 4 x 128
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
         load_fp8(P, C, M, W, group);
-    else
-        load_by_tma(P, C, M, W, group);
+    } else {
+        if (kFp8)
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+        if (warp == kScoreWarp)
+            multiply_scores<kBf16>(P, C, M, W);
+        else if (warp == kValueWarp)
+            multiply_values<kBf16>(P, C, M, W);
+        else if (!kFp8)
+            load_by_tma(P, C, M, W, group);
+    }
     // lengths that cannot be served
     if (blockIdx.x == 0)
         for (int r = threadIdx.x; r < P.R; r += blockDim.x)
@@ -1494,7 +1504,7 @@ extern "C" int lmc_attend(const lmc_layout *L, const lmc_entries *e, const void 
     if (!allow_shared_memory(fp8 ? 2 : bf16 ? 1 : 0, kern))
         return LMC_ERR_CUDA;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    if (!follow(kern, dim3((unsigned)(P.cols * P.head_groups)), (kFirstLoader + (fp8 ? kFp8Loaders : 1)) * 32, smem, s,
+    if (!follow(kern, dim3((unsigned)(P.cols * P.head_groups)), fp8 ? kThreads<true> : kThreads<false>, smem, s,
                 P) ||
         !follow(lmc_attend_join_kernel, dim3((unsigned)std::min<int64_t>(P.cols, R), (unsigned)H), kJoinWarps * 32, 0,
                 s, P))
