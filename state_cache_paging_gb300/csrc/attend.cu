@@ -23,7 +23,7 @@
 //
 // A CTA: a loader brings the tile's entries to shared memory (panels of 64
 // values, 128-byte swizzle), one warp issues the products on the tensor cores,
-// four warps do the softmax.
+// eight warps do the softmax.
 //   S [64 heads x 64 tokens]   = Q . K^T    (A = Q, B = the tile, both with
 //                                            the summed axis contiguous)
 //   O^T [V values x heads]    += V^T . P^T  (A = the same tile read along its
@@ -65,11 +65,11 @@ constexpr int kMaxHeads = 64;         // heads per CTA
 constexpr int kPanel = kTile * 128;   // bytes of 64 values of a tile's rows
 constexpr int kMaxStages = 4;
 constexpr int kMaxCols = 160;         // CTAs along the cache's length (an SM each)
-constexpr int kSoftWarps = 4;
-constexpr int kScoreWarp = 4;          // issues S = Q K^T
-constexpr int kValueWarp = 5;          // issues O^T += V^T P^T
-constexpr int kFirstLoader = 6;        // 16-bit entries: one warp
-constexpr int kFirstFp8Loader = 8;     // fp8: eight, two whole warpgroups
+constexpr int kSoftWarps = 8;
+constexpr int kScoreWarp = 8;          // issues S = Q K^T
+constexpr int kValueWarp = 9;          // issues O^T += V^T P^T
+constexpr int kFirstLoader = 10;       // 16-bit entries: one warp
+constexpr int kFirstFp8Loader = 12;    // fp8: eight, two whole warpgroups
 constexpr int kFp8Loaders = 8;        // warps, eight of a tile's rows each
 #ifndef LMC_AHEAD
 #define LMC_AHEAD 2
@@ -79,6 +79,15 @@ constexpr int kAhead = LMC_AHEAD;     // tiles
 #define LMC_FP8_AHEAD 2
 #endif
 constexpr int kFp8Ahead = LMC_FP8_AHEAD;
+#ifndef LMC_EARLYP
+#define LMC_EARLYP 5
+#endif
+#ifndef LMC_SOFT
+#define LMC_SOFT 80
+#endif
+#ifndef LMC_LOADR
+#define LMC_LOADR 136
+#endif
 template <bool kFp8>
 constexpr int kThreads = (kFp8 ? kFirstFp8Loader + kFp8Loaders : kFirstLoader + 1) * 32;
 constexpr float kLag = 8.0f;          // how far (log2) a logit may exceed the reference
@@ -97,6 +106,7 @@ struct Control {
     uint32_t tmem;
     uint32_t gave_up;            // a wait ran out: nothing waits any more
     float factor[kMaxHeads];     // rescaling of a head's O
+    float half[2][kMaxHeads];    // a head's maximum or sum in each half of the tokens
     alignas(16) float inverse[kMaxHeads];  // 1 / l
     float q_scale[kMaxHeads];    // fp8: what q was divided by
 };
@@ -325,14 +335,14 @@ __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::aft
 __device__ __forceinline__ void wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
 __device__ __forceinline__ void wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-__device__ __forceinline__ void soft_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+__device__ __forceinline__ void soft_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 
 __device__ __forceinline__ bool soft_any(bool x) {
     uint32_t r;
     asm volatile(
         "{\n\t.reg .pred p, q;\n\t"
         "setp.ne.u32 p, %1, 0;\n\t"
-        "barrier.cta.red.or.pred q, 1, 128, p;\n\t"
+        "barrier.cta.red.or.pred q, 1, 256, p;\n\t"
         "selp.u32 %0, 1, 0, q;\n\t}"
         : "=r"(r)
         : "r"((uint32_t)x)
@@ -384,17 +394,14 @@ __device__ __forceinline__ void commit(uint64_t *bar) {
                  : "memory");
 }
 
-// 16 lanes x 64 columns: lane l of the warp holds rows l / 4 (s[4j], s[4j+1])
+// 16 lanes x 32 columns: lane l of the warp holds rows l / 4 (s[4j], s[4j+1])
 // and l / 4 + 8 (s[4j+2], s[4j+3]), columns 8j + 2 (l % 4) and the next.
-__device__ __forceinline__ void load_s(uint32_t (&s)[32], uint32_t addr) {
+__device__ __forceinline__ void load_s(uint32_t (&s)[16], uint32_t addr) {
     asm volatile(
-        "tcgen05.ld.sync.aligned.16x256b.x8.b32 "
-        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
         : "=r"(s[0]), "=r"(s[1]), "=r"(s[2]), "=r"(s[3]), "=r"(s[4]), "=r"(s[5]), "=r"(s[6]), "=r"(s[7]), "=r"(s[8]),
-          "=r"(s[9]), "=r"(s[10]), "=r"(s[11]), "=r"(s[12]), "=r"(s[13]), "=r"(s[14]), "=r"(s[15]), "=r"(s[16]),
-          "=r"(s[17]), "=r"(s[18]), "=r"(s[19]), "=r"(s[20]), "=r"(s[21]), "=r"(s[22]), "=r"(s[23]), "=r"(s[24]),
-          "=r"(s[25]), "=r"(s[26]), "=r"(s[27]), "=r"(s[28]), "=r"(s[29]), "=r"(s[30]), "=r"(s[31])
+          "=r"(s[9]), "=r"(s[10]), "=r"(s[11]), "=r"(s[12]), "=r"(s[13]), "=r"(s[14]), "=r"(s[15])
         : "r"(addr)
         : "memory");
 }
@@ -650,9 +657,10 @@ __device__ __forceinline__ void query_to_f16(const AttendPlan &P, Control &C, co
 // holds eight of a tile's rows, four lanes to a row: a lane takes 16 codes of
 // each panel, so a panel's codes are read as 64-byte pieces and its two
 // 16-byte halves are stored without bank conflicts, at offsets that do not
-// change from tile to tile. A tile is widened in registers before its stage is
-// free (only the stores wait for that) while the next one's codes are in
-// flight from L2.
+// change from tile to tile. Half of a tile is widened in registers before its
+// stage is free, while the next one's codes come from L2 into the registers
+// that this frees; the other half goes through registers only after that (all
+// of it widened early takes 72 registers more, and the softmax pays for them).
 __device__ __forceinline__ void load_fp8(const AttendPlan &P, Control &C, const Memory &M, Walk &W, int group) {
     constexpr int kPanels = kMaxEntry / 64;
     const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) - kFirstFp8Loader;
@@ -662,9 +670,11 @@ __device__ __forceinline__ void load_fp8(const AttendPlan &P, Control &C, const 
     uint32_t bad = 0, n = 0, segments = 0;
     if (warp == 0 && elect())
         asm volatile("prefetch.tensormap [%0];" ::"l"(&P.query) : "memory");
+    constexpr int kEarly = LMC_EARLYP;  // panels
     uint4 codes[kPanels];
-    uint32_t wide[kPanels][8];
-    uint64_t next_valid = 0;
+    uint32_t wide[kEarly][8];
+    uint64_t valid = 0, next_valid = 0;
+    const uint8_t *src = nullptr;  // the next tile's codes
     LastPage last, last_ahead;
     const int my_page = P.pages_per_tile == 1 ? 0 : row / P.block_size;
     const int my_row = row - my_page * P.block_size;
@@ -684,19 +694,31 @@ __device__ __forceinline__ void load_fp8(const AttendPlan &P, Control &C, const 
             __syncwarp();
         }
     };
-    auto load = [&](int j) {
+    auto find = [&](int j) {
         const Tile T = tile_at(P, W.first + j);
         const int block = resolve(P, W, T, next_valid, bad, last);
         const int64_t b = __shfl_sync(0xffffffffu, block, my_page & 31);
-        const bool mine = next_valid >> row & 1;
-        const uint8_t *src = P.pool + b * P.block_stride + (int64_t)(T.row0 + my_row) * P.token_bytes + piece * 16;
+        src = P.pool + b * P.block_stride + (int64_t)(T.row0 + my_row) * P.token_bytes + piece * 16;
+    };
+    auto load = [&](int i) {
+        codes[i] = make_uint4(0, 0, 0, 0);
+        if ((next_valid >> row & 1) && i * 4 + piece < chunks)
+            asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+                         : "=r"(codes[i].x), "=r"(codes[i].y), "=r"(codes[i].z), "=r"(codes[i].w)
+                         : "l"(src + i * 64));
+    };
+    auto widen = [&](uint32_t(&o)[8], const uint4 &c) {
+        const uint32_t w[4] = {c.x, c.y, c.z, c.w};
 #pragma unroll
-        for (int i = 0; i < kPanels; i++) {
-            codes[i] = make_uint4(0, 0, 0, 0);
-            if (mine && i * 4 + piece < chunks)
-                asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-                             : "=r"(codes[i].x), "=r"(codes[i].y), "=r"(codes[i].z), "=r"(codes[i].w)
-                             : "l"(src + i * 64));
+        for (int k = 0; k < 8; k++)
+            asm volatile("cvt.rn.f16x2.e4m3x2 %0, %1;"
+                         : "=r"(o[k])
+                         : "h"((unsigned short)(w[k >> 1] >> (16 * (k & 1)))));
+    };
+    auto put = [&](uint8_t *to, int i, const uint32_t(&o)[8]) {
+        if (i * 4 + piece < chunks) {
+            *reinterpret_cast<uint4 *>(to + i * kPanel + at0) = make_uint4(o[0], o[1], o[2], o[3]);
+            *reinterpret_cast<uint4 *>(to + i * kPanel + at1) = make_uint4(o[4], o[5], o[6], o[7]);
         }
     };
 
@@ -713,41 +735,51 @@ __device__ __forceinline__ void load_fp8(const AttendPlan &P, Control &C, const 
                 tma_box(&P.query, M.q + i * P.padded_heads * 128, i * 64, group * P.group_heads, r, &C.q_raw);
         }
         __syncwarp();
-        bar_wait(C, &C.q_raw, segments & 1, P.status);
-        segments++;
-        query_to_f16(P, C, M, warp);
-        fence_async();
-        __syncwarp();
-        if (lane == 0)
-            bar_arrive(&C.q_full);
-        load(0);
+        // a turn stores tile j and loads tile j + 1
 #pragma unroll 1
-        for (int j = 0; j < W.count; j++, n++) {
+        for (int j = -1; j < W.count; j++) {
+            const bool store = j >= 0, more = j + 1 < W.count;
+            valid = next_valid;
+            if (store)
 #pragma unroll
-            for (int i = 0; i < kPanels; i++) {
-                const uint32_t w[4] = {codes[i].x, codes[i].y, codes[i].z, codes[i].w};
+                for (int i = 0; i < kEarly; i++)
+                    widen(wide[i], codes[i]);
+            if (more) {
+                find(j + 1);
 #pragma unroll
-                for (int k = 0; k < 8; k++)
-                    asm volatile("cvt.rn.f16x2.e4m3x2 %0, %1;"
-                                 : "=r"(wide[i][k])
-                                 : "h"((unsigned short)(w[k >> 1] >> (16 * (k & 1)))));
+                for (int i = 0; i < kEarly; i++)
+                    load(i);
             }
-            const uint64_t valid = next_valid;
-            if (j + 1 < W.count)
-                load(j + 1);
-            prefetch(j + kFp8Ahead);
-            const int st = n % P.stages;
-            if (n >= (uint32_t)P.stages)
-                bar_wait(C, &C.kv_free[st], (n / P.stages - 1) & 1, P.status);
-            uint8_t *to = M.kv + (size_t)st * M.stage_bytes;
+            if (store) {
+                prefetch(j + kFp8Ahead);
+                const int st = n % P.stages;
+                if (n >= (uint32_t)P.stages)
+                    bar_wait(C, &C.kv_free[st], (n / P.stages - 1) & 1, P.status);
+                uint8_t *to = M.kv + (size_t)st * M.stage_bytes;
 #pragma unroll
-            for (int i = 0; i < kPanels; i++)
-                if (i * 4 + piece < chunks) {
-                    *reinterpret_cast<uint4 *>(to + i * kPanel + at0) =
-                        make_uint4(wide[i][0], wide[i][1], wide[i][2], wide[i][3]);
-                    *reinterpret_cast<uint4 *>(to + i * kPanel + at1) =
-                        make_uint4(wide[i][4], wide[i][5], wide[i][6], wide[i][7]);
+                for (int i = 0; i < kEarly; i++)
+                    put(to, i, wide[i]);
+#pragma unroll
+                for (int i = kEarly; i < kPanels; i++) {
+                    widen(wide[i - kEarly], codes[i]);
+                    put(to, i, wide[i - kEarly]);
                 }
+            }
+            if (more)
+#pragma unroll
+                for (int i = kEarly; i < kPanels; i++)
+                    load(i);
+            if (!store) {  // the queries, while the first tile is on its way
+                bar_wait(C, &C.q_raw, segments & 1, P.status);
+                segments++;
+                query_to_f16(P, C, M, warp);
+                fence_async();
+                __syncwarp();
+                if (lane == 0)
+                    bar_arrive(&C.q_full);
+                continue;
+            }
+            const int st = n % P.stages;
             if (warp == 0 && lane == 0) {
                 C.valid[n % (2 * kMaxStages)] = valid;
                 C.zero[n % (2 * kMaxStages)] = 0;  // the rows left out hold zeros
@@ -756,6 +788,7 @@ __device__ __forceinline__ void load_fp8(const AttendPlan &P, Control &C, const 
             __syncwarp();
             if (lane == 0)
                 bar_arrive(&C.kv_full[st]);
+            n++;
         }
     }
     if (bad)
@@ -842,50 +875,54 @@ __device__ __forceinline__ void multiply_values(const AttendPlan &P, Control &C,
 
 // A tile's logits (log2) to the workspace, for the token weights: pairs of
 // tokens where the whole tile is attended and its first token lies on an even
-// place, else one by one.
+// place, else one by one. c0: the thread's first token of the tile.
 __device__ __forceinline__ void keep_logits(const AttendPlan &P, const Walk &W, const Tile &T, const float *s, int head0,
-                                            int heads, int ra) {
-    const int at = T.t0 - (W.range.lo & ~1), c0 = 2 * (threadIdx.x & 3);
+                                            int heads, int ra, int c0) {
+    const int at = T.t0 - (W.range.lo & ~1);
     const uint64_t inside = bits(W.range.lo - T.t0, min(T.rows, W.range.L - T.t0));
     float *a = P.logits + ((int64_t)W.r * P.H + head0 + ra) * P.logit_stride + at + c0, *b = a + 8 * P.logit_stride;
     if (inside == ~0ull && (at & 1) == 0) {
         if (ra < heads)
 #pragma unroll
-            for (int i = 0; i < 8; i++)
+            for (int i = 0; i < 4; i++)
                 *reinterpret_cast<float2 *>(a + 8 * i) = make_float2(s[4 * i], s[4 * i + 1]);
         if (ra + 8 < heads)
 #pragma unroll
-            for (int i = 0; i < 8; i++)
+            for (int i = 0; i < 4; i++)
                 *reinterpret_cast<float2 *>(b + 8 * i) = make_float2(s[4 * i + 2], s[4 * i + 3]);
         return;
     }
 #pragma unroll
-    for (int i = 0; i < 32; i++) {
+    for (int i = 0; i < 16; i++) {
         const int c = 8 * (i >> 2) + (i & 1);
         if ((inside >> (c + c0) & 1) && ((i & 2) ? ra + 8 : ra) < heads)
             ((i & 2) ? b : a)[c] = s[i];
     }
 }
 
-// Four warps: the softmax, P, and the results. Warp w holds heads 16 w ..
-// 16 w + 15 of S, and values 32 w .. 32 w + 31 of each 128 of O^T.
+// Eight warps: the softmax, P, and the results. Warps w and w + 4 share heads
+// 16 w .. 16 w + 15 of S (the lanes of tensor memory that both may read): w
+// takes the tile's first 32 tokens, w + 4 the last. Of O^T they hold values
+// 32 w .. 32 w + 31 of each 128, w of the even 128s and w + 4 of the odd.
 template <bool kBf16, bool kFp8>
 __device__ __forceinline__ void soften(const AttendPlan &P, Control &C, const Memory &M, Walk &W, int col, int group) {
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const uint32_t lanes = C.tmem + ((uint32_t)(warp * 32) << 16);
-    const int ra = warp * 16 + lane / 4, rb = ra + 8;  // this thread's heads
-    const bool active = warp * 16 < P.padded_heads;
+    const int lane = threadIdx.x & 31, quarter = (threadIdx.x >> 5) & 3, half = threadIdx.x >> 7;
+    const uint32_t lanes = C.tmem + ((uint32_t)(quarter * 32) << 16);
+    const int ra = quarter * 16 + lane / 4, rb = ra + 8;  // this thread's heads
+    const int c0 = 32 * half + 2 * (lane & 3);            // and its first token
+    const bool active = quarter * 16 < P.padded_heads;
     const int head0 = group * P.group_heads;
     const int heads = min(P.group_heads, P.H - head0);
-    uint32_t n = 0, segments = 0;
+    uint32_t n = 0;
     int2 left[2] = {make_int2(-1, 0), make_int2(-1, 0)};  // what the CTA leaves unfinished
+    uint8_t *const pa = M.p + ra * 128 + 4 * (lane & 3), *const pb = M.p + rb * 128 + 4 * (lane & 3);
 
-    while (W.next(P)) {
+    for (uint32_t segments = 0; W.next(P); segments++) {
         float ma = -INFINITY, mb = -INFINITY, la = 0.0f, lb = 0.0f;
         float ca = P.log2_scale, cb = P.log2_scale;
+#pragma unroll 1
         for (int j = 0; j < W.count; j++, n++) {
             const int st = n % P.stages;
-            const Tile T = tile_at(P, W.first + j);
             bar_wait(C, &C.kv_full[st], (n / P.stages) & 1, P.status);
             if (kFp8 && j == 0) {
                 bar_wait(C, &C.q_full, segments & 1, P.status);
@@ -900,11 +937,11 @@ __device__ __forceinline__ void soften(const AttendPlan &P, Control &C, const Me
             const uint64_t valid = C.valid[n % (2 * kMaxStages)], zero = C.zero[n % (2 * kMaxStages)];
             bar_wait(C, &C.s_full[n & 1], (n >> 1) & 1, P.status);
             fence_after();
-            uint32_t raw[32];
+            uint32_t raw[16];
             float *s = reinterpret_cast<float *>(raw);
             float xa = -INFINITY, xb = -INFINITY;
             if (active) {
-                load_s(raw, lanes + (n & 1) * 64);
+                load_s(raw, lanes + (n & 1) * 64 + half * 32);
                 wait_ld();
             }
             fence_before();
@@ -913,28 +950,39 @@ __device__ __forceinline__ void soften(const AttendPlan &P, Control &C, const Me
                 bar_arrive(&C.s_free[n & 1]);
             if (active) {
 #pragma unroll
-                for (int i = 0; i < 32; i++)
+                for (int i = 0; i < 16; i++)
                     s[i] *= (i & 2) ? cb : ca;
                 if (valid != ~0ull) {
-                    const uint64_t mine = valid >> (2 * (lane & 3));
+                    const uint64_t mine = valid >> c0;
 #pragma unroll
-                    for (int i = 0; i < 32; i++)
+                    for (int i = 0; i < 16; i++)
                         if (!(mine >> (8 * (i >> 2) + (i & 1)) & 1))
                             s[i] = -INFINITY;
                 }
 #pragma unroll
-                for (int i = 0; i < 32; i += 4) {
+                for (int i = 0; i < 16; i += 4) {
                     xa = fmaxf(xa, fmaxf(s[i], s[i + 1]));
                     xb = fmaxf(xb, fmaxf(s[i + 2], s[i + 3]));
                 }
+                if (P.logits != nullptr)
+                    keep_logits(P, W, tile_at(P, W.first + j), s, head0, heads, ra, c0);
+            }
+            // Does any logit exceed its head's reference by too much? (Each
+            // thread asks for its own; the heads' maxima are only made then.)
+            if (soft_any(xa > ma + kLag || xb > mb + kLag)) {
                 xa = fmaxf(xa, __shfl_xor_sync(0xffffffffu, xa, 1));
                 xb = fmaxf(xb, __shfl_xor_sync(0xffffffffu, xb, 1));
                 xa = fmaxf(xa, __shfl_xor_sync(0xffffffffu, xa, 2));
                 xb = fmaxf(xb, __shfl_xor_sync(0xffffffffu, xb, 2));
-                if (P.logits != nullptr)
-                    keep_logits(P, W, T, s, head0, heads, ra);
-            }
-            if (soft_any(xa > ma + kLag || xb > mb + kLag)) {
+                if (active && (lane & 3) == 0) {
+                    C.half[half][ra] = xa;
+                    C.half[half][rb] = xb;
+                }
+                soft_sync();
+                if (active) {
+                    xa = fmaxf(xa, C.half[half ^ 1][ra]);
+                    xb = fmaxf(xb, C.half[half ^ 1][rb]);
+                }
                 float fa = 1.0f, fb = 1.0f;
                 if (xa > ma + kLag) {
                     fa = exp2_fast(ma - xa);
@@ -947,14 +995,16 @@ __device__ __forceinline__ void soften(const AttendPlan &P, Control &C, const Me
                 la *= fa;
                 lb *= fb;
                 if (j > 0) {
-                    if (active && (lane & 3) == 0) {
+                    if (active && half == 0 && (lane & 3) == 0) {
                         C.factor[ra] = fa;
                         C.factor[rb] = fb;
                     }
                     soft_sync();
                     bar_wait(C, &C.pv_done, (n - 1) & 1, P.status);
                     fence_after();
-                    for (int t = 0; t < P.value_tiles; t++)
+#pragma unroll 1
+                    for (int t = half; t < P.value_tiles; t += 2)
+#pragma unroll 1
                         for (int c = 0; c < P.padded_heads; c += 16) {
                             uint32_t o[16];
                             const uint32_t at = lanes + 128 + t * P.padded_heads + c;
@@ -967,24 +1017,23 @@ __device__ __forceinline__ void soften(const AttendPlan &P, Control &C, const Me
                         }
                     wait_st();
                     fence_before();
-                    soft_sync();  // the factors may be written again
                 }
+                soft_sync();  // the maxima and factors may be written again
             }
             // P and the cleared rows go where the last tile's product read
             if (n > 0)
                 bar_wait(C, &C.pv_done, (n - 1) & 1, P.status);
             if (active) {
                 const float na = ma == -INFINITY ? 0.0f : ma, nb = mb == -INFINITY ? 0.0f : mb;
-                uint8_t *const pa = M.p + ra * 128 + 4 * (lane & 3), *const pb = M.p + rb * 128 + 4 * (lane & 3);
                 const int x = ra & 7;  // rb & 7 is the same
 #pragma unroll
-                for (int i = 0; i < 8; i++) {
+                for (int i = 0; i < 4; i++) {
                     const float p0 = exp2_fast(s[4 * i] - na), p1 = exp2_fast(s[4 * i + 1] - na);
                     const float p2 = exp2_fast(s[4 * i + 2] - nb), p3 = exp2_fast(s[4 * i + 3] - nb);
                     la += p0 + p1;
                     lb += p2 + p3;
-                    *reinterpret_cast<uint32_t *>(pa + ((i ^ x) << 4)) = pack<kBf16>(p0, p1);
-                    *reinterpret_cast<uint32_t *>(pb + ((i ^ x) << 4)) = pack<kBf16>(p2, p3);
+                    *reinterpret_cast<uint32_t *>(pa + (((i + 4 * half) ^ x) << 4)) = pack<kBf16>(p0, p1);
+                    *reinterpret_cast<uint32_t *>(pb + (((i + 4 * half) ^ x) << 4)) = pack<kBf16>(p2, p3);
                 }
             }
             if (!kFp8 && zero != 0) {
@@ -993,7 +1042,7 @@ __device__ __forceinline__ void soften(const AttendPlan &P, Control &C, const Me
                 uint8_t *kv = M.kv + (size_t)st * M.stage_bytes;
                 const int row = threadIdx.x & 63;
                 if (zero >> row & 1)
-                    for (int i = threadIdx.x >> 6; i < 2 * P.value_tiles; i += 2)
+                    for (int i = threadIdx.x >> 6; i < 2 * P.value_tiles; i += kSoftWarps / 2)
                         for (int c = 0; c < 8; c++)
                             *reinterpret_cast<uint4 *>(kv + i * kPanel + row * 128 + c * 16) = make_uint4(0, 0, 0, 0);
             }
@@ -1003,20 +1052,25 @@ __device__ __forceinline__ void soften(const AttendPlan &P, Control &C, const Me
                 bar_arrive(&C.p_full);
         }
 
-        // the segment's end
+        // the segment's end: each head's sum over its threads
         la += __shfl_xor_sync(0xffffffffu, la, 1);
         lb += __shfl_xor_sync(0xffffffffu, lb, 1);
         la += __shfl_xor_sync(0xffffffffu, la, 2);
         lb += __shfl_xor_sync(0xffffffffu, lb, 2);
+        if (active && half == 1 && (lane & 3) == 0) {
+            C.half[1][ra] = la;
+            C.half[1][rb] = lb;
+        }
+        soft_sync();
         const bool whole = W.begins && W.ends;
         const int slot = 2 * col + (W.begins ? 1 : 0);
-        if (active && (lane & 3) == 0) {
-            const float na = ma == -INFINITY ? 0.0f : ma, nb = mb == -INFINITY ? 0.0f : mb;
-            C.inverse[ra] = whole ? (la == 0.0f ? 0.0f : P.scale / la) : P.scale;
-            C.inverse[rb] = whole ? (lb == 0.0f ? 0.0f : P.scale / lb) : P.scale;
+        if (active && half == 0 && (lane & 3) == 0) {
+#pragma unroll
             for (int k = 0; k < 2; k++) {
                 const int row = k ? rb : ra;
-                const float m = k ? nb : na, l = k ? lb : la;
+                const float m0 = k ? mb : ma, m = m0 == -INFINITY ? 0.0f : m0;
+                const float l = (k ? lb : la) + C.half[1][row];
+                C.inverse[row] = whole ? (l == 0.0f ? 0.0f : P.scale / l) : P.scale;
                 if (row >= heads)
                     continue;
                 const int h = head0 + row;
@@ -1035,8 +1089,10 @@ __device__ __forceinline__ void soften(const AttendPlan &P, Control &C, const Me
         soft_sync();
         bar_wait(C, &C.pv_done, (n - 1) & 1, P.status);
         fence_after();
-        for (int t = 0; t < P.value_tiles; t++) {
-            const int v = t * 128 + warp * 32 + lane;
+#pragma unroll 1
+        for (int t = half; t < P.value_tiles; t += 2) {
+            const int v = t * 128 + quarter * 32 + lane;
+#pragma unroll 1
             for (int c = 0; c < P.padded_heads; c += 16) {
                 uint32_t o[16];
                 load_o(o, lanes + 128 + t * P.padded_heads + c);
@@ -1056,6 +1112,7 @@ __device__ __forceinline__ void soften(const AttendPlan &P, Control &C, const Me
                         for (int k = 0; k < 16; k++, to += P.out_head_stride)
                             *to = to_out(__uint_as_float(o[k]) * inv[k], P.q_bf16);
                     } else {
+#pragma unroll 1
                         for (int k = 0; c + k < heads; k++, to += P.out_head_stride)
                             *to = to_out(__uint_as_float(at16(o, k)) * C.inverse[c + k], P.q_bf16);
                     }
@@ -1066,6 +1123,7 @@ __device__ __forceinline__ void soften(const AttendPlan &P, Control &C, const Me
                         for (int k = 0; k < 16; k++, to += P.V)
                             *to = __uint_as_float(o[k]) * inv[k];
                     } else {
+#pragma unroll 1
                         for (int k = 0; c + k < heads; k++, to += P.V)
                             *to = __uint_as_float(at16(o, k)) * C.inverse[c + k];
                     }
@@ -1076,7 +1134,6 @@ __device__ __forceinline__ void soften(const AttendPlan &P, Control &C, const Me
         soft_sync();  // the inverses may be written again
         if (lane == 0)
             bar_arrive(&C.o_free);
-        segments++;
     }
     if (threadIdx.x == 0 && group == 0) {
         P.segment[2 * col] = left[0];
@@ -1127,11 +1184,13 @@ __global__ void __launch_bounds__(kThreads<kFp8>, 1) lmc_attend_kernel(const __g
     Walk W;
     W.init(P, col);
     if (warp < kSoftWarps) {
+        if (kFp8)
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(LMC_SOFT));
         soften<kBf16, kFp8>(P, C, M, W, col, group);
     } else if (kFp8 && warp >= kFirstFp8Loader) {
-        // registers for a tile as f16 and the next one's codes, from the
-        // warpgroup that issues the products: 128 + 40 + 2 x 168 of 4 x 128
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 168;");
+        // registers for a tile as f16 and the next one's codes, from the other
+        // warpgroups: 2 x 80 + 40 + 2 x 136 of 5 x 96
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(LMC_LOADR));
         load_fp8(P, C, M, W, group);
     } else {
         if (kFp8)
