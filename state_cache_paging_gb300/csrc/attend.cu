@@ -1308,28 +1308,49 @@ __global__ void __launch_bounds__(kJoinWarps * 32) lmc_attend_join_kernel(const 
 }
 
 constexpr int kWeightThreads = 256;
+constexpr int kWeightTokens = 256;  // of a block: four per thread
+constexpr int kWeightParts = 4;     // the heads are dealt out to as many threads
 
-// A thread per token: the sum over the heads of 2^(logit - lse).
+// Each token's sum over the heads of 2^(logit - lse). A thread has four tokens
+// and a quarter of the heads, so all of its loads are in flight at once; the
+// quarters are added in shared memory, always in the same order.
 __global__ void __launch_bounds__(kWeightThreads) lmc_attend_weights_kernel(const __grid_constant__ AttendPlan P) {
+    __shared__ float4 sums[kWeightParts][kWeightTokens / 4];
     const int r = blockIdx.y;
     wait_for_launch();
     let_next_start();
     const Range g = range_of(P, r);
-    if (!g.ok)
+    const int base = g.lo & ~1;  // the logits' first place, and 16-byte aligned
+    const int first = blockIdx.x * kWeightTokens;
+    if (!g.ok || g.L == 0 || first >= g.L - base)
         return;
-    const int64_t t = g.lo + blockIdx.x * (int64_t)kWeightThreads + threadIdx.x;
-    if (t >= g.L)
-        return;
-    const float *x = P.logits + (int64_t)r * P.H * P.logit_stride + (t - (g.lo & ~1));
+    const int four = threadIdx.x % (kWeightTokens / 4), part = threadIdx.x / (kWeightTokens / 4);
+    const float *x = P.logits + (int64_t)r * P.H * P.logit_stride + first + 4 * four;
     const float *lse = P.lse2 + (int64_t)r * P.H;
-    float w = 0.0f;
-#pragma unroll 16
-    for (int h = 0; h < P.H; h++) {
-        const float top = __ldg(lse + h);
-        const float p = exp2_fast(__ldcs(x + h * P.logit_stride) - top);
-        w += top == -INFINITY ? 0.0f : p;
+    float4 w = {};
+    if (first + 4 * four < g.L - base) {
+#pragma unroll 8
+        for (int h = part; h < P.H; h += kWeightParts) {
+            const float top = __ldg(lse + h);
+            const float4 v = __ldcs(reinterpret_cast<const float4 *>(x + h * P.logit_stride));
+            if (top != -INFINITY) {
+                w.x += exp2_fast(v.x - top);
+                w.y += exp2_fast(v.y - top);
+                w.z += exp2_fast(v.z - top);
+                w.w += exp2_fast(v.w - top);
+            }
+        }
     }
-    P.weights[r * P.weights_request_stride + t] += w;
+    sums[part][four] = w;
+    __syncthreads();
+    const int t = base + first + (int)threadIdx.x;
+    if (t < g.lo || t >= g.L)
+        return;
+    float sum = 0.0f;
+#pragma unroll
+    for (int k = 0; k < kWeightParts; k++)
+        sum += reinterpret_cast<const float *>(sums[k])[threadIdx.x];
+    P.weights[r * P.weights_request_stride + t] += sum;
 }
 
 // ---- host ------------------------------------------------------------------------
@@ -1571,7 +1592,7 @@ extern "C" int lmc_attend(const lmc_layout *L, const lmc_entries *e, const void 
     if (P.weights != nullptr) {
         const int64_t tokens = P.window > 0 ? std::min(P.max_length, P.window) : std::max(P.max_length, 1);
         if (!follow(lmc_attend_weights_kernel,
-                    dim3((unsigned)((tokens + kWeightThreads - 1) / kWeightThreads), (unsigned)R), kWeightThreads, 0, s,
+                    dim3((unsigned)((tokens + 1 + kWeightTokens - 1) / kWeightTokens), (unsigned)R), kWeightThreads, 0, s,
                     P))
             return LMC_ERR_CUDA;
     }
