@@ -144,6 +144,7 @@ struct AttendPlan {
     int32_t pages_per_tile;    // > 1 where several pages fit a tile
     int32_t span;              // tokens of a page, or of a tile's pages
     int32_t tiles_per_span;
+    uint32_t span_inverse, tiles_inverse;  // see quotient()
     int32_t cols;              // CTAs along the length
     int32_t head_groups, group_heads;  // heads of a CTA
     int32_t padded_heads;      // rounded up to 16
@@ -163,18 +164,27 @@ struct Range {
     bool ok;    // a length that can be served
 };
 
-__device__ __forceinline__ Range range_of(const AttendPlan &P, int r) {
+__device__ __forceinline__ Range range_for(const AttendPlan &P, int length) {
     Range g;
-    g.L = __ldg(P.lengths + r);
+    g.L = length;
     g.ok = g.L >= 0 && g.L <= P.max_length;
     g.lo = P.window > 0 ? max(0, g.L - P.window) : 0;
     return g;
 }
 
+// n / d for 0 <= n < 2^31 by m = floor(2^32 / d) (2^32 - 1 for d = 1): the
+// product's upper half is the quotient or one less.
+__device__ __forceinline__ int quotient(int n, int d, uint32_t m) {
+    const int q = (int)__umulhi((uint32_t)n, m);
+    return q + (n - q * d >= d ? 1 : 0);
+}
+
 __device__ __forceinline__ int tile_of(const AttendPlan &P, int t) {
-    const int s = t / P.span;
+    const int s = quotient(t, P.span, P.span_inverse);
     return s * P.tiles_per_span + (t - s * P.span) / kTile;
 }
+
+__device__ __forceinline__ Range range_of(const AttendPlan &P, int r) { return range_for(P, __ldg(P.lengths + r)); }
 
 __device__ __forceinline__ int tiles_of(const AttendPlan &P, const Range &g) {
     return !g.ok || g.L == 0 ? 0 : tile_of(P, g.L - 1) + 1 - tile_of(P, g.lo);
@@ -184,7 +194,8 @@ __device__ __forceinline__ int tiles_of(const AttendPlan &P, const Range &g) {
 // time, a lane each. (All requests' tiles together number less than 2^31.)
 struct Walk {
     int pos, end;     // the CTA's tiles still to come, of all requests' in a row
-    int start, stop;  // this lane's request's tiles
+    int length;       // this lane's request's,
+    int start, stop;  // and its tiles
     int r0;           // the first of the 32 requests at hand
 
     // the current segment
@@ -194,7 +205,8 @@ struct Walk {
 
     __device__ __forceinline__ void load(const AttendPlan &P, int base) {
         const int lane = threadIdx.x & 31;
-        const int n = r0 + lane < P.R ? tiles_of(P, range_of(P, r0 + lane)) : 0;
+        length = r0 + lane < P.R ? __ldg(P.lengths + r0 + lane) : 0;
+        const int n = tiles_of(P, range_for(P, length));
         int sum = n;
         for (int o = 1; o < 32; o <<= 1) {
             const int x = __shfl_up_sync(0xffffffffu, sum, o);
@@ -232,7 +244,7 @@ struct Walk {
         const int k = __ffs(here) - 1;
         const int s = __shfl_sync(0xffffffffu, start, k), e = __shfl_sync(0xffffffffu, stop, k);
         r = r0 + k;
-        range = range_of(P, r);
+        range = range_for(P, __shfl_sync(0xffffffffu, length, k));
         begins = s == pos;
         ends = e <= end;
         first = pos - s + tile_of(P, range.lo);
@@ -249,7 +261,7 @@ struct Tile {
 
 __device__ __forceinline__ Tile tile_at(const AttendPlan &P, int tile) {
     Tile T;
-    const int s = tile / P.tiles_per_span;
+    const int s = quotient(tile, P.tiles_per_span, P.tiles_inverse);
     T.row0 = (tile - s * P.tiles_per_span) * kTile;
     T.t0 = s * P.span + T.row0;
     T.rows = min(kTile, P.span - T.row0);
@@ -531,17 +543,7 @@ __device__ __forceinline__ void load_by_tma(const AttendPlan &P, Control &C, con
         asm volatile("prefetch.tensormap [%0];" ::"l"(&P.query) : "memory");
     }
     while (W.next(P)) {
-        if (segments > 0)
-            bar_wait(C, &C.q_free, (segments - 1) & 1, P.status);
         const int row_panels = (P.E + 63) / 64;
-        const int r = (int)uniform(W.r);
-        if (elect()) {
-            bar_expect(&C.q_full, (uint32_t)(row_panels * P.padded_heads * 128));
-            for (int i = 0; i < P.query_copies; i++)
-                tma_box(&P.query, M.q + i * P.padded_heads * 128, i * 64, group * P.group_heads, r, &C.q_full);
-        }
-        __syncwarp();
-        segments++;
         for (int j = 0; j < W.count; j++, n++) {
             const int st = (int)uniform(n % P.stages);
             const Tile T = tile_at(P, W.first + j);
@@ -581,6 +583,19 @@ __device__ __forceinline__ void load_by_tma(const AttendPlan &P, Control &C, con
                 }
             }
             __syncwarp();
+            if (j == 0) {  // the queries second: their place is free later than the first tile's
+                const int r = (int)uniform(W.r);
+                if (segments > 0)
+                    bar_wait(C, &C.q_free, (segments - 1) & 1, P.status);
+                __syncwarp();
+                if (elect()) {
+                    bar_expect(&C.q_full, (uint32_t)(row_panels * P.padded_heads * 128));
+                    for (int i = 0; i < P.query_copies; i++)
+                        tma_box(&P.query, M.q + i * P.padded_heads * 128, i * 64, group * P.group_heads, r, &C.q_full);
+                }
+                __syncwarp();
+                segments++;
+            }
             if (j + kAhead < W.count) {
                 const Tile A = tile_at(P, W.first + j + kAhead);
                 uint64_t unused;
@@ -723,18 +738,9 @@ __device__ __forceinline__ void load_fp8(const AttendPlan &P, Control &C, const 
     };
 
     while (W.next(P)) {
-        if (segments > 0)
-            bar_wait(C, &C.q_free, (segments - 1) & 1, P.status);
 #pragma unroll 1
-        for (int j = 0; j < kFp8Ahead; j++)
+        for (int j = 1; j < kFp8Ahead; j++)
             prefetch(j);
-        const int r = (int)uniform(W.r);
-        if (warp == 0 && elect()) {
-            bar_expect(&C.q_raw, (uint32_t)((P.E + 63) / 64 * P.padded_heads * 128));
-            for (int i = 0; i < P.query_copies; i++)
-                tma_box(&P.query, M.q + i * P.padded_heads * 128, i * 64, group * P.group_heads, r, &C.q_raw);
-        }
-        __syncwarp();
         // a turn stores tile j and loads tile j + 1
 #pragma unroll 1
         for (int j = -1; j < W.count; j++) {
@@ -770,6 +776,16 @@ __device__ __forceinline__ void load_fp8(const AttendPlan &P, Control &C, const 
                 for (int i = kEarly; i < kPanels; i++)
                     load(i);
             if (!store) {  // the queries, while the first tile is on its way
+                const int r = (int)uniform(W.r);
+                if (segments > 0)
+                    bar_wait(C, &C.q_free, (segments - 1) & 1, P.status);
+                __syncwarp();
+                if (warp == 0 && elect()) {
+                    bar_expect(&C.q_raw, (uint32_t)((P.E + 63) / 64 * P.padded_heads * 128));
+                    for (int i = 0; i < P.query_copies; i++)
+                        tma_box(&P.query, M.q + i * P.padded_heads * 128, i * 64, group * P.group_heads, r, &C.q_raw);
+                }
+                __syncwarp();
                 bar_wait(C, &C.q_raw, segments & 1, P.status);
                 segments++;
                 query_to_f16(P, C, M, warp);
@@ -870,6 +886,28 @@ __device__ __forceinline__ void multiply_values(const AttendPlan &P, Control &C,
             __syncwarp();
         }
         segments++;
+    }
+}
+
+// One value of up to 16 heads, times each head's factor: without a test per
+// head where there are 16 (a test per store costs three times the store).
+template <typename T, typename F>
+__device__ __forceinline__ void write_heads(const uint32_t (&o)[16], const float *factor, int heads, T *to, int64_t stride,
+                                            F convert) {
+    if (heads >= 16) {
+#pragma unroll
+        for (int k = 0; k < 16; k += 4) {
+            const float4 f = *reinterpret_cast<const float4 *>(factor + k);
+            to[0] = convert(__uint_as_float(o[k]) * f.x);
+            to[stride] = convert(__uint_as_float(o[k + 1]) * f.y);
+            to[2 * stride] = convert(__uint_as_float(o[k + 2]) * f.z);
+            to[3 * stride] = convert(__uint_as_float(o[k + 3]) * f.w);
+            to += 4 * stride;
+        }
+    } else {
+#pragma unroll 1
+        for (int k = 0; k < heads; k++, to += stride)
+            *to = convert(__uint_as_float(at16(o, k)) * factor[k]);
     }
 }
 
@@ -1039,12 +1077,13 @@ __device__ __forceinline__ void soften(const AttendPlan &P, Control &C, const Me
             if (!kFp8 && zero != 0) {
                 // tokens that are not attended take part with p = 0: their
                 // values must not be infinite or NaN
-                uint8_t *kv = M.kv + (size_t)st * M.stage_bytes;
-                const int row = threadIdx.x & 63;
-                if (zero >> row & 1)
-                    for (int i = threadIdx.x >> 6; i < 2 * P.value_tiles; i += kSoftWarps / 2)
-                        for (int c = 0; c < 8; c++)
-                            *reinterpret_cast<uint4 *>(kv + i * kPanel + row * 128 + c * 16) = make_uint4(0, 0, 0, 0);
+                // (eight lanes to a row's panel: whole rows' stores would all
+                // fall into the same banks)
+                uint8_t *kv = M.kv + (size_t)st * M.stage_bytes + (threadIdx.x & 7) * 16;
+                for (int row = threadIdx.x >> 3; row < kTile; row += kSoftWarps * 4)
+                    if (zero >> row & 1)
+                        for (int i = 0; i < 2 * P.value_tiles; i++)
+                            *reinterpret_cast<uint4 *>(kv + i * kPanel + row * 128) = make_uint4(0, 0, 0, 0);
             }
             fence_async();
             __syncwarp();
@@ -1092,41 +1131,28 @@ __device__ __forceinline__ void soften(const AttendPlan &P, Control &C, const Me
 #pragma unroll 1
         for (int t = half; t < P.value_tiles; t += 2) {
             const int v = t * 128 + quarter * 32 + lane;
+            uint32_t o[kFp8 ? 1 : 2][16];  // (an fp8 cache leaves the softmax few registers)
+            constexpr int kTake = kFp8 ? 1 : 2;
 #pragma unroll 1
-            for (int c = 0; c < P.padded_heads; c += 16) {
-                uint32_t o[16];
-                load_o(o, lanes + 128 + t * P.padded_heads + c);
-                float inv[16];
-#pragma unroll
-                for (int k = 0; k < 16; k += 4)
-                    *reinterpret_cast<float4 *>(inv + k) = *reinterpret_cast<const float4 *>(C.inverse + c + k);
+            for (int c0 = 0; c0 < P.padded_heads; c0 += 16 * kTake) {
+                load_o(o[0], lanes + 128 + t * P.padded_heads + c0);
+                if (kTake > 1 && c0 + 16 < P.padded_heads)
+                    load_o(o[kTake - 1], lanes + 128 + t * P.padded_heads + c0 + 16);
                 wait_ld();
-                if (v >= P.V)
-                    continue;
-                // 16 heads without a test each where there are as many (a
-                // test per store costs three times the store)
-                if (whole) {
-                    uint16_t *to = P.out + W.r * P.out_request_stride + (head0 + c) * P.out_head_stride + v;
-                    if (c + 16 <= heads) {
 #pragma unroll
-                        for (int k = 0; k < 16; k++, to += P.out_head_stride)
-                            *to = to_out(__uint_as_float(o[k]) * inv[k], P.q_bf16);
+                for (int i = 0; i < kTake; i++) {
+                    const int c = c0 + 16 * i;
+                    if (v >= P.V) {
+                        // not a value: nothing to write
+                    } else if (whole) {
+                        uint16_t *to = P.out + W.r * P.out_request_stride + (head0 + c) * P.out_head_stride + v;
+                        write_heads(o[i], C.inverse + c, heads - c, to, P.out_head_stride,
+                                    [&](float x) { return to_out(x, P.q_bf16); });
                     } else {
-#pragma unroll 1
-                        for (int k = 0; c + k < heads; k++, to += P.out_head_stride)
-                            *to = to_out(__uint_as_float(at16(o, k)) * C.inverse[c + k], P.q_bf16);
+                        float *to = P.part_o + ((int64_t)slot * P.H + head0 + c) * P.V + v;
+                        write_heads(o[i], C.inverse + c, heads - c, to, (int64_t)P.V, [](float x) { return x; });
                     }
-                } else {
-                    float *to = P.part_o + ((int64_t)slot * P.H + head0 + c) * P.V + v;
-                    if (c + 16 <= heads) {
-#pragma unroll
-                        for (int k = 0; k < 16; k++, to += P.V)
-                            *to = __uint_as_float(o[k]) * inv[k];
-                    } else {
-#pragma unroll 1
-                        for (int k = 0; c + k < heads; k++, to += P.V)
-                            *to = __uint_as_float(at16(o, k)) * C.inverse[c + k];
-                    }
+                    __syncwarp();  // together again for the next read of tensor memory
                 }
             }
         }
@@ -1551,6 +1577,9 @@ extern "C" int lmc_attend(const lmc_layout *L, const lmc_entries *e, const void 
     P.pages_per_tile = N < kTile && N % 8 == 0 ? (int32_t)(kTile / N) : 1;
     P.span = (int32_t)N * P.pages_per_tile;
     P.tiles_per_span = (P.span + kTile - 1) / kTile;
+    auto inverse = [](int32_t d) { return d == 1 ? ~0u : (uint32_t)(((uint64_t)1 << 32) / (uint32_t)d); };
+    P.span_inverse = inverse(P.span);
+    P.tiles_inverse = inverse(P.tiles_per_span);
     if (R * (P.max_length / P.span + 1) * P.tiles_per_span > INT32_MAX)
         return LMC_ERR_OVERFLOW;
     P.head_groups = W.head_groups;
