@@ -129,7 +129,7 @@ struct AttendPlan {
     float *weights;  // caller's, or NULL
     int64_t weights_request_stride;
     // workspace
-    int2 *segment;   // [2 cols]: (request, tiles) a CTA left unfinished, or (-1, 0)
+    int4 *segment;   // [2 cols]: (request, tiles here, all its tiles, 0) a CTA left unfinished, or (-1, ..)
     float2 *part_ml; // [2 cols][H]
     float *part_o;   // [2 cols][H][V]
     float *lse2;     // [R][H], log2
@@ -200,6 +200,7 @@ struct Walk {
 
     // the current segment
     int r, first, count;  // request, its first tile here (of the request's), tiles
+    int tiles;            // the request's
     bool begins, ends;    // the request begins / ends in this CTA
     Range range;
 
@@ -249,6 +250,7 @@ struct Walk {
         ends = e <= end;
         first = pos - s + tile_of(P, range.lo);
         count = min(e, end) - pos;
+        tiles = e - s;
         pos += count;
         return true;
     }
@@ -952,8 +954,21 @@ __device__ __forceinline__ void soften(const AttendPlan &P, Control &C, const Me
     const int head0 = group * P.group_heads;
     const int heads = min(P.group_heads, P.H - head0);
     uint32_t n = 0;
-    int2 left[2] = {make_int2(-1, 0), make_int2(-1, 0)};  // what the CTA leaves unfinished
+    int4 left[2] = {make_int4(-1, 0, 0, 0), make_int4(-1, 0, 0, 0)};  // what the CTA leaves unfinished
     uint8_t *const pa = M.p + ra * 128 + 4 * (lane & 3), *const pb = M.p + rb * 128 + 4 * (lane & 3);
+
+    // the rows of requests without tokens, while the first tile is on its way
+    for (int r = col; r < P.R; r += P.cols) {
+        const Range g = range_of(P, r);
+        if (!g.ok || g.L != 0)
+            continue;
+        for (int h = head0 + (threadIdx.x >> 5); h < head0 + heads; h += kSoftWarps) {
+            for (int v = lane; v < P.V; v += 32)
+                P.out[r * P.out_request_stride + h * P.out_head_stride + v] = 0;
+            if (lane == 0 && P.lse != nullptr)
+                P.lse[r * P.lse_request_stride + h] = -INFINITY;
+        }
+    }
 
     for (uint32_t segments = 0; W.next(P); segments++) {
         float ma = -INFINITY, mb = -INFINITY, la = 0.0f, lb = 0.0f;
@@ -1124,7 +1139,7 @@ __device__ __forceinline__ void soften(const AttendPlan &P, Control &C, const Me
             }
         }
         if (!whole)
-            left[slot & 1] = make_int2(W.r, W.count);
+            left[slot & 1] = make_int4(W.r, W.count, W.tiles, 0);
         soft_sync();
         bar_wait(C, &C.pv_done, (n - 1) & 1, P.status);
         fence_after();
@@ -1242,95 +1257,122 @@ __global__ void __launch_bounds__(kThreads<kFp8>, 1) lmc_attend_kernel(const __g
 
 // ---- joining -------------------------------------------------------------------
 
-constexpr int kJoinWarps = kMaxValue / 128;  // a warp for 128 values each
+constexpr int kJoinWarps = 4;
+constexpr int kJoinNotes = kMaxCols / 32;  // per lane
 
-// Block (x, h): joins head h of the x-th request that spans several CTAs (each
+// Block (x, y): joins heads of the x-th request that spans several CTAs (each
 // begins in a CTA of its own, so there are at most as many as requests and
-// CTAs); and writes the rows of requests without tokens (r = x, x + blocks,
-// ...).
+// CTAs). A warp joins a head, or (kSlices = 4) a quarter of its values. What
+// bounds it is latency, so it makes three trips to memory: all CTAs' notes,
+// the parts' factors, the parts. (Looking for the request in a loop over the
+// notes and reading its length again took 14.5 us for 152 requests of 32 heads,
+// four warps to a head in every case 12 us; with few heads to join, one warp to
+// a head leaves the device idle.)
+template <int kSlices>
 __global__ void __launch_bounds__(kJoinWarps * 32) lmc_attend_join_kernel(const __grid_constant__ AttendPlan P) {
+    constexpr int kTake = kMaxValue / 128 / kSlices;  // float4s per lane
     __shared__ float factors[kJoinWarps][kMaxCols];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int h = blockIdx.y, v = threadIdx.x * 4;
+    const int h = kSlices == 1 ? blockIdx.y * kJoinWarps + warp : blockIdx.y;
+    const int v0 = 4 * lane + (kSlices == 1 ? 0 : 128 * warp);
     wait_for_launch();
     let_next_start();
-    for (int r = blockIdx.x; r < P.R; r += gridDim.x) {
-        const Range g = range_of(P, r);
-        if (!g.ok || g.L != 0)
-            continue;
-        for (int i = threadIdx.x; i < P.V; i += kJoinWarps * 32)
-            P.out[r * P.out_request_stride + h * P.out_head_stride + i] = 0;
-        if (threadIdx.x == 0 && P.lse != nullptr)
-            P.lse[r * P.lse_request_stride + h] = -INFINITY;
+    if (h >= P.H)
+        return;
+    int4 begun[kJoinNotes];
+    int2 gone_on[kJoinNotes];
+#pragma unroll
+    for (int i = 0; i < kJoinNotes; i++) {
+        const int c = 32 * i + lane;
+        begun[i] = make_int4(-1, 0, 0, 0);
+        gone_on[i] = make_int2(-1, 0);
+        if (c < P.cols) {
+            begun[i] = P.segment[2 * c + 1];
+            gone_on[i] = *reinterpret_cast<const int2 *>(P.segment + 2 * c);
+        }
     }
-    int col = -1, seen = 0;
-    for (int c0 = 0; c0 < P.cols; c0 += 32) {
-        const bool begins = c0 + lane < P.cols && P.segment[2 * (c0 + lane) + 1].x >= 0;
-        const uint32_t here = __ballot_sync(0xffffffffu, begins);
+    int col = -1, seen = 0, r = -1, rest = 0;
+#pragma unroll
+    for (int i = 0; i < kJoinNotes; i++) {
+        const uint32_t here = __ballot_sync(0xffffffffu, begun[i].x >= 0);
         const int rank = seen + __popc(here & ((1u << lane) - 1u));
-        const uint32_t mine = __ballot_sync(0xffffffffu, begins && rank == (int)blockIdx.x);
-        if (mine != 0)
-            col = c0 + __ffs(mine) - 1;
+        const uint32_t mine = __ballot_sync(0xffffffffu, begun[i].x >= 0 && rank == (int)blockIdx.x);
+        if (mine != 0) {
+            const int k = __ffs(mine) - 1;
+            col = 32 * i + k;
+            r = __shfl_sync(0xffffffffu, begun[i].x, k);
+            rest = __shfl_sync(0xffffffffu, begun[i].z - begun[i].y, k);
+        }
         seen += __popc(here);
     }
     if (col < 0)
         return;
-    const int2 head = P.segment[2 * col + 1];
-    const int r = head.x;
     // parts: slot 2 col + 1, then 2 (col + 1), ...; all CTAs but the last have
     // as many tiles as the next one
-    const int rest = tiles_of(P, range_of(P, r)) - head.y;
-    int parts = 1;
-    if (rest > 0 && col + 1 < P.cols && P.segment[2 * col + 2].x == r) {
-        const int each = max(1, P.segment[2 * col + 2].y);
-        parts = min(P.cols - col, 1 + (rest + each - 1) / each);
-    }
-    // each warp has the factors for itself: no barrier
+    int next_r = -1, each = 0;
+#pragma unroll
+    for (int i = 0; i < kJoinNotes; i++)
+        if (32 * i + lane == col + 1) {
+            next_r = gone_on[i].x;
+            each = gone_on[i].y;
+        }
+    next_r = __shfl_sync(0xffffffffu, next_r, (col + 1) & 31);
+    each = __shfl_sync(0xffffffffu, each, (col + 1) & 31);
+    const int parts = rest > 0 && next_r == r ? min(P.cols - col, 1 + (rest + each - 1) / max(1, each)) : 1;
     const float2 *ml = P.part_ml + (int64_t)2 * col * P.H + h;
+    float2 x[kJoinNotes];
     float top = -INFINITY;
-    for (int i = lane; i < parts; i += 32) {
-        const float2 x = ml[(int64_t)(2 * i + (i == 0)) * P.H];
-        if (x.y != 0.0f)
-            top = fmaxf(top, x.x);
+#pragma unroll
+    for (int i = 0; i < kJoinNotes; i++) {
+        const int k = 32 * i + lane;
+        x[i] = k < parts ? ml[(int64_t)(2 * k + (k == 0)) * P.H] : make_float2(0.0f, 0.0f);
+        if (x[i].y != 0.0f)
+            top = fmaxf(top, x[i].x);
     }
     for (int o = 16; o > 0; o >>= 1)
         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
     float sum = 0.0f;
-    for (int i = lane; i < parts; i += 32) {
-        const float2 x = ml[(int64_t)(2 * i + (i == 0)) * P.H];
-        const float f = x.y == 0.0f ? 0.0f : exp2_fast(x.x - top);
-        factors[warp][i] = f;
-        sum += x.y == 0.0f ? 0.0f : x.y * f;
+#pragma unroll
+    for (int i = 0; i < kJoinNotes; i++) {
+        const float f = x[i].y == 0.0f ? 0.0f : exp2_fast(x[i].x - top);
+        factors[warp][32 * i + lane] = f;
+        sum += x[i].y == 0.0f ? 0.0f : x[i].y * f;
     }
     for (int o = 16; o > 0; o >>= 1)
         sum += __shfl_xor_sync(0xffffffffu, sum, o);
     __syncwarp();
-    if (threadIdx.x == 0) {
+    if (lane == 0 && (kSlices == 1 || warp == 0)) {
         const float lse = sum == 0.0f ? -INFINITY : top + log2f(sum);
         P.lse2[(int64_t)r * P.H + h] = lse;
         if (P.lse != nullptr)
             P.lse[r * P.lse_request_stride + h] = lse * 0.693147180559945309f;
     }
-    if (v >= P.V)
-        return;
-    float4 acc = {};
-    const float *part = P.part_o + ((int64_t)2 * col * P.H + h) * P.V + v;
+    float4 acc[kTake] = {};
+    const float *part = P.part_o + ((int64_t)2 * col * P.H + h) * P.V + v0;
     const int64_t step = (int64_t)P.H * P.V;
-#pragma unroll 8
+#pragma unroll(kSlices == 1 ? 2 : 20)
     for (int i = 0; i < parts; i++) {
         const float f = factors[warp][i];
-        const float4 x = __ldcs(reinterpret_cast<const float4 *>(part + (2 * i + (i == 0)) * step));
-        acc.x += x.x * f;
-        acc.y += x.y * f;
-        acc.z += x.z * f;
-        acc.w += x.w * f;
+#pragma unroll
+        for (int k = 0; k < kTake; k++)
+            if (v0 + 128 * k < P.V) {
+                const float4 y = __ldcs(reinterpret_cast<const float4 *>(part + (2 * i + (i == 0)) * step + 128 * k));
+                acc[k].x += y.x * f;
+                acc[k].y += y.y * f;
+                acc[k].z += y.z * f;
+                acc[k].w += y.w * f;
+            }
     }
     const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
-    uint16_t *to = P.out + r * P.out_request_stride + h * P.out_head_stride + v;
-    to[0] = to_out(acc.x * inv, P.q_bf16);
-    to[1] = to_out(acc.y * inv, P.q_bf16);
-    to[2] = to_out(acc.z * inv, P.q_bf16);
-    to[3] = to_out(acc.w * inv, P.q_bf16);
+    uint16_t *to = P.out + r * P.out_request_stride + h * P.out_head_stride + v0;
+#pragma unroll
+    for (int k = 0; k < kTake; k++, to += 128)
+        if (v0 + 128 * k < P.V) {
+            to[0] = to_out(acc[k].x * inv, P.q_bf16);
+            to[1] = to_out(acc[k].y * inv, P.q_bf16);
+            to[2] = to_out(acc[k].z * inv, P.q_bf16);
+            to[3] = to_out(acc[k].w * inv, P.q_bf16);
+        }
 }
 
 constexpr int kWeightThreads = 256;
@@ -1407,7 +1449,7 @@ int work_space(const lmc_layout *L, int32_t layer, int64_t R, int64_t H, int64_t
         at += (bytes + 255) / 256 * 256;
         return here;
     };
-    W.segment = take(2 * W.cols * 8);
+    W.segment = take(2 * W.cols * 16);
     W.part_ml = take(2 * W.cols * H * 8);
     W.part_o = take(2 * W.cols * H * V * 4);
     W.lse2 = take(R * H * 4);
@@ -1559,7 +1601,7 @@ extern "C" int lmc_attend(const lmc_layout *L, const lmc_entries *e, const void 
     P.weights = a->weights;
     P.weights_request_stride = a->weights_request_stride;
     uint8_t *ws = static_cast<uint8_t *>(workspace);
-    P.segment = reinterpret_cast<int2 *>(ws + W.segment);
+    P.segment = reinterpret_cast<int4 *>(ws + W.segment);
     P.part_ml = reinterpret_cast<float2 *>(ws + W.part_ml);
     P.part_o = reinterpret_cast<float *>(ws + W.part_o);
     P.lse2 = reinterpret_cast<float *>(ws + W.lse2);
@@ -1613,10 +1655,14 @@ extern "C" int lmc_attend(const lmc_layout *L, const lmc_entries *e, const void 
     if (!allow_shared_memory(fp8 ? 2 : bf16 ? 1 : 0, kern))
         return LMC_ERR_CUDA;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
+    // a warp per head fills the device from about eight warps an SM
+    const unsigned splits = (unsigned)std::min<int64_t>(P.cols, R);
+    const bool few = (int64_t)splits * H < 8 * (int64_t)sms;
     if (!follow(kern, dim3((unsigned)(P.cols * P.head_groups)), fp8 ? kThreads<true> : kThreads<false>, smem, s,
                 P) ||
-        !follow(lmc_attend_join_kernel, dim3((unsigned)std::min<int64_t>(P.cols, R), (unsigned)H), kJoinWarps * 32, 0,
-                s, P))
+        !(few ? follow(lmc_attend_join_kernel<4>, dim3(splits, (unsigned)H), kJoinWarps * 32, 0, s, P)
+              : follow(lmc_attend_join_kernel<1>, dim3(splits, (unsigned)((H + kJoinWarps - 1) / kJoinWarps)),
+                       kJoinWarps * 32, 0, s, P)))
         return LMC_ERR_CUDA;
     if (P.weights != nullptr) {
         const int64_t tokens = P.window > 0 ? std::min(P.max_length, P.window) : std::max(P.max_length, 1);

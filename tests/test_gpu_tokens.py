@@ -71,6 +71,28 @@ def test_append_writes_exactly_the_named_rows(lmc, status, E, cache, act, N, pac
         assert diff.numel() == 0
 
 
+@pytest.mark.parametrize("act", ["bf16", "f16"])
+def test_append_codes_of_every_value(lmc, status, act):
+    """All 65536 patterns of the rows' type under scales that are powers of
+    two, odd, near the ends of binary32 and with every significand bit set:
+    the code of the IEEE quotient each time."""
+    patterns = torch.arange(65536, dtype=torch.int32).to(torch.int16).view(T.TYPES[act]).view(128, 512).to(DEV)
+    L = lmc.lmc_layout_build([{"kind": "MLA", "token_bytes": 512}], 128, False, 128 * 512)
+    req, pos = _int32(np.zeros(128)), _int32(np.arange(128))
+    all_ones = float(np.uint32(0x3FFFFFFF).view(np.float32))
+    for scale in (1.0, 0.05, 0.0625, 3.0, 1 / 3, 448.0, 2.0 ** -90, 1.7e-31, 2.0 ** -126, 1e-42, 2.0 ** 99, 3e38,
+                  all_ones, all_ones * 2.0 ** -5, 0.0123):
+        pool = torch.full((L.pool_bytes,), 0x55, dtype=torch.uint8, device=DEV)
+        lmc.lmc_append(L, 0, pool, _int32([[0]]), req, pos, patterns, status, scale=scale)
+        s = torch.tensor(scale, dtype=torch.float32, device=DEV)
+        want = (patterns.float() / s).clamp(-448, 448).to(torch.float8_e4m3fn).view(torch.uint8)
+        got = pool.view(128, 512)
+        nan = torch.isnan(patterns.float())
+        assert torch.equal(got[~nan], want[~nan]), scale
+        assert ((got[nan] & 0x7F) == 0x7F).all()
+    assert status.item() == 0
+
+
 def test_append_skips_bad_rows_with_status(lmc, status):
     M = T.Model(lmc, 32, "bf16", 4, layers=1, blocks=3)
     table = _int32([[0, -1], [99, 1]])
