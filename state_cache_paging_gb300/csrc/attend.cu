@@ -12,7 +12,7 @@
 // (576 values, 512 of them the value): 60 at 32 heads, 121 at 64. The copy
 // rate allows 270 per byte at the dense tensor rate, so the call is bound by
 // HBM, and the tensor cores have to run beside the loads. CUDA cores cannot
-// (4.3 ms against 45 us for 32 requests of 8192 tokens).
+// (6.3 ms for 32 requests of 8192 tokens; the copy rate's floor is 45 us).
 //
 // Split. The cache is cut into tiles of up to 64 tokens of one page; all
 // requests' tiles in a row are shared out evenly over the CTAs (one per SM),
@@ -35,8 +35,9 @@
 // as bf16 or f16 (the entries' type; f16 for an fp8 cache): the only rounding
 // below 32 bits on the way, at most half a step of p (2^-8 bf16, 2^-11 f16)
 // per token. l is summed from p before it is rounded. The reference m only
-// moves when a logit exceeds it by 8 (p up to 2^8 fits either type), so O is
-// rarely rescaled.
+// moves when a logit exceeds it by 8, so O is rarely rescaled; p is at most 2^8
+// then, or, as f16, 2^15: there it is lifted by 2^7, so that the many small
+// weights of a long cache stay above f16's smallest values.
 //
 // Entries of 16 bits come by TMA: a tensor map over (values, page rows,
 // blocks) needs no address arithmetic, and rows past a page's end read as
@@ -49,10 +50,9 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstdint>
-#include <mutex>
-#include <vector>
 
 #include "lmc_internal.h"
 
@@ -71,23 +71,11 @@ constexpr int kValueWarp = 9;          // issues O^T += V^T P^T
 constexpr int kFirstLoader = 10;       // 16-bit entries: one warp
 constexpr int kFirstFp8Loader = 12;    // fp8: eight, two whole warpgroups
 constexpr int kFp8Loaders = 8;        // warps, eight of a tile's rows each
-#ifndef LMC_AHEAD
-#define LMC_AHEAD 2
-#endif
-constexpr int kAhead = LMC_AHEAD;     // tiles
-#ifndef LMC_FP8_AHEAD
-#define LMC_FP8_AHEAD 2
-#endif
-constexpr int kFp8Ahead = LMC_FP8_AHEAD;
-#ifndef LMC_EARLYP
-#define LMC_EARLYP 5
-#endif
-#ifndef LMC_SOFT
-#define LMC_SOFT 80
-#endif
-#ifndef LMC_LOADR
-#define LMC_LOADR 136
-#endif
+constexpr int kAhead = 2;             // tiles sent on to L2 ahead of their copy (90 -> 87 us when measured; 3: 89)
+constexpr int kEarlyPanels = 5;       // of an fp8 tile, widened before its stage is free (6: the same, 8: 126 -> 133 us)
+// Registers per thread of an fp8 CTA's warpgroups; 2 x 80 + 40 + 2 x 136 of the
+// 5 x 96 it starts with. (64 / 152 with all panels early: 137 us, 80 / 136: 190.)
+constexpr int kSoftRegisters = 80, kIssueRegisters = 40, kLoadRegisters = 136;
 template <bool kFp8>
 constexpr int kThreads = (kFp8 ? kFirstFp8Loader + kFp8Loaders : kFirstLoader + 1) * 32;
 constexpr float kLag = 8.0f;          // how far (log2) a logit may exceed the reference
@@ -687,7 +675,7 @@ __device__ __forceinline__ void load_fp8(const AttendPlan &P, Control &C, const 
     uint32_t bad = 0, n = 0, segments = 0;
     if (warp == 0 && elect())
         asm volatile("prefetch.tensormap [%0];" ::"l"(&P.query) : "memory");
-    constexpr int kEarly = LMC_EARLYP;  // panels
+    constexpr int kEarly = kEarlyPanels;
     uint4 codes[kPanels];
     uint32_t wide[kEarly][8];
     uint64_t valid = 0, next_valid = 0;
@@ -741,7 +729,7 @@ __device__ __forceinline__ void load_fp8(const AttendPlan &P, Control &C, const 
 
     while (W.next(P)) {
 #pragma unroll 1
-        for (int j = 1; j < kFp8Ahead; j++)
+        for (int j = 1; j < kAhead; j++)
             prefetch(j);
         // a turn stores tile j and loads tile j + 1
 #pragma unroll 1
@@ -759,7 +747,7 @@ __device__ __forceinline__ void load_fp8(const AttendPlan &P, Control &C, const 
                     load(i);
             }
             if (store) {
-                prefetch(j + kFp8Ahead);
+                prefetch(j + kAhead);
                 const int st = n % P.stages;
                 if (n >= (uint32_t)P.stages)
                     bar_wait(C, &C.kv_free[st], (n / P.stages - 1) & 1, P.status);
@@ -953,6 +941,7 @@ __device__ __forceinline__ void soften(const AttendPlan &P, Control &C, const Me
     const bool active = quarter * 16 < P.padded_heads;
     const int head0 = group * P.group_heads;
     const int heads = min(P.group_heads, P.H - head0);
+    constexpr float kLift = kBf16 ? 0.0f : 7.0f;  // log2 of p's factor
     uint32_t n = 0;
     int4 left[2] = {make_int4(-1, 0, 0, 0), make_int4(-1, 0, 0, 0)};  // what the CTA leaves unfinished
     uint8_t *const pa = M.p + ra * 128 + 4 * (lane & 3), *const pb = M.p + rb * 128 + 4 * (lane & 3);
@@ -1077,7 +1066,7 @@ __device__ __forceinline__ void soften(const AttendPlan &P, Control &C, const Me
             if (n > 0)
                 bar_wait(C, &C.pv_done, (n - 1) & 1, P.status);
             if (active) {
-                const float na = ma == -INFINITY ? 0.0f : ma, nb = mb == -INFINITY ? 0.0f : mb;
+                const float na = ma == -INFINITY ? 0.0f : ma - kLift, nb = mb == -INFINITY ? 0.0f : mb - kLift;
                 const int x = ra & 7;  // rb & 7 is the same
 #pragma unroll
                 for (int i = 0; i < 4; i++) {
@@ -1122,7 +1111,7 @@ __device__ __forceinline__ void soften(const AttendPlan &P, Control &C, const Me
 #pragma unroll
             for (int k = 0; k < 2; k++) {
                 const int row = k ? rb : ra;
-                const float m0 = k ? mb : ma, m = m0 == -INFINITY ? 0.0f : m0;
+                const float m0 = k ? mb : ma, m = m0 == -INFINITY ? 0.0f : m0 - kLift;
                 const float l = (k ? lb : la) + C.half[1][row];
                 C.inverse[row] = whole ? (l == 0.0f ? 0.0f : P.scale / l) : P.scale;
                 if (row >= heads)
@@ -1226,16 +1215,14 @@ __global__ void __launch_bounds__(kThreads<kFp8>, 1) lmc_attend_kernel(const __g
     W.init(P, col);
     if (warp < kSoftWarps) {
         if (kFp8)
-            asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(LMC_SOFT));
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kSoftRegisters));
         soften<kBf16, kFp8>(P, C, M, W, col, group);
     } else if (kFp8 && warp >= kFirstFp8Loader) {
-        // registers for a tile as f16 and the next one's codes, from the other
-        // warpgroups: 2 x 80 + 40 + 2 x 136 of 5 x 96
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(LMC_LOADR));
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kLoadRegisters));
         load_fp8(P, C, M, W, group);
     } else {
         if (kFp8)
-            asm volatile("setmaxnreg.dec.sync.aligned.u32 40;");
+            asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegisters));
         if (warp == kScoreWarp)
             multiply_scores<kBf16>(P, C, M, W);
         else if (warp == kValueWarp)
@@ -1501,20 +1488,17 @@ bool tensor_map(CUtensorMap *map, bool bf16, const void *base, int64_t values, i
 // Lets the attention kernels take a whole SM's shared memory (once per kernel
 // and device: the call costs as much as a launch).
 bool allow_shared_memory(int which, void (*kern)(AttendPlan)) {
-    static std::mutex mu;
-    static std::vector<int> done[3];
+    static std::atomic<bool> done[3][64];
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess)
         return false;
-    std::lock_guard<std::mutex> lock(mu);
-    if ((int)done[which].size() <= dev)
-        done[which].resize(dev + 1, 0);
-    if (!done[which][dev]) {
-        if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                 kSmemLimit - (int)((sizeof(Control) + 1023) / 1024 * 1024)) != cudaSuccess)
-            return false;
-        done[which][dev] = 1;
-    }
+    if (dev < 64 && done[which][dev].load(std::memory_order_acquire))
+        return true;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             kSmemLimit - (int)((sizeof(Control) + 1023) / 1024 * 1024)) != cudaSuccess)
+        return false;
+    if (dev < 64)
+        done[which][dev].store(true, std::memory_order_release);
     return true;
 }
 

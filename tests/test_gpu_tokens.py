@@ -172,6 +172,9 @@ CASES = [
     (80, 72, 5, "bf16", "bf16", 1, False, 0, [1, 2, 9, 0]),
     (16, 8, 3, "f16", "f16", 2, True, 0, [1, 2, 3, 30]),
     (64, 64, 64, "e4m3", "bf16", 1000, False, 0, [999, 64, 1]),
+    (192, 128, 8, "bf16", "bf16", 75, True, 151, [150, 151, 400, 77]),   # whole tiles that begin on odd tokens
+    (576, 512, 48, "e4m3", "f16", 8, False, 0, [7, 8, 9, 70]),           # eight pages in a tile
+    (128, 128, 130, "bf16", "bf16", 40, True, 0, [40, 41, 300]),         # three groups of heads, one of them short
 ]
 
 
@@ -245,6 +248,40 @@ def test_attend_peaked_growing_and_flat_logits(lmc, status, softmax_scale, shift
     out, lse, ss = _attend(lmc, M, 0, table, [n], q, V, status, softmax_scale=softmax_scale)
     assert status.item() == 0
     _check_attend(M, 0, table, [n], q, V, 1.0, ss, out, lse, "bf16")
+
+
+def test_attend_one_large_weight_among_many_small(lmc, status):
+    """A first token that outweighs each of the others by 2^24 and 2^30, all of
+    them together by a factor of 2^9 and less: in f16 the small weights must
+    not be lost (they are lifted), whatever the order."""
+    rng = np.random.default_rng(4)
+    N, E, V, H, n = 64, 64, 64, 16, 40_000
+    blocks = -(-n // N)
+    for where in (0, n // 2, n - 1):
+        M = T.Model(lmc, E, "f16", N, blocks=blocks)
+        table = T.tables([n], N, blocks, rng)
+        e = rng.standard_normal((n, E)) * 0.01
+        e[:, 0], e[:, 1] = 0.0, 1.0   # the second value is 1 for all but the large one
+        e[where, 0], e[where, 1] = 16.0, 0.0
+        pages = M.pages(0)
+        flat = torch.from_numpy(e).to(torch.float16).view(torch.uint8)
+        pad = torch.zeros((blocks * N, E * 2), dtype=torch.uint8)
+        pad[:n] = flat
+        pages[table[0].long()] = pad.view(blocks, N, E * 2)
+        q = torch.zeros((1, H, E), dtype=torch.float16, device=DEV)
+        q[:, :8, 0] = 24 * math.log(2) / 16
+        q[:, 8:, 0] = 30 * math.log(2) / 16
+        out, lse, ss = _attend(lmc, M, 0, table, [n], q, V, status, softmax_scale=1.0)
+        assert status.item() == 0
+        # the others' share of the weight, by their second value
+        for h in (0, 8):
+            bits = float(q[0, h, 0]) * 16 / math.log(2)  # as f16 holds q
+            share = (n - 1) / (n - 1 + 2.0 ** bits)
+            got = float(out[0, h, 1])
+            # p of the small ones is 2^(7 - bits) where the large one comes first: f16's half step is 2^-25 there;
+            # the output's is 2^-11 of it, or 2^-25 where it is not normal
+            slack = share * (2.0 ** -25 / 2.0 ** (7 - bits) + 2.0 ** -10) + 2.0 ** -24
+            assert abs(got - share) <= slack, (where, bits, got, share)
 
 
 @pytest.mark.parametrize("cache", ["bf16", "e4m3"])
