@@ -634,3 +634,14 @@ def test_serving_loop_captured_and_replayed(lmc, status):
     for x, y in zip(a["outs"], b["outs"]):
         for u, v in zip(x, y):
             assert torch.equal(u, v)
+
+
+def test_decode_example_runs():
+    """The decode example (tests/example_decode.py, also printed in the README)
+    runs as written. Each step adds one unit of weight per head; the last 64
+    of 1203 tokens are kept."""
+    import example_decode
+    got = example_decode.run(DEV)
+    assert got["status"] == 0 and got["finite"] and got["kept_length"] == 256
+    assert all(abs(w - 3 * 32) <= 3 * 32 * 1e-4 for w in got["weight"])
+    assert got["kept"][192:] == list(range(1203 - 64, 1203)) and got["kept"] == sorted(set(got["kept"]))
