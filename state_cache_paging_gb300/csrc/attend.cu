@@ -207,17 +207,17 @@ struct Walk {
     }
 
     __device__ __forceinline__ void init(const AttendPlan &P, int col) {
+        r0 = 0;
+        load(P, 0);
         int total = 0;
-        for (int i = threadIdx.x & 31; i < P.R; i += 32)
+        for (int i = 32 + (threadIdx.x & 31); i < P.R; i += 32)
             total += tiles_of(P, range_of(P, i));
-        total = __reduce_add_sync(0xffffffffu, total);
+        total = __reduce_add_sync(0xffffffffu, total) + __shfl_sync(0xffffffffu, stop, 31);
         // equal shares, so only the last CTAs may have none (in 64 bits: a
         // share times a CTA's number may pass the total)
         const int64_t each = (total + P.cols - 1) / P.cols;
         pos = (int)min(col * each, (int64_t)total);
         end = (int)min(pos + each, (int64_t)total);
-        r0 = 0;
-        load(P, 0);
     }
 
     __device__ __forceinline__ bool next(const AttendPlan &P) {
@@ -463,7 +463,8 @@ __device__ __forceinline__ float from_q(uint32_t h, bool bf16) {
 
 // Kernels of this file are launched so that each may start while the one
 // before it in the stream still runs. The first waits for that one to be done
-// and its writes to be seen; nothing in global memory is touched before it.
+// and its writes to be seen; nothing in global memory is touched before it
+// (the tensor maps are the kernel's own arguments).
 // The second lets the next one be brought in (the short kernels do; blocks
 // that only wait slow the long one down: 161 -> 173 us at four fp8 requests of
 // 131072 tokens).
@@ -528,10 +529,6 @@ __device__ __forceinline__ void load_by_tma(const AttendPlan &P, Control &C, con
     const int lane = threadIdx.x & 31;
     uint32_t bad = 0, n = 0, segments = 0;
     LastPage last, last_ahead;
-    if (elect()) {
-        asm volatile("prefetch.tensormap [%0];" ::"l"(&P.cache) : "memory");
-        asm volatile("prefetch.tensormap [%0];" ::"l"(&P.query) : "memory");
-    }
     while (W.next(P)) {
         const int row_panels = (P.E + 63) / 64;
         for (int j = 0; j < W.count; j++, n++) {
@@ -673,8 +670,6 @@ __device__ __forceinline__ void load_fp8(const AttendPlan &P, Control &C, const 
     const int chunks = P.E / 16;  // of an entry
     const uint32_t at0 = row * 128 + (((2 * piece) ^ (row & 7)) << 4), at1 = row * 128 + (((2 * piece + 1) ^ (row & 7)) << 4);
     uint32_t bad = 0, n = 0, segments = 0;
-    if (warp == 0 && elect())
-        asm volatile("prefetch.tensormap [%0];" ::"l"(&P.query) : "memory");
     constexpr int kEarly = kEarlyPanels;
     uint4 codes[kPanels];
     uint32_t wide[kEarly][8];
@@ -1182,6 +1177,11 @@ __global__ void __launch_bounds__(kThreads<kFp8>, 1) lmc_attend_kernel(const __g
     M.stage_bytes = P.panels * kPanel;
     M.kv = M.q + (size_t)((P.E + 63) / 64) * P.padded_heads * 128;
     M.p = M.kv + (size_t)P.stages * M.stage_bytes;
+    if (threadIdx.x == 32) {
+        asm volatile("prefetch.tensormap [%0];" ::"l"(&P.query) : "memory");
+        if (!kFp8)
+            asm volatile("prefetch.tensormap [%0];" ::"l"(&P.cache) : "memory");
+    }
     if (threadIdx.x == 0) {
         bar_init(&C.q_full, kFp8 ? kFp8Loaders : 1);
         bar_init(&C.q_raw, 1);
@@ -1244,24 +1244,29 @@ __global__ void __launch_bounds__(kThreads<kFp8>, 1) lmc_attend_kernel(const __g
 
 // ---- joining -------------------------------------------------------------------
 
-constexpr int kJoinWarps = 4;
+// Warps of a joining block: a head each, or all of them one head: four take a
+// quarter of its values each, four times, for every fourth part.
+template <int kSlices>
+constexpr int kJoinWarps = kSlices == 1 ? 4 : 16;
 constexpr int kJoinNotes = kMaxCols / 32;  // per lane
 
 // Block (x, y): joins heads of the x-th request that spans several CTAs (each
 // begins in a CTA of its own, so there are at most as many as requests and
-// CTAs). A warp joins a head, or (kSlices = 4) a quarter of its values. What
-// bounds it is latency, so it makes three trips to memory: all CTAs' notes,
-// the parts' factors, the parts. (Looking for the request in a loop over the
-// notes and reading its length again took 14.5 us for 152 requests of 32 heads,
-// four warps to a head in every case 12 us; with few heads to join, one warp to
-// a head leaves the device idle.)
+// CTAs). A warp joins a head, or (kSlices = 4) a quarter of its values and of
+// its parts. What bounds it is latency, so it makes three trips to memory: all
+// CTAs' notes, the parts' factors, the parts. (Looking for the request in a
+// loop over the notes and reading its length again took 14.5 us for 152
+// requests of 32 heads, four warps to a head in every case 12 us; with few
+// heads to join, one warp to a head leaves the device idle.)
 template <int kSlices>
-__global__ void __launch_bounds__(kJoinWarps * 32) lmc_attend_join_kernel(const __grid_constant__ AttendPlan P) {
+__global__ void __launch_bounds__(kJoinWarps<kSlices> * 32) lmc_attend_join_kernel(const __grid_constant__ AttendPlan P) {
     constexpr int kTake = kMaxValue / 128 / kSlices;  // float4s per lane
-    __shared__ float factors[kJoinWarps][kMaxCols];
+    constexpr int kShare = kSlices == 1 ? 1 : 4;      // a warp takes every kShare-th part
+    __shared__ float factors[kJoinWarps<kSlices>][kMaxCols];
+    __shared__ float4 shares[kShare][kShare == 1 ? 1 : kMaxValue / 4];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int h = kSlices == 1 ? blockIdx.y * kJoinWarps + warp : blockIdx.y;
-    const int v0 = 4 * lane + (kSlices == 1 ? 0 : 128 * warp);
+    const int h = kSlices == 1 ? blockIdx.y * kJoinWarps<1> + warp : blockIdx.y;
+    const int v0 = 4 * lane + (kSlices == 1 ? 0 : 128 * (warp & 3)), share = kSlices == 1 ? 0 : warp >> 2;
     wait_for_launch();
     let_next_start();
     if (h >= P.H)
@@ -1337,8 +1342,8 @@ __global__ void __launch_bounds__(kJoinWarps * 32) lmc_attend_join_kernel(const 
     float4 acc[kTake] = {};
     const float *part = P.part_o + ((int64_t)2 * col * P.H + h) * P.V + v0;
     const int64_t step = (int64_t)P.H * P.V;
-#pragma unroll(kSlices == 1 ? 2 : 20)
-    for (int i = 0; i < parts; i++) {
+#pragma unroll(kSlices == 1 ? 2 : 10)
+    for (int i = share; i < parts; i += kShare) {
         const float f = factors[warp][i];
 #pragma unroll
         for (int k = 0; k < kTake; k++)
@@ -1349,6 +1354,19 @@ __global__ void __launch_bounds__(kJoinWarps * 32) lmc_attend_join_kernel(const 
                 acc[k].z += y.z * f;
                 acc[k].w += y.w * f;
             }
+    }
+    if constexpr (kShare > 1) {
+        shares[share][v0 / 4] = acc[0];
+        __syncthreads();
+        if (share > 0)
+            return;
+        for (int k = 1; k < kShare; k++) {
+            const float4 y = shares[k][v0 / 4];
+            acc[0].x += y.x;
+            acc[0].y += y.y;
+            acc[0].z += y.z;
+            acc[0].w += y.w;
+        }
     }
     const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
     uint16_t *to = P.out + r * P.out_request_stride + h * P.out_head_stride + v0;
@@ -1639,14 +1657,17 @@ extern "C" int lmc_attend(const lmc_layout *L, const lmc_entries *e, const void 
     if (!allow_shared_memory(fp8 ? 2 : bf16 ? 1 : 0, kern))
         return LMC_ERR_CUDA;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    // a warp per head fills the device from about eight warps an SM
+    // A warp per head where that is a few warps an SM; else a request has many
+    // parts and the heads are few (4 x 131072 tokens, 64 heads: 38 parts each,
+    // 12 us by a warp per head, 6 us by sixteen; 32 requests of 32 heads, 5
+    // parts each: 12 us by sixteen).
     const unsigned splits = (unsigned)std::min<int64_t>(P.cols, R);
-    const bool few = (int64_t)splits * H < 8 * (int64_t)sms;
+    const bool few = (int64_t)splits * H < 4 * (int64_t)sms;
     if (!follow(kern, dim3((unsigned)(P.cols * P.head_groups)), fp8 ? kThreads<true> : kThreads<false>, smem, s,
                 P) ||
-        !(few ? follow(lmc_attend_join_kernel<4>, dim3(splits, (unsigned)H), kJoinWarps * 32, 0, s, P)
-              : follow(lmc_attend_join_kernel<1>, dim3(splits, (unsigned)((H + kJoinWarps - 1) / kJoinWarps)),
-                       kJoinWarps * 32, 0, s, P)))
+        !(few ? follow(lmc_attend_join_kernel<4>, dim3(splits, (unsigned)H), kJoinWarps<4> * 32, 0, s, P)
+              : follow(lmc_attend_join_kernel<1>, dim3(splits, (unsigned)((H + kJoinWarps<1> - 1) / kJoinWarps<1>)),
+                       kJoinWarps<1> * 32, 0, s, P)))
         return LMC_ERR_CUDA;
     if (P.weights != nullptr) {
         const int64_t tokens = P.window > 0 ? std::min(P.max_length, P.window) : std::max(P.max_length, 1);

@@ -476,9 +476,12 @@ __global__ void __launch_bounds__(kSelThreads, kSelPerSm) lmc_select_kernel(cons
         }
         cluster.sync();  // also a barrier of this CTA
         if (tid < 256) {
+            // (all CTAs' reads in flight at once)
             uint32_t sum = 0;
-            for (int c = 0; c < P.cluster; c++)
-                sum += cluster.map_shared_rank(&S.totals[buf][0], c)[tid];
+#pragma unroll
+            for (int c = 0; c < kSelMaxCluster; c++)
+                if (c < P.cluster)
+                    sum += cluster.map_shared_rank(&S.totals[buf][0], c)[tid];
             S.all[tid] = sum;
         }
         __syncthreads();
@@ -565,11 +568,13 @@ __global__ void __launch_bounds__(kSelThreads, kSelPerSm) lmc_select_kernel(cons
     }
     cluster.sync();
     uint32_t a_before = S.warp_above[warp], e_before = S.warp_equal[warp];
-    for (int c = 0; c < rank; c++) {
-        const uint32_t *other = cluster.map_shared_rank(&S.counts[0], c);
-        a_before += other[0];
-        e_before += other[1];
-    }
+#pragma unroll
+    for (int c = 0; c < kSelMaxCluster - 1; c++)
+        if (c < rank) {
+            const uint32_t *other = cluster.map_shared_rank(&S.counts[0], c);
+            a_before += other[0];
+            e_before += other[1];
+        }
     const uint32_t lanes_below = (1u << lane) - 1u;
     for (int32_t i0 = w0; i0 < w1; i0 += 32) {
         const int32_t i = i0 + lane;

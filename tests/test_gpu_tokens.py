@@ -346,6 +346,56 @@ def test_attend_strides_untouched_bytes_and_side_stream(lmc, status):
     assert torch.equal(pool.cpu(), M.pool)
 
 
+def test_attend_on_two_streams_beside_matrix_products(lmc, status):
+    """Two batches at once on two streams, each with its own workspace, while
+    a third stream multiplies matrices: the same bits as one after the other."""
+    rng = np.random.default_rng(12)
+    N, E, V, H = 64, 192, 128, 24
+    jobs = []
+    for cache, lengths in (("bf16", [3000, 17, 900]), ("e4m3", [2500, 64, 1, 0])):
+        blocks = sum(-(-n // N) for n in lengths)
+        M = T.Model(lmc, E, cache, N, blocks=blocks)
+        raw = torch.from_numpy(rng.standard_normal((blocks, N, E)).astype(np.float32)).to(T.TYPES[cache])
+        M.pages(0).copy_(raw.view(torch.uint8))
+        table = T.tables(lengths, N, blocks, rng).to(DEV)
+        q = torch.from_numpy(rng.standard_normal((len(lengths), H, E))).to(torch.bfloat16).to(DEV)
+        n = lmc.lmc_attend_workspace(M.layout, 0, len(lengths), H, V, 3000, True)
+        jobs.append((M, M.pool.to(DEV), table, _int32(lengths), q, torch.empty(n, dtype=torch.uint8, device=DEV)))
+
+    def call(job, out, lse, weights, stream=None):
+        M, pool, table, lengths, q, ws = job
+        lmc.lmc_attend(M.layout, 0, pool, table, lengths, q, V, 0.1, out, ws, status, max_length=3000, lse=lse,
+                       weights=weights, stream=stream)
+
+    def buffers(job):
+        R = job[4].shape[0]
+        return (torch.empty((R, H, V), dtype=torch.bfloat16, device=DEV), torch.empty((R, H), device=DEV),
+                torch.zeros((R, 3000), device=DEV))
+
+    want = [buffers(j) for j in jobs]
+    for j, w in zip(jobs, want):
+        call(j, *w)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    a = torch.randn((2048, 2048), device=DEV).bfloat16()
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(10):
+        with torch.cuda.stream(streams[2]):
+            for _ in range(4):
+                a @ a
+        for j, s in zip(jobs, streams):
+            g = buffers(j)
+            s.wait_stream(torch.cuda.current_stream())
+            call(j, *g, stream=s)
+            got.append((j, g))
+    torch.cuda.synchronize()
+    assert status.item() == 0
+    for j, g in got:
+        for x, y in zip(g, want[0] if j is jobs[0] else want[1]):
+            assert torch.equal(x.view(torch.uint8), y.view(torch.uint8))
+
+
 def test_attend_values_that_are_not_finite_reach_the_result(lmc, status):
     """An infinity or NaN in a token that is attended shows in the output, as
     in the plain softmax; one behind the length or before the window does not."""
