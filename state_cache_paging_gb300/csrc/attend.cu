@@ -68,16 +68,22 @@ constexpr int kMaxCols = 160;         // CTAs along the cache's length (an SM ea
 constexpr int kSoftWarps = 8;
 constexpr int kScoreWarp = 8;          // issues S = Q K^T
 constexpr int kValueWarp = 9;          // issues O^T += V^T P^T
-constexpr int kFirstLoader = 10;       // 16-bit entries: one warp
+constexpr int kAheadWarp = 10;         // sends tiles to come on to L2
+constexpr int kLoaderWarp = 11;        // 16-bit entries: one warp
 constexpr int kFirstFp8Loader = 12;    // fp8: eight, two whole warpgroups
 constexpr int kFp8Loaders = 8;        // warps, eight of a tile's rows each
-constexpr int kAhead = 2;             // tiles sent on to L2 ahead of their copy (90 -> 87 us when measured; 3: 89)
+// Tiles sent on to L2 before their copy is issued. Measured at 32 x 8192 tokens
+// and at 256 windows of 4096: none 66.8 / 177 us, one 62.4 / 165, two 63.5 /
+// 166, three 67.5 / 177, five 81 / 224 (they are gone again when they are
+// wanted).
+constexpr int kAhead = 1;
+constexpr int kNap = 300;             // ns between looks at the loaders' progress (100: the same, 800: 63.8 / 169 us)
 constexpr int kEarlyPanels = 5;       // of an fp8 tile, widened before its stage is free (6: the same, 8: 126 -> 133 us)
-// Registers per thread of an fp8 CTA's warpgroups; 2 x 80 + 40 + 2 x 136 of the
-// 5 x 96 it starts with. (64 / 152 with all panels early: 137 us, 80 / 136: 190.)
-constexpr int kSoftRegisters = 80, kIssueRegisters = 40, kLoadRegisters = 136;
+// Registers per thread of an fp8 CTA's warpgroups: 2 x 80 + 56 + 2 x 128 of the
+// 5 x 96 it starts with (fewer for the softmax or the loaders spill).
+constexpr int kSoftRegisters = 80, kIssueRegisters = 56, kLoadRegisters = 128;
 template <bool kFp8>
-constexpr int kThreads = (kFp8 ? kFirstFp8Loader + kFp8Loaders : kFirstLoader + 1) * 32;
+constexpr int kThreads = (kFp8 ? kFirstFp8Loader + kFp8Loaders : kLoaderWarp + 1) * 32;
 constexpr float kLag = 8.0f;          // how far (log2) a logit may exceed the reference
 constexpr uint32_t kWaitLimit = 1u << 22;
 constexpr int kSmemLimit = 227 * 1024;
@@ -93,6 +99,7 @@ struct Control {
     uint64_t zero[2 * kMaxStages];   // and those to be cleared before they are values
     uint32_t tmem;
     uint32_t gave_up;            // a wait ran out: nothing waits any more
+    int32_t loading;             // the tile whose load was issued last
     float factor[kMaxHeads];     // rescaling of a head's O
     float half[2][kMaxHeads];    // a head's maximum or sum in each half of the tokens
     alignas(16) float inverse[kMaxHeads];  // 1 / l
@@ -361,12 +368,6 @@ __device__ __forceinline__ void tma_box(const CUtensorMap *map, void *dst, int x
         : "memory");
 }
 
-__device__ __forceinline__ void tma_prefetch(const CUtensorMap *map, int x, int y, int w) {
-    asm volatile("cp.async.bulk.prefetch.tensor.4d.L2.global.tile [%0, {%1, %2, %3, %4}];" ::"l"(map), "r"(x), "r"(y),
-                 "r"(0), "r"(w)
-                 : "memory");
-}
-
 // Shared-memory matrix descriptor: 128-byte swizzle, 8-row groups `stride`
 // bytes apart, and (where the summed axis is not the contiguous one) 64-value
 // blocks of the other axis `leading` bytes apart.
@@ -528,7 +529,7 @@ __device__ __forceinline__ int resolve(const AttendPlan &P, const Walk &W, const
 __device__ __forceinline__ void load_by_tma(const AttendPlan &P, Control &C, const Memory &M, Walk &W, int group) {
     const int lane = threadIdx.x & 31;
     uint32_t bad = 0, n = 0, segments = 0;
-    LastPage last, last_ahead;
+    LastPage last;
     while (W.next(P)) {
         const int row_panels = (P.E + 63) / 64;
         for (int j = 0; j < W.count; j++, n++) {
@@ -570,6 +571,8 @@ __device__ __forceinline__ void load_by_tma(const AttendPlan &P, Control &C, con
                 }
             }
             __syncwarp();
+            if (lane == 0)
+                *(volatile int32_t *)&C.loading = (int)n;
             if (j == 0) {  // the queries second: their place is free later than the first tile's
                 const int r = (int)uniform(W.r);
                 if (segments > 0)
@@ -582,20 +585,6 @@ __device__ __forceinline__ void load_by_tma(const AttendPlan &P, Control &C, con
                 }
                 __syncwarp();
                 segments++;
-            }
-            if (j + kAhead < W.count) {
-                const Tile A = tile_at(P, W.first + j + kAhead);
-                uint64_t unused;
-                uint32_t later = 0;  // raised when the tile itself is loaded
-                const int ahead = resolve(P, W, A, unused, later, last_ahead);
-                const int arow = (int)uniform(A.row0);
-                for (int k = 0; k < P.pages_per_tile; k++) {
-                    const int b = __shfl_sync(0xffffffffu, ahead, k);
-                    if (b >= 0 && elect())
-                        for (int i = 0; i < P.cache_copies; i++)
-                            tma_prefetch(&P.cache, i * 64, arow, b);
-                    __syncwarp();
-                }
             }
         }
     }
@@ -675,30 +664,17 @@ __device__ __forceinline__ void load_fp8(const AttendPlan &P, Control &C, const 
     uint32_t wide[kEarly][8];
     uint64_t valid = 0, next_valid = 0;
     const uint8_t *src = nullptr;  // the next tile's codes
-    LastPage last, last_ahead;
+    LastPage last;
     const int my_page = P.pages_per_tile == 1 ? 0 : row / P.block_size;
     const int my_row = row - my_page * P.block_size;
 
-    // a tile of one page is a run of bytes: sent on its way to L2
-    auto prefetch = [&](int j) {
-        if (warp == 0 && P.pages_per_tile == 1 && j < W.count) {
-            const Tile A = tile_at(P, W.first + j);
-            uint64_t unused;
-            uint32_t later = 0;  // raised when the tile itself is loaded
-            const int64_t ahead = resolve(P, W, A, unused, later, last_ahead);
-            if (ahead >= 0 && elect())
-                asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(
-                                 P.pool + ahead * P.block_stride + (int64_t)A.row0 * P.token_bytes),
-                             "r"(A.rows * P.token_bytes)
-                             : "memory");
-            __syncwarp();
-        }
-    };
     auto find = [&](int j) {
         const Tile T = tile_at(P, W.first + j);
         const int block = resolve(P, W, T, next_valid, bad, last);
         const int64_t b = __shfl_sync(0xffffffffu, block, my_page & 31);
         src = P.pool + b * P.block_stride + (int64_t)(T.row0 + my_row) * P.token_bytes + piece * 16;
+        if (warp == 0 && lane == 0)
+            *(volatile int32_t *)&C.loading = (int)n + (j > 0);
     };
     auto load = [&](int i) {
         codes[i] = make_uint4(0, 0, 0, 0);
@@ -723,9 +699,6 @@ __device__ __forceinline__ void load_fp8(const AttendPlan &P, Control &C, const 
     };
 
     while (W.next(P)) {
-#pragma unroll 1
-        for (int j = 1; j < kAhead; j++)
-            prefetch(j);
         // a turn stores tile j and loads tile j + 1
 #pragma unroll 1
         for (int j = -1; j < W.count; j++) {
@@ -742,7 +715,6 @@ __device__ __forceinline__ void load_fp8(const AttendPlan &P, Control &C, const 
                     load(i);
             }
             if (store) {
-                prefetch(j + kAhead);
                 const int st = n % P.stages;
                 if (n >= (uint32_t)P.stages)
                     bar_wait(C, &C.kv_free[st], (n / P.stages - 1) & 1, P.status);
@@ -797,6 +769,39 @@ __device__ __forceinline__ void load_fp8(const AttendPlan &P, Control &C, const 
     // a CTA that gave up leaves no copy of its own in flight
     if (warp == 0 && *(volatile uint32_t *)&C.gave_up)
         for (uint32_t i = 0; segments > 0 && i < kWaitLimit && !bar_try(&C.q_raw, (segments - 1) & 1); i++) {
+        }
+}
+
+// One warp: sends tiles on to L2, kAhead of them before they are loaded (the
+// two stages hold too little to cover the latency of HBM), over the ends of
+// requests too. A page's rows are one run of bytes. It goes by the loaders'
+// progress, but nothing waits for it.
+__device__ __forceinline__ void send_ahead(const AttendPlan &P, Control &C, Walk &W) {
+    uint32_t unused = 0;  // bad pages are raised when they are loaded
+    uint64_t valid;
+    LastPage last;
+    int n = 0;
+    while (W.next(P))
+        for (int j = 0; j < W.count; j++, n++) {
+            if (n < P.stages)
+                continue;  // loaded at once
+            for (uint32_t k = 0; k < kWaitLimit; k++) {
+                if ((int)uniform(*(volatile uint32_t *)&C.loading) >= n - kAhead)
+                    break;
+                if (uniform(*(volatile uint32_t *)&C.gave_up))
+                    return;
+                __nanosleep(kNap);
+            }
+            const Tile T = tile_at(P, W.first + j);
+            const int block = resolve(P, W, T, valid, unused, last);
+            const int rows = P.pages_per_tile == 1 ? T.rows : P.block_size;
+            const bool mine = (threadIdx.x & 31) < P.pages_per_tile;
+            if (mine && block >= 0)
+                asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(
+                                 P.pool + (int64_t)block * P.block_stride + (int64_t)T.row0 * P.token_bytes),
+                             "r"(rows * P.token_bytes)
+                             : "memory");
+            __syncwarp();
         }
 }
 
@@ -1198,6 +1203,7 @@ __global__ void __launch_bounds__(kThreads<kFp8>, 1) lmc_attend_kernel(const __g
         bar_init(&C.pv_done, 1);
         bar_init(&C.o_free, kSoftWarps);
         C.gave_up = 0;
+        C.loading = -1;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         fence_async();
     }
@@ -1211,22 +1217,28 @@ __global__ void __launch_bounds__(kThreads<kFp8>, 1) lmc_attend_kernel(const __g
     fence_after();
     wait_for_launch();
 
-    Walk W;
-    W.init(P, col);
     if (warp < kSoftWarps) {
         if (kFp8)
             asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kSoftRegisters));
+        Walk W;
+        W.init(P, col);
         soften<kBf16, kFp8>(P, C, M, W, col, group);
     } else if (kFp8 && warp >= kFirstFp8Loader) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kLoadRegisters));
+        Walk W;
+        W.init(P, col);
         load_fp8(P, C, M, W, group);
     } else {
         if (kFp8)
             asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kIssueRegisters));
+        Walk W;
+        W.init(P, col);
         if (warp == kScoreWarp)
             multiply_scores<kBf16>(P, C, M, W);
         else if (warp == kValueWarp)
             multiply_values<kBf16>(P, C, M, W);
+        else if (warp == kAheadWarp)
+            send_ahead(P, C, W);
         else if (!kFp8)
             load_by_tma(P, C, M, W, group);
     }
