@@ -727,8 +727,17 @@ __device__ __forceinline__ void load_fp8(const AttendPlan &P, Control &C, const 
                     widen(wide[i - kEarly], codes[i]);
                     put(to, i, wide[i - kEarly]);
                 }
+                if (warp == 0 && lane == 0) {
+                    C.valid[n % (2 * kMaxStages)] = valid;
+                    C.zero[n % (2 * kMaxStages)] = 0;  // the rows left out hold zeros
+                }
+                fence_async();
+                __syncwarp();
+                if (lane == 0)
+                    bar_arrive(&C.kv_full[st]);
+                n++;
             }
-            if (more)
+            if (more)  // behind the arrival, which the fence would hold up until they are there
 #pragma unroll
                 for (int i = kEarly; i < kPanels; i++)
                     load(i);
@@ -750,18 +759,7 @@ __device__ __forceinline__ void load_fp8(const AttendPlan &P, Control &C, const 
                 __syncwarp();
                 if (lane == 0)
                     bar_arrive(&C.q_full);
-                continue;
             }
-            const int st = n % P.stages;
-            if (warp == 0 && lane == 0) {
-                C.valid[n % (2 * kMaxStages)] = valid;
-                C.zero[n % (2 * kMaxStages)] = 0;  // the rows left out hold zeros
-            }
-            fence_async();
-            __syncwarp();
-            if (lane == 0)
-                bar_arrive(&C.kv_full[st]);
-            n++;
         }
     }
     if (bad)
