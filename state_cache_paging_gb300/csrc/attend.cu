@@ -1446,6 +1446,11 @@ struct Work {
     int64_t segment, part_ml, part_o, lse2, logits, bytes;  // offsets
 };
 
+// 0: none (a full-attention layer's spec may hold any number there).
+int32_t window_of(const lmc_layout *L, int32_t layer) {
+    return L->specs[layer].kind == LMC_LAYER_SWA ? L->specs[layer].window : 0;
+}
+
 int work_space(const lmc_layout *L, int32_t layer, int64_t R, int64_t H, int64_t V, int64_t max_length, bool weights,
                Work &W) {
     if (L == nullptr || layer < 0 || (size_t)layer >= L->desc.size() || L->specs[layer].kind == LMC_LAYER_KDA ||
@@ -1455,7 +1460,7 @@ int work_space(const lmc_layout *L, int32_t layer, int64_t R, int64_t H, int64_t
     W.head_groups = (int32_t)((H + kMaxHeads - 1) / kMaxHeads);
     W.group_heads = (int32_t)((H + W.head_groups - 1) / W.head_groups);
     W.cols = std::max(1, kMaxCols / W.head_groups);
-    const int64_t window = L->specs[layer].window;
+    const int64_t window = window_of(L, layer);
     const int64_t tokens = window > 0 ? std::min(max_length, window) : max_length;
     W.logit_stride = (tokens + 1 + 3) / 4 * 4;
     int64_t at = 0;
@@ -1624,7 +1629,7 @@ extern "C" int lmc_attend(const lmc_layout *L, const lmc_entries *e, const void 
     P.H = (int32_t)H;
     P.E = e->entry_dim;
     P.V = a->value_dim;
-    P.window = L->specs[e->layer].kind == LMC_LAYER_SWA ? L->specs[e->layer].window : 0;
+    P.window = window_of(L, e->layer);
     P.block_size = (int32_t)N;
     P.token_bytes = (int32_t)L->specs[e->layer].token_bytes;
     // several small pages share a tile where each fills whole 8-row groups of it

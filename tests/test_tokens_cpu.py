@@ -108,6 +108,15 @@ def test_attend_workspace_sizes_and_refusals(lmc, env):
         assert ei.value.code == lmc.LMC_ERR_INVALID_ARG, args
 
 
+def test_attend_workspace_takes_no_window_from_a_full_attention_layer(lmc):
+    """Only SWA layers have one; the logits of all tokens are kept."""
+    plain, odd = W.mla(1152), dict(W.mla(1152), window=16)
+    need = [lmc.lmc_attend_workspace(lmc.lmc_layout_build([x], 64, False, 1 << 24), 0, 2, 4, 512, 1000, True)
+            for x in (plain, odd)]
+    assert need[0] == need[1]
+    assert need[1] >= 2 * 4 * 1000 * 4
+
+
 def _select(lmc, base, **kw):
     a = dict(scores=base, ss=100, rs=10, sets=2, n=2, lengths=base, most=10, budget=4, recent=1, kept=base, ks=base,
              kl=base, status=base)
