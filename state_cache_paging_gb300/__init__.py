@@ -516,48 +516,72 @@ def _refuse(what: str):
 # Decode steps make these calls with little work each, so their checks are kept
 # to a few attribute reads per tensor.
 
-def _table(name: str, t) -> lmc_block_table:
+def _home(name: str, t) -> int:
+    """The current device, which a call's tensors must be on (or pinned)."""
     import torch
-    _visible(name, t)
+    home = t.get_device()
+    if home < 0:
+        _visible(name, t)
+        return torch._C._cuda_getDevice()
+    if home != torch._C._cuda_getDevice():
+        _refuse(f"{name} is on cuda:{home}, which is not the current device")
+    return home
+
+
+def _near(name: str, t, home: int) -> None:
+    device = t.get_device()
+    if device != home:
+        _visible(name, t)
+        if device >= 0:
+            _refuse(f"{name} is on cuda:{device}, not on cuda:{home}")
+
+
+def _apart(name: str, rows: int, stride: int, cols: int) -> int:
+    """The stride of rows of `cols` elements, which may not overlap (an
+    expanded tensor's do)."""
+    if stride >= cols:
+        return stride
+    if rows > 1:
+        _refuse(f"{name}: rows of {cols} elements, {stride} apart")
+    return cols
+
+
+def _table(name: str, t, home: int) -> lmc_block_table:
+    import torch
+    _near(name, t, home)
     shape, stride = t.shape, t.stride()
     if len(shape) != 2 or t.dtype != torch.int32 or (stride[1] != 1 and shape[1] > 1):
         _refuse(f"{name} must be int32 [num_requests, cols] with unit column stride")
     cols = shape[1]
-    return lmc_block_table(t.data_ptr(), stride[0] if stride[0] > cols else cols, cols)
+    return lmc_block_table(t.data_ptr(), _apart(name, shape[0], stride[0], cols), cols)
 
 
-def _ints(name: str, t, *shape):
+def _ints(name: str, t, home: int, *shape):
     """The address of an int32 tensor of `shape`, contiguous."""
     import torch
-    _visible(name, t)
+    _near(name, t, home)
     if t.dtype != torch.int32 or t.shape != shape or not t.is_contiguous():
         _refuse(f"{name} must be contiguous int32 {list(shape)}")
     return t.data_ptr()
 
 
-def _floats(name: str, t, rows: int, cols: int):
+def _floats(name: str, t, home: int, rows: int, cols: int):
     """(address, row stride) of a float32 [rows, >= cols] tensor."""
     import torch
-    _visible(name, t)
+    _near(name, t, home)
     shape, stride = t.shape, t.stride()
     if len(shape) != 2 or t.dtype != torch.float32 or shape[0] != rows or shape[1] < cols or \
             (stride[1] != 1 and shape[1] > 1):
         _refuse(f"{name} must be float32 [{rows}, {cols}] with unit column stride")
-    return t.data_ptr(), stride[0] if stride[0] > cols else cols
+    return t.data_ptr(), _apart(name, rows, stride[0], cols)
 
 
-def _status(t):
-    _visible("status", t)
-    if t.numel() * t.element_size() < 4:
-        _refuse("status holds at least 4 bytes")
+def _bytes(name: str, t, home: int, least: int):
+    """The address of contiguous memory of at least `least` bytes."""
+    _near(name, t, home)
+    if t.nbytes < least or not t.is_contiguous():
+        _refuse(f"{name} must be contiguous and hold at least {least} bytes")
     return t.data_ptr()
-
-
-def _pool(layout: Layout, pool):
-    _visible("pool", pool)
-    if pool.nbytes < layout.pool_bytes or not pool.is_contiguous():
-        _refuse(f"pool must be contiguous and hold the {layout.pool_bytes} bytes the layout addresses")
-    return pool.data_ptr()
 
 
 def _value_type(t) -> int:
@@ -571,14 +595,14 @@ def _value_type(t) -> int:
     _refuse(f"values must be bfloat16 or float16, not {dtype}")
 
 
-def _entries(layout: Layout, layer: int, table, entry_dim: int, value_type: int, scale: float) -> lmc_entries:
+def _entries(layout: Layout, layer: int, table, home: int, entry_dim: int, value_type: int, scale: float) -> lmc_entries:
     """The layer's entries: of `value_type` where its token_bytes hold
     entry_dim 16-bit values, fp8 e4m3 where they hold entry_dim bytes."""
     if not 0 <= layer < layout.num_layers:
         _refuse(f"layer {layer} of {layout.num_layers}")
     if layout.real_bytes[layer] == layout.block_size * entry_dim:
         value_type = LMC_E_E4M3
-    return lmc_entries(layer, value_type, entry_dim, table.shape[0], scale, 0, _table("block table", table))
+    return lmc_entries(layer, value_type, entry_dim, table.shape[0], scale, 0, _table("block table", table, home))
 
 
 def lmc_append(layout: Layout, layer: int, pool, table, requests, positions, entries, status, scale: float = 1.0,
@@ -587,16 +611,18 @@ def lmc_append(layout: Layout, layer: int, pool, table, requests, positions, ent
     row stride) as the entry at position positions[i] of request requests[i]
     (int32 device tensors; request -1: skipped) of a paged layer. A layer
     whose token_bytes equal entry_dim holds fp8 e4m3 codes of value / scale."""
-    _visible("entries", entries)
+    home = _home("pool", pool)
+    _near("entries", entries, home)
     shape, stride = entries.shape, entries.stride()
     if len(shape) != 2 or (stride[1] != 1 and shape[1] > 1):
         _refuse("entries must be [rows, entry_dim] with unit column stride")
     n, dim = shape
     vt = _value_type(entries)
-    e = _entries(layout, layer, table, dim, vt, scale)
-    rc = _lib.lmc_append(layout.handle, e, _pool(layout, pool), _ints("requests", requests, n),
-                         _ints("positions", positions, n), entries.data_ptr(), vt,
-                         stride[0] if stride[0] > dim else dim, n, _status(status),
+    e = _entries(layout, layer, table, home, dim, vt, scale)
+    rc = _lib.lmc_append(layout.handle, e, _bytes("pool", pool, home, layout.pool_bytes),
+                         _ints("requests", requests, home, n), _ints("positions", positions, home, n),
+                         entries.data_ptr(), vt, _apart("entries", n, stride[0], dim), n,
+                         _bytes("status", status, home, 4),
                          _stream_ptr(stream, pool, table, requests, positions, entries, status))
     if rc != LMC_OK:
         raise LmcError(rc, "lmc_append")
@@ -621,9 +647,9 @@ def lmc_attend(layout: Layout, layer: int, pool, table, lengths, q, value_dim: i
     table holds). lse (float32 [requests, heads]) receives the log of the sum
     of exponentials; weights (float32 [requests, >= max_length]) has the sum
     over the heads of each token's probability added to it."""
-    _visible("q", q)
-    _visible("out", out)
-    _visible("workspace", workspace)
+    home = _home("pool", pool)
+    _near("q", q, home)
+    _near("out", out, home)
     shape, qs, os_ = q.shape, q.stride(), out.stride()
     if len(shape) != 3 or len(os_) != 3 or qs[2] != 1 or os_[2] != 1 or out.dtype != q.dtype:
         _refuse("q and out must be [requests, heads, dim] of one type with a contiguous last dimension")
@@ -631,15 +657,15 @@ def lmc_attend(layout: Layout, layer: int, pool, table, lengths, q, value_dim: i
     if out.shape != (R, H, value_dim) or table.shape[0] != R:
         _refuse(f"out must be [{R}, {H}, {value_dim}] and the block table have {R} rows")
     vt = _value_type(q)
-    e = _entries(layout, layer, table, dim, vt, scale)
+    e = _entries(layout, layer, table, home, dim, vt, scale)
     if max_length is None:
         max_length = max(1, e.table.num_cols * layout.block_size)
-    lse_p, lse_s = (None, 0) if lse is None else _floats("lse", lse, R, H)
-    w_p, w_s = (None, 0) if weights is None else _floats("weights", weights, R, max_length)
-    a = lmc_attention(_ints("lengths", lengths, R), max_length, q.data_ptr(), qs[0], qs[1], out.data_ptr(), os_[0],
+    lse_p, lse_s = (None, 0) if lse is None else _floats("lse", lse, home, R, H)
+    w_p, w_s = (None, 0) if weights is None else _floats("weights", weights, home, R, max_length)
+    a = lmc_attention(_ints("lengths", lengths, home, R), max_length, q.data_ptr(), qs[0], qs[1], out.data_ptr(), os_[0],
                       os_[1], lse_p, lse_s, w_p, w_s, vt, H, value_dim, softmax_scale)
-    rc = _lib.lmc_attend(layout.handle, e, _pool(layout, pool), a, workspace.data_ptr(), workspace.nbytes,
-                         _status(status),
+    rc = _lib.lmc_attend(layout.handle, e, _bytes("pool", pool, home, layout.pool_bytes), a,
+                         _bytes("workspace", workspace, home, 0), workspace.nbytes, _bytes("status", status, home, 4),
                          _stream_ptr(stream, pool, table, lengths, q, out, workspace, status, lse, weights))
     if rc != LMC_OK:
         raise LmcError(rc, "lmc_attend")
@@ -654,20 +680,21 @@ def lmc_select_tokens(scores, lengths, budget: int, recent: int, kept, kept_scor
     positions in increasing order and their scores, kept_lengths (int32
     [requests]) how many there are."""
     import torch
-    _visible("scores", scores)
+    home = _home("scores", scores)
     shape, stride = scores.shape, scores.stride()
     if len(shape) != 3 or scores.dtype != torch.float32 or (stride[2] != 1 and shape[2] > 1):
         _refuse("scores must be float32 [sets, requests, tokens] with unit token stride")
     S, R, T = shape
     scores_out = None
     if kept_scores is not None:
-        _visible("kept_scores", kept_scores)
+        _near("kept_scores", kept_scores, home)
         if kept_scores.dtype != torch.float32 or kept_scores.shape != (S, R, budget) or not kept_scores.is_contiguous():
             _refuse(f"kept_scores must be contiguous float32 {[S, R, budget]}")
         scores_out = kept_scores.data_ptr()
-    rc = _lib.lmc_select_tokens(scores.data_ptr(), stride[0], stride[1], S, R, _ints("lengths", lengths, R), T, budget,
-                                recent, _ints("kept", kept, S, R, budget), scores_out,
-                                _ints("kept_lengths", kept_lengths, R), _status(status),
+    rc = _lib.lmc_select_tokens(scores.data_ptr(), stride[0], stride[1], S, R,
+                                _ints("lengths", lengths, home, R), T, budget, recent,
+                                _ints("kept", kept, home, S, R, budget), scores_out,
+                                _ints("kept_lengths", kept_lengths, home, R), _bytes("status", status, home, 4),
                                 _stream_ptr(stream, scores, lengths, kept, kept_scores, kept_lengths, status))
     if rc != LMC_OK:
         raise LmcError(rc, "lmc_select_tokens")
@@ -680,17 +707,18 @@ def lmc_move_tokens(layout: Layout, kv_group: int, pool, src_table, dst_table, k
     positions j under `dst_table`, whose blocks must be others. kept: int32
     [sets, requests, most], with one set for all layers or one per layer."""
     import torch
-    _visible("kept", kept)
+    home = _home("pool", pool)
+    _near("kept", kept, home)
     shape, stride = kept.shape, kept.stride()
     if len(shape) != 3 or kept.dtype != torch.int32 or (stride[2] != 1 and shape[2] > 1):
         _refuse("kept must be int32 [sets, requests, most] with unit last stride")
     S, R, K = shape
-    src, dst = _table("source table", src_table), _table("destination table", dst_table)
+    src, dst = _table("source table", src_table, home), _table("destination table", dst_table, home)
     if src_table.shape[0] != R or dst_table.shape[0] != R:
         _refuse(f"the block tables must have {R} rows")
-    rc = _lib.lmc_move_tokens(layout.handle, kv_group, _pool(layout, pool), R, src, dst, kept.data_ptr(), S, stride[0],
-                              stride[1] if stride[1] > K else K, _ints("kept_lengths", kept_lengths, R), K,
-                              _status(status),
+    rc = _lib.lmc_move_tokens(layout.handle, kv_group, _bytes("pool", pool, home, layout.pool_bytes), R, src, dst,
+                              kept.data_ptr(), S, stride[0], _apart("kept", R, stride[1], K),
+                              _ints("kept_lengths", kept_lengths, home, R), K, _bytes("status", status, home, 4),
                               _stream_ptr(stream, pool, src_table, dst_table, kept, kept_lengths, status))
     if rc != LMC_OK:
         raise LmcError(rc, "lmc_move_tokens")

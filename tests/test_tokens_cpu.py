@@ -183,3 +183,84 @@ def test_binding_refuses_wrong_tensors(lmc, env):
         with pytest.raises(lmc.LmcError) as ei:
             call()
         assert ei.value.code == lmc.LMC_ERR_INVALID_ARG
+
+
+@pytest.fixture()
+def as_if_on_device(lmc, monkeypatch):
+    """Host tensors pass as ones of the current device; nothing is launched."""
+    monkeypatch.setattr(lmc, "_home", lambda name, t: 0)
+    monkeypatch.setattr(lmc, "_near", lambda name, t, home: None)
+    monkeypatch.setattr(lmc, "_stream_ptr", lambda stream, *buffers: None)
+
+    class Library:
+        calls = 0
+
+        def __getattr__(self, name):
+            if name == "lmc_strerror":
+                return lambda code: b"refused"
+
+            def call(*args):
+                Library.calls += 1
+                return lmc.LMC_OK
+            return call
+    monkeypatch.setattr(lmc, "_lib", Library())
+    return Library
+
+
+def test_binding_refuses_rows_that_overlap(lmc, env, as_if_on_device):
+    """An expanded tensor's rows lie 0 apart: taken as rows of their own they
+    would be read past its memory."""
+    import torch
+    L, _, _ = env
+    pool = torch.zeros(L.pool_bytes, dtype=torch.uint8)
+    t = torch.zeros((2, 3), dtype=torch.int32)
+    x = torch.zeros((2, 576), dtype=torch.bfloat16)
+    q, out = torch.zeros((2, 4, 576), dtype=torch.bfloat16), torch.zeros((2, 4, 512), dtype=torch.bfloat16)
+    f = torch.zeros((2, 200))
+    i, kept = torch.zeros(2, dtype=torch.int32), torch.zeros((1, 2, 4), dtype=torch.int32)
+    ws = torch.zeros(1024, dtype=torch.uint8)
+
+    def append(table=t, rows=x, status=i):
+        lmc.lmc_append(L, 1, pool, table, i, i, rows, status)
+
+    def attend(table=t, workspace=ws, **kw):
+        lmc.lmc_attend(L, 1, pool, table, i, q, 512, 0.1, out, workspace, i, max_length=190, **kw)
+
+    def move(src=t, dst=t.clone(), kept=kept):
+        lmc.lmc_move_tokens(L, 1, pool, src, dst, kept, i, i)
+
+    one = [torch.Tensor.expand(y[:1], *y.shape) for y in (t, x, f)]
+    for call in (lambda: append(table=one[0]), lambda: append(rows=one[1]),
+                 lambda: append(status=torch.zeros(1, dtype=torch.uint8).expand(4)),
+                 lambda: attend(table=one[0]), lambda: attend(lse=one[2]), lambda: attend(weights=one[2]),
+                 lambda: attend(workspace=torch.zeros(1, dtype=torch.uint8).expand(1024)),
+                 lambda: attend(weights=torch.zeros(2 * 150).as_strided((2, 200), (100, 1))),
+                 lambda: move(src=one[0]), lambda: move(dst=one[0]), lambda: move(kept=kept[:, :1].expand(1, 2, 4))):
+        before = as_if_on_device.calls
+        with pytest.raises(lmc.LmcError) as ei:
+            call()
+        assert ei.value.code == lmc.LMC_ERR_INVALID_ARG
+        assert as_if_on_device.calls == before
+    for call in (append, attend, move):  # the same calls without one
+        call()
+    assert as_if_on_device.calls >= 3
+
+
+def test_binding_refuses_tensors_of_another_device(lmc, monkeypatch):
+    import torch
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0)
+
+    class On:
+        def __init__(self, device):
+            self.is_cuda, self.get_device = device >= 0, lambda: device
+
+        def is_pinned(self):
+            return True
+
+    assert lmc._home("pool", On(0)) == lmc._home("pool", On(-1)) == 0
+    for device in (0, -1):
+        lmc._near("q", On(device), 0)
+    for call in (lambda: lmc._home("pool", On(1)), lambda: lmc._near("q", On(1), 0)):
+        with pytest.raises(lmc.LmcError) as ei:
+            call()
+        assert ei.value.code == lmc.LMC_ERR_INVALID_ARG
