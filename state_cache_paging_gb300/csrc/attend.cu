@@ -99,6 +99,8 @@ struct Control {
     uint64_t zero[2 * kMaxStages];   // and those to be cleared before they are values
     uint32_t tmem;
     uint32_t gave_up;            // a wait ran out: nothing waits any more
+    uint64_t ended[2];           // all of an issuing warp's products, after that
+    uint32_t tiles, segments;    // that the loaders asked for
     int32_t loading;             // the tile whose load was issued last
     float factor[kMaxHeads];     // rescaling of a head's O
     float half[2][kMaxHeads];    // a head's maximum or sum in each half of the tokens
@@ -321,6 +323,12 @@ __device__ __forceinline__ void bar_wait(Control &C, uint64_t *bar, uint32_t par
     atomicOr(status, LMC_ST_TIMEOUT);
 }
 
+// Whether the CTA has given up, the same for the whole warp. Copies are only
+// asked for where it has not: an earlier one of the same barrier may still run.
+__device__ __forceinline__ bool gone(Control &C) {
+    return __any_sync(0xffffffffu, *(volatile uint32_t *)&C.gave_up != 0);
+}
+
 // One lane of a converged warp. The products are issued behind this, not
 // behind a lane number: the compiler then knows that one thread runs and keeps
 // the descriptors in uniform registers (115 cycles an instruction otherwise).
@@ -530,6 +538,14 @@ __device__ __forceinline__ void load_by_tma(const AttendPlan &P, Control &C, con
     const int lane = threadIdx.x & 31;
     uint32_t bad = 0, n = 0, segments = 0;
     LastPage last;
+    auto end = [&] {
+        if (bad)
+            atomicOr(P.status, bad);
+        if (lane == 0) {
+            C.tiles = n;
+            C.segments = segments;
+        }
+    };
     while (W.next(P)) {
         const int row_panels = (P.E + 63) / 64;
         for (int j = 0; j < W.count; j++, n++) {
@@ -552,7 +568,8 @@ __device__ __forceinline__ void load_by_tma(const AttendPlan &P, Control &C, con
             const int block0 = (int)uniform(block);
             if (n >= (uint32_t)P.stages)
                 bar_wait(C, &C.kv_free[st], (n / P.stages - 1) & 1, P.status);
-            __syncwarp();
+            if (gone(C))
+                return end();
             if (P.pages_per_tile == 1) {
                 if (elect()) {
                     bar_expect(&C.kv_full[st], bytes);
@@ -577,7 +594,10 @@ __device__ __forceinline__ void load_by_tma(const AttendPlan &P, Control &C, con
                 const int r = (int)uniform(W.r);
                 if (segments > 0)
                     bar_wait(C, &C.q_free, (segments - 1) & 1, P.status);
-                __syncwarp();
+                if (gone(C)) {
+                    n++;
+                    return end();
+                }
                 if (elect()) {
                     bar_expect(&C.q_full, (uint32_t)(row_panels * P.padded_heads * 128));
                     for (int i = 0; i < P.query_copies; i++)
@@ -588,16 +608,7 @@ __device__ __forceinline__ void load_by_tma(const AttendPlan &P, Control &C, con
             }
         }
     }
-    if (bad)
-        atomicOr(P.status, bad);
-    // a CTA that gave up leaves no copy of its own in flight
-    if (*(volatile uint32_t *)&C.gave_up) {
-        for (uint32_t k = n > (uint32_t)P.stages ? n - P.stages : 0; k < n; k++)
-            for (uint32_t i = 0; i < kWaitLimit && !bar_try(&C.kv_full[k % P.stages], (k / P.stages) & 1); i++) {
-            }
-        for (uint32_t i = 0; segments > 0 && i < kWaitLimit && !bar_try(&C.q_full, (segments - 1) & 1); i++) {
-        }
-    }
+    end();
 }
 
 // Queries to f16 where they lie in shared memory, each head's times a power of
@@ -698,6 +709,12 @@ __device__ __forceinline__ void load_fp8(const AttendPlan &P, Control &C, const 
         }
     };
 
+    auto end = [&] {
+        if (bad)
+            atomicOr(P.status, bad);
+        if (warp == 0 && lane == 0)
+            C.segments = segments;
+    };
     while (W.next(P)) {
         // a turn stores tile j and loads tile j + 1
 #pragma unroll 1
@@ -745,7 +762,8 @@ __device__ __forceinline__ void load_fp8(const AttendPlan &P, Control &C, const 
                 const int r = (int)uniform(W.r);
                 if (segments > 0)
                     bar_wait(C, &C.q_free, (segments - 1) & 1, P.status);
-                __syncwarp();
+                if (gone(C))
+                    return end();
                 if (warp == 0 && elect()) {
                     bar_expect(&C.q_raw, (uint32_t)((P.E + 63) / 64 * P.padded_heads * 128));
                     for (int i = 0; i < P.query_copies; i++)
@@ -762,12 +780,32 @@ __device__ __forceinline__ void load_fp8(const AttendPlan &P, Control &C, const 
             }
         }
     }
-    if (bad)
-        atomicOr(P.status, bad);
-    // a CTA that gave up leaves no copy of its own in flight
-    if (warp == 0 && *(volatile uint32_t *)&C.gave_up)
-        for (uint32_t i = 0; segments > 0 && i < kWaitLimit && !bar_try(&C.q_raw, (segments - 1) & 1); i++) {
-        }
+    end();
+}
+
+// A CTA that gave up, all its roles ended: what it left running ends (or the
+// limit runs out) before its memory goes to another. The two warps that issue
+// products commit all of theirs once more; the third waits for the copies.
+__device__ __forceinline__ void outlast(uint64_t *bar, uint32_t parity) {
+    for (uint32_t i = 0; i < kWaitLimit && !bar_try(bar, parity); i++) {
+    }
+}
+
+template <bool kFp8>
+__device__ void wind_up(const AttendPlan &P, Control &C, int warp) {
+    if (warp == kScoreWarp || warp == kValueWarp) {
+        uint64_t *const done = &C.ended[warp - kScoreWarp];
+        if (elect())
+            commit(done);
+        __syncwarp();
+        outlast(done, 0);
+    } else if (warp == kAheadWarp) {
+        if (!kFp8)
+            for (uint32_t k = C.tiles > (uint32_t)P.stages ? C.tiles - P.stages : 0; k < C.tiles; k++)
+                outlast(&C.kv_full[k % P.stages], (k / P.stages) & 1);
+        if (C.segments > 0)
+            outlast(kFp8 ? &C.q_raw : &C.q_full, (C.segments - 1) & 1);
+    }
 }
 
 // One warp: sends tiles on to L2, kAhead of them before they are loaded (the
@@ -1200,6 +1238,8 @@ __global__ void __launch_bounds__(kThreads<kFp8>, 1) lmc_attend_kernel(const __g
         bar_init(&C.p_full, kSoftWarps);
         bar_init(&C.pv_done, 1);
         bar_init(&C.o_free, kSoftWarps);
+        bar_init(&C.ended[0], 1);
+        bar_init(&C.ended[1], 1);
         C.gave_up = 0;
         C.loading = -1;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -1248,6 +1288,10 @@ __global__ void __launch_bounds__(kThreads<kFp8>, 1) lmc_attend_kernel(const __g
     fence_before();
     __syncthreads();
     fence_after();
+    if (C.gave_up) {
+        wind_up<kFp8>(P, C, warp);
+        __syncthreads();
+    }
     if (warp == kScoreWarp)
         asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(C.tmem));
 }
