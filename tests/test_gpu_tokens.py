@@ -200,6 +200,42 @@ def test_attend_matches_64_bits(lmc, status, E, V, H, cache, act, N, packed, win
     _check_attend(M, 1, table, lengths, q, V, scale, ss, out, lse, act, W, before)
 
 
+@pytest.mark.parametrize("R,longest,N,window,H,cache,act", [
+    (1, 128, 64, 0, 32, "bf16", "bf16"), (5, 190, 64, 0, 4, "f16", "f16"), (153, 64, 944, 0, 8, "e4m3", "bf16"),
+    (300, 128, 16, 0, 20, "bf16", "bf16"), (40, 400, 944, 33, 96, "bf16", "bf16"), (310, 60, 20, 0, 3, "e4m3", "f16"),
+    (700, 60, 64, 0, 2, "f16", "f16"), (90, 1, 64, 0, 130, "bf16", "bf16")])
+def test_attend_of_short_caches(lmc, status, R, longest, N, window, H, cache, act):
+    """Caches of a tile or a few, so that requests are not split; one length
+    among them cannot be served. The same again sized for long caches."""
+    E, V = 128, 96
+    rng = np.random.default_rng(R)
+    lengths = [int(n) for n in rng.integers(0, longest + 1, R)]
+    lengths[-1] = longest
+    blocks = sum(-(-n // N) for n in lengths) + 2
+    scale = 0.0625 if cache == "e4m3" else 1.0
+    M = T.Model(lmc, E, cache, N, False, layers=2, window=window, state=16 * N, blocks=blocks)
+    table = T.tables(lengths, N, blocks, rng)
+    for r, n in enumerate(lengths):
+        lo = max(0, n - window) if window else 0
+        M.write(1, table, r, lo, torch.from_numpy(rng.standard_normal((n - lo, E))) / scale)
+    q = torch.from_numpy(rng.standard_normal((R, H, E))).to(T.TYPES[act]).to(DEV)
+    bad = R // 2 if R > 2 else None
+    given = [1 << 20 if r == bad else n for r, n in enumerate(lengths)]
+    before = torch.from_numpy(rng.random((R, 4096))).float()
+    for max_length in (longest, 4096):
+        W = before.to(DEV)
+        status.zero_()
+        out, lse, ss = _attend(lmc, M, 1, table, given, q, V, status, scale, weights=W, max_length=max_length)
+        assert status.item() == (0 if bad is None else lmc.LMC_ST_BAD_JOB)
+        if bad is not None:
+            assert (out[bad] == 7.0).all() and (lse[bad] == 7.0).all()
+            assert torch.equal(W[bad].cpu(), before[bad])
+        at = [r for r in range(R) if r != bad]
+        sub = table[at]
+        _check_attend(M, 1, sub, [lengths[r] for r in at], q[at], V, scale, ss, out[at], lse[at], act, W[at],
+                      before[at])
+
+
 @pytest.mark.parametrize("cache,act", [("bf16", "bf16"), ("e4m3", "bf16"), ("f16", "f16")])
 def test_attend_split_over_a_long_cache_and_many_requests(lmc, status, cache, act):
     """One long request beside many short ones: the work is shared over the
