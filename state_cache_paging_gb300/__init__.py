@@ -514,26 +514,32 @@ def _refuse(what: str):
 
 
 # Decode steps make these calls with little work each, so their checks are kept
-# to a few attribute reads per tensor.
+# to a few attribute reads per tensor (an import statement costs as much as
+# one, a call of a function as two).
+
+_torch = None  # bound by the first call
+
 
 def _home(name: str, t) -> int:
     """The current device, which a call's tensors must be on (or pinned)."""
-    import torch
+    global _torch
+    if _torch is None:
+        import torch
+        _torch = torch
     home = t.get_device()
     if home < 0:
         _visible(name, t)
-        return torch._C._cuda_getDevice()
-    if home != torch._C._cuda_getDevice():
+        return _torch._C._cuda_getDevice()
+    if home != _torch._C._cuda_getDevice():
         _refuse(f"{name} is on cuda:{home}, which is not the current device")
     return home
 
 
-def _near(name: str, t, home: int) -> None:
-    device = t.get_device()
-    if device != home:
-        _visible(name, t)
-        if device >= 0:
-            _refuse(f"{name} is on cuda:{device}, not on cuda:{home}")
+def _away(name: str, t, home: int) -> None:
+    """A tensor that is not on `home` must be pinned host memory."""
+    _visible(name, t)
+    if t.get_device() >= 0:
+        _refuse(f"{name} is on cuda:{t.get_device()}, not on cuda:{home}")
 
 
 def _apart(name: str, rows: int, stride: int, cols: int) -> int:
@@ -547,10 +553,10 @@ def _apart(name: str, rows: int, stride: int, cols: int) -> int:
 
 
 def _table(name: str, t, home: int) -> lmc_block_table:
-    import torch
-    _near(name, t, home)
+    if t.get_device() != home:
+        _away(name, t, home)
     shape, stride = t.shape, t.stride()
-    if len(shape) != 2 or t.dtype != torch.int32 or (stride[1] != 1 and shape[1] > 1):
+    if len(shape) != 2 or t.dtype != _torch.int32 or (stride[1] != 1 and shape[1] > 1):
         _refuse(f"{name} must be int32 [num_requests, cols] with unit column stride")
     cols = shape[1]
     return lmc_block_table(t.data_ptr(), _apart(name, shape[0], stride[0], cols), cols)
@@ -558,19 +564,19 @@ def _table(name: str, t, home: int) -> lmc_block_table:
 
 def _ints(name: str, t, home: int, *shape):
     """The address of an int32 tensor of `shape`, contiguous."""
-    import torch
-    _near(name, t, home)
-    if t.dtype != torch.int32 or t.shape != shape or not t.is_contiguous():
+    if t.get_device() != home:
+        _away(name, t, home)
+    if t.dtype != _torch.int32 or t.shape != shape or not t.is_contiguous():
         _refuse(f"{name} must be contiguous int32 {list(shape)}")
     return t.data_ptr()
 
 
 def _floats(name: str, t, home: int, rows: int, cols: int):
     """(address, row stride) of a float32 [rows, >= cols] tensor."""
-    import torch
-    _near(name, t, home)
+    if t.get_device() != home:
+        _away(name, t, home)
     shape, stride = t.shape, t.stride()
-    if len(shape) != 2 or t.dtype != torch.float32 or shape[0] != rows or shape[1] < cols or \
+    if len(shape) != 2 or t.dtype != _torch.float32 or shape[0] != rows or shape[1] < cols or \
             (stride[1] != 1 and shape[1] > 1):
         _refuse(f"{name} must be float32 [{rows}, {cols}] with unit column stride")
     return t.data_ptr(), _apart(name, rows, stride[0], cols)
@@ -578,7 +584,8 @@ def _floats(name: str, t, home: int, rows: int, cols: int):
 
 def _bytes(name: str, t, home: int, least: int):
     """The address of contiguous memory of at least `least` bytes."""
-    _near(name, t, home)
+    if t.get_device() != home:
+        _away(name, t, home)
     if t.nbytes < least or not t.is_contiguous():
         _refuse(f"{name} must be contiguous and hold at least {least} bytes")
     return t.data_ptr()
@@ -586,11 +593,10 @@ def _bytes(name: str, t, home: int, least: int):
 
 def _value_type(t) -> int:
     """LMC_E_* of a bfloat16 or float16 tensor."""
-    import torch
     dtype = t.dtype
-    if dtype == torch.bfloat16:
+    if dtype == _torch.bfloat16:
         return LMC_E_BF16
-    if dtype == torch.float16:
+    if dtype == _torch.float16:
         return LMC_E_F16
     _refuse(f"values must be bfloat16 or float16, not {dtype}")
 
@@ -612,7 +618,8 @@ def lmc_append(layout: Layout, layer: int, pool, table, requests, positions, ent
     (int32 device tensors; request -1: skipped) of a paged layer. A layer
     whose token_bytes equal entry_dim holds fp8 e4m3 codes of value / scale."""
     home = _home("pool", pool)
-    _near("entries", entries, home)
+    if entries.get_device() != home:
+        _away("entries", entries, home)
     shape, stride = entries.shape, entries.stride()
     if len(shape) != 2 or (stride[1] != 1 and shape[1] > 1):
         _refuse("entries must be [rows, entry_dim] with unit column stride")
@@ -648,8 +655,10 @@ def lmc_attend(layout: Layout, layer: int, pool, table, lengths, q, value_dim: i
     of exponentials; weights (float32 [requests, >= max_length]) has the sum
     over the heads of each token's probability added to it."""
     home = _home("pool", pool)
-    _near("q", q, home)
-    _near("out", out, home)
+    if q.get_device() != home:
+        _away("q", q, home)
+    if out.get_device() != home:
+        _away("out", out, home)
     shape, qs, os_ = q.shape, q.stride(), out.stride()
     if len(shape) != 3 or len(os_) != 3 or qs[2] != 1 or os_[2] != 1 or out.dtype != q.dtype:
         _refuse("q and out must be [requests, heads, dim] of one type with a contiguous last dimension")
@@ -679,16 +688,16 @@ def lmc_select_tokens(scores, lengths, budget: int, recent: int, kept, kept_scor
     kept_scores (float32, or None) [sets, requests, budget] receive the kept
     positions in increasing order and their scores, kept_lengths (int32
     [requests]) how many there are."""
-    import torch
     home = _home("scores", scores)
     shape, stride = scores.shape, scores.stride()
-    if len(shape) != 3 or scores.dtype != torch.float32 or (stride[2] != 1 and shape[2] > 1):
+    if len(shape) != 3 or scores.dtype != _torch.float32 or (stride[2] != 1 and shape[2] > 1):
         _refuse("scores must be float32 [sets, requests, tokens] with unit token stride")
     S, R, T = shape
     scores_out = None
     if kept_scores is not None:
-        _near("kept_scores", kept_scores, home)
-        if kept_scores.dtype != torch.float32 or kept_scores.shape != (S, R, budget) or not kept_scores.is_contiguous():
+        if kept_scores.get_device() != home:
+            _away("kept_scores", kept_scores, home)
+        if kept_scores.dtype != _torch.float32 or kept_scores.shape != (S, R, budget) or not kept_scores.is_contiguous():
             _refuse(f"kept_scores must be contiguous float32 {[S, R, budget]}")
         scores_out = kept_scores.data_ptr()
     rc = _lib.lmc_select_tokens(scores.data_ptr(), stride[0], stride[1], S, R,
@@ -706,11 +715,11 @@ def lmc_move_tokens(layout: Layout, kv_group: int, pool, src_table, dst_table, k
     kept[set, request, j] (j < kept_lengths[request]) under `src_table` to
     positions j under `dst_table`, whose blocks must be others. kept: int32
     [sets, requests, most], with one set for all layers or one per layer."""
-    import torch
     home = _home("pool", pool)
-    _near("kept", kept, home)
+    if kept.get_device() != home:
+        _away("kept", kept, home)
     shape, stride = kept.shape, kept.stride()
-    if len(shape) != 3 or kept.dtype != torch.int32 or (stride[2] != 1 and shape[2] > 1):
+    if len(shape) != 3 or kept.dtype != _torch.int32 or (stride[2] != 1 and shape[2] > 1):
         _refuse("kept must be int32 [sets, requests, most] with unit last stride")
     S, R, K = shape
     src, dst = _table("source table", src_table, home), _table("destination table", dst_table, home)

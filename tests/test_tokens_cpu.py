@@ -188,8 +188,9 @@ def test_binding_refuses_wrong_tensors(lmc, env):
 @pytest.fixture()
 def as_if_on_device(lmc, monkeypatch):
     """Host tensors pass as ones of the current device; nothing is launched."""
-    monkeypatch.setattr(lmc, "_home", lambda name, t: 0)
-    monkeypatch.setattr(lmc, "_near", lambda name, t, home: None)
+    import torch
+    monkeypatch.setattr(lmc, "_torch", torch)
+    monkeypatch.setattr(lmc, "_home", lambda name, t: -1)
     monkeypatch.setattr(lmc, "_stream_ptr", lambda stream, *buffers: None)
 
     class Library:
@@ -258,9 +259,9 @@ def test_binding_refuses_tensors_of_another_device(lmc, monkeypatch):
             return True
 
     assert lmc._home("pool", On(0)) == lmc._home("pool", On(-1)) == 0
-    for device in (0, -1):
-        lmc._near("q", On(device), 0)
-    for call in (lambda: lmc._home("pool", On(1)), lambda: lmc._near("q", On(1), 0)):
+    lmc._away("q", On(-1), 0)
+    for call in (lambda: lmc._home("pool", On(1)), lambda: lmc._away("q", On(1), 0),
+                 lambda: lmc._ints("lengths", On(1), 0, 2)):
         with pytest.raises(lmc.LmcError) as ei:
             call()
         assert ei.value.code == lmc.LMC_ERR_INVALID_ARG
