@@ -31,7 +31,7 @@ CXX = os.environ.get("CXX", "g++")
 def _sources():
     out = []
     for name in sorted(os.listdir(CSRC)):
-        if name.endswith((".cu", ".cpp", ".h", ".map")):
+        if name.endswith((".cu", ".cuh", ".cpp", ".h", ".map")):
             out.append(os.path.join(CSRC, name))
     out.append(os.path.join(INCLUDE, "lmc.h"))
     return out

@@ -54,9 +54,14 @@
 #include <cmath>
 #include <cstdint>
 
+#include "follow.cuh"
 #include "lmc_internal.h"
 
 namespace {
+
+using lmc::follow;
+using lmc::let_next_start;
+using lmc::wait_for_launch;
 
 constexpr int kMaxEntry = 576;
 constexpr int kMaxValue = 512;
@@ -479,17 +484,6 @@ __device__ __forceinline__ uint16_t to_out(float x, bool bf16) {
 __device__ __forceinline__ float from_q(uint32_t h, bool bf16) {
     return bf16 ? __uint_as_float(h << 16) : __half2float(__ushort_as_half((unsigned short)h));
 }
-
-// Kernels of this file are launched so that each may start while the one
-// before it in the stream still runs. The first waits for that one to be done
-// and its writes to be seen; nothing in global memory is touched before it
-// (the tensor maps are the kernel's own arguments).
-// The second lets the next one be brought in (the short kernels do; blocks
-// that only wait slow the long one down: 161 -> 173 us at four fp8 requests of
-// 131072 tokens).
-__device__ __forceinline__ void wait_for_launch() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
-__device__ __forceinline__ void let_next_start() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
-
 
 // ---- the CTA's roles ---------------------------------------------------------
 
@@ -1608,22 +1602,6 @@ bool allow_shared_memory(int which, void (*kern)(AttendPlan)) {
     if (dev < 64)
         done[which][dev].store(true, std::memory_order_release);
     return true;
-}
-
-// Launches a kernel that may start while the one before it in the stream still
-// runs (it waits for that one itself): its start-up costs no gap.
-bool follow(void (*kern)(AttendPlan), dim3 grid, int threads, size_t smem, cudaStream_t s, const AttendPlan &P) {
-    cudaLaunchAttribute attr[1];
-    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
-    attr[0].val.programmaticStreamSerializationAllowed = 1;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid;
-    cfg.blockDim = dim3((unsigned)threads);
-    cfg.dynamicSmemBytes = smem;
-    cfg.stream = s;
-    cfg.attrs = attr;
-    cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, kern, P) == cudaSuccess;
 }
 
 }  // namespace
