@@ -317,12 +317,14 @@ __global__ void __launch_bounds__(kRowThreads) lmc_move_kernel(const __grid_cons
 // eight columns, by lane: scores share few exponents, and one counter per bin
 // would serialise a warp's increments. Then each warp walks its own run of
 // tokens in order, and a token's place among the kept is the number kept
-// before it.
+// before it: a scan over the lanes adds up four blocks of 128 keys at once (a
+// byte each; by ballots and their bit counts it took 56 us, this 54).
 constexpr int kSelThreads = 512;
 constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kSelMaxCluster = 8;
 constexpr int kSelColumns = 8;
-constexpr int kSelPerSm = 3;  // CTAs an SM holds (96 rows of 131072: 2: 81 us, 3: 57 us, 4: 60 us, registers spilled)
+constexpr int kSelBlocks = 4;  // of 128 keys, counted at once by a warp at the end
+constexpr int kSelPerSm = 3;  // CTAs an SM holds (96 rows of 131072: two take 1.4 times as long, four 1.05: they spill)
 
 struct SelectPlan {
     const float *scores;
@@ -340,10 +342,8 @@ struct SelectPlan {
 
 // Keeps the order of the scores; NaN below every number, -0 as 0.
 __device__ __forceinline__ uint32_t order_key(float x) {
-    if (x != x)
-        return 0;  // below every number
-    const uint32_t u = __float_as_uint(x == 0.0f ? 0.0f : x);
-    return (u & 0x80000000u) ? ~u : (u | 0x80000000u);
+    const uint32_t u = __float_as_uint(__fadd_rn(x, 0.0f));  // -0 becomes 0
+    return x != x ? 0u : u ^ ((uint32_t)((int32_t)u >> 31) | 0x80000000u);
 }
 
 // The score of a key, but for the two that more than one pattern maps to.
@@ -356,7 +356,7 @@ struct alignas(16) SelectShared {
     union {
         uint32_t hist[256 * kSelColumns];
         uint32_t all[256];                // the cluster's totals, once hist is summed
-        uint32_t picked[kSelWarps][128];  // at the end: positions a warp takes of 128
+        uint16_t picked[kSelWarps][256];  // at the end: positions a warp takes of 256
     };
     uint32_t totals[2][256];              // this CTA's, read by the cluster
     uint32_t warp_above[kSelWarps];
@@ -442,9 +442,17 @@ __global__ void __launch_bounds__(kSelThreads, kSelPerSm) lmc_select_kernel(cons
             reinterpret_cast<uint4 *>(S.hist)[i] = make_uint4(0, 0, 0, 0);
         __syncthreads();
         uint32_t *const bins = S.hist + column;
+        const uint32_t bins_at = (uint32_t)__cvta_generic_to_shared(bins), last = ~mask;
+        // a key that matches differs from the prefix in the unknown bits only;
+        // predicated, for a branch per key costs twice the rest
         auto count = [&](uint32_t k) {
-            if ((k & mask) == prefix)
-                atomicAdd(bins + ((k >> shift) & 255u) * kSelColumns, 1u);
+            const uint32_t t = k ^ prefix;
+            asm volatile(
+                "{\n\t.reg .pred p;\n\t"
+                "setp.le.u32 p, %0, %1;\n\t"
+                "@p red.shared.add.u32 [%2], 1;\n\t}" ::"r"(t),
+                "r"(last), "r"(bins_at + (t >> shift) * (4 * kSelColumns))
+                : "memory");
         };
         if (kCached && pass == 0) {
             const float4 *const four = reinterpret_cast<const float4 *>(score + lo);
@@ -586,55 +594,12 @@ __global__ void __launch_bounds__(kSelThreads, kSelPerSm) lmc_select_kernel(cons
             a_before += other[0];
             e_before += other[1];
         }
-    const uint32_t lanes_below = (1u << lane) - 1u;
-    for (int32_t i0 = w0; i0 < w1; i0 += 32) {
-        const int32_t i = i0 + lane;
-        uint4 k = {};
-        if (i < w1)
-            k = keys_at<kCached>(keys, score + lo, i, mine);
-        const uint32_t v[4] = {k.x, k.y, k.z, k.w};
-        const bool real = i < w1;
-        // the warp's picks, close together, then written as one run
-        const uint32_t first = a_before + min(e_before, left);
-        uint32_t *const picked = S.picked[warp];
-        if (whole) {
-            uint32_t at = 0, picks = 0;
-#pragma unroll
-            for (int j = 0; j < 4; j++) {
-                const uint32_t va = __ballot_sync(0xffffffffu, v[j] > high);
-                at += __popc(va & lanes_below);
-                picks += __popc(va);
-            }
-            a_before += picks;
-#pragma unroll
-            for (int j = 0; j < 4; j++)
-                if (v[j] > high)
-                    picked[at++] = (uint32_t)(4 * i + j);
-        } else {
-            uint32_t a_at = a_before, e_at = e_before;
-#pragma unroll
-            for (int j = 0; j < 4; j++) {
-                const bool a = v[j] > high, e = real && v[j] >= prefix && !a;
-                const uint32_t va = __ballot_sync(0xffffffffu, a), ve = __ballot_sync(0xffffffffu, e);
-                a_at += __popc(va & lanes_below);
-                e_at += __popc(ve & lanes_below);
-                a_before += __popc(va);
-                e_before += __popc(ve);
-            }
-#pragma unroll
-            for (int j = 0; j < 4; j++) {
-                const bool a = v[j] > high, e = real && v[j] >= prefix && !a;
-                if (a || (e && e_at < left))
-                    picked[a_at + min(e_at, left) - first] = (uint32_t)(4 * i + j);
-                a_at += a;
-                e_at += e;
-            }
-        }
-        __syncwarp();
-        const int32_t picks = (int32_t)(a_before + min(e_before, left) - first);
+    uint16_t *const picked = S.picked[warp];
+    auto write = [&](int32_t at0, uint32_t first, int32_t picks) {
+        int32_t *const to = kept + first;
         for (int32_t q = lane; q < picks; q += 32) {
-            const uint32_t at = picked[q];
-            kept[first + q] = lo + (int32_t)at;
+            const int32_t at = at0 + picked[q];
+            to[q] = lo + at;
             if (kept_scores != nullptr) {
                 float x = 0.0f;
                 if (!kCached || !key_score(keys[at], x))
@@ -643,6 +608,82 @@ __global__ void __launch_bounds__(kSelThreads, kSelPerSm) lmc_select_kernel(cons
             }
         }
         __syncwarp();
+    };
+    for (int32_t i0 = w0; i0 < w1; i0 += 32 * kSelBlocks) {
+        // a lane's picks of kSelBlocks blocks of 128 keys, a byte each, summed
+        // over the lanes below at once
+        auto four = [&](int block) {
+            const int32_t i = i0 + 32 * block + lane;
+            return i < w1 ? keys_at<kCached>(keys, score + lo, i, mine) : make_uint4(0, 0, 0, 0);
+        };
+        auto sum_lanes = [&](uint32_t x) {
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const uint32_t y = __shfl_up_sync(0xffffffffu, x, o);
+                x += lane >= o ? y : 0u;
+            }
+            return x;
+        };
+        uint32_t a_mine = 0;
+#pragma unroll
+        for (int block = 0; block < kSelBlocks; block++) {
+            const uint4 k = four(block);
+            const uint32_t n = (k.x > high) + (k.y > high) + (k.z > high) + (k.w > high);
+            a_mine += n << (8 * block);
+        }
+        const uint32_t a_sum = sum_lanes(a_mine), a_all = __shfl_sync(0xffffffffu, a_sum, 31);
+        if (whole) {
+#pragma unroll
+            for (int pair = 0; pair < kSelBlocks; pair += 2) {
+                // the warp's picks of two blocks, close together, then written as one run
+                uint32_t picks = 0;
+#pragma unroll
+                for (int block = pair; block < pair + 2; block++) {
+                    const uint4 k = four(block);
+                    const uint32_t v[4] = {k.x, k.y, k.z, k.w};
+                    uint16_t *to = picked + picks + ((a_sum - a_mine) >> (8 * block) & 255u);
+#pragma unroll
+                    for (int j = 0; j < 4; j++)
+                        if (v[j] > high)
+                            *to++ = (uint16_t)(4 * (32 * block + lane) + j);
+                    picks += a_all >> (8 * block) & 255u;
+                }
+                __syncwarp();
+                write(4 * i0, a_before, (int32_t)picks);
+                a_before += picks;
+            }
+            continue;
+        }
+        uint32_t e_mine = 0;
+#pragma unroll
+        for (int block = 0; block < kSelBlocks; block++) {
+            const uint4 k = four(block);
+            const uint32_t n = (k.x >= prefix) + (k.y >= prefix) + (k.z >= prefix) + (k.w >= prefix);
+            e_mine += (i0 + 32 * block + lane < w1 ? n : 0u) << (8 * block);
+        }
+        e_mine -= a_mine;
+        const uint32_t e_sum = sum_lanes(e_mine), e_all = __shfl_sync(0xffffffffu, e_sum, 31);
+#pragma unroll 1
+        for (int block = 0; block < kSelBlocks; block++) {
+            const uint32_t first = a_before + min(e_before, left);
+            const uint4 k = four(block);
+            const uint32_t v[4] = {k.x, k.y, k.z, k.w};
+            const bool real = i0 + 32 * block + lane < w1;
+            uint32_t a_at = a_before + ((a_sum - a_mine) >> (8 * block) & 255u);
+            uint32_t e_at = e_before + ((e_sum - e_mine) >> (8 * block) & 255u);
+#pragma unroll
+            for (int j = 0; j < 4; j++) {
+                const bool a = v[j] > high, e = real && v[j] >= prefix && !a;
+                if (a || (e && e_at < left))
+                    picked[a_at + min(e_at, left) - first] = (uint16_t)(4 * (32 * block + lane) + j);
+                a_at += a;
+                e_at += e;
+            }
+            a_before += a_all >> (8 * block) & 255u;
+            e_before += e_all >> (8 * block) & 255u;
+            __syncwarp();
+            write(4 * i0, first, (int32_t)(a_before + min(e_before, left) - first));
+        }
     }
     cluster.sync();  // no CTA leaves while another may read its counts
 }
