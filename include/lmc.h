@@ -479,7 +479,8 @@ typedef struct {
     int64_t out_head_stride;
     float *lse;              /* device [num_requests][num_heads], or NULL */
     int64_t lse_request_stride;
-    float *weights;          /* device [num_requests][>= max_length], or NULL */
+    float *weights;          /* device [num_requests][>= max_length], or NULL; rows may
+                                not overlap */
     int64_t weights_request_stride;
     int32_t q_dtype;         /* LMC_E_BF16 or LMC_E_F16; the entries' type where they
                                 are of 16 bits */
@@ -491,8 +492,11 @@ typedef struct {
 /* Entries: entry_dim a multiple of 16, at most 576; the layer's base, stride
  * and the pool 16-byte aligned. `workspace` is device memory of at least
  * lmc_attend_workspace bytes, 256-byte aligned; its content does not matter
- * and calls that may run at the same time each need their own. Asynchronous
- * on `stream`; results do not depend on anything but the arguments (repeated
+ * and calls that may run at the same time each need their own. At most 65535
+ * requests and heads; q's strides are > 0 and out's at least value_dim where
+ * there is more than one request or head; OVERFLOW where the requests could
+ * have 2^31 tiles (of 64 tokens, or of a smaller page) or more. out must not
+ * overlap q. Asynchronous on `stream`; results do not depend on anything but the arguments (repeated
  * calls give the same bits). Status: BAD_JOB (a length below 0, above
  * max_length or past the table: that request's rows of out, lse and weights
  * are left as they were), NO_BLOCK, BLOCK_OOR, TIMEOUT.
