@@ -32,7 +32,10 @@ bool follow(void (*kern)(Plan), dim3 grid, int threads, size_t smem, cudaStream_
     cfg.stream = stream;
     cfg.attrs = attr;
     cfg.numAttrs = cluster > 0 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, kern, P) == cudaSuccess;
+    if (cudaLaunchKernelEx(&cfg, kern, P) == cudaSuccess)
+        return true;
+    cudaGetLastError();  // the caller reports it: not again at another call
+    return false;
 }
 
 }  // namespace lmc
