@@ -149,6 +149,7 @@ struct AttendPlan {
     uint32_t span_inverse, tiles_inverse;  // see quotient()
     int32_t cols;              // CTAs along the length
     int32_t whole;             // a request is one CTA's; nothing is joined
+    int32_t brief;             // the stream's next kernel, another call's, may be brought in at once
     int32_t head_groups, group_heads;  // heads of a CTA
     int32_t padded_heads;      // rounded up to 16
     int32_t panels;            // of an entry in shared memory
@@ -1258,6 +1259,8 @@ __global__ void __launch_bounds__(kThreads<kFp8>, 1) lmc_attend_kernel(const __g
     __syncthreads();
     fence_after();
     wait_for_launch();
+    if (P.brief)
+        let_next_start();
 
     if (warp < kSoftWarps) {
         if (kFp8)
@@ -1705,6 +1708,10 @@ extern "C" int lmc_attend(const lmc_layout *L, const lmc_entries *e, const void 
     P.log2_scale = (float)((double)a->softmax_scale * e->scale * 1.4426950408889634);
     const int64_t turns = ((R + P.cols - 1) / P.cols) * most_tiles(P);
     P.whole = turns <= kWholeTiles && turns <= (R * most_tiles(P) + P.cols - 1) / P.cols + kWholeExtra;
+    if (P.whole) {  // no CTA without a request (32 fp8 requests of 128 tokens 15.3 -> 14.4 us with the next)
+        P.cols = (int32_t)std::min<int64_t>(P.cols, R);
+        P.brief = P.weights == nullptr;
+    }
     const int64_t fixed = (int64_t)((P.E + 63) / 64) * P.padded_heads * 128 + P.padded_heads * 128 + sizeof(Control) + 1024;
     P.stages = (int32_t)std::min<int64_t>(kMaxStages, (kSmemLimit - fixed) / ((int64_t)P.panels * kPanel));
     const size_t smem = std::max<size_t>((size_t)((P.E + 63) / 64) * P.padded_heads * 128 + (size_t)P.padded_heads * 128 +
