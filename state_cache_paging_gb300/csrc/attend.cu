@@ -684,11 +684,20 @@ __device__ __forceinline__ void load_fp8(const AttendPlan &P, Control &C, const 
     const int my_page = P.pages_per_tile == 1 ? 0 : row / P.block_size;
     const int my_row = row - my_page * P.block_size;
 
+    Tile T;
     auto find = [&](int j) {
-        const Tile T = tile_at(P, W.first + j);
-        const int block = resolve(P, W, T, next_valid, bad, last);
-        const int64_t b = __shfl_sync(0xffffffffu, block, my_page & 31);
-        src = P.pool + b * P.block_stride + (int64_t)(T.row0 + my_row) * P.token_bytes + piece * 16;
+        if (j > 0 && T.row0 + 2 * kTile <= P.span && T.t0 + 2 * kTile <= W.range.L && last.block >= 0) {
+            // most often: a whole tile behind another of the same page
+            T.row0 += kTile;
+            T.t0 += kTile;
+            src += kTile * P.token_bytes;
+            next_valid = ~0ull;
+        } else {
+            T = tile_at(P, W.first + j);
+            const int block = resolve(P, W, T, next_valid, bad, last);
+            const int64_t b = __shfl_sync(0xffffffffu, block, my_page & 31);
+            src = P.pool + b * P.block_stride + (int64_t)(T.row0 + my_row) * P.token_bytes + piece * 16;
+        }
         if (warp == 0 && lane == 0)
             *(volatile int32_t *)&C.loading = (int)n + (j > 0);
     };
