@@ -83,7 +83,7 @@ constexpr int kFp8Loaders = 8;        // warps, eight of a tile's rows each
 // wanted).
 constexpr int kAhead = 1;
 constexpr int kNap = 300;             // ns between looks at the loaders' progress (100: the same, 800: 63.8 / 169 us)
-constexpr int kEarlyPanels = 5;       // of an fp8 tile, widened before its stage is free (6: the same, 8: 126 -> 133 us)
+constexpr int kEarlyPanels = 5;       // of an fp8 tile, widened before its stage is free (3: 1 us more, 6: 6, 7: 11 of 122)
 // Registers per thread of an fp8 CTA's warpgroups: 2 x 80 + 56 + 2 x 128 of the
 // 5 x 96 it starts with (fewer for the softmax or the loaders spill).
 constexpr int kSoftRegisters = 80, kIssueRegisters = 56, kLoadRegisters = 128;
