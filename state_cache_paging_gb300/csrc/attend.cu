@@ -1259,6 +1259,10 @@ __global__ void __launch_bounds__(kThreads<kFp8>, 1) lmc_attend_kernel(const __g
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
         fence_async();
     }
+    // Tensor memory is asked for after the wait: a kernel before this one that
+    // has yet to ask for its own would wait for this one, which waits for it.
+    // (And the next one may only start when this one's is had.)
+    wait_for_launch();
     if (warp == kScoreWarp) {
         asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(&C.tmem))
                      : "memory");
@@ -1267,7 +1271,6 @@ __global__ void __launch_bounds__(kThreads<kFp8>, 1) lmc_attend_kernel(const __g
     fence_before();
     __syncthreads();
     fence_after();
-    wait_for_launch();
     if (P.brief)
         let_next_start();
 
