@@ -148,7 +148,8 @@ struct AttendPlan {
     int32_t tiles_per_span;
     uint32_t span_inverse, tiles_inverse;  // see quotient()
     int32_t cols;              // CTAs along the length
-    int32_t whole;             // a request is one CTA's; nothing is joined
+    uint32_t cols_inverse;
+    int32_t whole;             // > 0: a CTA has as many requests to itself; nothing is joined
     int32_t brief;             // the stream's next kernel, another call's, may be brought in at once
     int32_t head_groups, group_heads;  // heads of a CTA
     int32_t padded_heads;      // rounded up to 16
@@ -225,8 +226,13 @@ struct Walk {
     __device__ __forceinline__ void init(const AttendPlan &P, int col) {
         r0 = 0;
         load(P, 0);
-        if (P.whole) {  // requests [a, b), none of them shared
-            const int a = (int)((int64_t)col * P.R / P.cols), b = (int)((int64_t)(col + 1) * P.R / P.cols);
+        if (P.whole > 0) {  // requests [a, b), none of them shared
+            const int a = col * P.whole, b = min(a + P.whole, P.R);
+            if (b <= 32) {
+                pos = __shfl_sync(0xffffffffu, start, a);
+                end = __shfl_sync(0xffffffffu, stop, b - 1);
+                return;
+            }
             int before = 0, here = 0;
             for (int i = threadIdx.x & 31; i < b; i += 32)
                 (i < a ? before : here) += tiles_of(P, range_of(P, i));
@@ -240,7 +246,7 @@ struct Walk {
         total = __reduce_add_sync(0xffffffffu, total) + __shfl_sync(0xffffffffu, stop, 31);
         // equal shares, so only the last CTAs may have none (in 64 bits: a
         // share times a CTA's number may pass the total)
-        const int64_t each = (total + P.cols - 1) / P.cols;
+        const int64_t each = quotient(total + P.cols - 1, P.cols, P.cols_inverse);
         pos = (int)min(col * each, (int64_t)total);
         end = (int)min(pos + each, (int64_t)total);
     }
@@ -1707,7 +1713,7 @@ extern "C" int lmc_attend(const lmc_layout *L, const lmc_entries *e, const void 
     auto inverse = [](int32_t d) { return d == 1 ? ~0u : (uint32_t)(((uint64_t)1 << 32) / (uint32_t)d); };
     P.span_inverse = inverse(P.span);
     P.tiles_inverse = inverse(P.tiles_per_span);
-    if (R * (P.max_length / P.span + 1) * P.tiles_per_span > INT32_MAX)
+    if (R * (P.max_length / P.span + 1) * P.tiles_per_span > INT32_MAX - kMaxCols)
         return LMC_ERR_OVERFLOW;
     P.head_groups = W.head_groups;
     P.group_heads = W.group_heads;
@@ -1719,11 +1725,13 @@ extern "C" int lmc_attend(const lmc_layout *L, const lmc_entries *e, const void 
     P.scale = e->scale;
     P.log2_scale = (float)((double)a->softmax_scale * e->scale * 1.4426950408889634);
     const int64_t turns = ((R + P.cols - 1) / P.cols) * most_tiles(P);
-    P.whole = turns <= kWholeTiles && turns <= (R * most_tiles(P) + P.cols - 1) / P.cols + kWholeExtra;
-    if (P.whole) {  // no CTA without a request (32 fp8 requests of 128 tokens 15.3 -> 14.4 us with the next)
-        P.cols = (int32_t)std::min<int64_t>(P.cols, R);
+    if (turns <= kWholeTiles && turns <= (R * most_tiles(P) + P.cols - 1) / P.cols + kWholeExtra) {
+        // no CTA without a request (32 fp8 requests of 128 tokens 15.3 -> 14.4 us with the next line)
+        P.whole = (int32_t)((R + P.cols - 1) / P.cols);
+        P.cols = (int32_t)((R + P.whole - 1) / P.whole);
         P.brief = P.weights == nullptr;
     }
+    P.cols_inverse = inverse(P.cols);
     const int64_t fixed = (int64_t)((P.E + 63) / 64) * P.padded_heads * 128 + P.padded_heads * 128 + sizeof(Control) + 1024;
     P.stages = (int32_t)std::min<int64_t>(kMaxStages, (kSmemLimit - fixed) / ((int64_t)P.panels * kPanel));
     const size_t smem = std::max<size_t>((size_t)((P.E + 63) / 64) * P.padded_heads * 128 + (size_t)P.padded_heads * 128 +
