@@ -1754,18 +1754,20 @@ extern "C" int lmc_attend(const lmc_layout *L, const lmc_entries *e, const void 
     if (!allow_shared_memory(fp8 ? 2 : bf16 ? 1 : 0, kern))
         return LMC_ERR_CUDA;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
-    // A warp per head where that is a few warps an SM; else a request has many
-    // parts and the heads are few (4 x 131072 tokens, 64 heads: 38 parts each,
-    // 12 us by a warp per head, 6 us by sixteen; 32 requests of 32 heads, 5
-    // parts each: 12 us by sixteen).
-    const unsigned splits = (unsigned)std::min<int64_t>(P.cols, R);
-    const bool few = (int64_t)splits * H < 4 * (int64_t)sms;
-    if (!follow(kern, dim3((unsigned)(P.cols * P.head_groups)), fp8 ? kThreads<true> : kThreads<false>, smem, s,
-                P) ||
-        P.whole ? false : !(few ? follow(lmc_attend_join_kernel<4>, dim3(splits, (unsigned)H), kJoinWarps<4> * 32, 0, s, P)
-              : follow(lmc_attend_join_kernel<1>, dim3(splits, (unsigned)((H + kJoinWarps<1> - 1) / kJoinWarps<1>)),
-                       kJoinWarps<1> * 32, 0, s, P)))
+    if (!follow(kern, dim3((unsigned)(P.cols * P.head_groups)), fp8 ? kThreads<true> : kThreads<false>, smem, s, P))
         return LMC_ERR_CUDA;
+    if (P.whole == 0) {
+        // A warp per head where that is a few warps an SM; else a request has
+        // many parts and the heads are few (4 x 131072 tokens, 64 heads: 38
+        // parts each, 12 us by a warp per head, 6 us by sixteen; 32 requests of
+        // 32 heads, 5 parts each: 12 us by sixteen).
+        const unsigned splits = (unsigned)std::min<int64_t>(P.cols, R);
+        const bool few = (int64_t)splits * H < 4 * (int64_t)sms;
+        if (!(few ? follow(lmc_attend_join_kernel<4>, dim3(splits, (unsigned)H), kJoinWarps<4> * 32, 0, s, P)
+                  : follow(lmc_attend_join_kernel<1>, dim3(splits, (unsigned)((H + kJoinWarps<1> - 1) / kJoinWarps<1>)),
+                           kJoinWarps<1> * 32, 0, s, P)))
+            return LMC_ERR_CUDA;
+    }
     if (P.weights != nullptr) {
         const int64_t tokens = P.window > 0 ? std::min(P.max_length, P.window) : std::max(P.max_length, 1);
         if (!follow(lmc_attend_weights_kernel,
