@@ -1556,7 +1556,7 @@ int work_space(const lmc_layout *L, int32_t layer, int64_t R, int64_t H, int64_t
 // equal share. (Graphs of calls of 32 heads, shared out and whole: one request
 // of 128 tokens 10.5 and 9.5 us, of 256 10.7 and 12.3; 152 requests of 128
 // tokens 14.1 and 12.1, of 256 17.2 and 15.1; 256 requests of 128 tokens 19.8
-// and 18.6. More tiles gain as much where all lengths are near the longest, but
+// and 18.6. Since then the whole ones gained half a microsecond more. More tiles gain as much where all lengths are near the longest, but
 // they may not be.)
 constexpr int kWholeTiles = 4, kWholeExtra = 2;
 
