@@ -1608,23 +1608,6 @@ bool tensor_map(CUtensorMap *map, bool bf16, const void *base, int64_t values, i
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-// Lets the attention kernels take a whole SM's shared memory (once per kernel
-// and device: the call costs as much as a launch).
-bool allow_shared_memory(int which, void (*kern)(AttendPlan)) {
-    static std::atomic<bool> done[3][64];
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess)
-        return false;
-    if (dev < 64 && done[which][dev].load(std::memory_order_acquire))
-        return true;
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             kSmemLimit - (int)((sizeof(Control) + 1023) / 1024 * 1024)) != cudaSuccess)
-        return false;
-    if (dev < 64)
-        done[which][dev].store(true, std::memory_order_release);
-    return true;
-}
-
 }  // namespace
 
 extern "C" int lmc_attend_workspace(const lmc_layout *L, int32_t layer, int32_t num_requests, int32_t num_heads,
@@ -1751,7 +1734,9 @@ extern "C" int lmc_attend(const lmc_layout *L, const lmc_entries *e, const void 
                              tile ? kTile : (int)N, whole && tile)))
         return LMC_ERR_CUDA;
     auto kern = fp8 ? lmc_attend_kernel<false, true> : bf16 ? lmc_attend_kernel<true, false> : lmc_attend_kernel<false, false>;
-    if (!allow_shared_memory(fp8 ? 2 : bf16 ? 1 : 0, kern))
+    static std::atomic<uint64_t> allowed[3];
+    if (!lmc::allow_shared_memory(allowed[fp8 ? 2 : bf16 ? 1 : 0], kern,
+                                  kSmemLimit - (int)((sizeof(Control) + 1023) / 1024 * 1024)))
         return LMC_ERR_CUDA;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (!follow(kern, dim3((unsigned)(P.cols * P.head_groups)), fp8 ? kThreads<true> : kThreads<false>, smem, s, P))

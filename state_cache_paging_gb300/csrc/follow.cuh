@@ -4,6 +4,9 @@
 
 #include <cuda_runtime.h>
 
+#include <atomic>
+#include <cstdint>
+
 namespace lmc {
 
 // A kernel launched by follow() waits with the first for the one before it in
@@ -37,6 +40,24 @@ bool follow(void (*kern)(Plan), dim3 grid, int threads, size_t smem, cudaStream_
         return true;
     cudaGetLastError();  // the caller reports it: not again at another call
     return false;
+}
+
+// Lets a kernel's launches take up to `bytes` of dynamic shared memory. The
+// limit belongs to the kernel, for all host threads, and the call costs as much
+// as a launch: so every caller gives a kernel's largest, and it is set once per
+// device (`done`: a bit for each, of this kernel).
+template <typename Plan>
+bool allow_shared_memory(std::atomic<uint64_t> &done, void (*kern)(Plan), int bytes) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess)
+        return false;
+    const uint64_t bit = dev < 64 ? (uint64_t)1 << dev : 0;
+    if (done.load(std::memory_order_acquire) & bit)
+        return true;
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
+        return false;
+    done.fetch_or(bit, std::memory_order_release);
+    return true;
 }
 
 }  // namespace lmc

@@ -11,6 +11,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 #include <cstring>
@@ -324,6 +325,7 @@ constexpr int kSelWarps = kSelThreads / 32;
 constexpr int kSelMaxCluster = 8;
 constexpr int kSelColumns = 8;
 constexpr int kSelBlocks = 4;  // of 128 keys, counted at once by a warp at the end
+constexpr int kSmemLimit = 227 * 1024;
 constexpr int kSelPerSm = 3;  // CTAs an SM holds (96 rows of 131072: two take 1.4 times as long, four 1.05: they spill)
 
 struct SelectPlan {
@@ -891,14 +893,15 @@ extern "C" int lmc_select_tokens(const float *scores, int64_t set_stride, int64_
            (max_length > (int64_t)c * 16384 || (rows * c < sms && max_length > (int64_t)c * 2048)))
         c *= 2;
     P.cluster = c;
-    const int64_t most = 227 * 1024 - (int64_t)sizeof(SelectShared);
+    const int64_t most = kSmemLimit - (int64_t)sizeof(SelectShared);
     const int64_t want = ((max_length + c - 1) / c + 7) / 4 * 16;  // a part is rounded up to fours
     const bool cached = want <= most;
     const size_t smem = sizeof(SelectShared) + (cached ? (size_t)(want + 15) / 16 * 16 : 0);
     if (rows * c > INT32_MAX)
         return LMC_ERR_INVALID_ARG;
     auto kern = cached ? lmc_select_kernel<true> : lmc_select_kernel<false>;
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem) != cudaSuccess)
+    static std::atomic<uint64_t> allowed[2];
+    if (!lmc::allow_shared_memory(allowed[cached], kern, kSmemLimit))
         return LMC_ERR_CUDA;
     return lmc::follow(kern, dim3((unsigned)(rows * c)), kSelThreads, smem, static_cast<cudaStream_t>(stream), P,
                        (unsigned)c)

@@ -1,0 +1,91 @@
+"""What the token operators' host code launches, without a GPU: their own
+translation units linked with a fake of the CUDA calls they make
+(tests/fake_cuda.cpp), which writes launches down and can be made to fail."""
+import ctypes
+import os
+import shutil
+import subprocess
+
+import numpy as np
+import pytest
+
+import workloads as W
+
+HERE = os.path.dirname(os.path.abspath(__file__))
+ROOT = os.path.dirname(HERE)
+CSRC = os.path.join(ROOT, "state_cache_paging_gb300", "csrc")
+CUDA = next((d for d in (os.environ.get("CUDA_HOME"), "/usr/local/cuda")
+             if d and os.path.exists(os.path.join(d, "include", "cuda_runtime.h"))), None)
+
+
+@pytest.fixture(scope="module")
+def fake_lib(lmc, tmp_path_factory):
+    nvcc = os.environ.get("NVCC", "nvcc")
+    if shutil.which(nvcc) is None or shutil.which("g++") is None or CUDA is None:
+        pytest.skip("the CUDA compiler is not available")
+    d = tmp_path_factory.mktemp("fake")
+    inc = ["-I", os.path.join(ROOT, "include"), "-I", CSRC]
+    cmds = [[nvcc, "-O1", "-std=c++17", "-gencode", "arch=compute_103a,code=compute_103a", "-Xcompiler", "-fPIC", *inc,
+             "-c", os.path.join(CSRC, f"{u}.cu"), "-o", str(d / f"{u}.o")] for u in ("tokens", "attend")]
+    cmds += [["g++", "-O1", "-std=c++17", "-fPIC", *inc, "-I", os.path.join(CUDA, "include"), "-c", src, "-o",
+              str(d / (os.path.basename(src)[:-4] + ".o"))]
+             for src in (os.path.join(CSRC, "layout.cpp"), os.path.join(CSRC, "checks.cpp"),
+                         os.path.join(HERE, "fake_cuda.cpp"))]
+    procs = [subprocess.Popen(c, stdout=subprocess.PIPE, stderr=subprocess.STDOUT, text=True) for c in cmds]
+    for c, p in zip(cmds, procs):
+        out, _ = p.communicate()
+        assert p.returncode == 0, f"{' '.join(c)}\n{out}"
+    so = d / "libfake.so"
+    # -Bsymbolic: the fake's calls, whatever CUDA runtime is loaded beside it
+    subprocess.run(["g++", "-shared", "-Wl,-Bsymbolic", "-o", str(so), *map(str, sorted(d.glob("*.o")))], check=True,
+                   capture_output=True, text=True)
+    lib = ctypes.CDLL(str(so))
+    lib.fake_launch.restype = ctypes.c_char_p
+    for name in ("lmc_select_tokens", "lmc_attend", "lmc_attend_workspace", "lmc_append", "lmc_move_tokens"):
+        getattr(lib, name).argtypes = getattr(lmc._lib, name).argtypes
+    return lib
+
+
+@pytest.fixture()
+def fake(fake_lib):
+    fake_lib.fake_reset()
+    return fake_lib
+
+
+@pytest.fixture()
+def env(lmc):
+    layers = [W.kda(768, 3, 4, 64), W.mla(1152), W.swa(64, 128), W.mla(576)]
+    L = lmc.lmc_layout_build(layers, 64, False, 1 << 28)
+    buf = np.zeros(8192, dtype=np.uint8)
+    return L, (buf.ctypes.data + 255) // 256 * 256, buf
+
+
+def launches(lib):
+    out = []
+    for i in range(lib.fake_launches()):
+        x = (ctypes.c_longlong * 5)()
+        name = lib.fake_launch(i, x).decode()
+        out.append((name, tuple(x[:3]), x[3], x[4]))
+    return out
+
+
+def select(lib, base, sets=1, requests=1, most=100, budget=4, recent=1, **kw):
+    a = dict(scores=base, kept=base + 512, ks=base + 1024, kl=base + 1536, lengths=base + 2048, status=base + 2560)
+    a.update(kw)
+    return lib.lmc_select_tokens(a["scores"], most * requests, most, sets, requests, a["lengths"], most, budget, recent,
+                                 a["kept"], a["ks"], a["kl"], a["status"], None)
+
+
+def test_a_selection_between_anothers_preparation_and_launch(lmc, fake, env):
+    """Two host threads select at once: a call of short rows that comes between
+    another's preparation and its launch takes nothing from it (the shared
+    memory a kernel may take belongs to the kernel, not to the call)."""
+    _, base, _ = env
+    inner = []
+    for sizes in ((131_072, 100), (300_000, 2_000_000), (100, 131_072)):
+        fake.fake_reset()
+        hook = ctypes.CFUNCTYPE(None)(lambda: inner.append(select(fake, base, most=sizes[1])))
+        fake.fake_before_launch(hook)
+        assert select(fake, base, most=sizes[0]) == lmc.LMC_OK, sizes
+        assert inner.pop() == lmc.LMC_OK
+        assert len(launches(fake)) == 2
