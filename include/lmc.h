@@ -64,7 +64,8 @@ extern "C" {
 #define LMC_ERR_OVERFLOW (-6)     /* a size does not fit 64-bit arithmetic */
 #define LMC_ERR_BUDGET (-7)       /* scheduler budget outside the allowed range */
 #define LMC_ERR_OVERLAP (-8)      /* copies that would race: a block written twice, or
-                                     written by one copy and read by another */
+                                     written by one copy and read by another; an
+                                     output over an input (lmc_select_tokens) */
 
 /* ---- device status bits (OR-ed into *status) ----------------------------- */
 #define LMC_ST_BLOCK_OOR 0x1u   /* block id < -1 or >= num_blocks */
@@ -520,9 +521,13 @@ LMC_API int lmc_attend_workspace(const lmc_layout *layout, int32_t layer, int32_
  * scores, kept_lengths[r] = min(L, budget); elements of kept past that are
  * left as they were. scores: device, strides in elements between sets and
  * requests (no length is above max_length); kept, kept_scores: device
- * [num_sets][num_requests][budget], contiguous; 0 <= recent <= budget.
+ * [num_sets][num_requests][budget], contiguous; 0 <= recent <= budget. With
+ * no sets or no requests nothing is done. kept, kept_scores and kept_lengths
+ * may overlap neither one another nor lengths nor the scores (from the first
+ * to the last, strides included): OVERLAP; to cut lengths in place, copy
+ * kept_lengths over them afterwards.
  * Status: BAD_JOB (a length below 0 or above max_length: nothing is written
- * for that request). Errors: INVALID_ARG, ALIGN, CUDA. */
+ * for that request). Errors: INVALID_ARG, ALIGN, OVERLAP, OVERFLOW, CUDA. */
 LMC_API int lmc_select_tokens(const float *scores, int64_t set_stride, int64_t request_stride, int32_t num_sets,
                               int32_t num_requests, const int32_t *lengths, int64_t max_length, int64_t budget,
                               int64_t recent, int32_t *kept, float *kept_scores, int32_t *kept_lengths,

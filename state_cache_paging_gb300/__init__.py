@@ -687,7 +687,7 @@ def lmc_select_tokens(scores, lengths, budget: int, recent: int, kept, kept_scor
     requests, >= longest length], lengths: int32 [requests]; kept (int32) and
     kept_scores (float32, or None) [sets, requests, budget] receive the kept
     positions in increasing order and their scores, kept_lengths (int32
-    [requests]) how many there are."""
+    [requests], not the memory of lengths) how many there are."""
     home = _home("scores", scores)
     shape, stride = scores.shape, scores.stride()
     if len(shape) != 3 or scores.dtype != _torch.float32 or (stride[2] != 1 and shape[2] > 1):

@@ -718,6 +718,15 @@ int piece_bytes(std::initializer_list<int64_t> values) {
     return (all & 15) == 0 ? 16 : (all & 3) == 0 ? 4 : 1;
 }
 
+// Bytes [at, end) of 4-byte elements that a call reads or writes.
+struct Extent {
+    uint64_t at, end;
+    bool meets(const Extent &o) const { return std::max(at, o.at) < std::min(end, o.end); }
+};
+Extent extent(const void *p, int64_t elements) {
+    return Extent{(uint64_t)(uintptr_t)p, (uint64_t)(uintptr_t)p + (p == nullptr ? 0 : 4 * (uint64_t)elements)};
+}
+
 }  // namespace
 
 namespace lmc {
@@ -869,6 +878,19 @@ extern "C" int lmc_select_tokens(const float *scores, int64_t set_stride, int64_
     if (lengths == nullptr || kept_lengths == nullptr || (scores == nullptr && max_length > 0) ||
         (kept == nullptr && budget > 0))
         return LMC_ERR_INVALID_ARG;
+    // A row is read by several CTAs, its length by those of every set: neither
+    // may be written meanwhile.
+    const int64_t rows = (int64_t)num_sets * num_requests;
+    int64_t sets_end, requests_end, kept_count;
+    if (!lmc::mul_ok(set_stride, num_sets - 1, &sets_end) || !lmc::mul_ok(request_stride, num_requests - 1, &requests_end) ||
+        !lmc::add_ok(sets_end, requests_end, &sets_end) || sets_end > INT64_MAX / 8 || !lmc::mul_ok(rows, budget, &kept_count) ||
+        kept_count > INT64_MAX / 8)
+        return LMC_ERR_OVERFLOW;
+    const Extent in[2] = {extent(scores, max_length > 0 ? sets_end + max_length : 0), extent(lengths, num_requests)};
+    const Extent out[3] = {extent(kept, kept_count), extent(kept_scores, kept_count), extent(kept_lengths, num_requests)};
+    for (int i = 0; i < 3; i++)
+        if (out[i].meets(in[0]) || out[i].meets(in[1]) || out[i].meets(out[(i + 1) % 3]))
+            return LMC_ERR_OVERLAP;
     const int sms = lmc::sm_count();
     if (sms <= 0)
         return LMC_ERR_CUDA;
@@ -885,7 +907,6 @@ extern "C" int lmc_select_tokens(const float *scores, int64_t set_stride, int64_
     P.budget = (int32_t)budget;
     P.recent = (int32_t)recent;
     P.num_requests = num_requests;
-    const int64_t rows = (int64_t)num_sets * num_requests;
     // 16384 keys (64 KB) per CTA let two CTAs share an SM; fewer where there
     // are not enough rows for all SMs
     int c = 1;

@@ -70,7 +70,9 @@ def launches(lib):
 
 
 def select(lib, base, sets=1, requests=1, most=100, budget=4, recent=1, **kw):
-    a = dict(scores=base, kept=base + 512, ks=base + 1024, kl=base + 1536, lengths=base + 2048, status=base + 2560)
+    # (addresses are only compared: nothing lies there)
+    a = dict(kept=base, ks=base + (1 << 30), kl=base + (2 << 30), lengths=base + (3 << 30), status=base + (4 << 30),
+             scores=base + (5 << 30))
     a.update(kw)
     return lib.lmc_select_tokens(a["scores"], most * requests, most, sets, requests, a["lengths"], most, budget, recent,
                                  a["kept"], a["ks"], a["kl"], a["status"], None)
@@ -89,3 +91,35 @@ def test_a_selection_between_anothers_preparation_and_launch(lmc, fake, env):
         assert select(fake, base, most=sizes[0]) == lmc.LMC_OK, sizes
         assert inner.pop() == lmc.LMC_OK
         assert len(launches(fake)) == 2
+
+
+@pytest.mark.parametrize("which,at", [
+    ("kl", "lengths"), ("kl", "lengths+4"), ("kept", "lengths"), ("ks", "lengths"), ("kept", "scores"),
+    ("ks", "scores"), ("ks", "scores+1596"), ("kl", "scores+1596"), ("ks", "kept"), ("kl", "kept+60"), ("kl", "ks+60")])
+def test_select_refuses_outputs_over_inputs_and_each_other(lmc, fake, env, which, at):
+    """Cutting the lengths in place is the obvious call: other CTAs still read
+    what one of them cuts. Two sets of two requests of 100 scores (400 floats)
+    and a budget of 4 (16 elements kept)."""
+    _, base, _ = env
+    place = dict(scores=base, kept=base + 1600, ks=base + 1664, kl=base + 1728, lengths=base + 1736)
+
+    def call(**kw):
+        a = {**place, **kw}
+        return fake.lmc_select_tokens(a["scores"], 200, 100, 2, 2, a["lengths"], 100, 4, 1, a["kept"], a["ks"], a["kl"],
+                                      base + 2000, None)
+
+    assert call() == call(ks=None) == lmc.LMC_OK  # side by side, to the byte
+    n = len(launches(fake))
+    name, _, off = at.partition("+")
+    assert call(**{which: place[name] + int(off or 0)}) == lmc.LMC_ERR_OVERLAP
+    assert len(launches(fake)) == n
+
+
+def test_select_of_nothing_overlaps_nothing(lmc, fake, env):
+    """Memory of no elements may lie anywhere; sizes past 64 bits are refused."""
+    _, base, _ = env
+    assert select(fake, base, budget=0, recent=0, kept=base + (5 << 30), ks=base + (3 << 30)) == lmc.LMC_OK
+    assert select(fake, base, most=0, scores=base) == lmc.LMC_OK
+    big = 1 << 62
+    assert fake.lmc_select_tokens(base, big, 100, 9, 1, base, 100, 4, 1, base, None, base, base, None) == \
+        lmc.LMC_ERR_OVERFLOW
