@@ -645,10 +645,12 @@ __device__ __forceinline__ void query_to_f16(const AttendPlan &P, Control &C, co
         }
         for (int o = 4; o > 0; o >>= 1)
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-        // 2^e with e = 14 - floor(log2(top)), kept within what one float
-        // holds; 1 where there is nothing to scale (zero, infinity)
+        // 2^e with e = 14 - floor(log2(top)), at least -113. 2^126 and its
+        // inverse are the last that normal floats hold: every bf16 is a multiple
+        // of 2^-133, so times that f16 holds it as it is. 1 where there is
+        // nothing to scale (zero, infinity)
         const int exponent = (int)(__float_as_uint(top) >> 23) - 127;
-        const int e = top == 0.0f || exponent == 128 ? 0 : max(-100, min(100, 14 - exponent));
+        const int e = top == 0.0f || exponent == 128 ? 0 : min(126, 14 - exponent);
         const float up = __uint_as_float((uint32_t)(127 + e) << 23);
         if (piece == 0)
             C.q_scale[h] = __uint_as_float((uint32_t)(127 - e) << 23);
