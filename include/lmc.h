@@ -466,7 +466,13 @@ LMC_API int lmc_append(const lmc_layout *layout, const lmc_entries *entries, voi
  * block are left out of the sums, with a status bit; a request whose tokens
  * are all missing gives out = 0, lse = -inf. Nothing outside the range is
  * read into a result, whatever its bytes. (out, lse) of disjoint parts of a
- * cache can be joined by their lse. */
+ * cache can be joined by their lse.
+ *
+ * Values that are not finite: a token whose logit is -inf has p = 0; a head all
+ * of whose logits are -inf is as one without tokens (p = 0, lse = -inf); a head
+ * with a logit of +inf or NaN has no softmax: its rows of out and lse, and all
+ * of the request's weights, become NaN. Where a token's value is infinite or
+ * NaN, p = 0 times it is NaN, as in any sum of products. */
 typedef struct {
     const int32_t *lengths;  /* device [num_requests] */
     int64_t max_length;      /* no length is above it (>= 1); it sizes the work

@@ -647,10 +647,11 @@ __device__ __forceinline__ void query_to_f16(const AttendPlan &P, Control &C, co
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
         // 2^e with e = 14 - floor(log2(top)), at least -113. 2^126 and its
         // inverse are the last that normal floats hold: every bf16 is a multiple
-        // of 2^-133, so times that f16 holds it as it is. 1 where there is
-        // nothing to scale (zero, infinity)
+        // of 2^-133, so times that f16 holds it as it is. Beside an infinity
+        // (e = -114) all finite values stay finite: what is lost of them does
+        // not show in logits that are infinite. 1 where all are zero
         const int exponent = (int)(__float_as_uint(top) >> 23) - 127;
-        const int e = top == 0.0f || exponent == 128 ? 0 : min(126, 14 - exponent);
+        const int e = top == 0.0f ? 0 : min(126, 14 - exponent);
         const float up = __uint_as_float((uint32_t)(127 + e) << 23);
         if (piece == 0)
             C.q_scale[h] = __uint_as_float((uint32_t)(127 - e) << 23);

@@ -1,5 +1,6 @@
 """Token operators on the GPU where they are easily got wrong: host threads
-side by side and the ends of the types' ranges."""
+side by side, the ends of the types' ranges and values that are not finite."""
+import math
 import threading
 
 import numpy as np
@@ -99,3 +100,82 @@ def test_attend_fp8_queries_over_the_whole_range(lmc, status, act, exponent):
     assert torch.isfinite(out).all() and torch.isfinite(lse).all()
     assert ((out[0] - o).abs() <= d_o).all(), float((out[0] - o).abs().max())
     assert ((lse[0] - l).abs() <= d_l).all(), float((lse[0] - l).abs().max())
+
+
+@pytest.mark.parametrize("n", [100, 5000])
+@pytest.mark.parametrize("cache", ["bf16", "f16"])
+def test_attend_infinite_keys(lmc, status, cache, n):
+    """One key with an infinity among its last values: a head that it gives a
+    logit of -inf goes on without that token, one that it gives +inf has no
+    softmax (NaN). n = 5000: the request is shared by several CTAs."""
+    rng = np.random.default_rng(n)
+    N, E, V, H = 64, 64, 32, 4
+    blocks = -(-n // N)
+    M = T.Model(lmc, E, cache, N, blocks=blocks)
+    table = T.tables([n], N, blocks, rng)
+    e = torch.from_numpy(rng.standard_normal((n, E)))
+    e[n // 2, 40] = math.inf
+    M.write(0, table, 0, 0, e)
+    q = torch.from_numpy(rng.standard_normal((1, H, E)))
+    q[0, :, 40] = torch.tensor([1.0, -1.0, -2.0, 0.5])
+    q = q.to(T.TYPES[cache])
+    out, lse = _call(lmc, M, table, [n], q.to(DEV), V, status, 0.125)
+    at = [t for t in range(n) if t != n // 2]
+    o, l, _, d_o, d_l, _ = T.attend(M.read(0, table, 0, at), q[0].double(), V, 0.125, 1.0, cache, cache)
+    for h in (1, 2):
+        assert ((out[0, h] - o[h]).abs() <= d_o[h]).all() and abs(lse[0, h] - l[h]) <= d_l[h]
+    for h in (0, 3):
+        assert torch.isnan(out[0, h]).all() and torch.isnan(lse[0, h])
+    # with weights, the heads that have a softmax alone; then one that has none
+    weights = torch.zeros((1, n), device=DEV)
+    _call(lmc, M, table, [n], q[:, 1:3].contiguous().to(DEV), V, status, 0.125, weights=weights)
+    assert weights[0, n // 2] == 0 and abs(float(weights.double().sum()) - 2) < 1e-4
+    _call(lmc, M, table, [n], q[:, :3].contiguous().to(DEV), V, status, 0.125, weights=weights)
+    assert torch.isnan(weights).all()
+
+
+@pytest.mark.parametrize("n", [100, 5000])
+@pytest.mark.parametrize("cache,act", [("bf16", "bf16"), ("f16", "f16"), ("e4m3", "bf16"), ("e4m3", "f16")])
+def test_attend_heads_whose_logits_are_all_minus_infinity(lmc, status, cache, act, n):
+    """Such a head is as one without tokens: zeros, lse of -inf, nothing added
+    to the weights, whatever other finite values its query holds (an fp8 cache
+    holds the query as f16: what f16 cannot hold must not become an infinity
+    of its own, which would make NaN beside the other)."""
+    rng = np.random.default_rng(n)
+    N, E, V, H = 64, 64, 32, 3
+    blocks = -(-n // N)
+    M = T.Model(lmc, E, cache, N, blocks=blocks)
+    table = T.tables([n], N, blocks, rng)
+    e = torch.from_numpy(rng.standard_normal((n, E)))
+    e[:, 40], e[:, 41] = 1.0, 1.0
+    M.write(0, table, 0, 0, e)
+    q = torch.from_numpy(rng.standard_normal((1, H, E)))
+    q[0, 0, 40], q[0, 0, 41] = -math.inf, 6e4 if act == "f16" else 1e30
+    q[0, 1, 40] = -math.inf
+    q = q.to(T.TYPES[act])
+    before = torch.from_numpy(rng.random((1, n))).float()
+    weights = before.to(DEV)
+    out, lse = _call(lmc, M, table, [n], q.to(DEV), V, status, 0.125, weights=weights)
+    assert (out[0, :2] == 0).all() and (lse[0, :2] == -math.inf).all()
+    o, l, w, d_o, d_l, d_w = T.attend(M.read(0, table, 0, list(range(n))), q[0, 2:].double(), V, 0.125, 1.0, cache, act)
+    assert ((out[0, 2:] - o).abs() <= d_o).all() and abs(lse[0, 2] - l[0]) <= d_l[0]
+    added = weights[0].cpu().double() - before[0].double()
+    # (the sum with what was there before is rounded once: at most half a step of 2)
+    assert ((added - w).abs() <= d_w + 2.0 ** -23).all()
+
+
+@pytest.mark.parametrize("cache", ["bf16", "e4m3"])
+def test_attend_nan_just_before_a_window(lmc, status, cache):
+    """Tokens before the window, in the window's first tile too, do not show."""
+    rng = np.random.default_rng(2)
+    N, E, V, H, n, window = 64, 64, 32, 4, 300, 70
+    M = T.Model(lmc, E, cache, N, window=window, blocks=5)
+    table = T.tables([n], N, 5, rng)
+    e = torch.from_numpy(rng.standard_normal((n, E)))
+    e[:n - window] = math.nan
+    M.write(0, table, 0, 0, e)
+    q = torch.from_numpy(rng.standard_normal((1, H, E))).to(torch.bfloat16)
+    out, lse = _call(lmc, M, table, [n], q.to(DEV), V, status, 0.125)
+    o, l, _, d_o, d_l, _ = T.attend(M.read(0, table, 0, list(range(n - window, n))), q[0].double(), V, 0.125, 1.0,
+                                    cache, "bf16")
+    assert ((out[0] - o).abs() <= d_o).all() and ((lse[0] - l).abs() <= d_l).all()
