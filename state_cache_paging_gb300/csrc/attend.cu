@@ -189,7 +189,7 @@ __device__ __forceinline__ int tile_of(const AttendPlan &P, int t) {
     return s * P.tiles_per_span + (t - s * P.span) / kTile;
 }
 
-__device__ __forceinline__ Range range_of(const AttendPlan &P, int r) { return range_for(P, __ldg(P.lengths + r)); }
+__device__ __forceinline__ Range range_of(const AttendPlan &P, int r) { return range_for(P, __ldca(P.lengths + r)); }
 
 __device__ __forceinline__ int tiles_of(const AttendPlan &P, const Range &g) {
     return !g.ok || g.L == 0 ? 0 : tile_of(P, g.L - 1) + 1 - tile_of(P, g.lo);
@@ -211,7 +211,7 @@ struct Walk {
 
     __device__ __forceinline__ void load(const AttendPlan &P, int base) {
         const int lane = threadIdx.x & 31;
-        length = r0 + lane < P.R ? __ldg(P.lengths + r0 + lane) : 0;
+        length = r0 + lane < P.R ? __ldca(P.lengths + r0 + lane) : 0;
         const int n = tiles_of(P, range_for(P, length));
         int sum = n;
         for (int o = 1; o < 32; o <<= 1) {
@@ -513,7 +513,7 @@ __device__ __forceinline__ int resolve(const AttendPlan &P, const Walk &W, const
     valid = bits(W.range.lo - T.t0, min(T.rows, W.range.L - T.t0));
     if (P.pages_per_tile == 1) {
         if (W.r != last.r || T.page != last.page) {
-            int block = __ldg(P.table + W.r * P.row_stride + T.page);
+            int block = P.table[W.r * P.row_stride + T.page];
             if (block < 0 || block >= P.num_blocks) {
                 bad |= block == -1 ? LMC_ST_NO_BLOCK : LMC_ST_BLOCK_OOR;
                 block = -1;
@@ -529,7 +529,7 @@ __device__ __forceinline__ int resolve(const AttendPlan &P, const Walk &W, const
     int block = -1;
     const int64_t p0 = ((int64_t)T.page + lane) * P.block_size;  // the page's tokens
     if (lane < P.pages_per_tile && p0 < W.range.L && p0 + P.block_size > W.range.lo) {
-        block = __ldg(P.table + W.r * P.row_stride + T.page + lane);
+        block = P.table[W.r * P.row_stride + T.page + lane];
         if (block < 0 || block >= P.num_blocks) {
             bad |= block == -1 ? LMC_ST_NO_BLOCK : LMC_ST_BLOCK_OOR;
             block = -1;
@@ -713,7 +713,7 @@ __device__ __forceinline__ void load_fp8(const AttendPlan &P, Control &C, const 
     auto load = [&](int i) {
         codes[i] = make_uint4(0, 0, 0, 0);
         if ((next_valid >> row & 1) && i * 4 + piece < chunks)
-            asm volatile("ld.global.nc.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+            asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
                          : "=r"(codes[i].x), "=r"(codes[i].y), "=r"(codes[i].z), "=r"(codes[i].w)
                          : "l"(src + i * 64));
     };
@@ -1486,7 +1486,7 @@ __global__ void __launch_bounds__(kWeightThreads) lmc_attend_weights_kernel(cons
     if (first + 4 * four < g.L - base) {
 #pragma unroll 8
         for (int h = part; h < P.H; h += kWeightParts) {
-            const float top = __ldg(lse + h);
+            const float top = __ldca(lse + h);
             const float4 v = __ldcs(reinterpret_cast<const float4 *>(x + h * P.logit_stride));
             if (top != -INFINITY) {
                 w.x += exp2_fast(v.x - top);

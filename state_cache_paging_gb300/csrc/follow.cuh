@@ -11,7 +11,10 @@ namespace lmc {
 
 // A kernel launched by follow() waits with the first for the one before it in
 // the stream to be done and its writes to be seen; it touches nothing in
-// global memory before that (its own arguments are no part of it). The second
+// global memory before that (its own arguments are no part of it). It is there
+// while the one before writes what it reads, so it reads nothing by the
+// read-only path (__ldg, ld.global.nc), which is for memory that does not change
+// in a kernel's lifetime, but by plain loads and __ldca. The second
 // lets the next one be brought in. The short kernels do that at once, which
 // hides its start-up; the attention kernel does not where its own joining (or
 // weighing) blocks would be what waits beside it (two requests of 517 tokens

@@ -47,7 +47,7 @@ __device__ __forceinline__ int64_t entry_offset(const Pages &G, const TokenTable
         bad |= LMC_ST_BAD_JOB;
         return -1;
     }
-    const int32_t block = __ldg(T.ptr + req * T.row_stride + page);
+    const int32_t block = __ldca(T.ptr + req * T.row_stride + page);
     if (block < 0 || block >= G.num_blocks) {
         bad |= block == -1 ? LMC_ST_NO_BLOCK : LMC_ST_BLOCK_OOR;
         return -1;
@@ -125,7 +125,7 @@ __device__ __forceinline__ int resolve_append(const AppendPlan &P, const uint8_t
     const int n = (int)min((int64_t)P.rows_per_cta, P.num_rows - first);
     if ((int)threadIdx.x < n) {
         const int64_t i = first + threadIdx.x;
-        const int32_t req = __ldg(P.requests + i);
+        const int32_t req = __ldca(P.requests + i);
         const uint8_t *s = nullptr;
         uint8_t *d = nullptr;
         if (req != -1) {
@@ -134,7 +134,7 @@ __device__ __forceinline__ int resolve_append(const AppendPlan &P, const uint8_t
             if (req < 0 || req >= P.num_requests)
                 bad = LMC_ST_BAD_JOB;
             else
-                off = entry_offset(P.pages, P.table, req, __ldg(P.positions + i), bad);
+                off = entry_offset(P.pages, P.table, req, __ldca(P.positions + i), bad);
             if (bad)
                 atomicOr(P.status, bad);
             if (off >= 0) {
@@ -275,7 +275,7 @@ __global__ void __launch_bounds__(kRowThreads) lmc_move_kernel(const __grid_cons
     const int64_t layer = unit / P.num_requests;
     lmc::wait_for_launch();
     lmc::let_next_start();
-    const int64_t kept = __ldg(P.kept_lengths + req);
+    const int64_t kept = __ldca(P.kept_lengths + req);
     if (kept < 0 || kept > P.max_kept) {
         if (threadIdx.x == 0)
             atomicOr(P.status, LMC_ST_BAD_JOB);
@@ -289,7 +289,7 @@ __global__ void __launch_bounds__(kRowThreads) lmc_move_kernel(const __grid_cons
         const int64_t j = first + threadIdx.x;
         uint32_t bad = 0;
         const int64_t from = entry_offset(P.pages, P.src, req,
-                                          __ldg(P.kept + layer * P.set_stride + req * P.request_stride + j), bad);
+                                          __ldca(P.kept + layer * P.set_stride + req * P.request_stride + j), bad);
         const int64_t to = entry_offset(P.pages, P.dst, req, (int32_t)j, bad);
         if (bad)
             atomicOr(P.status, bad);
@@ -379,7 +379,7 @@ __device__ __forceinline__ uint4 keys_at(const uint32_t *keys, const float *scor
         uint32_t k[4];
 #pragma unroll
         for (int j = 0; j < 4; j++)
-            k[j] = 4 * i + j < mine ? order_key(__ldg(score + 4 * i + j)) : 0u;
+            k[j] = 4 * i + j < mine ? order_key(__ldca(score + 4 * i + j)) : 0u;
         return make_uint4(k[0], k[1], k[2], k[3]);
     }
 }
@@ -398,7 +398,7 @@ __global__ void __launch_bounds__(kSelThreads, kSelPerSm) lmc_select_kernel(cons
     lmc::wait_for_launch();
     lmc::let_next_start();
     // uniform over the cluster, so leaving here leaves no CTA waiting
-    const int64_t L = __ldg(P.lengths + req);
+    const int64_t L = __ldca(P.lengths + req);
     if (L < 0 || L > P.max_length) {
         if (rank == 0 && tid == 0)
             atomicOr(P.status, LMC_ST_BAD_JOB);

@@ -123,3 +123,15 @@ def test_select_of_nothing_overlaps_nothing(lmc, fake, env):
     big = 1 << 62
     assert fake.lmc_select_tokens(base, big, 100, 9, 1, base, 100, 4, 1, base, None, base, base, None) == \
         lmc.LMC_ERR_OVERFLOW
+
+
+@pytest.mark.parametrize("unit", ["tokens.cu", "attend.cu"])
+def test_kernels_that_start_early_read_no_constant_memory(unit):
+    """These kernels are launched while the one before them may still write
+    what they read. The read-only path (__ldg, ld.global.nc, restrict) is for
+    memory that does not change while the kernel is there."""
+    import re
+    with open(os.path.join(CSRC, unit)) as f:
+        text = re.sub(r"//[^\n]*", "", f.read())
+    assert "follow(" in text
+    assert not re.findall(r"__ldg|\.nc\b|__restrict__", text)
