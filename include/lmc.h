@@ -508,7 +508,9 @@ typedef struct {
  * calls give the same bits). Status: BAD_JOB (a length below 0, above
  * max_length or past the table: that request's rows of out, lse and weights
  * are left as they were), NO_BLOCK, BLOCK_OOR, TIMEOUT.
- * Errors: INVALID_ARG, ALIGN, OVERFLOW, CUDA. */
+ * Errors: INVALID_ARG, ALIGN, OVERFLOW, CUDA. A call is up to three launches;
+ * where a later one is refused (CUDA) the earlier ones run: out and lse are
+ * then not defined, weights as they were (the last launch adds to them). */
 LMC_API int lmc_attend(const lmc_layout *layout, const lmc_entries *entries, const void *pool,
                        const lmc_attention *attention, void *workspace, int64_t workspace_bytes, uint32_t *status,
                        void *stream);

@@ -1763,5 +1763,5 @@ extern "C" int lmc_attend(const lmc_layout *L, const lmc_entries *e, const void 
                     P))
             return LMC_ERR_CUDA;
     }
-    return cudaGetLastError() == cudaSuccess ? LMC_OK : LMC_ERR_CUDA;
+    return LMC_OK;  // every launch was asked for its own error
 }

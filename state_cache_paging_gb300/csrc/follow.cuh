@@ -57,8 +57,10 @@ bool allow_shared_memory(std::atomic<uint64_t> &done, void (*kern)(Plan), int by
     const uint64_t bit = dev < 64 ? (uint64_t)1 << dev : 0;
     if (done.load(std::memory_order_acquire) & bit)
         return true;
-    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
+    if (cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess) {
+        cudaGetLastError();
         return false;
+    }
     done.fetch_or(bit, std::memory_order_release);
     return true;
 }

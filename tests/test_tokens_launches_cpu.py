@@ -135,3 +135,73 @@ def test_kernels_that_start_early_read_no_constant_memory(unit):
         text = re.sub(r"//[^\n]*", "", f.read())
     assert "follow(" in text
     assert not re.findall(r"__ldg|\.nc\b|__restrict__", text)
+
+
+def attend(lmc, lib, L, base, requests=2, heads=4, max_length=190, weights=False, cols=3, layer=1, scale=0.1, dtype=0,
+           entry_scale=1.0, ws=None, **kw):
+    """One call over addresses that are only compared. Layer 1 holds 576 16-bit
+    values, layer 3 as many fp8 codes."""
+    far = base + (1 << 40)
+    e = lmc.lmc_entries(layer, dtype, 576, requests, entry_scale, 0, lmc.lmc_block_table(far, cols, cols))
+    a = lmc.lmc_attention(far, max_length, base, 576 * heads, 576, far, 512 * heads, 512, None, 0,
+                          far if weights else None, max_length, lmc.LMC_E_BF16, heads, 512, scale)
+    n = ctypes.c_int64()
+    rc = lib.lmc_attend_workspace(L.handle, layer, requests, heads, 512, max_length, int(weights), ctypes.byref(n))
+    assert rc == lmc.LMC_OK
+    return lib.lmc_attend(L.handle, ctypes.byref(e), base, ctypes.byref(a), far, n.value, far, None)
+
+
+def test_attend_does_not_answer_for_another_calls_error(lmc, fake, env):
+    """An error that some earlier call left behind is neither reported (the
+    caller would make the call again and add the weights twice) nor cleared."""
+    L, base, _ = env
+    for kw in (dict(), dict(weights=True), dict(max_length=128, cols=2)):
+        fake.fake_reset()
+        fake.fake_set_last_error(98)
+        assert attend(lmc, fake, L, base, **kw) == lmc.LMC_OK
+        assert fake.fake_last_error() == 98
+
+
+@pytest.mark.parametrize("fails", [0, 1, 2])
+def test_attend_reports_a_launch_that_fails(lmc, fake, env, fails):
+    """The weights are added by the last kernel: a call that fails has not
+    added any, and leaves no error for the next."""
+    L, base, _ = env
+    fake.fake_fail_launch(fails)
+    assert attend(lmc, fake, L, base, weights=True, max_length=1900, cols=30) == lmc.LMC_ERR_CUDA
+    assert fake.fake_last_error() == 0
+    names = [x[0] for x in launches(fake)]
+    assert len(names) == fails and not any("weights" in n for n in names)
+    fake.fake_reset()
+    assert attend(lmc, fake, L, base, weights=True, max_length=1900, cols=30) == lmc.LMC_OK
+    names = [x[0] for x in launches(fake)]
+    assert len(names) == 3 and "join" in names[1] and "weights" in names[2]
+
+
+def test_a_failed_limit_leaves_no_error(lmc, fake_lib, env, tmp_path):
+    """The largest shared memory is asked for once per kernel; in a fresh
+    process the request fails, is reported, and leaves no error behind."""
+    import sys
+    code = f"""
+import ctypes, sys
+sys.path[:0] = [{ROOT!r}, {HERE!r}]
+import state_cache_paging_gb300 as lmc
+import test_tokens_launches_cpu as t
+import workloads as W
+lib = ctypes.CDLL({fake_lib._name!r})
+for name in ("lmc_select_tokens", "lmc_attend", "lmc_attend_workspace"):
+    getattr(lib, name).argtypes = getattr(lmc._lib, name).argtypes
+L = lmc.lmc_layout_build([W.kda(768, 3, 4, 64), W.mla(1152)], 64, False, 1 << 28)
+base = 1 << 20
+lib.fake_fail_attributes(1)
+for call in (lambda: t.select(lib, base), lambda: t.attend(lmc, lib, L, base)):
+    assert call() == lmc.LMC_ERR_CUDA
+    assert lib.fake_last_error() == 0, "left behind"
+    assert lib.fake_launches() == 0
+lib.fake_fail_attributes(0)
+for call in (lambda: t.select(lib, base), lambda: t.attend(lmc, lib, L, base)):
+    assert call() == call() == lmc.LMC_OK
+assert lib.fake_attributes() == 4  # two that failed, then one for each kernel
+"""
+    r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0, r.stdout + r.stderr
