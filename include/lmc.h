@@ -475,8 +475,10 @@ LMC_API int lmc_append(const lmc_layout *layout, const lmc_entries *entries, voi
  * NaN, p = 0 times it is NaN, as in any sum of products. */
 typedef struct {
     const int32_t *lengths;  /* device [num_requests] */
-    int64_t max_length;      /* no length is above it (>= 1); it sizes the work
-                                space, not the work */
+    int64_t max_length;      /* no length is above it (>= 1). It sizes the work
+                                space; and requests are left whole, one kernel
+                                less, only where it allows a few tiles of 64
+                                tokens, whatever their lengths are */
     const void *q;           /* device [num_requests][num_heads][entry_dim], 16-byte
                                 aligned, strides multiples of 8 elements */
     int64_t q_request_stride; /* elements */

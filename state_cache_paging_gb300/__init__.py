@@ -651,7 +651,7 @@ def lmc_attend(layout: Layout, layer: int, pool, table, lengths, q, value_dim: i
     q [requests, heads, entry_dim] -> out [requests, heads, value_dim] (both
     bfloat16 or both float16; the last dimension contiguous). lengths: int32
     [requests] device tensor, none above max_length (default: what the block
-    table holds). lse (float32 [requests, heads]) receives the log of the sum
+    table holds; a closer bound spares short caches a kernel). lse (float32 [requests, heads]) receives the log of the sum
     of exponentials; weights (float32 [requests, >= max_length]) has the sum
     over the heads of each token's probability added to it."""
     home = _home("pool", pool)

@@ -1463,12 +1463,19 @@ __global__ void __launch_bounds__(kJoinWarps<kSlices> * 32) lmc_attend_join_kern
 }
 
 constexpr int kWeightThreads = 256;
-constexpr int kWeightTokens = 256;  // of a block: four per thread
+constexpr int kWeightTokens = 256;  // of a block's turn: four per thread
 constexpr int kWeightParts = 4;     // the heads are dealt out to as many threads
+// Blocks per SM, about. (256 requests of 100 tokens in a batch that could hold
+// 131072: one block for every 256 tokens that there might be 161 us, 64 an SM 34,
+// 32 an SM 30, 8 an SM 26; 64 ragged requests of up to 32768: 108.0, 108.2, 109.3
+// and 120.)
+constexpr int kWeightPerSm = 64;
 
 // Each token's sum over the heads of 2^(logit - lse). A thread has four tokens
 // and a quarter of the heads, so all of its loads are in flight at once; the
-// quarters are added in shared memory, always in the same order.
+// quarters are added in shared memory, always in the same order. A request's
+// blocks take turns along its tokens, so that the grid does not grow with the
+// lengths that a batch might have.
 __global__ void __launch_bounds__(kWeightThreads) lmc_attend_weights_kernel(const __grid_constant__ AttendPlan P) {
     __shared__ float4 sums[kWeightParts][kWeightTokens / 4];
     const int r = blockIdx.y;
@@ -1476,36 +1483,37 @@ __global__ void __launch_bounds__(kWeightThreads) lmc_attend_weights_kernel(cons
     let_next_start();
     const Range g = range_of(P, r);
     const int base = g.lo & ~1;  // the logits' first place, and 16-byte aligned
-    const int first = blockIdx.x * kWeightTokens;
-    if (!g.ok || g.L == 0 || first >= g.L - base)
-        return;
     const int four = threadIdx.x % (kWeightTokens / 4), part = threadIdx.x / (kWeightTokens / 4);
-    const float *x = P.logits + (int64_t)r * P.H * P.logit_stride + first + 4 * four;
     const float *lse = P.lse2 + (int64_t)r * P.H;
-    float4 w = {};
-    if (first + 4 * four < g.L - base) {
+    const int end = g.ok && g.L > 0 ? g.L - base : 0;
+    for (int64_t first = (int64_t)blockIdx.x * kWeightTokens; first < end; first += (int64_t)gridDim.x * kWeightTokens) {
+        const float *x = P.logits + (int64_t)r * P.H * P.logit_stride + first + 4 * four;
+        float4 w = {};
+        if (first + 4 * four < end) {
 #pragma unroll 8
-        for (int h = part; h < P.H; h += kWeightParts) {
-            const float top = __ldca(lse + h);
-            const float4 v = __ldcs(reinterpret_cast<const float4 *>(x + h * P.logit_stride));
-            if (top != -INFINITY) {
-                w.x += exp2_fast(v.x - top);
-                w.y += exp2_fast(v.y - top);
-                w.z += exp2_fast(v.z - top);
-                w.w += exp2_fast(v.w - top);
+            for (int h = part; h < P.H; h += kWeightParts) {
+                const float top = __ldca(lse + h);
+                const float4 v = __ldcs(reinterpret_cast<const float4 *>(x + h * P.logit_stride));
+                if (top != -INFINITY) {
+                    w.x += exp2_fast(v.x - top);
+                    w.y += exp2_fast(v.y - top);
+                    w.z += exp2_fast(v.z - top);
+                    w.w += exp2_fast(v.w - top);
+                }
             }
         }
-    }
-    sums[part][four] = w;
-    __syncthreads();
-    const int t = base + first + (int)threadIdx.x;
-    if (t < g.lo || t >= g.L)
-        return;
-    float sum = 0.0f;
+        sums[part][four] = w;
+        __syncthreads();
+        const int64_t t = base + first + (int)threadIdx.x;
+        if (t >= g.lo && t < g.L) {
+            float sum = 0.0f;
 #pragma unroll
-    for (int k = 0; k < kWeightParts; k++)
-        sum += reinterpret_cast<const float *>(sums[k])[threadIdx.x];
-    P.weights[r * P.weights_request_stride + t] += sum;
+            for (int k = 0; k < kWeightParts; k++)
+                sum += reinterpret_cast<const float *>(sums[k])[threadIdx.x];
+            P.weights[r * P.weights_request_stride + t] += sum;
+        }
+        __syncthreads();  // the sums may be written again
+    }
 }
 
 // ---- host ------------------------------------------------------------------------
@@ -1757,10 +1765,9 @@ extern "C" int lmc_attend(const lmc_layout *L, const lmc_entries *e, const void 
             return LMC_ERR_CUDA;
     }
     if (P.weights != nullptr) {
-        const int64_t tokens = P.window > 0 ? std::min(P.max_length, P.window) : std::max(P.max_length, 1);
-        if (!follow(lmc_attend_weights_kernel,
-                    dim3((unsigned)((tokens + 1 + kWeightTokens - 1) / kWeightTokens), (unsigned)R), kWeightThreads, 0, s,
-                    P))
+        const int64_t tokens = P.window > 0 ? std::min(P.max_length, P.window) : P.max_length;
+        const int64_t blocks = std::min(tokens / kWeightTokens + 1, ((int64_t)kWeightPerSm * sms + R - 1) / R);
+        if (!follow(lmc_attend_weights_kernel, dim3((unsigned)blocks, (unsigned)R), kWeightThreads, 0, s, P))
             return LMC_ERR_CUDA;
     }
     return LMC_OK;  // every launch was asked for its own error

@@ -205,3 +205,16 @@ assert lib.fake_attributes() == 4  # two that failed, then one for each kernel
 """
     r = subprocess.run([sys.executable, "-c", code], capture_output=True, text=True, timeout=300)
     assert r.returncode == 0, r.stdout + r.stderr
+
+
+def test_attend_weights_grid_is_bounded(lmc, fake, env):
+    """The tokens' weights of short requests in a batch that could hold long
+    ones: no block for every 256 tokens that there might be."""
+    L, base, _ = env
+    for requests, max_length in ((256, 131_072), (1, 131_072), (65_535, 64 * 40), (3, 10)):
+        fake.fake_reset()
+        assert attend(lmc, fake, L, base, requests=requests, heads=2, max_length=max_length, cols=-(-max_length // 64),
+                      weights=True) == lmc.LMC_OK
+        name, grid, _, _ = launches(fake)[-1]
+        assert "weights" in name and grid[1] == requests
+        assert 1 <= grid[0] <= max(1, -(-64 * 152 // requests)) and grid[0] <= max_length // 256 + 1
