@@ -495,8 +495,9 @@ typedef struct {
                                 are of 16 bits */
     int32_t num_heads;       /* >= 1 */
     int32_t value_dim;       /* a multiple of 8, <= entry_dim and <= 512 */
-    float softmax_scale;     /* finite; softmax_scale * scale * log2(e) times any
-                                value of q lies in binary32's range */
+    float softmax_scale;     /* finite, and so is softmax_scale * scale * log2(e) in
+                                binary32 (else INVALID_ARG); over fp8 entries that
+                                times the largest value of q, too */
 } lmc_attention;
 
 /* Entries: entry_dim a multiple of 16, at most 576; the layer's base, stride

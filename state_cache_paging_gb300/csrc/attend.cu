@@ -1641,6 +1641,9 @@ extern "C" int lmc_attend(const lmc_layout *L, const lmc_entries *e, const void 
         a->num_heads <= 0 || a->value_dim <= 0 || a->value_dim % 8 != 0 || a->value_dim > e->entry_dim ||
         a->value_dim > kMaxValue || !std::isfinite(a->softmax_scale))
         return LMC_ERR_INVALID_ARG;
+    const float log2_scale = (float)((double)a->softmax_scale * e->scale * 1.4426950408889634);
+    if (!std::isfinite(log2_scale))
+        return LMC_ERR_INVALID_ARG;
     const int64_t R = e->num_requests, H = a->num_heads;
     if (a->q_request_stride < 0 || a->q_head_stride < 0 || a->out_request_stride < 0 || a->out_head_stride < 0 ||
         a->q_request_stride % 8 != 0 || a->q_head_stride % 8 != 0 || (H > 1 && a->q_head_stride == 0) ||
@@ -1717,7 +1720,7 @@ extern "C" int lmc_attend(const lmc_layout *L, const lmc_entries *e, const void 
     P.panels = std::max((P.E + 63) / 64, 2 * P.value_tiles);
     P.q_bf16 = bf16;
     P.scale = e->scale;
-    P.log2_scale = (float)((double)a->softmax_scale * e->scale * 1.4426950408889634);
+    P.log2_scale = log2_scale;
     const int64_t turns = ((R + P.cols - 1) / P.cols) * most_tiles(P);
     if (turns <= kWholeTiles && turns <= (R * most_tiles(P) + P.cols - 1) / P.cols + kWholeExtra) {
         // no CTA without a request (32 fp8 requests of 128 tokens 15.3 -> 14.4 us with the next line)

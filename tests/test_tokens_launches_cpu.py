@@ -218,3 +218,16 @@ def test_attend_weights_grid_is_bounded(lmc, fake, env):
         name, grid, _, _ = launches(fake)[-1]
         assert "weights" in name and grid[1] == requests
         assert 1 <= grid[0] <= max(1, -(-64 * 152 // requests)) and grid[0] <= max_length // 256 + 1
+
+
+def test_attend_refuses_scales_whose_product_is_infinite(lmc, fake, env):
+    """Logits are scaled by one binary32 number; an infinite one would make NaN
+    of logits that are 0."""
+    L, base, _ = env
+    assert attend(lmc, fake, L, base, scale=3e38) == lmc.LMC_ERR_INVALID_ARG
+    assert attend(lmc, fake, L, base, scale=-3e38) == lmc.LMC_ERR_INVALID_ARG
+    fp8 = dict(layer=3, dtype=lmc.LMC_E_E4M3)
+    assert attend(lmc, fake, L, base, scale=1e20, entry_scale=1e20, **fp8) == lmc.LMC_ERR_INVALID_ARG
+    assert not launches(fake)
+    for kw in (dict(scale=2e38), dict(scale=1e20, entry_scale=1e18, **fp8), dict(scale=1e20, entry_scale=1e-20, **fp8)):
+        assert attend(lmc, fake, L, base, **kw) == lmc.LMC_OK
