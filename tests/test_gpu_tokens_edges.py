@@ -1,6 +1,10 @@
 """Token operators on the GPU where they are easily got wrong: host threads
-side by side, the ends of the types' ranges and values that are not finite."""
+side by side, the ends of the types' ranges, values that are not finite and
+the calls from C."""
 import math
+import os
+import shutil
+import subprocess
 import threading
 
 import numpy as np
@@ -179,3 +183,46 @@ def test_attend_nan_just_before_a_window(lmc, status, cache):
     o, l, _, d_o, d_l, _ = T.attend(M.read(0, table, 0, list(range(n - window, n))), q[0].double(), V, 0.125, 1.0,
                                     cache, "bf16")
     assert ((out[0] - o).abs() <= d_o).all() and ((lse[0] - l).abs() <= d_l).all()
+
+
+def test_token_operators_from_c(lmc, tmp_path):
+    """A C11 program (tests/c_abi_tokens_client.c) makes the four calls through
+    the C ABI alone; its results against the 64-bit forms."""
+    here = os.path.dirname(os.path.abspath(__file__))
+    root = os.path.dirname(here)
+    cuda = next((d for d in (os.environ.get("CUDA_HOME"), "/usr/local/cuda")
+                 if d and os.path.exists(os.path.join(d, "include", "cuda_runtime.h"))), None)
+    if shutil.which("gcc") is None or cuda is None:
+        pytest.skip("gcc or the CUDA toolkit headers not available")
+    exe, libdir = tmp_path / "tokens_client", os.path.join(root, "state_cache_paging_gb300")
+    subprocess.run(["gcc", "-std=c11", "-pedantic", "-Wall", "-Wextra", "-Werror", "-I", os.path.join(root, "include"),
+                    "-I", os.path.join(cuda, "include"), os.path.join(here, "c_abi_tokens_client.c"), "-o", str(exe),
+                    f"-L{libdir}", "-llmc", f"-L{os.path.join(cuda, 'lib64')}", "-lcudart", "-lm",
+                    f"-Wl,-rpath,{libdir}", f"-Wl,-rpath,{os.path.join(cuda, 'lib64')}"],
+                   check=True, capture_output=True, text=True)
+    N, E, V, H, n, budget, recent = 64, 192, 128, 5, 500, 96, 32
+    rng = np.random.default_rng(6)
+    rows = torch.from_numpy(rng.standard_normal((n, E))).bfloat16()
+    q = torch.from_numpy(rng.standard_normal((H, E))).bfloat16()
+    (tmp_path / "case.txt").write_text(f"{N} {E} {V} {H} {n} {budget} {recent}\n")
+    rows.view(torch.int16).numpy().tofile(tmp_path / "rows.bin")
+    q.view(torch.int16).numpy().tofile(tmp_path / "q.bin")
+    r = subprocess.run([str(exe), str(tmp_path)], capture_output=True, text=True, timeout=300)
+    assert r.returncode == 0 and r.stdout.strip() == "done", r.stdout + r.stderr
+
+    def read(name, dtype):
+        return torch.from_numpy(np.fromfile(tmp_path / name, dtype=dtype))
+
+    assert (tmp_path / "status.out").read_text().split() == ["0", str(budget)]
+    scale = float(np.float32(1.0) / np.sqrt(np.float32(E)))
+    o, l, w, d_o, d_l, d_w = T.attend(rows.double(), q.double(), V, scale, 1.0, "bf16", "bf16")
+    out = read("out.out", np.int16).view(torch.bfloat16).view(H, V).double()
+    assert ((out - o).abs() <= d_o).all()
+    assert ((read("lse.out", np.float32).double() - l).abs() <= d_l).all()
+    weights = read("weights.out", np.float32)
+    assert ((weights.double() - w).abs() <= d_w).all()
+    want = T.select(weights.tolist(), n, budget, recent)  # by the weights as the kernel accumulated them
+    assert read("kept.out", np.int32).tolist() == want
+    assert torch.equal(read("scores.out", np.float32), weights[want])
+    moved = read("moved.out", np.int16).view(torch.bfloat16).view(budget, E)
+    assert torch.equal(moved.view(torch.int16), rows[want].view(torch.int16))
