@@ -19,7 +19,8 @@
 // whatever the lengths, so a CTA works through a run of segments (request,
 // tiles). A request inside one CTA is finished there; one that spans several
 // leaves its (m, l, O) per CTA in the workspace and a second kernel joins
-// them. (Caches of a few tiles each are not split.) Above 64 heads, groups of heads take CTAs of their own, side by side.
+// them. (Caches of a few tiles each are not split.) Above 64 heads, groups of
+// heads take CTAs of their own, side by side.
 //
 // A CTA: a loader brings the tile's entries to shared memory (panels of 64
 // values, 128-byte swizzle), one warp issues the products on the tensor cores,
@@ -1576,11 +1577,11 @@ int work_space(const lmc_layout *L, int32_t layer, int64_t R, int64_t H, int64_t
 
 // Short caches: each request is left to one CTA, and nothing has to be joined,
 // where a CTA then has at most kWholeTiles tiles, at most kWholeExtra above an
-// equal share. (Graphs of calls of 32 heads, shared out and whole: one request
-// of 128 tokens 10.5 and 9.5 us, of 256 10.7 and 12.3; 152 requests of 128
-// tokens 14.1 and 12.1, of 256 17.2 and 15.1; 256 requests of 128 tokens 19.8
-// and 18.6. Since then the whole ones gained half a microsecond more. More tiles gain as much where all lengths are near the longest, but
-// they may not be.)
+// equal share. (Graphs of calls of 32 heads, whole and shared out: one request of
+// 64 tokens 7.8 and 9.3 us, of 128 8.8 and 10.6, of 192 10.5 and 10.7; one of 256
+// is shared out, 10.7; 152 requests of 64 tokens 10.7 and 13.1, of 256 14.7 and
+// 17.2; 304 of 128 18.5 and 20.8; 608 of 64 27.6 and 30.1. More tiles gain as much
+// where all lengths are near the longest, but they may not be.)
 constexpr int kWholeTiles = 4, kWholeExtra = 2;
 
 // An upper bound of a request's tiles (exact without a window).

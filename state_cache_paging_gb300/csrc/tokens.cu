@@ -188,7 +188,7 @@ __device__ __forceinline__ uint32_t codes2(float2 v, float scale, float inverse)
 }
 
 // Rows of 16-bit values T2 (pairs) written as fp8 codes: each piece is 16
-// values where the addresses allow (kVec), else two.
+// values where the addresses allow (kVec), else one.
 template <typename T2, bool kVec>
 __global__ void __launch_bounds__(kRowThreads) lmc_append_e4m3_kernel(const __grid_constant__ AppendPlan P) {
     __shared__ const uint8_t *src[kMaxRows];
@@ -907,8 +907,11 @@ extern "C" int lmc_select_tokens(const float *scores, int64_t set_stride, int64_
     P.budget = (int32_t)budget;
     P.recent = (int32_t)recent;
     P.num_requests = num_requests;
-    // 16384 keys (64 KB) per CTA let two CTAs share an SM; fewer where there
-    // are not enough rows for all SMs
+    // 16384 keys (64 KB) per CTA let three CTAs share an SM; fewer where there
+    // are not enough rows for all SMs. Eight CTAs a row is the most there is: above
+    // some 132700 tokens two of their parts fit an SM, above some 210000 one (96
+    // rows of 132000 scores 53.0 us, of 133500 63.3, of 196608 80.9, of 262144
+    // 160.6), and above some 444000 the scores are read again for every pass
     int c = 1;
     while (c < kSelMaxCluster &&
            (max_length > (int64_t)c * 16384 || (rows * c < sms && max_length > (int64_t)c * 2048)))
