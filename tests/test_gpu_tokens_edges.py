@@ -1,6 +1,6 @@
 """Token operators on the GPU where they are easily got wrong: host threads
-side by side, the ends of the types' ranges, values that are not finite and
-the calls from C."""
+side by side, the ends of the types' ranges, values that are not finite, the
+calls from C, and the largest sizes."""
 import math
 import os
 import shutil
@@ -226,3 +226,137 @@ def test_token_operators_from_c(lmc, tmp_path):
     assert torch.equal(read("scores.out", np.float32), weights[want])
     moved = read("moved.out", np.int16).view(torch.bfloat16).view(budget, E)
     assert torch.equal(moved.view(torch.int16), rows[want].view(torch.int16))
+
+
+# Sixteen values a token, all below 6: logits are below 16. In units of log 2 the
+# sum of products (8 of absolute value) is off by 8 * 1.45 * 2^-22 at most, the two
+# roundings behind it by 16 * 1.45 * 2^-24 each, the exponential by 2^-20: together
+# 2^-17, and the same again in lse.
+OFF = 2.0 ** -16
+# p and the result in f16: half a step each
+OUT_OFF = 6 * (2.0 ** -10 + OFF) + 2.0 ** -24
+
+
+def _plain(entries, q, V, softmax_scale):
+    """[R, T, E] and [R, H, E] in 64 bits, none of a request's tokens left out."""
+    x = torch.einsum("rhe,rte->rht", q, entries) * softmax_scale
+    return torch.softmax(x, -1) @ entries[:, :, :V], torch.logsumexp(x, -1), torch.softmax(x, -1).sum(1)
+
+
+def test_attend_of_the_most_requests(lmc, status):
+    """65535 requests of up to three tokens over shared blocks, one of them of
+    a thousand: walked, shared out and joined."""
+    g = torch.Generator().manual_seed(1)
+    N, E, V, R, long = 16, 16, 8, 65535, 1000
+    blocks = 64
+    L = lmc.lmc_layout_build([{"kind": "MLA", "token_bytes": 2 * E}], N, False, blocks * N * E * 2)
+    entries = torch.randn((blocks, N, E), generator=g).half()
+    pool = entries.to(DEV).view(torch.uint8).flatten()
+    lengths = torch.randint(0, 4, (R,), generator=g).int()
+    at = 40_000
+    lengths[at] = long
+    table = torch.randint(0, blocks, (R, 1), generator=g).int().repeat(1, 63)
+    table[at] = torch.randperm(blocks, generator=g)[:63].int()
+    q = torch.randn((R, 1, E), generator=g).half()
+    out, lse = torch.full((R, 1, V), 7.0, dtype=torch.half, device=DEV), torch.full((R, 1), 7.0, device=DEV)
+    weights = torch.zeros((R, long), device=DEV)
+    ws = torch.empty(lmc.lmc_attend_workspace(L, 0, R, 1, V, long, True), dtype=torch.uint8, device=DEV)
+    lmc.lmc_attend(L, 0, pool, table.to(DEV), lengths.to(DEV), q.to(DEV), V, 0.25, out, ws, status, max_length=long,
+                   lse=lse, weights=weights)
+    assert status.item() == 0
+    out, lse, weights = out.cpu().double(), lse.cpu().double(), weights.cpu().double()
+    for n in (0, 1, 2, 3, long):
+        at_n = torch.nonzero(lengths == n).flatten()
+        if n == 0:
+            assert (out[at_n] == 0).all() and (lse[at_n] == -math.inf).all() and (weights[at_n] == 0).all()
+            continue
+        e = entries[table[at_n, :-(-n // N)].long()].reshape(len(at_n), -1, E)[:, :n].double()
+        o, l, w = _plain(e, q[at_n].double(), V, 0.25)
+        assert float((out[at_n] - o).abs().max()) <= OUT_OFF
+        assert float((lse[at_n] - l).abs().max()) <= OFF
+        assert float((weights[at_n, :n] - w).abs().max()) <= OFF and (weights[at_n, n:] == 0).all()
+
+
+@pytest.mark.parametrize("H", [9999, 65535])
+def test_attend_of_more_heads_than_the_device_has_groups_for(lmc, status, H):
+    g = torch.Generator().manual_seed(H)
+    N, E, V, n = 64, 16, 8, 200
+    L = lmc.lmc_layout_build([{"kind": "MLA", "token_bytes": 2 * E}], N, False, 4 * N * E * 2)
+    entries = torch.randn((4 * N, E), generator=g).half()
+    q = torch.randn((2, H, E), generator=g).half()
+    out, lse = torch.full((2, H, V), 7.0, dtype=torch.half, device=DEV), torch.full((2, H), 7.0, device=DEV)
+    ws = torch.empty(lmc.lmc_attend_workspace(L, 0, 2, H, V, 4 * N, True), dtype=torch.uint8, device=DEV)
+    lengths = [n, 70]
+    for most in (n, 4 * N):
+        weights = torch.zeros((2, most), device=DEV)
+        lmc.lmc_attend(L, 0, entries.to(DEV).view(torch.uint8).flatten(), _int32([[0, 1, 2, 3]] * 2), _int32(lengths),
+                       q.to(DEV), V, 0.25, out, ws, status, max_length=most, lse=lse, weights=weights)
+        assert status.item() == 0
+        for r, k in enumerate(lengths):
+            o, l, w = _plain(entries[None, :k].double(), q[r:r + 1].double(), V, 0.25)
+            assert float((out[r].cpu().double() - o[0]).abs().max()) <= OUT_OFF
+            assert float((lse[r].cpu().double() - l[0]).abs().max()) <= OFF
+            # H terms, each off by OFF of itself at most, added in binary32
+            got = weights[r].cpu().double()
+            assert float(((got[:k] - w[0]).abs() / w[0]).max()) <= OFF + H * 2.0 ** -24 and (got[k:] == 0).all()
+
+
+def test_attend_weights_in_turns_behind_a_window(lmc, status):
+    """400 requests that could have 26 blocks' tokens each, one more than their
+    share of the grid; windows that begin on odd tokens."""
+    rng = np.random.default_rng(13)
+    N, E, V, H, R, window = 64, 16, 8, 2, 400, 6400
+    lengths = [6401, 6500, 6400, 12_801] + [int(x) for x in rng.integers(0, 70, R - 4)]
+    blocks = sum(-(-n // N) for n in lengths)
+    M = T.Model(lmc, E, "f16", N, window=window, blocks=blocks)
+    raw = torch.from_numpy(rng.standard_normal((blocks, N, E))).half()
+    M.pages(0).copy_(raw.view(torch.uint8))
+    table = T.tables(lengths, N, blocks, rng)
+    q = torch.from_numpy(rng.standard_normal((R, H, E))).half()
+    before = torch.from_numpy(rng.random((R, max(lengths)))).float()
+    weights = before.to(DEV)
+    _call(lmc, M, table, lengths, q.to(DEV), V, status, 0.25, weights=weights)
+    got = weights.cpu()
+    for r, n in enumerate(lengths):
+        lo = max(0, n - window)
+        assert torch.equal(got[r, :lo], before[r, :lo]) and torch.equal(got[r, n:], before[r, n:])
+        if n:
+            _, _, w, _, _, d_w = T.attend(M.read(0, table, r, list(range(lo, n))), q[r].double(), V, 0.25, 1.0, "f16", "f16")
+            want = before[r, lo:n].double() + w
+            assert ((got[r, lo:n].double() - want).abs() <= d_w + want * 2.0 ** -23).all(), r
+
+
+@pytest.mark.parametrize("cache", ["f16", "e4m3"])
+def test_attend_of_three_hundred_million_tokens(lmc, status, cache):
+    """One request whose entries take more than 2^32 bytes: a value that is 1 in
+    the tokens of every fourth page, the others' 0, and a last token that all
+    of one head's weight falls on."""
+    N, V, H, n = 1000, 8, 2, 300_000_007
+    E = 16
+    elem = 2 if cache == "f16" else 1
+    blocks = -(-n // N)
+    L = lmc.lmc_layout_build([{"kind": "MLA", "token_bytes": E * elem}], N, False, blocks * N * E * elem)
+    pool = torch.zeros(L.pool_bytes, dtype=torch.uint8, device=DEV)
+    one = torch.ones((1,), device=DEV).to(T.TYPES[cache])
+    # the table is the blocks in reverse: page k of the request lies in block blocks - 1 - k
+    table = torch.arange(blocks - 1, -1, -1, dtype=torch.int32, device=DEV)[None]
+    raw = pool.view(torch.int16 if elem == 2 else torch.uint8).view(blocks, N, E)
+    raw[torch.arange(blocks - 1, -1, -4, device=DEV), :, 0] = one.view(raw.dtype)
+    last = raw[blocks - 1 - (n - 1) // N, (n - 1) % N]
+    last[0], last[1], last[15] = 0, one.view(raw.dtype), (one.float() * 64).to(T.TYPES[cache]).view(raw.dtype)
+    q = torch.zeros((1, H, E), dtype=torch.half, device=DEV)
+    q[0, 1, 15] = 1.0
+    out, lse = torch.empty((1, H, V), dtype=torch.half, device=DEV), torch.empty((1, H), device=DEV)
+    ws = torch.empty(lmc.lmc_attend_workspace(L, 0, 1, H, V, n), dtype=torch.uint8, device=DEV)
+    lmc.lmc_attend(L, 0, pool, table, _int32([n]), q, V, 1.0, out, ws, status, max_length=n, lse=lse)
+    assert status.item() == 0
+    ones = ((blocks + 3) // 4 - (1 if (blocks - 1) % 4 == 0 else 0)) * N
+    ones += (n - (blocks - 1) * N - 1) if (blocks - 1) % 4 == 0 else 0
+    got = out[0].cpu().double()
+    # sums of whole numbers that one thread holds stay below 2^24; parts are joined in binary32; the result is f16
+    assert abs(float(got[0, 0]) - ones / n) <= ones / n * (2.0 ** -11 + 2.0 ** -16)
+    assert (got[0, 2:] == 0).all() and float(got[0, 1]) <= 2.0 ** -24
+    assert abs(float(lse[0, 0]) - math.log(n)) <= 2.0 ** -16
+    # the others' n - 1 weigh e^-64 each
+    assert float(got[1, 1]) == 1.0 and (got[1, [0, 2, 3, 4, 5, 6, 7]] == 0).all()
+    assert abs(float(lse[0, 1]) - 64.0) <= 2.0 ** -16
