@@ -57,12 +57,11 @@
 
 #include "follow.cuh"
 #include "lmc_internal.h"
+#include "tensor.cuh"
 
 namespace {
 
-using lmc::follow;
-using lmc::let_next_start;
-using lmc::wait_for_launch;
+using namespace lmc;
 
 constexpr int kMaxEntry = 576;
 constexpr int kMaxValue = 512;
@@ -305,35 +304,6 @@ __device__ __forceinline__ uint64_t bits(int lo, int hi) {  // [lo, hi) of 64
 
 // ---- barriers, tensor cores ------------------------------------------------
 
-__device__ __forceinline__ uint32_t smem_addr(const void *p) {
-    return static_cast<uint32_t>(__cvta_generic_to_shared(p));
-}
-
-__device__ __forceinline__ void bar_init(uint64_t *bar, int count) {
-    asm volatile("mbarrier.init.shared::cta.b64 [%0], %1;" ::"r"(smem_addr(bar)), "r"(count) : "memory");
-}
-
-__device__ __forceinline__ void bar_arrive(uint64_t *bar) {
-    asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0];" ::"r"(smem_addr(bar)) : "memory");
-}
-
-__device__ __forceinline__ void bar_expect(uint64_t *bar, uint32_t bytes) {
-    asm volatile("mbarrier.arrive.expect_tx.shared::cta.b64 _, [%0], %1;" ::"r"(smem_addr(bar)), "r"(bytes)
-                 : "memory");
-}
-
-__device__ __forceinline__ bool bar_try(uint64_t *bar, uint32_t parity) {
-    uint32_t done;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(done)
-        : "r"(smem_addr(bar)), "r"(parity)
-        : "memory");
-    return done != 0;
-}
-
 // Waits for a phase. When the limit runs out the CTA gives up as a whole: no
 // later wait waits, every warp runs its loops to their end (so that the
 // barriers among threads stay matched) and the status word says so.
@@ -356,29 +326,6 @@ __device__ __forceinline__ bool gone(Control &C) {
     return __any_sync(0xffffffffu, *(volatile uint32_t *)&C.gave_up != 0);
 }
 
-// One lane of a converged warp. The products are issued behind this, not
-// behind a lane number: the compiler then knows that one thread runs and keeps
-// the descriptors in uniform registers (115 cycles an instruction otherwise).
-__device__ __forceinline__ bool elect() {
-    uint32_t one;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "elect.sync _|p, 0xffffffff;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(one));
-    return one != 0;
-}
-
-// The same value in every lane, said so that the compiler may keep it in a
-// uniform register.
-__device__ __forceinline__ uint32_t uniform(uint32_t x) { return __shfl_sync(0xffffffffu, x, 0); }
-
-__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
-__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
-__device__ __forceinline__ void wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
-
 __device__ __forceinline__ void soft_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 
 __device__ __forceinline__ bool soft_any(bool x) {
@@ -394,76 +341,6 @@ __device__ __forceinline__ bool soft_any(bool x) {
     return r != 0;
 }
 
-// One copy of a box of rows: (64 values, rows, panels, a block or request).
-__device__ __forceinline__ void tma_box(const CUtensorMap *map, void *dst, int x, int y, int w, uint64_t *bar) {
-    asm volatile(
-        "cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], "
-        "[%6];" ::"r"(smem_addr(dst)),
-        "l"(map), "r"(x), "r"(y), "r"(0), "r"(w), "r"(smem_addr(bar))
-        : "memory");
-}
-
-// Shared-memory matrix descriptor: 128-byte swizzle, 8-row groups `stride`
-// bytes apart, and (where the summed axis is not the contiguous one) 64-value
-// blocks of the other axis `leading` bytes apart.
-__device__ __forceinline__ uint64_t matrix(uint32_t addr, uint32_t leading, uint32_t stride) {
-    return (uint64_t)((addr >> 4) & 0x3FFF) | (uint64_t)(leading >> 4) << 16 | (uint64_t)(stride >> 4) << 32 |
-           (uint64_t)1 << 46 | (uint64_t)2 << 61;
-}
-
-// f32 accumulators; A and B both f16 or both bf16; `turned`: A is read with
-// its rows' axis contiguous.
-__device__ __forceinline__ uint32_t instruction(bool bf16, bool turned, int m, int n) {
-    const uint32_t t = bf16 ? 1u : 0u;
-    return 1u << 4 | t << 7 | t << 10 | (turned ? 1u << 15 : 0u) | (uint32_t)(n >> 3) << 17 | (uint32_t)(m >> 4) << 24;
-}
-
-__device__ __forceinline__ void mma(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "setp.ne.u32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d),
-        "l"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
-        : "memory");
-}
-
-__device__ __forceinline__ void commit(uint64_t *bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_addr(bar))
-                 : "memory");
-}
-
-// 16 lanes x 32 columns: lane l of the warp holds rows l / 4 (s[4j], s[4j+1])
-// and l / 4 + 8 (s[4j+2], s[4j+3]), columns 8j + 2 (l % 4) and the next.
-__device__ __forceinline__ void load_s(uint32_t (&s)[16], uint32_t addr) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
-        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
-        : "=r"(s[0]), "=r"(s[1]), "=r"(s[2]), "=r"(s[3]), "=r"(s[4]), "=r"(s[5]), "=r"(s[6]), "=r"(s[7]), "=r"(s[8]),
-          "=r"(s[9]), "=r"(s[10]), "=r"(s[11]), "=r"(s[12]), "=r"(s[13]), "=r"(s[14]), "=r"(s[15])
-        : "r"(addr)
-        : "memory");
-}
-
-// 32 lanes x 16 columns: a lane's row.
-__device__ __forceinline__ void load_o(uint32_t (&o)[16], uint32_t addr) {
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];"
-        : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3]), "=r"(o[4]), "=r"(o[5]), "=r"(o[6]), "=r"(o[7]), "=r"(o[8]),
-          "=r"(o[9]), "=r"(o[10]), "=r"(o[11]), "=r"(o[12]), "=r"(o[13]), "=r"(o[14]), "=r"(o[15])
-        : "r"(addr)
-        : "memory");
-}
-
-__device__ __forceinline__ void store_o(const uint32_t (&o)[16], uint32_t addr) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%16], "
-        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15};" ::"r"(o[0]),
-        "r"(o[1]), "r"(o[2]), "r"(o[3]), "r"(o[4]), "r"(o[5]), "r"(o[6]), "r"(o[7]), "r"(o[8]), "r"(o[9]), "r"(o[10]),
-        "r"(o[11]), "r"(o[12]), "r"(o[13]), "r"(o[14]), "r"(o[15]), "r"(addr)
-        : "memory");
-}
-
 // o[k] for a k known at run time, without an indexed (local memory) array.
 __device__ __forceinline__ uint32_t at16(const uint32_t (&o)[16], int k) {
     uint32_t x = o[0];
@@ -471,30 +348,6 @@ __device__ __forceinline__ uint32_t at16(const uint32_t (&o)[16], int k) {
     for (int i = 1; i < 16; i++)
         x = k == i ? o[i] : x;
     return x;
-}
-
-__device__ __forceinline__ float exp2_fast(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
-template <bool kBf16>
-__device__ __forceinline__ uint32_t pack(float lo, float hi) {
-    uint32_t r;
-    if (kBf16)
-        asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    else
-        asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-
-__device__ __forceinline__ uint16_t to_out(float x, bool bf16) {
-    return bf16 ? __bfloat16_as_ushort(__float2bfloat16_rn(x)) : __half_as_ushort(__float2half_rn(x));
-}
-
-__device__ __forceinline__ float from_q(uint32_t h, bool bf16) {
-    return bf16 ? __uint_as_float(h << 16) : __half2float(__ushort_as_half((unsigned short)h));
 }
 
 // ---- the CTA's roles ---------------------------------------------------------
@@ -1594,23 +1447,6 @@ int64_t most_tiles(const AttendPlan &P) {
     }
     const int64_t more = P.window - 1;  // a window begins anywhere in a tile
     return more / std::min(kTile, P.span) + 2 + (P.span > kTile ? more / P.span + 1 : 0);
-}
-
-using EncodeTiled = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
-                                 const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
-                                 CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeTiled encoder() {
-    static const EncodeTiled fn = [] {
-        void *p = nullptr;
-        cudaDriverEntryPointQueryResult found;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &found) !=
-                cudaSuccess ||
-            found != cudaDriverEntryPointSuccess)
-            p = nullptr;
-        return reinterpret_cast<EncodeTiled>(p);
-    }();
-    return fn;
 }
 
 // (values, rows, slices) of 16 bits each, read in boxes of `box` rows of one
