@@ -568,6 +568,153 @@ LMC_API int lmc_move_tokens(const lmc_layout *layout, int32_t kv_group, void *po
                             int32_t num_sets, int64_t set_stride, int64_t request_stride, const int32_t *kept_lengths,
                             int64_t max_kept, uint32_t *status, void *stream);
 
+/* ---- norms and position rotations ---------------------------------------------- */
+
+#define LMC_ROT_HALVES 0 /* value i turns with value i + rot_dim / 2 */
+#define LMC_ROT_PAIRS 1  /* value 2 i turns with value 2 i + 1 */
+
+/* What is done to each head of a row of values: a head's first norm_dim values
+ * are normalised by their root mean square,
+ *   y_i = x_i * norm_weight[i] / sqrt(mean(x_0^2 .. x_(norm_dim - 1)^2) + eps),
+ * and then rot_dim of its values, from rot_first on, are turned pair by pair,
+ *   (a, b) -> mscale * (a cos t - b sin t, a sin t + b cos t),
+ *   t = position * frequencies[i] for pair i.
+ * The two ranges may overlap; values in neither stay as they are. All of it is
+ * done in binary32 and rounded once, to the result's type; t is reduced exactly
+ * (a whole number of 2^-64 turns per position), so far positions lose nothing.
+ * A head's sum of squares is taken in binary32: values whose squares overflow
+ * it are outside the norm's domain. */
+typedef struct {
+    int32_t num_heads;   /* >= 1 */
+    int32_t head_dim;    /* values of a head, at most 4096 */
+    int32_t norm_dim;    /* 0 (no norm) .. head_dim */
+    int32_t rot_first;   /* >= 0 */
+    int32_t rot_dim;     /* even, 0 (no rotation) .. head_dim - rot_first */
+    int32_t rot_mode;    /* LMC_ROT_* */
+    float eps;           /* finite, >= 0 */
+    float mscale;        /* finite; 1 where the rotation keeps lengths */
+    const float *norm_weight;  /* device [norm_dim], or NULL for ones */
+    const float *frequencies;  /* device [rot_dim / 2], radians per position, finite,
+                                  below 2^24 in magnitude */
+    const int32_t *positions;  /* device [rows]; any int32 */
+} lmc_rotation;
+
+/* Rotate: norm and rotation of rows of heads in one pass (queries on their way
+ * to lmc_attend; keys that stay activations). x: device [num_rows][num_heads]
+ * [head_dim] of dtype (LMC_E_BF16 or LMC_E_F16), strides in elements, heads that
+ * do not overlap in either order (rows of heads, or heads of rows). out:
+ * likewise; it may be x itself with x's strides (values that are neither
+ * normalised nor turned are then not touched), and may not overlap it otherwise
+ * (OVERLAP, from the first element to the last). Errors: INVALID_ARG, ALIGN,
+ * OVERLAP, OVERFLOW, CUDA. */
+LMC_API int lmc_rotate(const lmc_rotation *rotation, int32_t dtype, const void *x, int64_t x_row_stride,
+                       int64_t x_head_stride, void *out, int64_t out_row_stride, int64_t out_head_stride,
+                       int64_t num_rows, void *stream);
+
+/* Append with norm and rotation on the way: lmc_append's call, its rules,
+ * status bits and errors, where a row's first num_heads * head_dim values (at
+ * most entry_dim) are the heads of `rotation` and the others are taken as they
+ * are. A latent entry is one head of entry_dim values (its first 512
+ * normalised, its last 64 turned); an entry of keys and values is the keys'
+ * heads with the values behind them. rotation->positions may be NULL: the angles
+ * are then those of the cache positions; they are given apart where the two
+ * differ (a cache that was cut to the tokens a request keeps). LMC_E_E4M3
+ * entries hold e4m3(clamp(y / scale)) of the binary32 result y. */
+LMC_API int lmc_append_rotated(const lmc_layout *layout, const lmc_entries *entries, const lmc_rotation *rotation,
+                               void *pool, const int32_t *requests, const int32_t *positions, const void *rows,
+                               int32_t rows_dtype, int64_t row_stride, int64_t num_rows, uint32_t *status,
+                               void *stream);
+
+/* ---- linear attention over state pages ------------------------------------------- */
+
+/* The calls below compute with the states that a KDA layer's pages hold:
+ * linear attention with a decay for each head. Head h of a request has a state
+ * S of key_dim x value_dim binary32 numbers; token t changes it and reads it,
+ *   S_t = exp(decay[t][h]) S_(t-1) + k_t v_t^T,   out[t][h] = scale * S_t^T q_t,
+ * S_(-1) = 0, where k_t and q_t are those of key head h / (num_heads /
+ * num_key_heads). A page holds conv_bytes that these calls leave as they are,
+ * then the states [num_heads][key_dim][value_dim] (rec_bytes in all).
+ *
+ * Where states lie: the state after a request's first n tokens is held by the
+ * page at block position (n - 1) / N of the layer's KV group. A call on tokens
+ * n .. n + m - 1 reads the page at position (n - 1) / N (none where n = 0) and
+ * writes the one at (n + m - 1) / N and, on the way, a snapshot for every block
+ * that it completes and whose table entry is not -1 ([KL] snapshots at block
+ * boundaries): what lmc_store moves. The page that was read is left as it was
+ * unless it is also the one to be written. Pages that the requests of one call
+ * write must differ from one another and from those that others read.
+ *
+ * decay is a log, at most 0 (-inf forgets everything before the token). Values
+ * below -1000 count as -1000, whose exponential is 0 in binary32. Sums, states and
+ * products with them are binary32 (lmc_linear_scan's products run on the tensor
+ * cores; see there); the result is rounded once to `dtype`. */
+typedef struct {
+    int32_t layer;          /* a KDA layer of the layout */
+    int32_t dtype;          /* LMC_E_BF16 or LMC_E_F16: q, k, v and out */
+    int32_t num_requests;   /* rows of the block table, at most 2^20 */
+    int32_t num_heads;      /* states of a page, 1 .. 65535 */
+    int32_t num_key_heads;  /* divides num_heads */
+    int32_t key_dim;        /* multiples of 8, at most 128; num_heads * key_dim * */
+    int32_t value_dim;      /* value_dim * 4 is the layer's rec_bytes */
+    float scale;            /* finite */
+    lmc_block_table table;  /* device block table of the layer's KV group */
+    const int32_t *lengths; /* device [num_requests]: the tokens before this call's;
+                               -1 skips the request (padding of a fixed-size batch) */
+    const void *q;          /* device [rows][num_key_heads][key_dim]; q, k and v:
+                               16-byte aligned, strides (in elements) multiples of 8,
+                               a head's at least its dim, a row's at least that */
+    const void *k;          /* device [rows][num_key_heads][key_dim] */
+    const void *v;          /* device [rows][num_heads][value_dim] */
+    void *out;              /* device [rows][num_heads][value_dim] */
+    const float *decay;     /* device [rows][num_heads]; strides of 0 are taken (a
+                               decay per head for all tokens, or one for all heads) */
+    int64_t q_row_stride, q_head_stride;
+    int64_t k_row_stride, k_head_stride;
+    int64_t v_row_stride, v_head_stride;
+    int64_t out_row_stride, out_head_stride;
+    int64_t decay_row_stride, decay_head_stride;
+} lmc_linear;
+
+/* One new token per request (a decode step): row r is request r's token. The
+ * pool and the layer's base, stride and conv_bytes are 16-byte aligned. out may
+ * overlap none of q, k, v and decay (OVERLAP, from the first element to the
+ * last). Asynchronous on `stream`. Status: BAD_JOB (a length below -1, or the
+ * token's position past the table), NO_SNAPSHOT (-1 where a state is read or
+ * written), BLOCK_OOR; such a request's row of out and pages are left as they
+ * were. Errors: INVALID_ARG, ALIGN, OVERLAP, CUDA. */
+LMC_API int lmc_linear_step(const lmc_layout *layout, const lmc_linear *linear, void *pool, uint32_t *status,
+                            void *stream);
+
+/* Prompts: request r's tokens are rows starts[r] .. starts[r + 1] - 1 (starts:
+ * device [num_requests + 1], not decreasing, within [0, num_rows]; rows of no
+ * request are left as they were, a request without rows is left out). Results
+ * are those of lmc_linear_step token by token up to rounding, for chunks of up
+ * to 64 tokens at a time.
+ *
+ * Rounding: the tensor cores multiply 16-bit numbers of q's type, with binary32
+ * sums. The state and what is added to it are held in as many 16-bit parts as
+ * binary32 needs; the weights inside a chunk, (q_t . k_j) * exp(sum of decays),
+ * are rounded to the type once (half a step each, as the result is). A token
+ * whose values are not finite may make NaN of the results of up to 63 tokens
+ * before it in its request's block, of the same head; other requests are not
+ * touched.
+ *
+ * `workspace`: device memory of at least lmc_linear_scan_workspace bytes,
+ * 256-byte aligned; its content does not matter, and calls that may run at the
+ * same time each need their own. Status as lmc_linear_step (BAD_JOB also where
+ * starts decreases or leaves [0, num_rows]; NO_SNAPSHOT for the page before
+ * the request's tokens and the last one); an entry in between that lies outside
+ * the pool raises BLOCK_OOR and only that snapshot is left out; TIMEOUT.
+ * Errors: INVALID_ARG, ALIGN, OVERLAP, OVERFLOW, CUDA. */
+LMC_API int lmc_linear_scan(const lmc_layout *layout, const lmc_linear *linear, const int32_t *starts,
+                            int64_t num_rows, void *pool, void *workspace, int64_t workspace_bytes, uint32_t *status,
+                            void *stream);
+
+/* Bytes of lmc_linear_scan's workspace for num_requests requests of num_rows
+ * tokens together and num_heads states of a page. */
+LMC_API int lmc_linear_scan_workspace(const lmc_layout *layout, int32_t layer, int32_t num_requests, int64_t num_rows,
+                                      int32_t num_heads, int64_t *out);
+
 /* ---- diagnostics ----------------------------------------------------------- */
 
 /* Self-test of the device-side failure reporting: launches one thread that

@@ -52,6 +52,9 @@ LMC_E_BF16 = 0
 LMC_E_F16 = 1
 LMC_E_E4M3 = 2
 
+LMC_ROT_HALVES = 0
+LMC_ROT_PAIRS = 1
+
 LMC_LAYER = {"MLA": 0, "KDA": 1, "SWA": 2}
 LMC_LAYER_NAME = {v: k for k, v in LMC_LAYER.items()}
 LMC_MAX_LAYERS = 256
@@ -128,6 +131,26 @@ class lmc_attention(ctypes.Structure):
                 ("num_heads", ctypes.c_int32), ("value_dim", ctypes.c_int32), ("softmax_scale", ctypes.c_float)]
 
 
+class lmc_rotation(ctypes.Structure):
+    _fields_ = [("num_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("norm_dim", ctypes.c_int32),
+                ("rot_first", ctypes.c_int32), ("rot_dim", ctypes.c_int32), ("rot_mode", ctypes.c_int32),
+                ("eps", ctypes.c_float), ("mscale", ctypes.c_float), ("norm_weight", ctypes.c_void_p),
+                ("frequencies", ctypes.c_void_p), ("positions", ctypes.c_void_p)]
+
+
+class lmc_linear(ctypes.Structure):
+    _fields_ = [("layer", ctypes.c_int32), ("dtype", ctypes.c_int32), ("num_requests", ctypes.c_int32),
+                ("num_heads", ctypes.c_int32), ("num_key_heads", ctypes.c_int32), ("key_dim", ctypes.c_int32),
+                ("value_dim", ctypes.c_int32), ("scale", ctypes.c_float), ("table", lmc_block_table),
+                ("lengths", ctypes.c_void_p), ("q", ctypes.c_void_p), ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("out", ctypes.c_void_p), ("decay", ctypes.c_void_p),
+                ("q_row_stride", ctypes.c_int64), ("q_head_stride", ctypes.c_int64),
+                ("k_row_stride", ctypes.c_int64), ("k_head_stride", ctypes.c_int64),
+                ("v_row_stride", ctypes.c_int64), ("v_head_stride", ctypes.c_int64),
+                ("out_row_stride", ctypes.c_int64), ("out_head_stride", ctypes.c_int64),
+                ("decay_row_stride", ctypes.c_int64), ("decay_head_stride", ctypes.c_int64)]
+
+
 _P = ctypes.POINTER
 _i64 = ctypes.c_int64
 
@@ -175,6 +198,16 @@ def _bind(so: ctypes.CDLL) -> ctypes.CDLL:
     so.lmc_move_tokens.argtypes = [ctypes.c_void_p, ctypes.c_int32, ctypes.c_void_p, ctypes.c_int32,
                                    _P(lmc_block_table), _P(lmc_block_table), ctypes.c_void_p, ctypes.c_int32, _i64,
                                    _i64, ctypes.c_void_p, _i64, ctypes.c_void_p, ctypes.c_void_p]
+    so.lmc_rotate.argtypes = [_P(lmc_rotation), ctypes.c_int32, ctypes.c_void_p, _i64, _i64, ctypes.c_void_p, _i64, _i64,
+                              _i64, ctypes.c_void_p]
+    so.lmc_append_rotated.argtypes = [ctypes.c_void_p, _P(lmc_entries), _P(lmc_rotation), ctypes.c_void_p,
+                                      ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p, ctypes.c_int32, _i64, _i64,
+                                      ctypes.c_void_p, ctypes.c_void_p]
+    so.lmc_linear_step.argtypes = [ctypes.c_void_p, _P(lmc_linear), ctypes.c_void_p, ctypes.c_void_p, ctypes.c_void_p]
+    so.lmc_linear_scan.argtypes = [ctypes.c_void_p, _P(lmc_linear), ctypes.c_void_p, _i64, ctypes.c_void_p,
+                                   ctypes.c_void_p, _i64, ctypes.c_void_p, ctypes.c_void_p]
+    so.lmc_linear_scan_workspace.argtypes = [ctypes.c_void_p, ctypes.c_int32, ctypes.c_int32, _i64, ctypes.c_int32,
+                                             _P(_i64)]
     so.lmc_selftest_wait.argtypes = [ctypes.c_void_p, _i64, ctypes.c_void_p]
     so.lmc_selftest_row_scale.argtypes = [ctypes.c_void_p] * 4 + [_i64, ctypes.c_void_p]
     so.lmc_strerror.argtypes = [ctypes.c_int]
@@ -731,6 +764,161 @@ def lmc_move_tokens(layout: Layout, kv_group: int, pool, src_table, dst_table, k
                               _stream_ptr(stream, pool, src_table, dst_table, kept, kept_lengths, status))
     if rc != LMC_OK:
         raise LmcError(rc, "lmc_move_tokens")
+
+
+# ----------------------------------------------------------------------------
+# Norms and position rotations
+# ----------------------------------------------------------------------------
+
+def _rotation(home: int, rows: int, heads: int, head_dim: int, angles, frequencies, rot_first: int, pairs: bool,
+              mscale: float, norm_dim: int, norm_weight, eps: float) -> lmc_rotation:
+    freq_p = angle_p = weight_p = None
+    rot_dim = 0
+    if frequencies is not None:
+        if frequencies.get_device() != home:
+            _away("frequencies", frequencies, home)
+        if frequencies.dtype != _torch.float32 or len(frequencies.shape) != 1 or not frequencies.is_contiguous():
+            _refuse("frequencies must be contiguous float32 [rot_dim / 2]")
+        rot_dim = 2 * frequencies.shape[0]
+        freq_p = frequencies.data_ptr()
+        if angles is not None:
+            angle_p = _ints("angles", angles, home, rows)
+    if norm_weight is not None:
+        if norm_weight.get_device() != home:
+            _away("norm_weight", norm_weight, home)
+        if norm_weight.dtype != _torch.float32 or norm_weight.shape != (norm_dim,) or not norm_weight.is_contiguous():
+            _refuse(f"norm_weight must be contiguous float32 [{norm_dim}]")
+        weight_p = norm_weight.data_ptr()
+    return lmc_rotation(heads, head_dim, norm_dim, rot_first, rot_dim, LMC_ROT_PAIRS if pairs else LMC_ROT_HALVES, eps,
+                        mscale, weight_p, freq_p, angle_p)
+
+
+def lmc_rotate(x, angles, out, frequencies, rot_first: int = 0, pairs: bool = False, mscale: float = 1.0,
+               norm_dim: int = 0, norm_weight=None, eps: float = 1e-6, stream=None) -> None:
+    """Norm and rotation of the heads of x ([rows, heads, head_dim], bfloat16 or
+    float16, the last dimension contiguous) into out, which may be x itself: a
+    head's first norm_dim values are normalised by their root mean square (times
+    norm_weight, float32 [norm_dim]), then 2 * len(frequencies) values from
+    rot_first on are turned by angles[row] * frequencies (int32 [rows], float32;
+    None: no rotation), value i with the one half of them on, or with its
+    neighbour (`pairs`)."""
+    home = _home("x", x)
+    if out.get_device() != home:
+        _away("out", out, home)
+    shape, xs, os_ = x.shape, x.stride(), out.stride()
+    if len(shape) != 3 or out.shape != shape or (shape[2] > 1 and (xs[2] != 1 or os_[2] != 1)) or out.dtype != x.dtype:
+        _refuse("x and out must be [rows, heads, head_dim] of one type with a contiguous last dimension")
+    n, heads, dim = shape
+    if frequencies is not None and angles is None and n > 0:
+        _refuse("angles are needed beside frequencies")
+    rot = _rotation(home, n, heads, dim, angles, frequencies, rot_first, pairs, mscale, norm_dim, norm_weight, eps)
+    rc = _lib.lmc_rotate(rot, _value_type(x), x.data_ptr(), xs[0], xs[1], out.data_ptr(), os_[0], os_[1], n,
+                         _stream_ptr(stream, x, angles, out, frequencies, norm_weight))
+    if rc != LMC_OK:
+        raise LmcError(rc, "lmc_rotate")
+
+
+def lmc_append_rotated(layout: Layout, layer: int, pool, table, requests, positions, entries, status, frequencies,
+                       num_heads: int = 1, head_dim: int | None = None, rot_first: int = 0, pairs: bool = False,
+                       mscale: float = 1.0, norm_dim: int = 0, norm_weight=None, eps: float = 1e-6, angles=None,
+                       scale: float = 1.0, stream=None) -> None:
+    """lmc_append with lmc_rotate's norm and rotation on the way: the first
+    num_heads * head_dim values of a row of `entries` are the heads (default:
+    one head, the whole entry), the others are taken as they are. angles (int32
+    [rows]): where a token's angle is not that of its cache position."""
+    home = _home("pool", pool)
+    if entries.get_device() != home:
+        _away("entries", entries, home)
+    shape, stride = entries.shape, entries.stride()
+    if len(shape) != 2 or (stride[1] != 1 and shape[1] > 1):
+        _refuse("entries must be [rows, entry_dim] with unit column stride")
+    n, dim = shape
+    vt = _value_type(entries)
+    e = _entries(layout, layer, table, home, dim, vt, scale)
+    rot = _rotation(home, n, num_heads, dim if head_dim is None else head_dim, angles, frequencies, rot_first, pairs,
+                    mscale, norm_dim, norm_weight, eps)
+    rc = _lib.lmc_append_rotated(layout.handle, e, rot, _bytes("pool", pool, home, layout.pool_bytes),
+                                 _ints("requests", requests, home, n), _ints("positions", positions, home, n),
+                                 entries.data_ptr(), vt, _apart("entries", n, stride[0], dim), n,
+                                 _bytes("status", status, home, 4),
+                                 _stream_ptr(stream, pool, table, requests, positions, entries, status, frequencies,
+                                             norm_weight, angles))
+    if rc != LMC_OK:
+        raise LmcError(rc, "lmc_append_rotated")
+
+
+# ----------------------------------------------------------------------------
+# Linear attention over state pages
+# ----------------------------------------------------------------------------
+
+def _linear(layout: Layout, layer: int, table, home: int, lengths, q, k, v, decay, out, scale: float) -> lmc_linear:
+    for name, t in (("q", q), ("k", k), ("v", v), ("out", out), ("decay", decay)):
+        if t.get_device() != home:
+            _away(name, t, home)
+    qs, ks, vs, os_, ds = q.stride(), k.stride(), v.stride(), out.stride(), decay.stride()
+    shape, n = v.shape, v.shape[0]
+    if len(q.shape) != 3 or len(shape) != 3 or k.shape != q.shape or out.shape != shape or q.shape[0] != n or \
+            qs[2] != 1 or ks[2] != 1 or vs[2] != 1 or os_[2] != 1:
+        _refuse("q and k must be [rows, key heads, key_dim], v and out [rows, heads, value_dim], with a contiguous last "
+                "dimension")
+    dtype = q.dtype
+    if k.dtype != dtype or v.dtype != dtype or out.dtype != dtype:
+        _refuse("q, k, v and out must be of one type")
+    H, K = shape[1], q.shape[1]
+    if decay.dtype != _torch.float32 or decay.shape != (n, H):
+        _refuse(f"decay must be float32 [{n}, {H}]")
+    R = table.shape[0]
+    if K == 0 or H % K:
+        _refuse(f"{K} key heads do not divide {H} heads")
+    if not 0 <= layer < layout.num_layers:
+        _refuse(f"layer {layer} of {layout.num_layers}")
+    return lmc_linear(layer, _value_type(q), R, H, K, q.shape[2], shape[2], scale, _table("block table", table, home),
+                      _ints("lengths", lengths, home, R), q.data_ptr(), k.data_ptr(), v.data_ptr(), out.data_ptr(),
+                      decay.data_ptr(), qs[0], qs[1], ks[0], ks[1], vs[0], vs[1], os_[0], os_[1], ds[0], ds[1])
+
+
+def lmc_linear_step(layout: Layout, layer: int, pool, table, lengths, q, k, v, decay, out, status, scale: float = 1.0,
+                    stream=None) -> None:
+    """One token per request of linear attention over a KDA layer's states: q, k
+    [requests, key heads, key_dim], v, out [requests, heads, value_dim]
+    (bfloat16 or float16), decay float32 [requests, heads] (logs, any strides,
+    expanded ones too), lengths int32 [requests]: the tokens before (-1: the
+    request is skipped). The state before is read from the page of the token
+    before, the new one written to the page of the token's block position."""
+    home = _home("pool", pool)
+    a = _linear(layout, layer, table, home, lengths, q, k, v, decay, out, scale)
+    if v.shape[0] != a.num_requests:
+        _refuse(f"one row per request: {v.shape[0]} rows, {a.num_requests} requests")
+    rc = _lib.lmc_linear_step(layout.handle, a, _bytes("pool", pool, home, layout.pool_bytes),
+                              _bytes("status", status, home, 4),
+                              _stream_ptr(stream, pool, table, lengths, q, k, v, decay, out, status))
+    if rc != LMC_OK:
+        raise LmcError(rc, "lmc_linear_step")
+
+
+def lmc_linear_scan_workspace(layout: Layout, layer: int, num_requests: int, num_rows: int, num_heads: int) -> int:
+    """Bytes of lmc_linear_scan's workspace tensor."""
+    out = _i64(0)
+    _check(_lib.lmc_linear_scan_workspace(layout.handle, int(layer), int(num_requests), int(num_rows), int(num_heads),
+                                          ctypes.byref(out)), "lmc_linear_scan_workspace")
+    return out.value
+
+
+def lmc_linear_scan(layout: Layout, layer: int, pool, table, starts, lengths, q, k, v, decay, out, workspace, status,
+                    scale: float = 1.0, stream=None) -> None:
+    """Linear attention of whole prompts (or of a step's share of them) over a
+    KDA layer's states: request r's tokens are rows starts[r] .. starts[r + 1]
+    (int32 [requests + 1]) and follow the lengths[r] that its state has seen.
+    Every block that is completed on the way leaves its snapshot in its page,
+    where the table has one. Other arguments as for lmc_linear_step."""
+    home = _home("pool", pool)
+    a = _linear(layout, layer, table, home, lengths, q, k, v, decay, out, scale)
+    rc = _lib.lmc_linear_scan(layout.handle, a, _ints("starts", starts, home, a.num_requests + 1), v.shape[0],
+                              _bytes("pool", pool, home, layout.pool_bytes), _bytes("workspace", workspace, home, 0),
+                              workspace.nbytes, _bytes("status", status, home, 4),
+                              _stream_ptr(stream, pool, table, starts, lengths, q, k, v, decay, out, workspace, status))
+    if rc != LMC_OK:
+        raise LmcError(rc, "lmc_linear_scan")
 
 
 def lmc_selftest_wait(status, rounds: int, stream=None) -> None:

@@ -24,7 +24,7 @@ LIB_PATH = os.path.join(PKG, "liblmc.so")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC = os.environ.get("NVCC", "nvcc")
 HOST_UNITS = ("layout", "checks")  # host C++ translation units in csrc/
-CUDA_UNITS = ("paging", "tokens", "attend")  # CUDA translation units in csrc/
+CUDA_UNITS = ("paging", "tokens", "attend", "rotate", "linear")  # CUDA translation units in csrc/
 CXX = os.environ.get("CXX", "g++")
 
 

@@ -1,0 +1,526 @@
+// rotate.cu -- norms and position rotations of heads, for sm_103a: queries (and
+// keys) as activations, and entries on their way into a paged attention layer.
+//
+// Mathematics. y = x / sqrt(mean(x^2) + eps) * w on a head's first values, then
+// pairs turned by t = position * frequency. The angle is kept as a whole number
+// of 2^-64 turns: a step F = frequency * 2^64 / (2 pi), from the frequency's
+// significand times a 64-bit constant, times the position modulo 2^64. Its upper
+// 32 bits are the angle to 2^-32 turns however far the position is, without
+// 64-bit floating point (which this GPU is slow at).
+//
+// Bound: the copy rate. A row's angles are the same for all its heads, so a CTA
+// takes whole rows, makes their cosines and sines once in shared memory, and
+// then a group of 4 to 32 lanes takes a head: it holds the head's values in
+// registers between the sum of squares and the result, so they are read once.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cmath>
+#include <cstdint>
+
+#include "follow.cuh"
+#include "lmc_internal.h"
+#include "tokens.cuh"
+
+namespace {
+
+using namespace lmc;
+
+constexpr int kThreads = 256;
+constexpr int kMaxRows = 64;           // of a CTA
+constexpr int kMaxAngles = 4096;       // of a CTA's rows together (32 KB)
+constexpr int kMaxHeadDim = 4096;
+
+enum Result { kRows, kEntries, kCodes };  // activations; a page's entries, as they are or as fp8 codes
+
+struct RotatePlan {
+    const uint16_t *x;
+    int64_t x_row, x_head;      // strides, elements
+    uint16_t *out;
+    int64_t out_row, out_head;
+    const float *weight;
+    const float *frequencies;
+    const int32_t *angles;      // positions they are made from
+    // entries
+    Pages pages;
+    TokenTable table;
+    const int32_t *requests;
+    const int32_t *positions;
+    uint8_t *pool;
+    uint32_t *status;
+    int32_t num_requests;
+    float code_scale, code_inverse;
+    int64_t num_rows;
+    int32_t rows_per_cta;
+    int32_t heads, head_dim, norm_dim, rot_first, half;
+    int32_t rest;               // values behind the heads, taken as they are,
+    int32_t rest_unit;          // so many at a time
+    int32_t units;              // heads and units of the rest, per row
+    int32_t turned;             // a head's items that are turned,
+    int32_t items;              // and all of them
+    int32_t group;              // lanes of a head
+    int32_t pairs;
+    int32_t touch_only;         // the result lies where x does
+    float eps, mscale;
+};
+
+// frequency * 2^64 / (2 pi) modulo 2^64: the significand times 2^64 / (2 pi)
+// = 2935890503282001226.5, shifted by the exponent.
+__device__ __forceinline__ uint64_t step_of(float frequency) {
+    const uint32_t bits = __float_as_uint(frequency);
+    const int exponent = (int)(bits >> 23 & 255u);
+    const uint64_t m = (bits & 0x7fffffu) | (exponent > 0 ? 0x800000u : 0u);
+    const uint64_t c = 2935890503282001226ull;
+    const int down = 150 - max(exponent, 1);  // frequency = m * 2^-down
+    const uint64_t lo = m * c, hi = __umul64hi(m, c);
+    uint64_t f = 0;
+    if (down <= 0)
+        f = down > -64 ? lo << -down : 0;
+    else if (down < 64)
+        f = lo >> down | hi << (64 - down);
+    else if (down < 128)
+        f = hi >> (down - 64);
+    return bits >> 31 ? 0 - f : f;
+}
+
+// (cos, sin) of position steps.
+__device__ __forceinline__ float2 turn(int32_t position, uint64_t step) {
+    const uint64_t phase = (uint64_t)(int64_t)position * step;
+    float s, c;
+    sincospif((float)(int32_t)(phase >> 32) * 0x1p-31f, &s, &c);
+    return make_float2(c, s);
+}
+
+template <typename T2>
+__device__ __forceinline__ float2 widen(uint32_t v) {
+    return to_float2(*reinterpret_cast<const T2 *>(&v));
+}
+template <typename T2>
+__device__ __forceinline__ uint32_t narrow(float lo, float hi);
+template <>
+__device__ __forceinline__ uint32_t narrow<__nv_bfloat162>(float lo, float hi) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+template <>
+__device__ __forceinline__ uint32_t narrow<__half2>(float lo, float hi) {
+    const __half2 v = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t *>(&v);
+}
+
+// A head's items: what is turned comes first (W pairs of pieces a half apart,
+// or pieces of W whole pairs; single pairs where W is 1), then the pieces of W
+// values that are not. First value of item i's piece (and of its second one).
+template <int W>
+__device__ __forceinline__ int first_value(const RotatePlan &P, int i, int &second) {
+    if (i < P.turned) {
+        if (W == 1 && P.pairs) {
+            second = P.rot_first + 2 * i + 1;
+            return P.rot_first + 2 * i;
+        }
+        second = P.pairs ? -1 : P.rot_first + P.half + i * W;
+        return P.rot_first + i * W;
+    }
+    second = -1;
+    const int v = (i - P.turned) * W;
+    return v < P.rot_first ? v : v + 2 * P.half;
+}
+
+template <int W>
+__device__ __forceinline__ void load_values(uint32_t (&raw)[(W + 1) / 2], const uint16_t *at) {
+    if constexpr (W == 8) {
+        const uint4 v = __ldcs(reinterpret_cast<const uint4 *>(at));
+        raw[0] = v.x, raw[1] = v.y, raw[2] = v.z, raw[3] = v.w;
+    } else {
+        raw[0] = *at;
+    }
+}
+
+template <typename T2, int W>
+__device__ __forceinline__ void widen_values(float (&x)[W], const uint32_t (&raw)[(W + 1) / 2]) {
+    if constexpr (W == 8) {
+#pragma unroll
+        for (int k = 0; k < 4; k++) {
+            const float2 v = widen<T2>(raw[k]);
+            x[2 * k] = v.x, x[2 * k + 1] = v.y;
+        }
+    } else {
+        x[0] = widen<T2>(raw[0]).x;
+    }
+}
+
+template <typename T2, int W, Result kTo>
+__device__ __forceinline__ void store_values(const RotatePlan &P, uint8_t *at, const float (&y)[W]) {
+    if constexpr (kTo == kCodes && W == 8) {
+        uint32_t w[2];
+#pragma unroll
+        for (int k = 0; k < 2; k++)
+            w[k] = codes2(make_float2(y[4 * k], y[4 * k + 1]), P.code_scale, P.code_inverse) |
+                   codes2(make_float2(y[4 * k + 2], y[4 * k + 3]), P.code_scale, P.code_inverse) << 16;
+        __stcs(reinterpret_cast<uint2 *>(at), make_uint2(w[0], w[1]));
+    } else if constexpr (kTo == kCodes) {
+        *at = (uint8_t)codes2(make_float2(y[0], 0.0f), P.code_scale, P.code_inverse);
+    } else if constexpr (W == 8) {
+        __stcs(reinterpret_cast<uint4 *>(at), make_uint4(narrow<T2>(y[0], y[1]), narrow<T2>(y[2], y[3]),
+                                                         narrow<T2>(y[4], y[5]), narrow<T2>(y[6], y[7])));
+    } else {
+        *reinterpret_cast<uint16_t *>(at) = (uint16_t)narrow<T2>(y[0], 0.0f);
+    }
+}
+
+// One item of a head (or of the rest): normalised, turned, written.
+template <typename T2, int W, Result kTo>
+__device__ __forceinline__ void finish(const RotatePlan &P, const float2 *cs, uint8_t *dst, int i, int first, int second,
+                                       float norm, bool head, const uint32_t (&lo)[(W + 1) / 2],
+                                       const uint32_t (&hi)[(W + 1) / 2]) {
+    constexpr int kBytes = kTo == kCodes ? 1 : 2;
+    float a[W], b[W];
+    widen_values<T2, W>(a, lo);
+    widen_values<T2, W>(b, hi);
+    const bool turned = head && i < P.turned;
+    if (head && first < P.norm_dim)
+#pragma unroll
+        for (int k = 0; k < W; k++)
+            a[k] = a[k] * norm * (P.weight != nullptr ? __ldca(P.weight + first + k) : 1.0f);
+    if (turned && second >= 0) {
+        if (second < P.norm_dim)
+#pragma unroll
+            for (int k = 0; k < W; k++)
+                b[k] = b[k] * norm * (P.weight != nullptr ? __ldca(P.weight + second + k) : 1.0f);
+#pragma unroll
+        for (int k = 0; k < W; k++) {
+            const float2 r = cs[i * W + k];
+            const float x = a[k], y = b[k];
+            a[k] = x * r.x - y * r.y;
+            b[k] = x * r.y + y * r.x;
+        }
+        store_values<T2, W, kTo>(P, dst + (int64_t)second * kBytes, b);
+    } else if (W == 8 && turned) {
+#pragma unroll
+        for (int k = 0; k < W / 2; k++) {
+            const float2 r = cs[i * (W / 2) + k];
+            const float x = a[2 * k], y = a[2 * k + 1];
+            a[2 * k] = x * r.x - y * r.y;
+            a[2 * k + 1] = x * r.y + y * r.x;
+        }
+    }
+    store_values<T2, W, kTo>(P, dst + (int64_t)first * kBytes, a);
+}
+
+// W: values of a piece, 8 (16 bytes) where every address allows it, else 1.
+// kItems: items of a head per lane, held in registers; 0: as many as it takes,
+// read a second time after the norm (long heads, and pieces of one value).
+template <typename T2, int W, int kItems, Result kTo>
+__global__ void __launch_bounds__(kThreads) lmc_rotate_kernel(const __grid_constant__ RotatePlan P) {
+    extern __shared__ float2 cs[];  // [rows][half]
+    __shared__ uint8_t *dst[kMaxRows];
+    constexpr int kBytes = kTo == kCodes ? 1 : 2;
+    const int64_t row0 = (int64_t)blockIdx.x * P.rows_per_cta;
+    const int rows = (int)min((int64_t)P.rows_per_cta, P.num_rows - row0);
+    wait_for_launch();
+    let_next_start();
+    if (kTo != kRows && (int)threadIdx.x < rows) {
+        const int64_t i = row0 + threadIdx.x;
+        const int32_t req = __ldca(P.requests + i);
+        int64_t at = -1;
+        if (req != -1) {
+            uint32_t bad = 0;
+            if (req < 0 || req >= P.num_requests)
+                bad = LMC_ST_BAD_JOB;
+            else
+                at = entry_offset(P.pages, P.table, req, __ldca(P.positions + i), bad);
+            if (bad)
+                atomicOr(P.status, bad);
+        }
+        dst[threadIdx.x] = at < 0 ? nullptr : P.pool + at;
+    }
+    for (int k = threadIdx.x; k < rows * P.half; k += kThreads) {
+        const int row = k / P.half;
+        float2 r = turn(__ldca(P.angles + row0 + row), step_of(__ldca(P.frequencies + k - row * P.half)));
+        r.x *= P.mscale;
+        r.y *= P.mscale;
+        cs[k] = r;
+    }
+    __syncthreads();
+
+    const int lane = threadIdx.x & (P.group - 1);
+    const uint32_t mine = (P.group == 32 ? ~0u : (1u << P.group) - 1) << (threadIdx.x & 31 & ~(P.group - 1));
+    const int all = rows * P.units;
+    for (int u = threadIdx.x / P.group; u < all; u += kThreads / P.group) {
+        const int row = u / P.units, unit = u - row * P.units;
+        const bool head = unit < P.heads;
+        const uint16_t *src = P.x + (row0 + row) * P.x_row;
+        uint8_t *to;
+        int items = P.items;
+        if (head) {
+            src += unit * P.x_head;
+            if (kTo == kRows)
+                to = reinterpret_cast<uint8_t *>(P.out + (row0 + row) * P.out_row + unit * P.out_head);
+            else
+                to = dst[row] + (int64_t)unit * P.head_dim * kBytes;
+        } else {
+            const int from = (unit - P.heads) * P.rest_unit;
+            src += P.heads * P.head_dim + from;
+            to = dst[row] + (int64_t)(P.heads * P.head_dim + from) * kBytes;
+            items = min(P.rest_unit, P.rest - from) / W;
+        }
+        if (kTo != kRows && dst[row] == nullptr)
+            continue;
+        auto place = [&](int i, int &second) {
+            second = -1;
+            return head ? first_value<W>(P, i, second) : i * W;
+        };
+        // an item that is neither normalised nor turned, where it lies already
+        auto skip = [&](int i, int first) {
+            return kTo == kRows && P.touch_only && i >= P.turned && first >= P.norm_dim;
+        };
+        float sum = 0.0f;
+        auto add = [&](const uint32_t(&raw)[(W + 1) / 2], int first) {
+            if (!head || first >= P.norm_dim)
+                return;
+            float x[W];
+            widen_values<T2, W>(x, raw);
+#pragma unroll
+            for (int k = 0; k < W; k++)
+                sum = fmaf(x[k], x[k], sum);
+        };
+        if constexpr (kItems > 0) {
+            uint32_t lo[kItems][(W + 1) / 2] = {}, hi[kItems][(W + 1) / 2] = {};
+#pragma unroll
+            for (int n = 0; n < kItems; n++) {
+                const int i = lane + n * P.group;
+                if (i < items) {
+                    int second;
+                    const int first = place(i, second);
+                    if (!skip(i, first))
+                        load_values<W>(lo[n], src + first);
+                    if (second >= 0)
+                        load_values<W>(hi[n], src + second);
+                }
+            }
+            float norm = 1.0f;
+            if (P.norm_dim > 0) {
+#pragma unroll
+                for (int n = 0; n < kItems; n++) {
+                    const int i = lane + n * P.group;
+                    if (i < items) {
+                        int second;
+                        add(lo[n], place(i, second));
+                        if (second >= 0)
+                            add(hi[n], second);
+                    }
+                }
+                for (int o = P.group / 2; o > 0; o >>= 1)
+                    sum += __shfl_xor_sync(mine, sum, o);
+                norm = 1.0f / sqrtf(sum / (float)P.norm_dim + P.eps);
+            }
+#pragma unroll
+            for (int n = 0; n < kItems; n++) {
+                const int i = lane + n * P.group;
+                if (i < items) {
+                    int second;
+                    const int first = place(i, second);
+                    if (!skip(i, first))
+                        finish<T2, W, kTo>(P, cs + row * P.half, to, i, first, second, norm, head, lo[n], hi[n]);
+                }
+            }
+        } else {
+            float norm = 1.0f;
+            if (P.norm_dim > 0 && head) {  // (a group's lanes are at one unit)
+                for (int i = lane; i * W < P.norm_dim; i += P.group) {
+                    uint32_t raw[(W + 1) / 2];
+                    load_values<W>(raw, src + i * W);
+                    add(raw, i * W);
+                }
+                for (int o = P.group / 2; o > 0; o >>= 1)
+                    sum += __shfl_xor_sync(mine, sum, o);
+                norm = 1.0f / sqrtf(sum / (float)P.norm_dim + P.eps);
+            }
+            for (int i = lane; i < items; i += P.group) {
+                int second;
+                const int first = place(i, second);
+                if (skip(i, first))
+                    continue;
+                uint32_t lo[(W + 1) / 2], hi[(W + 1) / 2] = {};
+                load_values<W>(lo, src + first);
+                if (second >= 0)
+                    load_values<W>(hi, src + second);
+                finish<T2, W, kTo>(P, cs + row * P.half, to, i, first, second, norm, head, lo, hi);
+            }
+        }
+    }
+}
+
+// ---- host ------------------------------------------------------------------------
+
+// The rules on the norm and the rotation that do not depend on the rows.
+int check_rotation(const lmc_rotation *r) {
+    if (r == nullptr || r->num_heads <= 0 || r->head_dim <= 0 || r->head_dim > kMaxHeadDim || r->norm_dim < 0 ||
+        r->norm_dim > r->head_dim || r->rot_first < 0 || r->rot_dim < 0 || r->rot_dim % 2 != 0 ||
+        r->rot_first > r->head_dim || r->rot_dim > r->head_dim - r->rot_first ||
+        (r->rot_mode != LMC_ROT_HALVES && r->rot_mode != LMC_ROT_PAIRS) || !std::isfinite(r->eps) || r->eps < 0.0f ||
+        !std::isfinite(r->mscale) || (r->rot_dim > 0 && r->frequencies == nullptr))
+        return LMC_ERR_INVALID_ARG;
+    if ((((uintptr_t)r->norm_weight | (uintptr_t)r->frequencies | (uintptr_t)r->positions) & 3) != 0)
+        return LMC_ERR_ALIGN;
+    return LMC_OK;
+}
+
+// Fills in what follows from the rotation, and how a head is shared out over lanes.
+void plan_heads(RotatePlan &P, const lmc_rotation *r, int width) {
+    P.weight = r->norm_weight;
+    P.frequencies = r->frequencies;
+    P.heads = r->num_heads;
+    P.head_dim = r->head_dim;
+    P.norm_dim = r->norm_dim;
+    P.rot_first = r->rot_first;
+    P.half = r->rot_dim / 2;
+    P.pairs = r->rot_mode == LMC_ROT_PAIRS;
+    P.eps = r->eps;
+    P.mscale = r->mscale;
+    P.turned = width == 1 ? P.half : P.pairs ? r->rot_dim / width : P.half / width;
+    P.items = P.turned + (P.head_dim - r->rot_dim) / width;
+    if (P.touch_only && P.norm_dim == 0)
+        P.items = P.turned;
+    P.group = 4;
+    while (P.group < 32 && P.group < P.items)
+        P.group *= 2;
+    P.rest_unit = std::max(1, P.items) * width;
+    P.units = P.heads + (P.rest + P.rest_unit - 1) / P.rest_unit;
+}
+
+template <typename T2, Result kTo>
+int launch(RotatePlan &P, int width, cudaStream_t stream) {
+    // Rows of a CTA: enough heads for every group of lanes a few times, so that
+    // the angles are made while other CTAs' loads run.
+    const int at_once = kThreads / P.group;
+    int64_t rows = std::max<int64_t>(1, (int64_t)at_once * 4 / P.units);
+    rows = std::min<int64_t>({rows, kMaxRows, std::max(1, kMaxAngles / std::max(1, P.half))});
+    P.rows_per_cta = (int32_t)rows;
+    const int64_t grid = (P.num_rows + rows - 1) / rows;
+    if (grid > INT32_MAX)
+        return LMC_ERR_INVALID_ARG;
+    const int per_lane = (P.items + P.group - 1) / P.group;
+    auto kern = width == 1     ? lmc_rotate_kernel<T2, 1, 0, kTo>
+                : per_lane > 3 ? lmc_rotate_kernel<T2, 8, 0, kTo>
+                : per_lane == 3 ? lmc_rotate_kernel<T2, 8, 3, kTo>
+                : per_lane == 2 ? lmc_rotate_kernel<T2, 8, 2, kTo>
+                                : lmc_rotate_kernel<T2, 8, 1, kTo>;
+    return follow(kern, dim3((unsigned)grid), kThreads, (size_t)rows * P.half * sizeof(float2), stream, P) ? LMC_OK
+                                                                                                          : LMC_ERR_CUDA;
+}
+
+// Whether every piece of eight values lies on a multiple of its size.
+bool eights(const lmc_rotation *r, std::initializer_list<int64_t> bytes16) {
+    int64_t all = (int64_t)(uintptr_t)r->norm_weight;
+    for (int64_t b : bytes16)
+        all |= b;
+    return (all & 15) == 0 && r->head_dim % 8 == 0 && r->norm_dim % 8 == 0 && r->rot_first % 8 == 0 &&
+           r->rot_dim % (r->rot_mode == LMC_ROT_PAIRS ? 8 : 16) == 0;
+}
+
+// Elements [0, end) that heads of rows take up; false where heads overlap or the
+// extent does not fit.
+bool heads_extent(int64_t rows, int64_t row, int64_t heads, int64_t head, int64_t dim, int64_t *end) {
+    if ((rows > 1 && row < dim) || (heads > 1 && head < dim) || row < 0 || head < 0)
+        return false;
+    int64_t by_rows = 0, by_heads = 0;
+    if ((rows > 1 && !mul_ok(row, rows - 1, &by_rows)) || (heads > 1 && !mul_ok(head, heads - 1, &by_heads)) ||
+        !add_ok(by_rows, by_heads, end) || !add_ok(*end, dim, end) || *end > INT64_MAX / 4)
+        return false;
+    return rows <= 1 || heads <= 1 || row >= by_heads + dim || head >= by_rows + dim;
+}
+
+}  // namespace
+
+extern "C" int lmc_rotate(const lmc_rotation *r, int32_t dtype, const void *x, int64_t x_row_stride,
+                          int64_t x_head_stride, void *out, int64_t out_row_stride, int64_t out_head_stride,
+                          int64_t num_rows, void *stream) {
+    if (const int rc = check_rotation(r); rc != LMC_OK)
+        return rc;
+    int64_t x_end, out_end;
+    if ((dtype != LMC_E_BF16 && dtype != LMC_E_F16) || num_rows < 0 ||
+        !heads_extent(num_rows, x_row_stride, r->num_heads, x_head_stride, r->head_dim, &x_end) ||
+        !heads_extent(num_rows, out_row_stride, r->num_heads, out_head_stride, r->head_dim, &out_end) ||
+        (num_rows > 0 && (x == nullptr || out == nullptr || (r->rot_dim > 0 && r->positions == nullptr))))
+        return LMC_ERR_INVALID_ARG;
+    if ((((uintptr_t)x | (uintptr_t)out) & 1) != 0)
+        return LMC_ERR_ALIGN;
+    if (num_rows == 0)
+        return LMC_OK;
+    const bool same = x == out && (num_rows == 1 || x_row_stride == out_row_stride) &&
+                      (r->num_heads == 1 || x_head_stride == out_head_stride);
+    const uint64_t xa = (uint64_t)(uintptr_t)x, oa = (uint64_t)(uintptr_t)out;
+    if (!same && std::max(xa, oa) < std::min(xa + 2 * (uint64_t)x_end, oa + 2 * (uint64_t)out_end))
+        return LMC_ERR_OVERLAP;
+    RotatePlan P = {};
+    P.x = static_cast<const uint16_t *>(x);
+    P.x_row = x_row_stride;
+    P.x_head = x_head_stride;
+    P.out = static_cast<uint16_t *>(out);
+    P.out_row = out_row_stride;
+    P.out_head = out_head_stride;
+    P.angles = r->positions;
+    P.num_rows = num_rows;
+    P.touch_only = same;
+    const int width = eights(r, {(int64_t)xa, (int64_t)oa, num_rows > 1 ? 2 * x_row_stride : 0,
+                                 r->num_heads > 1 ? 2 * x_head_stride : 0, num_rows > 1 ? 2 * out_row_stride : 0,
+                                 r->num_heads > 1 ? 2 * out_head_stride : 0})
+                          ? 8
+                          : 1;
+    plan_heads(P, r, width);
+    if (P.items == 0)
+        return LMC_OK;  // in place, neither normalised nor turned
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    return dtype == LMC_E_BF16 ? launch<__nv_bfloat162, kRows>(P, width, s) : launch<__half2, kRows>(P, width, s);
+}
+
+extern "C" int lmc_append_rotated(const lmc_layout *L, const lmc_entries *e, const lmc_rotation *r, void *pool,
+                                  const int32_t *requests, const int32_t *positions, const void *rows,
+                                  int32_t rows_dtype, int64_t row_stride, int64_t num_rows, uint32_t *status,
+                                  void *stream) {
+    if (const int rc = check_entries(L, e); rc != LMC_OK)
+        return rc;
+    if (const int rc = check_rotation(r); rc != LMC_OK)
+        return rc;
+    if (status == nullptr || num_rows < 0 || (rows_dtype != LMC_E_BF16 && rows_dtype != LMC_E_F16) ||
+        (e->dtype != LMC_E_E4M3 && e->dtype != rows_dtype) || row_stride < e->entry_dim ||
+        row_stride > INT64_MAX / 4 || (int64_t)r->num_heads * r->head_dim > e->entry_dim)
+        return LMC_ERR_INVALID_ARG;
+    if (num_rows > 0 && (pool == nullptr || requests == nullptr || positions == nullptr || rows == nullptr))
+        return LMC_ERR_INVALID_ARG;
+    if ((((uintptr_t)status | (uintptr_t)requests | (uintptr_t)positions) & 3) != 0 || ((uintptr_t)rows & 1) != 0)
+        return LMC_ERR_ALIGN;
+    if (num_rows == 0)
+        return LMC_OK;
+    const lmc_layer_desc &d = L->desc[e->layer];
+    RotatePlan P = {};
+    P.x = static_cast<const uint16_t *>(rows);
+    P.x_row = row_stride;
+    P.x_head = r->head_dim;
+    P.angles = r->positions != nullptr ? r->positions : positions;
+    P.pages = Pages{d.base, d.stride, L->num_blocks, (int32_t)L->block_size, (int32_t)L->specs[e->layer].token_bytes};
+    P.table = token_table(e->table);
+    P.requests = requests;
+    P.positions = positions;
+    P.pool = static_cast<uint8_t *>(pool);
+    P.status = status;
+    P.num_requests = e->num_requests;
+    P.code_scale = e->scale;
+    P.code_inverse = inverse_scale(e->scale);
+    P.num_rows = num_rows;
+    P.rest = e->entry_dim - r->num_heads * r->head_dim;
+    const int64_t page = (int64_t)(uintptr_t)pool | d.base | d.stride | P.pages.token_bytes;
+    const int width = P.rest % 8 == 0 &&
+                              eights(r, {(int64_t)(uintptr_t)rows, 2 * row_stride, e->dtype == LMC_E_E4M3 ? 2 * page : page})
+                          ? 8
+                          : 1;
+    plan_heads(P, r, width);
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const bool bf16 = rows_dtype == LMC_E_BF16;
+    if (e->dtype == LMC_E_E4M3)
+        return bf16 ? launch<__nv_bfloat162, kCodes>(P, width, s) : launch<__half2, kCodes>(P, width, s);
+    return bf16 ? launch<__nv_bfloat162, kEntries>(P, width, s) : launch<__half2, kEntries>(P, width, s);
+}
