@@ -5,6 +5,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <atomic>
 #include <cmath>
 #include <cstdint>
 
@@ -47,14 +48,18 @@ struct Span {
     int64_t before;     // tokens before
     int64_t count;      // its tokens; 0: nothing to do
     int32_t first;      // block of the state before them; -1: none
+    int32_t last;       // block of the state after them
     uint32_t bad;       // status bits
 };
+
+// The larger one; NaN where x is.
+__device__ __forceinline__ float fmaxf_nan(float x, float least) { return x < least ? least : x; }
 
 __device__ __forceinline__ Span span_of(const LinearPlan &P, int r) {
     Span S;
     S.row = r;
     S.count = 1;
-    S.first = -1;
+    S.first = S.last = -1;
     S.bad = 0;
     S.before = __ldca(P.lengths + r);
     if (P.starts != nullptr) {
@@ -70,14 +75,14 @@ __device__ __forceinline__ Span span_of(const LinearPlan &P, int r) {
             S.bad = LMC_ST_BAD_JOB;
         } else {
             const int32_t *blocks = P.table + r * P.row_stride;
-            const int32_t end = __ldca(blocks + last / P.block_size);
+            S.last = __ldca(blocks + last / P.block_size);
             if (S.before > 0) {
                 S.first = __ldca(blocks + (S.before - 1) / P.block_size);
                 if (S.first < 0 || S.first >= P.num_blocks)
                     S.bad |= S.first == -1 ? LMC_ST_NO_SNAPSHOT : LMC_ST_BLOCK_OOR;
             }
-            if (end < 0 || end >= P.num_blocks)
-                S.bad |= end == -1 ? LMC_ST_NO_SNAPSHOT : LMC_ST_BLOCK_OOR;
+            if (S.last < 0 || S.last >= P.num_blocks)
+                S.bad |= S.last == -1 ? LMC_ST_NO_SNAPSHOT : LMC_ST_BLOCK_OOR;
         }
     }
     if (S.bad != 0 || S.before < 0)
@@ -100,11 +105,12 @@ __global__ void __launch_bounds__(kStepThreads) lmc_linear_step_kernel(const __g
     constexpr int kTurns = kMaxDim / kRows;
     __shared__ float qs[kMaxDim], ks[kMaxDim];
     __shared__ float4 sums[kRows][kLanes];
-    const int h = blockIdx.x % P.H, r = blockIdx.x / P.H;
+    const int h = (int)(blockIdx.x % P.H);
+    const int64_t r = blockIdx.x / P.H;
     const int lane = threadIdx.x % kLanes, row = threadIdx.x / kLanes, c = 4 * lane;
     wait_for_launch();
     let_next_start();
-    const Span S = span_of(P, r);
+    const Span S = span_of(P, (int)r);
     if (S.bad && h == 0 && threadIdx.x == 0)
         atomicOr(P.status, S.bad);
     if (S.count == 0)
@@ -120,62 +126,913 @@ __global__ void __launch_bounds__(kStepThreads) lmc_linear_step_kernel(const __g
                 s[i] = __ldcs(reinterpret_cast<const float4 *>(page + (int64_t)(row + i * kRows) * P.dv));
     }
     const int kh = h / P.shared;
-    for (int64_t t = 0; t < S.count; t++) {
-        const int64_t x = S.row + t;
-        if (t > 0)
-            __syncthreads();
-        if ((int)threadIdx.x < P.dk)
-            qs[threadIdx.x] = from_q(P.q[x * P.q_row + kh * P.q_head + threadIdx.x], P.bf16);
-        else if (threadIdx.x >= kMaxDim && (int)threadIdx.x - kMaxDim < P.dk)
-            ks[threadIdx.x - kMaxDim] = from_q(P.k[x * P.k_row + kh * P.k_head + threadIdx.x - kMaxDim], P.bf16);
-        float4 v = {}, o = {};
-        if (mine) {
-            const uint2 w = *reinterpret_cast<const uint2 *>(P.v + x * P.v_row + h * P.v_head + c);
-            v = make_float4(from_q(w.x & 0xffff, P.bf16), from_q(w.x >> 16, P.bf16), from_q(w.y & 0xffff, P.bf16),
-                            from_q(w.y >> 16, P.bf16));
-        }
-        const float a = expf(fmaxf(P.decay[x * P.decay_row + h * P.decay_head], kLeastDecay));
-        __syncthreads();
+    if ((int)threadIdx.x < P.dk)
+        qs[threadIdx.x] = from_q(P.q[r * P.q_row + kh * P.q_head + threadIdx.x], P.bf16);
+    else if (threadIdx.x >= kMaxDim && (int)threadIdx.x - kMaxDim < P.dk)
+        ks[threadIdx.x - kMaxDim] = from_q(P.k[r * P.k_row + kh * P.k_head + threadIdx.x - kMaxDim], P.bf16);
+    float4 v = {}, o = {};
+    if (mine) {
+        const uint2 w = *reinterpret_cast<const uint2 *>(P.v + r * P.v_row + h * P.v_head + c);
+        v = make_float4(from_q(w.x & 0xffff, P.bf16), from_q(w.x >> 16, P.bf16), from_q(w.y & 0xffff, P.bf16),
+                        from_q(w.y >> 16, P.bf16));
+    }
+    // a state that decays slowly keeps its own digits: s + (decay - 1) s (a decay
+    // near 1 rounded to 24 bits would let it drift by 2^-25 a token)
+    const float g = fmaxf_nan(P.decay[r * P.decay_row + h * P.decay_head], kLeastDecay);
+    const bool slow = g > -0.5f && g < 0.5f;
+    const float grow = slow ? expm1f(g) : expf(g), keep = slow ? 1.0f : 0.0f;
+    __syncthreads();
 #pragma unroll
-        for (int i = 0; i < kTurns; i++) {
-            const int j = row + i * kRows;
-            if (j < P.dk) {
-                const float k = ks[j], q = qs[j];
-                s[i].x = fmaf(k, v.x, a * s[i].x);
-                s[i].y = fmaf(k, v.y, a * s[i].y);
-                s[i].z = fmaf(k, v.z, a * s[i].z);
-                s[i].w = fmaf(k, v.w, a * s[i].w);
-                o.x = fmaf(q, s[i].x, o.x);
-                o.y = fmaf(q, s[i].y, o.y);
-                o.z = fmaf(q, s[i].z, o.z);
-                o.w = fmaf(q, s[i].w, o.w);
-            }
+    for (int i = 0; i < kTurns; i++) {
+        const int j = row + i * kRows;
+        if (j < P.dk) {
+            const float k = ks[j], q = qs[j];
+            s[i].x = fmaf(keep, s[i].x, fmaf(k, v.x, grow * s[i].x));
+            s[i].y = fmaf(keep, s[i].y, fmaf(k, v.y, grow * s[i].y));
+            s[i].z = fmaf(keep, s[i].z, fmaf(k, v.z, grow * s[i].z));
+            s[i].w = fmaf(keep, s[i].w, fmaf(k, v.w, grow * s[i].w));
+            o.x = fmaf(q, s[i].x, o.x);
+            o.y = fmaf(q, s[i].y, o.y);
+            o.z = fmaf(q, s[i].z, o.z);
+            o.w = fmaf(q, s[i].w, o.w);
         }
-        // the state after a block's last token, and after the call's
-        const int64_t done = S.before + t + 1;
-        if (t + 1 == S.count || done % P.block_size == 0) {
-            const int32_t block = __ldca(P.table + r * P.row_stride + (done - 1) / P.block_size);
-            if (block >= 0 && block < P.num_blocks) {
-                if (mine) {
-                    float *page = P.pages + block * P.page_stride + at;
+    }
+    if (mine) {
+        float *page = P.pages + S.last * P.page_stride + at;
 #pragma unroll
-                    for (int i = 0; i < kTurns; i++)
-                        if (row + i * kRows < P.dk)
-                            __stcs(reinterpret_cast<float4 *>(page + (int64_t)(row + i * kRows) * P.dv), s[i]);
-                }
-            } else if (block != -1 && threadIdx.x == 0) {
-                atomicOr(P.status, LMC_ST_BLOCK_OOR);
-            }
-        }
-        sums[row][lane] = o;
-        __syncthreads();
-        if ((int)threadIdx.x < P.dv) {
-            float y = 0.0f;
+        for (int i = 0; i < kTurns; i++)
+            if (row + i * kRows < P.dk)
+                __stcs(reinterpret_cast<float4 *>(page + (int64_t)(row + i * kRows) * P.dv), s[i]);
+    }
+    sums[row][lane] = o;
+    __syncthreads();
+    if ((int)threadIdx.x < P.dv) {
+        float y = 0.0f;
 #pragma unroll 8
-            for (int i = 0; i < kRows; i++)
-                y += reinterpret_cast<const float *>(sums[i])[threadIdx.x];
-            P.out[x * P.out_row + h * P.out_head + threadIdx.x] = to_out(y * P.scale, P.bf16);
+        for (int i = 0; i < kRows; i++)
+            y += reinterpret_cast<const float *>(sums[i])[threadIdx.x];
+        P.out[r * P.out_row + h * P.out_head + threadIdx.x] = to_out(y * P.scale, P.bf16);
+    }
+}
+
+// ---------------------------------------------------------------------------
+// Prompts: 64 tokens at a time on the tensor cores
+// ---------------------------------------------------------------------------
+
+constexpr int kTile = 64;             // tokens of a tile, all of one block of a request
+constexpr int kPanel = kTile * 128;   // bytes of 64 values of a tile's rows
+constexpr int kStages = 3;
+constexpr int kStageBytes = 6 * kPanel;  // q, k, v, two panels each
+constexpr int kParts = 3;                // of k times its decay: bf16; f16 takes two
+constexpr int kStateWarps = 8;
+constexpr int kFirstWeightWarp = 8, kWeightWarps = 4;
+constexpr int kLoadWarp = 12, kForwardWarp = 13, kStateProductWarp = 14;
+constexpr int kScanThreads = 15 * 32;
+constexpr int kScanMemory = kStages * kStageBytes + kParts * 2 * kPanel + 2 * kPanel;
+constexpr uint32_t kWaitLimit = 1u << 22;
+// columns of tensor memory
+constexpr uint32_t kScores = 0, kUpdate = 128, kFromState = 256, kFromTile = 320, kStateHigh = 384, kStateLow = 448;
+constexpr int kRing = 4;              // tiles whose decays are at hand
+constexpr int kSms = 152;
+constexpr int64_t kLeastSegment = 512;  // tokens
+
+struct ScanPlan {
+    CUtensorMap q, k, v;
+    LinearPlan L;
+    int64_t segment;     // a request of n of these tokens (n >= 2) is cut into n segments
+    float *slots;        // [num_rows / segment][H][dk][dv]: the states before segments
+    float *totals;       // [num_rows / segment][H]: the decay over the segment before
+    int32_t k_copies, v_copies, k_panels, v_panels;  // copies for all panels, panels
+};
+
+// A CTA's tokens: a segment of a request, one head.
+struct Item {
+    int64_t row;         // first row
+    int64_t page;        // its block position,
+    int32_t phase;       // and the tokens of the block before it
+    int32_t count;       // tokens
+    int32_t r, h;
+    int32_t first;       // block of the state before them, -1: none
+    int32_t slot;        // of the segment; -1: the request is not cut
+    int32_t ends;        // the request ends with it
+    int32_t work;
+};
+
+// What a tile's tokens' decays give.
+struct alignas(16) Decays {
+    float2 log[kTile];   // sum up to and with the token, in units of log 2 (high, low)
+    float left[kTile];   // from the token to the tile's end
+    float since[kTile];  // from the tile's start up to the token
+    float lift[kTile];   // f16: what the token's weights were divided by
+    float grow, keep;    // state = grow * state + keep * state + update * unit
+    float unit;          // f16: what k times its decay was divided by
+};
+
+static_assert(sizeof(Decays) % 16 == 0, "two tokens' logs are read at once");
+
+struct ScanControl {
+    uint64_t full[kStages], free[kStages];
+    uint64_t decays_full[2];
+    uint64_t score_full[2], score_free[2];
+    uint64_t weight_full[2], weight_free[2];
+    uint64_t keys_full, keys_free;
+    uint64_t update_full, update_free;
+    uint64_t state_full, out_full, out_free;
+    uint64_t ended[2];
+    uint32_t tmem;
+    uint32_t gave_up;
+    uint32_t tiles;      // that were asked for
+    Item item;
+    Decays decays[kRing];
+    float top[kWeightWarps];     // f16: largest of k times its decay
+    float row_top[2][kMaxDim];   // f16: largest of the state's rows, by halves
+};
+
+// The tiles of an item, in order; every role walks them by itself.
+struct Tiles {
+    int32_t done, total, phase, N;
+    int32_t rows;        // of the current tile
+    int64_t row, page;   // its first row; its block position
+    bool block_ends;
+    uint32_t n;
+
+    __device__ __forceinline__ Tiles(const Item &I, int32_t block_size)
+        : done(0), total(I.count), phase(I.phase), N(block_size), rows(0), row(I.row), page(I.page), block_ends(false),
+          n(~0u) {}
+    __device__ __forceinline__ bool next() {
+        done += rows;
+        row += rows;
+        phase += rows;
+        if (phase == N) {
+            phase = 0;
+            page += rows > 0;
         }
+        if (done >= total)
+            return false;
+        rows = min(min(kTile, total - done), N - phase);
+        block_ends = phase + rows == N;
+        n++;
+        return true;
+    }
+    __device__ __forceinline__ bool last() const { return done + rows == total; }
+};
+
+__device__ __forceinline__ void scan_wait(ScanControl &C, uint64_t *bar, uint32_t parity, uint32_t *status) {
+    if (bar_try(bar, parity))
+        return;
+    for (uint32_t i = 0; i < kWaitLimit; i++) {
+        if (bar_try(bar, parity))
+            return;
+        if ((i & 255u) == 255u && *(volatile uint32_t *)&C.gave_up)
+            return;
+    }
+    // the CTA gives up as a whole: no later wait waits, every role runs to its end
+    *(volatile uint32_t *)&C.gave_up = 1;
+    atomicOr(status, LMC_ST_TIMEOUT);
+}
+
+__device__ __forceinline__ bool scan_gone(ScanControl &C) {
+    return __any_sync(0xffffffffu, *(volatile uint32_t *)&C.gave_up != 0);
+}
+
+// A of the product from tensor memory.
+__device__ __forceinline__ void mma_held(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.u32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+        : "memory");
+}
+
+__device__ __forceinline__ void weights_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+
+// The upper halves of two words: a's below b's.
+__device__ __forceinline__ uint32_t upper(float a, float b) {
+    return __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
+}
+__device__ __forceinline__ float truncated(float x) { return __uint_as_float(__float_as_uint(x) & 0xffff0000u); }
+
+// 2^e for e in [-126, 127], and the e that brings x into [2^14, 2^15).
+__device__ __forceinline__ float power(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
+__device__ __forceinline__ int lift_of(float x) {
+    const int e = (int)(__float_as_uint(x) >> 23 & 255u) - 127;  // x >= 0
+    return x == 0.0f ? 0 : max(-112, min(126, 14 - e));
+}
+
+// Largest r in [0, R) with starts[r] / segment + (shift ? r : 0) <= v; -1: none.
+// A warp together: 32 places at a time.
+__device__ __forceinline__ int request_of(const ScanPlan &P, int64_t v, bool shift) {
+    const int lane = threadIdx.x & 31;
+    int64_t lo = 0, hi = P.L.R;
+    for (;;) {
+        const int64_t step = (hi - lo + 31) / 32, i = lo + step * lane;
+        const bool below = i < hi && __ldca(P.L.starts + i) / P.segment + (shift ? i : 0) <= v;
+        const int found = __popc(__ballot_sync(0xffffffffu, below));
+        if (found == 0)
+            return -1;
+        lo += step * (found - 1);
+        hi = min(hi, lo + step);
+        if (hi - lo <= 1)
+            return (int)lo;
+    }
+}
+
+// First token of segment i of n of a request of T tokens after `before`: near i
+// T / n, where the tiles of a block begin anyway.
+__device__ __forceinline__ int64_t cut(int64_t T, int64_t i, int64_t n, int64_t before, int32_t N) {
+    if (i == 0 || i == n)
+        return i == 0 ? 0 : T;
+    const int64_t t = T * i / n;
+    return t - (before + t) % N % kTile;
+}
+
+// States only: all segments but a request's last.
+template <bool kStatesOnly>
+__device__ __forceinline__ void find_item(const ScanPlan &P, Item &I) {
+    const int lane = threadIdx.x & 31;
+    const int64_t v = blockIdx.x / P.L.H;
+    const int r = request_of(P, v, !kStatesOnly);
+    Item J = {};
+    J.h = (int)(blockIdx.x % P.L.H);
+    J.r = r;
+    if (r >= 0) {
+        const Span S = span_of(P.L, r);
+        const int64_t slot = __ldca(P.L.starts + r) / P.segment, i = v - slot - (kStatesOnly ? 0 : r);
+        const int64_t n = max((int64_t)1, S.count / P.segment);
+        if (!kStatesOnly && i == 0 && J.h == 0 && lane == 0 && S.bad != 0)
+            atomicOr(P.L.status, S.bad);
+        if (S.count > 0 && i < (kStatesOnly ? n - 1 : n)) {
+            const int64_t a = cut(S.count, i, n, S.before, P.L.block_size), b = cut(S.count, i + 1, n, S.before, P.L.block_size);
+            J.row = S.row + a;
+            J.page = (S.before + a) / P.L.block_size;
+            J.phase = (int)((S.before + a) % P.L.block_size);
+            J.count = (int)(b - a);
+            J.first = S.first;
+            J.slot = n > 1 ? (int)(slot + i) : -1;
+            J.ends = i == n - 1;
+            J.work = 1;
+        }
+    }
+    if (lane == 0)
+        I = J;
+}
+
+// One warp: q, k and v of each tile by TMA. (Rows behind a tile's last one come
+// along; they are not read into a result.)
+template <bool kStatesOnly>
+__device__ __forceinline__ void load_tiles(const ScanPlan &P, ScanControl &C, uint8_t *mem) {
+    Tiles T(C.item, P.L.block_size);
+    const int h = C.item.h, kh = h / P.L.shared;
+    const uint32_t bytes = (uint32_t)((kStatesOnly ? 1 : 2) * P.k_panels + P.v_panels) * kPanel;
+    uint32_t asked = 0;
+    while (T.next()) {
+        const int st = (int)uniform(T.n % kStages);
+        if (T.n >= kStages)
+            scan_wait(C, &C.free[st], (T.n / kStages - 1) & 1, P.L.status);
+        if (scan_gone(C))
+            break;
+        uint8_t *to = mem + st * kStageBytes;
+        const int row = (int)uniform((int)T.row);
+        if (elect()) {
+            uint64_t *bar = &C.full[st];
+            bar_expect(bar, bytes);
+            for (int i = 0; i < P.k_copies; i++)
+                tma_box(&P.k, to + 2 * kPanel + i * kPanel, i * 64, row, kh, bar);
+            for (int i = 0; i < P.v_copies; i++)
+                tma_box(&P.v, to + 4 * kPanel + i * kPanel, i * 64, row, h, bar);
+            if (!kStatesOnly)
+                for (int i = 0; i < P.k_copies; i++)
+                    tma_box(&P.q, to + i * kPanel, i * 64, row, kh, bar);
+        }
+        __syncwarp();
+        asked++;
+    }
+    if ((threadIdx.x & 31) == 0)
+        C.tiles = asked;
+}
+
+// One warp: the products that need no state. Scores Q K^T [tokens x tokens], and
+// what the tile adds to the state, turned: V^T (K decayed) [values x keys].
+template <bool kBf16, bool kStatesOnly>
+__device__ __forceinline__ void multiply_forward(const ScanPlan &P, ScanControl &C, uint8_t *mem) {
+    Tiles T(C.item, P.L.block_size);
+    const uint32_t tmem = uniform(C.tmem);
+    const int keys = 64 * P.k_panels, steps = (P.L.dk + 15) / 16;
+    const uint32_t scores = instruction(kBf16, false, 64, kTile);
+    const uint32_t update = instruction(kBf16, true, 128, keys) | 1u << 16;  // B turned, too
+    const uint64_t part0 = matrix(smem_addr(mem) + kStages * kStageBytes, kPanel, 1024);
+    while (T.next()) {
+        const uint32_t n = T.n;
+        const int st = (int)uniform(n % kStages);
+        const uint32_t at = smem_addr(mem) + st * kStageBytes, d = tmem + kScores + uniform(n & 1) * 64;
+        scan_wait(C, &C.full[st], (n / kStages) & 1, P.L.status);
+        if (!kStatesOnly) {
+            if (n >= 2)
+                scan_wait(C, &C.score_free[n & 1], (n / 2 - 1) & 1, P.L.status);
+            __syncwarp();
+            fence_after();
+            if (elect()) {
+                const uint64_t q = matrix(at, 16, 1024), k = matrix(at + 2 * kPanel, 16, 1024);
+                for (int s = 0; s < steps; s++)
+                    mma(d, q + (s >> 2) * (kPanel >> 4) + (s & 3) * 2,
+                        k + (s >> 2) * (kPanel >> 4) + (s & 3) * 2, scores, s > 0);
+                commit(&C.score_full[n & 1]);
+            }
+            __syncwarp();
+        }
+        scan_wait(C, &C.keys_full, n & 1, P.L.status);
+        if (n >= 1)
+            scan_wait(C, &C.update_free, (n - 1) & 1, P.L.status);
+        __syncwarp();
+        fence_after();
+        if (elect()) {
+            const uint64_t v = matrix(at + 4 * kPanel, kPanel, 1024);
+            // the small parts first
+#pragma unroll
+            for (int part = (kBf16 ? 3 : 2) - 1; part >= 0; part--)
+#pragma unroll
+                for (int s = 0; s < kTile / 16; s++)
+                    mma(tmem + kUpdate, v + s * (2048 >> 4), part0 + part * (2 * kPanel >> 4) + s * (2048 >> 4), update,
+                        part < (kBf16 ? 2 : 1) || s > 0);
+            commit(&C.update_full);
+            commit(&C.keys_free);
+            commit(&C.free[st]);
+        }
+        __syncwarp();
+    }
+}
+
+// One warp: the products that make the result, turned: S^T Q^T from the state
+// before the tile, V^T P^T from the tile's own tokens [values x tokens].
+template <bool kBf16>
+__device__ __forceinline__ void multiply_state(const ScanPlan &P, ScanControl &C, uint8_t *mem) {
+    Tiles T(C.item, P.L.block_size);
+    const uint32_t tmem = uniform(C.tmem);
+    const int steps = (P.L.dk + 15) / 16;
+    const uint32_t from_state = instruction(kBf16, false, 128, kTile), from_tile = instruction(kBf16, true, 128, kTile);
+    const uint64_t weight0 = matrix(smem_addr(mem) + kStages * kStageBytes + kParts * 2 * kPanel, 16, 1024);
+    while (T.next()) {
+        const uint32_t n = T.n;
+        const int st = (int)uniform(n % kStages);
+        const uint32_t at = smem_addr(mem) + st * kStageBytes;
+        const uint64_t weight = weight0 + uniform(n & 1) * (kPanel >> 4);
+        scan_wait(C, &C.full[st], (n / kStages) & 1, P.L.status);
+        scan_wait(C, &C.state_full, n & 1, P.L.status);
+        if (n >= 1)
+            scan_wait(C, &C.out_free, (n - 1) & 1, P.L.status);
+        __syncwarp();
+        fence_after();
+        if (elect()) {
+            const uint64_t q = matrix(at, 16, 1024);
+            for (int s = 0; s < steps; s++)
+                mma_held(tmem + kFromState, tmem + kStateLow + 8 * s, q + (s >> 2) * (kPanel >> 4) + (s & 3) * 2, from_state,
+                         s > 0);
+            for (int s = 0; s < steps; s++)
+                mma_held(tmem + kFromState, tmem + kStateHigh + 8 * s, q + (s >> 2) * (kPanel >> 4) + (s & 3) * 2,
+                         from_state, true);
+        }
+        __syncwarp();
+        scan_wait(C, &C.weight_full[n & 1], (n >> 1) & 1, P.L.status);
+        __syncwarp();
+        fence_after();
+        if (elect()) {
+            const uint64_t v = matrix(at + 4 * kPanel, kPanel, 1024);
+#pragma unroll
+            for (int s = 0; s < kTile / 16; s++)
+                mma(tmem + kFromTile, v + s * (2048 >> 4), weight + s * 2, from_tile, s > 0);
+            commit(&C.out_full);
+            commit(&C.weight_free[n & 1]);
+            commit(&C.free[st]);
+        }
+        __syncwarp();
+    }
+}
+
+// A tile's decays, by one warp: lane l's are those of tokens 2 l and 2 l + 1.
+// They are summed as whole numbers of 2^-40 (exactly, in any order), so sums far
+// from 0 lose nothing of the differences that count.
+__device__ __forceinline__ void sum_decays(Decays &D, float g0, float g1, int rows) {
+    const int lane = threadIdx.x & 31;
+    const float nan = __int_as_float(0x7fffffff);
+    const uint32_t bad0 = __ballot_sync(0xffffffffu, g0 != g0), bad1 = __ballot_sync(0xffffffffu, g1 != g1);
+    const int first_bad = min(bad0 ? 2 * (__ffs(bad0) - 1) : kTile, bad1 ? 2 * (__ffs(bad1) - 1) + 1 : kTile);
+    auto whole = [](float g) {
+        return __float2ll_rn(fminf(fmaxf(g, kLeastDecay), -kLeastDecay) * 1.44269504088896340736f * 0x1p40f);
+    };
+    const long long a = whole(g0), b = whole(g1);
+    long long sum = a + b;
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long x = __shfl_up_sync(0xffffffffu, sum, o);
+        if (lane >= o)
+            sum += x;
+    }
+    const long long total = __shfl_sync(0xffffffffu, sum, 31);
+#pragma unroll
+    for (int i = 0; i < 2; i++) {
+        const int t = 2 * lane + i;
+        const long long g = i ? sum : sum - b;
+        const float high = (float)g, low = (float)(g - (long long)high);
+        D.log[t] = t < first_bad ? make_float2(high * 0x1p-40f, low * 0x1p-40f) : make_float2(nan, nan);
+        D.since[t] = t < first_bad ? exp2f(high * 0x1p-40f) : nan;
+        D.left[t] = t < rows ? exp2f((float)(total - g) * 0x1p-40f) : 0.0f;
+    }
+    if (lane == 0) {
+        // a state that decays slowly keeps its own digits: grow = decay - 1, and the
+        // state itself beside it (a decay near 1 rounded to 24 bits, times the
+        // state, tile after tile, would drift by 2^-25 each)
+        const float x = (float)total * 0x1p-40f;
+        const bool slow = x > -0.7f && x < 0.7f;
+        D.grow = first_bad < kTile ? nan : slow ? expm1f(x * 0.693147180559945309417f) : exp2f(x);
+        D.keep = slow ? 1.0f : 0.0f;
+    }
+}
+
+// Four warps: k times the decay to the tile's end, in parts of 16 bits, and the
+// weights P = (Q K^T) * decays, of tokens up to the row's own.
+template <bool kBf16, bool kStatesOnly>
+__device__ __forceinline__ void weigh(const ScanPlan &P, ScanControl &C, uint8_t *mem) {
+    Tiles T(C.item, P.L.block_size), ahead(C.item, P.L.block_size);
+    const int lane = threadIdx.x & 31, quarter = (threadIdx.x >> 5) - kFirstWeightWarp, tid = threadIdx.x - kFirstWeightWarp * 32;
+    const uint32_t lanes = C.tmem + ((uint32_t)(quarter * 32) << 16);
+    const int ra = quarter * 16 + lane / 4, rb = ra + 8;  // this thread's rows of P
+    uint8_t *const parts = mem + kStages * kStageBytes, *const weights = parts + kParts * 2 * kPanel;
+    const float *const decay = P.L.decay + (int64_t)C.item.h * P.L.decay_head;
+    float g0 = 0.0f, g1 = 0.0f;
+    auto fetch = [&] {
+        g0 = g1 = 0.0f;
+        if (quarter == 0 && ahead.next()) {
+            const float *at = decay + (ahead.row + 2 * lane) * P.L.decay_row;
+            if (2 * lane < ahead.rows)
+                g0 = *at;
+            if (2 * lane + 1 < ahead.rows)
+                g1 = at[P.L.decay_row];
+        }
+    };
+    fetch();
+    while (T.next()) {
+        const uint32_t n = T.n;
+        const int st = n % kStages;
+        Decays &D = C.decays[n % kRing];
+        if (n >= 1)
+            scan_wait(C, &C.keys_free, (n - 1) & 1, P.L.status);
+        if (quarter == 0) {
+            sum_decays(D, g0, g1, T.rows);
+            fetch();
+        }
+        weights_sync();
+        if (kBf16 && tid == 0)
+            bar_arrive(&C.decays_full[n & 1]);
+        scan_wait(C, &C.full[st], (n / kStages) & 1, P.L.status);
+        const uint8_t *const keys = mem + st * kStageBytes + 2 * kPanel;
+        if constexpr (kBf16) {
+            // three truncated parts hold all 24 bits
+#pragma unroll 2
+            for (int c = tid; c < P.k_panels * (kPanel / 16); c += kWeightWarps * 32) {
+                const int row = c >> 3 & (kTile - 1);
+                uint32_t o[3][4] = {};
+                if (row < T.rows) {
+                    const uint4 k = *reinterpret_cast<const uint4 *>(keys + c * 16);
+                    const uint32_t w[4] = {k.x, k.y, k.z, k.w};
+                    const float f = D.left[row];
+#pragma unroll
+                    for (int i = 0; i < 4; i++) {
+                        const float x = __uint_as_float(w[i] << 16) * f, y = __uint_as_float(w[i] & 0xffff0000u) * f;
+                        const float x1 = x - truncated(x), y1 = y - truncated(y);
+                        o[0][i] = upper(x, y);
+                        o[1][i] = upper(x1, y1);
+                        o[2][i] = upper(x1 - truncated(x1), y1 - truncated(y1));
+                    }
+                }
+#pragma unroll
+                for (int p = 0; p < 3; p++)
+                    *reinterpret_cast<uint4 *>(parts + p * 2 * kPanel + c * 16) = make_uint4(o[p][0], o[p][1], o[p][2], o[p][3]);
+            }
+        } else {
+            // two rounded parts of the values brought below 2^15 by a power of two
+            float top = 0.0f;
+            for (int c = tid; c < P.k_panels * (kPanel / 16); c += kWeightWarps * 32) {
+                const int row = c >> 3 & (kTile - 1);
+                if (row < T.rows) {
+                    const uint4 k = *reinterpret_cast<const uint4 *>(keys + c * 16);
+                    const uint32_t w[4] = {k.x, k.y, k.z, k.w};
+                    const float f = D.left[row];
+#pragma unroll
+                    for (int i = 0; i < 4; i++)
+                        top = fmaxf(top, fmaxf(fabsf(from_q(w[i] & 0xffff, false)), fabsf(from_q(w[i] >> 16, false))) * f);
+                }
+            }
+            top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
+            if (lane == 0)
+                C.top[quarter] = top;
+            weights_sync();
+            top = fmaxf(fmaxf(C.top[0], C.top[1]), fmaxf(C.top[2], C.top[3]));
+            const int e = lift_of(top);
+            const float up = power(e);
+            if (tid == 0) {
+                D.unit = power(-e);
+                bar_arrive(&C.decays_full[n & 1]);
+            }
+#pragma unroll 2
+            for (int c = tid; c < P.k_panels * (kPanel / 16); c += kWeightWarps * 32) {
+                const int row = c >> 3 & (kTile - 1);
+                uint32_t o[2][4] = {};
+                if (row < T.rows) {
+                    const uint4 k = *reinterpret_cast<const uint4 *>(keys + c * 16);
+                    const uint32_t w[4] = {k.x, k.y, k.z, k.w};
+                    const float f = D.left[row];
+#pragma unroll
+                    for (int i = 0; i < 4; i++) {
+                        const float x = from_q(w[i] & 0xffff, false) * f * up, y = from_q(w[i] >> 16, false) * f * up;
+                        o[0][i] = pack<false>(x, y);
+                        o[1][i] = pack<false>(x - from_q(o[0][i] & 0xffff, false), y - from_q(o[0][i] >> 16, false));
+                    }
+                }
+#pragma unroll
+                for (int p = 0; p < 2; p++)
+                    *reinterpret_cast<uint4 *>(parts + p * 2 * kPanel + c * 16) = make_uint4(o[p][0], o[p][1], o[p][2], o[p][3]);
+            }
+        }
+        // rows behind the tile's last belong to others: as values they take part
+        // with weights of 0, which infinities and NaN would not bear
+        if (T.rows < kTile) {
+            uint8_t *const values = mem + st * kStageBytes + 4 * kPanel;
+            for (int c = tid; c < P.v_panels * (kPanel / 16); c += kWeightWarps * 32)
+                if ((c >> 3 & (kTile - 1)) >= T.rows)
+                    *reinterpret_cast<uint4 *>(values + c * 16) = make_uint4(0, 0, 0, 0);
+        }
+        fence_async();
+        __syncwarp();
+        if (lane == 0)
+            bar_arrive(&C.keys_full);
+        if (kStatesOnly)
+            continue;
+
+        scan_wait(C, &C.score_full[n & 1], (n >> 1) & 1, P.L.status);
+        fence_after();
+        uint32_t raw[2][16];
+        load_s(raw[0], lanes + kScores + (n & 1) * 64);
+        if (quarter >= 2)
+            load_s(raw[1], lanes + kScores + (n & 1) * 64 + 32);
+        wait_ld();
+        fence_before();
+        __syncwarp();
+        if (lane == 0)
+            bar_arrive(&C.score_free[n & 1]);
+        if (n >= 2)
+            scan_wait(C, &C.weight_free[n & 1], (n / 2 - 1) & 1, P.L.status);
+        const float2 la = D.log[ra], lb = D.log[rb];
+        uint8_t *const pa = weights + (n & 1) * kPanel + ra * 128 + 4 * (lane & 3), *const pb = pa + 8 * 128;
+        const int x = ra & 7;  // rb & 7 is the same
+        float p[8][4];
+        float ta = 0.0f, tb = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 8; i++) {
+            if (i > 2 * quarter + 1)
+                continue;  // tokens behind the rows': 0 from the start
+            const float4 lc = *reinterpret_cast<const float4 *>(&D.log[8 * i + 2 * (lane & 3)]);
+            const uint32_t *s = &raw[i >> 2][4 * (i & 3)];
+            p[i][0] = __uint_as_float(s[0]) * exp2_fast((la.x - lc.x) + (la.y - lc.y));
+            p[i][1] = __uint_as_float(s[1]) * exp2_fast((la.x - lc.z) + (la.y - lc.w));
+            p[i][2] = __uint_as_float(s[2]) * exp2_fast((lb.x - lc.x) + (lb.y - lc.y));
+            p[i][3] = __uint_as_float(s[3]) * exp2_fast((lb.x - lc.z) + (lb.y - lc.w));
+            if (i >= 2 * quarter) {
+                const int c = 8 * i + 2 * (lane & 3);
+                p[i][0] = c <= ra ? p[i][0] : 0.0f;
+                p[i][1] = c + 1 <= ra ? p[i][1] : 0.0f;
+                p[i][2] = c <= rb ? p[i][2] : 0.0f;
+                p[i][3] = c + 1 <= rb ? p[i][3] : 0.0f;
+            }
+            if constexpr (!kBf16) {
+                ta = fmaxf(ta, fmaxf(fabsf(p[i][0]), fabsf(p[i][1])));
+                tb = fmaxf(tb, fmaxf(fabsf(p[i][2]), fabsf(p[i][3])));
+            }
+        }
+        float ua = 1.0f, ub = 1.0f;
+        if constexpr (!kBf16) {
+            // f16 has not binary32's range: a row's weights are brought below 2^15
+            for (int o = 1; o < 4; o <<= 1) {
+                ta = fmaxf(ta, __shfl_xor_sync(0xffffffffu, ta, o));
+                tb = fmaxf(tb, __shfl_xor_sync(0xffffffffu, tb, o));
+            }
+            const int ea = lift_of(ta), eb = lift_of(tb);
+            ua = power(ea);
+            ub = power(eb);
+            if ((lane & 3) == 0) {
+                D.lift[ra] = power(-ea);
+                D.lift[rb] = power(-eb);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 8; i++) {
+            if (i > 2 * quarter + 1)
+                continue;
+            *reinterpret_cast<uint32_t *>(pa + ((i ^ x) << 4)) = pack<kBf16>(p[i][0] * ua, p[i][1] * ua);
+            *reinterpret_cast<uint32_t *>(pb + ((i ^ x) << 4)) = pack<kBf16>(p[i][2] * ub, p[i][3] * ub);
+        }
+        fence_async();
+        __syncwarp();
+        if (lane == 0)
+            bar_arrive(&C.weight_full[n & 1]);
+    }
+}
+
+// Eight warps: the state, turned, in registers: warps w and w + 4 hold values 32 w
+// .. 32 w + 31 (a lane each), w the first 64 keys, w + 4 the others. Of the
+// result w takes the tile's first 32 tokens, w + 4 the last.
+template <bool kBf16, bool kStatesOnly>
+__device__ __forceinline__ void carry(const ScanPlan &P, ScanControl &C) {
+    Tiles T(C.item, P.L.block_size);
+    const LinearPlan &L = P.L;
+    const Item &I = C.item;
+    const int lane = threadIdx.x & 31, quarter = (threadIdx.x >> 5) & 3, half = threadIdx.x >> 7;
+    const uint32_t lanes = C.tmem + ((uint32_t)(quarter * 32) << 16);
+    const int j = quarter * 32 + lane, i0 = 64 * half;
+    const bool mine = i0 < L.dk;
+    const int64_t head = (int64_t)I.h * L.dk * L.dv, at = (int64_t)i0 * L.dv + j;
+    const int64_t slot_size = (int64_t)L.H * L.dk * L.dv;
+    float s[64];
+#pragma unroll
+    for (int i = 0; i < 64; i++)
+        s[i] = 0.0f;
+    auto read = [&](const float *from) {
+        if (j < L.dv)
+#pragma unroll
+            for (int i = 0; i < 64; i++)
+                if (i0 + i < L.dk)
+                    s[i] = __ldcs(from + at + (int64_t)i * L.dv);
+    };
+    auto write = [&](float *to) {
+        if (j < L.dv)
+#pragma unroll
+            for (int i = 0; i < 64; i++)
+                if (i0 + i < L.dk)
+                    __stcs(to + at + (int64_t)i * L.dv, s[i]);
+    };
+    // where a state is at hand before the item's tokens
+    float *const slot = P.slots + (int64_t)I.slot * slot_size + head;
+    if (kStatesOnly) {
+        if (I.row == __ldca(L.starts + I.r)) {  // the request's first segment
+            if (I.first >= 0)
+                read(L.pages + I.first * L.page_stride + head);
+            write(slot);
+        }
+    } else if (I.slot >= 0) {
+        read(slot);
+    } else if (I.first >= 0) {
+        read(L.pages + I.first * L.page_stride + head);
+    }
+    float total = 0.0f;  // log2 of the decay over the item
+    while (T.next()) {
+        const uint32_t n = T.n;
+        const Decays &D = C.decays[n % kRing];
+        float from_state = L.scale;  // f16: times what the state's row was divided by
+        if (!kStatesOnly) {
+            float up = 1.0f;
+            if constexpr (!kBf16) {
+                float top = 0.0f;
+#pragma unroll
+                for (int i = 0; i < 64; i++)
+                    top = fmaxf(top, fabsf(s[i]));
+                C.row_top[half][j] = top;
+                asm volatile("bar.sync %0, 64;" ::"r"(2 + quarter) : "memory");
+                top = fmaxf(top, C.row_top[half ^ 1][j]);
+                const int e = lift_of(top);
+                up = power(e);
+                from_state *= power(-e);
+            }
+            if (mine) {
+#pragma unroll
+                for (int c = 0; c < 2; c++) {
+                    uint32_t high[16], low[16];
+#pragma unroll
+                    for (int i = 0; i < 16; i++) {
+                        const float x = s[32 * c + 2 * i] * up, y = s[32 * c + 2 * i + 1] * up;
+                        if constexpr (kBf16) {
+                            high[i] = upper(x, y);
+                            low[i] = pack<true>(x - truncated(x), y - truncated(y));
+                        } else {
+                            high[i] = pack<false>(x, y);
+                            low[i] = pack<false>(x - from_q(high[i] & 0xffff, false), y - from_q(high[i] >> 16, false));
+                        }
+                    }
+                    store_o(high, lanes + kStateHigh + 32 * half + 16 * c);
+                    store_o(low, lanes + kStateLow + 32 * half + 16 * c);
+                }
+                wait_st();
+            }
+            fence_before();
+            __syncwarp();
+            if (lane == 0)
+                bar_arrive(&C.state_full);
+        }
+        // the block that is written to, asked for early
+        int32_t block = -1;
+        if (!kStatesOnly && (T.block_ends || (I.ends && T.last())))
+            block = __ldca(L.table + I.r * L.row_stride + T.page);
+
+        scan_wait(C, &C.decays_full[n & 1], (n >> 1) & 1, L.status);
+        const float grow = D.grow, keep = D.keep, unit = kBf16 ? 1.0f : D.unit;
+        if (kStatesOnly)
+            total += D.log[kTile - 1].x + D.log[kTile - 1].y;
+        if (!kBf16 && !kStatesOnly)
+            scan_wait(C, &C.weight_full[n & 1], (n >> 1) & 1, L.status);
+        scan_wait(C, &C.update_full, n & 1, L.status);
+        fence_after();
+        if (mine) {
+#pragma unroll
+            for (int c = 0; c < 4; c++) {
+                uint32_t u[16];
+                load_o(u, lanes + kUpdate + i0 + 16 * c);
+                wait_ld();
+#pragma unroll
+                for (int i = 0; i < 16; i++) {
+                    const float x = kBf16 ? __uint_as_float(u[i]) : __uint_as_float(u[i]) * unit;
+                    float &y = s[16 * c + i];
+                    y = fmaf(keep, y, fmaf(grow, y, x));
+                }
+            }
+        }
+        fence_before();
+        __syncwarp();
+        if (lane == 0)
+            bar_arrive(&C.update_free);
+        if (block >= 0 && block < L.num_blocks)
+            write(L.pages + block * L.page_stride + head);
+        else if (block != -1 && threadIdx.x == 0)
+            atomicOr(L.status, LMC_ST_BLOCK_OOR);
+        __syncwarp();
+        if (kStatesOnly)
+            continue;
+
+        scan_wait(C, &C.out_full, n & 1, L.status);
+        fence_after();
+        uint16_t *out = L.out + (T.row + 32 * half) * L.out_row + (int64_t)I.h * L.out_head + j;
+        const int rows = T.rows - 32 * half;
+#pragma unroll
+        for (int c = 0; c < 2; c++) {
+            uint32_t a[16], b[16];
+            load_o(a, lanes + kFromState + 32 * half + 16 * c);
+            load_o(b, lanes + kFromTile + 32 * half + 16 * c);
+            wait_ld();
+            if (j < L.dv)
+#pragma unroll
+                for (int i = 0; i < 16; i++) {
+                    const int t = 32 * half + 16 * c + i;
+                    const float x = __uint_as_float(a[i]) * (D.since[t] * from_state);
+                    const float y = kBf16 ? L.scale : L.scale * D.lift[t];
+                    if (16 * c + i < rows)
+                        out[(int64_t)(16 * c + i) * L.out_row] = to_out(fmaf(__uint_as_float(b[i]), y, x), kBf16);
+                }
+            __syncwarp();
+        }
+        fence_before();
+        __syncwarp();
+        if (lane == 0)
+            bar_arrive(&C.out_free);
+    }
+    if (kStatesOnly) {
+        write(slot + slot_size);
+        if (threadIdx.x == 0)
+            P.totals[((int64_t)I.slot + 1) * L.H + I.h] = total;
+    }
+}
+
+// A CTA that gave up: what it left running ends (or the limit runs out) before
+// its memory goes to another.
+__device__ __forceinline__ void scan_outlast(uint64_t *bar, uint32_t parity) {
+    for (uint32_t i = 0; i < kWaitLimit && !bar_try(bar, parity); i++) {
+    }
+}
+
+__device__ void scan_wind_up(ScanControl &C, int warp) {
+    if (warp == kForwardWarp || warp == kStateProductWarp) {
+        uint64_t *const done = &C.ended[warp - kForwardWarp];
+        if (elect())
+            commit(done);
+        __syncwarp();
+        scan_outlast(done, 0);
+    } else if (warp == kLoadWarp) {
+        for (uint32_t k = C.tiles > kStages ? C.tiles - kStages : 0; k < C.tiles; k++)
+            scan_outlast(&C.full[k % kStages], (k / kStages) & 1);
+    }
+}
+
+template <bool kBf16, bool kStatesOnly>
+__global__ void __launch_bounds__(kScanThreads, 1) lmc_linear_scan_kernel(const __grid_constant__ ScanPlan P) {
+    extern __shared__ __align__(1024) uint8_t scan_mem[];
+    __shared__ ScanControl C;
+    const int warp = threadIdx.x >> 5;
+    if (threadIdx.x == 0) {
+        for (int i = 0; i < kStages; i++) {
+            bar_init(&C.full[i], 1);
+            bar_init(&C.free[i], kStatesOnly ? 1 : 2);
+        }
+        for (int i = 0; i < 2; i++) {
+            bar_init(&C.decays_full[i], 1);
+            bar_init(&C.score_full[i], 1);
+            bar_init(&C.score_free[i], kWeightWarps);
+            bar_init(&C.weight_full[i], kWeightWarps);
+            bar_init(&C.weight_free[i], 1);
+            bar_init(&C.ended[i], 1);
+        }
+        bar_init(&C.keys_full, kWeightWarps);
+        bar_init(&C.keys_free, 1);
+        bar_init(&C.update_full, 1);
+        bar_init(&C.update_free, kStateWarps);
+        bar_init(&C.state_full, kStateWarps);
+        bar_init(&C.out_full, 1);
+        bar_init(&C.out_free, kStateWarps);
+        C.gave_up = 0;
+        C.tiles = 0;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    // weights of tokens behind a row's own are never written: 0
+    for (int i = threadIdx.x; i < 2 * kPanel / 16; i += kScanThreads)
+        reinterpret_cast<uint4 *>(scan_mem + kStages * kStageBytes + kParts * 2 * kPanel)[i] = make_uint4(0, 0, 0, 0);
+    fence_async();
+    wait_for_launch();
+    if (warp == 0)
+        find_item<kStatesOnly>(P, C.item);
+    __syncthreads();
+    if (!C.item.work)
+        return;
+    // (asked for after the wait: a kernel before this one may still hold it)
+    if (warp == kForwardWarp) {
+        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_addr(&C.tmem))
+                     : "memory");
+        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+    }
+    fence_before();
+    __syncthreads();
+    fence_after();
+    let_next_start();
+
+    if (warp < kStateWarps)
+        carry<kBf16, kStatesOnly>(P, C);
+    else if (warp < kLoadWarp)
+        weigh<kBf16, kStatesOnly>(P, C, scan_mem);
+    else if (warp == kLoadWarp)
+        load_tiles<kStatesOnly>(P, C, scan_mem);
+    else if (warp == kForwardWarp)
+        multiply_forward<kBf16, kStatesOnly>(P, C, scan_mem);
+    else if (!kStatesOnly)
+        multiply_state<kBf16>(P, C, scan_mem);
+    __syncwarp();
+    fence_before();
+    __syncthreads();
+    fence_after();
+    if (C.gave_up) {
+        scan_wind_up(C, warp);
+        __syncthreads();
+    }
+    if (warp == kForwardWarp)
+        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(C.tmem));
+}
+
+// The states before a cut request's segments, from what each segment adds: slot
+// i + 1 holds the state after segment 0 (i = 0), or what segment i adds, and
+// gets the state after it.
+constexpr int kJoinThreads = 256;
+
+__global__ void __launch_bounds__(kJoinThreads) lmc_linear_join_kernel(const __grid_constant__ ScanPlan P) {
+    __shared__ int32_t first, cuts;
+    const LinearPlan &L = P.L;
+    const int parts = (L.dk * L.dv / 4 + kJoinThreads - 1) / kJoinThreads;
+    const int part = blockIdx.x % parts, h = blockIdx.x / parts % L.H;
+    const int64_t v = blockIdx.x / parts / L.H;
+    wait_for_launch();
+    let_next_start();
+    if (threadIdx.x < 32) {
+        const int r = request_of(P, v, false);
+        int n = 0;
+        int64_t slot = -1;
+        if (r >= 0) {
+            slot = __ldca(L.starts + r) / P.segment;
+            n = (int)(span_of(L, r).count / P.segment);
+        }
+        if (threadIdx.x == 0) {
+            first = slot == v ? 1 : 0;
+            cuts = n;
+        }
+    }
+    __syncthreads();
+    const int e = part * kJoinThreads + threadIdx.x;
+    if (!first || cuts < 3 || e >= L.dk * L.dv / 4)
+        return;
+    const int64_t stride = (int64_t)L.H * L.dk * L.dv / 4;
+    float4 *at = reinterpret_cast<float4 *>(P.slots) + (v + 1) * stride + (int64_t)h * (L.dk * L.dv / 4) + e;
+    float4 s = __ldcg(at);
+#pragma unroll 8
+    for (int i = 2; i < cuts; i++) {
+        at += stride;
+        const float4 u = __ldcg(at);
+        const float a = exp2f(__ldca(P.totals + (v + i) * L.H + h));
+        s.x = fmaf(a, s.x, u.x);
+        s.y = fmaf(a, s.y, u.y);
+        s.z = fmaf(a, s.z, u.z);
+        s.w = fmaf(a, s.w, u.w);
+        __stcg(at, s);
     }
 }
 
@@ -288,6 +1145,45 @@ int launch_steps(const LinearPlan &P, cudaStream_t stream) {
     return follow(kern, dim3((unsigned)grid), kStepThreads, 0, stream, P) ? LMC_OK : LMC_ERR_CUDA;
 }
 
+// Tokens of an SM's even share: no request is cut into segments shorter than that.
+int64_t segment_of(int64_t num_rows, int64_t H) {
+    return std::max(kLeastSegment, ((num_rows * H + kSms - 1) / kSms + kTile - 1) / kTile * kTile);
+}
+
+struct ScanWork {
+    int64_t segment, slots, totals, bytes;  // tokens; offsets
+};
+
+ScanWork scan_work(int64_t rec_bytes, int64_t H, int64_t num_rows) {
+    ScanWork W;
+    W.segment = segment_of(num_rows, H);
+    const int64_t n = num_rows / W.segment;
+    W.slots = 0;
+    W.totals = (n * rec_bytes + 255) / 256 * 256;
+    W.bytes = W.totals + (n * H * 4 + 255) / 256 * 256 + 256;
+    return W;
+}
+
+// (values, rows, heads) of 16 bits each, read in boxes of a tile's rows of one
+// head: of both panels of 64 values at once (`whole`), or of one.
+bool rows_map(CUtensorMap *map, bool bf16, const void *base, int64_t dim, int64_t rows, int64_t heads, int64_t row,
+              int64_t head, bool whole) {
+    const EncodeTiled fn = encoder();
+    if (fn == nullptr)
+        return false;
+    const cuuint64_t panels = whole ? (cuuint64_t)dim / 64 : 1;
+    const cuuint64_t row_bytes = rows > 1 ? (cuuint64_t)row * 2 : (cuuint64_t)dim * 2;
+    const cuuint64_t head_bytes = heads > 1 ? (cuuint64_t)head * 2 : (cuuint64_t)dim * 2;
+    const cuuint64_t dims[4] = {whole ? 64 : (cuuint64_t)dim, (cuuint64_t)rows, panels, (cuuint64_t)heads};
+    const cuuint64_t strides[3] = {row_bytes, 128, head_bytes};
+    const cuuint32_t boxes[4] = {64, kTile, (cuuint32_t)panels, 1};
+    const cuuint32_t steps[4] = {1, 1, 1, 1};
+    return fn(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
+              const_cast<void *>(base), dims, strides, boxes, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
+           CUDA_SUCCESS;
+}
+
 }  // namespace
 
 extern "C" int lmc_linear_step(const lmc_layout *L, const lmc_linear *a, void *pool, uint32_t *status, void *stream) {
@@ -303,9 +1199,10 @@ extern "C" int lmc_linear_step(const lmc_layout *L, const lmc_linear *a, void *p
 extern "C" int lmc_linear_scan_workspace(const lmc_layout *L, int32_t layer, int32_t num_requests, int64_t num_rows,
                                          int32_t num_heads, int64_t *out) {
     if (L == nullptr || layer < 0 || (size_t)layer >= L->desc.size() || L->specs[layer].kind != LMC_LAYER_KDA ||
-        num_requests < 0 || num_requests > 1 << 20 || num_rows < 0 || num_heads <= 0 || num_heads > 65535 || out == nullptr)
+        num_requests < 0 || num_requests > 1 << 20 || num_rows < 0 || num_rows > INT32_MAX || num_heads <= 0 ||
+        num_heads > 65535 || out == nullptr)
         return LMC_ERR_INVALID_ARG;
-    *out = 256;
+    *out = scan_work(L->specs[layer].rec_bytes, num_heads, num_rows).bytes;
     return LMC_OK;
 }
 
@@ -313,14 +1210,48 @@ extern "C" int lmc_linear_scan(const lmc_layout *L, const lmc_linear *a, const i
                                void *pool, void *workspace, int64_t workspace_bytes, uint32_t *status, void *stream) {
     if (const int rc = check_linear(L, a, num_rows, pool, status); rc != LMC_OK)
         return rc;
-    if (workspace == nullptr || workspace_bytes < 256 || starts == nullptr)
+    if (num_rows > INT32_MAX)
+        return LMC_ERR_INVALID_ARG;
+    const ScanWork W = scan_work(L->specs[a->layer].rec_bytes, a->num_heads, num_rows);
+    if (workspace == nullptr || workspace_bytes < W.bytes || starts == nullptr)
         return LMC_ERR_INVALID_ARG;
     if (((uintptr_t)workspace & 255) != 0 || ((uintptr_t)starts & 3) != 0)
         return LMC_ERR_ALIGN;
     if (num_rows == 0 || a->num_requests == 0)
         return LMC_OK;
-    LinearPlan P = {};
-    plan_linear(P, L, a, num_rows, pool, status);
-    P.starts = starts;
-    return launch_steps(P, static_cast<cudaStream_t>(stream));
+    ScanPlan P = {};
+    plan_linear(P.L, L, a, num_rows, pool, status);
+    P.L.starts = starts;
+    P.segment = W.segment;
+    P.slots = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + W.slots);
+    P.totals = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + W.totals);
+    P.k_panels = (P.L.dk + 63) / 64;
+    P.v_panels = (P.L.dv + 63) / 64;
+    const bool bf16 = P.L.bf16, whole_k = P.L.dk % 64 == 0, whole_v = P.L.dv % 64 == 0;
+    P.k_copies = whole_k ? 1 : P.k_panels;
+    P.v_copies = whole_v ? 1 : P.v_panels;
+    const int64_t H = a->num_heads, K = a->num_key_heads;
+    const int64_t cuts = num_rows / W.segment;
+    const int64_t grid = (cuts + a->num_requests) * H, states = cuts * H;
+    if (grid > INT32_MAX)
+        return LMC_ERR_OVERFLOW;
+    if (!rows_map(&P.q, bf16, a->q, P.L.dk, num_rows, K, a->q_row_stride, a->q_head_stride, whole_k) ||
+        !rows_map(&P.k, bf16, a->k, P.L.dk, num_rows, K, a->k_row_stride, a->k_head_stride, whole_k) ||
+        !rows_map(&P.v, bf16, a->v, P.L.dv, num_rows, H, a->v_row_stride, a->v_head_stride, whole_v))
+        return LMC_ERR_CUDA;
+    auto scan = bf16 ? lmc_linear_scan_kernel<true, false> : lmc_linear_scan_kernel<false, false>;
+    auto segments = bf16 ? lmc_linear_scan_kernel<true, true> : lmc_linear_scan_kernel<false, true>;
+    static std::atomic<uint64_t> allowed[4];
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (!allow_shared_memory(allowed[bf16], scan, kScanMemory) ||
+        !allow_shared_memory(allowed[2 + bf16], segments, kScanMemory))
+        return LMC_ERR_CUDA;
+    if (cuts >= 2) {  // a request may be cut
+        if (!follow(segments, dim3((unsigned)states), kScanThreads, kScanMemory, s, P))
+            return LMC_ERR_CUDA;
+        const int64_t parts = (P.L.dk * P.L.dv / 4 + kJoinThreads - 1) / kJoinThreads;
+        if (cuts >= 3 && !follow(lmc_linear_join_kernel, dim3((unsigned)(states * parts)), kJoinThreads, 0, s, P))
+            return LMC_ERR_CUDA;
+    }
+    return follow(scan, dim3((unsigned)grid), kScanThreads, kScanMemory, s, P) ? LMC_OK : LMC_ERR_CUDA;
 }
