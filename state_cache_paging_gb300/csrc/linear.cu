@@ -188,10 +188,13 @@ constexpr int kStateWarps = 8;
 constexpr int kFirstWeightWarp = 8, kWeightWarps = 4;
 constexpr int kLoadWarp = 12, kForwardWarp = 13, kStateProductWarp = 14;
 constexpr int kScanThreads = 15 * 32;
-constexpr int kScanMemory = kStages * kStageBytes + kParts * 2 * kPanel + 2 * kPanel;
+// shared memory behind the stages: k's parts, the weights, the result on its way
+constexpr int kKeysAt = kStages * kStageBytes, kWeightsAt = kKeysAt + kParts * 2 * kPanel, kResultAt = kWeightsAt + kPanel;
+constexpr int kWarpResult = 32 * 64;  // bytes of a warp's part of a result: 32 tokens, 32 values
+constexpr int kScanMemory = kResultAt + kStateWarps * kWarpResult;
 constexpr uint32_t kWaitLimit = 1u << 22;
 // columns of tensor memory
-constexpr uint32_t kScores = 0, kUpdate = 128, kFromState = 256, kFromTile = 320, kStateHigh = 384, kStateLow = 448;
+constexpr uint32_t kScores = 0, kUpdate = 128, kFromState = 256, kFromTile = 384, kState = 448;
 constexpr int kRing = 4;              // tiles whose decays are at hand
 constexpr int kSms = 152;
 constexpr int64_t kLeastSegment = 512;  // tokens
@@ -203,6 +206,7 @@ struct ScanPlan {
     float *slots;        // [num_rows / segment][H][dk][dv]: the states before segments
     float *totals;       // [num_rows / segment][H]: the decay over the segment before
     int32_t k_copies, v_copies, k_panels, v_panels;  // copies for all panels, panels
+    int32_t wide_out;    // the result is written 16 bytes at a time
 };
 
 // A CTA's tokens: a segment of a request, one head.
@@ -224,7 +228,7 @@ struct alignas(16) Decays {
     float left[kTile];   // from the token to the tile's end
     float since[kTile];  // from the tile's start up to the token
     float lift[kTile];   // f16: what the token's weights were divided by
-    float grow, keep;    // state = grow * state + keep * state + update * unit
+    float grow;          // decay over the tile
     float unit;          // f16: what k times its decay was divided by
 };
 
@@ -232,9 +236,10 @@ static_assert(sizeof(Decays) % 16 == 0, "two tokens' logs are read at once");
 
 struct ScanControl {
     uint64_t full[kStages], free[kStages];
-    uint64_t decays_full[2];
+    uint64_t decays_full[kRing];
+    uint64_t unit_full[2], lift_full[2];  // f16
     uint64_t score_full[2], score_free[2];
-    uint64_t weight_full[2], weight_free[2];
+    uint64_t weight_full, weight_free;
     uint64_t keys_full, keys_free;
     uint64_t update_full, update_free;
     uint64_t state_full, out_full, out_free;
@@ -378,16 +383,70 @@ __device__ __forceinline__ void find_item(const ScanPlan &P, Item &I) {
         I = J;
 }
 
-// One warp: q, k and v of each tile by TMA. (Rows behind a tile's last one come
-// along; they are not read into a result.)
+// A tile's decays, by one warp: lane l's are those of tokens 2 l and 2 l + 1.
+// They are summed as whole numbers of 2^-40 (exactly, in any order), so sums far
+// from 0 lose nothing of the differences that count.
+// `drift`: how much the tiles' rounded decays lack of the exact ones so far,
+// relatively; a tile's makes up for it, so that a state that decays slowly by
+// the same factor tile after tile keeps its digits.
+__device__ __forceinline__ void sum_decays(Decays &D, float g0, float g1, int rows, float &drift) {
+    const int lane = threadIdx.x & 31;
+    const float nan = __int_as_float(0x7fffffff);
+    const uint32_t bad0 = __ballot_sync(0xffffffffu, g0 != g0), bad1 = __ballot_sync(0xffffffffu, g1 != g1);
+    const int first_bad = min(bad0 ? 2 * (__ffs(bad0) - 1) : kTile, bad1 ? 2 * (__ffs(bad1) - 1) + 1 : kTile);
+    auto whole = [](float g) {
+        return __float2ll_rn(fminf(fmaxf(g, kLeastDecay), -kLeastDecay) * 1.44269504088896340736f * 0x1p40f);
+    };
+    const long long a = whole(g0), b = whole(g1);
+    long long sum = a + b;
+    for (int o = 1; o < 32; o <<= 1) {
+        const long long x = __shfl_up_sync(0xffffffffu, sum, o);
+        if (lane >= o)
+            sum += x;
+    }
+    const long long total = __shfl_sync(0xffffffffu, sum, 31);
+#pragma unroll
+    for (int i = 0; i < 2; i++) {
+        const int t = 2 * lane + i;
+        const long long g = i ? sum : sum - b;
+        const float high = (float)g, low = (float)(g - (long long)high);
+        D.log[t] = t < first_bad ? make_float2(high * 0x1p-40f, low * 0x1p-40f) : make_float2(nan, nan);
+        D.since[t] = t < first_bad ? exp2f(high * 0x1p-40f) : nan;
+        D.left[t] = t < rows ? exp2f((float)(total - g) * 0x1p-40f) : 0.0f;
+    }
+    const float x = (float)total * 0x1p-40f;
+    float grow;
+    if (x > -0.7f && x < 0.7f) {
+        const float less = expm1f(x * 0.693147180559945309417f), high = 1.0f + less;
+        const float low = fmaf(high, drift, less - (high - 1.0f));
+        grow = high + low;
+        drift = ((high - grow) + low) / grow;
+    } else {
+        grow = exp2f(x);
+        drift = 0.0f;
+    }
+    if (lane == 0)
+        D.grow = first_bad < kTile ? nan : grow;
+}
+
+// One warp: q, k and v of each tile by TMA, and its decays. (Rows behind a
+// tile's last one come along; they are not read into a result.)
 template <bool kStatesOnly>
 __device__ __forceinline__ void load_tiles(const ScanPlan &P, ScanControl &C, uint8_t *mem) {
     Tiles T(C.item, P.L.block_size);
-    const int h = C.item.h, kh = h / P.L.shared;
+    const int lane = threadIdx.x & 31, h = C.item.h, kh = h / P.L.shared;
     const uint32_t bytes = (uint32_t)((kStatesOnly ? 1 : 2) * P.k_panels + P.v_panels) * kPanel;
+    const float *const decay = P.L.decay + (int64_t)h * P.L.decay_head;
     uint32_t asked = 0;
+    float drift = 0.0f;
     while (T.next()) {
         const int st = (int)uniform(T.n % kStages);
+        float g0 = 0.0f, g1 = 0.0f;
+        const float *const at = decay + (T.row + 2 * lane) * P.L.decay_row;
+        if (2 * lane < T.rows)
+            g0 = *at;
+        if (2 * lane + 1 < T.rows)
+            g1 = at[P.L.decay_row];
         if (T.n >= kStages)
             scan_wait(C, &C.free[st], (T.n / kStages - 1) & 1, P.L.status);
         if (scan_gone(C))
@@ -407,8 +466,12 @@ __device__ __forceinline__ void load_tiles(const ScanPlan &P, ScanControl &C, ui
         }
         __syncwarp();
         asked++;
+        sum_decays(C.decays[T.n % kRing], g0, g1, T.rows, drift);
+        __syncwarp();
+        if (lane == 0)
+            bar_arrive(&C.decays_full[T.n % kRing]);
     }
-    if ((threadIdx.x & 31) == 0)
+    if (lane == 0)
         C.tiles = asked;
 }
 
@@ -421,7 +484,7 @@ __device__ __forceinline__ void multiply_forward(const ScanPlan &P, ScanControl 
     const int keys = 64 * P.k_panels, steps = (P.L.dk + 15) / 16;
     const uint32_t scores = instruction(kBf16, false, 64, kTile);
     const uint32_t update = instruction(kBf16, true, 128, keys) | 1u << 16;  // B turned, too
-    const uint64_t part0 = matrix(smem_addr(mem) + kStages * kStageBytes, kPanel, 1024);
+    const uint64_t part0 = matrix(smem_addr(mem) + kKeysAt, kPanel, 1024);
     while (T.next()) {
         const uint32_t n = T.n;
         const int st = (int)uniform(n % kStages);
@@ -464,36 +527,33 @@ __device__ __forceinline__ void multiply_forward(const ScanPlan &P, ScanControl 
 }
 
 // One warp: the products that make the result, turned: S^T Q^T from the state
-// before the tile, V^T P^T from the tile's own tokens [values x tokens].
+// before the tile, V^T P^T from the tile's own tokens [values x tokens]. The
+// first goes to turns of tensor memory, so that it does not wait for the tile
+// before to be read.
 template <bool kBf16>
 __device__ __forceinline__ void multiply_state(const ScanPlan &P, ScanControl &C, uint8_t *mem) {
     Tiles T(C.item, P.L.block_size);
     const uint32_t tmem = uniform(C.tmem);
     const int steps = (P.L.dk + 15) / 16;
     const uint32_t from_state = instruction(kBf16, false, 128, kTile), from_tile = instruction(kBf16, true, 128, kTile);
-    const uint64_t weight0 = matrix(smem_addr(mem) + kStages * kStageBytes + kParts * 2 * kPanel, 16, 1024);
+    const uint64_t weight = matrix(smem_addr(mem) + kWeightsAt, 16, 1024);
     while (T.next()) {
         const uint32_t n = T.n;
         const int st = (int)uniform(n % kStages);
-        const uint32_t at = smem_addr(mem) + st * kStageBytes;
-        const uint64_t weight = weight0 + uniform(n & 1) * (kPanel >> 4);
+        const uint32_t at = smem_addr(mem) + st * kStageBytes, d = tmem + kFromState + uniform(n & 1) * 64;
         scan_wait(C, &C.full[st], (n / kStages) & 1, P.L.status);
         scan_wait(C, &C.state_full, n & 1, P.L.status);
-        if (n >= 1)
-            scan_wait(C, &C.out_free, (n - 1) & 1, P.L.status);
         __syncwarp();
         fence_after();
         if (elect()) {
             const uint64_t q = matrix(at, 16, 1024);
             for (int s = 0; s < steps; s++)
-                mma_held(tmem + kFromState, tmem + kStateLow + 8 * s, q + (s >> 2) * (kPanel >> 4) + (s & 3) * 2, from_state,
-                         s > 0);
-            for (int s = 0; s < steps; s++)
-                mma_held(tmem + kFromState, tmem + kStateHigh + 8 * s, q + (s >> 2) * (kPanel >> 4) + (s & 3) * 2,
-                         from_state, true);
+                mma_held(d, tmem + kState + 8 * s, q + (s >> 2) * (kPanel >> 4) + (s & 3) * 2, from_state, s > 0);
         }
         __syncwarp();
-        scan_wait(C, &C.weight_full[n & 1], (n >> 1) & 1, P.L.status);
+        scan_wait(C, &C.weight_full, n & 1, P.L.status);
+        if (n >= 1)
+            scan_wait(C, &C.out_free, (n - 1) & 1, P.L.status);
         __syncwarp();
         fence_after();
         if (elect()) {
@@ -502,49 +562,10 @@ __device__ __forceinline__ void multiply_state(const ScanPlan &P, ScanControl &C
             for (int s = 0; s < kTile / 16; s++)
                 mma(tmem + kFromTile, v + s * (2048 >> 4), weight + s * 2, from_tile, s > 0);
             commit(&C.out_full);
-            commit(&C.weight_free[n & 1]);
+            commit(&C.weight_free);
             commit(&C.free[st]);
         }
         __syncwarp();
-    }
-}
-
-// A tile's decays, by one warp: lane l's are those of tokens 2 l and 2 l + 1.
-// They are summed as whole numbers of 2^-40 (exactly, in any order), so sums far
-// from 0 lose nothing of the differences that count.
-__device__ __forceinline__ void sum_decays(Decays &D, float g0, float g1, int rows) {
-    const int lane = threadIdx.x & 31;
-    const float nan = __int_as_float(0x7fffffff);
-    const uint32_t bad0 = __ballot_sync(0xffffffffu, g0 != g0), bad1 = __ballot_sync(0xffffffffu, g1 != g1);
-    const int first_bad = min(bad0 ? 2 * (__ffs(bad0) - 1) : kTile, bad1 ? 2 * (__ffs(bad1) - 1) + 1 : kTile);
-    auto whole = [](float g) {
-        return __float2ll_rn(fminf(fmaxf(g, kLeastDecay), -kLeastDecay) * 1.44269504088896340736f * 0x1p40f);
-    };
-    const long long a = whole(g0), b = whole(g1);
-    long long sum = a + b;
-    for (int o = 1; o < 32; o <<= 1) {
-        const long long x = __shfl_up_sync(0xffffffffu, sum, o);
-        if (lane >= o)
-            sum += x;
-    }
-    const long long total = __shfl_sync(0xffffffffu, sum, 31);
-#pragma unroll
-    for (int i = 0; i < 2; i++) {
-        const int t = 2 * lane + i;
-        const long long g = i ? sum : sum - b;
-        const float high = (float)g, low = (float)(g - (long long)high);
-        D.log[t] = t < first_bad ? make_float2(high * 0x1p-40f, low * 0x1p-40f) : make_float2(nan, nan);
-        D.since[t] = t < first_bad ? exp2f(high * 0x1p-40f) : nan;
-        D.left[t] = t < rows ? exp2f((float)(total - g) * 0x1p-40f) : 0.0f;
-    }
-    if (lane == 0) {
-        // a state that decays slowly keeps its own digits: grow = decay - 1, and the
-        // state itself beside it (a decay near 1 rounded to 24 bits, times the
-        // state, tile after tile, would drift by 2^-25 each)
-        const float x = (float)total * 0x1p-40f;
-        const bool slow = x > -0.7f && x < 0.7f;
-        D.grow = first_bad < kTile ? nan : slow ? expm1f(x * 0.693147180559945309417f) : exp2f(x);
-        D.keep = slow ? 1.0f : 0.0f;
     }
 }
 
@@ -552,38 +573,20 @@ __device__ __forceinline__ void sum_decays(Decays &D, float g0, float g1, int ro
 // weights P = (Q K^T) * decays, of tokens up to the row's own.
 template <bool kBf16, bool kStatesOnly>
 __device__ __forceinline__ void weigh(const ScanPlan &P, ScanControl &C, uint8_t *mem) {
-    Tiles T(C.item, P.L.block_size), ahead(C.item, P.L.block_size);
+    Tiles T(C.item, P.L.block_size);
     const int lane = threadIdx.x & 31, quarter = (threadIdx.x >> 5) - kFirstWeightWarp, tid = threadIdx.x - kFirstWeightWarp * 32;
     const uint32_t lanes = C.tmem + ((uint32_t)(quarter * 32) << 16);
     const int ra = quarter * 16 + lane / 4, rb = ra + 8;  // this thread's rows of P
-    uint8_t *const parts = mem + kStages * kStageBytes, *const weights = parts + kParts * 2 * kPanel;
-    const float *const decay = P.L.decay + (int64_t)C.item.h * P.L.decay_head;
-    float g0 = 0.0f, g1 = 0.0f;
-    auto fetch = [&] {
-        g0 = g1 = 0.0f;
-        if (quarter == 0 && ahead.next()) {
-            const float *at = decay + (ahead.row + 2 * lane) * P.L.decay_row;
-            if (2 * lane < ahead.rows)
-                g0 = *at;
-            if (2 * lane + 1 < ahead.rows)
-                g1 = at[P.L.decay_row];
-        }
-    };
-    fetch();
+    uint8_t *const parts = mem + kKeysAt;
+    uint8_t *const pa = mem + kWeightsAt + ra * 128 + 4 * (lane & 3), *const pb = pa + 8 * 128;
     while (T.next()) {
         const uint32_t n = T.n;
         const int st = n % kStages;
         Decays &D = C.decays[n % kRing];
+        scan_wait(C, &C.decays_full[n % kRing], (n / kRing) & 1, P.L.status);
+        scan_wait(C, &C.full[st], (n / kStages) & 1, P.L.status);
         if (n >= 1)
             scan_wait(C, &C.keys_free, (n - 1) & 1, P.L.status);
-        if (quarter == 0) {
-            sum_decays(D, g0, g1, T.rows);
-            fetch();
-        }
-        weights_sync();
-        if (kBf16 && tid == 0)
-            bar_arrive(&C.decays_full[n & 1]);
-        scan_wait(C, &C.full[st], (n / kStages) & 1, P.L.status);
         const uint8_t *const keys = mem + st * kStageBytes + 2 * kPanel;
         if constexpr (kBf16) {
             // three truncated parts hold all 24 bits
@@ -631,7 +634,7 @@ __device__ __forceinline__ void weigh(const ScanPlan &P, ScanControl &C, uint8_t
             const float up = power(e);
             if (tid == 0) {
                 D.unit = power(-e);
-                bar_arrive(&C.decays_full[n & 1]);
+                bar_arrive(&C.unit_full[n & 1]);
             }
 #pragma unroll 2
             for (int c = tid; c < P.k_panels * (kPanel / 16); c += kWeightWarps * 32) {
@@ -679,10 +682,7 @@ __device__ __forceinline__ void weigh(const ScanPlan &P, ScanControl &C, uint8_t
         __syncwarp();
         if (lane == 0)
             bar_arrive(&C.score_free[n & 1]);
-        if (n >= 2)
-            scan_wait(C, &C.weight_free[n & 1], (n / 2 - 1) & 1, P.L.status);
         const float2 la = D.log[ra], lb = D.log[rb];
-        uint8_t *const pa = weights + (n & 1) * kPanel + ra * 128 + 4 * (lane & 3), *const pb = pa + 8 * 128;
         const int x = ra & 7;  // rb & 7 is the same
         float p[8][4];
         float ta = 0.0f, tb = 0.0f;
@@ -722,7 +722,12 @@ __device__ __forceinline__ void weigh(const ScanPlan &P, ScanControl &C, uint8_t
                 D.lift[ra] = power(-ea);
                 D.lift[rb] = power(-eb);
             }
+            __syncwarp();
+            if (lane == 0)
+                bar_arrive(&C.lift_full[n & 1]);
         }
+        if (n >= 1)
+            scan_wait(C, &C.weight_free, (n - 1) & 1, P.L.status);
 #pragma unroll
         for (int i = 0; i < 8; i++) {
             if (i > 2 * quarter + 1)
@@ -733,7 +738,7 @@ __device__ __forceinline__ void weigh(const ScanPlan &P, ScanControl &C, uint8_t
         fence_async();
         __syncwarp();
         if (lane == 0)
-            bar_arrive(&C.weight_full[n & 1]);
+            bar_arrive(&C.weight_full);
     }
 }
 
@@ -741,11 +746,11 @@ __device__ __forceinline__ void weigh(const ScanPlan &P, ScanControl &C, uint8_t
 // .. 32 w + 31 (a lane each), w the first 64 keys, w + 4 the others. Of the
 // result w takes the tile's first 32 tokens, w + 4 the last.
 template <bool kBf16, bool kStatesOnly>
-__device__ __forceinline__ void carry(const ScanPlan &P, ScanControl &C) {
+__device__ __forceinline__ void carry(const ScanPlan &P, ScanControl &C, uint8_t *mem) {
     Tiles T(C.item, P.L.block_size);
     const LinearPlan &L = P.L;
     const Item &I = C.item;
-    const int lane = threadIdx.x & 31, quarter = (threadIdx.x >> 5) & 3, half = threadIdx.x >> 7;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, quarter = warp & 3, half = warp >> 2;
     const uint32_t lanes = C.tmem + ((uint32_t)(quarter * 32) << 16);
     const int j = quarter * 32 + lane, i0 = 64 * half;
     const bool mine = i0 < L.dk;
@@ -769,6 +774,40 @@ __device__ __forceinline__ void carry(const ScanPlan &P, ScanControl &C) {
                 if (i0 + i < L.dk)
                     __stcs(to + at + (int64_t)i * L.dv, s[i]);
     };
+    // The state as A of its product with q, in 16 bits; what is to be multiplied
+    // to its row's results (f16, which has not binary32's range: rows are brought
+    // below 2^15).
+    auto hand_over = [&] {
+        float up = 1.0f, down = L.scale;
+        if constexpr (!kBf16) {
+            float top = 0.0f;
+#pragma unroll
+            for (int i = 0; i < 64; i++)
+                top = fmaxf(top, fabsf(s[i]));
+            C.row_top[half][j] = top;
+            asm volatile("bar.sync %0, 64;" ::"r"(2 + quarter) : "memory");
+            top = fmaxf(top, C.row_top[half ^ 1][j]);
+            const int e = lift_of(top);
+            up = power(e);
+            down *= power(-e);
+        }
+        if (mine) {
+#pragma unroll
+            for (int c = 0; c < 2; c++) {
+                uint32_t x[16];
+#pragma unroll
+                for (int i = 0; i < 16; i++)
+                    x[i] = pack<kBf16>(s[32 * c + 2 * i] * up, s[32 * c + 2 * i + 1] * up);
+                store_o(x, lanes + kState + 32 * half + 16 * c);
+            }
+            wait_st();
+        }
+        fence_before();
+        __syncwarp();
+        if (lane == 0)
+            bar_arrive(&C.state_full);
+        return down;
+    };
     // where a state is at hand before the item's tokens
     float *const slot = P.slots + (int64_t)I.slot * slot_size + head;
     if (kStatesOnly) {
@@ -783,60 +822,30 @@ __device__ __forceinline__ void carry(const ScanPlan &P, ScanControl &C) {
         read(L.pages + I.first * L.page_stride + head);
     }
     float total = 0.0f;  // log2 of the decay over the item
+    float down = 1.0f;
+    if (!kStatesOnly && I.count > 0)
+        down = hand_over();
+    // a warp's part of a result: rows of 64 bytes, a token each
+    uint8_t *const staged = mem + kResultAt + warp * kWarpResult;
+    const int64_t out_at = (int64_t)I.h * L.out_head + quarter * 32;
     while (T.next()) {
         const uint32_t n = T.n;
         const Decays &D = C.decays[n % kRing];
-        float from_state = L.scale;  // f16: times what the state's row was divided by
-        if (!kStatesOnly) {
-            float up = 1.0f;
-            if constexpr (!kBf16) {
-                float top = 0.0f;
-#pragma unroll
-                for (int i = 0; i < 64; i++)
-                    top = fmaxf(top, fabsf(s[i]));
-                C.row_top[half][j] = top;
-                asm volatile("bar.sync %0, 64;" ::"r"(2 + quarter) : "memory");
-                top = fmaxf(top, C.row_top[half ^ 1][j]);
-                const int e = lift_of(top);
-                up = power(e);
-                from_state *= power(-e);
-            }
-            if (mine) {
-#pragma unroll
-                for (int c = 0; c < 2; c++) {
-                    uint32_t high[16], low[16];
-#pragma unroll
-                    for (int i = 0; i < 16; i++) {
-                        const float x = s[32 * c + 2 * i] * up, y = s[32 * c + 2 * i + 1] * up;
-                        if constexpr (kBf16) {
-                            high[i] = upper(x, y);
-                            low[i] = pack<true>(x - truncated(x), y - truncated(y));
-                        } else {
-                            high[i] = pack<false>(x, y);
-                            low[i] = pack<false>(x - from_q(high[i] & 0xffff, false), y - from_q(high[i] >> 16, false));
-                        }
-                    }
-                    store_o(high, lanes + kStateHigh + 32 * half + 16 * c);
-                    store_o(low, lanes + kStateLow + 32 * half + 16 * c);
-                }
-                wait_st();
-            }
-            fence_before();
-            __syncwarp();
-            if (lane == 0)
-                bar_arrive(&C.state_full);
-        }
         // the block that is written to, asked for early
         int32_t block = -1;
         if (!kStatesOnly && (T.block_ends || (I.ends && T.last())))
             block = __ldca(L.table + I.r * L.row_stride + T.page);
 
-        scan_wait(C, &C.decays_full[n & 1], (n >> 1) & 1, L.status);
-        const float grow = D.grow, keep = D.keep, unit = kBf16 ? 1.0f : D.unit;
+        scan_wait(C, &C.decays_full[n % kRing], (n / kRing) & 1, L.status);
+        const float grow = D.grow;
         if (kStatesOnly)
             total += D.log[kTile - 1].x + D.log[kTile - 1].y;
-        if (!kBf16 && !kStatesOnly)
-            scan_wait(C, &C.weight_full[n & 1], (n >> 1) & 1, L.status);
+        if (!kBf16) {
+            scan_wait(C, &C.unit_full[n & 1], (n >> 1) & 1, L.status);
+            if (!kStatesOnly)
+                scan_wait(C, &C.lift_full[n & 1], (n >> 1) & 1, L.status);
+        }
+        const float unit = kBf16 ? 1.0f : D.unit;
         scan_wait(C, &C.update_full, n & 1, L.status);
         fence_after();
         if (mine) {
@@ -846,11 +855,9 @@ __device__ __forceinline__ void carry(const ScanPlan &P, ScanControl &C) {
                 load_o(u, lanes + kUpdate + i0 + 16 * c);
                 wait_ld();
 #pragma unroll
-                for (int i = 0; i < 16; i++) {
-                    const float x = kBf16 ? __uint_as_float(u[i]) : __uint_as_float(u[i]) * unit;
-                    float &y = s[16 * c + i];
-                    y = fmaf(keep, y, fmaf(grow, y, x));
-                }
+                for (int i = 0; i < 16; i++)
+                    s[16 * c + i] =
+                        fmaf(grow, s[16 * c + i], kBf16 ? __uint_as_float(u[i]) : __uint_as_float(u[i]) * unit);
             }
         }
         fence_before();
@@ -867,29 +874,52 @@ __device__ __forceinline__ void carry(const ScanPlan &P, ScanControl &C) {
 
         scan_wait(C, &C.out_full, n & 1, L.status);
         fence_after();
-        uint16_t *out = L.out + (T.row + 32 * half) * L.out_row + (int64_t)I.h * L.out_head + j;
-        const int rows = T.rows - 32 * half;
+        const float before = down;
+        if (!T.last())
+            down = hand_over();
+        fence_after();
 #pragma unroll
         for (int c = 0; c < 2; c++) {
             uint32_t a[16], b[16];
-            load_o(a, lanes + kFromState + 32 * half + 16 * c);
+            load_o(a, lanes + kFromState + (n & 1) * 64 + 32 * half + 16 * c);
             load_o(b, lanes + kFromTile + 32 * half + 16 * c);
             wait_ld();
-            if (j < L.dv)
 #pragma unroll
-                for (int i = 0; i < 16; i++) {
-                    const int t = 32 * half + 16 * c + i;
-                    const float x = __uint_as_float(a[i]) * (D.since[t] * from_state);
-                    const float y = kBf16 ? L.scale : L.scale * D.lift[t];
-                    if (16 * c + i < rows)
-                        out[(int64_t)(16 * c + i) * L.out_row] = to_out(fmaf(__uint_as_float(b[i]), y, x), kBf16);
+            for (int i = 0; i < 16; i += 4) {
+                const int t = 32 * half + 16 * c + i;
+                const float4 e = *reinterpret_cast<const float4 *>(&D.since[t]);
+                const float f[4] = {e.x, e.y, e.z, e.w};
+                float g[4] = {L.scale, L.scale, L.scale, L.scale};
+                if constexpr (!kBf16) {
+                    const float4 l = *reinterpret_cast<const float4 *>(&D.lift[t]);
+                    g[0] *= l.x, g[1] *= l.y, g[2] *= l.z, g[3] *= l.w;
                 }
-            __syncwarp();
+#pragma unroll
+                for (int k = 0; k < 4; k++)
+                    *reinterpret_cast<uint16_t *>(staged + (16 * c + i + k) * 64 + 2 * lane) =
+                        to_out(fmaf(__uint_as_float(b[i + k]), g[k], __uint_as_float(a[i + k]) * f[k] * before), kBf16);
+            }
         }
         fence_before();
         __syncwarp();
         if (lane == 0)
             bar_arrive(&C.out_free);
+        const int rows = T.rows - 32 * half;
+        if (P.wide_out) {
+            const int v = 8 * (lane & 3);
+            uint16_t *out = L.out + (T.row + 32 * half + (lane >> 2)) * L.out_row + out_at + v;
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                const uint4 x = *reinterpret_cast<const uint4 *>(staged + i * 512 + 16 * lane);
+                if (8 * i + (lane >> 2) < rows && quarter * 32 + v < L.dv)
+                    __stcs(reinterpret_cast<uint4 *>(out + 8 * i * L.out_row), x);
+            }
+        } else if (j < L.dv) {
+            for (int i = 0; i < rows && i < 32; i++)
+                L.out[(T.row + 32 * half + i) * L.out_row + out_at + lane] =
+                    *reinterpret_cast<const uint16_t *>(staged + i * 64 + 2 * lane);
+        }
+        __syncwarp();
     }
     if (kStatesOnly) {
         write(slot + slot_size);
@@ -928,14 +958,17 @@ __global__ void __launch_bounds__(kScanThreads, 1) lmc_linear_scan_kernel(const 
             bar_init(&C.full[i], 1);
             bar_init(&C.free[i], kStatesOnly ? 1 : 2);
         }
-        for (int i = 0; i < 2; i++) {
+        for (int i = 0; i < kRing; i++)
             bar_init(&C.decays_full[i], 1);
+        for (int i = 0; i < 2; i++) {
+            bar_init(&C.unit_full[i], 1);
+            bar_init(&C.lift_full[i], kWeightWarps);
             bar_init(&C.score_full[i], 1);
             bar_init(&C.score_free[i], kWeightWarps);
-            bar_init(&C.weight_full[i], kWeightWarps);
-            bar_init(&C.weight_free[i], 1);
             bar_init(&C.ended[i], 1);
         }
+        bar_init(&C.weight_full, kWeightWarps);
+        bar_init(&C.weight_free, 1);
         bar_init(&C.keys_full, kWeightWarps);
         bar_init(&C.keys_free, 1);
         bar_init(&C.update_full, 1);
@@ -948,8 +981,8 @@ __global__ void __launch_bounds__(kScanThreads, 1) lmc_linear_scan_kernel(const 
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     // weights of tokens behind a row's own are never written: 0
-    for (int i = threadIdx.x; i < 2 * kPanel / 16; i += kScanThreads)
-        reinterpret_cast<uint4 *>(scan_mem + kStages * kStageBytes + kParts * 2 * kPanel)[i] = make_uint4(0, 0, 0, 0);
+    for (int i = threadIdx.x; i < kPanel / 16; i += kScanThreads)
+        reinterpret_cast<uint4 *>(scan_mem + kWeightsAt)[i] = make_uint4(0, 0, 0, 0);
     fence_async();
     wait_for_launch();
     if (warp == 0)
@@ -969,7 +1002,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) lmc_linear_scan_kernel(const 
     let_next_start();
 
     if (warp < kStateWarps)
-        carry<kBf16, kStatesOnly>(P, C);
+        carry<kBf16, kStatesOnly>(P, C, scan_mem);
     else if (warp < kLoadWarp)
         weigh<kBf16, kStatesOnly>(P, C, scan_mem);
     else if (warp == kLoadWarp)
@@ -1228,6 +1261,8 @@ extern "C" int lmc_linear_scan(const lmc_layout *L, const lmc_linear *a, const i
     P.k_panels = (P.L.dk + 63) / 64;
     P.v_panels = (P.L.dv + 63) / 64;
     const bool bf16 = P.L.bf16, whole_k = P.L.dk % 64 == 0, whole_v = P.L.dv % 64 == 0;
+    P.wide_out = ((uintptr_t)a->out & 15) == 0 && (num_rows == 1 || a->out_row_stride % 8 == 0) &&
+                 (a->num_heads == 1 || a->out_head_stride % 8 == 0);
     P.k_copies = whole_k ? 1 : P.k_panels;
     P.v_copies = whole_v ? 1 : P.v_panels;
     const int64_t H = a->num_heads, K = a->num_key_heads;
