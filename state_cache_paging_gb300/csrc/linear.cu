@@ -282,9 +282,9 @@ struct Tiles {
     __device__ __forceinline__ bool last() const { return done + rows == total; }
 };
 
-__device__ __forceinline__ void scan_wait(ScanControl &C, uint64_t *bar, uint32_t parity, uint32_t *status) {
-    if (bar_try(bar, parity))
-        return;
+// (Not inlined: the loops of all roles together have to stay in the SM's
+// instruction cache.)
+__device__ __noinline__ void scan_wait_on(ScanControl &C, uint64_t *bar, uint32_t parity, uint32_t *status) {
     for (uint32_t i = 0; i < kWaitLimit; i++) {
         if (bar_try(bar, parity))
             return;
@@ -294,6 +294,11 @@ __device__ __forceinline__ void scan_wait(ScanControl &C, uint64_t *bar, uint32_
     // the CTA gives up as a whole: no later wait waits, every role runs to its end
     *(volatile uint32_t *)&C.gave_up = 1;
     atomicOr(status, LMC_ST_TIMEOUT);
+}
+
+__device__ __forceinline__ void scan_wait(ScanControl &C, uint64_t *bar, uint32_t parity, uint32_t *status) {
+    if (!bar_try(bar, parity))
+        scan_wait_on(C, bar, parity, status);
 }
 
 __device__ __forceinline__ bool scan_gone(ScanControl &C) {
@@ -399,6 +404,7 @@ __device__ __forceinline__ void sum_decays(Decays &D, float g0, float g1, int ro
     };
     const long long a = whole(g0), b = whole(g1);
     long long sum = a + b;
+#pragma unroll 1
     for (int o = 1; o < 32; o <<= 1) {
         const long long x = __shfl_up_sync(0xffffffffu, sum, o);
         if (lane >= o)
@@ -411,18 +417,29 @@ __device__ __forceinline__ void sum_decays(Decays &D, float g0, float g1, int ro
         const long long g = i ? sum : sum - b;
         const float high = (float)g, low = (float)(g - (long long)high);
         D.log[t] = t < first_bad ? make_float2(high * 0x1p-40f, low * 0x1p-40f) : make_float2(nan, nan);
-        D.since[t] = t < first_bad ? exp2f(high * 0x1p-40f) : nan;
-        D.left[t] = t < rows ? exp2f((float)(total - g) * 0x1p-40f) : 0.0f;
+        D.since[t] = t < first_bad ? exp2_fast(high * 0x1p-40f) : nan;
+        D.left[t] = t < rows ? exp2_fast((float)(total - g) * 0x1p-40f) : 0.0f;
     }
     const float x = (float)total * 0x1p-40f;
     float grow;
     if (x > -0.7f && x < 0.7f) {
-        const float less = expm1f(x * 0.693147180559945309417f), high = 1.0f + less;
+        // exp(y) - 1 by its series: |y| < 0.486, what is left out is below 2^-29 of y
+        const float y = x * 0.693147180559945309417f;
+        float less = 1.0f / 362880.0f;
+        less = fmaf(less, y, 1.0f / 40320.0f);
+        less = fmaf(less, y, 1.0f / 5040.0f);
+        less = fmaf(less, y, 1.0f / 720.0f);
+        less = fmaf(less, y, 1.0f / 120.0f);
+        less = fmaf(less, y, 1.0f / 24.0f);
+        less = fmaf(less, y, 1.0f / 6.0f);
+        less = fmaf(less, y, 0.5f);
+        less = fmaf(less * y, y, y);
+        const float high = 1.0f + less;
         const float low = fmaf(high, drift, less - (high - 1.0f));
         grow = high + low;
         drift = ((high - grow) + low) / grow;
     } else {
-        grow = exp2f(x);
+        grow = exp2_fast(x);
         drift = 0.0f;
     }
     if (lane == 0)
@@ -456,12 +473,15 @@ __device__ __forceinline__ void load_tiles(const ScanPlan &P, ScanControl &C, ui
         if (elect()) {
             uint64_t *bar = &C.full[st];
             bar_expect(bar, bytes);
+#pragma unroll 1
             for (int i = 0; i < P.k_copies; i++)
                 tma_box(&P.k, to + 2 * kPanel + i * kPanel, i * 64, row, kh, bar);
+#pragma unroll 1
             for (int i = 0; i < P.v_copies; i++)
                 tma_box(&P.v, to + 4 * kPanel + i * kPanel, i * 64, row, h, bar);
             if (!kStatesOnly)
-                for (int i = 0; i < P.k_copies; i++)
+    #pragma unroll 1
+            for (int i = 0; i < P.k_copies; i++)
                     tma_box(&P.q, to + i * kPanel, i * 64, row, kh, bar);
         }
         __syncwarp();
@@ -497,6 +517,7 @@ __device__ __forceinline__ void multiply_forward(const ScanPlan &P, ScanControl 
             fence_after();
             if (elect()) {
                 const uint64_t q = matrix(at, 16, 1024), k = matrix(at + 2 * kPanel, 16, 1024);
+#pragma unroll 1
                 for (int s = 0; s < steps; s++)
                     mma(d, q + (s >> 2) * (kPanel >> 4) + (s & 3) * 2,
                         k + (s >> 2) * (kPanel >> 4) + (s & 3) * 2, scores, s > 0);
@@ -512,7 +533,7 @@ __device__ __forceinline__ void multiply_forward(const ScanPlan &P, ScanControl 
         if (elect()) {
             const uint64_t v = matrix(at + 4 * kPanel, kPanel, 1024);
             // the small parts first
-#pragma unroll
+#pragma unroll 1
             for (int part = (kBf16 ? 3 : 2) - 1; part >= 0; part--)
 #pragma unroll
                 for (int s = 0; s < kTile / 16; s++)
@@ -547,6 +568,7 @@ __device__ __forceinline__ void multiply_state(const ScanPlan &P, ScanControl &C
         fence_after();
         if (elect()) {
             const uint64_t q = matrix(at, 16, 1024);
+#pragma unroll 1
             for (int s = 0; s < steps; s++)
                 mma_held(d, tmem + kState + 8 * s, q + (s >> 2) * (kPanel >> 4) + (s & 3) * 2, from_state, s > 0);
         }
@@ -590,7 +612,7 @@ __device__ __forceinline__ void weigh(const ScanPlan &P, ScanControl &C, uint8_t
         const uint8_t *const keys = mem + st * kStageBytes + 2 * kPanel;
         if constexpr (kBf16) {
             // three truncated parts hold all 24 bits
-#pragma unroll 2
+#pragma unroll 1
             for (int c = tid; c < P.k_panels * (kPanel / 16); c += kWeightWarps * 32) {
                 const int row = c >> 3 & (kTile - 1);
                 uint32_t o[3][4] = {};
@@ -636,7 +658,7 @@ __device__ __forceinline__ void weigh(const ScanPlan &P, ScanControl &C, uint8_t
                 D.unit = power(-e);
                 bar_arrive(&C.unit_full[n & 1]);
             }
-#pragma unroll 2
+#pragma unroll 1
             for (int c = tid; c < P.k_panels * (kPanel / 16); c += kWeightWarps * 32) {
                 const int row = c >> 3 & (kTile - 1);
                 uint32_t o[2][4] = {};
@@ -660,6 +682,7 @@ __device__ __forceinline__ void weigh(const ScanPlan &P, ScanControl &C, uint8_t
         // with weights of 0, which infinities and NaN would not bear
         if (T.rows < kTile) {
             uint8_t *const values = mem + st * kStageBytes + 4 * kPanel;
+#pragma unroll 1
             for (int c = tid; c < P.v_panels * (kPanel / 16); c += kWeightWarps * 32)
                 if ((c >> 3 & (kTile - 1)) >= T.rows)
                     *reinterpret_cast<uint4 *>(values + c * 16) = make_uint4(0, 0, 0, 0);
@@ -761,18 +784,26 @@ __device__ __forceinline__ void carry(const ScanPlan &P, ScanControl &C, uint8_t
     for (int i = 0; i < 64; i++)
         s[i] = 0.0f;
     auto read = [&](const float *from) {
-        if (j < L.dv)
+        if (j < L.dv) {
+            from += at;
 #pragma unroll
-            for (int i = 0; i < 64; i++)
-                if (i0 + i < L.dk)
-                    s[i] = __ldcs(from + at + (int64_t)i * L.dv);
+            for (int g = 0; g < 64; g += 8)
+                if (i0 + g < L.dk)
+#pragma unroll
+                    for (int i = g; i < g + 8; i++, from += L.dv)
+                        s[i] = __ldcs(from);
+        }
     };
     auto write = [&](float *to) {
-        if (j < L.dv)
+        if (j < L.dv) {
+            to += at;
 #pragma unroll
-            for (int i = 0; i < 64; i++)
-                if (i0 + i < L.dk)
-                    __stcs(to + at + (int64_t)i * L.dv, s[i]);
+            for (int g = 0; g < 64; g += 8)
+                if (i0 + g < L.dk)
+#pragma unroll
+                    for (int i = g; i < g + 8; i++, to += L.dv)
+                        __stcs(to, s[i]);
+        }
     };
     // The state as A of its product with q, in 16 bits; what is to be multiplied
     // to its row's results (f16, which has not binary32's range: rows are brought
@@ -810,17 +841,14 @@ __device__ __forceinline__ void carry(const ScanPlan &P, ScanControl &C, uint8_t
     };
     // where a state is at hand before the item's tokens
     float *const slot = P.slots + (int64_t)I.slot * slot_size + head;
-    if (kStatesOnly) {
-        if (I.row == __ldca(L.starts + I.r)) {  // the request's first segment
-            if (I.first >= 0)
-                read(L.pages + I.first * L.page_stride + head);
-            write(slot);
-        }
-    } else if (I.slot >= 0) {
-        read(slot);
-    } else if (I.first >= 0) {
-        read(L.pages + I.first * L.page_stride + head);
-    }
+    const bool first = kStatesOnly && I.row == __ldca(L.starts + I.r);  // the request's first segment
+    const float *const from = !kStatesOnly && I.slot >= 0                     ? slot
+                              : I.first >= 0 && (!kStatesOnly || first) ? L.pages + I.first * L.page_stride + head
+                                                                        : nullptr;
+    if (from != nullptr)
+        read(from);
+    if (first)
+        write(slot);
     float total = 0.0f;  // log2 of the decay over the item
     float down = 1.0f;
     if (!kStatesOnly && I.count > 0)
@@ -878,7 +906,7 @@ __device__ __forceinline__ void carry(const ScanPlan &P, ScanControl &C, uint8_t
         if (!T.last())
             down = hand_over();
         fence_after();
-#pragma unroll
+#pragma unroll 1
         for (int c = 0; c < 2; c++) {
             uint32_t a[16], b[16];
             load_o(a, lanes + kFromState + (n & 1) * 64 + 32 * half + 16 * c);
@@ -915,6 +943,7 @@ __device__ __forceinline__ void carry(const ScanPlan &P, ScanControl &C, uint8_t
                     __stcs(reinterpret_cast<uint4 *>(out + 8 * i * L.out_row), x);
             }
         } else if (j < L.dv) {
+#pragma unroll 1
             for (int i = 0; i < rows && i < 32; i++)
                 L.out[(T.row + 32 * half + i) * L.out_row + out_at + lane] =
                     *reinterpret_cast<const uint16_t *>(staged + i * 64 + 2 * lane);
