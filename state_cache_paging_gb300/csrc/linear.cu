@@ -181,20 +181,20 @@ __global__ void __launch_bounds__(kStepThreads) lmc_linear_step_kernel(const __g
 
 constexpr int kTile = 64;             // tokens of a tile, all of one block of a request
 constexpr int kPanel = kTile * 128;   // bytes of 64 values of a tile's rows
-constexpr int kStages = 3;
+constexpr int kStages = 4;
 constexpr int kStageBytes = 6 * kPanel;  // q, k, v, two panels each
-constexpr int kParts = 3;                // of k times its decay: bf16; f16 takes two
 constexpr int kStateWarps = 8;
 constexpr int kFirstWeightWarp = 8, kWeightWarps = 4;
 constexpr int kLoadWarp = 12, kForwardWarp = 13, kStateProductWarp = 14;
 constexpr int kScanThreads = 15 * 32;
-// shared memory behind the stages: k's parts, the weights, the result on its way
-constexpr int kKeysAt = kStages * kStageBytes, kWeightsAt = kKeysAt + kParts * 2 * kPanel, kResultAt = kWeightsAt + kPanel;
+// shared memory behind the stages: the weights, the result on its way
+constexpr int kWeightsAt = kStages * kStageBytes, kResultAt = kWeightsAt + kPanel;
 constexpr int kWarpResult = 32 * 64;  // bytes of a warp's part of a result: 32 tokens, 32 values
 constexpr int kScanMemory = kResultAt + kStateWarps * kWarpResult;
 constexpr uint32_t kWaitLimit = 1u << 22;
 // columns of tensor memory
-constexpr uint32_t kScores = 0, kUpdate = 128, kFromState = 256, kFromTile = 384, kState = 448;
+constexpr uint32_t kScores = 0, kUpdate = 64, kFromState = 192, kFromTile = 256, kState = 320, kParts = 384;
+constexpr uint32_t kPartColumns = kTile / 2;
 constexpr int kRing = 4;              // tiles whose decays are at hand
 constexpr int kSms = 152;
 constexpr int64_t kLeastSegment = 512;  // tokens
@@ -224,23 +224,22 @@ struct Item {
 
 // What a tile's tokens' decays give.
 struct alignas(16) Decays {
-    float2 log[kTile];   // sum up to and with the token, in units of log 2 (high, low)
-    float left[kTile];   // from the token to the tile's end
-    float since[kTile];  // from the tile's start up to the token
-    float lift[kTile];   // f16: what the token's weights were divided by
-    float grow;          // decay over the tile
-    float unit;          // f16: what k times its decay was divided by
+    float2 log[kTile];      // sum up to and with the token, in units of log 2 (high, low)
+    uint4 left[kTile / 2];  // from the token to the tile's end, two tokens: as three bf16 parts, or (f16) as it is
+    float since[kTile];     // from the tile's start up to the token, times the call's scale
+    float lift[kTile];      // f16: what the token's weights were divided by, times the scale
+    float unit[kMaxDim];    // f16: what a value's row of v times its decay was divided by
+    float grow;             // decay over the tile
 };
-
 static_assert(sizeof(Decays) % 16 == 0, "two tokens' logs are read at once");
 
 struct ScanControl {
     uint64_t full[kStages], free[kStages];
     uint64_t decays_full[kRing];
     uint64_t unit_full[2], lift_full[2];  // f16
-    uint64_t score_full[2], score_free[2];
+    uint64_t score_full, score_free;
     uint64_t weight_full, weight_free;
-    uint64_t keys_full, keys_free;
+    uint64_t parts_full, parts_free;
     uint64_t update_full, update_free;
     uint64_t state_full, out_full, out_free;
     uint64_t ended[2];
@@ -249,7 +248,6 @@ struct ScanControl {
     uint32_t tiles;      // that were asked for
     Item item;
     Decays decays[kRing];
-    float top[kWeightWarps];     // f16: largest of k times its decay
     float row_top[2][kMaxDim];   // f16: largest of the state's rows, by halves
 };
 
@@ -317,11 +315,43 @@ __device__ __forceinline__ void mma_held(uint32_t d, uint32_t a, uint64_t b, uin
 
 __device__ __forceinline__ void weights_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
 
-// The upper halves of two words: a's below b's.
-__device__ __forceinline__ uint32_t upper(float a, float b) {
-    return __byte_perm(__float_as_uint(a), __float_as_uint(b), 0x7632);
+// Four 8 x 8 matrices of 16 bits, turned: a lane gives one of their rows'
+// addresses and gets row l / 4, columns 2 (l % 4) and the next, of each column by
+// column.
+__device__ __forceinline__ void load_turned(uint32_t (&v)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
+                 : "r"(addr)
+                 : "memory");
 }
-__device__ __forceinline__ float truncated(float x) { return __uint_as_float(__float_as_uint(x) & 0xffff0000u); }
+__device__ __forceinline__ void store_turned(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    asm volatile("stmatrix.sync.aligned.m8n8.x4.trans.shared.b16 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(a), "r"(b),
+                 "r"(c), "r"(d)
+                 : "memory");
+}
+// 16 lanes x 8 columns of tensor memory: lane l of the warp holds rows l / 4
+// (v[0], v[2]) and l / 4 + 8 (v[1], v[3]), columns l % 4 and l % 4 + 4.
+__device__ __forceinline__ void store_part(uint32_t addr, const uint32_t (&v)[4]) {
+    asm volatile("tcgen05.st.sync.aligned.16x128b.x2.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v[0]), "r"(v[1]),
+                 "r"(v[2]), "r"(v[3])
+                 : "memory");
+}
+
+__device__ __forceinline__ uint32_t times(uint32_t a, uint32_t b) {
+    uint32_t r;
+    asm("mul.rn.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+__device__ __forceinline__ uint32_t plus_product(uint32_t a, uint32_t b, uint32_t c) {
+    uint32_t r;
+    asm("fma.rn.bf16x2 %0, %1, %2, %3;" : "=r"(r) : "r"(a), "r"(b), "r"(c));
+    return r;
+}
+__device__ __forceinline__ uint32_t minus(uint32_t a) {
+    uint32_t r;
+    asm("neg.bf16x2 %0, %1;" : "=r"(r) : "r"(a));
+    return r;
+}
 
 // 2^e for e in [-126, 127], and the e that brings x into [2^14, 2^15).
 __device__ __forceinline__ float power(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
@@ -394,7 +424,8 @@ __device__ __forceinline__ void find_item(const ScanPlan &P, Item &I) {
 // `drift`: how much the tiles' rounded decays lack of the exact ones so far,
 // relatively; a tile's makes up for it, so that a state that decays slowly by
 // the same factor tile after tile keeps its digits.
-__device__ __forceinline__ void sum_decays(Decays &D, float g0, float g1, int rows, float &drift) {
+template <bool kBf16>
+__device__ __forceinline__ void sum_decays(Decays &D, float g0, float g1, int rows, float scale, float &drift) {
     const int lane = threadIdx.x & 31;
     const float nan = __int_as_float(0x7fffffff);
     const uint32_t bad0 = __ballot_sync(0xffffffffu, g0 != g0), bad1 = __ballot_sync(0xffffffffu, g1 != g1);
@@ -417,8 +448,17 @@ __device__ __forceinline__ void sum_decays(Decays &D, float g0, float g1, int ro
         const long long g = i ? sum : sum - b;
         const float high = (float)g, low = (float)(g - (long long)high);
         D.log[t] = t < first_bad ? make_float2(high * 0x1p-40f, low * 0x1p-40f) : make_float2(nan, nan);
-        D.since[t] = t < first_bad ? exp2_fast(high * 0x1p-40f) : nan;
-        D.left[t] = t < rows ? exp2_fast((float)(total - g) * 0x1p-40f) : 0.0f;
+        D.since[t] = t < first_bad ? exp2_fast(high * 0x1p-40f) * scale : nan;
+    }
+    const float f0 = 2 * lane < rows ? exp2_fast((float)(total - (sum - b)) * 0x1p-40f) : 0.0f;
+    const float f1 = 2 * lane + 1 < rows ? exp2_fast((float)(total - sum) * 0x1p-40f) : 0.0f;
+    if constexpr (kBf16) {
+        const uint32_t p = pack<true>(f0, f1);
+        const float r0 = f0 - from_q(p & 0xffff, true), r1 = f1 - from_q(p >> 16, true);
+        const uint32_t q = pack<true>(r0, r1);
+        D.left[lane] = make_uint4(p, q, pack<true>(r0 - from_q(q & 0xffff, true), r1 - from_q(q >> 16, true)), 0);
+    } else {
+        D.left[lane] = make_uint4(__float_as_uint(f0), __float_as_uint(f1), 0, 0);
     }
     const float x = (float)total * 0x1p-40f;
     float grow;
@@ -448,14 +488,25 @@ __device__ __forceinline__ void sum_decays(Decays &D, float g0, float g1, int ro
 
 // One warp: q, k and v of each tile by TMA, and its decays. (Rows behind a
 // tile's last one come along; they are not read into a result.)
-template <bool kStatesOnly>
+template <bool kBf16, bool kStatesOnly>
 __device__ __forceinline__ void load_tiles(const ScanPlan &P, ScanControl &C, uint8_t *mem) {
     Tiles T(C.item, P.L.block_size);
     const int lane = threadIdx.x & 31, h = C.item.h, kh = h / P.L.shared;
     const uint32_t bytes = (uint32_t)((kStatesOnly ? 1 : 2) * P.k_panels + P.v_panels) * kPanel;
     const float *const decay = P.L.decay + (int64_t)h * P.L.decay_head;
     uint32_t asked = 0;
-    float drift = 0.0f;
+    float drift = 0.0f, h0 = 0.0f, h1 = 0.0f;  // the tile before's decays,
+    int rows = 0;                              // and rows
+    // A tile's decays go to its place of the ring when the next tile's copies have
+    // been asked for: the stage that these take was free, so the result of the tile
+    // before that stage's last one has been read, and with it that place.
+    static_assert(kRing >= kStages, "a place is read until the next tile's result is made");
+    auto tell = [&](uint32_t n) {
+        sum_decays<kBf16>(C.decays[n % kRing], h0, h1, rows, P.L.scale, drift);
+        __syncwarp();
+        if (lane == 0)
+            bar_arrive(&C.decays_full[n % kRing]);
+    };
     while (T.next()) {
         const int st = (int)uniform(T.n % kStages);
         float g0 = 0.0f, g1 = 0.0f;
@@ -469,78 +520,81 @@ __device__ __forceinline__ void load_tiles(const ScanPlan &P, ScanControl &C, ui
         if (scan_gone(C))
             break;
         uint8_t *to = mem + st * kStageBytes;
-        const int row = (int)uniform((int)T.row);
+        const int row0 = (int)uniform((int)T.row);
         if (elect()) {
             uint64_t *bar = &C.full[st];
             bar_expect(bar, bytes);
 #pragma unroll 1
             for (int i = 0; i < P.k_copies; i++)
-                tma_box(&P.k, to + 2 * kPanel + i * kPanel, i * 64, row, kh, bar);
+                tma_box(&P.k, to + 2 * kPanel + i * kPanel, i * 64, row0, kh, bar);
 #pragma unroll 1
             for (int i = 0; i < P.v_copies; i++)
-                tma_box(&P.v, to + 4 * kPanel + i * kPanel, i * 64, row, h, bar);
+                tma_box(&P.v, to + 4 * kPanel + i * kPanel, i * 64, row0, h, bar);
             if (!kStatesOnly)
     #pragma unroll 1
             for (int i = 0; i < P.k_copies; i++)
-                    tma_box(&P.q, to + i * kPanel, i * 64, row, kh, bar);
+                    tma_box(&P.q, to + i * kPanel, i * 64, row0, kh, bar);
         }
         __syncwarp();
+        if (asked > 0)
+            tell(asked - 1);
         asked++;
-        sum_decays(C.decays[T.n % kRing], g0, g1, T.rows, drift);
-        __syncwarp();
-        if (lane == 0)
-            bar_arrive(&C.decays_full[T.n % kRing]);
+        h0 = g0;
+        h1 = g1;
+        rows = T.rows;
     }
+    if (asked > 0)
+        tell(asked - 1);
     if (lane == 0)
         C.tiles = asked;
 }
 
 // One warp: the products that need no state. Scores Q K^T [tokens x tokens], and
-// what the tile adds to the state, turned: V^T (K decayed) [values x keys].
+// what the tile adds to the state, turned: (V decayed)^T K [values x keys].
 template <bool kBf16, bool kStatesOnly>
 __device__ __forceinline__ void multiply_forward(const ScanPlan &P, ScanControl &C, uint8_t *mem) {
     Tiles T(C.item, P.L.block_size);
     const uint32_t tmem = uniform(C.tmem);
     const int keys = 64 * P.k_panels, steps = (P.L.dk + 15) / 16;
     const uint32_t scores = instruction(kBf16, false, 64, kTile);
-    const uint32_t update = instruction(kBf16, true, 128, keys) | 1u << 16;  // B turned, too
-    const uint64_t part0 = matrix(smem_addr(mem) + kKeysAt, kPanel, 1024);
+    const uint32_t update = instruction(kBf16, false, 128, keys) | 1u << 16;  // B turned
     while (T.next()) {
         const uint32_t n = T.n;
         const int st = (int)uniform(n % kStages);
-        const uint32_t at = smem_addr(mem) + st * kStageBytes, d = tmem + kScores + uniform(n & 1) * 64;
+        const uint32_t at = smem_addr(mem) + st * kStageBytes;
         scan_wait(C, &C.full[st], (n / kStages) & 1, P.L.status);
         if (!kStatesOnly) {
-            if (n >= 2)
-                scan_wait(C, &C.score_free[n & 1], (n / 2 - 1) & 1, P.L.status);
+            if (n >= 1)
+                scan_wait(C, &C.score_free, (n - 1) & 1, P.L.status);
             __syncwarp();
             fence_after();
             if (elect()) {
                 const uint64_t q = matrix(at, 16, 1024), k = matrix(at + 2 * kPanel, 16, 1024);
 #pragma unroll 1
                 for (int s = 0; s < steps; s++)
-                    mma(d, q + (s >> 2) * (kPanel >> 4) + (s & 3) * 2,
-                        k + (s >> 2) * (kPanel >> 4) + (s & 3) * 2, scores, s > 0);
-                commit(&C.score_full[n & 1]);
+                    mma(tmem + kScores, q + (s >> 2) * (kPanel >> 4) + (s & 3) * 2, k + (s >> 2) * (kPanel >> 4) + (s & 3) * 2,
+                        scores, s > 0);
+                commit(&C.score_full);
             }
             __syncwarp();
         }
-        scan_wait(C, &C.keys_full, n & 1, P.L.status);
+        scan_wait(C, &C.parts_full, n & 1, P.L.status);
         if (n >= 1)
             scan_wait(C, &C.update_free, (n - 1) & 1, P.L.status);
         __syncwarp();
         fence_after();
         if (elect()) {
-            const uint64_t v = matrix(at + 4 * kPanel, kPanel, 1024);
+            const uint64_t k = matrix(at + 2 * kPanel, kPanel, 1024);
             // the small parts first
+            constexpr int kLast = (kBf16 ? 4 : 2) - 1;
 #pragma unroll 1
-            for (int part = (kBf16 ? 3 : 2) - 1; part >= 0; part--)
+            for (int part = kLast; part >= 0; part--)
 #pragma unroll
                 for (int s = 0; s < kTile / 16; s++)
-                    mma(tmem + kUpdate, v + s * (2048 >> 4), part0 + part * (2 * kPanel >> 4) + s * (2048 >> 4), update,
-                        part < (kBf16 ? 2 : 1) || s > 0);
+                    mma_held(tmem + kUpdate, tmem + kParts + part * kPartColumns + 8 * s, k + s * (2048 >> 4), update,
+                             part < kLast || s > 0);
             commit(&C.update_full);
-            commit(&C.keys_free);
+            commit(&C.parts_free);
             commit(&C.free[st]);
         }
         __syncwarp();
@@ -548,9 +602,7 @@ __device__ __forceinline__ void multiply_forward(const ScanPlan &P, ScanControl 
 }
 
 // One warp: the products that make the result, turned: S^T Q^T from the state
-// before the tile, V^T P^T from the tile's own tokens [values x tokens]. The
-// first goes to turns of tensor memory, so that it does not wait for the tile
-// before to be read.
+// before the tile, V^T P^T from the tile's own tokens [values x tokens].
 template <bool kBf16>
 __device__ __forceinline__ void multiply_state(const ScanPlan &P, ScanControl &C, uint8_t *mem) {
     Tiles T(C.item, P.L.block_size);
@@ -561,21 +613,21 @@ __device__ __forceinline__ void multiply_state(const ScanPlan &P, ScanControl &C
     while (T.next()) {
         const uint32_t n = T.n;
         const int st = (int)uniform(n % kStages);
-        const uint32_t at = smem_addr(mem) + st * kStageBytes, d = tmem + kFromState + uniform(n & 1) * 64;
+        const uint32_t at = smem_addr(mem) + st * kStageBytes;
         scan_wait(C, &C.full[st], (n / kStages) & 1, P.L.status);
         scan_wait(C, &C.state_full, n & 1, P.L.status);
+        if (n >= 1)
+            scan_wait(C, &C.out_free, (n - 1) & 1, P.L.status);
         __syncwarp();
         fence_after();
         if (elect()) {
             const uint64_t q = matrix(at, 16, 1024);
 #pragma unroll 1
             for (int s = 0; s < steps; s++)
-                mma_held(d, tmem + kState + 8 * s, q + (s >> 2) * (kPanel >> 4) + (s & 3) * 2, from_state, s > 0);
+                mma_held(tmem + kFromState, tmem + kState + 8 * s, q + (s >> 2) * (kPanel >> 4) + (s & 3) * 2, from_state, s > 0);
         }
         __syncwarp();
         scan_wait(C, &C.weight_full, n & 1, P.L.status);
-        if (n >= 1)
-            scan_wait(C, &C.out_free, (n - 1) & 1, P.L.status);
         __syncwarp();
         fence_after();
         if (elect()) {
@@ -591,120 +643,133 @@ __device__ __forceinline__ void multiply_state(const ScanPlan &P, ScanControl &C
     }
 }
 
-// Four warps: k times the decay to the tile's end, in parts of 16 bits, and the
-// weights P = (Q K^T) * decays, of tokens up to the row's own.
+// Four warps: v times the decay to the tile's end, turned, in parts of 16 bits,
+// to tensor memory (warp w: values 32 w .. 32 w + 31), and the weights
+// P = (Q K^T) * decays, of tokens up to the row's own (rows 16 w .. 16 w + 15).
+//
+// What is added to the state keeps binary32's digits: with f = f1 + f2 + f3 in
+// bf16, v f = A + B + C + D where A = rn(v f1), B = v f1 - A (exact: a product of
+// two numbers of 8 bits has 16), C = rn(v f2) and D = rn(v f3 + (v f2 - C)), each
+// a bf16: off by 2^-26. In pairs of bf16 that is five instructions for two values
+// (three truncated parts of a binary32 product are fifteen).
 template <bool kBf16, bool kStatesOnly>
 __device__ __forceinline__ void weigh(const ScanPlan &P, ScanControl &C, uint8_t *mem) {
     Tiles T(C.item, P.L.block_size);
     const int lane = threadIdx.x & 31, quarter = (threadIdx.x >> 5) - kFirstWeightWarp, tid = threadIdx.x - kFirstWeightWarp * 32;
     const uint32_t lanes = C.tmem + ((uint32_t)(quarter * 32) << 16);
     const int ra = quarter * 16 + lane / 4, rb = ra + 8;  // this thread's rows of P
-    uint8_t *const parts = mem + kKeysAt;
     uint8_t *const pa = mem + kWeightsAt + ra * 128 + 4 * (lane & 3), *const pb = pa + 8 * 128;
+    // the row of four 8 x 8 matrices that this lane names: tokens 8 (lane / 16) +
+    // lane % 8 of a step's, values 8 (lane / 8 % 2) .. of 16
+    const uint32_t values = smem_addr(mem) + 4 * kPanel + (quarter >> 1) * kPanel + (8 * (lane >> 4) + (lane & 7)) * 128;
+    const int chunk = 4 * (quarter & 1) + (lane >> 3 & 1);
     while (T.next()) {
         const uint32_t n = T.n;
         const int st = n % kStages;
         Decays &D = C.decays[n % kRing];
         scan_wait(C, &C.decays_full[n % kRing], (n / kRing) & 1, P.L.status);
         scan_wait(C, &C.full[st], (n / kStages) & 1, P.L.status);
-        if (n >= 1)
-            scan_wait(C, &C.keys_free, (n - 1) & 1, P.L.status);
-        const uint8_t *const keys = mem + st * kStageBytes + 2 * kPanel;
-        if constexpr (kBf16) {
-            // three truncated parts hold all 24 bits
-#pragma unroll 1
-            for (int c = tid; c < P.k_panels * (kPanel / 16); c += kWeightWarps * 32) {
-                const int row = c >> 3 & (kTile - 1);
-                uint32_t o[3][4] = {};
-                if (row < T.rows) {
-                    const uint4 k = *reinterpret_cast<const uint4 *>(keys + c * 16);
-                    const uint32_t w[4] = {k.x, k.y, k.z, k.w};
-                    const float f = D.left[row];
-#pragma unroll
-                    for (int i = 0; i < 4; i++) {
-                        const float x = __uint_as_float(w[i] << 16) * f, y = __uint_as_float(w[i] & 0xffff0000u) * f;
-                        const float x1 = x - truncated(x), y1 = y - truncated(y);
-                        o[0][i] = upper(x, y);
-                        o[1][i] = upper(x1, y1);
-                        o[2][i] = upper(x1 - truncated(x1), y1 - truncated(y1));
-                    }
-                }
-#pragma unroll
-                for (int p = 0; p < 3; p++)
-                    *reinterpret_cast<uint4 *>(parts + p * 2 * kPanel + c * 16) = make_uint4(o[p][0], o[p][1], o[p][2], o[p][3]);
-            }
-        } else {
-            // two rounded parts of the values brought below 2^15 by a power of two
-            float top = 0.0f;
-            for (int c = tid; c < P.k_panels * (kPanel / 16); c += kWeightWarps * 32) {
-                const int row = c >> 3 & (kTile - 1);
-                if (row < T.rows) {
-                    const uint4 k = *reinterpret_cast<const uint4 *>(keys + c * 16);
-                    const uint32_t w[4] = {k.x, k.y, k.z, k.w};
-                    const float f = D.left[row];
-#pragma unroll
-                    for (int i = 0; i < 4; i++)
-                        top = fmaxf(top, fmaxf(fabsf(from_q(w[i] & 0xffff, false)), fabsf(from_q(w[i] >> 16, false))) * f);
-                }
-            }
-            top = __uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(top)));
-            if (lane == 0)
-                C.top[quarter] = top;
-            weights_sync();
-            top = fmaxf(fmaxf(C.top[0], C.top[1]), fmaxf(C.top[2], C.top[3]));
-            const int e = lift_of(top);
-            const float up = power(e);
-            if (tid == 0) {
-                D.unit = power(-e);
-                bar_arrive(&C.unit_full[n & 1]);
-            }
-#pragma unroll 1
-            for (int c = tid; c < P.k_panels * (kPanel / 16); c += kWeightWarps * 32) {
-                const int row = c >> 3 & (kTile - 1);
-                uint32_t o[2][4] = {};
-                if (row < T.rows) {
-                    const uint4 k = *reinterpret_cast<const uint4 *>(keys + c * 16);
-                    const uint32_t w[4] = {k.x, k.y, k.z, k.w};
-                    const float f = D.left[row];
-#pragma unroll
-                    for (int i = 0; i < 4; i++) {
-                        const float x = from_q(w[i] & 0xffff, false) * f * up, y = from_q(w[i] >> 16, false) * f * up;
-                        o[0][i] = pack<false>(x, y);
-                        o[1][i] = pack<false>(x - from_q(o[0][i] & 0xffff, false), y - from_q(o[0][i] >> 16, false));
-                    }
-                }
-#pragma unroll
-                for (int p = 0; p < 2; p++)
-                    *reinterpret_cast<uint4 *>(parts + p * 2 * kPanel + c * 16) = make_uint4(o[p][0], o[p][1], o[p][2], o[p][3]);
-            }
-        }
-        // rows behind the tile's last belong to others: as values they take part
-        // with weights of 0, which infinities and NaN would not bear
+        // rows behind the tile's last belong to others: their k and v take part
+        // times 0, which infinities and NaN would not bear
         if (T.rows < kTile) {
-            uint8_t *const values = mem + st * kStageBytes + 4 * kPanel;
+            uint8_t *const rows = mem + st * kStageBytes + 2 * kPanel;
 #pragma unroll 1
-            for (int c = tid; c < P.v_panels * (kPanel / 16); c += kWeightWarps * 32)
+            for (int c = tid; c < 4 * (kPanel / 16); c += kWeightWarps * 32)
                 if ((c >> 3 & (kTile - 1)) >= T.rows)
-                    *reinterpret_cast<uint4 *>(values + c * 16) = make_uint4(0, 0, 0, 0);
+                    *reinterpret_cast<uint4 *>(rows + c * 16) = make_uint4(0, 0, 0, 0);
+            fence_async();
+            weights_sync();
         }
-        fence_async();
+        if (n >= 1)
+            scan_wait(C, &C.parts_free, (n - 1) & 1, P.L.status);
+        fence_after();
+        const uint32_t from = values + st * kStageBytes;
+#pragma unroll 1
+        for (int block = 0; block < 2; block++) {  // of 16 values
+            const uint32_t row = from + (((chunk + 2 * block) ^ (lane & 7)) << 4);
+            const uint32_t to = lanes + ((uint32_t)(16 * block) << 16) + kParts;
+            if constexpr (kBf16) {
+#pragma unroll
+                for (int s = 0; s < kTile / 16; s++) {
+                    uint32_t v[4], part[4][4];
+                    load_turned(v, row + s * 2048);
+                    const uint4 fa = D.left[8 * s + (lane & 3)], fb = D.left[8 * s + 4 + (lane & 3)];
+#pragma unroll
+                    for (int i = 0; i < 4; i++) {
+                        const uint4 f = i < 2 ? fa : fb;
+                        part[0][i] = times(v[i], f.x);
+                        part[1][i] = plus_product(v[i], f.x, minus(part[0][i]));
+                        part[2][i] = times(v[i], f.y);
+                        part[3][i] = plus_product(v[i], f.z, plus_product(v[i], f.y, minus(part[2][i])));
+                    }
+#pragma unroll
+                    for (int p = 0; p < 4; p++)
+                        store_part(to + p * kPartColumns + 8 * s, part[p]);
+                }
+            } else {
+                // two rounded parts of the product, whose row (a value's, of 64
+                // tokens: four lanes) is brought below 2^15 by a power of two
+                uint32_t v[kTile / 16][4];
+                float top[2] = {0.0f, 0.0f};
+#pragma unroll
+                for (int s = 0; s < kTile / 16; s++) {
+                    load_turned(v[s], row + s * 2048);
+#pragma unroll
+                    for (int i = 0; i < 4; i++) {
+                        const uint4 f = D.left[8 * s + (i < 2 ? 0 : 4) + (lane & 3)];
+                        top[i & 1] = fmaxf(top[i & 1], fmaxf(fabsf(from_q(v[s][i] & 0xffff, false)) * __uint_as_float(f.x),
+                                                             fabsf(from_q(v[s][i] >> 16, false)) * __uint_as_float(f.y)));
+                    }
+                }
+                float up[2];
+#pragma unroll
+                for (int k = 0; k < 2; k++) {
+                    top[k] = fmaxf(top[k], __shfl_xor_sync(0xffffffffu, top[k], 1));
+                    top[k] = fmaxf(top[k], __shfl_xor_sync(0xffffffffu, top[k], 2));
+                    const int e = lift_of(top[k]);
+                    up[k] = power(e);
+                    if ((lane & 3) == 0)
+                        D.unit[32 * quarter + 16 * block + 8 * k + lane / 4] = power(-e);
+                }
+#pragma unroll
+                for (int s = 0; s < kTile / 16; s++) {
+                    uint32_t part[2][4];
+#pragma unroll
+                    for (int i = 0; i < 4; i++) {
+                        const uint4 f = D.left[8 * s + (i < 2 ? 0 : 4) + (lane & 3)];
+                        const float x = from_q(v[s][i] & 0xffff, false) * __uint_as_float(f.x) * up[i & 1];
+                        const float y = from_q(v[s][i] >> 16, false) * __uint_as_float(f.y) * up[i & 1];
+                        part[0][i] = pack<false>(x, y);
+                        part[1][i] = pack<false>(x - from_q(part[0][i] & 0xffff, false), y - from_q(part[0][i] >> 16, false));
+                    }
+#pragma unroll
+                    for (int p = 0; p < 2; p++)
+                        store_part(to + p * kPartColumns + 8 * s, part[p]);
+                }
+            }
+        }
+        wait_st();
+        fence_before();
         __syncwarp();
-        if (lane == 0)
-            bar_arrive(&C.keys_full);
+        if (lane == 0) {
+            if (!kBf16)
+                bar_arrive(&C.unit_full[n & 1]);
+            bar_arrive(&C.parts_full);
+        }
         if (kStatesOnly)
             continue;
 
-        scan_wait(C, &C.score_full[n & 1], (n >> 1) & 1, P.L.status);
+        scan_wait(C, &C.score_full, n & 1, P.L.status);
         fence_after();
         uint32_t raw[2][16];
-        load_s(raw[0], lanes + kScores + (n & 1) * 64);
+        load_s(raw[0], lanes + kScores);
         if (quarter >= 2)
-            load_s(raw[1], lanes + kScores + (n & 1) * 64 + 32);
+            load_s(raw[1], lanes + kScores + 32);
         wait_ld();
         fence_before();
         __syncwarp();
         if (lane == 0)
-            bar_arrive(&C.score_free[n & 1]);
+            bar_arrive(&C.score_free);
         const float2 la = D.log[ra], lb = D.log[rb];
         const int x = ra & 7;  // rb & 7 is the same
         float p[8][4];
@@ -742,8 +807,8 @@ __device__ __forceinline__ void weigh(const ScanPlan &P, ScanControl &C, uint8_t
             ua = power(ea);
             ub = power(eb);
             if ((lane & 3) == 0) {
-                D.lift[ra] = power(-ea);
-                D.lift[rb] = power(-eb);
+                D.lift[ra] = power(-ea) * P.L.scale;
+                D.lift[rb] = power(-eb) * P.L.scale;
             }
             __syncwarp();
             if (lane == 0)
@@ -809,7 +874,7 @@ __device__ __forceinline__ void carry(const ScanPlan &P, ScanControl &C, uint8_t
     // to its row's results (f16, which has not binary32's range: rows are brought
     // below 2^15).
     auto hand_over = [&] {
-        float up = 1.0f, down = L.scale;
+        float up = 1.0f, down = 1.0f;
         if constexpr (!kBf16) {
             float top = 0.0f;
 #pragma unroll
@@ -820,7 +885,7 @@ __device__ __forceinline__ void carry(const ScanPlan &P, ScanControl &C, uint8_t
             top = fmaxf(top, C.row_top[half ^ 1][j]);
             const int e = lift_of(top);
             up = power(e);
-            down *= power(-e);
+            down = power(-e);
         }
         if (mine) {
 #pragma unroll
@@ -854,7 +919,7 @@ __device__ __forceinline__ void carry(const ScanPlan &P, ScanControl &C, uint8_t
     if (!kStatesOnly && I.count > 0)
         down = hand_over();
     // a warp's part of a result: rows of 64 bytes, a token each
-    uint8_t *const staged = mem + kResultAt + warp * kWarpResult;
+    const uint32_t staged = smem_addr(mem) + kResultAt + warp * kWarpResult;
     const int64_t out_at = (int64_t)I.h * L.out_head + quarter * 32;
     while (T.next()) {
         const uint32_t n = T.n;
@@ -873,7 +938,7 @@ __device__ __forceinline__ void carry(const ScanPlan &P, ScanControl &C, uint8_t
             if (!kStatesOnly)
                 scan_wait(C, &C.lift_full[n & 1], (n >> 1) & 1, L.status);
         }
-        const float unit = kBf16 ? 1.0f : D.unit;
+        const float unit = kBf16 ? 1.0f : D.unit[j];
         scan_wait(C, &C.update_full, n & 1, L.status);
         fence_after();
         if (mine) {
@@ -902,51 +967,67 @@ __device__ __forceinline__ void carry(const ScanPlan &P, ScanControl &C, uint8_t
 
         scan_wait(C, &C.out_full, n & 1, L.status);
         fence_after();
-        const float before = down;
-        if (!T.last())
-            down = hand_over();
-        fence_after();
 #pragma unroll 1
-        for (int c = 0; c < 2; c++) {
+        for (int b16 = 0; b16 < 2; b16++) {  // 16 values
             uint32_t a[16], b[16];
-            load_o(a, lanes + kFromState + (n & 1) * 64 + 32 * half + 16 * c);
-            load_o(b, lanes + kFromTile + 32 * half + 16 * c);
-            wait_ld();
-#pragma unroll
-            for (int i = 0; i < 16; i += 4) {
-                const int t = 32 * half + 16 * c + i;
-                const float4 e = *reinterpret_cast<const float4 *>(&D.since[t]);
-                const float f[4] = {e.x, e.y, e.z, e.w};
-                float g[4] = {L.scale, L.scale, L.scale, L.scale};
-                if constexpr (!kBf16) {
-                    const float4 l = *reinterpret_cast<const float4 *>(&D.lift[t]);
-                    g[0] *= l.x, g[1] *= l.y, g[2] *= l.z, g[3] *= l.w;
-                }
-#pragma unroll
-                for (int k = 0; k < 4; k++)
-                    *reinterpret_cast<uint16_t *>(staged + (16 * c + i + k) * 64 + 2 * lane) =
-                        to_out(fmaf(__uint_as_float(b[i + k]), g[k], __uint_as_float(a[i + k]) * f[k] * before), kBf16);
+            const uint32_t at16 = lanes + ((uint32_t)(16 * b16) << 16) + 32 * half;
+            load_s(a, at16 + kFromState);
+            load_s(b, at16 + kFromTile);
+            float da = 1.0f, db = 1.0f;
+            if constexpr (!kBf16) {
+                da = __shfl_sync(0xffffffffu, down, 16 * b16 + lane / 4);
+                db = __shfl_sync(0xffffffffu, down, 16 * b16 + lane / 4 + 8);
             }
+            wait_ld();
+            uint32_t y[8];
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                const int t = 32 * half + 8 * i + 2 * (lane & 3);
+                const float2 e = *reinterpret_cast<const float2 *>(&D.since[t]);
+                float2 g = make_float2(L.scale, L.scale);
+                if constexpr (!kBf16)
+                    g = *reinterpret_cast<const float2 *>(&D.lift[t]);
+#pragma unroll
+                for (int k = 0; k < 2; k++) {
+                    float x0 = __uint_as_float(a[4 * i + 2 * k]) * e.x, x1 = __uint_as_float(a[4 * i + 2 * k + 1]) * e.y;
+                    if constexpr (!kBf16) {
+                        x0 *= k ? db : da;
+                        x1 *= k ? db : da;
+                    }
+                    y[2 * i + k] = pack<kBf16>(fmaf(__uint_as_float(b[4 * i + 2 * k]), g.x, x0),
+                                               fmaf(__uint_as_float(b[4 * i + 2 * k + 1]), g.y, x1));
+                }
+            }
+            // a row of 32 values, 64 bytes, per token; 16-byte pieces in turns, so
+            // that no two of eight rows fall into the same banks
+            const int t = 8 * (lane >> 4) + (lane & 7);
+            const uint32_t to = staged + t * 64 + (((2 * b16 + (lane >> 3 & 1)) ^ (t >> 1 & 3)) << 4);
+            store_turned(to, y[0], y[1], y[2], y[3]);
+            store_turned(to + 16 * 64, y[4], y[5], y[6], y[7]);
         }
         fence_before();
         __syncwarp();
         if (lane == 0)
             bar_arrive(&C.out_free);
+        if (!T.last())
+            down = hand_over();
         const int rows = T.rows - 32 * half;
+        const uint8_t *const mine8 = mem + kResultAt + warp * kWarpResult;
         if (P.wide_out) {
             const int v = 8 * (lane & 3);
             uint16_t *out = L.out + (T.row + 32 * half + (lane >> 2)) * L.out_row + out_at + v;
 #pragma unroll
             for (int i = 0; i < 4; i++) {
-                const uint4 x = *reinterpret_cast<const uint4 *>(staged + i * 512 + 16 * lane);
-                if (8 * i + (lane >> 2) < rows && quarter * 32 + v < L.dv)
+                const int t = 8 * i + (lane >> 2);
+                const uint4 x = *reinterpret_cast<const uint4 *>(mine8 + t * 64 + (((lane & 3) ^ (t >> 1 & 3)) << 4));
+                if (t < rows && quarter * 32 + v < L.dv)
                     __stcs(reinterpret_cast<uint4 *>(out + 8 * i * L.out_row), x);
             }
         } else if (j < L.dv) {
 #pragma unroll 1
-            for (int i = 0; i < rows && i < 32; i++)
-                L.out[(T.row + 32 * half + i) * L.out_row + out_at + lane] =
-                    *reinterpret_cast<const uint16_t *>(staged + i * 64 + 2 * lane);
+            for (int t = 0; t < rows && t < 32; t++)
+                L.out[(T.row + 32 * half + t) * L.out_row + out_at + lane] =
+                    *reinterpret_cast<const uint16_t *>(mine8 + t * 64 + (((lane >> 3) ^ (t >> 1 & 3)) << 4) + 2 * (lane & 7));
         }
         __syncwarp();
     }
@@ -990,16 +1071,16 @@ __global__ void __launch_bounds__(kScanThreads, 1) lmc_linear_scan_kernel(const 
         for (int i = 0; i < kRing; i++)
             bar_init(&C.decays_full[i], 1);
         for (int i = 0; i < 2; i++) {
-            bar_init(&C.unit_full[i], 1);
+            bar_init(&C.unit_full[i], kWeightWarps);
             bar_init(&C.lift_full[i], kWeightWarps);
-            bar_init(&C.score_full[i], 1);
-            bar_init(&C.score_free[i], kWeightWarps);
             bar_init(&C.ended[i], 1);
         }
         bar_init(&C.weight_full, kWeightWarps);
         bar_init(&C.weight_free, 1);
-        bar_init(&C.keys_full, kWeightWarps);
-        bar_init(&C.keys_free, 1);
+        bar_init(&C.score_full, 1);
+        bar_init(&C.score_free, kWeightWarps);
+        bar_init(&C.parts_full, kWeightWarps);
+        bar_init(&C.parts_free, 1);
         bar_init(&C.update_full, 1);
         bar_init(&C.update_free, kStateWarps);
         bar_init(&C.state_full, kStateWarps);
@@ -1035,7 +1116,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) lmc_linear_scan_kernel(const 
     else if (warp < kLoadWarp)
         weigh<kBf16, kStatesOnly>(P, C, scan_mem);
     else if (warp == kLoadWarp)
-        load_tiles<kStatesOnly>(P, C, scan_mem);
+        load_tiles<kBf16, kStatesOnly>(P, C, scan_mem);
     else if (warp == kForwardWarp)
         multiply_forward<kBf16, kStatesOnly>(P, C, scan_mem);
     else if (!kStatesOnly)
