@@ -185,13 +185,18 @@ constexpr int kStages = 4;
 constexpr int kStageBytes = 6 * kPanel;  // q, k, v, two panels each
 constexpr int kStateWarps = 8;
 constexpr int kFirstWeightWarp = 8, kWeightWarps = 4;
-constexpr int kLoadWarp = 12, kForwardWarp = 13, kStateProductWarp = 14;
-constexpr int kScanThreads = 15 * 32;
+constexpr int kFirstResultWarp = 12, kResultWarps = 4;
+constexpr int kLoadWarp = 16, kForwardWarp = 17, kStateProductWarp = 18;
+constexpr int kScanThreads = 20 * 32;
+// Registers per thread of the warpgroups: 2 x 128 + 96 + 72 + 56 of the 5 x 96 the
+// CTA starts with.
+constexpr int kStateRegisters = 128, kWeightRegisters = 96, kResultRegisters = 72, kOtherRegisters = 56;
 // shared memory behind the stages: the weights, the result on its way
 constexpr int kWeightsAt = kStages * kStageBytes, kResultAt = kWeightsAt + kPanel;
-constexpr int kWarpResult = 32 * 64;  // bytes of a warp's part of a result: 32 tokens, 32 values
-constexpr int kScanMemory = kResultAt + kStateWarps * kWarpResult;
-constexpr uint32_t kWaitLimit = 1u << 22;
+constexpr int kWarpResult = kTile * 64;  // bytes of a warp's part of a result: 32 values of each token
+constexpr int kScanMemory = kResultAt + kResultWarps * kWarpResult;
+constexpr uint32_t kWaitLimit = 1u << 18;  // looks at a barrier, of up to
+constexpr uint32_t kLook = 4000;           // so many ns each
 // columns of tensor memory
 constexpr uint32_t kScores = 0, kUpdate = 64, kFromState = 192, kFromTile = 256, kState = 320, kParts = 384;
 constexpr uint32_t kPartColumns = kTile / 2;
@@ -211,8 +216,8 @@ struct ScanPlan {
 
 // A CTA's tokens: a segment of a request, one head.
 struct Item {
-    int64_t row;         // first row
-    int64_t page;        // its block position,
+    int32_t row;         // first row
+    int32_t page;        // its block position,
     int32_t phase;       // and the tokens of the block before it
     int32_t count;       // tokens
     int32_t r, h;
@@ -236,26 +241,27 @@ static_assert(sizeof(Decays) % 16 == 0, "two tokens' logs are read at once");
 struct ScanControl {
     uint64_t full[kStages], free[kStages];
     uint64_t decays_full[kRing];
-    uint64_t unit_full[2], lift_full[2];  // f16
+    uint64_t unit_full[2], lift_full[2], down_full[2];  // f16
     uint64_t score_full, score_free;
     uint64_t weight_full, weight_free;
     uint64_t parts_full, parts_free;
     uint64_t update_full, update_free;
-    uint64_t state_full, out_full, out_free;
+    uint64_t state_full, state_free, out_full, out_free;
     uint64_t ended[2];
     uint32_t tmem;
     uint32_t gave_up;
     uint32_t tiles;      // that were asked for
     Item item;
     Decays decays[kRing];
-    float row_top[2][kMaxDim];   // f16: largest of the state's rows, by halves
+    float row_top[2][kMaxDim];   // f16: largest of the state's rows, by halves;
+    float down[2][kMaxDim];      // and what they were divided by, in turns
 };
 
 // The tiles of an item, in order; every role walks them by itself.
 struct Tiles {
     int32_t done, total, phase, N;
     int32_t rows;        // of the current tile
-    int64_t row, page;   // its first row; its block position
+    int32_t row, page;   // its first row; its block position
     bool block_ends;
     uint32_t n;
 
@@ -280,23 +286,29 @@ struct Tiles {
     __device__ __forceinline__ bool last() const { return done + rows == total; }
 };
 
-// (Not inlined: the loops of all roles together have to stay in the SM's
-// instruction cache.)
-__device__ __noinline__ void scan_wait_on(ScanControl &C, uint64_t *bar, uint32_t parity, uint32_t *status) {
-    for (uint32_t i = 0; i < kWaitLimit; i++) {
-        if (bar_try(bar, parity))
-            return;
-        if ((i & 255u) == 255u && *(volatile uint32_t *)&C.gave_up)
-            return;
-    }
-    // the CTA gives up as a whole: no later wait waits, every role runs to its end
-    *(volatile uint32_t *)&C.gave_up = 1;
-    atomicOr(status, LMC_ST_TIMEOUT);
+// Waits for a phase. When the limit runs out the CTA gives up as a whole: no
+// later wait waits, every role runs to its end, and the status word says so.
+// (As few instructions as can be: the loops of all roles together have to stay in
+// the SM's instruction cache. With 110 KB of code instead of 65 the call took 1.5
+// times as long.)
+__device__ __forceinline__ bool bar_try_long(uint64_t *bar, uint32_t parity) {
+    uint32_t done;
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "selp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(done)
+        : "r"(smem_addr(bar)), "r"(parity), "r"(kLook)
+        : "memory");
+    return done != 0;
 }
 
-__device__ __forceinline__ void scan_wait(ScanControl &C, uint64_t *bar, uint32_t parity, uint32_t *status) {
-    if (!bar_try(bar, parity))
-        scan_wait_on(C, bar, parity, status);
+__device__ __forceinline__ void scan_wait(ScanControl &C, uint64_t *bar, uint32_t parity) {
+    for (uint32_t i = 1; !bar_try_long(bar, parity); i++)
+        if ((i & 15u) == 0 && (i > kWaitLimit || *(volatile uint32_t *)&C.gave_up)) {
+            *(volatile uint32_t *)&C.gave_up = 1;
+            return;
+        }
 }
 
 __device__ __forceinline__ bool scan_gone(ScanControl &C) {
@@ -318,7 +330,7 @@ __device__ __forceinline__ void weights_sync() { asm volatile("bar.sync 1, 128;"
 // Four 8 x 8 matrices of 16 bits, turned: a lane gives one of their rows'
 // addresses and gets row l / 4, columns 2 (l % 4) and the next, of each column by
 // column.
-__device__ __forceinline__ void load_turned(uint32_t (&v)[4], uint32_t addr) {
+__device__ __forceinline__ void load_turned(uint32_t *v, uint32_t addr) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
                  : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3])
                  : "r"(addr)
@@ -329,12 +341,15 @@ __device__ __forceinline__ void store_turned(uint32_t addr, uint32_t a, uint32_t
                  "r"(c), "r"(d)
                  : "memory");
 }
-// 16 lanes x 8 columns of tensor memory: lane l of the warp holds rows l / 4
-// (v[0], v[2]) and l / 4 + 8 (v[1], v[3]), columns l % 4 and l % 4 + 4.
-__device__ __forceinline__ void store_part(uint32_t addr, const uint32_t (&v)[4]) {
-    asm volatile("tcgen05.st.sync.aligned.16x128b.x2.b32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v[0]), "r"(v[1]),
-                 "r"(v[2]), "r"(v[3])
-                 : "memory");
+// 16 lanes x 32 columns of tensor memory: lane l of the warp holds rows l / 4
+// (v[2 i]) and l / 4 + 8 (v[2 i + 1]), column 4 i + l % 4.
+__device__ __forceinline__ void store_part(uint32_t addr, const uint32_t (&v)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.16x128b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16};" ::"r"(addr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
+        "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+        : "memory");
 }
 
 __device__ __forceinline__ uint32_t times(uint32_t a, uint32_t b) {
@@ -404,8 +419,8 @@ __device__ __forceinline__ void find_item(const ScanPlan &P, Item &I) {
             atomicOr(P.L.status, S.bad);
         if (S.count > 0 && i < (kStatesOnly ? n - 1 : n)) {
             const int64_t a = cut(S.count, i, n, S.before, P.L.block_size), b = cut(S.count, i + 1, n, S.before, P.L.block_size);
-            J.row = S.row + a;
-            J.page = (S.before + a) / P.L.block_size;
+            J.row = (int)(S.row + a);
+            J.page = (int)((S.before + a) / P.L.block_size);
             J.phase = (int)((S.before + a) % P.L.block_size);
             J.count = (int)(b - a);
             J.first = S.first;
@@ -497,9 +512,9 @@ __device__ __forceinline__ void load_tiles(const ScanPlan &P, ScanControl &C, ui
     uint32_t asked = 0;
     float drift = 0.0f, h0 = 0.0f, h1 = 0.0f;  // the tile before's decays,
     int rows = 0;                              // and rows
-    // A tile's decays go to its place of the ring when the next tile's copies have
-    // been asked for: the stage that these take was free, so the result of the tile
-    // before that stage's last one has been read, and with it that place.
+    // A tile's decays go to its place of the ring when the next tile's stage is
+    // free: the products of that stage's last tile are done, so the result of the
+    // tile before it has been read, whose place this was.
     static_assert(kRing >= kStages, "a place is read until the next tile's result is made");
     auto tell = [&](uint32_t n) {
         sum_decays<kBf16>(C.decays[n % kRing], h0, h1, rows, P.L.scale, drift);
@@ -507,44 +522,48 @@ __device__ __forceinline__ void load_tiles(const ScanPlan &P, ScanControl &C, ui
         if (lane == 0)
             bar_arrive(&C.decays_full[n % kRing]);
     };
-    while (T.next()) {
-        const int st = (int)uniform(T.n % kStages);
+    for (bool more = true; more;) {
+        more = T.next();
         float g0 = 0.0f, g1 = 0.0f;
-        const float *const at = decay + (T.row + 2 * lane) * P.L.decay_row;
-        if (2 * lane < T.rows)
-            g0 = *at;
-        if (2 * lane + 1 < T.rows)
-            g1 = at[P.L.decay_row];
-        if (T.n >= kStages)
-            scan_wait(C, &C.free[st], (T.n / kStages - 1) & 1, P.L.status);
-        if (scan_gone(C))
-            break;
-        uint8_t *to = mem + st * kStageBytes;
-        const int row0 = (int)uniform((int)T.row);
-        if (elect()) {
-            uint64_t *bar = &C.full[st];
-            bar_expect(bar, bytes);
-#pragma unroll 1
-            for (int i = 0; i < P.k_copies; i++)
-                tma_box(&P.k, to + 2 * kPanel + i * kPanel, i * 64, row0, kh, bar);
-#pragma unroll 1
-            for (int i = 0; i < P.v_copies; i++)
-                tma_box(&P.v, to + 4 * kPanel + i * kPanel, i * 64, row0, h, bar);
-            if (!kStatesOnly)
-    #pragma unroll 1
-            for (int i = 0; i < P.k_copies; i++)
-                    tma_box(&P.q, to + i * kPanel, i * 64, row0, kh, bar);
+        const int st = (int)uniform(asked % kStages);
+        if (more) {
+            const float *const at = decay + ((int64_t)T.row + 2 * lane) * P.L.decay_row;
+            if (2 * lane < T.rows)
+                g0 = *at;
+            if (2 * lane + 1 < T.rows)
+                g1 = at[P.L.decay_row];
         }
-        __syncwarp();
+        // (behind the last tile, too: its decays' place has to be free)
+        if (asked >= kStages)
+            scan_wait(C, &C.free[st], (asked / kStages - 1) & 1);
+        if (more) {
+            more = !scan_gone(C);
+            uint8_t *to = mem + st * kStageBytes;
+            const int row0 = (int)uniform(T.row);
+            if (more && elect()) {
+                uint64_t *bar = &C.full[st];
+                bar_expect(bar, bytes);
+#pragma unroll 1
+                for (int i = 0; i < P.k_copies; i++)
+                    tma_box(&P.k, to + 2 * kPanel + i * kPanel, i * 64, row0, kh, bar);
+#pragma unroll 1
+                for (int i = 0; i < P.v_copies; i++)
+                    tma_box(&P.v, to + 4 * kPanel + i * kPanel, i * 64, row0, h, bar);
+                if (!kStatesOnly) {
+#pragma unroll 1
+                    for (int i = 0; i < P.k_copies; i++)
+                        tma_box(&P.q, to + i * kPanel, i * 64, row0, kh, bar);
+                }
+            }
+            __syncwarp();
+        }
         if (asked > 0)
             tell(asked - 1);
-        asked++;
+        asked += more;
         h0 = g0;
         h1 = g1;
         rows = T.rows;
     }
-    if (asked > 0)
-        tell(asked - 1);
     if (lane == 0)
         C.tiles = asked;
 }
@@ -562,10 +581,10 @@ __device__ __forceinline__ void multiply_forward(const ScanPlan &P, ScanControl 
         const uint32_t n = T.n;
         const int st = (int)uniform(n % kStages);
         const uint32_t at = smem_addr(mem) + st * kStageBytes;
-        scan_wait(C, &C.full[st], (n / kStages) & 1, P.L.status);
+        scan_wait(C, &C.full[st], (n / kStages) & 1);
         if (!kStatesOnly) {
             if (n >= 1)
-                scan_wait(C, &C.score_free, (n - 1) & 1, P.L.status);
+                scan_wait(C, &C.score_free, (n - 1) & 1);
             __syncwarp();
             fence_after();
             if (elect()) {
@@ -578,9 +597,9 @@ __device__ __forceinline__ void multiply_forward(const ScanPlan &P, ScanControl 
             }
             __syncwarp();
         }
-        scan_wait(C, &C.parts_full, n & 1, P.L.status);
+        scan_wait(C, &C.parts_full, n & 1);
         if (n >= 1)
-            scan_wait(C, &C.update_free, (n - 1) & 1, P.L.status);
+            scan_wait(C, &C.update_free, (n - 1) & 1);
         __syncwarp();
         fence_after();
         if (elect()) {
@@ -614,10 +633,10 @@ __device__ __forceinline__ void multiply_state(const ScanPlan &P, ScanControl &C
         const uint32_t n = T.n;
         const int st = (int)uniform(n % kStages);
         const uint32_t at = smem_addr(mem) + st * kStageBytes;
-        scan_wait(C, &C.full[st], (n / kStages) & 1, P.L.status);
-        scan_wait(C, &C.state_full, n & 1, P.L.status);
+        scan_wait(C, &C.full[st], (n / kStages) & 1);
+        scan_wait(C, &C.state_full, n & 1);
         if (n >= 1)
-            scan_wait(C, &C.out_free, (n - 1) & 1, P.L.status);
+            scan_wait(C, &C.out_free, (n - 1) & 1);
         __syncwarp();
         fence_after();
         if (elect()) {
@@ -625,9 +644,10 @@ __device__ __forceinline__ void multiply_state(const ScanPlan &P, ScanControl &C
 #pragma unroll 1
             for (int s = 0; s < steps; s++)
                 mma_held(tmem + kFromState, tmem + kState + 8 * s, q + (s >> 2) * (kPanel >> 4) + (s & 3) * 2, from_state, s > 0);
+            commit(&C.state_free);
         }
         __syncwarp();
-        scan_wait(C, &C.weight_full, n & 1, P.L.status);
+        scan_wait(C, &C.weight_full, n & 1);
         __syncwarp();
         fence_after();
         if (elect()) {
@@ -667,8 +687,8 @@ __device__ __forceinline__ void weigh(const ScanPlan &P, ScanControl &C, uint8_t
         const uint32_t n = T.n;
         const int st = n % kStages;
         Decays &D = C.decays[n % kRing];
-        scan_wait(C, &C.decays_full[n % kRing], (n / kRing) & 1, P.L.status);
-        scan_wait(C, &C.full[st], (n / kStages) & 1, P.L.status);
+        scan_wait(C, &C.decays_full[n % kRing], (n / kRing) & 1);
+        scan_wait(C, &C.full[st], (n / kStages) & 1);
         // rows behind the tile's last belong to others: their k and v take part
         // times 0, which infinities and NaN would not bear
         if (T.rows < kTile) {
@@ -681,45 +701,50 @@ __device__ __forceinline__ void weigh(const ScanPlan &P, ScanControl &C, uint8_t
             weights_sync();
         }
         if (n >= 1)
-            scan_wait(C, &C.parts_free, (n - 1) & 1, P.L.status);
+            scan_wait(C, &C.parts_free, (n - 1) & 1);
         fence_after();
         const uint32_t from = values + st * kStageBytes;
+        uint32_t f1[8], f2[8], f3[8];  // bf16: the decays' parts
+        if constexpr (kBf16) {
+#pragma unroll
+            for (int i = 0; i < 8; i++) {
+                const uint4 f = D.left[4 * i + (lane & 3)];
+                f1[i] = f.x, f2[i] = f.y, f3[i] = f.z;
+            }
+        }
 #pragma unroll 1
         for (int block = 0; block < 2; block++) {  // of 16 values
             const uint32_t row = from + (((chunk + 2 * block) ^ (lane & 7)) << 4);
             const uint32_t to = lanes + ((uint32_t)(16 * block) << 16) + kParts;
+            uint32_t v[16];  // [4 s + i]
+#pragma unroll
+            for (int s = 0; s < kTile / 16; s++)
+                load_turned(v + 4 * s, row + s * 2048);
             if constexpr (kBf16) {
+                uint32_t a[16], b[16];
 #pragma unroll
-                for (int s = 0; s < kTile / 16; s++) {
-                    uint32_t v[4], part[4][4];
-                    load_turned(v, row + s * 2048);
-                    const uint4 fa = D.left[8 * s + (lane & 3)], fb = D.left[8 * s + 4 + (lane & 3)];
-#pragma unroll
-                    for (int i = 0; i < 4; i++) {
-                        const uint4 f = i < 2 ? fa : fb;
-                        part[0][i] = times(v[i], f.x);
-                        part[1][i] = plus_product(v[i], f.x, minus(part[0][i]));
-                        part[2][i] = times(v[i], f.y);
-                        part[3][i] = plus_product(v[i], f.z, plus_product(v[i], f.y, minus(part[2][i])));
-                    }
-#pragma unroll
-                    for (int p = 0; p < 4; p++)
-                        store_part(to + p * kPartColumns + 8 * s, part[p]);
+                for (int k = 0; k < 16; k++) {
+                    a[k] = times(v[k], f1[k >> 1]);
+                    b[k] = plus_product(v[k], f1[k >> 1], minus(a[k]));
                 }
+                store_part(to, a);
+                store_part(to + kPartColumns, b);
+#pragma unroll
+                for (int k = 0; k < 16; k++) {
+                    a[k] = times(v[k], f2[k >> 1]);
+                    b[k] = plus_product(v[k], f3[k >> 1], plus_product(v[k], f2[k >> 1], minus(a[k])));
+                }
+                store_part(to + 2 * kPartColumns, a);
+                store_part(to + 3 * kPartColumns, b);
             } else {
                 // two rounded parts of the product, whose row (a value's, of 64
                 // tokens: four lanes) is brought below 2^15 by a power of two
-                uint32_t v[kTile / 16][4];
                 float top[2] = {0.0f, 0.0f};
 #pragma unroll
-                for (int s = 0; s < kTile / 16; s++) {
-                    load_turned(v[s], row + s * 2048);
-#pragma unroll
-                    for (int i = 0; i < 4; i++) {
-                        const uint4 f = D.left[8 * s + (i < 2 ? 0 : 4) + (lane & 3)];
-                        top[i & 1] = fmaxf(top[i & 1], fmaxf(fabsf(from_q(v[s][i] & 0xffff, false)) * __uint_as_float(f.x),
-                                                             fabsf(from_q(v[s][i] >> 16, false)) * __uint_as_float(f.y)));
-                    }
+                for (int k = 0; k < 16; k++) {
+                    const float2 f = *reinterpret_cast<const float2 *>(&D.left[4 * (k >> 1) + (lane & 3)]);
+                    top[k & 1] = fmaxf(top[k & 1], fmaxf(fabsf(from_q(v[k] & 0xffff, false)) * f.x,
+                                                         fabsf(from_q(v[k] >> 16, false)) * f.y));
                 }
                 float up[2];
 #pragma unroll
@@ -731,21 +756,17 @@ __device__ __forceinline__ void weigh(const ScanPlan &P, ScanControl &C, uint8_t
                     if ((lane & 3) == 0)
                         D.unit[32 * quarter + 16 * block + 8 * k + lane / 4] = power(-e);
                 }
+                uint32_t a[16], b[16];
 #pragma unroll
-                for (int s = 0; s < kTile / 16; s++) {
-                    uint32_t part[2][4];
-#pragma unroll
-                    for (int i = 0; i < 4; i++) {
-                        const uint4 f = D.left[8 * s + (i < 2 ? 0 : 4) + (lane & 3)];
-                        const float x = from_q(v[s][i] & 0xffff, false) * __uint_as_float(f.x) * up[i & 1];
-                        const float y = from_q(v[s][i] >> 16, false) * __uint_as_float(f.y) * up[i & 1];
-                        part[0][i] = pack<false>(x, y);
-                        part[1][i] = pack<false>(x - from_q(part[0][i] & 0xffff, false), y - from_q(part[0][i] >> 16, false));
-                    }
-#pragma unroll
-                    for (int p = 0; p < 2; p++)
-                        store_part(to + p * kPartColumns + 8 * s, part[p]);
+                for (int k = 0; k < 16; k++) {
+                    const float2 f = *reinterpret_cast<const float2 *>(&D.left[4 * (k >> 1) + (lane & 3)]);
+                    const float x = from_q(v[k] & 0xffff, false) * f.x * up[k & 1];
+                    const float y = from_q(v[k] >> 16, false) * f.y * up[k & 1];
+                    a[k] = pack<false>(x, y);
+                    b[k] = pack<false>(x - from_q(a[k] & 0xffff, false), y - from_q(a[k] >> 16, false));
                 }
+                store_part(to, a);
+                store_part(to + kPartColumns, b);
             }
         }
         wait_st();
@@ -759,82 +780,92 @@ __device__ __forceinline__ void weigh(const ScanPlan &P, ScanControl &C, uint8_t
         if (kStatesOnly)
             continue;
 
-        scan_wait(C, &C.score_full, n & 1, P.L.status);
+        scan_wait(C, &C.score_full, n & 1);
         fence_after();
-        uint32_t raw[2][16];
-        load_s(raw[0], lanes + kScores);
-        if (quarter >= 2)
-            load_s(raw[1], lanes + kScores + 32);
-        wait_ld();
-        fence_before();
-        __syncwarp();
-        if (lane == 0)
-            bar_arrive(&C.score_free);
         const float2 la = D.log[ra], lb = D.log[rb];
-        const int x = ra & 7;  // rb & 7 is the same
-        float p[8][4];
-        float ta = 0.0f, tb = 0.0f;
+        // tokens behind the rows' own: 0 from the start
+        const int halves = 1 + (quarter >> 1);
+        // 32 tokens' weights of the thread's rows: (ra, c), (ra, c + 1), (rb, c), (rb, c
+        // + 1) with c = 32 half + 8 i + 2 (lane % 4)
+        auto make = [&](int half, float (&p)[4][4]) {
+            uint32_t raw[16];
+            load_s(raw, lanes + kScores + 32 * half);
+            wait_ld();
 #pragma unroll
-        for (int i = 0; i < 8; i++) {
-            if (i > 2 * quarter + 1)
-                continue;  // tokens behind the rows': 0 from the start
-            const float4 lc = *reinterpret_cast<const float4 *>(&D.log[8 * i + 2 * (lane & 3)]);
-            const uint32_t *s = &raw[i >> 2][4 * (i & 3)];
-            p[i][0] = __uint_as_float(s[0]) * exp2_fast((la.x - lc.x) + (la.y - lc.y));
-            p[i][1] = __uint_as_float(s[1]) * exp2_fast((la.x - lc.z) + (la.y - lc.w));
-            p[i][2] = __uint_as_float(s[2]) * exp2_fast((lb.x - lc.x) + (lb.y - lc.y));
-            p[i][3] = __uint_as_float(s[3]) * exp2_fast((lb.x - lc.z) + (lb.y - lc.w));
-            if (i >= 2 * quarter) {
-                const int c = 8 * i + 2 * (lane & 3);
-                p[i][0] = c <= ra ? p[i][0] : 0.0f;
-                p[i][1] = c + 1 <= ra ? p[i][1] : 0.0f;
-                p[i][2] = c <= rb ? p[i][2] : 0.0f;
-                p[i][3] = c + 1 <= rb ? p[i][3] : 0.0f;
+            for (int i = 0; i < 4; i++) {
+                const int c = 32 * half + 8 * i + 2 * (lane & 3);
+                const float4 lc = *reinterpret_cast<const float4 *>(&D.log[c]);
+                const float w0 = exp2_fast((la.x - lc.x) + (la.y - lc.y)), w1 = exp2_fast((la.x - lc.z) + (la.y - lc.w));
+                const float w2 = exp2_fast((lb.x - lc.x) + (lb.y - lc.y)), w3 = exp2_fast((lb.x - lc.z) + (lb.y - lc.w));
+                p[i][0] = c <= ra ? __uint_as_float(raw[4 * i]) * w0 : 0.0f;
+                p[i][1] = c < ra ? __uint_as_float(raw[4 * i + 1]) * w1 : 0.0f;
+                p[i][2] = c <= rb ? __uint_as_float(raw[4 * i + 2]) * w2 : 0.0f;
+                p[i][3] = c < rb ? __uint_as_float(raw[4 * i + 3]) * w3 : 0.0f;
             }
-            if constexpr (!kBf16) {
-                ta = fmaxf(ta, fmaxf(fabsf(p[i][0]), fabsf(p[i][1])));
-                tb = fmaxf(tb, fmaxf(fabsf(p[i][2]), fabsf(p[i][3])));
+        };
+        auto put = [&](int half, const float (&p)[4][4], float ua, float ub) {
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                const int at = ((i + 4 * half) ^ (ra & 7)) << 4;  // rb & 7 is the same
+                *reinterpret_cast<uint32_t *>(pa + at) = pack<kBf16>(p[i][0] * ua, p[i][1] * ua);
+                *reinterpret_cast<uint32_t *>(pb + at) = pack<kBf16>(p[i][2] * ub, p[i][3] * ub);
             }
-        }
-        float ua = 1.0f, ub = 1.0f;
-        if constexpr (!kBf16) {
+        };
+        if constexpr (kBf16) {
+            if (n >= 1)
+                scan_wait(C, &C.weight_free, (n - 1) & 1);
+#pragma unroll 1
+            for (int half = 0; half < halves; half++) {
+                float p[4][4];
+                make(half, p);
+                put(half, p, 1.0f, 1.0f);
+            }
+            fence_before();
+        } else {
             // f16 has not binary32's range: a row's weights are brought below 2^15
+            float p[2][4][4], ta = 0.0f, tb = 0.0f;
+            make(0, p[0]);
+            if (halves > 1)
+                make(1, p[1]);
+            fence_before();
+#pragma unroll
+            for (int half = 0; half < 2; half++)
+                if (half < halves)
+#pragma unroll
+                    for (int i = 0; i < 4; i++) {
+                        ta = fmaxf(ta, fmaxf(fabsf(p[half][i][0]), fabsf(p[half][i][1])));
+                        tb = fmaxf(tb, fmaxf(fabsf(p[half][i][2]), fabsf(p[half][i][3])));
+                    }
             for (int o = 1; o < 4; o <<= 1) {
                 ta = fmaxf(ta, __shfl_xor_sync(0xffffffffu, ta, o));
                 tb = fmaxf(tb, __shfl_xor_sync(0xffffffffu, tb, o));
             }
             const int ea = lift_of(ta), eb = lift_of(tb);
-            ua = power(ea);
-            ub = power(eb);
             if ((lane & 3) == 0) {
                 D.lift[ra] = power(-ea) * P.L.scale;
                 D.lift[rb] = power(-eb) * P.L.scale;
             }
-            __syncwarp();
-            if (lane == 0)
-                bar_arrive(&C.lift_full[n & 1]);
-        }
-        if (n >= 1)
-            scan_wait(C, &C.weight_free, (n - 1) & 1, P.L.status);
-#pragma unroll
-        for (int i = 0; i < 8; i++) {
-            if (i > 2 * quarter + 1)
-                continue;
-            *reinterpret_cast<uint32_t *>(pa + ((i ^ x) << 4)) = pack<kBf16>(p[i][0] * ua, p[i][1] * ua);
-            *reinterpret_cast<uint32_t *>(pb + ((i ^ x) << 4)) = pack<kBf16>(p[i][2] * ub, p[i][3] * ub);
+            if (n >= 1)
+                scan_wait(C, &C.weight_free, (n - 1) & 1);
+            put(0, p[0], power(ea), power(eb));
+            if (halves > 1)
+                put(1, p[1], power(ea), power(eb));
         }
         fence_async();
         __syncwarp();
-        if (lane == 0)
+        if (lane == 0) {
+            bar_arrive(&C.score_free);
+            if (!kBf16)
+                bar_arrive(&C.lift_full[n & 1]);
             bar_arrive(&C.weight_full);
+        }
     }
 }
 
 // Eight warps: the state, turned, in registers: warps w and w + 4 hold values 32 w
-// .. 32 w + 31 (a lane each), w the first 64 keys, w + 4 the others. Of the
-// result w takes the tile's first 32 tokens, w + 4 the last.
+// .. 32 w + 31 (a lane each), w the first 64 keys, w + 4 the others.
 template <bool kBf16, bool kStatesOnly>
-__device__ __forceinline__ void carry(const ScanPlan &P, ScanControl &C, uint8_t *mem) {
+__device__ __forceinline__ void carry(const ScanPlan &P, ScanControl &C) {
     Tiles T(C.item, P.L.block_size);
     const LinearPlan &L = P.L;
     const Item &I = C.item;
@@ -873,8 +904,8 @@ __device__ __forceinline__ void carry(const ScanPlan &P, ScanControl &C, uint8_t
     // The state as A of its product with q, in 16 bits; what is to be multiplied
     // to its row's results (f16, which has not binary32's range: rows are brought
     // below 2^15).
-    auto hand_over = [&] {
-        float up = 1.0f, down = 1.0f;
+    auto hand_over = [&](uint32_t n) {
+        float up = 1.0f;
         if constexpr (!kBf16) {
             float top = 0.0f;
 #pragma unroll
@@ -885,7 +916,8 @@ __device__ __forceinline__ void carry(const ScanPlan &P, ScanControl &C, uint8_t
             top = fmaxf(top, C.row_top[half ^ 1][j]);
             const int e = lift_of(top);
             up = power(e);
-            down = power(-e);
+            if (half == 0)
+                C.down[n & 1][j] = power(-e);
         }
         if (mine) {
 #pragma unroll
@@ -900,9 +932,11 @@ __device__ __forceinline__ void carry(const ScanPlan &P, ScanControl &C, uint8_t
         }
         fence_before();
         __syncwarp();
-        if (lane == 0)
+        if (lane == 0) {
+            if (!kBf16)
+                bar_arrive(&C.down_full[n & 1]);
             bar_arrive(&C.state_full);
-        return down;
+        }
     };
     // where a state is at hand before the item's tokens
     float *const slot = P.slots + (int64_t)I.slot * slot_size + head;
@@ -915,12 +949,8 @@ __device__ __forceinline__ void carry(const ScanPlan &P, ScanControl &C, uint8_t
     if (first)
         write(slot);
     float total = 0.0f;  // log2 of the decay over the item
-    float down = 1.0f;
     if (!kStatesOnly && I.count > 0)
-        down = hand_over();
-    // a warp's part of a result: rows of 64 bytes, a token each
-    const uint32_t staged = smem_addr(mem) + kResultAt + warp * kWarpResult;
-    const int64_t out_at = (int64_t)I.h * L.out_head + quarter * 32;
+        hand_over(0);
     while (T.next()) {
         const uint32_t n = T.n;
         const Decays &D = C.decays[n % kRing];
@@ -929,17 +959,14 @@ __device__ __forceinline__ void carry(const ScanPlan &P, ScanControl &C, uint8_t
         if (!kStatesOnly && (T.block_ends || (I.ends && T.last())))
             block = __ldca(L.table + I.r * L.row_stride + T.page);
 
-        scan_wait(C, &C.decays_full[n % kRing], (n / kRing) & 1, L.status);
+        scan_wait(C, &C.decays_full[n % kRing], (n / kRing) & 1);
         const float grow = D.grow;
         if (kStatesOnly)
             total += D.log[kTile - 1].x + D.log[kTile - 1].y;
-        if (!kBf16) {
-            scan_wait(C, &C.unit_full[n & 1], (n >> 1) & 1, L.status);
-            if (!kStatesOnly)
-                scan_wait(C, &C.lift_full[n & 1], (n >> 1) & 1, L.status);
-        }
+        if (!kBf16)
+            scan_wait(C, &C.unit_full[n & 1], (n >> 1) & 1);
         const float unit = kBf16 ? 1.0f : D.unit[j];
-        scan_wait(C, &C.update_full, n & 1, L.status);
+        scan_wait(C, &C.update_full, n & 1);
         fence_after();
         if (mine) {
 #pragma unroll
@@ -962,31 +989,68 @@ __device__ __forceinline__ void carry(const ScanPlan &P, ScanControl &C, uint8_t
         else if (block != -1 && threadIdx.x == 0)
             atomicOr(L.status, LMC_ST_BLOCK_OOR);
         __syncwarp();
-        if (kStatesOnly)
-            continue;
+        if (!kStatesOnly && !T.last()) {
+            scan_wait(C, &C.state_free, n & 1);
+            fence_after();
+            hand_over(n + 1);
+        }
+    }
+    if (kStatesOnly) {
+        write(slot + slot_size);
+        if (threadIdx.x == 0)
+            P.totals[((int64_t)I.slot + 1) * L.H + I.h] = total;
+    }
+}
 
-        scan_wait(C, &C.out_full, n & 1, L.status);
+// Four warps: the result of each tile. Warp w takes values 32 w .. 32 w + 31.
+template <bool kBf16>
+__device__ __forceinline__ void deliver(const ScanPlan &P, ScanControl &C, uint8_t *mem) {
+    Tiles T(C.item, P.L.block_size);
+    const LinearPlan &L = P.L;
+    const int lane = threadIdx.x & 31, quarter = (threadIdx.x >> 5) - kFirstResultWarp;
+    const uint32_t lanes = C.tmem + ((uint32_t)(quarter * 32) << 16);
+    uint8_t *const mine = mem + kResultAt + quarter * kWarpResult;
+    // A row of 32 values, 64 bytes, per token; its 16-byte pieces change places
+    // from row to row, so that no two of eight rows' fall into the same banks.
+    // The row of four 8 x 8 matrices that this lane names:
+    const int named = 8 * (lane >> 4) + (lane & 7), piece = lane >> 3 & 1;
+    const uint32_t staged = smem_addr(mine) + named * 64, turn = named >> 1 & 3;
+    const int64_t out_at = (int64_t)C.item.h * L.out_head + quarter * 32;
+    while (T.next()) {
+        const uint32_t n = T.n;
+        const Decays &D = C.decays[n % kRing];
+        scan_wait(C, &C.decays_full[n % kRing], (n / kRing) & 1);
+        if (!kBf16) {
+            scan_wait(C, &C.lift_full[n & 1], (n >> 1) & 1);
+            scan_wait(C, &C.down_full[n & 1], (n >> 1) & 1);
+        }
+        scan_wait(C, &C.out_full, n & 1);
         fence_after();
+        float2 since[4];
 #pragma unroll 1
-        for (int b16 = 0; b16 < 2; b16++) {  // 16 values
+        for (int part = 0; part < 4; part++) {  // 32 tokens, 16 values
+            const int half = part >> 1, b16 = part & 1;
+            if (b16 == 0)
+#pragma unroll
+                for (int i = 0; i < 4; i++)
+                    since[i] = *reinterpret_cast<const float2 *>(&D.since[32 * half + 8 * i + 2 * (lane & 3)]);
             uint32_t a[16], b[16];
-            const uint32_t at16 = lanes + ((uint32_t)(16 * b16) << 16) + 32 * half;
-            load_s(a, at16 + kFromState);
-            load_s(b, at16 + kFromTile);
+            const uint32_t at = lanes + ((uint32_t)(16 * b16) << 16) + 32 * half;
+            load_s(a, at + kFromState);
+            load_s(b, at + kFromTile);
             float da = 1.0f, db = 1.0f;
             if constexpr (!kBf16) {
-                da = __shfl_sync(0xffffffffu, down, 16 * b16 + lane / 4);
-                db = __shfl_sync(0xffffffffu, down, 16 * b16 + lane / 4 + 8);
+                da = C.down[n & 1][32 * quarter + 16 * b16 + lane / 4];
+                db = C.down[n & 1][32 * quarter + 16 * b16 + lane / 4 + 8];
             }
             wait_ld();
             uint32_t y[8];
 #pragma unroll
             for (int i = 0; i < 4; i++) {
-                const int t = 32 * half + 8 * i + 2 * (lane & 3);
-                const float2 e = *reinterpret_cast<const float2 *>(&D.since[t]);
+                const float2 e = since[i];
                 float2 g = make_float2(L.scale, L.scale);
                 if constexpr (!kBf16)
-                    g = *reinterpret_cast<const float2 *>(&D.lift[t]);
+                    g = *reinterpret_cast<const float2 *>(&D.lift[32 * half + 8 * i + 2 * (lane & 3)]);
 #pragma unroll
                 for (int k = 0; k < 2; k++) {
                     float x0 = __uint_as_float(a[4 * i + 2 * k]) * e.x, x1 = __uint_as_float(a[4 * i + 2 * k + 1]) * e.y;
@@ -998,10 +1062,7 @@ __device__ __forceinline__ void carry(const ScanPlan &P, ScanControl &C, uint8_t
                                                fmaf(__uint_as_float(b[4 * i + 2 * k + 1]), g.y, x1));
                 }
             }
-            // a row of 32 values, 64 bytes, per token; 16-byte pieces in turns, so
-            // that no two of eight rows fall into the same banks
-            const int t = 8 * (lane >> 4) + (lane & 7);
-            const uint32_t to = staged + t * 64 + (((2 * b16 + (lane >> 3 & 1)) ^ (t >> 1 & 3)) << 4);
+            const uint32_t to = staged + half * 32 * 64 + (((2 * b16 + piece) ^ turn) << 4);
             store_turned(to, y[0], y[1], y[2], y[3]);
             store_turned(to + 16 * 64, y[4], y[5], y[6], y[7]);
         }
@@ -1009,32 +1070,25 @@ __device__ __forceinline__ void carry(const ScanPlan &P, ScanControl &C, uint8_t
         __syncwarp();
         if (lane == 0)
             bar_arrive(&C.out_free);
-        if (!T.last())
-            down = hand_over();
-        const int rows = T.rows - 32 * half;
-        const uint8_t *const mine8 = mem + kResultAt + warp * kWarpResult;
         if (P.wide_out) {
-            const int v = 8 * (lane & 3);
-            uint16_t *out = L.out + (T.row + 32 * half + (lane >> 2)) * L.out_row + out_at + v;
-#pragma unroll
-            for (int i = 0; i < 4; i++) {
-                const int t = 8 * i + (lane >> 2);
-                const uint4 x = *reinterpret_cast<const uint4 *>(mine8 + t * 64 + (((lane & 3) ^ (t >> 1 & 3)) << 4));
-                if (t < rows && quarter * 32 + v < L.dv)
-                    __stcs(reinterpret_cast<uint4 *>(out + 8 * i * L.out_row), x);
+            const int v = 8 * (lane & 3), t0 = lane >> 2;
+            uint16_t *out = L.out + ((int64_t)T.row + t0) * L.out_row + out_at + v;
+            const bool inside = quarter * 32 + v < L.dv;
+#pragma unroll 2
+            for (int i = 0; i < 8; i++) {
+                const int t = 8 * i + t0;
+                const uint4 x = *reinterpret_cast<const uint4 *>(mine + t * 64 + (((lane & 3) ^ (t >> 1 & 3)) << 4));
+                if (inside && t < T.rows)
+                    __stcs(reinterpret_cast<uint4 *>(out), x);
+                out += 8 * L.out_row;
             }
-        } else if (j < L.dv) {
+        } else if (quarter * 32 + lane < L.dv) {
 #pragma unroll 1
-            for (int t = 0; t < rows && t < 32; t++)
-                L.out[(T.row + 32 * half + t) * L.out_row + out_at + lane] =
-                    *reinterpret_cast<const uint16_t *>(mine8 + t * 64 + (((lane >> 3) ^ (t >> 1 & 3)) << 4) + 2 * (lane & 7));
+            for (int t = 0; t < T.rows; t++)
+                L.out[((int64_t)T.row + t) * L.out_row + out_at + lane] =
+                    *reinterpret_cast<const uint16_t *>(mine + t * 64 + (((lane >> 3) ^ (t >> 1 & 3)) << 4) + 2 * (lane & 7));
         }
         __syncwarp();
-    }
-    if (kStatesOnly) {
-        write(slot + slot_size);
-        if (threadIdx.x == 0)
-            P.totals[((int64_t)I.slot + 1) * L.H + I.h] = total;
     }
 }
 
@@ -1073,6 +1127,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) lmc_linear_scan_kernel(const 
         for (int i = 0; i < 2; i++) {
             bar_init(&C.unit_full[i], kWeightWarps);
             bar_init(&C.lift_full[i], kWeightWarps);
+            bar_init(&C.down_full[i], kStateWarps);
             bar_init(&C.ended[i], 1);
         }
         bar_init(&C.weight_full, kWeightWarps);
@@ -1085,7 +1140,8 @@ __global__ void __launch_bounds__(kScanThreads, 1) lmc_linear_scan_kernel(const 
         bar_init(&C.update_free, kStateWarps);
         bar_init(&C.state_full, kStateWarps);
         bar_init(&C.out_full, 1);
-        bar_init(&C.out_free, kStateWarps);
+        bar_init(&C.state_free, 1);
+        bar_init(&C.out_free, kResultWarps);
         C.gave_up = 0;
         C.tiles = 0;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -1111,21 +1167,32 @@ __global__ void __launch_bounds__(kScanThreads, 1) lmc_linear_scan_kernel(const 
     fence_after();
     let_next_start();
 
-    if (warp < kStateWarps)
-        carry<kBf16, kStatesOnly>(P, C, scan_mem);
-    else if (warp < kLoadWarp)
+    if (warp < kStateWarps) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kStateRegisters));
+        carry<kBf16, kStatesOnly>(P, C);
+    } else if (warp < kFirstResultWarp) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kWeightRegisters));
         weigh<kBf16, kStatesOnly>(P, C, scan_mem);
-    else if (warp == kLoadWarp)
-        load_tiles<kBf16, kStatesOnly>(P, C, scan_mem);
-    else if (warp == kForwardWarp)
-        multiply_forward<kBf16, kStatesOnly>(P, C, scan_mem);
-    else if (!kStatesOnly)
-        multiply_state<kBf16>(P, C, scan_mem);
+    } else if (warp < kLoadWarp) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kResultRegisters));
+        if (!kStatesOnly)
+            deliver<kBf16>(P, C, scan_mem);
+    } else {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegisters));
+        if (warp == kLoadWarp)
+            load_tiles<kBf16, kStatesOnly>(P, C, scan_mem);
+        else if (warp == kForwardWarp)
+            multiply_forward<kBf16, kStatesOnly>(P, C, scan_mem);
+        else if (warp == kStateProductWarp && !kStatesOnly)
+            multiply_state<kBf16>(P, C, scan_mem);
+    }
     __syncwarp();
     fence_before();
     __syncthreads();
     fence_after();
     if (C.gave_up) {
+        if (threadIdx.x == 0)
+            atomicOr(P.L.status, LMC_ST_TIMEOUT);
         scan_wind_up(C, warp);
         __syncthreads();
     }
