@@ -184,13 +184,14 @@ constexpr int kPanel = kTile * 128;   // bytes of 64 values of a tile's rows
 constexpr int kStages = 4;
 constexpr int kStageBytes = 6 * kPanel;  // q, k, v, two panels each
 constexpr int kStateWarps = 8;
-constexpr int kFirstWeightWarp = 8, kWeightWarps = 4;
-constexpr int kFirstResultWarp = 12, kResultWarps = 4;
-constexpr int kLoadWarp = 16, kForwardWarp = 17, kStateProductWarp = 18;
-constexpr int kScanThreads = 20 * 32;
-// Registers per thread of the warpgroups: 2 x 128 + 96 + 72 + 56 of the 5 x 96 the
-// CTA starts with.
-constexpr int kStateRegisters = 128, kWeightRegisters = 96, kResultRegisters = 72, kOtherRegisters = 56;
+constexpr int kFirstPartWarp = 8, kPartWarps = 4;
+constexpr int kFirstWeightWarp = 12, kWeightWarps = 4;
+constexpr int kFirstResultWarp = 16, kResultWarps = 4;
+constexpr int kLoadWarp = 20, kForwardWarp = 21, kStateProductWarp = 22;
+constexpr int kScanThreads = 24 * 32;
+// Registers per thread of the warpgroups: 2 x 120 + 88 + 56 + 56 + 40 of the 6 x 80
+// the CTA starts with.
+constexpr int kStateRegisters = 120, kPartRegisters = 88, kWeightRegisters = 56, kResultRegisters = 56, kOtherRegisters = 40;
 // shared memory behind the stages: the weights, the result on its way
 constexpr int kWeightsAt = kStages * kStageBytes, kResultAt = kWeightsAt + kPanel;
 constexpr int kWarpResult = kTile * 64;  // bytes of a warp's part of a result: 32 values of each token
@@ -230,7 +231,7 @@ struct Item {
 // What a tile's tokens' decays give.
 struct alignas(16) Decays {
     float2 log[kTile];      // sum up to and with the token, in units of log 2 (high, low)
-    uint4 left[kTile / 2];  // from the token to the tile's end, two tokens: as three bf16 parts, or (f16) as it is
+    uint4 left[kTile / 2];  // from the token to the tile's end, two tokens: the first of three bf16 parts, twice, the others; or (f16) as it is
     float since[kTile];     // from the tile's start up to the token, times the call's scale
     float lift[kTile];      // f16: what the token's weights were divided by, times the scale
     float unit[kMaxDim];    // f16: what a value's row of v times its decay was divided by
@@ -244,7 +245,7 @@ struct ScanControl {
     uint64_t unit_full[2], lift_full[2], down_full[2];  // f16
     uint64_t score_full, score_free;
     uint64_t weight_full, weight_free;
-    uint64_t parts_full, parts_free;
+    uint64_t parts_full[2], parts_free[2];  // the upper and the lower parts
     uint64_t update_full, update_free;
     uint64_t state_full, state_free, out_full, out_free;
     uint64_t ended[2];
@@ -325,7 +326,15 @@ __device__ __forceinline__ void mma_held(uint32_t d, uint32_t a, uint64_t b, uin
         : "memory");
 }
 
-__device__ __forceinline__ void weights_sync() { asm volatile("bar.sync 1, 128;" ::: "memory"); }
+// Rows of `panels` panels behind a tile's last one, cleared by four warps: they
+// belong to others, and take part in products times 0, which infinities and NaN
+// would not bear.
+__device__ __forceinline__ void clear_rows(uint8_t *panels, int rows, int tid) {
+#pragma unroll 1
+    for (int c = tid; c < 2 * (kPanel / 16); c += 128)
+        if ((c >> 3 & (kTile - 1)) >= rows)
+            *reinterpret_cast<uint4 *>(panels + c * 16) = make_uint4(0, 0, 0, 0);
+}
 
 // Four 8 x 8 matrices of 16 bits, turned: a lane gives one of their rows'
 // addresses and gets row l / 4, columns 2 (l % 4) and the next, of each column by
@@ -471,7 +480,7 @@ __device__ __forceinline__ void sum_decays(Decays &D, float g0, float g1, int ro
         const uint32_t p = pack<true>(f0, f1);
         const float r0 = f0 - from_q(p & 0xffff, true), r1 = f1 - from_q(p >> 16, true);
         const uint32_t q = pack<true>(r0, r1);
-        D.left[lane] = make_uint4(p, q, pack<true>(r0 - from_q(q & 0xffff, true), r1 - from_q(q >> 16, true)), 0);
+        D.left[lane] = make_uint4(p, p, q, pack<true>(r0 - from_q(q & 0xffff, true), r1 - from_q(q >> 16, true)));
     } else {
         D.left[lane] = make_uint4(__float_as_uint(f0), __float_as_uint(f1), 0, 0);
     }
@@ -577,6 +586,7 @@ __device__ __forceinline__ void multiply_forward(const ScanPlan &P, ScanControl 
     const int keys = 64 * P.k_panels, steps = (P.L.dk + 15) / 16;
     const uint32_t scores = instruction(kBf16, false, 64, kTile);
     const uint32_t update = instruction(kBf16, false, 128, keys) | 1u << 16;  // B turned
+    constexpr int kHalf = kBf16 ? 2 : 1;
     while (T.next()) {
         const uint32_t n = T.n;
         const int st = (int)uniform(n % kStages);
@@ -597,26 +607,30 @@ __device__ __forceinline__ void multiply_forward(const ScanPlan &P, ScanControl 
             }
             __syncwarp();
         }
-        scan_wait(C, &C.parts_full, n & 1);
+        // as the parts come: the upper one or two, then the lower
+        const uint64_t k = matrix(at + 2 * kPanel, kPanel, 1024);
         if (n >= 1)
             scan_wait(C, &C.update_free, (n - 1) & 1);
-        __syncwarp();
-        fence_after();
-        if (elect()) {
-            const uint64_t k = matrix(at + 2 * kPanel, kPanel, 1024);
-            // the small parts first
-            constexpr int kLast = (kBf16 ? 4 : 2) - 1;
 #pragma unroll 1
-            for (int part = kLast; part >= 0; part--)
+        for (int half = 0; half < 2; half++) {
+            scan_wait(C, &C.parts_full[half], n & 1);
+            __syncwarp();
+            fence_after();
+            if (elect()) {
+#pragma unroll 1
+                for (int part = kHalf * half; part < kHalf * (half + 1); part++)
 #pragma unroll
-                for (int s = 0; s < kTile / 16; s++)
-                    mma_held(tmem + kUpdate, tmem + kParts + part * kPartColumns + 8 * s, k + s * (2048 >> 4), update,
-                             part < kLast || s > 0);
-            commit(&C.update_full);
-            commit(&C.parts_free);
-            commit(&C.free[st]);
+                    for (int s = 0; s < kTile / 16; s++)
+                        mma_held(tmem + kUpdate, tmem + kParts + part * kPartColumns + 8 * s, k + s * (2048 >> 4), update,
+                                 part > 0 || s > 0);
+                commit(&C.parts_free[half]);
+                if (half == 1) {
+                    commit(&C.update_full);
+                    commit(&C.free[st]);
+                }
+            }
+            __syncwarp();
         }
-        __syncwarp();
     }
 }
 
@@ -663,22 +677,30 @@ __device__ __forceinline__ void multiply_state(const ScanPlan &P, ScanControl &C
     }
 }
 
+// What a lane holds of 16 values' 64 tokens (load_turned): those behind the
+// tile's last row become 0.
+__device__ __forceinline__ void keep_rows(uint32_t (&v)[16], int rows) {
+    const int lane = threadIdx.x & 31;
+#pragma unroll
+    for (int k = 0; k < 16; k++) {
+        const int t = 8 * (k >> 1) + 2 * (lane & 3);
+        v[k] &= (t < rows ? 0xffffu : 0u) | (t + 1 < rows ? 0xffff0000u : 0u);
+    }
+}
+
 // Four warps: v times the decay to the tile's end, turned, in parts of 16 bits,
-// to tensor memory (warp w: values 32 w .. 32 w + 31), and the weights
-// P = (Q K^T) * decays, of tokens up to the row's own (rows 16 w .. 16 w + 15).
+// to tensor memory (warp w: values 32 w .. 32 w + 31).
 //
 // What is added to the state keeps binary32's digits: with f = f1 + f2 + f3 in
 // bf16, v f = A + B + C + D where A = rn(v f1), B = v f1 - A (exact: a product of
 // two numbers of 8 bits has 16), C = rn(v f2) and D = rn(v f3 + (v f2 - C)), each
 // a bf16: off by 2^-26. In pairs of bf16 that is five instructions for two values
 // (three truncated parts of a binary32 product are fifteen).
-template <bool kBf16, bool kStatesOnly>
-__device__ __forceinline__ void weigh(const ScanPlan &P, ScanControl &C, uint8_t *mem) {
+template <bool kBf16>
+__device__ __forceinline__ void split(const ScanPlan &P, ScanControl &C, uint8_t *mem) {
     Tiles T(C.item, P.L.block_size);
-    const int lane = threadIdx.x & 31, quarter = (threadIdx.x >> 5) - kFirstWeightWarp, tid = threadIdx.x - kFirstWeightWarp * 32;
+    const int lane = threadIdx.x & 31, quarter = (threadIdx.x >> 5) - kFirstPartWarp;
     const uint32_t lanes = C.tmem + ((uint32_t)(quarter * 32) << 16);
-    const int ra = quarter * 16 + lane / 4, rb = ra + 8;  // this thread's rows of P
-    uint8_t *const pa = mem + kWeightsAt + ra * 128 + 4 * (lane & 3), *const pb = pa + 8 * 128;
     // the row of four 8 x 8 matrices that this lane names: tokens 8 (lane / 16) +
     // lane % 8 of a step's, values 8 (lane / 8 % 2) .. of 16
     const uint32_t values = smem_addr(mem) + 4 * kPanel + (quarter >> 1) * kPanel + (8 * (lane >> 4) + (lane & 7)) * 128;
@@ -689,54 +711,68 @@ __device__ __forceinline__ void weigh(const ScanPlan &P, ScanControl &C, uint8_t
         Decays &D = C.decays[n % kRing];
         scan_wait(C, &C.decays_full[n % kRing], (n / kRing) & 1);
         scan_wait(C, &C.full[st], (n / kStages) & 1);
-        // rows behind the tile's last belong to others: their k and v take part
-        // times 0, which infinities and NaN would not bear
-        if (T.rows < kTile) {
-            uint8_t *const rows = mem + st * kStageBytes + 2 * kPanel;
-#pragma unroll 1
-            for (int c = tid; c < 4 * (kPanel / 16); c += kWeightWarps * 32)
-                if ((c >> 3 & (kTile - 1)) >= T.rows)
-                    *reinterpret_cast<uint4 *>(rows + c * 16) = make_uint4(0, 0, 0, 0);
+        if (T.rows < kTile) {  // the products' other side
+            clear_rows(mem + st * kStageBytes + 2 * kPanel, T.rows, threadIdx.x - kFirstPartWarp * 32);
             fence_async();
-            weights_sync();
         }
-        if (n >= 1)
-            scan_wait(C, &C.parts_free, (n - 1) & 1);
-        fence_after();
         const uint32_t from = values + st * kStageBytes;
-        uint32_t f1[8], f2[8], f3[8];  // bf16: the decays' parts
+        // Upper parts first: their products run while the lower are made, and the
+        // next tile's upper parts are made while the lower's run. (f16's two parts
+        // are made together, and go into one half each.)
         if constexpr (kBf16) {
-#pragma unroll
-            for (int i = 0; i < 8; i++) {
-                const uint4 f = D.left[4 * i + (lane & 3)];
-                f1[i] = f.x, f2[i] = f.y, f3[i] = f.z;
-            }
-        }
 #pragma unroll 1
-        for (int block = 0; block < 2; block++) {  // of 16 values
-            const uint32_t row = from + (((chunk + 2 * block) ^ (lane & 7)) << 4);
-            const uint32_t to = lanes + ((uint32_t)(16 * block) << 16) + kParts;
-            uint32_t v[16];  // [4 s + i]
+            for (int half = 0; half < 2; half++) {
+                uint32_t f[8], g[8];
 #pragma unroll
-            for (int s = 0; s < kTile / 16; s++)
-                load_turned(v + 4 * s, row + s * 2048);
-            if constexpr (kBf16) {
-                uint32_t a[16], b[16];
-#pragma unroll
-                for (int k = 0; k < 16; k++) {
-                    a[k] = times(v[k], f1[k >> 1]);
-                    b[k] = plus_product(v[k], f1[k >> 1], minus(a[k]));
+                for (int i = 0; i < 8; i++) {
+                    const uint2 x = reinterpret_cast<const uint2 *>(&D.left[4 * i + (lane & 3)])[half];
+                    f[i] = x.x, g[i] = x.y;
                 }
-                store_part(to, a);
-                store_part(to + kPartColumns, b);
+                if (n >= 1)
+                    scan_wait(C, &C.parts_free[half], (n - 1) & 1);
+                fence_after();
+#pragma unroll 1
+                for (int block = 0; block < 2; block++) {  // of 16 values
+                    uint32_t v[16], a[16], b[16];  // [4 s + i]
 #pragma unroll
-                for (int k = 0; k < 16; k++) {
-                    a[k] = times(v[k], f2[k >> 1]);
-                    b[k] = plus_product(v[k], f3[k >> 1], plus_product(v[k], f2[k >> 1], minus(a[k])));
+                    for (int s = 0; s < kTile / 16; s++)
+                        load_turned(v + 4 * s, from + (((chunk + 2 * block) ^ (lane & 7)) << 4) + s * 2048);
+                    if (T.rows < kTile)
+                        keep_rows(v, T.rows);
+#pragma unroll
+                    for (int k = 0; k < 16; k++) {
+                        a[k] = times(v[k], f[k >> 1]);
+                        b[k] = plus_product(v[k], f[k >> 1], minus(a[k]));
+                    }
+                    if (half == 1)
+#pragma unroll
+                        for (int k = 0; k < 16; k++)
+                            b[k] = plus_product(v[k], g[k >> 1], b[k]);
+                    const uint32_t to = lanes + ((uint32_t)(16 * block) << 16) + kParts + 2 * kPartColumns * half;
+                    store_part(to, a);
+                    store_part(to + kPartColumns, b);
                 }
-                store_part(to + 2 * kPartColumns, a);
-                store_part(to + 3 * kPartColumns, b);
-            } else {
+                wait_st();
+                fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    bar_arrive(&C.parts_full[half]);
+            }
+        } else {
+            if (n >= 1) {
+                scan_wait(C, &C.parts_free[0], (n - 1) & 1);
+                scan_wait(C, &C.parts_free[1], (n - 1) & 1);
+            }
+            fence_after();
+#pragma unroll 1
+            for (int block = 0; block < 2; block++) {  // of 16 values
+                const uint32_t to = lanes + ((uint32_t)(16 * block) << 16) + kParts;
+                uint32_t v[16];
+#pragma unroll
+                for (int s = 0; s < kTile / 16; s++)
+                    load_turned(v + 4 * s, from + (((chunk + 2 * block) ^ (lane & 7)) << 4) + s * 2048);
+                if (T.rows < kTile)
+                    keep_rows(v, T.rows);
                 // two rounded parts of the product, whose row (a value's, of 64
                 // tokens: four lanes) is brought below 2^15 by a power of two
                 float top[2] = {0.0f, 0.0f};
@@ -768,18 +804,35 @@ __device__ __forceinline__ void weigh(const ScanPlan &P, ScanControl &C, uint8_t
                 store_part(to, a);
                 store_part(to + kPartColumns, b);
             }
-        }
-        wait_st();
-        fence_before();
-        __syncwarp();
-        if (lane == 0) {
-            if (!kBf16)
+            wait_st();
+            fence_before();
+            __syncwarp();
+            if (lane == 0) {
                 bar_arrive(&C.unit_full[n & 1]);
-            bar_arrive(&C.parts_full);
+                bar_arrive(&C.parts_full[0]);
+                bar_arrive(&C.parts_full[1]);
+            }
         }
-        if (kStatesOnly)
-            continue;
+    }
+}
 
+// Four warps: the weights P = (Q K^T) * decays, of tokens up to the row's own (warp
+// w: rows 16 w .. 16 w + 15).
+template <bool kBf16>
+__device__ __forceinline__ void weigh(const ScanPlan &P, ScanControl &C, uint8_t *mem) {
+    Tiles T(C.item, P.L.block_size);
+    const int lane = threadIdx.x & 31, quarter = (threadIdx.x >> 5) - kFirstWeightWarp;
+    const uint32_t lanes = C.tmem + ((uint32_t)(quarter * 32) << 16);
+    const int ra = quarter * 16 + lane / 4, rb = ra + 8;  // this thread's rows of P
+    uint8_t *const pa = mem + kWeightsAt + ra * 128 + 4 * (lane & 3), *const pb = pa + 8 * 128;
+    while (T.next()) {
+        const uint32_t n = T.n;
+        Decays &D = C.decays[n % kRing];
+        scan_wait(C, &C.decays_full[n % kRing], (n / kRing) & 1);
+        if (T.rows < kTile) {
+            scan_wait(C, &C.full[n % kStages], (n / kStages) & 1);
+            clear_rows(mem + (n % kStages) * kStageBytes + 4 * kPanel, T.rows, threadIdx.x - kFirstWeightWarp * 32);
+        }
         scan_wait(C, &C.score_full, n & 1);
         fence_after();
         const float2 la = D.log[ra], lb = D.log[rb];
@@ -811,46 +864,42 @@ __device__ __forceinline__ void weigh(const ScanPlan &P, ScanControl &C, uint8_t
                 *reinterpret_cast<uint32_t *>(pb + at) = pack<kBf16>(p[i][2] * ub, p[i][3] * ub);
             }
         };
-        if constexpr (kBf16) {
-            if (n >= 1)
-                scan_wait(C, &C.weight_free, (n - 1) & 1);
+        float ua = 1.0f, ub = 1.0f;
+        if constexpr (!kBf16) {
+            // f16 has not binary32's range: a row's weights are brought below 2^15
+            // (made twice: held, they would be 32 registers)
+            float ta = 0.0f, tb = 0.0f;
 #pragma unroll 1
             for (int half = 0; half < halves; half++) {
                 float p[4][4];
                 make(half, p);
-                put(half, p, 1.0f, 1.0f);
+#pragma unroll
+                for (int i = 0; i < 4; i++) {
+                    ta = fmaxf(ta, fmaxf(fabsf(p[i][0]), fabsf(p[i][1])));
+                    tb = fmaxf(tb, fmaxf(fabsf(p[i][2]), fabsf(p[i][3])));
+                }
             }
-            fence_before();
-        } else {
-            // f16 has not binary32's range: a row's weights are brought below 2^15
-            float p[2][4][4], ta = 0.0f, tb = 0.0f;
-            make(0, p[0]);
-            if (halves > 1)
-                make(1, p[1]);
-            fence_before();
-#pragma unroll
-            for (int half = 0; half < 2; half++)
-                if (half < halves)
-#pragma unroll
-                    for (int i = 0; i < 4; i++) {
-                        ta = fmaxf(ta, fmaxf(fabsf(p[half][i][0]), fabsf(p[half][i][1])));
-                        tb = fmaxf(tb, fmaxf(fabsf(p[half][i][2]), fabsf(p[half][i][3])));
-                    }
             for (int o = 1; o < 4; o <<= 1) {
                 ta = fmaxf(ta, __shfl_xor_sync(0xffffffffu, ta, o));
                 tb = fmaxf(tb, __shfl_xor_sync(0xffffffffu, tb, o));
             }
             const int ea = lift_of(ta), eb = lift_of(tb);
+            ua = power(ea);
+            ub = power(eb);
             if ((lane & 3) == 0) {
                 D.lift[ra] = power(-ea) * P.L.scale;
                 D.lift[rb] = power(-eb) * P.L.scale;
             }
-            if (n >= 1)
-                scan_wait(C, &C.weight_free, (n - 1) & 1);
-            put(0, p[0], power(ea), power(eb));
-            if (halves > 1)
-                put(1, p[1], power(ea), power(eb));
         }
+        if (n >= 1)
+            scan_wait(C, &C.weight_free, (n - 1) & 1);
+#pragma unroll 1
+        for (int half = 0; half < halves; half++) {
+            float p[4][4];
+            make(half, p);
+            put(half, p, ua, ub);
+        }
+        fence_before();
         fence_async();
         __syncwarp();
         if (lane == 0) {
@@ -1125,17 +1174,17 @@ __global__ void __launch_bounds__(kScanThreads, 1) lmc_linear_scan_kernel(const 
         for (int i = 0; i < kRing; i++)
             bar_init(&C.decays_full[i], 1);
         for (int i = 0; i < 2; i++) {
-            bar_init(&C.unit_full[i], kWeightWarps);
+            bar_init(&C.unit_full[i], kPartWarps);
             bar_init(&C.lift_full[i], kWeightWarps);
             bar_init(&C.down_full[i], kStateWarps);
             bar_init(&C.ended[i], 1);
+            bar_init(&C.parts_full[i], kPartWarps);
+            bar_init(&C.parts_free[i], 1);
         }
         bar_init(&C.weight_full, kWeightWarps);
         bar_init(&C.weight_free, 1);
         bar_init(&C.score_full, 1);
         bar_init(&C.score_free, kWeightWarps);
-        bar_init(&C.parts_full, kWeightWarps);
-        bar_init(&C.parts_free, 1);
         bar_init(&C.update_full, 1);
         bar_init(&C.update_free, kStateWarps);
         bar_init(&C.state_full, kStateWarps);
@@ -1170,9 +1219,13 @@ __global__ void __launch_bounds__(kScanThreads, 1) lmc_linear_scan_kernel(const 
     if (warp < kStateWarps) {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kStateRegisters));
         carry<kBf16, kStatesOnly>(P, C);
+    } else if (warp < kFirstWeightWarp) {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kPartRegisters));
+        split<kBf16>(P, C, scan_mem);
     } else if (warp < kFirstResultWarp) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kWeightRegisters));
-        weigh<kBf16, kStatesOnly>(P, C, scan_mem);
+        if (!kStatesOnly)
+            weigh<kBf16>(P, C, scan_mem);
     } else if (warp < kLoadWarp) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kResultRegisters));
         if (!kStatesOnly)
