@@ -196,8 +196,8 @@ constexpr int kStateRegisters = 120, kPartRegisters = 88, kWeightRegisters = 56,
 constexpr int kWeightsAt = kStages * kStageBytes, kResultAt = kWeightsAt + kPanel;
 constexpr int kWarpResult = kTile * 64;  // bytes of a warp's part of a result: 32 values of each token
 constexpr int kScanMemory = kResultAt + kResultWarps * kWarpResult;
-constexpr uint32_t kWaitLimit = 1u << 18;  // looks at a barrier, of up to
-constexpr uint32_t kLook = 4000;           // so many ns each
+constexpr int kLooks = 1 << 17;   // at barriers in vain, of up to
+constexpr uint32_t kLook = 20000;  // so many ns each
 // columns of tensor memory
 constexpr uint32_t kScores = 0, kUpdate = 64, kFromState = 192, kFromTile = 256, kState = 320, kParts = 384;
 constexpr uint32_t kPartColumns = kTile / 2;
@@ -226,6 +226,7 @@ struct Item {
     int32_t slot;        // of the segment; -1: the request is not cut
     int32_t ends;        // the request ends with it
     int32_t work;
+    int32_t tiles;
 };
 
 // What a tile's tokens' decays give.
@@ -287,29 +288,29 @@ struct Tiles {
     __device__ __forceinline__ bool last() const { return done + rows == total; }
 };
 
-// Waits for a phase. When the limit runs out the CTA gives up as a whole: no
-// later wait waits, every role runs to its end, and the status word says so.
-// (As few instructions as can be: the loops of all roles together have to stay in
-// the SM's instruction cache. With 110 KB of code instead of 65 the call took 1.5
-// times as long.)
-__device__ __forceinline__ bool bar_try_long(uint64_t *bar, uint32_t parity) {
+// The loops of all roles together have to stay in the SM's instruction cache: from
+// some 40 KB on, instructions come at 0.38 a clock and scheduler (measured with
+// loops of sums), and the call's time doubles. So loops are not unrolled where they
+// need not be, and what is not expected lies behind.
+//
+// Waits for a phase. Each role has so many looks to waste altogether (each of up to
+// kLook ns; hardly any wait takes two). When they run out it waits no more, runs to
+// its end, and says so: no more copies are asked for, and the status word tells.
+__device__ __forceinline__ void scan_wait(ScanControl &C, uint64_t *bar, uint32_t parity, int &looks) {
     uint32_t done;
-    asm volatile(
-        "{\n\t.reg .pred p;\n\t"
-        "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-        "selp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(done)
-        : "r"(smem_addr(bar)), "r"(parity), "r"(kLook)
-        : "memory");
-    return done != 0;
-}
-
-__device__ __forceinline__ void scan_wait(ScanControl &C, uint64_t *bar, uint32_t parity) {
-    for (uint32_t i = 1; !bar_try_long(bar, parity); i++)
-        if ((i & 15u) == 0 && (i > kWaitLimit || *(volatile uint32_t *)&C.gave_up)) {
+    do {
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(done)
+            : "r"(smem_addr(bar)), "r"(parity), "r"(kLook)
+            : "memory");
+        if (done == 0 && --looks < 0) {
             *(volatile uint32_t *)&C.gave_up = 1;
             return;
         }
+    } while (done == 0);
 }
 
 __device__ __forceinline__ bool scan_gone(ScanControl &C) {
@@ -436,6 +437,10 @@ __device__ __forceinline__ void find_item(const ScanPlan &P, Item &I) {
             J.slot = n > 1 ? (int)(slot + i) : -1;
             J.ends = i == n - 1;
             J.work = 1;
+            // tiles of the first block, of whole ones, and of the last
+            const int N = P.L.block_size, head = min(J.count, N - J.phase), rest = J.count - head;
+            auto tiles = [](int tokens) { return (tokens + kTile - 1) / kTile; };
+            J.tiles = tiles(head) + rest / N * tiles(N) + tiles(rest % N);
         }
     }
     if (lane == 0)
@@ -501,7 +506,7 @@ __device__ __forceinline__ void sum_decays(Decays &D, float g0, float g1, int ro
         const float high = 1.0f + less;
         const float low = fmaf(high, drift, less - (high - 1.0f));
         grow = high + low;
-        drift = ((high - grow) + low) / grow;
+        drift = __fdividef((high - grow) + low, grow);
     } else {
         grow = exp2_fast(x);
         drift = 0.0f;
@@ -514,6 +519,7 @@ __device__ __forceinline__ void sum_decays(Decays &D, float g0, float g1, int ro
 // tile's last one come along; they are not read into a result.)
 template <bool kBf16, bool kStatesOnly>
 __device__ __forceinline__ void load_tiles(const ScanPlan &P, ScanControl &C, uint8_t *mem) {
+    int looks = kLooks;
     Tiles T(C.item, P.L.block_size);
     const int lane = threadIdx.x & 31, h = C.item.h, kh = h / P.L.shared;
     const uint32_t bytes = (uint32_t)((kStatesOnly ? 1 : 2) * P.k_panels + P.v_panels) * kPanel;
@@ -544,7 +550,7 @@ __device__ __forceinline__ void load_tiles(const ScanPlan &P, ScanControl &C, ui
         }
         // (behind the last tile, too: its decays' place has to be free)
         if (asked >= kStages)
-            scan_wait(C, &C.free[st], (asked / kStages - 1) & 1);
+            scan_wait(C, &C.free[st], (asked / kStages - 1) & 1, looks);
         if (more) {
             more = !scan_gone(C);
             uint8_t *to = mem + st * kStageBytes;
@@ -581,48 +587,45 @@ __device__ __forceinline__ void load_tiles(const ScanPlan &P, ScanControl &C, ui
 // what the tile adds to the state, turned: (V decayed)^T K [values x keys].
 template <bool kBf16, bool kStatesOnly>
 __device__ __forceinline__ void multiply_forward(const ScanPlan &P, ScanControl &C, uint8_t *mem) {
-    Tiles T(C.item, P.L.block_size);
+    int looks = kLooks;
     const uint32_t tmem = uniform(C.tmem);
-    const int keys = 64 * P.k_panels, steps = (P.L.dk + 15) / 16;
+    const int keys = 64 * P.k_panels, steps = (P.L.dk + 15) / 16, tiles = (int)uniform(C.item.tiles);
     const uint32_t scores = instruction(kBf16, false, 64, kTile);
     const uint32_t update = instruction(kBf16, false, 128, keys) | 1u << 16;  // B turned
-    constexpr int kHalf = kBf16 ? 2 : 1;
-    while (T.next()) {
-        const uint32_t n = T.n;
-        const int st = (int)uniform(n % kStages);
-        const uint32_t at = smem_addr(mem) + st * kStageBytes;
-        scan_wait(C, &C.full[st], (n / kStages) & 1);
+    constexpr int kSteps = (kBf16 ? 2 : 1) * (kTile / 16);  // of a half of the parts
+    const uint64_t q0 = matrix(smem_addr(mem), 16, 1024);
+    const uint64_t k0 = matrix(smem_addr(mem) + 2 * kPanel, kPanel, 1024);
+#pragma unroll 1
+    for (int n = 0; n < tiles; n++) {
+        const int st = n % kStages, stage = st * (kStageBytes >> 4);
+        scan_wait(C, &C.full[st], (n / kStages) & 1, looks);
         if (!kStatesOnly) {
             if (n >= 1)
-                scan_wait(C, &C.score_free, (n - 1) & 1);
+                scan_wait(C, &C.score_free, (n - 1) & 1, looks);
             __syncwarp();
             fence_after();
             if (elect()) {
-                const uint64_t q = matrix(at, 16, 1024), k = matrix(at + 2 * kPanel, 16, 1024);
 #pragma unroll 1
-                for (int s = 0; s < steps; s++)
-                    mma(tmem + kScores, q + (s >> 2) * (kPanel >> 4) + (s & 3) * 2, k + (s >> 2) * (kPanel >> 4) + (s & 3) * 2,
-                        scores, s > 0);
+                for (int s = 0; s < steps; s++) {
+                    const uint64_t q = q0 + (stage + (s >> 2) * (kPanel >> 4) + (s & 3) * 2);
+                    mma(tmem + kScores, q, q + (2 * kPanel >> 4), scores, s > 0);
+                }
                 commit(&C.score_full);
             }
             __syncwarp();
         }
         // as the parts come: the upper one or two, then the lower
-        const uint64_t k = matrix(at + 2 * kPanel, kPanel, 1024);
         if (n >= 1)
-            scan_wait(C, &C.update_free, (n - 1) & 1);
+            scan_wait(C, &C.update_free, (n - 1) & 1, looks);
 #pragma unroll 1
         for (int half = 0; half < 2; half++) {
-            scan_wait(C, &C.parts_full[half], n & 1);
+            scan_wait(C, &C.parts_full[half], n & 1, looks);
             __syncwarp();
             fence_after();
             if (elect()) {
 #pragma unroll 1
-                for (int part = kHalf * half; part < kHalf * (half + 1); part++)
-#pragma unroll
-                    for (int s = 0; s < kTile / 16; s++)
-                        mma_held(tmem + kUpdate, tmem + kParts + part * kPartColumns + 8 * s, k + s * (2048 >> 4), update,
-                                 part > 0 || s > 0);
+                for (int s = kSteps * half; s < kSteps * (half + 1); s++)
+                    mma_held(tmem + kUpdate, tmem + kParts + 8 * s, k0 + (stage + (s & 3) * (2048 >> 4)), update, s > 0);
                 commit(&C.parts_free[half]);
                 if (half == 1) {
                     commit(&C.update_full);
@@ -638,37 +641,37 @@ __device__ __forceinline__ void multiply_forward(const ScanPlan &P, ScanControl 
 // before the tile, V^T P^T from the tile's own tokens [values x tokens].
 template <bool kBf16>
 __device__ __forceinline__ void multiply_state(const ScanPlan &P, ScanControl &C, uint8_t *mem) {
-    Tiles T(C.item, P.L.block_size);
+    int looks = kLooks;
     const uint32_t tmem = uniform(C.tmem);
-    const int steps = (P.L.dk + 15) / 16;
+    const int steps = (P.L.dk + 15) / 16, tiles = (int)uniform(C.item.tiles);
     const uint32_t from_state = instruction(kBf16, false, 128, kTile), from_tile = instruction(kBf16, true, 128, kTile);
     const uint64_t weight = matrix(smem_addr(mem) + kWeightsAt, 16, 1024);
-    while (T.next()) {
-        const uint32_t n = T.n;
-        const int st = (int)uniform(n % kStages);
-        const uint32_t at = smem_addr(mem) + st * kStageBytes;
-        scan_wait(C, &C.full[st], (n / kStages) & 1);
-        scan_wait(C, &C.state_full, n & 1);
+    const uint64_t q0 = matrix(smem_addr(mem), 16, 1024);
+    const uint64_t v0 = matrix(smem_addr(mem) + 4 * kPanel, kPanel, 1024);
+#pragma unroll 1
+    for (int n = 0; n < tiles; n++) {
+        const int st = n % kStages, stage = st * (kStageBytes >> 4);
+        scan_wait(C, &C.full[st], (n / kStages) & 1, looks);
+        scan_wait(C, &C.state_full, n & 1, looks);
         if (n >= 1)
-            scan_wait(C, &C.out_free, (n - 1) & 1);
+            scan_wait(C, &C.out_free, (n - 1) & 1, looks);
         __syncwarp();
         fence_after();
         if (elect()) {
-            const uint64_t q = matrix(at, 16, 1024);
 #pragma unroll 1
             for (int s = 0; s < steps; s++)
-                mma_held(tmem + kFromState, tmem + kState + 8 * s, q + (s >> 2) * (kPanel >> 4) + (s & 3) * 2, from_state, s > 0);
+                mma_held(tmem + kFromState, tmem + kState + 8 * s, q0 + (stage + (s >> 2) * (kPanel >> 4) + (s & 3) * 2),
+                         from_state, s > 0);
             commit(&C.state_free);
         }
         __syncwarp();
-        scan_wait(C, &C.weight_full, n & 1);
+        scan_wait(C, &C.weight_full, n & 1, looks);
         __syncwarp();
         fence_after();
         if (elect()) {
-            const uint64_t v = matrix(at + 4 * kPanel, kPanel, 1024);
-#pragma unroll
+#pragma unroll 1
             for (int s = 0; s < kTile / 16; s++)
-                mma(tmem + kFromTile, v + s * (2048 >> 4), weight + s * 2, from_tile, s > 0);
+                mma(tmem + kFromTile, v0 + (stage + s * (2048 >> 4)), weight + s * 2, from_tile, s > 0);
             commit(&C.out_full);
             commit(&C.weight_free);
             commit(&C.free[st]);
@@ -698,6 +701,7 @@ __device__ __forceinline__ void keep_rows(uint32_t (&v)[16], int rows) {
 // (three truncated parts of a binary32 product are fifteen).
 template <bool kBf16>
 __device__ __forceinline__ void split(const ScanPlan &P, ScanControl &C, uint8_t *mem) {
+    int looks = kLooks;
     Tiles T(C.item, P.L.block_size);
     const int lane = threadIdx.x & 31, quarter = (threadIdx.x >> 5) - kFirstPartWarp;
     const uint32_t lanes = C.tmem + ((uint32_t)(quarter * 32) << 16);
@@ -709,8 +713,8 @@ __device__ __forceinline__ void split(const ScanPlan &P, ScanControl &C, uint8_t
         const uint32_t n = T.n;
         const int st = n % kStages;
         Decays &D = C.decays[n % kRing];
-        scan_wait(C, &C.decays_full[n % kRing], (n / kRing) & 1);
-        scan_wait(C, &C.full[st], (n / kStages) & 1);
+        scan_wait(C, &C.decays_full[n % kRing], (n / kRing) & 1, looks);
+        scan_wait(C, &C.full[st], (n / kStages) & 1, looks);
         if (T.rows < kTile) {  // the products' other side
             clear_rows(mem + st * kStageBytes + 2 * kPanel, T.rows, threadIdx.x - kFirstPartWarp * 32);
             fence_async();
@@ -729,7 +733,7 @@ __device__ __forceinline__ void split(const ScanPlan &P, ScanControl &C, uint8_t
                     f[i] = x.x, g[i] = x.y;
                 }
                 if (n >= 1)
-                    scan_wait(C, &C.parts_free[half], (n - 1) & 1);
+                    scan_wait(C, &C.parts_free[half], (n - 1) & 1, looks);
                 fence_after();
 #pragma unroll 1
                 for (int block = 0; block < 2; block++) {  // of 16 values
@@ -760,8 +764,8 @@ __device__ __forceinline__ void split(const ScanPlan &P, ScanControl &C, uint8_t
             }
         } else {
             if (n >= 1) {
-                scan_wait(C, &C.parts_free[0], (n - 1) & 1);
-                scan_wait(C, &C.parts_free[1], (n - 1) & 1);
+                scan_wait(C, &C.parts_free[0], (n - 1) & 1, looks);
+                scan_wait(C, &C.parts_free[1], (n - 1) & 1, looks);
             }
             fence_after();
 #pragma unroll 1
@@ -820,6 +824,7 @@ __device__ __forceinline__ void split(const ScanPlan &P, ScanControl &C, uint8_t
 // w: rows 16 w .. 16 w + 15).
 template <bool kBf16>
 __device__ __forceinline__ void weigh(const ScanPlan &P, ScanControl &C, uint8_t *mem) {
+    int looks = kLooks;
     Tiles T(C.item, P.L.block_size);
     const int lane = threadIdx.x & 31, quarter = (threadIdx.x >> 5) - kFirstWeightWarp;
     const uint32_t lanes = C.tmem + ((uint32_t)(quarter * 32) << 16);
@@ -828,12 +833,12 @@ __device__ __forceinline__ void weigh(const ScanPlan &P, ScanControl &C, uint8_t
     while (T.next()) {
         const uint32_t n = T.n;
         Decays &D = C.decays[n % kRing];
-        scan_wait(C, &C.decays_full[n % kRing], (n / kRing) & 1);
+        scan_wait(C, &C.decays_full[n % kRing], (n / kRing) & 1, looks);
         if (T.rows < kTile) {
-            scan_wait(C, &C.full[n % kStages], (n / kStages) & 1);
+            scan_wait(C, &C.full[n % kStages], (n / kStages) & 1, looks);
             clear_rows(mem + (n % kStages) * kStageBytes + 4 * kPanel, T.rows, threadIdx.x - kFirstWeightWarp * 32);
         }
-        scan_wait(C, &C.score_full, n & 1);
+        scan_wait(C, &C.score_full, n & 1, looks);
         fence_after();
         const float2 la = D.log[ra], lb = D.log[rb];
         // tokens behind the rows' own: 0 from the start
@@ -892,7 +897,7 @@ __device__ __forceinline__ void weigh(const ScanPlan &P, ScanControl &C, uint8_t
             }
         }
         if (n >= 1)
-            scan_wait(C, &C.weight_free, (n - 1) & 1);
+            scan_wait(C, &C.weight_free, (n - 1) & 1, looks);
 #pragma unroll 1
         for (int half = 0; half < halves; half++) {
             float p[4][4];
@@ -915,6 +920,7 @@ __device__ __forceinline__ void weigh(const ScanPlan &P, ScanControl &C, uint8_t
 // .. 32 w + 31 (a lane each), w the first 64 keys, w + 4 the others.
 template <bool kBf16, bool kStatesOnly>
 __device__ __forceinline__ void carry(const ScanPlan &P, ScanControl &C) {
+    int looks = kLooks;
     Tiles T(C.item, P.L.block_size);
     const LinearPlan &L = P.L;
     const Item &I = C.item;
@@ -1008,14 +1014,14 @@ __device__ __forceinline__ void carry(const ScanPlan &P, ScanControl &C) {
         if (!kStatesOnly && (T.block_ends || (I.ends && T.last())))
             block = __ldca(L.table + I.r * L.row_stride + T.page);
 
-        scan_wait(C, &C.decays_full[n % kRing], (n / kRing) & 1);
+        scan_wait(C, &C.decays_full[n % kRing], (n / kRing) & 1, looks);
         const float grow = D.grow;
         if (kStatesOnly)
             total += D.log[kTile - 1].x + D.log[kTile - 1].y;
         if (!kBf16)
-            scan_wait(C, &C.unit_full[n & 1], (n >> 1) & 1);
+            scan_wait(C, &C.unit_full[n & 1], (n >> 1) & 1, looks);
         const float unit = kBf16 ? 1.0f : D.unit[j];
-        scan_wait(C, &C.update_full, n & 1);
+        scan_wait(C, &C.update_full, n & 1, looks);
         fence_after();
         if (mine) {
 #pragma unroll
@@ -1039,7 +1045,7 @@ __device__ __forceinline__ void carry(const ScanPlan &P, ScanControl &C) {
             atomicOr(L.status, LMC_ST_BLOCK_OOR);
         __syncwarp();
         if (!kStatesOnly && !T.last()) {
-            scan_wait(C, &C.state_free, n & 1);
+            scan_wait(C, &C.state_free, n & 1, looks);
             fence_after();
             hand_over(n + 1);
         }
@@ -1054,6 +1060,7 @@ __device__ __forceinline__ void carry(const ScanPlan &P, ScanControl &C) {
 // Four warps: the result of each tile. Warp w takes values 32 w .. 32 w + 31.
 template <bool kBf16>
 __device__ __forceinline__ void deliver(const ScanPlan &P, ScanControl &C, uint8_t *mem) {
+    int looks = kLooks;
     Tiles T(C.item, P.L.block_size);
     const LinearPlan &L = P.L;
     const int lane = threadIdx.x & 31, quarter = (threadIdx.x >> 5) - kFirstResultWarp;
@@ -1068,12 +1075,12 @@ __device__ __forceinline__ void deliver(const ScanPlan &P, ScanControl &C, uint8
     while (T.next()) {
         const uint32_t n = T.n;
         const Decays &D = C.decays[n % kRing];
-        scan_wait(C, &C.decays_full[n % kRing], (n / kRing) & 1);
+        scan_wait(C, &C.decays_full[n % kRing], (n / kRing) & 1, looks);
         if (!kBf16) {
-            scan_wait(C, &C.lift_full[n & 1], (n >> 1) & 1);
-            scan_wait(C, &C.down_full[n & 1], (n >> 1) & 1);
+            scan_wait(C, &C.lift_full[n & 1], (n >> 1) & 1, looks);
+            scan_wait(C, &C.down_full[n & 1], (n >> 1) & 1, looks);
         }
-        scan_wait(C, &C.out_full, n & 1);
+        scan_wait(C, &C.out_full, n & 1, looks);
         fence_after();
         float2 since[4];
 #pragma unroll 1
@@ -1123,7 +1130,7 @@ __device__ __forceinline__ void deliver(const ScanPlan &P, ScanControl &C, uint8
             const int v = 8 * (lane & 3), t0 = lane >> 2;
             uint16_t *out = L.out + ((int64_t)T.row + t0) * L.out_row + out_at + v;
             const bool inside = quarter * 32 + v < L.dv;
-#pragma unroll 2
+#pragma unroll 1
             for (int i = 0; i < 8; i++) {
                 const int t = 8 * i + t0;
                 const uint4 x = *reinterpret_cast<const uint4 *>(mine + t * 64 + (((lane & 3) ^ (t >> 1 & 3)) << 4));
@@ -1144,7 +1151,7 @@ __device__ __forceinline__ void deliver(const ScanPlan &P, ScanControl &C, uint8
 // A CTA that gave up: what it left running ends (or the limit runs out) before
 // its memory goes to another.
 __device__ __forceinline__ void scan_outlast(uint64_t *bar, uint32_t parity) {
-    for (uint32_t i = 0; i < kWaitLimit && !bar_try(bar, parity); i++) {
+    for (uint32_t i = 0; i < (1u << 22) && !bar_try(bar, parity); i++) {
     }
 }
 
