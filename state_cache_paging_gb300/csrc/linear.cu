@@ -187,7 +187,7 @@ constexpr int kStateWarps = 8;
 constexpr int kFirstPartWarp = 8, kPartWarps = 4;
 constexpr int kFirstWeightWarp = 12, kWeightWarps = 4;
 constexpr int kFirstResultWarp = 16, kResultWarps = 4;
-constexpr int kLoadWarp = 20, kForwardWarp = 21, kStateProductWarp = 22;
+constexpr int kLoadWarp = 20, kForwardWarp = 21, kStateProductWarp = 22, kDecayWarp = 23;
 constexpr int kScanThreads = 24 * 32;
 // Registers per thread of the warpgroups: 2 x 120 + 88 + 56 + 56 + 40 of the 6 x 80
 // the CTA starts with.
@@ -201,6 +201,7 @@ constexpr uint32_t kLook = 20000;  // so many ns each
 // columns of tensor memory
 constexpr uint32_t kScores = 0, kUpdate = 64, kFromState = 192, kFromTile = 256, kState = 320, kParts = 384;
 constexpr uint32_t kPartColumns = kTile / 2;
+constexpr int kDecaysAhead = 4 * kTile;  // tokens whose decays are sent on to L2
 constexpr int kRing = 4;              // tiles whose decays are at hand
 constexpr int kSms = 152;
 constexpr int64_t kLeastSegment = 512;  // tokens
@@ -234,7 +235,7 @@ struct alignas(16) Decays {
     float2 log[kTile];      // sum up to and with the token, in units of log 2 (high, low)
     uint4 left[kTile / 2];  // from the token to the tile's end, two tokens: the first of three bf16 parts, twice, the others; or (f16) as it is
     float since[kTile];     // from the tile's start up to the token, times the call's scale
-    float lift[kTile];      // f16: what the token's weights were divided by, times the scale
+    float lift[kTile];      // f16: what the token's weights were divided by
     float unit[kMaxDim];    // f16: what a value's row of v times its decay was divided by
     float grow;             // decay over the tile
 };
@@ -335,6 +336,14 @@ __device__ __forceinline__ void clear_rows(uint8_t *panels, int rows, int tid) {
     for (int c = tid; c < 2 * (kPanel / 16); c += 128)
         if ((c >> 3 & (kTile - 1)) >= rows)
             *reinterpret_cast<uint4 *>(panels + c * 16) = make_uint4(0, 0, 0, 0);
+}
+
+// 16 lanes x 16 columns, as load_s.
+__device__ __forceinline__ void load_s8(uint32_t (&s)[8], uint32_t addr) {
+    asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(s[0]), "=r"(s[1]), "=r"(s[2]), "=r"(s[3]), "=r"(s[4]), "=r"(s[5]), "=r"(s[6]), "=r"(s[7])
+                 : "r"(addr)
+                 : "memory");
 }
 
 // Four 8 x 8 matrices of 16 bits, turned: a lane gives one of their rows'
@@ -447,40 +456,48 @@ __device__ __forceinline__ void find_item(const ScanPlan &P, Item &I) {
         I = J;
 }
 
-// A tile's decays, by one warp: lane l's are those of tokens 2 l and 2 l + 1.
-// They are summed as whole numbers of 2^-40 (exactly, in any order), so sums far
-// from 0 lose nothing of the differences that count.
+// A sum held in two numbers, its error in the lower (Knuth's two-sum; exact but for
+// the lower ones' own rounding, 2^-48 of the sum).
+struct Twice {
+    float high, low;
+};
+__device__ __forceinline__ Twice plus(const Twice &x, float high, float low) {
+    const float s = x.high + high, part = s - x.high;
+    return Twice{s, (x.high - (s - part)) + (high - part) + (x.low + low)};
+}
+
+// A tile's decays, by one warp: lane l's are those of tokens 2 l and 2 l + 1. Their
+// sums are held twice as long as binary32, so that sums far from 0 lose nothing of
+// the differences that count. (As whole numbers of 64 bits their conversions, on
+// the unit for 64-bit floating point, took 2500 clocks a tile.)
 // `drift`: how much the tiles' rounded decays lack of the exact ones so far,
 // relatively; a tile's makes up for it, so that a state that decays slowly by
 // the same factor tile after tile keeps its digits.
 template <bool kBf16>
 __device__ __forceinline__ void sum_decays(Decays &D, float g0, float g1, int rows, float scale, float &drift) {
     const int lane = threadIdx.x & 31;
-    const float nan = __int_as_float(0x7fffffff);
+    // a NaN makes one of everything behind it
     const uint32_t bad0 = __ballot_sync(0xffffffffu, g0 != g0), bad1 = __ballot_sync(0xffffffffu, g1 != g1);
-    const int first_bad = min(bad0 ? 2 * (__ffs(bad0) - 1) : kTile, bad1 ? 2 * (__ffs(bad1) - 1) + 1 : kTile);
-    auto whole = [](float g) {
-        return __float2ll_rn(fminf(fmaxf(g, kLeastDecay), -kLeastDecay) * 1.44269504088896340736f * 0x1p40f);
-    };
-    const long long a = whole(g0), b = whole(g1);
-    long long sum = a + b;
+    const float nan = __int_as_float(0x7fffffff);
+    auto log2_of = [](float g) { return fminf(fmaxf(g, kLeastDecay), -kLeastDecay) * 1.44269504088896340736f; };
+    const float a = log2_of(g0), b = log2_of(g1);
+    Twice sum = plus(Twice{a, 0.0f}, b, 0.0f);
 #pragma unroll 1
     for (int o = 1; o < 32; o <<= 1) {
-        const long long x = __shfl_up_sync(0xffffffffu, sum, o);
+        const float high = __shfl_up_sync(0xffffffffu, sum.high, o), low = __shfl_up_sync(0xffffffffu, sum.low, o);
         if (lane >= o)
-            sum += x;
+            sum = plus(sum, high, low);
     }
-    const long long total = __shfl_sync(0xffffffffu, sum, 31);
+    const Twice total = {__shfl_sync(0xffffffffu, sum.high, 31), __shfl_sync(0xffffffffu, sum.low, 31)};
+    const Twice first = plus(sum, -b, 0.0f);
 #pragma unroll
     for (int i = 0; i < 2; i++) {
-        const int t = 2 * lane + i;
-        const long long g = i ? sum : sum - b;
-        const float high = (float)g, low = (float)(g - (long long)high);
-        D.log[t] = t < first_bad ? make_float2(high * 0x1p-40f, low * 0x1p-40f) : make_float2(nan, nan);
-        D.since[t] = t < first_bad ? exp2_fast(high * 0x1p-40f) * scale : nan;
+        const Twice &g = i ? sum : first;
+        D.log[2 * lane + i] = make_float2(g.high, g.low);
+        D.since[2 * lane + i] = exp2_fast(g.high + g.low) * scale;
     }
-    const float f0 = 2 * lane < rows ? exp2_fast((float)(total - (sum - b)) * 0x1p-40f) : 0.0f;
-    const float f1 = 2 * lane + 1 < rows ? exp2_fast((float)(total - sum) * 0x1p-40f) : 0.0f;
+    const float f0 = 2 * lane < rows ? exp2_fast((total.high - first.high) + (total.low - first.low)) : 0.0f;
+    const float f1 = 2 * lane + 1 < rows ? exp2_fast((total.high - sum.high) + (total.low - sum.low)) : 0.0f;
     if constexpr (kBf16) {
         const uint32_t p = pack<true>(f0, f1);
         const float r0 = f0 - from_q(p & 0xffff, true), r1 = f1 - from_q(p >> 16, true);
@@ -489,7 +506,7 @@ __device__ __forceinline__ void sum_decays(Decays &D, float g0, float g1, int ro
     } else {
         D.left[lane] = make_uint4(__float_as_uint(f0), __float_as_uint(f1), 0, 0);
     }
-    const float x = (float)total * 0x1p-40f;
+    const float x = total.high + total.low;
     float grow;
     if (x > -0.7f && x < 0.7f) {
         // exp(y) - 1 by its series: |y| < 0.486, what is left out is below 2^-29 of y
@@ -512,75 +529,102 @@ __device__ __forceinline__ void sum_decays(Decays &D, float g0, float g1, int ro
         drift = 0.0f;
     }
     if (lane == 0)
-        D.grow = first_bad < kTile ? nan : grow;
+        D.grow = grow;
+    if (__builtin_expect((bad0 | bad1) != 0, 0)) {
+        const int start = min(bad0 ? 2 * (__ffs(bad0) - 1) : kTile, bad1 ? 2 * (__ffs(bad1) - 1) + 1 : kTile);
+#pragma unroll 1
+        for (int t = 2 * lane; t < 2 * lane + 2; t++)
+            if (t >= start) {
+                D.log[t] = make_float2(nan, nan);
+                D.since[t] = nan;
+            }
+        if (lane == 0)
+            D.grow = nan;
+    }
 }
 
-// One warp: q, k and v of each tile by TMA, and its decays. (Rows behind a
-// tile's last one come along; they are not read into a result.)
-template <bool kBf16, bool kStatesOnly>
+// One warp: q, k and v of each tile by TMA. (Rows behind a tile's last one come
+// along; they are not read into a result.)
+template <bool kStatesOnly>
 __device__ __forceinline__ void load_tiles(const ScanPlan &P, ScanControl &C, uint8_t *mem) {
     int looks = kLooks;
     Tiles T(C.item, P.L.block_size);
-    const int lane = threadIdx.x & 31, h = C.item.h, kh = h / P.L.shared;
+    const int h = C.item.h, kh = h / P.L.shared;
     const uint32_t bytes = (uint32_t)((kStatesOnly ? 1 : 2) * P.k_panels + P.v_panels) * kPanel;
-    const float *const decay = P.L.decay + (int64_t)h * P.L.decay_head;
     uint32_t asked = 0;
-    float drift = 0.0f, h0 = 0.0f, h1 = 0.0f;  // the tile before's decays,
-    int rows = 0;                              // and rows
-    // A tile's decays go to its place of the ring when the next tile's stage is
-    // free: the products of that stage's last tile are done, so the result of the
-    // tile before it has been read, whose place this was.
+    while (T.next()) {
+        const int st = (int)uniform(asked % kStages);
+        if (asked >= kStages)
+            scan_wait(C, &C.free[st], (asked / kStages - 1) & 1, looks);
+        if (scan_gone(C))
+            break;
+        uint8_t *to = mem + st * kStageBytes;
+        const int row = (int)uniform(T.row);
+        if (elect()) {
+            uint64_t *bar = &C.full[st];
+            bar_expect(bar, bytes);
+#pragma unroll 1
+            for (int i = 0; i < P.k_copies; i++)
+                tma_box(&P.k, to + 2 * kPanel + i * kPanel, i * 64, row, kh, bar);
+#pragma unroll 1
+            for (int i = 0; i < P.v_copies; i++)
+                tma_box(&P.v, to + 4 * kPanel + i * kPanel, i * 64, row, h, bar);
+            if (!kStatesOnly) {
+#pragma unroll 1
+                for (int i = 0; i < P.k_copies; i++)
+                    tma_box(&P.q, to + i * kPanel, i * 64, row, kh, bar);
+            }
+        }
+        __syncwarp();
+        asked++;
+    }
+    if ((threadIdx.x & 31) == 0)
+        C.tiles = asked;
+}
+
+// One warp: each tile's decays. They go to their place of the ring when the stage
+// of the tile behind is free: the products of that stage's last tile are done, so
+// the result of the tile before it has been read, whose place this was.
+template <bool kBf16>
+__device__ __forceinline__ void tell_decays(const ScanPlan &P, ScanControl &C) {
     static_assert(kRing >= kStages, "a place is read until the next tile's result is made");
-    auto tell = [&](uint32_t n) {
-        sum_decays<kBf16>(C.decays[n % kRing], h0, h1, rows, P.L.scale, drift);
+    int looks = kLooks;
+    Tiles T(C.item, P.L.block_size), ahead(C.item, P.L.block_size);
+    const int lane = threadIdx.x & 31;
+    const float *const decay = P.L.decay + (int64_t)C.item.h * P.L.decay_head;
+    float drift = 0.0f, g0, g1;
+    // (sent on to L2 some tiles before: under load HBM takes longer than a tile)
+    const int end = C.item.row + C.item.count;
+    auto send = [&](int row) {
+        if (row < end)
+            asm volatile("prefetch.global.L2 [%0];" ::"l"(decay + (int64_t)row * P.L.decay_row) : "memory");
+    };
+    for (int t = lane; t < kDecaysAhead; t += 32)
+        send(C.item.row + t);
+    auto fetch = [&] {
+        g0 = g1 = 0.0f;
+        if (ahead.next()) {
+            send(ahead.row + kDecaysAhead + lane);
+            send(ahead.row + kDecaysAhead + 32 + lane);
+            const float *const at = decay + ((int64_t)ahead.row + 2 * lane) * P.L.decay_row;
+            if (2 * lane < ahead.rows)
+                g0 = *at;
+            if (2 * lane + 1 < ahead.rows)
+                g1 = at[P.L.decay_row];
+        }
+    };
+    fetch();
+    while (T.next()) {
+        const uint32_t n = T.n;
+        const float h0 = g0, h1 = g1;
+        fetch();
+        if (n + 1 >= kStages)
+            scan_wait(C, &C.free[(n + 1) % kStages], ((n + 1) / kStages - 1) & 1, looks);
+        sum_decays<kBf16>(C.decays[n % kRing], h0, h1, T.rows, P.L.scale, drift);
         __syncwarp();
         if (lane == 0)
             bar_arrive(&C.decays_full[n % kRing]);
-    };
-    for (bool more = true; more;) {
-        more = T.next();
-        float g0 = 0.0f, g1 = 0.0f;
-        const int st = (int)uniform(asked % kStages);
-        if (more) {
-            const float *const at = decay + ((int64_t)T.row + 2 * lane) * P.L.decay_row;
-            if (2 * lane < T.rows)
-                g0 = *at;
-            if (2 * lane + 1 < T.rows)
-                g1 = at[P.L.decay_row];
-        }
-        // (behind the last tile, too: its decays' place has to be free)
-        if (asked >= kStages)
-            scan_wait(C, &C.free[st], (asked / kStages - 1) & 1, looks);
-        if (more) {
-            more = !scan_gone(C);
-            uint8_t *to = mem + st * kStageBytes;
-            const int row0 = (int)uniform(T.row);
-            if (more && elect()) {
-                uint64_t *bar = &C.full[st];
-                bar_expect(bar, bytes);
-#pragma unroll 1
-                for (int i = 0; i < P.k_copies; i++)
-                    tma_box(&P.k, to + 2 * kPanel + i * kPanel, i * 64, row0, kh, bar);
-#pragma unroll 1
-                for (int i = 0; i < P.v_copies; i++)
-                    tma_box(&P.v, to + 4 * kPanel + i * kPanel, i * 64, row0, h, bar);
-                if (!kStatesOnly) {
-#pragma unroll 1
-                    for (int i = 0; i < P.k_copies; i++)
-                        tma_box(&P.q, to + i * kPanel, i * 64, row0, kh, bar);
-                }
-            }
-            __syncwarp();
-        }
-        if (asked > 0)
-            tell(asked - 1);
-        asked += more;
-        h0 = g0;
-        h1 = g1;
-        rows = T.rows;
     }
-    if (lane == 0)
-        C.tiles = asked;
 }
 
 // One warp: the products that need no state. Scores Q K^T [tokens x tokens], and
@@ -623,7 +667,7 @@ __device__ __forceinline__ void multiply_forward(const ScanPlan &P, ScanControl 
             __syncwarp();
             fence_after();
             if (elect()) {
-#pragma unroll 1
+#pragma unroll 4
                 for (int s = kSteps * half; s < kSteps * (half + 1); s++)
                     mma_held(tmem + kUpdate, tmem + kParts + 8 * s, k0 + (stage + (s & 3) * (2048 >> 4)), update, s > 0);
                 commit(&C.parts_free[half]);
@@ -841,32 +885,25 @@ __device__ __forceinline__ void weigh(const ScanPlan &P, ScanControl &C, uint8_t
         scan_wait(C, &C.score_full, n & 1, looks);
         fence_after();
         const float2 la = D.log[ra], lb = D.log[rb];
-        // tokens behind the rows' own: 0 from the start
-        const int halves = 1 + (quarter >> 1);
-        // 32 tokens' weights of the thread's rows: (ra, c), (ra, c + 1), (rb, c), (rb, c
-        // + 1) with c = 32 half + 8 i + 2 (lane % 4)
-        auto make = [&](int half, float (&p)[4][4]) {
-            uint32_t raw[16];
-            load_s(raw, lanes + kScores + 32 * half);
+        // 16 tokens' weights of the thread's rows at a time, up to the rows' own (the
+        // others are 0 from the start): (ra, c), (ra, c + 1), (rb, c), (rb, c + 1) with
+        // c = 16 u + 8 i + 2 (lane % 4)
+        auto make = [&](int u, float (&p)[2][4]) {
+            uint32_t raw[8];
+            load_s8(raw, lanes + kScores + 16 * u);
             wait_ld();
 #pragma unroll
-            for (int i = 0; i < 4; i++) {
-                const int c = 32 * half + 8 * i + 2 * (lane & 3);
+            for (int i = 0; i < 2; i++) {
+                const int c = 16 * u + 8 * i + 2 * (lane & 3);
                 const float4 lc = *reinterpret_cast<const float4 *>(&D.log[c]);
                 const float w0 = exp2_fast((la.x - lc.x) + (la.y - lc.y)), w1 = exp2_fast((la.x - lc.z) + (la.y - lc.w));
                 const float w2 = exp2_fast((lb.x - lc.x) + (lb.y - lc.y)), w3 = exp2_fast((lb.x - lc.z) + (lb.y - lc.w));
-                p[i][0] = c <= ra ? __uint_as_float(raw[4 * i]) * w0 : 0.0f;
-                p[i][1] = c < ra ? __uint_as_float(raw[4 * i + 1]) * w1 : 0.0f;
-                p[i][2] = c <= rb ? __uint_as_float(raw[4 * i + 2]) * w2 : 0.0f;
-                p[i][3] = c < rb ? __uint_as_float(raw[4 * i + 3]) * w3 : 0.0f;
-            }
-        };
-        auto put = [&](int half, const float (&p)[4][4], float ua, float ub) {
-#pragma unroll
-            for (int i = 0; i < 4; i++) {
-                const int at = ((i + 4 * half) ^ (ra & 7)) << 4;  // rb & 7 is the same
-                *reinterpret_cast<uint32_t *>(pa + at) = pack<kBf16>(p[i][0] * ua, p[i][1] * ua);
-                *reinterpret_cast<uint32_t *>(pb + at) = pack<kBf16>(p[i][2] * ub, p[i][3] * ub);
+                const float x0 = __uint_as_float(raw[4 * i]) * P.L.scale, x1 = __uint_as_float(raw[4 * i + 1]) * P.L.scale;
+                const float x2 = __uint_as_float(raw[4 * i + 2]) * P.L.scale, x3 = __uint_as_float(raw[4 * i + 3]) * P.L.scale;
+                p[i][0] = c <= ra ? x0 * w0 : 0.0f;
+                p[i][1] = c < ra ? x1 * w1 : 0.0f;
+                p[i][2] = c <= rb ? x2 * w2 : 0.0f;
+                p[i][3] = c < rb ? x3 * w3 : 0.0f;
             }
         };
         float ua = 1.0f, ub = 1.0f;
@@ -875,11 +912,11 @@ __device__ __forceinline__ void weigh(const ScanPlan &P, ScanControl &C, uint8_t
             // (made twice: held, they would be 32 registers)
             float ta = 0.0f, tb = 0.0f;
 #pragma unroll 1
-            for (int half = 0; half < halves; half++) {
-                float p[4][4];
-                make(half, p);
+            for (int u = 0; u <= quarter; u++) {
+                float p[2][4];
+                make(u, p);
 #pragma unroll
-                for (int i = 0; i < 4; i++) {
+                for (int i = 0; i < 2; i++) {
                     ta = fmaxf(ta, fmaxf(fabsf(p[i][0]), fabsf(p[i][1])));
                     tb = fmaxf(tb, fmaxf(fabsf(p[i][2]), fabsf(p[i][3])));
                 }
@@ -892,17 +929,22 @@ __device__ __forceinline__ void weigh(const ScanPlan &P, ScanControl &C, uint8_t
             ua = power(ea);
             ub = power(eb);
             if ((lane & 3) == 0) {
-                D.lift[ra] = power(-ea) * P.L.scale;
-                D.lift[rb] = power(-eb) * P.L.scale;
+                D.lift[ra] = power(-ea);
+                D.lift[rb] = power(-eb);
             }
         }
         if (n >= 1)
             scan_wait(C, &C.weight_free, (n - 1) & 1, looks);
 #pragma unroll 1
-        for (int half = 0; half < halves; half++) {
-            float p[4][4];
-            make(half, p);
-            put(half, p, ua, ub);
+        for (int u = 0; u <= quarter; u++) {
+            float p[2][4];
+            make(u, p);
+#pragma unroll
+            for (int i = 0; i < 2; i++) {
+                const int at = ((2 * u + i) ^ (ra & 7)) << 4;  // rb & 7 is the same
+                *reinterpret_cast<uint32_t *>(pa + at) = pack<kBf16>(p[i][0] * ua, p[i][1] * ua);
+                *reinterpret_cast<uint32_t *>(pb + at) = pack<kBf16>(p[i][2] * ub, p[i][3] * ub);
+            }
         }
         fence_before();
         fence_async();
@@ -1104,18 +1146,22 @@ __device__ __forceinline__ void deliver(const ScanPlan &P, ScanControl &C, uint8
 #pragma unroll
             for (int i = 0; i < 4; i++) {
                 const float2 e = since[i];
-                float2 g = make_float2(L.scale, L.scale);
-                if constexpr (!kBf16)
-                    g = *reinterpret_cast<const float2 *>(&D.lift[32 * half + 8 * i + 2 * (lane & 3)]);
+                if constexpr (kBf16) {
 #pragma unroll
-                for (int k = 0; k < 2; k++) {
-                    float x0 = __uint_as_float(a[4 * i + 2 * k]) * e.x, x1 = __uint_as_float(a[4 * i + 2 * k + 1]) * e.y;
-                    if constexpr (!kBf16) {
-                        x0 *= k ? db : da;
-                        x1 *= k ? db : da;
+                    for (int k = 0; k < 2; k++)
+                        y[2 * i + k] = pack<true>(fmaf(__uint_as_float(a[4 * i + 2 * k]), e.x, __uint_as_float(b[4 * i + 2 * k])),
+                                                  fmaf(__uint_as_float(a[4 * i + 2 * k + 1]), e.y,
+                                                       __uint_as_float(b[4 * i + 2 * k + 1])));
+                } else {
+                    const float2 g = *reinterpret_cast<const float2 *>(&D.lift[32 * half + 8 * i + 2 * (lane & 3)]);
+#pragma unroll
+                    for (int k = 0; k < 2; k++) {
+                        const float d = k ? db : da;
+                        y[2 * i + k] =
+                            pack<false>(fmaf(__uint_as_float(a[4 * i + 2 * k]) * d, e.x, __uint_as_float(b[4 * i + 2 * k]) * g.x),
+                                        fmaf(__uint_as_float(a[4 * i + 2 * k + 1]) * d, e.y,
+                                             __uint_as_float(b[4 * i + 2 * k + 1]) * g.y));
                     }
-                    y[2 * i + k] = pack<kBf16>(fmaf(__uint_as_float(b[4 * i + 2 * k]), g.x, x0),
-                                               fmaf(__uint_as_float(b[4 * i + 2 * k + 1]), g.y, x1));
                 }
             }
             const uint32_t to = staged + half * 32 * 64 + (((2 * b16 + piece) ^ turn) << 4);
@@ -1130,7 +1176,7 @@ __device__ __forceinline__ void deliver(const ScanPlan &P, ScanControl &C, uint8
             const int v = 8 * (lane & 3), t0 = lane >> 2;
             uint16_t *out = L.out + ((int64_t)T.row + t0) * L.out_row + out_at + v;
             const bool inside = quarter * 32 + v < L.dv;
-#pragma unroll 1
+#pragma unroll 2
             for (int i = 0; i < 8; i++) {
                 const int t = 8 * i + t0;
                 const uint4 x = *reinterpret_cast<const uint4 *>(mine + t * 64 + (((lane & 3) ^ (t >> 1 & 3)) << 4));
@@ -1240,7 +1286,9 @@ __global__ void __launch_bounds__(kScanThreads, 1) lmc_linear_scan_kernel(const 
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegisters));
         if (warp == kLoadWarp)
-            load_tiles<kBf16, kStatesOnly>(P, C, scan_mem);
+            load_tiles<kStatesOnly>(P, C, scan_mem);
+        else if (warp == kDecayWarp)
+            tell_decays<kBf16>(P, C);
         else if (warp == kForwardWarp)
             multiply_forward<kBf16, kStatesOnly>(P, C, scan_mem);
         else if (warp == kStateProductWarp && !kStatesOnly)
