@@ -468,8 +468,7 @@ __device__ __forceinline__ Twice plus(const Twice &x, float high, float low) {
 
 // A tile's decays, by one warp: lane l's are those of tokens 2 l and 2 l + 1. Their
 // sums are held twice as long as binary32, so that sums far from 0 lose nothing of
-// the differences that count. (As whole numbers of 64 bits their conversions, on
-// the unit for 64-bit floating point, took 2500 clocks a tile.)
+// the differences that count.
 // `drift`: how much the tiles' rounded decays lack of the exact ones so far,
 // relatively; a tile's makes up for it, so that a state that decays slowly by
 // the same factor tile after tile keeps its digits.
