@@ -619,7 +619,8 @@ LMC_API int lmc_rotate(const lmc_rotation *rotation, int32_t dtype, const void *
  * heads with the values behind them. rotation->positions may be NULL: the angles
  * are then those of the cache positions; they are given apart where the two
  * differ (a cache that was cut to the tokens a request keeps). LMC_E_E4M3
- * entries hold e4m3(clamp(y / scale)) of the binary32 result y. */
+ * entries: values that are neither normalised nor turned become the codes that
+ * lmc_append makes; of the others 1 / scale, in binary32, is one more factor. */
 LMC_API int lmc_append_rotated(const lmc_layout *layout, const lmc_entries *entries, const lmc_rotation *rotation,
                                void *pool, const int32_t *requests, const int32_t *positions, const void *rows,
                                int32_t rows_dtype, int64_t row_stride, int64_t num_rows, uint32_t *status,

@@ -30,7 +30,7 @@ using namespace lmc;
 
 constexpr int kThreads = 256;
 constexpr int kMaxRows = 64;           // of a CTA
-constexpr int kMaxAngles = 4096;       // of a CTA's rows together (32 KB)
+constexpr int kMaxAngles = 2048;       // of a CTA's rows together (16 KB), where it has several
 constexpr int kMaxHeadDim = 4096;
 
 enum Result { kRows, kEntries, kCodes };  // activations; a page's entries, as they are or as fp8 codes
@@ -61,9 +61,10 @@ struct RotatePlan {
     int32_t turned;             // a head's items that are turned,
     int32_t items;              // and all of them
     int32_t group;              // lanes of a head
+    int32_t row_step, unit_step; // from a group's unit to its next
     int32_t pairs;
     int32_t touch_only;         // the result lies where x does
-    float eps, mscale;
+    float eps, mscale, inverse_norm_dim;
 };
 
 // frequency * 2^64 / (2 pi) modulo 2^64: the significand times 2^64 / (2 pi)
@@ -85,12 +86,24 @@ __device__ __forceinline__ uint64_t step_of(float frequency) {
     return bits >> 31 ? 0 - f : f;
 }
 
-// (cos, sin) of position steps.
+// (cos, sin) of position steps: the nearest quarter turn apart, the rest r, at most
+// an eighth of a turn, by the series of sine and cosine (what is left out is below
+// 2^-28 of the result). sincospif takes twice the instructions.
 __device__ __forceinline__ float2 turn(int32_t position, uint64_t step) {
     const uint64_t phase = (uint64_t)(int64_t)position * step;
-    float s, c;
-    sincospif((float)(int32_t)(phase >> 32) * 0x1p-31f, &s, &c);
-    return make_float2(c, s);
+    const uint32_t quarter = (uint32_t)((phase + (1ull << 61)) >> 62);
+    const float r = (float)(int32_t)((phase - ((uint64_t)quarter << 62)) >> 32) * (6.28318530717958647693f * 0x1p-32f);
+    const float x = r * r;
+    float s = fmaf(x, 1.0f / 362880.0f, -1.0f / 5040.0f), c = fmaf(x, -1.0f / 3628800.0f, 1.0f / 40320.0f);
+    s = fmaf(s, x, 1.0f / 120.0f);
+    c = fmaf(c, x, -1.0f / 720.0f);
+    s = fmaf(s, x, -1.0f / 6.0f);
+    c = fmaf(c, x, 1.0f / 24.0f);
+    s = fmaf(s * x, r, r);
+    c = fmaf(c, x, -0.5f);
+    c = fmaf(c, x, 1.0f);
+    const float a = quarter & 1 ? s : c, b = quarter & 1 ? c : s;
+    return make_float2((quarter + 1) & 2 ? -a : a, quarter & 2 ? -b : b);
 }
 
 template <typename T2>
@@ -170,6 +183,28 @@ __device__ __forceinline__ void store_values(const RotatePlan &P, uint8_t *at, c
     }
 }
 
+// Values of a result whose scale is in them already (codes): what was turned, and
+// most of what was normalised.
+template <typename T2, int W, Result kTo>
+__device__ __forceinline__ void store_scaled(const RotatePlan &P, uint8_t *at, const float (&y)[W]) {
+    if constexpr (kTo == kCodes) {
+        uint32_t w[(W + 1) / 2];
+#pragma unroll
+        for (int k = 0; k < (W + 1) / 2; k++) {
+            float2 v = make_float2(y[2 * k], W == 1 ? 0.0f : y[W == 1 ? 0 : 2 * k + 1]);
+            if (P.code_inverse == 0.0f)
+                v = make_float2(__fdiv_rn(v.x, P.code_scale), __fdiv_rn(v.y, P.code_scale));
+            w[k] = __nv_cvt_float2_to_fp8x2(v, __NV_SATFINITE, __NV_E4M3);
+        }
+        if constexpr (W == 8)
+            __stcs(reinterpret_cast<uint2 *>(at), make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16));
+        else
+            *at = (uint8_t)w[0];
+    } else {
+        store_values<T2, W, kTo>(P, at, y);
+    }
+}
+
 // One item of a head (or of the rest): normalised, turned, written.
 template <typename T2, int W, Result kTo>
 __device__ __forceinline__ void finish(const RotatePlan &P, const float2 *cs, uint8_t *dst, int i, int first, int second,
@@ -196,7 +231,7 @@ __device__ __forceinline__ void finish(const RotatePlan &P, const float2 *cs, ui
             a[k] = x * r.x - y * r.y;
             b[k] = x * r.y + y * r.x;
         }
-        store_values<T2, W, kTo>(P, dst + (int64_t)second * kBytes, b);
+        store_scaled<T2, W, kTo>(P, dst + (int64_t)second * kBytes, b);
     } else if (W == 8 && turned) {
 #pragma unroll
         for (int k = 0; k < W / 2; k++) {
@@ -206,21 +241,17 @@ __device__ __forceinline__ void finish(const RotatePlan &P, const float2 *cs, ui
             a[2 * k + 1] = x * r.y + y * r.x;
         }
     }
-    store_values<T2, W, kTo>(P, dst + (int64_t)first * kBytes, a);
+    if (turned)
+        store_scaled<T2, W, kTo>(P, dst + (int64_t)first * kBytes, a);
+    else
+        store_values<T2, W, kTo>(P, dst + (int64_t)first * kBytes, a);
 }
 
-// W: values of a piece, 8 (16 bytes) where every address allows it, else 1.
-// kItems: items of a head per lane, held in registers; 0: as many as it takes,
-// read a second time after the norm (long heads, and pieces of one value).
-template <typename T2, int W, int kItems, Result kTo>
-__global__ void __launch_bounds__(kThreads) lmc_rotate_kernel(const __grid_constant__ RotatePlan P) {
-    extern __shared__ float2 cs[];  // [rows][half]
-    __shared__ uint8_t *dst[kMaxRows];
-    constexpr int kBytes = kTo == kCodes ? 1 : 2;
-    const int64_t row0 = (int64_t)blockIdx.x * P.rows_per_cta;
-    const int rows = (int)min((int64_t)P.rows_per_cta, P.num_rows - row0);
-    wait_for_launch();
-    let_next_start();
+// Steps of the angles and the rows' cosines and sines in shared memory; where the
+// rows' entries lie.
+template <Result kTo>
+__device__ __forceinline__ void make_angles(const RotatePlan &P, float2 *cs, uint64_t *steps, uint8_t **dst, int64_t row0,
+                                            int rows) {
     if (kTo != kRows && (int)threadIdx.x < rows) {
         const int64_t i = row0 + threadIdx.x;
         const int32_t req = __ldca(P.requests + i);
@@ -236,13 +267,218 @@ __global__ void __launch_bounds__(kThreads) lmc_rotate_kernel(const __grid_const
         }
         dst[threadIdx.x] = at < 0 ? nullptr : P.pool + at;
     }
-    for (int k = threadIdx.x; k < rows * P.half; k += kThreads) {
-        const int row = k / P.half;
-        float2 r = turn(__ldca(P.angles + row0 + row), step_of(__ldca(P.frequencies + k - row * P.half)));
-        r.x *= P.mscale;
-        r.y *= P.mscale;
-        cs[k] = r;
+    for (int k = threadIdx.x; k < P.half; k += kThreads)
+        steps[k] = step_of(__ldca(P.frequencies + k));
+    __syncthreads();
+    // codes: times what the values are divided by, too
+    const float scale = kTo == kCodes && P.code_inverse != 0.0f ? P.mscale * P.code_inverse : P.mscale;
+    int row = 0, k = threadIdx.x;
+    for (;; k += kThreads) {
+        while (k >= P.half) {
+            k -= P.half;
+            if (++row >= rows)
+                return;
+        }
+        const float2 r = turn(__ldca(P.angles + row0 + row), steps[k]);
+        cs[row * P.half + k] = make_float2(r.x * scale, r.y * scale);
     }
+}
+
+// Pieces of eight values (16 bytes), a head's items held in registers by a group of
+// lanes, kItems each: a lane has the same items of every head, so where they lie and
+// what they are multiplied by is found once.
+template <typename T2, int kItems, bool kPairs, Result kTo>
+__global__ void __launch_bounds__(kThreads) lmc_rotate_eights_kernel(const __grid_constant__ RotatePlan P) {
+    extern __shared__ __align__(16) float2 cs[];  // [rows][half], then the steps [half]
+    __shared__ uint8_t *dst[kMaxRows];
+    constexpr int kBytes = kTo == kCodes ? 1 : 2;
+    constexpr int kSecond = kPairs ? 1 : kItems;   // items with a piece half a turned part away
+    const int64_t row0 = (int64_t)blockIdx.x * P.rows_per_cta;
+    const int rows = (int)min((int64_t)P.rows_per_cta, P.num_rows - row0);
+    const int lane = threadIdx.x & (P.group - 1), first_unit = threadIdx.x / P.group;
+    const uint32_t mine = (P.group == 32 ? ~0u : (1u << P.group) - 1) << (threadIdx.x & 31 & ~(P.group - 1));
+    int place[kItems];
+    bool there[kItems], turned[kItems], normed[kItems];
+#pragma unroll
+    for (int n = 0; n < kItems; n++) {
+        const int i = lane + n * P.group;
+        int second;
+        place[n] = first_value<8>(P, i, second);
+        turned[n] = i < P.turned;
+        normed[n] = place[n] < P.norm_dim;
+        // (not: an item that is neither normalised nor turned, where it lies already)
+        there[n] = i < P.items && !(kTo == kRows && P.touch_only && !turned[n] && !normed[n]);
+    }
+    wait_for_launch();
+    let_next_start();
+
+    int row = first_unit / P.units, unit = first_unit - row * P.units;
+    uint32_t lo[kItems][4], hi[kSecond][4];
+    auto load = [&] {
+        const uint16_t *src = P.x + (row0 + row) * P.x_row;
+        if (unit < P.heads) {
+            src += unit * P.x_head;
+#pragma unroll
+            for (int n = 0; n < kItems; n++)
+                if (there[n]) {
+                    load_values<8>(lo[n], src + place[n]);
+                    if (!kPairs && turned[n])
+                        load_values<8>(hi[kPairs ? 0 : n], src + place[n] + P.half);
+                }
+        } else {
+            const int from = (unit - P.heads) * P.rest_unit, most = min(P.rest_unit, P.rest - from) / 8;
+            src += P.heads * P.head_dim + from;
+#pragma unroll
+            for (int n = 0; n < kItems; n++)
+                if (lane + n * P.group < most)
+                    load_values<8>(lo[n], src + 8 * (lane + n * P.group));
+        }
+    };
+    if (row < rows)
+        load();  // while the angles are made
+    float weight[kItems][8], weight2[kPairs || kItems > 1 ? 1 : kItems][8];
+    auto weights_at = [&](float(&w)[8], int at) {
+#pragma unroll
+        for (int k = 0; k < 8; k++)
+            w[k] = 1.0f;
+        if (P.weight != nullptr && at < P.norm_dim) {
+            const float4 x = *reinterpret_cast<const float4 *>(P.weight + at), y = *reinterpret_cast<const float4 *>(P.weight + at + 4);
+            w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w, w[4] = y.x, w[5] = y.y, w[6] = y.z, w[7] = y.w;
+        }
+    };
+    if (P.norm_dim > 0) {
+#pragma unroll
+        for (int n = 0; n < kItems; n++)
+            weights_at(weight[n], there[n] ? place[n] : P.norm_dim);
+        if constexpr (!kPairs && kItems == 1)
+            weights_at(weight2[0], there[0] && turned[0] ? place[0] + P.half : P.norm_dim);
+    }
+    make_angles<kTo>(P, cs, reinterpret_cast<uint64_t *>(cs + rows * P.half), dst, row0, rows);
+    __syncthreads();
+
+    while (row < rows) {
+        const bool head = unit < P.heads;
+        uint8_t *to = nullptr;
+        if (kTo == kRows)
+            to = reinterpret_cast<uint8_t *>(P.out + (row0 + row) * P.out_row + unit * P.out_head);
+        else if (dst[row] != nullptr)
+            to = dst[row] + (head ? (int64_t)unit * P.head_dim
+                                  : (int64_t)P.heads * P.head_dim + (unit - P.heads) * P.rest_unit) * kBytes;
+        if (head) {
+            float norm = 1.0f;
+            if (P.norm_dim > 0) {
+                float sum = 0.0f;
+                auto add = [&](const uint32_t(&raw)[4]) {
+#pragma unroll
+                    for (int k = 0; k < 4; k++) {
+                        const float2 v = widen<T2>(raw[k]);
+                        sum = fmaf(v.x, v.x, sum);
+                        sum = fmaf(v.y, v.y, sum);
+                    }
+                };
+#pragma unroll
+                for (int n = 0; n < kItems; n++) {
+                    if (there[n] && normed[n])
+                        add(lo[n]);
+                    if (!kPairs && there[n] && turned[n] && place[n] + P.half < P.norm_dim)
+                        add(hi[kPairs ? 0 : n]);
+                }
+                for (int o = P.group / 2; o > 0; o >>= 1)
+                    sum += __shfl_xor_sync(mine, sum, o);
+                norm = rsqrtf(fmaf(sum, P.inverse_norm_dim, P.eps));
+            }
+            if (to != nullptr) {
+                const float2 *const angles = cs + row * P.half;
+                // codes: what is not turned is brought to its scale here
+                const float apart = kTo == kCodes && P.code_inverse != 0.0f ? norm * P.code_inverse : norm;
+#pragma unroll
+                for (int n = 0; n < kItems; n++) {
+                    if (!there[n])
+                        continue;
+                    float a[8];
+                    widen_values<T2, 8>(a, lo[n]);
+                    if (normed[n]) {
+                        const float f = turned[n] ? norm : apart;
+#pragma unroll
+                        for (int k = 0; k < 8; k++)
+                            a[k] = a[k] * f * weight[n][k];
+                    }
+                    uint8_t *const at = to + place[n] * kBytes;
+                    if (!turned[n]) {
+                        if (kTo == kCodes && !normed[n])
+                            store_values<T2, 8, kTo>(P, at, a);  // as lmc_append does
+                        else
+                            store_scaled<T2, 8, kTo>(P, at, a);
+                    } else if constexpr (kPairs) {
+                        const float4 *const r = reinterpret_cast<const float4 *>(angles + (lane + n * P.group) * 4);
+#pragma unroll
+                        for (int k = 0; k < 2; k++) {
+                            const float4 c = r[k];
+                            const float w = a[4 * k], x = a[4 * k + 1], y = a[4 * k + 2], z = a[4 * k + 3];
+                            a[4 * k] = w * c.x - x * c.y;
+                            a[4 * k + 1] = w * c.y + x * c.x;
+                            a[4 * k + 2] = y * c.z - z * c.w;
+                            a[4 * k + 3] = y * c.w + z * c.z;
+                        }
+                        store_scaled<T2, 8, kTo>(P, at, a);
+                    } else {
+                        float b[8];
+                        widen_values<T2, 8>(b, hi[n]);
+                        if (place[n] + P.half < P.norm_dim) {
+                            if constexpr (kItems > 1)
+                                weights_at(weight2[0], place[n] + P.half);
+#pragma unroll
+                            for (int k = 0; k < 8; k++)
+                                b[k] = b[k] * norm * weight2[0][k];
+                        }
+                        const float4 *const r = reinterpret_cast<const float4 *>(angles + (lane + n * P.group) * 8);
+#pragma unroll
+                        for (int k = 0; k < 4; k++) {
+                            const float4 c = r[k];
+                            const float w = a[2 * k], x = b[2 * k], y = a[2 * k + 1], z = b[2 * k + 1];
+                            a[2 * k] = w * c.x - x * c.y;
+                            b[2 * k] = w * c.y + x * c.x;
+                            a[2 * k + 1] = y * c.z - z * c.w;
+                            b[2 * k + 1] = y * c.w + z * c.z;
+                        }
+                        store_scaled<T2, 8, kTo>(P, at, a);
+                        store_scaled<T2, 8, kTo>(P, at + P.half * kBytes, b);
+                    }
+                }
+            }
+        } else if (to != nullptr) {
+            const int most = min(P.rest_unit, P.rest - (unit - P.heads) * P.rest_unit) / 8;
+#pragma unroll
+            for (int n = 0; n < kItems; n++)
+                if (lane + n * P.group < most) {
+                    float a[8];
+                    widen_values<T2, 8>(a, lo[n]);
+                    store_values<T2, 8, kTo>(P, to + 8 * (lane + n * P.group) * kBytes, a);
+                }
+        }
+        row += P.row_step;
+        unit += P.unit_step;
+        if (unit >= P.units) {
+            unit -= P.units;
+            row++;
+        }
+        if (row < rows)
+            load();
+    }
+}
+
+// Long heads, and rows that do not lie on multiples of 16 bytes: W values of a piece
+// (8, or 1), a head's items one after another, read a second time after the norm.
+template <typename T2, int W, Result kTo>
+__global__ void __launch_bounds__(kThreads) lmc_rotate_kernel(const __grid_constant__ RotatePlan P) {
+    extern __shared__ __align__(16) float2 cs[];  // [rows][half], then the steps [half]
+    __shared__ uint8_t *dst[kMaxRows];
+    constexpr int kBytes = kTo == kCodes ? 1 : 2;
+    const int64_t row0 = (int64_t)blockIdx.x * P.rows_per_cta;
+    const int rows = (int)min((int64_t)P.rows_per_cta, P.num_rows - row0);
+    wait_for_launch();
+    let_next_start();
+    make_angles<kTo>(P, cs, reinterpret_cast<uint64_t *>(cs + rows * P.half), dst, row0, rows);
     __syncthreads();
 
     const int lane = threadIdx.x & (P.group - 1);
@@ -268,87 +504,32 @@ __global__ void __launch_bounds__(kThreads) lmc_rotate_kernel(const __grid_const
         }
         if (kTo != kRows && dst[row] == nullptr)
             continue;
-        auto place = [&](int i, int &second) {
-            second = -1;
-            return head ? first_value<W>(P, i, second) : i * W;
-        };
-        // an item that is neither normalised nor turned, where it lies already
-        auto skip = [&](int i, int first) {
-            return kTo == kRows && P.touch_only && i >= P.turned && first >= P.norm_dim;
-        };
-        float sum = 0.0f;
-        auto add = [&](const uint32_t(&raw)[(W + 1) / 2], int first) {
-            if (!head || first >= P.norm_dim)
-                return;
-            float x[W];
-            widen_values<T2, W>(x, raw);
+        float sum = 0.0f, norm = 1.0f;
+        if (P.norm_dim > 0 && head) {  // (a group's lanes are at one unit)
+            for (int i = lane; i * W < P.norm_dim; i += P.group) {
+                uint32_t raw[(W + 1) / 2];
+                load_values<W>(raw, src + i * W);
+                float x[W];
+                widen_values<T2, W>(x, raw);
 #pragma unroll
-            for (int k = 0; k < W; k++)
-                sum = fmaf(x[k], x[k], sum);
-        };
-        if constexpr (kItems > 0) {
-            uint32_t lo[kItems][(W + 1) / 2] = {}, hi[kItems][(W + 1) / 2] = {};
-#pragma unroll
-            for (int n = 0; n < kItems; n++) {
-                const int i = lane + n * P.group;
-                if (i < items) {
-                    int second;
-                    const int first = place(i, second);
-                    if (!skip(i, first))
-                        load_values<W>(lo[n], src + first);
-                    if (second >= 0)
-                        load_values<W>(hi[n], src + second);
-                }
+                for (int k = 0; k < W; k++)
+                    sum = fmaf(x[k], x[k], sum);
             }
-            float norm = 1.0f;
-            if (P.norm_dim > 0) {
-#pragma unroll
-                for (int n = 0; n < kItems; n++) {
-                    const int i = lane + n * P.group;
-                    if (i < items) {
-                        int second;
-                        add(lo[n], place(i, second));
-                        if (second >= 0)
-                            add(hi[n], second);
-                    }
-                }
-                for (int o = P.group / 2; o > 0; o >>= 1)
-                    sum += __shfl_xor_sync(mine, sum, o);
-                norm = 1.0f / sqrtf(sum / (float)P.norm_dim + P.eps);
-            }
-#pragma unroll
-            for (int n = 0; n < kItems; n++) {
-                const int i = lane + n * P.group;
-                if (i < items) {
-                    int second;
-                    const int first = place(i, second);
-                    if (!skip(i, first))
-                        finish<T2, W, kTo>(P, cs + row * P.half, to, i, first, second, norm, head, lo[n], hi[n]);
-                }
-            }
-        } else {
-            float norm = 1.0f;
-            if (P.norm_dim > 0 && head) {  // (a group's lanes are at one unit)
-                for (int i = lane; i * W < P.norm_dim; i += P.group) {
-                    uint32_t raw[(W + 1) / 2];
-                    load_values<W>(raw, src + i * W);
-                    add(raw, i * W);
-                }
-                for (int o = P.group / 2; o > 0; o >>= 1)
-                    sum += __shfl_xor_sync(mine, sum, o);
-                norm = 1.0f / sqrtf(sum / (float)P.norm_dim + P.eps);
-            }
-            for (int i = lane; i < items; i += P.group) {
-                int second;
-                const int first = place(i, second);
-                if (skip(i, first))
-                    continue;
-                uint32_t lo[(W + 1) / 2], hi[(W + 1) / 2] = {};
-                load_values<W>(lo, src + first);
-                if (second >= 0)
-                    load_values<W>(hi, src + second);
-                finish<T2, W, kTo>(P, cs + row * P.half, to, i, first, second, norm, head, lo, hi);
-            }
+            for (int o = P.group / 2; o > 0; o >>= 1)
+                sum += __shfl_xor_sync(mine, sum, o);
+            norm = rsqrtf(fmaf(sum, P.inverse_norm_dim, P.eps));
+        }
+        for (int i = lane; i < items; i += P.group) {
+            int second = -1;
+            const int first = head ? first_value<W>(P, i, second) : i * W;
+            // an item that is neither normalised nor turned, where it lies already
+            if (kTo == kRows && P.touch_only && i >= P.turned && first >= P.norm_dim)
+                continue;
+            uint32_t lo[(W + 1) / 2], hi[(W + 1) / 2] = {};
+            load_values<W>(lo, src + first);
+            if (second >= 0)
+                load_values<W>(hi, src + second);
+            finish<T2, W, kTo>(P, cs + row * P.half, to, i, first, second, norm, head, lo, hi);
         }
     }
 }
@@ -380,6 +561,7 @@ void plan_heads(RotatePlan &P, const lmc_rotation *r, int width) {
     P.pairs = r->rot_mode == LMC_ROT_PAIRS;
     P.eps = r->eps;
     P.mscale = r->mscale;
+    P.inverse_norm_dim = r->norm_dim > 0 ? 1.0f / (float)r->norm_dim : 0.0f;
     P.turned = width == 1 ? P.half : P.pairs ? r->rot_dim / width : P.half / width;
     P.items = P.turned + (P.head_dim - r->rot_dim) / width;
     if (P.touch_only && P.norm_dim == 0)
@@ -402,14 +584,24 @@ int launch(RotatePlan &P, int width, cudaStream_t stream) {
     const int64_t grid = (P.num_rows + rows - 1) / rows;
     if (grid > INT32_MAX)
         return LMC_ERR_INVALID_ARG;
+    P.row_step = at_once / P.units;
+    P.unit_step = at_once % P.units;
     const int per_lane = (P.items + P.group - 1) / P.group;
-    auto kern = width == 1     ? lmc_rotate_kernel<T2, 1, 0, kTo>
-                : per_lane > 3 ? lmc_rotate_kernel<T2, 8, 0, kTo>
-                : per_lane == 3 ? lmc_rotate_kernel<T2, 8, 3, kTo>
-                : per_lane == 2 ? lmc_rotate_kernel<T2, 8, 2, kTo>
-                                : lmc_rotate_kernel<T2, 8, 1, kTo>;
-    return follow(kern, dim3((unsigned)grid), kThreads, (size_t)rows * P.half * sizeof(float2), stream, P) ? LMC_OK
-                                                                                                          : LMC_ERR_CUDA;
+    void (*kern)(RotatePlan) = nullptr;
+    if (width == 1)
+        kern = lmc_rotate_kernel<T2, 1, kTo>;
+    else if (per_lane > 3)
+        kern = lmc_rotate_kernel<T2, 8, kTo>;
+    else if (P.pairs)
+        kern = per_lane == 3   ? lmc_rotate_eights_kernel<T2, 3, true, kTo>
+               : per_lane == 2 ? lmc_rotate_eights_kernel<T2, 2, true, kTo>
+                               : lmc_rotate_eights_kernel<T2, 1, true, kTo>;
+    else
+        kern = per_lane == 3   ? lmc_rotate_eights_kernel<T2, 3, false, kTo>
+               : per_lane == 2 ? lmc_rotate_eights_kernel<T2, 2, false, kTo>
+                               : lmc_rotate_eights_kernel<T2, 1, false, kTo>;
+    const size_t smem = (size_t)rows * P.half * sizeof(float2) + (size_t)P.half * sizeof(uint64_t);
+    return follow(kern, dim3((unsigned)grid), kThreads, smem, stream, P) ? LMC_OK : LMC_ERR_CUDA;
 }
 
 // Whether every piece of eight values lies on a multiple of its size.
