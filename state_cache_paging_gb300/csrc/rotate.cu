@@ -33,6 +33,8 @@ constexpr int kMaxRows = 64;           // of a CTA
 constexpr int kMaxAngles = 2048;       // of a CTA's rows together (16 KB), where it has several
 constexpr int kMaxHeadDim = 4096;
 
+constexpr int kManyCtas = 152 * 16;   // waves of CTAs enough to even out
+
 enum Result { kRows, kEntries, kCodes };  // activations; a page's entries, as they are or as fp8 codes
 
 struct RotatePlan {
@@ -62,6 +64,7 @@ struct RotatePlan {
     int32_t items;              // and all of them
     int32_t group;              // lanes of a head
     int32_t row_step, unit_step; // from a group's unit to its next
+    int32_t angle_rows, angle_step; // from a thread's angle to its next
     int32_t pairs;
     int32_t touch_only;         // the result lies where x does
     float eps, mscale, inverse_norm_dim;
@@ -215,15 +218,17 @@ __device__ __forceinline__ void finish(const RotatePlan &P, const float2 *cs, ui
     widen_values<T2, W>(a, lo);
     widen_values<T2, W>(b, hi);
     const bool turned = head && i < P.turned;
-    if (head && first < P.norm_dim)
+    if (head && first < P.norm_dim) {
 #pragma unroll
         for (int k = 0; k < W; k++)
             a[k] = a[k] * norm * (P.weight != nullptr ? __ldca(P.weight + first + k) : 1.0f);
+    }
     if (turned && second >= 0) {
-        if (second < P.norm_dim)
+        if (second < P.norm_dim) {
 #pragma unroll
             for (int k = 0; k < W; k++)
                 b[k] = b[k] * norm * (P.weight != nullptr ? __ldca(P.weight + second + k) : 1.0f);
+        }
 #pragma unroll
         for (int k = 0; k < W; k++) {
             const float2 r = cs[i * W + k];
@@ -272,15 +277,18 @@ __device__ __forceinline__ void make_angles(const RotatePlan &P, float2 *cs, uin
     __syncthreads();
     // codes: times what the values are divided by, too
     const float scale = kTo == kCodes && P.code_inverse != 0.0f ? P.mscale * P.code_inverse : P.mscale;
-    int row = 0, k = threadIdx.x;
-    for (;; k += kThreads) {
-        while (k >= P.half) {
-            k -= P.half;
-            if (++row >= rows)
-                return;
-        }
+    if (P.half == 0)
+        return;
+    int row = threadIdx.x / P.half, k = threadIdx.x - row * P.half;
+    while (row < rows) {
         const float2 r = turn(__ldca(P.angles + row0 + row), steps[k]);
         cs[row * P.half + k] = make_float2(r.x * scale, r.y * scale);
+        row += P.angle_rows;
+        k += P.angle_step;
+        if (k >= P.half) {
+            k -= P.half;
+            row++;
+        }
     }
 }
 
@@ -397,53 +405,52 @@ __global__ void __launch_bounds__(kThreads) lmc_rotate_eights_kernel(const __gri
                         continue;
                     float a[8];
                     widen_values<T2, 8>(a, lo[n]);
+                    uint8_t *const at = to + place[n] * kBytes;
                     if (normed[n]) {
                         const float f = turned[n] ? norm : apart;
 #pragma unroll
                         for (int k = 0; k < 8; k++)
                             a[k] = a[k] * f * weight[n][k];
+                    } else if (kTo == kCodes && !turned[n]) {
+                        store_values<T2, 8, kTo>(P, at, a);  // as lmc_append does
+                        continue;
                     }
-                    uint8_t *const at = to + place[n] * kBytes;
-                    if (!turned[n]) {
-                        if (kTo == kCodes && !normed[n])
-                            store_values<T2, 8, kTo>(P, at, a);  // as lmc_append does
-                        else
-                            store_scaled<T2, 8, kTo>(P, at, a);
-                    } else if constexpr (kPairs) {
-                        const float4 *const r = reinterpret_cast<const float4 *>(angles + (lane + n * P.group) * 4);
+                    if (turned[n]) {
+                        if constexpr (kPairs) {
+                            const float4 *const r = reinterpret_cast<const float4 *>(angles + (lane + n * P.group) * 4);
 #pragma unroll
-                        for (int k = 0; k < 2; k++) {
-                            const float4 c = r[k];
-                            const float w = a[4 * k], x = a[4 * k + 1], y = a[4 * k + 2], z = a[4 * k + 3];
-                            a[4 * k] = w * c.x - x * c.y;
-                            a[4 * k + 1] = w * c.y + x * c.x;
-                            a[4 * k + 2] = y * c.z - z * c.w;
-                            a[4 * k + 3] = y * c.w + z * c.z;
-                        }
-                        store_scaled<T2, 8, kTo>(P, at, a);
-                    } else {
-                        float b[8];
-                        widen_values<T2, 8>(b, hi[n]);
-                        if (place[n] + P.half < P.norm_dim) {
-                            if constexpr (kItems > 1)
-                                weights_at(weight2[0], place[n] + P.half);
+                            for (int k = 0; k < 2; k++) {
+                                const float4 c = r[k];
+                                const float w = a[4 * k], x = a[4 * k + 1], y = a[4 * k + 2], z = a[4 * k + 3];
+                                a[4 * k] = w * c.x - x * c.y;
+                                a[4 * k + 1] = w * c.y + x * c.x;
+                                a[4 * k + 2] = y * c.z - z * c.w;
+                                a[4 * k + 3] = y * c.w + z * c.z;
+                            }
+                        } else {
+                            float b[8];
+                            widen_values<T2, 8>(b, hi[n]);
+                            if (place[n] + P.half < P.norm_dim) {
+                                if constexpr (kItems > 1)
+                                    weights_at(weight2[0], place[n] + P.half);
 #pragma unroll
-                            for (int k = 0; k < 8; k++)
-                                b[k] = b[k] * norm * weight2[0][k];
-                        }
-                        const float4 *const r = reinterpret_cast<const float4 *>(angles + (lane + n * P.group) * 8);
+                                for (int k = 0; k < 8; k++)
+                                    b[k] = b[k] * norm * weight2[0][k];
+                            }
+                            const float4 *const r = reinterpret_cast<const float4 *>(angles + (lane + n * P.group) * 8);
 #pragma unroll
-                        for (int k = 0; k < 4; k++) {
-                            const float4 c = r[k];
-                            const float w = a[2 * k], x = b[2 * k], y = a[2 * k + 1], z = b[2 * k + 1];
-                            a[2 * k] = w * c.x - x * c.y;
-                            b[2 * k] = w * c.y + x * c.x;
-                            a[2 * k + 1] = y * c.z - z * c.w;
-                            b[2 * k + 1] = y * c.w + z * c.z;
+                            for (int k = 0; k < 4; k++) {
+                                const float4 c = r[k];
+                                const float w = a[2 * k], x = b[2 * k], y = a[2 * k + 1], z = b[2 * k + 1];
+                                a[2 * k] = w * c.x - x * c.y;
+                                b[2 * k] = w * c.y + x * c.x;
+                                a[2 * k + 1] = y * c.z - z * c.w;
+                                b[2 * k + 1] = y * c.w + z * c.z;
+                            }
+                            store_scaled<T2, 8, kTo>(P, at + P.half * kBytes, b);
                         }
-                        store_scaled<T2, 8, kTo>(P, at, a);
-                        store_scaled<T2, 8, kTo>(P, at + P.half * kBytes, b);
                     }
+                    store_scaled<T2, 8, kTo>(P, at, a);
                 }
             }
         } else if (to != nullptr) {
@@ -578,12 +585,18 @@ int launch(RotatePlan &P, int width, cudaStream_t stream) {
     // Rows of a CTA: enough heads for every group of lanes a few times, so that
     // the angles are made while other CTAs' loads run.
     const int at_once = kThreads / P.group;
+    // (more of them where there are enough CTAs: what a lane finds out once is
+    // spread over more heads)
     int64_t rows = std::max<int64_t>(1, (int64_t)at_once * 4 / P.units);
+    while (P.num_rows / rows > kManyCtas && rows * P.units < (int64_t)at_once * 16)
+        rows *= 2;
     rows = std::min<int64_t>({rows, kMaxRows, std::max(1, kMaxAngles / std::max(1, P.half))});
     P.rows_per_cta = (int32_t)rows;
     const int64_t grid = (P.num_rows + rows - 1) / rows;
     if (grid > INT32_MAX)
         return LMC_ERR_INVALID_ARG;
+    P.angle_rows = P.half > 0 ? kThreads / P.half : 0;
+    P.angle_step = P.half > 0 ? kThreads % P.half : 0;
     P.row_step = at_once / P.units;
     P.unit_step = at_once % P.units;
     const int per_lane = (P.items + P.group - 1) / P.group;
