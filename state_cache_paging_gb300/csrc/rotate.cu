@@ -292,12 +292,39 @@ __device__ __forceinline__ void make_angles(const RotatePlan &P, float2 *cs, uin
     }
 }
 
+// Two binary32 operations at once.
+struct Two {
+    uint64_t v;
+};
+__device__ __forceinline__ Two two(float x, float y) {
+    Two r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r.v) : "f"(x), "f"(y));
+    return r;
+}
+__device__ __forceinline__ float2 apart(Two a) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(a.v));
+    return r;
+}
+__device__ __forceinline__ Two operator*(Two a, Two b) {
+    Two r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r.v) : "l"(a.v), "l"(b.v));
+    return r;
+}
+__device__ __forceinline__ Two plus_product(Two a, Two b, Two c) {
+    Two r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r.v) : "l"(a.v), "l"(b.v), "l"(c.v));
+    return r;
+}
+
 // Pieces of eight values (16 bytes), a head's items held in registers by a group of
-// lanes, kItems each: a lane has the same items of every head, so where they lie and
-// what they are multiplied by is found once.
+// lanes, kItems each: a lane has the same items of every head, so where they lie is
+// found once. What it costs are instructions (for a row of 576 values as fp8 codes
+// the copy rate leaves some 200 of a warp), so values are widened once and multiplied
+// by pairs, and the weights, 1 where there is no norm, lie in shared memory.
 template <typename T2, int kItems, bool kPairs, Result kTo>
 __global__ void __launch_bounds__(kThreads) lmc_rotate_eights_kernel(const __grid_constant__ RotatePlan P) {
-    extern __shared__ __align__(16) float2 cs[];  // [rows][half], then the steps [half]
+    extern __shared__ __align__(16) float2 cs[];  // [rows][half], the steps [half], the weights [head_dim]
     __shared__ uint8_t *dst[kMaxRows];
     constexpr int kBytes = kTo == kCodes ? 1 : 2;
     constexpr int kSecond = kPairs ? 1 : kItems;   // items with a piece half a turned part away
@@ -305,172 +332,220 @@ __global__ void __launch_bounds__(kThreads) lmc_rotate_eights_kernel(const __gri
     const int rows = (int)min((int64_t)P.rows_per_cta, P.num_rows - row0);
     const int lane = threadIdx.x & (P.group - 1), first_unit = threadIdx.x / P.group;
     const uint32_t mine = (P.group == 32 ? ~0u : (1u << P.group) - 1) << (threadIdx.x & 31 & ~(P.group - 1));
+    uint64_t *const steps = reinterpret_cast<uint64_t *>(cs + P.rows_per_cta * P.half);
+    float *const weights = reinterpret_cast<float *>(steps + (P.half + 1) / 2 * 2);
     int place[kItems];
-    bool there[kItems], turned[kItems], normed[kItems];
+    bool there[kItems], turned[kItems], plain[kItems];
 #pragma unroll
     for (int n = 0; n < kItems; n++) {
         const int i = lane + n * P.group;
         int second;
         place[n] = first_value<8>(P, i, second);
         turned[n] = i < P.turned;
-        normed[n] = place[n] < P.norm_dim;
+        plain[n] = !turned[n] && place[n] >= P.norm_dim;
         // (not: an item that is neither normalised nor turned, where it lies already)
-        there[n] = i < P.items && !(kTo == kRows && P.touch_only && !turned[n] && !normed[n]);
+        there[n] = i < P.items && !(kTo == kRows && P.touch_only && plain[n]);
     }
     wait_for_launch();
     let_next_start();
 
     int row = first_unit / P.units, unit = first_unit - row * P.units;
-    uint32_t lo[kItems][4], hi[kSecond][4];
+    uint4 lo[kItems], hi[kSecond];
     auto load = [&] {
         const uint16_t *src = P.x + (row0 + row) * P.x_row;
         if (unit < P.heads) {
             src += unit * P.x_head;
 #pragma unroll
-            for (int n = 0; n < kItems; n++)
+            for (int n = 0; n < kItems; n++) {
                 if (there[n]) {
-                    load_values<8>(lo[n], src + place[n]);
+                    lo[n] = __ldcs(reinterpret_cast<const uint4 *>(src + place[n]));
                     if (!kPairs && turned[n])
-                        load_values<8>(hi[kPairs ? 0 : n], src + place[n] + P.half);
+                        hi[kPairs ? 0 : n] = __ldcs(reinterpret_cast<const uint4 *>(src + place[n] + P.half));
                 }
+            }
         } else {
             const int from = (unit - P.heads) * P.rest_unit, most = min(P.rest_unit, P.rest - from) / 8;
             src += P.heads * P.head_dim + from;
 #pragma unroll
             for (int n = 0; n < kItems; n++)
                 if (lane + n * P.group < most)
-                    load_values<8>(lo[n], src + 8 * (lane + n * P.group));
+                    lo[n] = __ldcs(reinterpret_cast<const uint4 *>(src) + lane + n * P.group);
         }
     };
+#pragma unroll
+    for (int n = 0; n < kItems; n++)
+        lo[n] = make_uint4(0, 0, 0, 0);
+#pragma unroll
+    for (int n = 0; n < kSecond; n++)
+        hi[n] = make_uint4(0, 0, 0, 0);
     if (row < rows)
         load();  // while the angles are made
-    float weight[kItems][8], weight2[kPairs || kItems > 1 ? 1 : kItems][8];
-    auto weights_at = [&](float(&w)[8], int at) {
-#pragma unroll
-        for (int k = 0; k < 8; k++)
-            w[k] = 1.0f;
-        if (P.weight != nullptr && at < P.norm_dim) {
-            const float4 x = *reinterpret_cast<const float4 *>(P.weight + at), y = *reinterpret_cast<const float4 *>(P.weight + at + 4);
-            w[0] = x.x, w[1] = x.y, w[2] = x.z, w[3] = x.w, w[4] = y.x, w[5] = y.y, w[6] = y.z, w[7] = y.w;
-        }
-    };
-    if (P.norm_dim > 0) {
-#pragma unroll
-        for (int n = 0; n < kItems; n++)
-            weights_at(weight[n], there[n] ? place[n] : P.norm_dim);
-        if constexpr (!kPairs && kItems == 1)
-            weights_at(weight2[0], there[0] && turned[0] ? place[0] + P.half : P.norm_dim);
-    }
-    make_angles<kTo>(P, cs, reinterpret_cast<uint64_t *>(cs + rows * P.half), dst, row0, rows);
+    if (P.norm_dim > 0)
+        for (int k = threadIdx.x; k < P.head_dim; k += kThreads)
+            weights[k] = P.weight != nullptr && k < P.norm_dim ? __ldca(P.weight + k) : 1.0f;
+    make_angles<kTo>(P, cs, steps, dst, row0, rows);
     __syncthreads();
 
+    auto open = [](Two(&x)[4], const uint4 &raw) {
+        const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+#pragma unroll
+        for (int k = 0; k < 4; k++) {
+            const float2 v = widen<T2>(w[k]);
+            x[k] = two(v.x, v.y);
+        }
+    };
+    auto weigh = [&](Two(&x)[4], float f, int at) {
+        const float4 v = *reinterpret_cast<const float4 *>(weights + at), w = *reinterpret_cast<const float4 *>(weights + at + 4);
+        const Two g = two(f, f);
+        x[0] = x[0] * g * two(v.x, v.y);
+        x[1] = x[1] * g * two(v.z, v.w);
+        x[2] = x[2] * g * two(w.x, w.y);
+        x[3] = x[3] * g * two(w.z, w.w);
+    };
+    auto put = [&](uint8_t *at, const Two(&x)[4]) {
+        float y[8];
+#pragma unroll
+        for (int k = 0; k < 4; k++) {
+            const float2 v = apart(x[k]);
+            y[2 * k] = v.x;
+            y[2 * k + 1] = v.y;
+        }
+        store_scaled<T2, 8, kTo>(P, at, y);
+    };
+    // codes: what is not turned is brought to its scale by the norm's factor
+    const float code = kTo == kCodes && P.code_inverse != 0.0f ? P.code_inverse : 1.0f;
     while (row < rows) {
-        const bool head = unit < P.heads;
         uint8_t *to = nullptr;
         if (kTo == kRows)
             to = reinterpret_cast<uint8_t *>(P.out + (row0 + row) * P.out_row + unit * P.out_head);
-        else if (dst[row] != nullptr)
-            to = dst[row] + (head ? (int64_t)unit * P.head_dim
-                                  : (int64_t)P.heads * P.head_dim + (unit - P.heads) * P.rest_unit) * kBytes;
-        if (head) {
-            float norm = 1.0f;
-            if (P.norm_dim > 0) {
-                float sum = 0.0f;
-                auto add = [&](const uint32_t(&raw)[4]) {
+        else
+            to = dst[row];
+        if (unit < P.heads) {
+            Two a[kItems][4], b[kSecond][4];
 #pragma unroll
-                    for (int k = 0; k < 4; k++) {
-                        const float2 v = widen<T2>(raw[k]);
-                        sum = fmaf(v.x, v.x, sum);
-                        sum = fmaf(v.y, v.y, sum);
-                    }
-                };
+            for (int n = 0; n < kItems; n++)
+                open(a[n], lo[n]);
+            if constexpr (!kPairs) {
+#pragma unroll
+                for (int n = 0; n < kItems; n++)
+                    open(b[n], hi[n]);
+            }
+            const int here = row, here_unit = unit;
+            row += P.row_step;
+            unit += P.unit_step;
+            if (unit >= P.units) {
+                unit -= P.units;
+                row++;
+            }
+            if (row < rows)
+                load();
+            if (P.norm_dim > 0) {
+                Two sum = two(0.0f, 0.0f);
 #pragma unroll
                 for (int n = 0; n < kItems; n++) {
-                    if (there[n] && normed[n])
-                        add(lo[n]);
-                    if (!kPairs && there[n] && turned[n] && place[n] + P.half < P.norm_dim)
-                        add(hi[kPairs ? 0 : n]);
+                    if (there[n] && place[n] < P.norm_dim) {
+#pragma unroll
+                        for (int k = 0; k < 4; k++)
+                            sum = plus_product(a[n][k], a[n][k], sum);
+                    }
+                    if constexpr (!kPairs) {
+                        if (there[n] && turned[n] && place[n] + P.half < P.norm_dim) {
+#pragma unroll
+                            for (int k = 0; k < 4; k++)
+                                sum = plus_product(b[n][k], b[n][k], sum);
+                        }
+                    }
                 }
+                const float2 halves = apart(sum);
+                float all = halves.x + halves.y;
                 for (int o = P.group / 2; o > 0; o >>= 1)
-                    sum += __shfl_xor_sync(mine, sum, o);
-                norm = rsqrtf(fmaf(sum, P.inverse_norm_dim, P.eps));
+                    all += __shfl_xor_sync(mine, all, o);
+                const float norm = rsqrtf(fmaf(all, P.inverse_norm_dim, P.eps));
+#pragma unroll
+                for (int n = 0; n < kItems; n++) {
+                    if (there[n]) {
+                        weigh(a[n], place[n] >= P.norm_dim ? 1.0f : turned[n] ? norm : norm * code, place[n]);
+                        if constexpr (!kPairs) {
+                            if (turned[n])
+                                weigh(b[n], place[n] + P.half < P.norm_dim ? norm : 1.0f, place[n] + P.half);
+                        }
+                    }
+                }
             }
             if (to != nullptr) {
-                const float2 *const angles = cs + row * P.half;
-                // codes: what is not turned is brought to its scale here
-                const float apart = kTo == kCodes && P.code_inverse != 0.0f ? norm * P.code_inverse : norm;
+                if (kTo != kRows)
+                    to += here_unit * P.head_dim * kBytes;
+                const float2 *const angles = cs + here * P.half;
 #pragma unroll
                 for (int n = 0; n < kItems; n++) {
                     if (!there[n])
                         continue;
-                    float a[8];
-                    widen_values<T2, 8>(a, lo[n]);
                     uint8_t *const at = to + place[n] * kBytes;
-                    if (normed[n]) {
-                        const float f = turned[n] ? norm : apart;
-#pragma unroll
-                        for (int k = 0; k < 8; k++)
-                            a[k] = a[k] * f * weight[n][k];
-                    } else if (kTo == kCodes && !turned[n]) {
-                        store_values<T2, 8, kTo>(P, at, a);  // as lmc_append does
-                        continue;
-                    }
                     if (turned[n]) {
                         if constexpr (kPairs) {
                             const float4 *const r = reinterpret_cast<const float4 *>(angles + (lane + n * P.group) * 4);
 #pragma unroll
                             for (int k = 0; k < 2; k++) {
                                 const float4 c = r[k];
-                                const float w = a[4 * k], x = a[4 * k + 1], y = a[4 * k + 2], z = a[4 * k + 3];
-                                a[4 * k] = w * c.x - x * c.y;
-                                a[4 * k + 1] = w * c.y + x * c.x;
-                                a[4 * k + 2] = y * c.z - z * c.w;
-                                a[4 * k + 3] = y * c.w + z * c.z;
+                                const float2 u = apart(a[n][2 * k]), v = apart(a[n][2 * k + 1]);
+                                a[n][2 * k] = plus_product(two(u.x, u.x), two(c.x, c.y), two(u.y, u.y) * two(-c.y, c.x));
+                                a[n][2 * k + 1] = plus_product(two(v.x, v.x), two(c.z, c.w), two(v.y, v.y) * two(-c.w, c.z));
                             }
                         } else {
-                            float b[8];
-                            widen_values<T2, 8>(b, hi[n]);
-                            if (place[n] + P.half < P.norm_dim) {
-                                if constexpr (kItems > 1)
-                                    weights_at(weight2[0], place[n] + P.half);
-#pragma unroll
-                                for (int k = 0; k < 8; k++)
-                                    b[k] = b[k] * norm * weight2[0][k];
-                            }
                             const float4 *const r = reinterpret_cast<const float4 *>(angles + (lane + n * P.group) * 8);
 #pragma unroll
                             for (int k = 0; k < 4; k++) {
                                 const float4 c = r[k];
-                                const float w = a[2 * k], x = b[2 * k], y = a[2 * k + 1], z = b[2 * k + 1];
-                                a[2 * k] = w * c.x - x * c.y;
-                                b[2 * k] = w * c.y + x * c.x;
-                                a[2 * k + 1] = y * c.z - z * c.w;
-                                b[2 * k + 1] = y * c.w + z * c.z;
+                                const Two u = a[n][k], v = b[n][k], cosine = two(c.x, c.z);
+                                a[n][k] = plus_product(u, cosine, v * two(-c.y, -c.w));
+                                b[n][k] = plus_product(v, cosine, u * two(c.y, c.w));
                             }
-                            store_scaled<T2, 8, kTo>(P, at + P.half * kBytes, b);
+                            put(at + P.half * kBytes, b[n]);
                         }
+                    } else if (kTo == kCodes && plain[n]) {
+                        float y[8];  // as lmc_append does
+#pragma unroll
+                        for (int k = 0; k < 4; k++) {
+                            const float2 v = apart(a[n][k]);
+                            y[2 * k] = v.x;
+                            y[2 * k + 1] = v.y;
+                        }
+                        store_values<T2, 8, kTo>(P, at, y);
+                        continue;
                     }
-                    store_scaled<T2, 8, kTo>(P, at, a);
+                    put(at, a[n]);
                 }
             }
-        } else if (to != nullptr) {
-            const int most = min(P.rest_unit, P.rest - (unit - P.heads) * P.rest_unit) / 8;
+        } else {
+            const int from = (unit - P.heads) * P.rest_unit, most = to == nullptr ? 0 : min(P.rest_unit, P.rest - from) / 8;
+            to += (P.heads * P.head_dim + from) * kBytes;
+            uint4 x[kItems];
 #pragma unroll
             for (int n = 0; n < kItems; n++)
+                x[n] = lo[n];
+            row += P.row_step;
+            unit += P.unit_step;
+            if (unit >= P.units) {
+                unit -= P.units;
+                row++;
+            }
+            if (row < rows)
+                load();
+#pragma unroll
+            for (int n = 0; n < kItems; n++) {
                 if (lane + n * P.group < most) {
-                    float a[8];
-                    widen_values<T2, 8>(a, lo[n]);
-                    store_values<T2, 8, kTo>(P, to + 8 * (lane + n * P.group) * kBytes, a);
+                    uint8_t *const at = to + 8 * (lane + n * P.group) * kBytes;
+                    if constexpr (kTo == kCodes) {
+                        const uint32_t raw[4] = {x[n].x, x[n].y, x[n].z, x[n].w};
+                        float y[8];
+                        widen_values<T2, 8>(y, raw);
+                        store_values<T2, 8, kTo>(P, at, y);
+                    } else {
+                        __stcs(reinterpret_cast<uint4 *>(at), x[n]);
+                    }
                 }
+            }
         }
-        row += P.row_step;
-        unit += P.unit_step;
-        if (unit >= P.units) {
-            unit -= P.units;
-            row++;
-        }
-        if (row < rows)
-            load();
     }
 }
 
@@ -485,7 +560,7 @@ __global__ void __launch_bounds__(kThreads) lmc_rotate_kernel(const __grid_const
     const int rows = (int)min((int64_t)P.rows_per_cta, P.num_rows - row0);
     wait_for_launch();
     let_next_start();
-    make_angles<kTo>(P, cs, reinterpret_cast<uint64_t *>(cs + rows * P.half), dst, row0, rows);
+    make_angles<kTo>(P, cs, reinterpret_cast<uint64_t *>(cs + P.rows_per_cta * P.half), dst, row0, rows);
     __syncthreads();
 
     const int lane = threadIdx.x & (P.group - 1);
@@ -613,7 +688,8 @@ int launch(RotatePlan &P, int width, cudaStream_t stream) {
         kern = per_lane == 3   ? lmc_rotate_eights_kernel<T2, 3, false, kTo>
                : per_lane == 2 ? lmc_rotate_eights_kernel<T2, 2, false, kTo>
                                : lmc_rotate_eights_kernel<T2, 1, false, kTo>;
-    const size_t smem = (size_t)rows * P.half * sizeof(float2) + (size_t)P.half * sizeof(uint64_t);
+    const size_t smem = (size_t)rows * P.half * sizeof(float2) + (size_t)(P.half + 1) / 2 * 2 * sizeof(uint64_t) +
+                        (width == 8 && per_lane <= 3 && P.norm_dim > 0 ? (size_t)P.head_dim * sizeof(float) : 0);
     return follow(kern, dim3((unsigned)grid), kThreads, smem, stream, P) ? LMC_OK : LMC_ERR_CUDA;
 }
 
