@@ -317,10 +317,6 @@ __device__ __forceinline__ void scan_wait(ScanControl &C, uint64_t *bar, uint32_
     } while (done == 0);
 }
 
-__device__ __forceinline__ bool scan_gone(ScanControl &C) {
-    return __any_sync(0xffffffffu, *(volatile uint32_t *)&C.gave_up != 0);
-}
-
 // A of the product from tensor memory.
 __device__ __forceinline__ void mma_held(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
     asm volatile(
@@ -545,8 +541,10 @@ __device__ __forceinline__ void sum_decays(Decays &D, float g0, float g1, int ro
     }
 }
 
-// One warp: q, k and v of each tile by TMA. (Rows behind a tile's last one come
-// along; they are not read into a result.)
+// The roles that only ask for copies and products are one thread each.
+
+// q, k and v of each tile by TMA. (Rows behind a tile's last one come along; they
+// are not read into a result.)
 template <bool kStatesOnly>
 __device__ __forceinline__ void load_tiles(const ScanPlan &P, ScanControl &C, uint8_t *mem) {
     int looks = kLooks;
@@ -554,34 +552,30 @@ __device__ __forceinline__ void load_tiles(const ScanPlan &P, ScanControl &C, ui
     const int h = C.item.h, kh = h / P.L.shared;
     const uint32_t bytes = (uint32_t)((kStatesOnly ? 1 : 2) * P.k_panels + P.v_panels) * kPanel;
     uint32_t asked = 0;
+#pragma unroll 1
     while (T.next()) {
-        const int st = (int)uniform(asked % kStages);
+        const uint32_t st = asked % kStages;
         if (asked >= kStages)
             scan_wait(C, &C.free[st], (asked / kStages - 1) & 1, looks);
-        if (scan_gone(C))
+        if (*(volatile uint32_t *)&C.gave_up)
             break;
         uint8_t *to = mem + st * kStageBytes;
-        const int row = (int)uniform(T.row);
-        if (elect()) {
-            uint64_t *bar = &C.full[st];
-            bar_expect(bar, bytes);
+        uint64_t *bar = &C.full[st];
+        bar_expect(bar, bytes);
+#pragma unroll 1
+        for (int i = 0; i < P.k_copies; i++)
+            tma_box(&P.k, to + 2 * kPanel + i * kPanel, i * 64, T.row, kh, bar);
+#pragma unroll 1
+        for (int i = 0; i < P.v_copies; i++)
+            tma_box(&P.v, to + 4 * kPanel + i * kPanel, i * 64, T.row, h, bar);
+        if (!kStatesOnly) {
 #pragma unroll 1
             for (int i = 0; i < P.k_copies; i++)
-                tma_box(&P.k, to + 2 * kPanel + i * kPanel, i * 64, row, kh, bar);
-#pragma unroll 1
-            for (int i = 0; i < P.v_copies; i++)
-                tma_box(&P.v, to + 4 * kPanel + i * kPanel, i * 64, row, h, bar);
-            if (!kStatesOnly) {
-#pragma unroll 1
-                for (int i = 0; i < P.k_copies; i++)
-                    tma_box(&P.q, to + i * kPanel, i * 64, row, kh, bar);
-            }
+                tma_box(&P.q, to + i * kPanel, i * 64, T.row, kh, bar);
         }
-        __syncwarp();
         asked++;
     }
-    if ((threadIdx.x & 31) == 0)
-        C.tiles = asked;
+    C.tiles = asked;
 }
 
 // One warp: each tile's decays. They go to their place of the ring when the stage
@@ -629,13 +623,13 @@ __device__ __forceinline__ void tell_decays(const ScanPlan &P, ScanControl &C) {
     }
 }
 
-// One warp: the products that need no state. Scores Q K^T [tokens x tokens], and
-// what the tile adds to the state, turned: (V decayed)^T K [values x keys].
+// The products that need no state. Scores Q K^T [tokens x tokens], and what the
+// tile adds to the state, turned: (V decayed)^T K [values x keys].
 template <bool kBf16, bool kStatesOnly>
 __device__ __forceinline__ void multiply_forward(const ScanPlan &P, ScanControl &C, uint8_t *mem) {
     int looks = kLooks;
-    const uint32_t tmem = uniform(C.tmem);
-    const int keys = 64 * P.k_panels, steps = (P.L.dk + 15) / 16, tiles = (int)uniform(C.item.tiles);
+    constexpr uint32_t tmem = 0;  // all of it: see the kernel
+    const int keys = 64 * P.k_panels, steps = (P.L.dk + 15) / 16, tiles = C.item.tiles;
     const uint32_t scores = instruction(kBf16, false, 64, kTile);
     const uint32_t update = instruction(kBf16, false, 128, keys) | 1u << 16;  // B turned
     constexpr int kSteps = (kBf16 ? 2 : 1) * (kTile / 16);  // of a half of the parts
@@ -643,86 +637,71 @@ __device__ __forceinline__ void multiply_forward(const ScanPlan &P, ScanControl 
     const uint64_t k0 = matrix(smem_addr(mem) + 2 * kPanel, kPanel, 1024);
 #pragma unroll 1
     for (int n = 0; n < tiles; n++) {
-        const int st = n % kStages, stage = st * (kStageBytes >> 4);
+        const int st = n % kStages;
+        const uint64_t q = q0 + st * (kStageBytes >> 4), k = k0 + st * (kStageBytes >> 4);
         scan_wait(C, &C.full[st], (n / kStages) & 1, looks);
         if (!kStatesOnly) {
             if (n >= 1)
                 scan_wait(C, &C.score_free, (n - 1) & 1, looks);
-            __syncwarp();
             fence_after();
-            if (elect()) {
-#pragma unroll 1
-                for (int s = 0; s < steps; s++) {
-                    const uint64_t q = q0 + (stage + (s >> 2) * (kPanel >> 4) + (s & 3) * 2);
-                    mma(tmem + kScores, q, q + (2 * kPanel >> 4), scores, s > 0);
-                }
-                commit(&C.score_full);
-            }
-            __syncwarp();
+#pragma unroll
+            for (int s = 0; s < kMaxDim / 16; s++)
+                if (s < steps)
+                    mma(tmem + kScores, q + ((s >> 2) * (kPanel >> 4) + (s & 3) * 2),
+                        q + ((2 * kPanel >> 4) + (s >> 2) * (kPanel >> 4) + (s & 3) * 2), scores, s > 0);
+            commit(&C.score_full);
         }
         // as the parts come: the upper one or two, then the lower
         if (n >= 1)
             scan_wait(C, &C.update_free, (n - 1) & 1, looks);
-#pragma unroll 1
+#pragma unroll
         for (int half = 0; half < 2; half++) {
             scan_wait(C, &C.parts_full[half], n & 1, looks);
-            __syncwarp();
             fence_after();
-            if (elect()) {
-#pragma unroll 4
-                for (int s = kSteps * half; s < kSteps * (half + 1); s++)
-                    mma_held(tmem + kUpdate, tmem + kParts + 8 * s, k0 + (stage + (s & 3) * (2048 >> 4)), update, s > 0);
-                commit(&C.parts_free[half]);
-                if (half == 1) {
-                    commit(&C.update_full);
-                    commit(&C.free[st]);
-                }
-            }
-            __syncwarp();
+#pragma unroll
+            for (int s = kSteps * half; s < kSteps * (half + 1); s++)
+                mma_held(tmem + kUpdate, tmem + kParts + 8 * s, k + (s & 3) * (2048 >> 4), update, s > 0);
+            commit(&C.parts_free[half]);
         }
+        commit(&C.update_full);
+        commit(&C.free[st]);
     }
 }
 
-// One warp: the products that make the result, turned: S^T Q^T from the state
-// before the tile, V^T P^T from the tile's own tokens [values x tokens].
+// The products that make the result, turned: S^T Q^T from the state before the
+// tile, V^T P^T from the tile's own tokens [values x tokens].
 template <bool kBf16>
 __device__ __forceinline__ void multiply_state(const ScanPlan &P, ScanControl &C, uint8_t *mem) {
     int looks = kLooks;
-    const uint32_t tmem = uniform(C.tmem);
-    const int steps = (P.L.dk + 15) / 16, tiles = (int)uniform(C.item.tiles);
+    constexpr uint32_t tmem = 0;
+    const int steps = (P.L.dk + 15) / 16, tiles = C.item.tiles;
     const uint32_t from_state = instruction(kBf16, false, 128, kTile), from_tile = instruction(kBf16, true, 128, kTile);
     const uint64_t weight = matrix(smem_addr(mem) + kWeightsAt, 16, 1024);
     const uint64_t q0 = matrix(smem_addr(mem), 16, 1024);
     const uint64_t v0 = matrix(smem_addr(mem) + 4 * kPanel, kPanel, 1024);
 #pragma unroll 1
     for (int n = 0; n < tiles; n++) {
-        const int st = n % kStages, stage = st * (kStageBytes >> 4);
+        const int st = n % kStages;
+        const uint64_t q = q0 + st * (kStageBytes >> 4), v = v0 + st * (kStageBytes >> 4);
         scan_wait(C, &C.full[st], (n / kStages) & 1, looks);
         scan_wait(C, &C.state_full, n & 1, looks);
         if (n >= 1)
             scan_wait(C, &C.out_free, (n - 1) & 1, looks);
-        __syncwarp();
         fence_after();
-        if (elect()) {
-#pragma unroll 1
-            for (int s = 0; s < steps; s++)
-                mma_held(tmem + kFromState, tmem + kState + 8 * s, q0 + (stage + (s >> 2) * (kPanel >> 4) + (s & 3) * 2),
-                         from_state, s > 0);
-            commit(&C.state_free);
-        }
-        __syncwarp();
+#pragma unroll
+        for (int s = 0; s < kMaxDim / 16; s++)
+            if (s < steps)
+                mma_held(tmem + kFromState, tmem + kState + 8 * s, q + ((s >> 2) * (kPanel >> 4) + (s & 3) * 2), from_state,
+                         s > 0);
+        commit(&C.state_free);
         scan_wait(C, &C.weight_full, n & 1, looks);
-        __syncwarp();
         fence_after();
-        if (elect()) {
-#pragma unroll 1
-            for (int s = 0; s < kTile / 16; s++)
-                mma(tmem + kFromTile, v0 + (stage + s * (2048 >> 4)), weight + s * 2, from_tile, s > 0);
-            commit(&C.out_full);
-            commit(&C.weight_free);
-            commit(&C.free[st]);
-        }
-        __syncwarp();
+#pragma unroll
+        for (int s = 0; s < kTile / 16; s++)
+            mma(tmem + kFromTile, v + s * (2048 >> 4), weight + s * 2, from_tile, s > 0);
+        commit(&C.out_full);
+        commit(&C.weight_free);
+        commit(&C.free[st]);
     }
 }
 
@@ -1287,14 +1266,16 @@ __global__ void __launch_bounds__(kScanThreads, 1) lmc_linear_scan_kernel(const 
             deliver<kBf16>(P, C, scan_mem);
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegisters));
-        if (warp == kLoadWarp)
-            load_tiles<kStatesOnly>(P, C, scan_mem);
-        else if (warp == kDecayWarp)
+        if (warp == kDecayWarp) {
             tell_decays<kBf16>(P, C);
-        else if (warp == kForwardWarp)
-            multiply_forward<kBf16, kStatesOnly>(P, C, scan_mem);
-        else if (warp == kStateProductWarp && !kStatesOnly)
-            multiply_state<kBf16>(P, C, scan_mem);
+        } else if (elect()) {
+            if (warp == kLoadWarp)
+                load_tiles<kStatesOnly>(P, C, scan_mem);
+            else if (warp == kForwardWarp)
+                multiply_forward<kBf16, kStatesOnly>(P, C, scan_mem);
+            else if (!kStatesOnly)
+                multiply_state<kBf16>(P, C, scan_mem);
+        }
     }
     __syncwarp();
     fence_before();
