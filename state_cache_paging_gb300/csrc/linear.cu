@@ -204,7 +204,6 @@ constexpr uint32_t kLook = 20000;  // so many ns each
 // columns of tensor memory
 constexpr uint32_t kScores = 0, kUpdate = 64, kFromState = 192, kFromTile = 256, kState = 320, kParts = 384;
 constexpr uint32_t kPartColumns = kTile / 2;
-constexpr int kDecaysAhead = 4 * kTile;  // tokens whose decays are sent on to L2
 constexpr int kRing = 4;              // tiles whose decays are at hand
 constexpr int kSms = 152;
 constexpr int64_t kLeastSegment = 512;  // tokens
@@ -317,13 +316,28 @@ __device__ __forceinline__ void scan_wait(ScanControl &C, uint64_t *bar, uint32_
     } while (done == 0);
 }
 
-// A of the product from tensor memory.
-__device__ __forceinline__ void mma_held(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
+// Products with descriptors given by their lower words (the upper one is the same for
+// all of a kind: strides and swizzle): half of what has to be brought to uniform
+// registers. The first with A from shared memory, the second from tensor memory.
+constexpr uint32_t kMatrixUpper = 1024 >> 4 | 1u << 14 | 2u << 29;
+__device__ __forceinline__ uint32_t lower(uint32_t addr, uint32_t leading) { return (addr >> 4 & 0x3FFF) | (leading >> 4) << 16; }
+__device__ __forceinline__ void multiply(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool add) {
     asm volatile(
-        "{\n\t.reg .pred p;\n\t"
+        "{\n\t.reg .pred p;\n\t.reg .b64 x, y;\n\t"
         "setp.ne.u32 p, %4, 0;\n\t"
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
-        "r"(a), "l"(b), "r"(idesc), "r"((uint32_t)add)
+        "mov.b64 x, {%1, %5};\n\t"
+        "mov.b64 y, {%2, %5};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "r"((uint32_t)add), "r"(kMatrixUpper)
+        : "memory");
+}
+__device__ __forceinline__ void multiply_held(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, bool add) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t.reg .b64 y;\n\t"
+        "setp.ne.u32 p, %4, 0;\n\t"
+        "mov.b64 y, {%2, %5};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "r"((uint32_t)add), "r"(kMatrixUpper)
         : "memory");
 }
 
@@ -585,35 +599,22 @@ template <bool kBf16>
 __device__ __forceinline__ void tell_decays(const ScanPlan &P, ScanControl &C) {
     static_assert(kRing >= kStages, "a place is read until the next tile's result is made");
     int looks = kLooks;
-    Tiles T(C.item, P.L.block_size), ahead(C.item, P.L.block_size);
-    const int lane = threadIdx.x & 31;
+    Tiles T(C.item, P.L.block_size);
+    const int lane = threadIdx.x & 31, end = C.item.row + C.item.count;
     const float *const decay = P.L.decay + (int64_t)C.item.h * P.L.decay_head;
     float drift = 0.0f, g0, g1;
-    // (sent on to L2 some tiles before: under load HBM takes longer than a tile)
-    const int end = C.item.row + C.item.count;
-    auto send = [&](int row) {
-        if (row < end)
-            asm volatile("prefetch.global.L2 [%0];" ::"l"(decay + (int64_t)row * P.L.decay_row) : "memory");
+    // of 64 tokens from a row on, a tile ahead (whose tokens they are shows later)
+    auto fetch = [&](int row) {
+        const int64_t x = (int64_t)row + 2 * lane;
+        const float *const at = decay + x * P.L.decay_row;
+        g0 = x < end ? *at : 0.0f;
+        g1 = x + 1 < end ? at[P.L.decay_row] : 0.0f;
     };
-    for (int t = lane; t < kDecaysAhead; t += 32)
-        send(C.item.row + t);
-    auto fetch = [&] {
-        g0 = g1 = 0.0f;
-        if (ahead.next()) {
-            send(ahead.row + kDecaysAhead + lane);
-            send(ahead.row + kDecaysAhead + 32 + lane);
-            const float *const at = decay + ((int64_t)ahead.row + 2 * lane) * P.L.decay_row;
-            if (2 * lane < ahead.rows)
-                g0 = *at;
-            if (2 * lane + 1 < ahead.rows)
-                g1 = at[P.L.decay_row];
-        }
-    };
-    fetch();
+    fetch(C.item.row);
     while (T.next()) {
         const uint32_t n = T.n;
-        const float h0 = g0, h1 = g1;
-        fetch();
+        const float h0 = 2 * lane < T.rows ? g0 : 0.0f, h1 = 2 * lane + 1 < T.rows ? g1 : 0.0f;
+        fetch(T.row + T.rows);
         if (n + 1 >= kStages)
             scan_wait(C, &C.free[(n + 1) % kStages], ((n + 1) / kStages - 1) & 1, looks);
         sum_decays<kBf16>(C.decays[n % kRing], h0, h1, T.rows, P.L.scale, drift);
@@ -633,12 +634,12 @@ __device__ __forceinline__ void multiply_forward(const ScanPlan &P, ScanControl 
     const uint32_t scores = instruction(kBf16, false, 64, kTile);
     const uint32_t update = instruction(kBf16, false, 128, keys) | 1u << 16;  // B turned
     constexpr int kSteps = (kBf16 ? 2 : 1) * (kTile / 16);  // of a half of the parts
-    const uint64_t q0 = matrix(smem_addr(mem), 16, 1024);
-    const uint64_t k0 = matrix(smem_addr(mem) + 2 * kPanel, kPanel, 1024);
+    const uint32_t q0 = lower(smem_addr(mem), 16);
+    const uint32_t k0 = lower(smem_addr(mem) + 2 * kPanel, kPanel);
 #pragma unroll 1
     for (int n = 0; n < tiles; n++) {
         const int st = n % kStages;
-        const uint64_t q = q0 + st * (kStageBytes >> 4), k = k0 + st * (kStageBytes >> 4);
+        const uint32_t q = q0 + st * (kStageBytes >> 4), k = k0 + st * (kStageBytes >> 4);
         scan_wait(C, &C.full[st], (n / kStages) & 1, looks);
         if (!kStatesOnly) {
             if (n >= 1)
@@ -647,7 +648,7 @@ __device__ __forceinline__ void multiply_forward(const ScanPlan &P, ScanControl 
 #pragma unroll
             for (int s = 0; s < kMaxDim / 16; s++)
                 if (s < steps)
-                    mma(tmem + kScores, q + ((s >> 2) * (kPanel >> 4) + (s & 3) * 2),
+                    multiply(tmem + kScores, q + ((s >> 2) * (kPanel >> 4) + (s & 3) * 2),
                         q + ((2 * kPanel >> 4) + (s >> 2) * (kPanel >> 4) + (s & 3) * 2), scores, s > 0);
             commit(&C.score_full);
         }
@@ -660,7 +661,7 @@ __device__ __forceinline__ void multiply_forward(const ScanPlan &P, ScanControl 
             fence_after();
 #pragma unroll
             for (int s = kSteps * half; s < kSteps * (half + 1); s++)
-                mma_held(tmem + kUpdate, tmem + kParts + 8 * s, k + (s & 3) * (2048 >> 4), update, s > 0);
+                multiply_held(tmem + kUpdate, tmem + kParts + 8 * s, k + (s & 3) * (2048 >> 4), update, s > 0);
             commit(&C.parts_free[half]);
         }
         commit(&C.update_full);
@@ -676,13 +677,13 @@ __device__ __forceinline__ void multiply_state(const ScanPlan &P, ScanControl &C
     constexpr uint32_t tmem = 0;
     const int steps = (P.L.dk + 15) / 16, tiles = C.item.tiles;
     const uint32_t from_state = instruction(kBf16, false, 128, kTile), from_tile = instruction(kBf16, true, 128, kTile);
-    const uint64_t weight = matrix(smem_addr(mem) + kWeightsAt, 16, 1024);
-    const uint64_t q0 = matrix(smem_addr(mem), 16, 1024);
-    const uint64_t v0 = matrix(smem_addr(mem) + 4 * kPanel, kPanel, 1024);
+    const uint32_t weight = lower(smem_addr(mem) + kWeightsAt, 16);
+    const uint32_t q0 = lower(smem_addr(mem), 16);
+    const uint32_t v0 = lower(smem_addr(mem) + 4 * kPanel, kPanel);
 #pragma unroll 1
     for (int n = 0; n < tiles; n++) {
         const int st = n % kStages;
-        const uint64_t q = q0 + st * (kStageBytes >> 4), v = v0 + st * (kStageBytes >> 4);
+        const uint32_t q = q0 + st * (kStageBytes >> 4), v = v0 + st * (kStageBytes >> 4);
         scan_wait(C, &C.full[st], (n / kStages) & 1, looks);
         scan_wait(C, &C.state_full, n & 1, looks);
         if (n >= 1)
@@ -691,14 +692,14 @@ __device__ __forceinline__ void multiply_state(const ScanPlan &P, ScanControl &C
 #pragma unroll
         for (int s = 0; s < kMaxDim / 16; s++)
             if (s < steps)
-                mma_held(tmem + kFromState, tmem + kState + 8 * s, q + ((s >> 2) * (kPanel >> 4) + (s & 3) * 2), from_state,
+                multiply_held(tmem + kFromState, tmem + kState + 8 * s, q + ((s >> 2) * (kPanel >> 4) + (s & 3) * 2), from_state,
                          s > 0);
         commit(&C.state_free);
         scan_wait(C, &C.weight_full, n & 1, looks);
         fence_after();
 #pragma unroll
         for (int s = 0; s < kTile / 16; s++)
-            mma(tmem + kFromTile, v + s * (2048 >> 4), weight + s * 2, from_tile, s > 0);
+            multiply(tmem + kFromTile, v + s * (2048 >> 4), weight + s * 2, from_tile, s > 0);
         commit(&C.out_full);
         commit(&C.weight_free);
         commit(&C.free[st]);
