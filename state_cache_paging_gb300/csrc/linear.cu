@@ -187,14 +187,14 @@ constexpr int kPanel = kTile * 128;   // bytes of 64 values of a tile's rows
 constexpr int kStages = 4;
 constexpr int kStageBytes = 6 * kPanel;  // q, k, v, two panels each
 constexpr int kStateWarps = 8;
-constexpr int kFirstPartWarp = 8, kPartWarps = 4;
-constexpr int kFirstWeightWarp = 12, kWeightWarps = 4;
-constexpr int kFirstResultWarp = 16, kResultWarps = 4;
-constexpr int kLoadWarp = 20, kForwardWarp = 21, kStateProductWarp = 22, kDecayWarp = 23;
-constexpr int kScanThreads = 24 * 32;
-// Registers per thread of the warpgroups: 2 x 120 + 88 + 56 + 56 + 40 of the 6 x 80
-// the CTA starts with.
-constexpr int kStateRegisters = 120, kPartRegisters = 88, kWeightRegisters = 56, kResultRegisters = 56, kOtherRegisters = 40;
+constexpr int kFirstPartWarp = 8, kPartWarps = 8;
+constexpr int kFirstWeightWarp = 16, kWeightWarps = 4;
+constexpr int kFirstResultWarp = 20, kResultWarps = 4;
+constexpr int kLoadWarp = 24, kForwardWarp = 25, kStateProductWarp = 26, kDecayWarp = 27;
+constexpr int kScanThreads = 28 * 32;
+// Registers per thread of the warpgroups: 2 x 112 + 2 x 64 + 56 + 56 + 40 of the 7 x
+// 72 the CTA starts with.
+constexpr int kStateRegisters = 112, kPartRegisters = 64, kWeightRegisters = 56, kResultRegisters = 56, kOtherRegisters = 40;
 // shared memory behind the stages: the weights, the result on its way
 constexpr int kWeightsAt = kStages * kStageBytes, kResultAt = kWeightsAt + kPanel;
 constexpr int kWarpResult = kTile * 64;  // bytes of a warp's part of a result: 32 values of each token
@@ -341,12 +341,12 @@ __device__ __forceinline__ void multiply_held(uint32_t d, uint32_t a, uint32_t b
         : "memory");
 }
 
-// Rows of `panels` panels behind a tile's last one, cleared by four warps: they
+// Rows of two panels behind a tile's last one, cleared by `threads` threads: they
 // belong to others, and take part in products times 0, which infinities and NaN
 // would not bear.
-__device__ __forceinline__ void clear_rows(uint8_t *panels, int rows, int tid) {
+__device__ __forceinline__ void clear_rows(uint8_t *panels, int rows, int tid, int threads) {
 #pragma unroll 1
-    for (int c = tid; c < 2 * (kPanel / 16); c += 128)
+    for (int c = tid; c < 2 * (kPanel / 16); c += threads)
         if ((c >> 3 & (kTile - 1)) >= rows)
             *reinterpret_cast<uint4 *>(panels + c * 16) = make_uint4(0, 0, 0, 0);
 }
@@ -356,6 +356,19 @@ __device__ __forceinline__ void load_s8(uint32_t (&s)[8], uint32_t addr) {
     asm volatile("tcgen05.ld.sync.aligned.16x256b.x2.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
                  : "=r"(s[0]), "=r"(s[1]), "=r"(s[2]), "=r"(s[3]), "=r"(s[4]), "=r"(s[5]), "=r"(s[6]), "=r"(s[7])
                  : "r"(addr)
+                 : "memory");
+}
+
+// 32 lanes x 8 columns: a lane's row.
+__device__ __forceinline__ void load_o8(uint32_t (&o)[8], uint32_t addr) {
+    asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0, %1, %2, %3, %4, %5, %6, %7}, [%8];"
+                 : "=r"(o[0]), "=r"(o[1]), "=r"(o[2]), "=r"(o[3]), "=r"(o[4]), "=r"(o[5]), "=r"(o[6]), "=r"(o[7])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void store_o8(const uint32_t (&o)[8], uint32_t addr) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%8], {%0, %1, %2, %3, %4, %5, %6, %7};" ::"r"(o[0]), "r"(o[1]),
+                 "r"(o[2]), "r"(o[3]), "r"(o[4]), "r"(o[5]), "r"(o[6]), "r"(o[7]), "r"(addr)
                  : "memory");
 }
 
@@ -373,15 +386,12 @@ __device__ __forceinline__ void store_turned(uint32_t addr, uint32_t a, uint32_t
                  "r"(c), "r"(d)
                  : "memory");
 }
-// 16 lanes x 32 columns of tensor memory: lane l of the warp holds rows l / 4
+// 16 lanes x 16 columns of tensor memory: lane l of the warp holds rows l / 4
 // (v[2 i]) and l / 4 + 8 (v[2 i + 1]), column 4 i + l % 4.
-__device__ __forceinline__ void store_part(uint32_t addr, const uint32_t (&v)[16]) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.16x128b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
-        "%16};" ::"r"(addr),
-        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]), "r"(v[9]),
-        "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
-        : "memory");
+__device__ __forceinline__ void store_part(uint32_t addr, const uint32_t (&v)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.16x128b.x4.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(addr), "r"(v[0]),
+                 "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7])
+                 : "memory");
 }
 
 __device__ __forceinline__ uint32_t times(uint32_t a, uint32_t b) {
@@ -706,19 +716,43 @@ __device__ __forceinline__ void multiply_state(const ScanPlan &P, ScanControl &C
     }
 }
 
-// What a lane holds of 16 values' 64 tokens (load_turned): those behind the
-// tile's last row become 0.
-__device__ __forceinline__ void keep_rows(uint32_t (&v)[16], int rows) {
+// What a lane holds of 16 values and 32 tokens from `first` on (load_turned): those
+// behind the tile's last row become 0.
+__device__ __forceinline__ void keep_rows(uint32_t (&v)[8], int first, int rows) {
     const int lane = threadIdx.x & 31;
 #pragma unroll
-    for (int k = 0; k < 16; k++) {
-        const int t = 8 * (k >> 1) + 2 * (lane & 3);
+    for (int k = 0; k < 8; k++) {
+        const int t = first + 8 * (k >> 1) + 2 * (lane & 3);
         v[k] &= (t < rows ? 0xffffu : 0u) | (t + 1 < rows ? 0xffff0000u : 0u);
     }
 }
 
-// Four warps: v times the decay to the tile's end, turned, in parts of 16 bits,
-// to tensor memory (warp w: values 32 w .. 32 w + 31).
+// bf16: two parts of 16 values' products, x = rn(v f) and y = v f - x (+ v g), of 32
+// tokens.
+template <bool kLower>
+__device__ __forceinline__ void split_tokens(const Decays &D, uint32_t from, uint32_t to, int half, int rows) {
+    const int lane = threadIdx.x & 31;
+    uint32_t v[8], a[8], b[8];  // [4 s + i]
+#pragma unroll
+    for (int s = 0; s < 2; s++)
+        load_turned(v + 4 * s, from + (2 * half + s) * 2048);
+    if (rows < kTile)
+        keep_rows(v, 32 * half, rows);
+#pragma unroll
+    for (int k = 0; k < 8; k++) {
+        const uint2 f = reinterpret_cast<const uint2 *>(&D.left[16 * half + 4 * (k >> 1) + (lane & 3)])[kLower];
+        a[k] = times(v[k], f.x);
+        b[k] = plus_product(v[k], f.x, minus(a[k]));
+        if (kLower)
+            b[k] = plus_product(v[k], f.y, b[k]);
+    }
+    store_part(to + 16 * half, a);
+    store_part(to + kPartColumns + 16 * half, b);
+}
+
+// Eight warps: v times the decay to the tile's end, turned, in parts of 16 bits, to
+// tensor memory: of values 32 w .. 32 w + 31 warp w takes the first 16, w + 4 the
+// last.
 //
 // What is added to the state keeps binary32's digits: with f = f1 + f2 + f3 in
 // bf16, v f = A + B + C + D where A = rn(v f1), B = v f1 - A (exact: a product of
@@ -729,12 +763,12 @@ template <bool kBf16>
 __device__ __forceinline__ void split(const ScanPlan &P, ScanControl &C, uint8_t *mem) {
     int looks = kLooks;
     Tiles T(C.item, P.L.block_size);
-    const int lane = threadIdx.x & 31, quarter = (threadIdx.x >> 5) - kFirstPartWarp;
-    const uint32_t lanes = C.tmem + ((uint32_t)(quarter * 32) << 16);
+    const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) - kFirstPartWarp, quarter = warp & 3, block = warp >> 2;
+    const uint32_t to = C.tmem + ((uint32_t)(quarter * 32 + 16 * block) << 16) + kParts;
     // the row of four 8 x 8 matrices that this lane names: tokens 8 (lane / 16) +
     // lane % 8 of a step's, values 8 (lane / 8 % 2) .. of 16
     const uint32_t values = smem_addr(mem) + 4 * kPanel + (quarter >> 1) * kPanel + (8 * (lane >> 4) + (lane & 7)) * 128;
-    const int chunk = 4 * (quarter & 1) + (lane >> 3 & 1);
+    const int chunk = 4 * (quarter & 1) + 2 * block + (lane >> 3 & 1);
     while (T.next()) {
         const uint32_t n = T.n;
         const int st = n % kStages;
@@ -742,97 +776,88 @@ __device__ __forceinline__ void split(const ScanPlan &P, ScanControl &C, uint8_t
         scan_wait(C, &C.decays_full[n % kRing], (n / kRing) & 1, looks);
         scan_wait(C, &C.full[st], (n / kStages) & 1, looks);
         if (T.rows < kTile) {  // the products' other side
-            clear_rows(mem + st * kStageBytes + 2 * kPanel, T.rows, threadIdx.x - kFirstPartWarp * 32);
+            clear_rows(mem + st * kStageBytes + 2 * kPanel, T.rows, threadIdx.x - kFirstPartWarp * 32, kPartWarps * 32);
             fence_async();
         }
-        const uint32_t from = values + st * kStageBytes;
+        const uint32_t from = values + st * kStageBytes + ((chunk ^ (lane & 7)) << 4);
         // Upper parts first: their products run while the lower are made, and the
         // next tile's upper parts are made while the lower's run. (f16's two parts
         // are made together, and go into one half each.)
         if constexpr (kBf16) {
+            if (n >= 1)
+                scan_wait(C, &C.parts_free[0], (n - 1) & 1, looks);
+            fence_after();
+#pragma unroll 1
+            for (int half = 0; half < 2; half++)
+                split_tokens<false>(D, from, to, half, T.rows);
+            wait_st();
+            fence_before();
+            __syncwarp();
+            if (lane == 0)
+                bar_arrive(&C.parts_full[0]);
+            if (n >= 1)
+                scan_wait(C, &C.parts_free[1], (n - 1) & 1, looks);
+            fence_after();
+#pragma unroll 1
+            for (int half = 0; half < 2; half++)
+                split_tokens<true>(D, from, to + 2 * kPartColumns, half, T.rows);
+            wait_st();
+            fence_before();
+            __syncwarp();
+            if (lane == 0)
+                bar_arrive(&C.parts_full[1]);
+        } else {
+            // two rounded parts of the product, whose row (a value's, of 64 tokens:
+            // four lanes) is brought below 2^15 by a power of two
+            float top[2] = {0.0f, 0.0f};
 #pragma unroll 1
             for (int half = 0; half < 2; half++) {
-                uint32_t f[8], g[8];
+                uint32_t v[8];
 #pragma unroll
-                for (int i = 0; i < 8; i++) {
-                    const uint2 x = reinterpret_cast<const uint2 *>(&D.left[4 * i + (lane & 3)])[half];
-                    f[i] = x.x, g[i] = x.y;
+                for (int s = 0; s < 2; s++)
+                    load_turned(v + 4 * s, from + (2 * half + s) * 2048);
+                if (T.rows < kTile)
+                    keep_rows(v, 32 * half, T.rows);
+#pragma unroll
+                for (int k = 0; k < 8; k++) {
+                    const float2 f = *reinterpret_cast<const float2 *>(&D.left[16 * half + 4 * (k >> 1) + (lane & 3)]);
+                    top[k & 1] = fmaxf(top[k & 1], fmaxf(fabsf(from_q(v[k] & 0xffff, false)) * f.x,
+                                                         fabsf(from_q(v[k] >> 16, false)) * f.y));
                 }
-                if (n >= 1)
-                    scan_wait(C, &C.parts_free[half], (n - 1) & 1, looks);
-                fence_after();
-#pragma unroll 1
-                for (int block = 0; block < 2; block++) {  // of 16 values
-                    uint32_t v[16], a[16], b[16];  // [4 s + i]
-#pragma unroll
-                    for (int s = 0; s < kTile / 16; s++)
-                        load_turned(v + 4 * s, from + (((chunk + 2 * block) ^ (lane & 7)) << 4) + s * 2048);
-                    if (T.rows < kTile)
-                        keep_rows(v, T.rows);
-#pragma unroll
-                    for (int k = 0; k < 16; k++) {
-                        a[k] = times(v[k], f[k >> 1]);
-                        b[k] = plus_product(v[k], f[k >> 1], minus(a[k]));
-                    }
-                    if (half == 1)
-#pragma unroll
-                        for (int k = 0; k < 16; k++)
-                            b[k] = plus_product(v[k], g[k >> 1], b[k]);
-                    const uint32_t to = lanes + ((uint32_t)(16 * block) << 16) + kParts + 2 * kPartColumns * half;
-                    store_part(to, a);
-                    store_part(to + kPartColumns, b);
-                }
-                wait_st();
-                fence_before();
-                __syncwarp();
-                if (lane == 0)
-                    bar_arrive(&C.parts_full[half]);
             }
-        } else {
+            float up[2];
+#pragma unroll
+            for (int k = 0; k < 2; k++) {
+                top[k] = fmaxf(top[k], __shfl_xor_sync(0xffffffffu, top[k], 1));
+                top[k] = fmaxf(top[k], __shfl_xor_sync(0xffffffffu, top[k], 2));
+                const int e = lift_of(top[k]);
+                up[k] = power(e);
+                if ((lane & 3) == 0)
+                    D.unit[32 * quarter + 16 * block + 8 * k + lane / 4] = power(-e);
+            }
             if (n >= 1) {
                 scan_wait(C, &C.parts_free[0], (n - 1) & 1, looks);
                 scan_wait(C, &C.parts_free[1], (n - 1) & 1, looks);
             }
             fence_after();
 #pragma unroll 1
-            for (int block = 0; block < 2; block++) {  // of 16 values
-                const uint32_t to = lanes + ((uint32_t)(16 * block) << 16) + kParts;
-                uint32_t v[16];
+            for (int half = 0; half < 2; half++) {
+                uint32_t v[8], a[8], b[8];
 #pragma unroll
-                for (int s = 0; s < kTile / 16; s++)
-                    load_turned(v + 4 * s, from + (((chunk + 2 * block) ^ (lane & 7)) << 4) + s * 2048);
+                for (int s = 0; s < 2; s++)
+                    load_turned(v + 4 * s, from + (2 * half + s) * 2048);
                 if (T.rows < kTile)
-                    keep_rows(v, T.rows);
-                // two rounded parts of the product, whose row (a value's, of 64
-                // tokens: four lanes) is brought below 2^15 by a power of two
-                float top[2] = {0.0f, 0.0f};
+                    keep_rows(v, 32 * half, T.rows);
 #pragma unroll
-                for (int k = 0; k < 16; k++) {
-                    const float2 f = *reinterpret_cast<const float2 *>(&D.left[4 * (k >> 1) + (lane & 3)]);
-                    top[k & 1] = fmaxf(top[k & 1], fmaxf(fabsf(from_q(v[k] & 0xffff, false)) * f.x,
-                                                         fabsf(from_q(v[k] >> 16, false)) * f.y));
-                }
-                float up[2];
-#pragma unroll
-                for (int k = 0; k < 2; k++) {
-                    top[k] = fmaxf(top[k], __shfl_xor_sync(0xffffffffu, top[k], 1));
-                    top[k] = fmaxf(top[k], __shfl_xor_sync(0xffffffffu, top[k], 2));
-                    const int e = lift_of(top[k]);
-                    up[k] = power(e);
-                    if ((lane & 3) == 0)
-                        D.unit[32 * quarter + 16 * block + 8 * k + lane / 4] = power(-e);
-                }
-                uint32_t a[16], b[16];
-#pragma unroll
-                for (int k = 0; k < 16; k++) {
-                    const float2 f = *reinterpret_cast<const float2 *>(&D.left[4 * (k >> 1) + (lane & 3)]);
+                for (int k = 0; k < 8; k++) {
+                    const float2 f = *reinterpret_cast<const float2 *>(&D.left[16 * half + 4 * (k >> 1) + (lane & 3)]);
                     const float x = from_q(v[k] & 0xffff, false) * f.x * up[k & 1];
                     const float y = from_q(v[k] >> 16, false) * f.y * up[k & 1];
                     a[k] = pack<false>(x, y);
                     b[k] = pack<false>(x - from_q(a[k] & 0xffff, false), y - from_q(a[k] >> 16, false));
                 }
-                store_part(to, a);
-                store_part(to + kPartColumns, b);
+                store_part(to + 16 * half, a);
+                store_part(to + kPartColumns + 16 * half, b);
             }
             wait_st();
             fence_before();
@@ -862,7 +887,7 @@ __device__ __forceinline__ void weigh(const ScanPlan &P, ScanControl &C, uint8_t
         scan_wait(C, &C.decays_full[n % kRing], (n / kRing) & 1, looks);
         if (T.rows < kTile) {
             scan_wait(C, &C.full[n % kStages], (n / kStages) & 1, looks);
-            clear_rows(mem + (n % kStages) * kStageBytes + 4 * kPanel, T.rows, threadIdx.x - kFirstWeightWarp * 32);
+            clear_rows(mem + (n % kStages) * kStageBytes + 4 * kPanel, T.rows, threadIdx.x - kFirstWeightWarp * 32, kWeightWarps * 32);
         }
         scan_wait(C, &C.score_full, n & 1, looks);
         fence_after();
@@ -1000,12 +1025,12 @@ __device__ __forceinline__ void carry(const ScanPlan &P, ScanControl &C) {
         }
         if (mine) {
 #pragma unroll
-            for (int c = 0; c < 2; c++) {
-                uint32_t x[16];
+            for (int c = 0; c < 4; c++) {
+                uint32_t x[8];
 #pragma unroll
-                for (int i = 0; i < 16; i++)
-                    x[i] = pack<kBf16>(s[32 * c + 2 * i] * up, s[32 * c + 2 * i + 1] * up);
-                store_o(x, lanes + kState + 32 * half + 16 * c);
+                for (int i = 0; i < 8; i++)
+                    x[i] = pack<kBf16>(s[16 * c + 2 * i] * up, s[16 * c + 2 * i + 1] * up);
+                store_o8(x, lanes + kState + 32 * half + 8 * c);
             }
             wait_st();
         }
@@ -1049,14 +1074,14 @@ __device__ __forceinline__ void carry(const ScanPlan &P, ScanControl &C) {
         fence_after();
         if (mine) {
 #pragma unroll
-            for (int c = 0; c < 4; c++) {
-                uint32_t u[16];
-                load_o(u, lanes + kUpdate + i0 + 16 * c);
+            for (int c = 0; c < 8; c++) {
+                uint32_t u[8];
+                load_o8(u, lanes + kUpdate + i0 + 8 * c);
                 wait_ld();
 #pragma unroll
-                for (int i = 0; i < 16; i++)
-                    s[16 * c + i] =
-                        fmaf(grow, s[16 * c + i], kBf16 ? __uint_as_float(u[i]) : __uint_as_float(u[i]) * unit);
+                for (int i = 0; i < 8; i++)
+                    s[8 * c + i] =
+                        fmaf(grow, s[8 * c + i], kBf16 ? __uint_as_float(u[i]) : __uint_as_float(u[i]) * unit);
             }
         }
         fence_before();
@@ -1255,7 +1280,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) lmc_linear_scan_kernel(const 
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kStateRegisters));
         carry<kBf16, kStatesOnly>(P, C);
     } else if (warp < kFirstWeightWarp) {
-        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kPartRegisters));
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kPartRegisters));
         split<kBf16>(P, C, scan_mem);
     } else if (warp < kFirstResultWarp) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kWeightRegisters));
