@@ -235,7 +235,7 @@ struct Item {
 // What a tile's tokens' decays give.
 struct alignas(16) Decays {
     float2 log[kTile];      // sum up to and with the token, in units of log 2 (high, low)
-    uint4 left[kTile / 2];  // from the token to the tile's end, two tokens: the first of three bf16 parts, twice, the others; or (f16) as it is
+    uint4 left[kTile / 2];  // from the token to the tile's end, two tokens: three bf16 parts, the first with a 0 behind it; or (f16) as it is
     float since[kTile];     // from the tile's start up to the token, times the call's scale
     float lift[kTile];      // f16: what the token's weights were divided by
     float unit[kMaxDim];    // f16: what a value's row of v times its decay was divided by
@@ -498,10 +498,11 @@ __device__ __forceinline__ Twice plus(const Twice &x, float high, float low) {
 template <bool kBf16>
 __device__ __forceinline__ void sum_decays(Decays &D, float g0, float g1, int rows, float scale, float &drift) {
     const int lane = threadIdx.x & 31;
-    // a NaN makes one of everything behind it
-    const uint32_t bad0 = __ballot_sync(0xffffffffu, g0 != g0), bad1 = __ballot_sync(0xffffffffu, g1 != g1);
-    const float nan = __int_as_float(0x7fffffff);
-    auto log2_of = [](float g) { return fminf(fmaxf(g, kLeastDecay), -kLeastDecay) * 1.44269504088896340736f; };
+    // (a NaN is not clamped, and makes one of everything behind it)
+    auto log2_of = [](float g) {
+        g = g < kLeastDecay ? kLeastDecay : g;
+        return (g > -kLeastDecay ? -kLeastDecay : g) * 1.44269504088896340736f;
+    };
     const float a = log2_of(g0), b = log2_of(g1);
     Twice sum = plus(Twice{a, 0.0f}, b, 0.0f);
 #pragma unroll 1
@@ -524,7 +525,7 @@ __device__ __forceinline__ void sum_decays(Decays &D, float g0, float g1, int ro
         const uint32_t p = pack<true>(f0, f1);
         const float r0 = f0 - from_q(p & 0xffff, true), r1 = f1 - from_q(p >> 16, true);
         const uint32_t q = pack<true>(r0, r1);
-        D.left[lane] = make_uint4(p, p, q, pack<true>(r0 - from_q(q & 0xffff, true), r1 - from_q(q >> 16, true)));
+        D.left[lane] = make_uint4(p, 0, q, pack<true>(r0 - from_q(q & 0xffff, true), r1 - from_q(q >> 16, true)));
     } else {
         D.left[lane] = make_uint4(__float_as_uint(f0), __float_as_uint(f1), 0, 0);
     }
@@ -552,17 +553,6 @@ __device__ __forceinline__ void sum_decays(Decays &D, float g0, float g1, int ro
     }
     if (lane == 0)
         D.grow = grow;
-    if (__builtin_expect((bad0 | bad1) != 0, 0)) {
-        const int start = min(bad0 ? 2 * (__ffs(bad0) - 1) : kTile, bad1 ? 2 * (__ffs(bad1) - 1) + 1 : kTile);
-#pragma unroll 1
-        for (int t = 2 * lane; t < 2 * lane + 2; t++)
-            if (t >= start) {
-                D.log[t] = make_float2(nan, nan);
-                D.since[t] = nan;
-            }
-        if (lane == 0)
-            D.grow = nan;
-    }
 }
 
 // The roles that only ask for copies and products are one thread each.
@@ -665,13 +655,14 @@ __device__ __forceinline__ void multiply_forward(const ScanPlan &P, ScanControl 
         // as the parts come: the upper one or two, then the lower
         if (n >= 1)
             scan_wait(C, &C.update_free, (n - 1) & 1, looks);
-#pragma unroll
+#pragma unroll 1
         for (int half = 0; half < 2; half++) {
             scan_wait(C, &C.parts_full[half], n & 1, looks);
             fence_after();
 #pragma unroll
-            for (int s = kSteps * half; s < kSteps * (half + 1); s++)
-                multiply_held(tmem + kUpdate, tmem + kParts + 8 * s, k + (s & 3) * (2048 >> 4), update, s > 0);
+            for (int s = 0; s < kSteps; s++)
+                multiply_held(tmem + kUpdate, tmem + kParts + kSteps * 8 * half + 8 * s, k + (s & 3) * (2048 >> 4), update,
+                              s > 0 || half > 0);
             commit(&C.parts_free[half]);
         }
         commit(&C.update_full);
@@ -727,29 +718,6 @@ __device__ __forceinline__ void keep_rows(uint32_t (&v)[8], int first, int rows)
     }
 }
 
-// bf16: two parts of 16 values' products, x = rn(v f) and y = v f - x (+ v g), of 32
-// tokens.
-template <bool kLower>
-__device__ __forceinline__ void split_tokens(const Decays &D, uint32_t from, uint32_t to, int half, int rows) {
-    const int lane = threadIdx.x & 31;
-    uint32_t v[8], a[8], b[8];  // [4 s + i]
-#pragma unroll
-    for (int s = 0; s < 2; s++)
-        load_turned(v + 4 * s, from + (2 * half + s) * 2048);
-    if (rows < kTile)
-        keep_rows(v, 32 * half, rows);
-#pragma unroll
-    for (int k = 0; k < 8; k++) {
-        const uint2 f = reinterpret_cast<const uint2 *>(&D.left[16 * half + 4 * (k >> 1) + (lane & 3)])[kLower];
-        a[k] = times(v[k], f.x);
-        b[k] = plus_product(v[k], f.x, minus(a[k]));
-        if (kLower)
-            b[k] = plus_product(v[k], f.y, b[k]);
-    }
-    store_part(to + 16 * half, a);
-    store_part(to + kPartColumns + 16 * half, b);
-}
-
 // Eight warps: v times the decay to the tile's end, turned, in parts of 16 bits, to
 // tensor memory: of values 32 w .. 32 w + 31 warp w takes the first 16, w + 4 the
 // last.
@@ -784,28 +752,35 @@ __device__ __forceinline__ void split(const ScanPlan &P, ScanControl &C, uint8_t
         // next tile's upper parts are made while the lower's run. (f16's two parts
         // are made together, and go into one half each.)
         if constexpr (kBf16) {
-            if (n >= 1)
-                scan_wait(C, &C.parts_free[0], (n - 1) & 1, looks);
-            fence_after();
 #pragma unroll 1
-            for (int half = 0; half < 2; half++)
-                split_tokens<false>(D, from, to, half, T.rows);
-            wait_st();
-            fence_before();
-            __syncwarp();
-            if (lane == 0)
-                bar_arrive(&C.parts_full[0]);
-            if (n >= 1)
-                scan_wait(C, &C.parts_free[1], (n - 1) & 1, looks);
-            fence_after();
+            for (int lower = 0; lower < 2; lower++) {
+                if (n >= 1)
+                    scan_wait(C, &C.parts_free[lower], (n - 1) & 1, looks);
+                fence_after();
 #pragma unroll 1
-            for (int half = 0; half < 2; half++)
-                split_tokens<true>(D, from, to + 2 * kPartColumns, half, T.rows);
-            wait_st();
-            fence_before();
-            __syncwarp();
-            if (lane == 0)
-                bar_arrive(&C.parts_full[1]);
+                for (int half = 0; half < 2; half++) {  // 32 tokens
+                    uint32_t v[8], a[8], b[8];
+#pragma unroll
+                    for (int s = 0; s < 2; s++)
+                        load_turned(v + 4 * s, from + (2 * half + s) * 2048);
+                    if (T.rows < kTile)
+                        keep_rows(v, 32 * half, T.rows);
+                    // x = rn(v f) and y = v f - x + v g, g: f3, and 0 in the upper parts
+#pragma unroll
+                    for (int k = 0; k < 8; k++) {
+                        const uint2 f = reinterpret_cast<const uint2 *>(&D.left[16 * half + 4 * (k >> 1) + (lane & 3)])[lower];
+                        a[k] = times(v[k], f.x);
+                        b[k] = plus_product(v[k], f.y, plus_product(v[k], f.x, minus(a[k])));
+                    }
+                    store_part(to + 2 * kPartColumns * lower + 16 * half, a);
+                    store_part(to + 2 * kPartColumns * lower + kPartColumns + 16 * half, b);
+                }
+                wait_st();
+                fence_before();
+                __syncwarp();
+                if (lane == 0)
+                    bar_arrive(&C.parts_full[lower]);
+            }
         } else {
             // two rounded parts of the product, whose row (a value's, of 64 tokens:
             // four lanes) is brought below 2^15 by a power of two
