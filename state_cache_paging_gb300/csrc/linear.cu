@@ -209,13 +209,13 @@ constexpr int kSms = 152;
 constexpr int64_t kLeastSegment = 512;  // tokens
 
 struct ScanPlan {
-    CUtensorMap q, k, v;
+    CUtensorMap q, k, v, out;
     LinearPlan L;
     int64_t segment;     // a request of n of these tokens (n >= 2) is cut into n segments
     float *slots;        // [num_rows / segment][H][dk][dv]: the states before segments
     float *totals;       // [num_rows / segment][H]: the decay over the segment before
     int32_t k_copies, v_copies, k_panels, v_panels;  // copies for all panels, panels
-    int32_t wide_out;    // the result is written 16 bytes at a time
+    int32_t wide_out;    // whole tiles of the result are written by TMA, others 16 bytes at a time
 };
 
 // A CTA's tokens: a segment of a request, one head.
@@ -339,6 +339,15 @@ __device__ __forceinline__ void multiply_held(uint32_t d, uint32_t a, uint32_t b
         "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %3, p;\n\t}" ::"r"(d),
         "r"(a), "r"(b), "r"(idesc), "r"((uint32_t)add), "r"(kMatrixUpper)
         : "memory");
+}
+
+// A box of the result, of a tile's rows and 32 values, to (x, row y, head w). Its
+// rows lie in shared memory as the map's 64-byte swizzle has them.
+__device__ __forceinline__ void tma_store(const CUtensorMap *map, const void *src, int x, int y, int w) {
+    asm volatile("cp.async.bulk.tensor.4d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3, %4}], [%5];" ::"l"(map),
+                 "r"(x), "r"(y), "r"(0), "r"(w), "r"(smem_addr(src))
+                 : "memory");
+    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
 }
 
 // Rows of two panels behind a tile's last one, cleared by `threads` threads: they
@@ -1106,6 +1115,9 @@ __device__ __forceinline__ void deliver(const ScanPlan &P, ScanControl &C, uint8
         }
         scan_wait(C, &C.out_full, n & 1, looks);
         fence_after();
+        if (lane == 0)
+            asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");  // the tile before's
+        __syncwarp();
         float2 since[4];
 #pragma unroll 1
         for (int part = 0; part < 4; part++) {  // 32 tokens, 16 values
@@ -1154,11 +1166,16 @@ __device__ __forceinline__ void deliver(const ScanPlan &P, ScanControl &C, uint8
         __syncwarp();
         if (lane == 0)
             bar_arrive(&C.out_free);
-        if (P.wide_out) {
+        if (P.wide_out && T.rows == kTile) {
+            fence_async();
+            __syncwarp();
+            if (lane == 0 && quarter * 32 < L.dv)
+                tma_store(&P.out, mine, quarter * 32, T.row, C.item.h);
+        } else if (P.wide_out) {
             const int v = 8 * (lane & 3), t0 = lane >> 2;
             uint16_t *out = L.out + ((int64_t)T.row + t0) * L.out_row + out_at + v;
             const bool inside = quarter * 32 + v < L.dv;
-#pragma unroll 2
+#pragma unroll 1
             for (int i = 0; i < 8; i++) {
                 const int t = 8 * i + t0;
                 const uint4 x = *reinterpret_cast<const uint4 *>(mine + t * 64 + (((lane & 3) ^ (t >> 1 & 3)) << 4));
@@ -1174,6 +1191,8 @@ __device__ __forceinline__ void deliver(const ScanPlan &P, ScanControl &C, uint8
         }
         __syncwarp();
     }
+    if (lane == 0)
+        asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
 }
 
 // A CTA that gave up: what it left running ends (or the limit runs out) before
@@ -1466,9 +1485,10 @@ ScanWork scan_work(int64_t rec_bytes, int64_t H, int64_t num_rows) {
 }
 
 // (values, rows, heads) of 16 bits each, read in boxes of a tile's rows of one
-// head: of both panels of 64 values at once (`whole`), or of one.
+// head: of both panels of 64 values at once (`whole`), or of one; or written (`result`)
+// in boxes of 32 values.
 bool rows_map(CUtensorMap *map, bool bf16, const void *base, int64_t dim, int64_t rows, int64_t heads, int64_t row,
-              int64_t head, bool whole) {
+              int64_t head, bool whole, bool result = false) {
     const EncodeTiled fn = encoder();
     if (fn == nullptr)
         return false;
@@ -1477,12 +1497,12 @@ bool rows_map(CUtensorMap *map, bool bf16, const void *base, int64_t dim, int64_
     const cuuint64_t head_bytes = heads > 1 ? (cuuint64_t)head * 2 : (cuuint64_t)dim * 2;
     const cuuint64_t dims[4] = {whole ? 64 : (cuuint64_t)dim, (cuuint64_t)rows, panels, (cuuint64_t)heads};
     const cuuint64_t strides[3] = {row_bytes, 128, head_bytes};
-    const cuuint32_t boxes[4] = {64, kTile, (cuuint32_t)panels, 1};
+    const cuuint32_t boxes[4] = {result ? 32u : 64u, kTile, (cuuint32_t)panels, 1};
     const cuuint32_t steps[4] = {1, 1, 1, 1};
     return fn(map, bf16 ? CU_TENSOR_MAP_DATA_TYPE_BFLOAT16 : CU_TENSOR_MAP_DATA_TYPE_FLOAT16, 4,
               const_cast<void *>(base), dims, strides, boxes, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
-              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) ==
-           CUDA_SUCCESS;
+              result ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
 }  // namespace
@@ -1530,7 +1550,8 @@ extern "C" int lmc_linear_scan(const lmc_layout *L, const lmc_linear *a, const i
     P.v_panels = (P.L.dv + 63) / 64;
     const bool bf16 = P.L.bf16, whole_k = P.L.dk % 64 == 0, whole_v = P.L.dv % 64 == 0;
     P.wide_out = ((uintptr_t)a->out & 15) == 0 && (num_rows == 1 || a->out_row_stride % 8 == 0) &&
-                 (a->num_heads == 1 || a->out_head_stride % 8 == 0);
+                 (a->num_heads == 1 || a->out_head_stride % 8 == 0) &&
+                 a->out_row_stride < (int64_t)1 << 36 && a->out_head_stride < (int64_t)1 << 36;
     P.k_copies = whole_k ? 1 : P.k_panels;
     P.v_copies = whole_v ? 1 : P.v_panels;
     const int64_t H = a->num_heads, K = a->num_key_heads;
@@ -1540,7 +1561,9 @@ extern "C" int lmc_linear_scan(const lmc_layout *L, const lmc_linear *a, const i
         return LMC_ERR_OVERFLOW;
     if (!rows_map(&P.q, bf16, a->q, P.L.dk, num_rows, K, a->q_row_stride, a->q_head_stride, whole_k) ||
         !rows_map(&P.k, bf16, a->k, P.L.dk, num_rows, K, a->k_row_stride, a->k_head_stride, whole_k) ||
-        !rows_map(&P.v, bf16, a->v, P.L.dv, num_rows, H, a->v_row_stride, a->v_head_stride, whole_v))
+        !rows_map(&P.v, bf16, a->v, P.L.dv, num_rows, H, a->v_row_stride, a->v_head_stride, whole_v) ||
+        (P.wide_out &&
+         !rows_map(&P.out, bf16, a->out, P.L.dv, num_rows, H, a->out_row_stride, a->out_head_stride, false, true)))
         return LMC_ERR_CUDA;
     auto scan = bf16 ? lmc_linear_scan_kernel<true, false> : lmc_linear_scan_kernel<false, false>;
     auto segments = bf16 ? lmc_linear_scan_kernel<true, true> : lmc_linear_scan_kernel<false, true>;
