@@ -420,6 +420,16 @@ __device__ __forceinline__ uint32_t minus(uint32_t a) {
 }
 
 // 2^e for e in [-126, 127], and the e that brings x into [2^14, 2^15).
+// The greatest of a >= 0, |x| and |y|.
+__device__ __forceinline__ float greatest(float a, float x, float y) {
+    asm("max.abs.f32 %0, %0, %1, %2;" : "+f"(a) : "f"(x), "f"(y));
+    return a;
+}
+// a - b
+__device__ __forceinline__ float2 less(float2 a, float2 b) { return __ffma2_rn(b, make_float2(-1.0f, -1.0f), a); }
+__device__ __forceinline__ float2 from_halves(uint32_t x) {
+    return __half22float2(*reinterpret_cast<const __half2 *>(&x));
+}
 __device__ __forceinline__ float power(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
 __device__ __forceinline__ int lift_of(float x) {
     const int e = (int)(__float_as_uint(x) >> 23 & 255u) - 127;  // x >= 0
@@ -805,8 +815,8 @@ __device__ __forceinline__ void split(const ScanPlan &P, ScanControl &C, uint8_t
 #pragma unroll
                 for (int k = 0; k < 8; k++) {
                     const float2 f = *reinterpret_cast<const float2 *>(&D.left[16 * half + 4 * (k >> 1) + (lane & 3)]);
-                    top[k & 1] = fmaxf(top[k & 1], fmaxf(fabsf(from_q(v[k] & 0xffff, false)) * f.x,
-                                                         fabsf(from_q(v[k] >> 16, false)) * f.y));
+                    const float2 x = __fmul2_rn(from_halves(v[k]), f);
+                    top[k & 1] = greatest(top[k & 1], x.x, x.y);
                 }
             }
             float up[2];
@@ -835,10 +845,10 @@ __device__ __forceinline__ void split(const ScanPlan &P, ScanControl &C, uint8_t
 #pragma unroll
                 for (int k = 0; k < 8; k++) {
                     const float2 f = *reinterpret_cast<const float2 *>(&D.left[16 * half + 4 * (k >> 1) + (lane & 3)]);
-                    const float x = from_q(v[k] & 0xffff, false) * f.x * up[k & 1];
-                    const float y = from_q(v[k] >> 16, false) * f.y * up[k & 1];
-                    a[k] = pack<false>(x, y);
-                    b[k] = pack<false>(x - from_q(a[k] & 0xffff, false), y - from_q(a[k] >> 16, false));
+                    float2 x = __fmul2_rn(__fmul2_rn(from_halves(v[k]), f), make_float2(up[k & 1], up[k & 1]));
+                    a[k] = pack<false>(x.x, x.y);
+                    x = less(x, from_halves(a[k]));
+                    b[k] = pack<false>(x.x, x.y);
                 }
                 store_part(to + 16 * half, a);
                 store_part(to + kPartColumns + 16 * half, b);
@@ -887,14 +897,17 @@ __device__ __forceinline__ void weigh(const ScanPlan &P, ScanControl &C, uint8_t
             for (int i = 0; i < 2; i++) {
                 const int c = 16 * u + 8 * i + 2 * (lane & 3);
                 const float4 lc = *reinterpret_cast<const float4 *>(&D.log[c]);
-                const float w0 = exp2_fast((la.x - lc.x) + (la.y - lc.y)), w1 = exp2_fast((la.x - lc.z) + (la.y - lc.w));
-                const float w2 = exp2_fast((lb.x - lc.x) + (lb.y - lc.y)), w3 = exp2_fast((lb.x - lc.z) + (lb.y - lc.w));
-                const float x0 = __uint_as_float(raw[4 * i]) * P.L.scale, x1 = __uint_as_float(raw[4 * i + 1]) * P.L.scale;
-                const float x2 = __uint_as_float(raw[4 * i + 2]) * P.L.scale, x3 = __uint_as_float(raw[4 * i + 3]) * P.L.scale;
-                p[i][0] = c <= ra ? x0 * w0 : 0.0f;
-                p[i][1] = c < ra ? x1 * w1 : 0.0f;
-                p[i][2] = c <= rb ? x2 * w2 : 0.0f;
-                p[i][3] = c < rb ? x3 * w3 : 0.0f;
+                const float2 l0 = make_float2(lc.x, lc.y), l1 = make_float2(lc.z, lc.w);
+                const float2 d0 = less(la, l0), d1 = less(la, l1), d2 = less(lb, l0), d3 = less(lb, l1);
+                const float2 unit = make_float2(P.L.scale, P.L.scale);
+                float2 x = __fmul2_rn(make_float2(__uint_as_float(raw[4 * i]), __uint_as_float(raw[4 * i + 1])), unit);
+                float2 y = __fmul2_rn(make_float2(__uint_as_float(raw[4 * i + 2]), __uint_as_float(raw[4 * i + 3])), unit);
+                x = __fmul2_rn(x, make_float2(exp2_fast(d0.x + d0.y), exp2_fast(d1.x + d1.y)));
+                y = __fmul2_rn(y, make_float2(exp2_fast(d2.x + d2.y), exp2_fast(d3.x + d3.y)));
+                p[i][0] = c <= ra ? x.x : 0.0f;
+                p[i][1] = c < ra ? x.y : 0.0f;
+                p[i][2] = c <= rb ? y.x : 0.0f;
+                p[i][3] = c < rb ? y.y : 0.0f;
             }
         };
         float ua = 1.0f, ub = 1.0f;
@@ -908,8 +921,8 @@ __device__ __forceinline__ void weigh(const ScanPlan &P, ScanControl &C, uint8_t
                 make(u, p);
 #pragma unroll
                 for (int i = 0; i < 2; i++) {
-                    ta = fmaxf(ta, fmaxf(fabsf(p[i][0]), fabsf(p[i][1])));
-                    tb = fmaxf(tb, fmaxf(fabsf(p[i][2]), fabsf(p[i][3])));
+                    ta = greatest(ta, p[i][0], p[i][1]);
+                    tb = greatest(tb, p[i][2], p[i][3]);
                 }
             }
             for (int o = 1; o < 4; o <<= 1) {
@@ -963,10 +976,10 @@ __device__ __forceinline__ void carry(const ScanPlan &P, ScanControl &C) {
     const bool mine = i0 < L.dk;
     const int64_t head = (int64_t)I.h * L.dk * L.dv, at = (int64_t)i0 * L.dv + j;
     const int64_t slot_size = (int64_t)L.H * L.dk * L.dv;
-    float s[64];
+    float2 s[32];  // pairs of keys: two products an instruction
 #pragma unroll
-    for (int i = 0; i < 64; i++)
-        s[i] = 0.0f;
+    for (int i = 0; i < 32; i++)
+        s[i] = make_float2(0.0f, 0.0f);
     auto read = [&](const float *from) {
         if (j < L.dv) {
             from += at;
@@ -975,7 +988,7 @@ __device__ __forceinline__ void carry(const ScanPlan &P, ScanControl &C) {
                 if (i0 + g < L.dk)
 #pragma unroll
                     for (int i = g; i < g + 8; i++, from += L.dv)
-                        s[i] = __ldcs(from);
+                        (i & 1 ? s[i / 2].y : s[i / 2].x) = __ldcs(from);
         }
     };
     auto write = [&](float *to) {
@@ -986,7 +999,7 @@ __device__ __forceinline__ void carry(const ScanPlan &P, ScanControl &C) {
                 if (i0 + g < L.dk)
 #pragma unroll
                     for (int i = g; i < g + 8; i++, to += L.dv)
-                        __stcs(to, s[i]);
+                        __stcs(to, i & 1 ? s[i / 2].y : s[i / 2].x);
         }
     };
     // The state as A of its product with q, in 16 bits; what is to be multiplied
@@ -997,8 +1010,8 @@ __device__ __forceinline__ void carry(const ScanPlan &P, ScanControl &C) {
         if constexpr (!kBf16) {
             float top = 0.0f;
 #pragma unroll
-            for (int i = 0; i < 64; i++)
-                top = fmaxf(top, fabsf(s[i]));
+            for (int i = 0; i < 32; i++)
+                top = greatest(top, s[i].x, s[i].y);
             C.row_top[half][j] = top;
             asm volatile("bar.sync %0, 64;" ::"r"(2 + quarter) : "memory");
             top = fmaxf(top, C.row_top[half ^ 1][j]);
@@ -1012,8 +1025,10 @@ __device__ __forceinline__ void carry(const ScanPlan &P, ScanControl &C) {
             for (int c = 0; c < 4; c++) {
                 uint32_t x[8];
 #pragma unroll
-                for (int i = 0; i < 8; i++)
-                    x[i] = pack<kBf16>(s[16 * c + 2 * i] * up, s[16 * c + 2 * i + 1] * up);
+                for (int i = 0; i < 8; i++) {
+                    const float2 y = kBf16 ? s[8 * c + i] : __fmul2_rn(s[8 * c + i], make_float2(up, up));
+                    x[i] = pack<kBf16>(y.x, y.y);
+                }
                 store_o8(x, lanes + kState + 32 * half + 8 * c);
             }
             wait_st();
@@ -1063,9 +1078,12 @@ __device__ __forceinline__ void carry(const ScanPlan &P, ScanControl &C) {
                 load_o8(u, lanes + kUpdate + i0 + 8 * c);
                 wait_ld();
 #pragma unroll
-                for (int i = 0; i < 8; i++)
-                    s[8 * c + i] =
-                        fmaf(grow, s[8 * c + i], kBf16 ? __uint_as_float(u[i]) : __uint_as_float(u[i]) * unit);
+                for (int i = 0; i < 4; i++) {
+                    float2 y = make_float2(__uint_as_float(u[2 * i]), __uint_as_float(u[2 * i + 1]));
+                    if constexpr (!kBf16)
+                        y = __fmul2_rn(y, make_float2(unit, unit));
+                    s[4 * c + i] = __ffma2_rn(make_float2(grow, grow), s[4 * c + i], y);
+                }
             }
         }
         fence_before();
@@ -1140,22 +1158,19 @@ __device__ __forceinline__ void deliver(const ScanPlan &P, ScanControl &C, uint8
 #pragma unroll
             for (int i = 0; i < 4; i++) {
                 const float2 e = since[i];
-                if constexpr (kBf16) {
+                float2 g = make_float2(1.0f, 1.0f);
+                if constexpr (!kBf16)
+                    g = *reinterpret_cast<const float2 *>(&D.lift[32 * half + 8 * i + 2 * (lane & 3)]);
 #pragma unroll
-                    for (int k = 0; k < 2; k++)
-                        y[2 * i + k] = pack<true>(fmaf(__uint_as_float(a[4 * i + 2 * k]), e.x, __uint_as_float(b[4 * i + 2 * k])),
-                                                  fmaf(__uint_as_float(a[4 * i + 2 * k + 1]), e.y,
-                                                       __uint_as_float(b[4 * i + 2 * k + 1])));
-                } else {
-                    const float2 g = *reinterpret_cast<const float2 *>(&D.lift[32 * half + 8 * i + 2 * (lane & 3)]);
-#pragma unroll
-                    for (int k = 0; k < 2; k++) {
-                        const float d = k ? db : da;
-                        y[2 * i + k] =
-                            pack<false>(fmaf(__uint_as_float(a[4 * i + 2 * k]) * d, e.x, __uint_as_float(b[4 * i + 2 * k]) * g.x),
-                                        fmaf(__uint_as_float(a[4 * i + 2 * k + 1]) * d, e.y,
-                                             __uint_as_float(b[4 * i + 2 * k + 1]) * g.y));
+                for (int k = 0; k < 2; k++) {
+                    float2 x = make_float2(__uint_as_float(a[4 * i + 2 * k]), __uint_as_float(a[4 * i + 2 * k + 1]));
+                    float2 z = make_float2(__uint_as_float(b[4 * i + 2 * k]), __uint_as_float(b[4 * i + 2 * k + 1]));
+                    if constexpr (!kBf16) {
+                        x = __fmul2_rn(x, k ? make_float2(db, db) : make_float2(da, da));
+                        z = __fmul2_rn(z, g);
                     }
+                    x = __ffma2_rn(x, e, z);
+                    y[2 * i + k] = pack<kBf16>(x.x, x.y);
                 }
             }
             const uint32_t to = staged + half * 32 * 64 + (((2 * b16 + piece) ^ turn) << 4);
