@@ -682,23 +682,26 @@ typedef struct {
  * last). Asynchronous on `stream`. Status: BAD_JOB (a length below -1, or the
  * token's position past the table), NO_SNAPSHOT (-1 where a state is read or
  * written), BLOCK_OOR; such a request's row of out and pages are left as they
- * were. Errors: INVALID_ARG, ALIGN, OVERLAP, CUDA. */
+ * were. Errors: INVALID_ARG, ALIGN, OVERLAP, OVERFLOW (more thread blocks than a
+ * grid has), CUDA. */
 LMC_API int lmc_linear_step(const lmc_layout *layout, const lmc_linear *linear, void *pool, uint32_t *status,
                             void *stream);
 
 /* Prompts: request r's tokens are rows starts[r] .. starts[r + 1] - 1 (starts:
  * device [num_requests + 1], not decreasing, within [0, num_rows]; rows of no
- * request are left as they were, a request without rows is left out). Results
+ * request are left as they were, a request without rows is left out); num_rows is at most INT32_MAX. Results
  * are those of lmc_linear_step token by token up to rounding, for chunks of up
  * to 64 tokens at a time.
  *
  * Rounding: the tensor cores multiply 16-bit numbers of q's type, with binary32
- * sums. The state and what is added to it are held in as many 16-bit parts as
- * binary32 needs; the weights inside a chunk, (q_t . k_j) * exp(sum of decays),
- * are rounded to the type once (half a step each, as the result is). A token
- * whose values are not finite may make NaN of the results of up to 63 tokens
- * before it in its request's block, of the same head; other requests are not
- * touched.
+ * sums. States are binary32, and what is added to them is multiplied in as many
+ * 16-bit parts as keep its digits (BF16: four; F16: two, off by 2^-22 of
+ * themselves or 2^-38 of the largest of a chunk's tokens). For the result two factors are rounded to the
+ * type once, half a step each as the result is: the state before a chunk, and the
+ * weights inside it, (q_t . k_j) * exp(sum of decays). A token whose values or
+ * decay are not finite may make NaN of the results of up to 63 tokens before it
+ * in its request's block, of the same head (a key head's: of all its heads);
+ * other requests are not touched.
  *
  * `workspace`: device memory of at least lmc_linear_scan_workspace bytes,
  * 256-byte aligned; its content does not matter, and calls that may run at the
