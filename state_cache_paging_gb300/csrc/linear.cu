@@ -375,12 +375,16 @@ __device__ __forceinline__ void tma_store(const CUtensorMap *map, const void *sr
 
 // Rows of two panels behind a tile's last one, cleared by `threads` threads: they
 // belong to others, and take part in products times 0, which infinities and NaN
-// would not bear.
-__device__ __forceinline__ void clear_rows(uint8_t *panels, int rows, int tid, int threads) {
+// would not bear. `twice`: or that take the tile's rows a second time, half a tile on.
+__device__ __forceinline__ void clear_rows(uint8_t *panels, int rows, int tid, int threads, bool twice = false) {
+    constexpr int kHalf = kTile / 2;
 #pragma unroll 1
-    for (int c = tid; c < 2 * (kPanel / 16); c += threads)
-        if ((c >> 3 & (kTile - 1)) >= rows)
-            *reinterpret_cast<uint4 *>(panels + c * 16) = make_uint4(0, 0, 0, 0);
+    for (int c = tid; c < 2 * (kPanel / 16); c += threads) {
+        const int row = c >> 3 & (kTile - 1);
+        uint4 *const at = reinterpret_cast<uint4 *>(panels + c * 16);
+        if (row >= rows)
+            *at = twice && row >= kHalf && row - kHalf < rows ? at[-kHalf * 8] : make_uint4(0, 0, 0, 0);
+    }
 }
 
 // 16 lanes x 16 columns, as load_s.
@@ -894,6 +898,12 @@ __device__ __forceinline__ void split(const ScanPlan &P, ScanControl &C, uint8_t
 
 // Four warps: the weights P = (Q K^T) * decays, of tokens up to the row's own (warp
 // w: rows 16 w .. 16 w + 15).
+//
+// They are rounded to 16 bits, which over many of them makes the result's error
+// sqrt(2) of what rounding it alone makes. Over few it can be 2.5 times that (one
+// weight is a factor of a head's whole result), so tiles of at most 32 tokens hold
+// what rounding took off as weights of the same tokens, half a tile on: the products
+// are there anyway.
 template <bool kBf16>
 __device__ __forceinline__ void weigh(const ScanPlan &P, ScanControl &C, uint8_t *mem) {
     int looks = kLooks;
@@ -902,13 +912,16 @@ __device__ __forceinline__ void weigh(const ScanPlan &P, ScanControl &C, uint8_t
     const uint32_t lanes = C.tmem + ((uint32_t)(quarter * 32) << 16);
     const int ra = quarter * 16 + lane / 4, rb = ra + 8;  // this thread's rows of P
     uint8_t *const pa = mem + kWeightsAt + ra * 128 + 4 * (lane & 3), *const pb = pa + 8 * 128;
+    bool held = false;  // the rows' second halves hold something
     while (T.next()) {
         const uint32_t n = T.n;
+        const bool twice = T.rows <= kTile / 2;
         Decays &D = C.decays[n % kRing];
         scan_wait(C, &C.decays_full[n % kRing], (n / kRing) & 1, looks);
         if (T.rows < kTile) {
             scan_wait(C, &C.full[n % kStages], (n / kStages) & 1, looks);
-            clear_rows(mem + (n % kStages) * kStageBytes + 4 * kPanel, T.rows, threadIdx.x - kFirstWeightWarp * 32, kWeightWarps * 32);
+            clear_rows(mem + (n % kStages) * kStageBytes + 4 * kPanel, T.rows, threadIdx.x - kFirstWeightWarp * 32, kWeightWarps * 32,
+                       twice);
         }
         scan_wait(C, &C.score_full, n & 1, looks);
         fence_after();
@@ -939,24 +952,30 @@ __device__ __forceinline__ void weigh(const ScanPlan &P, ScanControl &C, uint8_t
         };
         float ua = 1.0f, ub = 1.0f;
         if constexpr (!kBf16) {
-            // f16 has not binary32's range: a row's weights are brought below 2^15
-            // (made twice: held, they would be 32 registers)
+            // f16 has not binary32's range: a row's weights are brought below 2^15, by
+            // the largest of its products (decays are at most 1; a weight keeps f16's
+            // steps down to 2^-28 of that one)
             float ta = 0.0f, tb = 0.0f;
 #pragma unroll 1
             for (int u = 0; u <= quarter; u++) {
-                float p[2][4];
-                make(u, p);
+                uint32_t raw[8];
+                load_s8(raw, lanes + kScores + 16 * u);
+                wait_ld();
 #pragma unroll
                 for (int i = 0; i < 2; i++) {
-                    ta = greatest(ta, p[i][0], p[i][1]);
-                    tb = greatest(tb, p[i][2], p[i][3]);
+                    const int c = 16 * u + 8 * i + 2 * (lane & 3);
+                    ta = greatest(ta, c <= ra ? __uint_as_float(raw[4 * i]) : 0.0f,
+                                  c < ra ? __uint_as_float(raw[4 * i + 1]) : 0.0f);
+                    tb = greatest(tb, c <= rb ? __uint_as_float(raw[4 * i + 2]) : 0.0f,
+                                  c < rb ? __uint_as_float(raw[4 * i + 3]) : 0.0f);
                 }
             }
             for (int o = 1; o < 4; o <<= 1) {
                 ta = fmaxf(ta, __shfl_xor_sync(0xffffffffu, ta, o));
                 tb = fmaxf(tb, __shfl_xor_sync(0xffffffffu, tb, o));
             }
-            const int ea = lift_of(ta), eb = lift_of(tb);
+            const float unit = fabsf(P.L.scale);
+            const int ea = lift_of(ta * unit), eb = lift_of(tb * unit);
             ua = power(ea);
             ub = power(eb);
             if ((lane & 3) == 0) {
@@ -976,6 +995,25 @@ __device__ __forceinline__ void weigh(const ScanPlan &P, ScanControl &C, uint8_t
                 *reinterpret_cast<uint32_t *>(pa + at) = pack<kBf16>(p[i][0] * ua, p[i][1] * ua);
                 *reinterpret_cast<uint32_t *>(pb + at) = pack<kBf16>(p[i][2] * ub, p[i][3] * ub);
             }
+        }
+        if (__builtin_expect(held || twice, false) && quarter < 2) {
+#pragma unroll 1
+            for (int u = 0; u < 2; u++) {
+                float p[2][4] = {};
+                if (twice && u <= quarter)
+                    make(u, p);
+#pragma unroll
+                for (int i = 0; i < 2; i++) {
+                    const int at = ((2 * u + i) ^ 4 ^ (ra & 7)) << 4;
+                    auto rest = [](float x, float y) {
+                        const uint32_t w = pack<kBf16>(x, y);
+                        return pack<kBf16>(x - from_q(w & 0xffff, kBf16), y - from_q(w >> 16, kBf16));
+                    };
+                    *reinterpret_cast<uint32_t *>(pa + at) = rest(p[i][0] * ua, p[i][1] * ua);
+                    *reinterpret_cast<uint32_t *>(pb + at) = rest(p[i][2] * ub, p[i][3] * ub);
+                }
+            }
+            held = twice;
         }
         fence_before();
         fence_async();

@@ -370,6 +370,33 @@ def test_f16_of_all_its_range(what, op):
     G.check(P, pool.cpu(), out.cpu(), had, new, table, start, q, k, v, dec, scale, "f16")
 
 
+@pytest.mark.parametrize("act", ["bf16", "f16"])
+@pytest.mark.parametrize("N,new", [(64, [1, 2, 5, 16, 17, 31, 32]), (20, [90, 21]), (96, [200, 96, 100])])
+def test_short_tiles_hold_their_weights_twice_as_long(N, new, act):
+    """Tiles of at most 32 tokens, alone and between whole ones: the first ones of
+    fresh requests are off by no more than the result's own rounding."""
+    H, d = 2, 64
+    P = R.States(lmc, H, d, d, N, 32)
+    table = R.tables([0] * len(new), new, N, 32, np.random.default_rng(0))
+    rows = sum(new)
+    q, k, v, dec, _ = G.inputs(rows, H, H, d, d, act, "token", 21)
+    start = np.concatenate([[0], np.cumsum(new)]).astype(np.int32)
+    pool, out, status = P.pool.cuda(), torch.full((rows, H, d), float("nan"), dtype=R.TYPES[act], device=DEV), flag()
+    lmc.lmc_linear_scan(P.layout, P.layer, pool, table.cuda(), ints(start.tolist()), ints([0] * len(new)),
+                        *[x.cuda() for x in (q, k, v, dec)], out, workspace(P, len(new), rows)[0], status, scale=0.1)
+    torch.cuda.synchronize()
+    assert int(status.item()) == 0
+    out, half = out.cpu(), R.HALF_STEP[act]
+    G.check(P, pool.cpu(), out, [0] * len(new), new, table, start, q, k, v, dec, 0.1, act)
+    for r, n in enumerate(new):
+        n = min(n, N) if min(n, N) <= 32 else 0  # the request's first tile
+        s = slice(int(start[r]), int(start[r]) + n)
+        o, mag, _ = R.linear(torch.zeros(H, d, d, dtype=torch.float64), q[s], k[s], v[s], dec[s], 0.1)
+        # a weight in two parts is off by half a step squared (2^-16 in bf16); sums and decays in binary32
+        most = half * o.abs() * (1 + 2.0 ** -10) + mag * (2.0 ** -14) + (2.0 ** -24 if act == "f16" else 0)
+        assert bool(((out[s].double() - o).abs() <= most).all()), (r, n)
+
+
 # ---- several calls at once, bad starts, pages that are shared -------------------------
 
 @pytest.mark.parametrize("act", ["bf16", "f16"])
