@@ -33,9 +33,13 @@ constexpr int kMaxRows = 64;           // of a CTA
 constexpr int kMaxAngles = 2048;       // of a CTA's rows together (16 KB), where it has several
 constexpr int kMaxHeadDim = 4096;
 
+constexpr int64_t kManyHeads = 152 * 4 * 32;  // long ones: of a GPU full of groups of eight lanes
 constexpr int kManyCtas = 152 * 16;   // waves of CTAs enough to even out
 
-enum Result { kRows, kEntries, kCodes };  // activations; a page's entries, as they are or as fp8 codes
+// Activations; a page's entries, as they are or as fp8 codes (kDivided: of a scale that
+// has no inverse to multiply by; such calls are rare and take the slower kernel).
+enum Result { kRows, kEntries, kCodes, kDivided };
+__host__ __device__ constexpr bool codes(Result to) { return to == kCodes || to == kDivided; }
 
 struct RotatePlan {
     const uint16_t *x;
@@ -167,17 +171,29 @@ __device__ __forceinline__ void widen_values(float (&x)[W], const uint32_t (&raw
     }
 }
 
+// What is to be divided by the scale, or has been multiplied by its inverse already
+// (`scaled`), as a pair of codes.
+template <Result kTo>
+__device__ __forceinline__ uint32_t code_pair(const RotatePlan &P, float x, float y, bool scaled) {
+    if (kTo == kDivided)
+        x = __fdiv_rn(x, P.code_scale), y = __fdiv_rn(y, P.code_scale);
+    else if (!scaled)
+        x = quotient_by_inverse(x, P.code_scale, P.code_inverse), y = quotient_by_inverse(y, P.code_scale, P.code_inverse);
+    return __nv_cvt_float2_to_fp8x2(make_float2(x, y), __NV_SATFINITE, __NV_E4M3);
+}
+
+// Values of a result; codes: `scaled` if the scale's inverse is in them (what was
+// turned, and most of what was normalised).
 template <typename T2, int W, Result kTo>
-__device__ __forceinline__ void store_values(const RotatePlan &P, uint8_t *at, const float (&y)[W]) {
-    if constexpr (kTo == kCodes && W == 8) {
-        uint32_t w[2];
+__device__ __forceinline__ void store_values(const RotatePlan &P, uint8_t *at, const float (&y)[W], bool scaled) {
+    if constexpr (codes(kTo) && W == 8) {
+        uint32_t w[4];
 #pragma unroll
-        for (int k = 0; k < 2; k++)
-            w[k] = codes2(make_float2(y[4 * k], y[4 * k + 1]), P.code_scale, P.code_inverse) |
-                   codes2(make_float2(y[4 * k + 2], y[4 * k + 3]), P.code_scale, P.code_inverse) << 16;
-        __stcs(reinterpret_cast<uint2 *>(at), make_uint2(w[0], w[1]));
-    } else if constexpr (kTo == kCodes) {
-        *at = (uint8_t)codes2(make_float2(y[0], 0.0f), P.code_scale, P.code_inverse);
+        for (int k = 0; k < 4; k++)
+            w[k] = code_pair<kTo>(P, y[2 * k], y[2 * k + 1], scaled);
+        __stcs(reinterpret_cast<uint2 *>(at), make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16));
+    } else if constexpr (codes(kTo)) {
+        *at = (uint8_t)code_pair<kTo>(P, y[0], 0.0f, scaled);
     } else if constexpr (W == 8) {
         __stcs(reinterpret_cast<uint4 *>(at), make_uint4(narrow<T2>(y[0], y[1]), narrow<T2>(y[2], y[3]),
                                                          narrow<T2>(y[4], y[5]), narrow<T2>(y[6], y[7])));
@@ -186,34 +202,12 @@ __device__ __forceinline__ void store_values(const RotatePlan &P, uint8_t *at, c
     }
 }
 
-// Values of a result whose scale is in them already (codes): what was turned, and
-// most of what was normalised.
-template <typename T2, int W, Result kTo>
-__device__ __forceinline__ void store_scaled(const RotatePlan &P, uint8_t *at, const float (&y)[W]) {
-    if constexpr (kTo == kCodes) {
-        uint32_t w[(W + 1) / 2];
-#pragma unroll
-        for (int k = 0; k < (W + 1) / 2; k++) {
-            float2 v = make_float2(y[2 * k], W == 1 ? 0.0f : y[W == 1 ? 0 : 2 * k + 1]);
-            if (P.code_inverse == 0.0f)
-                v = make_float2(__fdiv_rn(v.x, P.code_scale), __fdiv_rn(v.y, P.code_scale));
-            w[k] = __nv_cvt_float2_to_fp8x2(v, __NV_SATFINITE, __NV_E4M3);
-        }
-        if constexpr (W == 8)
-            __stcs(reinterpret_cast<uint2 *>(at), make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16));
-        else
-            *at = (uint8_t)w[0];
-    } else {
-        store_values<T2, W, kTo>(P, at, y);
-    }
-}
-
 // One item of a head (or of the rest): normalised, turned, written.
 template <typename T2, int W, Result kTo>
 __device__ __forceinline__ void finish(const RotatePlan &P, const float2 *cs, uint8_t *dst, int i, int first, int second,
                                        float norm, bool head, const uint32_t (&lo)[(W + 1) / 2],
                                        const uint32_t (&hi)[(W + 1) / 2]) {
-    constexpr int kBytes = kTo == kCodes ? 1 : 2;
+    constexpr int kBytes = codes(kTo) ? 1 : 2;
     float a[W], b[W];
     widen_values<T2, W>(a, lo);
     widen_values<T2, W>(b, hi);
@@ -236,7 +230,7 @@ __device__ __forceinline__ void finish(const RotatePlan &P, const float2 *cs, ui
             a[k] = x * r.x - y * r.y;
             b[k] = x * r.y + y * r.x;
         }
-        store_scaled<T2, W, kTo>(P, dst + (int64_t)second * kBytes, b);
+        store_values<T2, W, kTo>(P, dst + (int64_t)second * kBytes, b, true);
     } else if (W == 8 && turned) {
 #pragma unroll
         for (int k = 0; k < W / 2; k++) {
@@ -246,10 +240,7 @@ __device__ __forceinline__ void finish(const RotatePlan &P, const float2 *cs, ui
             a[2 * k + 1] = x * r.y + y * r.x;
         }
     }
-    if (turned)
-        store_scaled<T2, W, kTo>(P, dst + (int64_t)first * kBytes, a);
-    else
-        store_values<T2, W, kTo>(P, dst + (int64_t)first * kBytes, a);
+    store_values<T2, W, kTo>(P, dst + (int64_t)first * kBytes, a, turned);
 }
 
 // Steps of the angles and the rows' cosines and sines in shared memory; where the
@@ -276,7 +267,7 @@ __device__ __forceinline__ void make_angles(const RotatePlan &P, float2 *cs, uin
         steps[k] = step_of(__ldca(P.frequencies + k));
     __syncthreads();
     // codes: times what the values are divided by, too
-    const float scale = kTo == kCodes && P.code_inverse != 0.0f ? P.mscale * P.code_inverse : P.mscale;
+    const float scale = kTo == kCodes ? P.mscale * P.code_inverse : P.mscale;
     if (P.half == 0)
         return;
     int row = threadIdx.x / P.half, k = threadIdx.x - row * P.half;
@@ -317,6 +308,62 @@ __device__ __forceinline__ Two plus_product(Two a, Two b, Two c) {
     return r;
 }
 
+// Eight values as four pairs: from a piece, times a factor and the weights from `at` on,
+// turned (two whole pairs to a float4 of angles, or with the piece half a turned part
+// away), and written.
+template <typename T2>
+__device__ __forceinline__ void open(Two (&x)[4], const uint4 &raw) {
+    const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+#pragma unroll
+    for (int k = 0; k < 4; k++) {
+        const float2 v = widen<T2>(w[k]);
+        x[k] = two(v.x, v.y);
+    }
+}
+__device__ __forceinline__ void weigh(Two (&x)[4], const float *weights, float f, int at) {
+    const float4 v = *reinterpret_cast<const float4 *>(weights + at), w = *reinterpret_cast<const float4 *>(weights + at + 4);
+    const Two g = two(f, f);
+    x[0] = x[0] * g * two(v.x, v.y);
+    x[1] = x[1] * g * two(v.z, v.w);
+    x[2] = x[2] * g * two(w.x, w.y);
+    x[3] = x[3] * g * two(w.z, w.w);
+}
+__device__ __forceinline__ void turn_pairs(Two (&a)[4], const float2 *angles) {
+    const float4 *const r = reinterpret_cast<const float4 *>(angles);
+#pragma unroll
+    for (int k = 0; k < 2; k++) {
+        const float4 c = r[k];
+        const float2 u = apart(a[2 * k]), v = apart(a[2 * k + 1]);
+        a[2 * k] = plus_product(two(u.x, u.x), two(c.x, c.y), two(u.y, u.y) * two(-c.y, c.x));
+        a[2 * k + 1] = plus_product(two(v.x, v.x), two(c.z, c.w), two(v.y, v.y) * two(-c.w, c.z));
+    }
+}
+__device__ __forceinline__ void turn_halves(Two (&a)[4], Two (&b)[4], const float2 *angles) {
+    const float4 *const r = reinterpret_cast<const float4 *>(angles);
+#pragma unroll
+    for (int k = 0; k < 4; k++) {
+        const float4 c = r[k];
+        const Two u = a[k], v = b[k], cosine = two(c.x, c.z);
+        a[k] = plus_product(u, cosine, v * two(-c.y, -c.w));
+        b[k] = plus_product(v, cosine, u * two(c.y, c.w));
+    }
+}
+// `plain`: codes of values that were neither normalised nor turned, as lmc_append does.
+template <typename T2, Result kTo>
+__device__ __forceinline__ void put(const RotatePlan &P, uint8_t *at, const Two (&x)[4], bool plain = false) {
+    float y[8];
+#pragma unroll
+    for (int k = 0; k < 4; k++) {
+        const float2 v = apart(x[k]);
+        y[2 * k] = v.x;
+        y[2 * k + 1] = v.y;
+    }
+    if (codes(kTo) && plain)
+        store_values<T2, 8, kTo>(P, at, y, false);
+    else
+        store_values<T2, 8, kTo>(P, at, y, true);
+}
+
 // Pieces of eight values (16 bytes), a head's items held in registers by a group of
 // lanes, kItems each: a lane has the same items of every head, so where they lie is
 // found once. What it costs are instructions (for a row of 576 values as fp8 codes
@@ -326,7 +373,7 @@ template <typename T2, int kItems, bool kPairs, Result kTo>
 __global__ void __launch_bounds__(kThreads) lmc_rotate_eights_kernel(const __grid_constant__ RotatePlan P) {
     extern __shared__ __align__(16) float2 cs[];  // [rows][half], the steps [half], the weights [head_dim]
     __shared__ uint8_t *dst[kMaxRows];
-    constexpr int kBytes = kTo == kCodes ? 1 : 2;
+    constexpr int kBytes = codes(kTo) ? 1 : 2;
     constexpr int kSecond = kPairs ? 1 : kItems;   // items with a piece half a turned part away
     const int64_t row0 = (int64_t)blockIdx.x * P.rows_per_cta;
     const int rows = (int)min((int64_t)P.rows_per_cta, P.num_rows - row0);
@@ -386,34 +433,8 @@ __global__ void __launch_bounds__(kThreads) lmc_rotate_eights_kernel(const __gri
     make_angles<kTo>(P, cs, steps, dst, row0, rows);
     __syncthreads();
 
-    auto open = [](Two(&x)[4], const uint4 &raw) {
-        const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
-#pragma unroll
-        for (int k = 0; k < 4; k++) {
-            const float2 v = widen<T2>(w[k]);
-            x[k] = two(v.x, v.y);
-        }
-    };
-    auto weigh = [&](Two(&x)[4], float f, int at) {
-        const float4 v = *reinterpret_cast<const float4 *>(weights + at), w = *reinterpret_cast<const float4 *>(weights + at + 4);
-        const Two g = two(f, f);
-        x[0] = x[0] * g * two(v.x, v.y);
-        x[1] = x[1] * g * two(v.z, v.w);
-        x[2] = x[2] * g * two(w.x, w.y);
-        x[3] = x[3] * g * two(w.z, w.w);
-    };
-    auto put = [&](uint8_t *at, const Two(&x)[4]) {
-        float y[8];
-#pragma unroll
-        for (int k = 0; k < 4; k++) {
-            const float2 v = apart(x[k]);
-            y[2 * k] = v.x;
-            y[2 * k + 1] = v.y;
-        }
-        store_scaled<T2, 8, kTo>(P, at, y);
-    };
     // codes: what is not turned is brought to its scale by the norm's factor
-    const float code = kTo == kCodes && P.code_inverse != 0.0f ? P.code_inverse : 1.0f;
+    const float code = kTo == kCodes ? P.code_inverse : 1.0f;
     while (row < rows) {
         uint8_t *to = nullptr;
         if (kTo == kRows)
@@ -424,11 +445,11 @@ __global__ void __launch_bounds__(kThreads) lmc_rotate_eights_kernel(const __gri
             Two a[kItems][4], b[kSecond][4];
 #pragma unroll
             for (int n = 0; n < kItems; n++)
-                open(a[n], lo[n]);
+                open<T2>(a[n], lo[n]);
             if constexpr (!kPairs) {
 #pragma unroll
                 for (int n = 0; n < kItems; n++)
-                    open(b[n], hi[n]);
+                    open<T2>(b[n], hi[n]);
             }
             const int here = row, here_unit = unit;
             row += P.row_step;
@@ -464,10 +485,10 @@ __global__ void __launch_bounds__(kThreads) lmc_rotate_eights_kernel(const __gri
 #pragma unroll
                 for (int n = 0; n < kItems; n++) {
                     if (there[n]) {
-                        weigh(a[n], place[n] >= P.norm_dim ? 1.0f : turned[n] ? norm : norm * code, place[n]);
+                        weigh(a[n], weights, place[n] >= P.norm_dim ? 1.0f : turned[n] ? norm : norm * code, place[n]);
                         if constexpr (!kPairs) {
                             if (turned[n])
-                                weigh(b[n], place[n] + P.half < P.norm_dim ? norm : 1.0f, place[n] + P.half);
+                                weigh(b[n], weights, place[n] + P.half < P.norm_dim ? norm : 1.0f, place[n] + P.half);
                         }
                     }
                 }
@@ -483,37 +504,13 @@ __global__ void __launch_bounds__(kThreads) lmc_rotate_eights_kernel(const __gri
                     uint8_t *const at = to + place[n] * kBytes;
                     if (turned[n]) {
                         if constexpr (kPairs) {
-                            const float4 *const r = reinterpret_cast<const float4 *>(angles + (lane + n * P.group) * 4);
-#pragma unroll
-                            for (int k = 0; k < 2; k++) {
-                                const float4 c = r[k];
-                                const float2 u = apart(a[n][2 * k]), v = apart(a[n][2 * k + 1]);
-                                a[n][2 * k] = plus_product(two(u.x, u.x), two(c.x, c.y), two(u.y, u.y) * two(-c.y, c.x));
-                                a[n][2 * k + 1] = plus_product(two(v.x, v.x), two(c.z, c.w), two(v.y, v.y) * two(-c.w, c.z));
-                            }
+                            turn_pairs(a[n], angles + (lane + n * P.group) * 4);
                         } else {
-                            const float4 *const r = reinterpret_cast<const float4 *>(angles + (lane + n * P.group) * 8);
-#pragma unroll
-                            for (int k = 0; k < 4; k++) {
-                                const float4 c = r[k];
-                                const Two u = a[n][k], v = b[n][k], cosine = two(c.x, c.z);
-                                a[n][k] = plus_product(u, cosine, v * two(-c.y, -c.w));
-                                b[n][k] = plus_product(v, cosine, u * two(c.y, c.w));
-                            }
-                            put(at + P.half * kBytes, b[n]);
+                            turn_halves(a[n], b[n], angles + (lane + n * P.group) * 8);
+                            put<T2, kTo>(P, at + P.half * kBytes, b[n]);
                         }
-                    } else if (kTo == kCodes && plain[n]) {
-                        float y[8];  // as lmc_append does
-#pragma unroll
-                        for (int k = 0; k < 4; k++) {
-                            const float2 v = apart(a[n][k]);
-                            y[2 * k] = v.x;
-                            y[2 * k + 1] = v.y;
-                        }
-                        store_values<T2, 8, kTo>(P, at, y);
-                        continue;
                     }
-                    put(at, a[n]);
+                    put<T2, kTo>(P, at, a[n], plain[n]);
                 }
             }
         } else {
@@ -539,7 +536,7 @@ __global__ void __launch_bounds__(kThreads) lmc_rotate_eights_kernel(const __gri
                         const uint32_t raw[4] = {x[n].x, x[n].y, x[n].z, x[n].w};
                         float y[8];
                         widen_values<T2, 8>(y, raw);
-                        store_values<T2, 8, kTo>(P, at, y);
+                        store_values<T2, 8, kTo>(P, at, y, false);
                     } else {
                         __stcs(reinterpret_cast<uint4 *>(at), x[n]);
                     }
@@ -549,13 +546,116 @@ __global__ void __launch_bounds__(kThreads) lmc_rotate_eights_kernel(const __gri
     }
 }
 
-// Long heads, and rows that do not lie on multiples of 16 bytes: W values of a piece
+// Heads of more than 32 pieces, many of them: eight lanes take one, up to kLongItems
+// pieces each, which are widened twice. A latent's 72 pieces fill such a group's nine
+// rounds (of 32 lanes' three they would fill three quarters), four heads' sums of
+// squares take three shuffles together instead of five each, and 32 heads a CTA keep
+// many CTAs at different steps. (131072 fp8 entries of 576 values: @NEW@ us, with a warp
+// per head and the next one's pieces asked for ahead 77; two heads a group one after
+// another 72, CTAs that stay 84 and more.)
+constexpr int kLongItems = 9, kLongGroup = 8, kLongCtas = 4;
+
+template <typename T2, bool kPairs, Result kTo>
+__global__ void __launch_bounds__(kThreads, kLongCtas) lmc_rotate_long_kernel(const __grid_constant__ RotatePlan P) {
+    extern __shared__ __align__(16) float2 cs[];  // [rows][half], the steps [half], the weights [head_dim]
+    __shared__ uint8_t *dst[kMaxRows];
+    constexpr int kBytes = codes(kTo) ? 1 : 2;
+    const int64_t row0 = (int64_t)blockIdx.x * P.rows_per_cta;
+    const int rows = (int)min((int64_t)P.rows_per_cta, P.num_rows - row0);
+    const int lane = threadIdx.x & (kLongGroup - 1);
+    const int row = (int)(threadIdx.x / kLongGroup) / P.units, unit = threadIdx.x / kLongGroup - row * P.units;
+    uint64_t *const steps = reinterpret_cast<uint64_t *>(cs + P.rows_per_cta * P.half);
+    float *const weights = reinterpret_cast<float *>(steps + (P.half + 1) / 2 * 2);
+    int place[kLongItems];
+#pragma unroll
+    for (int n = 0; n < kLongItems; n++) {
+        int second;
+        place[n] = first_value<8>(P, lane + n * kLongGroup, second);
+    }
+    wait_for_launch();
+    let_next_start();
+    uint4 lo[kLongItems] = {}, hi = {};  // halves: only a lane's first piece has a second one
+    if (row < rows) {                    // while the angles are made
+        const uint16_t *const src = P.x + (row0 + row) * P.x_row + unit * P.x_head;
+#pragma unroll
+        for (int n = 0; n < kLongItems; n++)
+            if (lane + n * kLongGroup < P.items)
+                lo[n] = __ldcs(reinterpret_cast<const uint4 *>(src + place[n]));
+        if (!kPairs && lane < P.turned)
+            hi = __ldcs(reinterpret_cast<const uint4 *>(src + place[0] + P.half));
+    }
+    if (P.norm_dim > 0)
+        for (int k = threadIdx.x; k < P.head_dim; k += kThreads)
+            weights[k] = P.weight != nullptr && k < P.norm_dim ? __ldca(P.weight + k) : 1.0f;
+    make_angles<kTo>(P, cs, steps, dst, row0, rows);
+    __syncthreads();
+    if (row >= rows)
+        return;
+    uint8_t *to;
+    if (kTo == kRows)
+        to = reinterpret_cast<uint8_t *>(P.out + (row0 + row) * P.out_row + unit * P.out_head);
+    else if ((to = dst[row]) != nullptr)
+        to += unit * P.head_dim * kBytes;
+    float norm = 1.0f;
+    if (P.norm_dim > 0) {
+        Two sum = two(0.0f, 0.0f);
+        auto add = [&](const uint4 &raw) {
+            Two x[4];
+            open<T2>(x, raw);
+#pragma unroll
+            for (int k = 0; k < 4; k++)
+                sum = plus_product(x[k], x[k], sum);
+        };
+#pragma unroll
+        for (int n = 0; n < kLongItems; n++)
+            if (lane + n * kLongGroup < P.items && place[n] < P.norm_dim)
+                add(lo[n]);
+        if (!kPairs && lane < P.turned && place[0] + P.half < P.norm_dim)
+            add(hi);
+        const float2 halves = apart(sum);
+        float all = halves.x + halves.y;
+#pragma unroll
+        for (int o = kLongGroup / 2; o > 0; o >>= 1)
+            all += __shfl_xor_sync(0xffu << (threadIdx.x & 24), all, o);
+        norm = rsqrtf(fmaf(all, P.inverse_norm_dim, P.eps));
+    }
+    if (to == nullptr)
+        return;
+    const float2 *const angles = cs + row * P.half;
+    // codes: what is not turned is brought to its scale by the norm's factor
+    const float straight = kTo == kCodes ? norm * P.code_inverse : norm;
+#pragma unroll
+    for (int n = 0; n < kLongItems; n++) {
+        const bool turned = lane + n * kLongGroup < P.turned, plain = !turned && place[n] >= P.norm_dim;
+        if (lane + n * kLongGroup >= P.items || (kTo == kRows && P.touch_only && plain))
+            continue;
+        Two a[4], b[4];
+        open<T2>(a, lo[n]);
+        if (P.norm_dim > 0)
+            weigh(a, weights, place[n] >= P.norm_dim ? 1.0f : turned ? norm : straight, place[n]);
+        uint8_t *const at = to + place[n] * kBytes;
+        if (turned) {
+            if constexpr (kPairs) {
+                turn_pairs(a, angles + (lane + n * kLongGroup) * 4);
+            } else if (n == 0) {
+                open<T2>(b, hi);
+                if (P.norm_dim > 0)
+                    weigh(b, weights, place[n] + P.half < P.norm_dim ? norm : 1.0f, place[n] + P.half);
+                turn_halves(a, b, angles + lane * 8);
+                put<T2, kTo>(P, at + P.half * kBytes, b);
+            }
+        }
+        put<T2, kTo>(P, at, a, plain);
+    }
+}
+
+// Longer heads, and rows that do not lie on multiples of 16 bytes: W values of a piece
 // (8, or 1), a head's items one after another, read a second time after the norm.
 template <typename T2, int W, Result kTo>
 __global__ void __launch_bounds__(kThreads) lmc_rotate_kernel(const __grid_constant__ RotatePlan P) {
     extern __shared__ __align__(16) float2 cs[];  // [rows][half], then the steps [half]
     __shared__ uint8_t *dst[kMaxRows];
-    constexpr int kBytes = kTo == kCodes ? 1 : 2;
+    constexpr int kBytes = codes(kTo) ? 1 : 2;
     const int64_t row0 = (int64_t)blockIdx.x * P.rows_per_cta;
     const int rows = (int)min((int64_t)P.rows_per_cta, P.num_rows - row0);
     wait_for_launch();
@@ -657,6 +757,12 @@ void plan_heads(RotatePlan &P, const lmc_rotation *r, int width) {
 
 template <typename T2, Result kTo>
 int launch(RotatePlan &P, int width, cudaStream_t stream) {
+    // (a warp a head spreads fewer heads than that over more CTAs)
+    const bool eight_lanes = kTo != kDivided && width == 8 && P.items > 32 && P.items <= kLongItems * kLongGroup && P.rest == 0 &&
+                             (P.pairs || P.turned <= kLongGroup) && P.units <= kThreads / kLongGroup &&
+                             P.num_rows * P.units >= kManyHeads;
+    if (eight_lanes)
+        P.group = kLongGroup;
     // Rows of a CTA: enough heads for every group of lanes a few times, so that
     // the angles are made while other CTAs' loads run.
     const int at_once = kThreads / P.group;
@@ -665,9 +771,11 @@ int launch(RotatePlan &P, int width, cudaStream_t stream) {
     int64_t rows = std::max<int64_t>(1, (int64_t)at_once * 4 / P.units);
     while (P.num_rows / rows > kManyCtas && rows * P.units < (int64_t)at_once * 16)
         rows *= 2;
+    if (eight_lanes)  // a head per group and turn
+        rows = std::max(1, at_once / P.units);
     rows = std::min<int64_t>({rows, kMaxRows, std::max(1, kMaxAngles / std::max(1, P.half))});
     P.rows_per_cta = (int32_t)rows;
-    const int64_t grid = (P.num_rows + rows - 1) / rows;
+    int64_t grid = (P.num_rows + rows - 1) / rows;
     if (grid > INT32_MAX)
         return LMC_ERR_INVALID_ARG;
     P.angle_rows = P.half > 0 ? kThreads / P.half : 0;
@@ -676,20 +784,25 @@ int launch(RotatePlan &P, int width, cudaStream_t stream) {
     P.unit_step = at_once % P.units;
     const int per_lane = (P.items + P.group - 1) / P.group;
     void (*kern)(RotatePlan) = nullptr;
-    if (width == 1)
-        kern = lmc_rotate_kernel<T2, 1, kTo>;
-    else if (per_lane > 3)
-        kern = lmc_rotate_kernel<T2, 8, kTo>;
-    else if (P.pairs)
-        kern = per_lane == 3   ? lmc_rotate_eights_kernel<T2, 3, true, kTo>
-               : per_lane == 2 ? lmc_rotate_eights_kernel<T2, 2, true, kTo>
-                               : lmc_rotate_eights_kernel<T2, 1, true, kTo>;
-    else
-        kern = per_lane == 3   ? lmc_rotate_eights_kernel<T2, 3, false, kTo>
-               : per_lane == 2 ? lmc_rotate_eights_kernel<T2, 2, false, kTo>
-                               : lmc_rotate_eights_kernel<T2, 1, false, kTo>;
+    const bool in_registers = kTo != kDivided && width == 8 && (eight_lanes || per_lane <= 3);
+    if constexpr (kTo != kDivided) {
+        if (eight_lanes)
+            kern = P.pairs ? lmc_rotate_long_kernel<T2, true, kTo> : lmc_rotate_long_kernel<T2, false, kTo>;
+        else if (!in_registers)
+            ;
+        else if (P.pairs)
+            kern = per_lane == 3   ? lmc_rotate_eights_kernel<T2, 3, true, kTo>
+                   : per_lane == 2 ? lmc_rotate_eights_kernel<T2, 2, true, kTo>
+                                   : lmc_rotate_eights_kernel<T2, 1, true, kTo>;
+        else
+            kern = per_lane == 3   ? lmc_rotate_eights_kernel<T2, 3, false, kTo>
+                   : per_lane == 2 ? lmc_rotate_eights_kernel<T2, 2, false, kTo>
+                                   : lmc_rotate_eights_kernel<T2, 1, false, kTo>;
+    }
+    if (!in_registers)
+        kern = width == 8 ? lmc_rotate_kernel<T2, 8, kTo> : lmc_rotate_kernel<T2, 1, kTo>;
     const size_t smem = (size_t)rows * P.half * sizeof(float2) + (size_t)(P.half + 1) / 2 * 2 * sizeof(uint64_t) +
-                        (width == 8 && per_lane <= 3 && P.norm_dim > 0 ? (size_t)P.head_dim * sizeof(float) : 0);
+                        (in_registers && P.norm_dim > 0 ? (size_t)P.head_dim * sizeof(float) : 0);
     return follow(kern, dim3((unsigned)grid), kThreads, smem, stream, P) ? LMC_OK : LMC_ERR_CUDA;
 }
 
@@ -801,6 +914,8 @@ extern "C" int lmc_append_rotated(const lmc_layout *L, const lmc_entries *e, con
     plan_heads(P, r, width);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const bool bf16 = rows_dtype == LMC_E_BF16;
+    if (e->dtype == LMC_E_E4M3 && P.code_inverse == 0.0f)
+        return bf16 ? launch<__nv_bfloat162, kDivided>(P, width, s) : launch<__half2, kDivided>(P, width, s);
     if (e->dtype == LMC_E_E4M3)
         return bf16 ? launch<__nv_bfloat162, kCodes>(P, width, s) : launch<__half2, kCodes>(P, width, s);
     return bf16 ? launch<__nv_bfloat162, kEntries>(P, width, s) : launch<__half2, kEntries>(P, width, s);
