@@ -245,7 +245,14 @@ __device__ __forceinline__ void finish(const RotatePlan &P, const float2 *cs, ui
 
 // Steps of the angles and the rows' cosines and sines in shared memory; where the
 // rows' entries lie.
-template <Result kTo>
+//
+// kHalvesOrder, kPairsOrder: in the order in which lanes of consecutive pieces of eight values read
+// them, 16 bytes at a time without bank conflicts: a piece's first 16 bytes of all
+// pieces, then the second ones. For kHalvesOrder that is the cosines of two angles
+// and their sines, for kPairsOrder (cosine, sine) of two angles.
+enum Order { kPlainOrder, kHalvesOrder, kPairsOrder };
+
+template <Result kTo, Order kOrder = kPlainOrder>
 __device__ __forceinline__ void make_angles(const RotatePlan &P, float2 *cs, uint64_t *steps, uint8_t **dst, int64_t row0,
                                             int rows) {
     if (kTo != kRows && (int)threadIdx.x < rows) {
@@ -273,7 +280,15 @@ __device__ __forceinline__ void make_angles(const RotatePlan &P, float2 *cs, uin
     int row = threadIdx.x / P.half, k = threadIdx.x - row * P.half;
     while (row < rows) {
         const float2 r = turn(__ldca(P.angles + row0 + row), steps[k]);
-        cs[row * P.half + k] = make_float2(r.x * scale, r.y * scale);
+        if constexpr (kOrder == kHalvesOrder) {
+            float *const at = reinterpret_cast<float *>(cs + row * P.half) + ((k >> 1 & 3) * (P.half >> 3) + (k >> 3)) * 4 + (k & 1);
+            at[0] = r.x * scale;
+            at[2] = r.y * scale;
+        } else if constexpr (kOrder == kPairsOrder) {
+            cs[row * P.half + ((k >> 1 & 1) * (P.half >> 2) + (k >> 2)) * 2 + (k & 1)] = make_float2(r.x * scale, r.y * scale);
+        } else {
+            cs[row * P.half + k] = make_float2(r.x * scale, r.y * scale);
+        }
         row += P.angle_rows;
         k += P.angle_step;
         if (k >= P.half) {
@@ -308,9 +323,10 @@ __device__ __forceinline__ Two plus_product(Two a, Two b, Two c) {
     return r;
 }
 
-// Eight values as four pairs: from a piece, times a factor and the weights from `at` on,
-// turned (two whole pairs to a float4 of angles, or with the piece half a turned part
-// away), and written.
+// Eight values as four pairs: from a piece, times a factor and the weights of the
+// values from `at` on (first halves of all pieces, then second ones), turned as the
+// head's `piece` (two whole pairs to a float4 of angles, or with the piece half a
+// turned part away), and written.
 template <typename T2>
 __device__ __forceinline__ void open(Two (&x)[4], const uint4 &raw) {
     const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
@@ -320,32 +336,33 @@ __device__ __forceinline__ void open(Two (&x)[4], const uint4 &raw) {
         x[k] = two(v.x, v.y);
     }
 }
-__device__ __forceinline__ void weigh(Two (&x)[4], const float *weights, float f, int at) {
-    const float4 v = *reinterpret_cast<const float4 *>(weights + at), w = *reinterpret_cast<const float4 *>(weights + at + 4);
+__device__ __forceinline__ void weigh(Two (&x)[4], const float *weights, int head_dim, float f, int at) {
+    const float4 v = *reinterpret_cast<const float4 *>(weights + at / 2);
+    const float4 w = *reinterpret_cast<const float4 *>(weights + (head_dim + at) / 2);
     const Two g = two(f, f);
     x[0] = x[0] * g * two(v.x, v.y);
     x[1] = x[1] * g * two(v.z, v.w);
     x[2] = x[2] * g * two(w.x, w.y);
     x[3] = x[3] * g * two(w.z, w.w);
 }
-__device__ __forceinline__ void turn_pairs(Two (&a)[4], const float2 *angles) {
-    const float4 *const r = reinterpret_cast<const float4 *>(angles);
+__device__ __forceinline__ void turn_pairs(Two (&a)[4], const float2 *angles, int half, int piece) {
+    const float4 *const r = reinterpret_cast<const float4 *>(angles) + piece;
 #pragma unroll
     for (int k = 0; k < 2; k++) {
-        const float4 c = r[k];
+        const float4 c = r[k * (half >> 2)];
         const float2 u = apart(a[2 * k]), v = apart(a[2 * k + 1]);
         a[2 * k] = plus_product(two(u.x, u.x), two(c.x, c.y), two(u.y, u.y) * two(-c.y, c.x));
         a[2 * k + 1] = plus_product(two(v.x, v.x), two(c.z, c.w), two(v.y, v.y) * two(-c.w, c.z));
     }
 }
-__device__ __forceinline__ void turn_halves(Two (&a)[4], Two (&b)[4], const float2 *angles) {
-    const float4 *const r = reinterpret_cast<const float4 *>(angles);
+__device__ __forceinline__ void turn_halves(Two (&a)[4], Two (&b)[4], const float2 *angles, int half, int piece) {
+    const float4 *const r = reinterpret_cast<const float4 *>(angles) + piece;
 #pragma unroll
     for (int k = 0; k < 4; k++) {
-        const float4 c = r[k];
-        const Two u = a[k], v = b[k], cosine = two(c.x, c.z);
-        a[k] = plus_product(u, cosine, v * two(-c.y, -c.w));
-        b[k] = plus_product(v, cosine, u * two(c.y, c.w));
+        const float4 c = r[k * (half >> 3)];
+        const Two u = a[k], v = b[k], cosine = two(c.x, c.y);
+        a[k] = plus_product(u, cosine, v * two(-c.z, -c.w));
+        b[k] = plus_product(v, cosine, u * two(c.z, c.w));
     }
 }
 // `plain`: codes of values that were neither normalised nor turned, as lmc_append does.
@@ -429,8 +446,9 @@ __global__ void __launch_bounds__(kThreads) lmc_rotate_eights_kernel(const __gri
         load();  // while the angles are made
     if (P.norm_dim > 0)
         for (int k = threadIdx.x; k < P.head_dim; k += kThreads)
-            weights[k] = P.weight != nullptr && k < P.norm_dim ? __ldca(P.weight + k) : 1.0f;
-    make_angles<kTo>(P, cs, steps, dst, row0, rows);
+            weights[(k >> 2 & 1) * (P.head_dim >> 1) + (k >> 3) * 4 + (k & 3)] =
+                P.weight != nullptr && k < P.norm_dim ? __ldca(P.weight + k) : 1.0f;
+    make_angles<kTo, kPairs ? kPairsOrder : kHalvesOrder>(P, cs, steps, dst, row0, rows);
     __syncthreads();
 
     // codes: what is not turned is brought to its scale by the norm's factor
@@ -485,10 +503,10 @@ __global__ void __launch_bounds__(kThreads) lmc_rotate_eights_kernel(const __gri
 #pragma unroll
                 for (int n = 0; n < kItems; n++) {
                     if (there[n]) {
-                        weigh(a[n], weights, place[n] >= P.norm_dim ? 1.0f : turned[n] ? norm : norm * code, place[n]);
+                        weigh(a[n], weights, P.head_dim, place[n] >= P.norm_dim ? 1.0f : turned[n] ? norm : norm * code, place[n]);
                         if constexpr (!kPairs) {
                             if (turned[n])
-                                weigh(b[n], weights, place[n] + P.half < P.norm_dim ? norm : 1.0f, place[n] + P.half);
+                                weigh(b[n], weights, P.head_dim, place[n] + P.half < P.norm_dim ? norm : 1.0f, place[n] + P.half);
                         }
                     }
                 }
@@ -504,9 +522,9 @@ __global__ void __launch_bounds__(kThreads) lmc_rotate_eights_kernel(const __gri
                     uint8_t *const at = to + place[n] * kBytes;
                     if (turned[n]) {
                         if constexpr (kPairs) {
-                            turn_pairs(a[n], angles + (lane + n * P.group) * 4);
+                            turn_pairs(a[n], angles, P.half, lane + n * P.group);
                         } else {
-                            turn_halves(a[n], b[n], angles + (lane + n * P.group) * 8);
+                            turn_halves(a[n], b[n], angles, P.half, lane + n * P.group);
                             put<T2, kTo>(P, at + P.half * kBytes, b[n]);
                         }
                     }
@@ -586,8 +604,9 @@ __global__ void __launch_bounds__(kThreads, kLongCtas) lmc_rotate_long_kernel(co
     }
     if (P.norm_dim > 0)
         for (int k = threadIdx.x; k < P.head_dim; k += kThreads)
-            weights[k] = P.weight != nullptr && k < P.norm_dim ? __ldca(P.weight + k) : 1.0f;
-    make_angles<kTo>(P, cs, steps, dst, row0, rows);
+            weights[(k >> 2 & 1) * (P.head_dim >> 1) + (k >> 3) * 4 + (k & 3)] =
+                P.weight != nullptr && k < P.norm_dim ? __ldca(P.weight + k) : 1.0f;
+    make_angles<kTo, kPairs ? kPairsOrder : kHalvesOrder>(P, cs, steps, dst, row0, rows);
     __syncthreads();
     if (row >= rows)
         return;
@@ -632,16 +651,16 @@ __global__ void __launch_bounds__(kThreads, kLongCtas) lmc_rotate_long_kernel(co
         Two a[4], b[4];
         open<T2>(a, lo[n]);
         if (P.norm_dim > 0)
-            weigh(a, weights, place[n] >= P.norm_dim ? 1.0f : turned ? norm : straight, place[n]);
+            weigh(a, weights, P.head_dim, place[n] >= P.norm_dim ? 1.0f : turned ? norm : straight, place[n]);
         uint8_t *const at = to + place[n] * kBytes;
         if (turned) {
             if constexpr (kPairs) {
-                turn_pairs(a, angles + (lane + n * kLongGroup) * 4);
+                turn_pairs(a, angles, P.half, lane + n * kLongGroup);
             } else if (n == 0) {
                 open<T2>(b, hi);
                 if (P.norm_dim > 0)
-                    weigh(b, weights, place[n] + P.half < P.norm_dim ? norm : 1.0f, place[n] + P.half);
-                turn_halves(a, b, angles + lane * 8);
+                    weigh(b, weights, P.head_dim, place[n] + P.half < P.norm_dim ? norm : 1.0f, place[n] + P.half);
+                turn_halves(a, b, angles, P.half, lane);
                 put<T2, kTo>(P, at + P.half * kBytes, b);
             }
         }
