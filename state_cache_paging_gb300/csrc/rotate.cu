@@ -33,7 +33,6 @@ constexpr int kMaxRows = 64;           // of a CTA
 constexpr int kMaxAngles = 2048;       // of a CTA's rows together (16 KB), where it has several
 constexpr int kMaxHeadDim = 4096;
 
-constexpr int64_t kManyHeads = 152 * 4 * 32;  // long ones: of a GPU full of groups of eight lanes
 constexpr int kManyCtas = 152 * 16;   // waves of CTAs enough to even out
 
 // Activations; a page's entries, as they are or as fp8 codes (kDivided: of a scale that
@@ -387,7 +386,7 @@ __device__ __forceinline__ void put(const RotatePlan &P, uint8_t *at, const Two 
 // the copy rate leaves some 200 of a warp), so values are widened once and multiplied
 // by pairs, and the weights, 1 where there is no norm, lie in shared memory.
 template <typename T2, int kItems, bool kPairs, Result kTo>
-__global__ void __launch_bounds__(kThreads) lmc_rotate_eights_kernel(const __grid_constant__ RotatePlan P) {
+__global__ void __launch_bounds__(kThreads, kItems == 1 ? 5 : 5 - kItems) lmc_rotate_eights_kernel(const __grid_constant__ RotatePlan P) {
     extern __shared__ __align__(16) float2 cs[];  // [rows][half], the steps [half], the weights [head_dim]
     __shared__ uint8_t *dst[kMaxRows];
     constexpr int kBytes = codes(kTo) ? 1 : 2;
@@ -564,13 +563,13 @@ __global__ void __launch_bounds__(kThreads) lmc_rotate_eights_kernel(const __gri
     }
 }
 
-// Heads of more than 32 pieces, many of them: eight lanes take one, up to kLongItems
-// pieces each, which are widened twice. A latent's 72 pieces fill such a group's nine
-// rounds (of 32 lanes' three they would fill three quarters), four heads' sums of
-// squares take three shuffles together instead of five each, and 32 heads a CTA keep
-// many CTAs at different steps. (131072 fp8 entries of 576 values: @NEW@ us, with a warp
-// per head and the next one's pieces asked for ahead 77; two heads a group one after
-// another 72, CTAs that stay 84 and more.)
+// Heads of more than 32 pieces: eight lanes take one, up to kLongItems pieces each,
+// which are widened twice. A latent's 72 pieces fill such a group's nine rounds (of 32
+// lanes' three they would fill three quarters), four heads' sums of squares take three
+// shuffles together instead of five each, and 32 heads a CTA keep many CTAs at
+// different steps. (131072 fp8 entries of 576 values: 63 us; 1024 of them 6.0. With a
+// warp per head and the next one's pieces asked for ahead 77 and 7.6; two heads a group
+// one after another 72; CTAs that stay 84.)
 constexpr int kLongItems = 9, kLongGroup = 8, kLongCtas = 4;
 
 template <typename T2, bool kPairs, Result kTo>
@@ -776,10 +775,8 @@ void plan_heads(RotatePlan &P, const lmc_rotation *r, int width) {
 
 template <typename T2, Result kTo>
 int launch(RotatePlan &P, int width, cudaStream_t stream) {
-    // (a warp a head spreads fewer heads than that over more CTAs)
     const bool eight_lanes = kTo != kDivided && width == 8 && P.items > 32 && P.items <= kLongItems * kLongGroup && P.rest == 0 &&
-                             (P.pairs || P.turned <= kLongGroup) && P.units <= kThreads / kLongGroup &&
-                             P.num_rows * P.units >= kManyHeads;
+                             (P.pairs || P.turned <= kLongGroup) && P.units <= kThreads / kLongGroup;
     if (eight_lanes)
         P.group = kLongGroup;
     // Rows of a CTA: enough heads for every group of lanes a few times, so that

@@ -74,7 +74,7 @@ CALLS = {
     "scan": lambda f, L, base: C._scan(f, L, base),
     "long scan": lambda f, L, base: C._scan(f, L, base, n=1 << 20),
 }
-KERNELS = {"rotate": ["eights"], "rotate odd": ["rotate_kernel"], "append": ["eights"], "append odd": ["rotate_kernel"],
+KERNELS = {"rotate": ["eights"], "rotate odd": ["rotate_kernel"], "append": ["long"], "append odd": ["rotate_kernel"],
            "step": ["step"], "scan": ["scan"], "long scan": ["scan", "join", "scan"]}
 
 
