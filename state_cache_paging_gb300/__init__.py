@@ -852,9 +852,11 @@ def lmc_append_rotated(layout: Layout, layer: int, pool, table, requests, positi
 # ----------------------------------------------------------------------------
 
 def _linear(layout: Layout, layer: int, table, home: int, lengths, q, k, v, decay, out, scale: float) -> lmc_linear:
-    for name, t in (("q", q), ("k", k), ("v", v), ("out", out), ("decay", decay)):
-        if t.get_device() != home:
-            _away(name, t, home)
+    for name, t in (("q", q), ("k", k), ("v", v), ("out", out)):
+        if t.get_device() != home:  # (copied by TMA: no host memory)
+            _refuse(f"{name} must be on the current device")
+    if decay.get_device() != home:
+        _away("decay", decay, home)
     qs, ks, vs, os_, ds = q.stride(), k.stride(), v.stride(), out.stride(), decay.stride()
     shape, n = v.shape, v.shape[0]
     if len(q.shape) != 3 or len(shape) != 3 or k.shape != q.shape or out.shape != shape or q.shape[0] != n or \

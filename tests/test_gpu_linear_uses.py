@@ -473,3 +473,34 @@ def test_a_shared_prefix(op):
     torch.cuda.synchronize()
     assert int(status.item()) == 0
     G.check(P, pool.cpu(), out.cpu(), [N, N], new, table, start, q, k, v, dec, 0.1, "bf16")
+
+
+@pytest.mark.parametrize("op", ["scan", "step"])
+def test_the_binding_refuses(op):
+    """Tensors of other memory, types and shapes, before anything is enqueued."""
+    H, d, N = 2, 64, 32
+    P = R.States(lmc, H, d, d, N, 4)
+    x, status = torch.randn(1, H, d, device=DEV).bfloat16(), flag()
+    args = dict(q=x, k=x, v=x, decay=torch.zeros(1, H, device=DEV), out=torch.zeros_like(x))
+    pool = P.pool.cuda()
+
+    def call(lengths=ints([0]), table=ints([[0]]), starts=ints([0, 1]), ws=None, **kw):
+        a = {**args, **kw}
+        a = [a[n] for n in ("q", "k", "v", "decay", "out")]
+        if op == "scan":
+            lmc.lmc_linear_scan(P.layout, P.layer, pool, table, starts, lengths, *a, workspace(P, 1, 1)[0] if ws is None else ws,
+                                status)
+        else:
+            lmc.lmc_linear_step(P.layout, P.layer, pool, table, lengths, *a, status)
+    call()
+    bad = [dict(q=x.cpu().pin_memory()), dict(out=torch.zeros(1, H, d).bfloat16().pin_memory()), dict(q=x.half()),
+           dict(v=x[:, :, :32]), dict(k=x[:, :1]), dict(q=x[0]), dict(decay=args["decay"].double()),
+           dict(decay=args["decay"][:, :1]), dict(decay=torch.zeros(1, H)), dict(lengths=torch.zeros(1, dtype=torch.int64, device=DEV)),
+           dict(lengths=ints([0, 0])), dict(table=ints([0])), dict(out=x), dict(q=x.expand(2, H, d))]
+    if op == "scan":
+        bad += [dict(starts=ints([0])), dict(ws=torch.zeros(16, dtype=torch.uint8, device=DEV))]
+    for kw in bad:
+        with pytest.raises(lmc.LmcError):
+            call(**kw)
+    torch.cuda.synchronize()
+    assert int(status.item()) == 0
