@@ -10,9 +10,9 @@
 // update. What leaves a tile for the next is only S, in binary32.
 //
 // One token is bound by reading and writing the states: 256 requests of 32 heads of
-// 128 x 128 take 167 us, 95 % of the measured copy rate. Prompts are bound by the
+// 128 x 128 take 166 us, 96 % of the measured copy rate. Prompts are bound by the
 // instructions between the products: 32 requests of 8192 tokens of 32 heads in bf16
-// take 1634 us, 83 % of what reading q, k and v and writing the results takes at the
+// take 1670 us, 82 % of what reading q, k and v and writing the results takes at the
 // copy rate (in f16 some 58 %: binary32's range is brought into f16's row by row).
 // What brought it there from 3245 us: one role per kind of work (a warp waits for
 // nothing that it does not need), four exact bf16 parts of v instead of three truncated
@@ -20,9 +20,10 @@
 // instruction, and results that leave by TMA.
 //
 // Long requests are cut where there are fewer heads than SMs: a first pass finds what
-// each segment adds to the state, a second one joins them, and the third makes the
-// results of all segments at once (131072 tokens of one request: 341 us; the first two
-// passes 160 of them).
+// each segment adds to the state (updates taking turns in two places of tensor memory:
+// 347 us become 339), a second one joins them, and the third makes the results of all
+// segments at once (131072 tokens of one request, 8 heads: 339 us, the first two passes
+// some 145 of them).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
@@ -218,6 +219,8 @@ constexpr int kScanThreads = 28 * 32;
 // Registers per thread of the warpgroups: 2 x 112 + 2 x 64 + 56 + 56 + 40 of the 7 x
 // 72 the CTA starts with.
 constexpr int kStateRegisters = 112, kPartRegisters = 64, kWeightRegisters = 56, kResultRegisters = 56, kOtherRegisters = 40;
+static_assert(2 * kStateRegisters + 2 * kPartRegisters + kWeightRegisters + kResultRegisters + kOtherRegisters == 7 * 72,
+              "a split of more registers than the CTA has would wait forever");
 // shared memory behind the stages: the weights, the result on its way
 constexpr int kWeightsAt = kStages * kStageBytes, kResultAt = kWeightsAt + kPanel;
 constexpr int kWarpResult = kTile * 64;  // bytes of a warp's part of a result: 32 values of each token
@@ -227,6 +230,7 @@ constexpr uint32_t kLook = 20000;  // so many ns each
 // columns of tensor memory
 constexpr uint32_t kScores = 0, kUpdate = 64, kFromState = 192, kFromTile = 256, kState = 320, kParts = 384;
 constexpr uint32_t kPartColumns = kTile / 2;
+constexpr uint32_t kOtherUpdate = kFromState;  // where only states are made: updates in turns
 constexpr int kRing = 4;              // tiles whose decays are at hand
 constexpr int kSms = 152;
 constexpr int64_t kLeastSegment = 512;  // tokens
@@ -269,11 +273,11 @@ static_assert(sizeof(Decays) % 16 == 0, "two tokens' logs are read at once");
 struct ScanControl {
     uint64_t full[kStages], free[kStages];
     uint64_t decays_full[kRing];
-    uint64_t unit_full[2], lift_full[2], down_full[2];  // f16
+    uint64_t unit_full[kRing], lift_full[2], down_full[2];  // f16
     uint64_t score_full, score_free;
     uint64_t weight_full, weight_free;
     uint64_t parts_full[2], parts_free[2];  // the upper and the lower parts
-    uint64_t update_full, update_free;
+    uint64_t update_full[2], update_free[2];  // (one, but where only states are made)
     uint64_t state_full, state_free, out_full, out_free;
     uint64_t ended[2];
     uint32_t tmem;
@@ -545,8 +549,10 @@ __device__ __forceinline__ Twice plus(const Twice &x, float high, float low) {
 // `drift`: how much the tiles' rounded decays lack of the exact ones so far,
 // relatively; a tile's makes up for it, so that a state that decays slowly by
 // the same factor tile after tile keeps its digits.
-template <bool kBf16>
-__device__ __forceinline__ void sum_decays(Decays &D, float g0, float g1, int rows, float scale, float &drift) {
+// `ready` waits until they may be written.
+template <bool kBf16, typename Ready>
+__device__ __forceinline__ void sum_decays(Decays &D, float g0, float g1, int rows, float scale, float &drift,
+                                           Ready ready) {
     const int lane = threadIdx.x & 31;
     // (a NaN is not clamped, and makes one of everything behind it)
     auto log2_of = [](float g) {
@@ -563,21 +569,17 @@ __device__ __forceinline__ void sum_decays(Decays &D, float g0, float g1, int ro
     }
     const Twice total = {__shfl_sync(0xffffffffu, sum.high, 31), __shfl_sync(0xffffffffu, sum.low, 31)};
     const Twice first = plus(sum, -b, 0.0f);
-#pragma unroll
-    for (int i = 0; i < 2; i++) {
-        const Twice &g = i ? sum : first;
-        D.log[2 * lane + i] = make_float2(g.high, g.low);
-        D.since[2 * lane + i] = exp2_fast(g.high + g.low) * scale;
-    }
+    const float2 since = make_float2(exp2_fast(first.high + first.low) * scale, exp2_fast(sum.high + sum.low) * scale);
     const float f0 = 2 * lane < rows ? exp2_fast((total.high - first.high) + (total.low - first.low)) : 0.0f;
     const float f1 = 2 * lane + 1 < rows ? exp2_fast((total.high - sum.high) + (total.low - sum.low)) : 0.0f;
+    uint4 left;
     if constexpr (kBf16) {
         const uint32_t p = pack<true>(f0, f1);
         const float r0 = f0 - from_q(p & 0xffff, true), r1 = f1 - from_q(p >> 16, true);
         const uint32_t q = pack<true>(r0, r1);
-        D.left[lane] = make_uint4(p, 0, q, pack<true>(r0 - from_q(q & 0xffff, true), r1 - from_q(q >> 16, true)));
+        left = make_uint4(p, 0, q, pack<true>(r0 - from_q(q & 0xffff, true), r1 - from_q(q >> 16, true)));
     } else {
-        D.left[lane] = make_uint4(__float_as_uint(f0), __float_as_uint(f1), 0, 0);
+        left = make_uint4(__float_as_uint(f0), __float_as_uint(f1), 0, 0);
     }
     const float x = total.high + total.low;
     float grow;
@@ -601,6 +603,10 @@ __device__ __forceinline__ void sum_decays(Decays &D, float g0, float g1, int ro
         grow = exp2_fast(x);
         drift = 0.0f;
     }
+    ready();
+    *reinterpret_cast<float4 *>(&D.log[2 * lane]) = make_float4(first.high, first.low, sum.high, sum.low);
+    *reinterpret_cast<float2 *>(&D.since[2 * lane]) = since;
+    D.left[lane] = left;
     if (lane == 0)
         D.grow = grow;
 }
@@ -644,8 +650,10 @@ __device__ __forceinline__ void load_tiles(const ScanPlan &P, ScanControl &C, ui
 
 // One warp: each tile's decays. They go to their place of the ring when the stage
 // of the tile behind is free: the products of that stage's last tile are done, so
-// the result of the tile before it has been read, whose place this was.
-template <bool kBf16>
+// the result of the tile before it has been read, whose place this was. (Where only
+// states are made, updates take turns, and it is the tile before that one: the stage
+// of two tiles behind.)
+template <bool kBf16, bool kStatesOnly>
 __device__ __forceinline__ void tell_decays(const ScanPlan &P, ScanControl &C) {
     static_assert(kRing >= kStages, "a place is read until the next tile's result is made");
     int looks = kLooks;
@@ -665,9 +673,11 @@ __device__ __forceinline__ void tell_decays(const ScanPlan &P, ScanControl &C) {
         const uint32_t n = T.n;
         const float h0 = 2 * lane < T.rows ? g0 : 0.0f, h1 = 2 * lane + 1 < T.rows ? g1 : 0.0f;
         fetch(T.row + T.rows);
-        if (n + 1 >= kStages)
-            scan_wait(C, &C.free[(n + 1) % kStages], ((n + 1) / kStages - 1) & 1, looks);
-        sum_decays<kBf16>(C.decays[n % kRing], h0, h1, T.rows, P.L.scale, drift);
+        sum_decays<kBf16>(C.decays[n % kRing], h0, h1, T.rows, P.L.scale, drift, [&] {
+            constexpr uint32_t kAhead = kStatesOnly ? 2 : 1;
+            if (n + kAhead >= kStages)
+                scan_wait(C, &C.free[(n + kAhead) % kStages], ((n + kAhead) / kStages - 1) & 1, looks);
+        });
         __syncwarp();
         if (lane == 0)
             bar_arrive(&C.decays_full[n % kRing]);
@@ -703,19 +713,21 @@ __device__ __forceinline__ void multiply_forward(const ScanPlan &P, ScanControl 
             commit(&C.score_full);
         }
         // as the parts come: the upper one or two, then the lower
-        if (n >= 1)
-            scan_wait(C, &C.update_free, (n - 1) & 1, looks);
+        const int b = kStatesOnly ? n & 1 : 0, use = kStatesOnly ? n >> 1 : n;
+        const uint32_t to = tmem + (b ? kOtherUpdate : kUpdate);
+        if (use >= 1)
+            scan_wait(C, &C.update_free[b], (use - 1) & 1, looks);
 #pragma unroll 1
         for (int half = 0; half < 2; half++) {
             scan_wait(C, &C.parts_full[half], n & 1, looks);
             fence_after();
 #pragma unroll
             for (int s = 0; s < kSteps; s++)
-                multiply_held(tmem + kUpdate, tmem + kParts + kSteps * 8 * half + 8 * s, k + (s & 3) * (2048 >> 4), update,
+                multiply_held(to, tmem + kParts + kSteps * 8 * half + 8 * s, k + (s & 3) * (2048 >> 4), update,
                               s > 0 || half > 0);
             commit(&C.parts_free[half]);
         }
-        commit(&C.update_full);
+        commit(&C.update_full[b]);
         commit(&C.free[st]);
     }
 }
@@ -888,7 +900,7 @@ __device__ __forceinline__ void split(const ScanPlan &P, ScanControl &C, uint8_t
             fence_before();
             __syncwarp();
             if (lane == 0) {
-                bar_arrive(&C.unit_full[n & 1]);
+                bar_arrive(&C.unit_full[n % kRing]);
                 bar_arrive(&C.parts_full[0]);
                 bar_arrive(&C.parts_full[1]);
             }
@@ -1132,15 +1144,16 @@ __device__ __forceinline__ void carry(const ScanPlan &P, ScanControl &C) {
         if (kStatesOnly)
             total += D.log[kTile - 1].x + D.log[kTile - 1].y;
         if (!kBf16)
-            scan_wait(C, &C.unit_full[n & 1], (n >> 1) & 1, looks);
+            scan_wait(C, &C.unit_full[n % kRing], (n / kRing) & 1, looks);
         const float unit = kBf16 ? 1.0f : D.unit[j];
-        scan_wait(C, &C.update_full, n & 1, looks);
+        const int b = kStatesOnly ? n & 1 : 0;
+        scan_wait(C, &C.update_full[b], (kStatesOnly ? n >> 1 : n) & 1, looks);
         fence_after();
         if (mine) {
 #pragma unroll
             for (int c = 0; c < 8; c++) {
                 uint32_t u[8];
-                load_o8(u, lanes + kUpdate + i0 + 8 * c);
+                load_o8(u, lanes + (b ? kOtherUpdate : kUpdate) + i0 + 8 * c);
                 wait_ld();
 #pragma unroll
                 for (int i = 0; i < 4; i++) {
@@ -1154,7 +1167,7 @@ __device__ __forceinline__ void carry(const ScanPlan &P, ScanControl &C) {
         fence_before();
         __syncwarp();
         if (lane == 0)
-            bar_arrive(&C.update_free);
+            bar_arrive(&C.update_free[b]);
         if (block >= 0 && block < L.num_blocks)
             write(L.pages + block * L.page_stride + head);
         else if (block != -1 && threadIdx.x == 0)
@@ -1305,22 +1318,23 @@ __global__ void __launch_bounds__(kScanThreads, 1) lmc_linear_scan_kernel(const 
             bar_init(&C.full[i], 1);
             bar_init(&C.free[i], kStatesOnly ? 1 : 2);
         }
-        for (int i = 0; i < kRing; i++)
+        for (int i = 0; i < kRing; i++) {
             bar_init(&C.decays_full[i], 1);
-        for (int i = 0; i < 2; i++) {
             bar_init(&C.unit_full[i], kPartWarps);
+        }
+        for (int i = 0; i < 2; i++) {
             bar_init(&C.lift_full[i], kWeightWarps);
             bar_init(&C.down_full[i], kStateWarps);
             bar_init(&C.ended[i], 1);
             bar_init(&C.parts_full[i], kPartWarps);
             bar_init(&C.parts_free[i], 1);
+            bar_init(&C.update_full[i], 1);
+            bar_init(&C.update_free[i], kStateWarps);
         }
         bar_init(&C.weight_full, kWeightWarps);
         bar_init(&C.weight_free, 1);
         bar_init(&C.score_full, 1);
         bar_init(&C.score_free, kWeightWarps);
-        bar_init(&C.update_full, 1);
-        bar_init(&C.update_free, kStateWarps);
         bar_init(&C.state_full, kStateWarps);
         bar_init(&C.out_full, 1);
         bar_init(&C.state_free, 1);
@@ -1367,7 +1381,7 @@ __global__ void __launch_bounds__(kScanThreads, 1) lmc_linear_scan_kernel(const 
     } else {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kOtherRegisters));
         if (warp == kDecayWarp) {
-            tell_decays<kBf16>(P, C);
+            tell_decays<kBf16, kStatesOnly>(P, C);
         } else if (elect()) {
             if (warp == kLoadWarp)
                 load_tiles<kStatesOnly>(P, C, scan_mem);
