@@ -715,7 +715,8 @@ LMC_API int lmc_linear_scan(const lmc_layout *layout, const lmc_linear *linear, 
                             void *stream);
 
 /* Bytes of lmc_linear_scan's workspace for num_requests requests of num_rows
- * tokens together and num_heads states of a page. */
+ * tokens together and num_heads states of a page: enough for calls of fewer
+ * requests and tokens, too. */
 LMC_API int lmc_linear_scan_workspace(const lmc_layout *layout, int32_t layer, int32_t num_requests, int64_t num_rows,
                                       int32_t num_heads, int64_t *out);
 

@@ -1571,7 +1571,9 @@ struct ScanWork {
 ScanWork scan_work(int64_t rec_bytes, int64_t H, int64_t num_rows) {
     ScanWork W;
     W.segment = segment_of(num_rows, H);
-    const int64_t n = num_rows / W.segment;
+    // at least num_rows / segment, and never less for more rows: memory for the largest
+    // call serves all smaller ones
+    const int64_t n = std::min(num_rows / kLeastSegment, kSms / H);
     W.slots = 0;
     W.totals = (n * rec_bytes + 255) / 256 * 256;
     W.bytes = W.totals + (n * H * 4 + 255) / 256 * 256 + 256;

@@ -504,3 +504,41 @@ def test_the_binding_refuses(op):
             call(**kw)
     torch.cuda.synchronize()
     assert int(status.item()) == 0
+
+
+@pytest.mark.parametrize("N", [1, 7, 33])
+def test_small_blocks(N):
+    """Tiles of a token or a few, each with its snapshot."""
+    G.run([0, 5, 12], [40, 1, 9], N=N, act="f16")
+
+
+def test_a_captured_scan_of_other_lengths():
+    """A padded batch: one graph, replayed with other starts, lengths and tables in
+    the same memory (requests that are skipped, empty, and cut into segments)."""
+    H, d, N, rows, R_ = 2, 64, 1024, 5000, 4
+    P = R.States(lmc, H, d, d, N, 14)
+    P.pages()[:] = torch.randn(14, H, d, d, generator=torch.Generator().manual_seed(5))
+    q, k, v, dec, _ = G.inputs(rows, H, H, d, d, "bf16", "token", 31)
+    a = [x.cuda() for x in (q, k, v, dec)]
+    pool, out, status = P.pool.cuda(), torch.zeros(rows, H, d, dtype=torch.bfloat16, device=DEV), flag()
+    table, starts, lengths = ints([[-1] * 5] * R_), ints([0] * (R_ + 1)), ints([-1] * R_)
+    ws = workspace(P, R_, rows)[0]
+    s, graph = torch.cuda.Stream(), torch.cuda.CUDAGraph()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.graph(graph, stream=s):
+        lmc.lmc_linear_scan(P.layout, P.layer, pool, table, starts, lengths, *a, out, ws, status, scale=0.1)
+    for had, new in (([0, 3, 1024, 0], [4096, 1, 500, 403]), ([-1, 0, 2047, 9], [7, 0, 1, 300]), ([0] * 4, [0, 0, 0, 5000]),
+                     ([-1] * 4, [0] * 4)):
+        t = torch.full((R_, 5), -1, dtype=torch.int32)
+        made = R.tables(had, new, N, 14, np.random.default_rng(1))
+        t[:, :made.shape[1]] = made
+        start = np.concatenate([[0], np.cumsum(new)]).astype(np.int32)
+        pool.copy_(P.pool)
+        out.fill_(float("nan"))
+        table.copy_(t)
+        starts.copy_(torch.from_numpy(start))
+        lengths.copy_(torch.tensor(had, dtype=torch.int32))
+        graph.replay()
+        torch.cuda.synchronize()
+        assert int(status.item()) == 0
+        G.check(P, pool.cpu(), out.cpu(), had, new, t, start, q, k, v, dec, 0.1, "bf16")

@@ -119,7 +119,9 @@ def test_scan_covers_every_segment_within_its_workspace(lmc, fake, env, R, n):
     assert fake.lmc_linear_scan_workspace(L.handle, 0, R, n, H, ctypes.byref(need)) == lmc.LMC_OK
     segment = max(512, -(-(-(-n * H // 152)) // 64) * 64)
     cuts = n // segment
-    assert cuts * rec + cuts * H * 4 <= need.value <= cuts * rec + cuts * H * 4 + 1024
+    assert cuts <= min(n // 512, 152 // H)
+    most = min(n // 512, 152 // H) * (rec + H * 4)
+    assert most <= need.value <= most + 1024
     f = Fake(lmc, fake)
     far = dict(out=base + (1 << 60))
     assert C._scan(f, L, base, R=R, n=n, ws_bytes=need.value - 1, **far) == lmc.LMC_ERR_INVALID_ARG
@@ -142,3 +144,19 @@ def test_grids_past_31_bits_are_refused(lmc, fake, env):
     assert C._step(f, L, base, **kw) == lmc.LMC_ERR_OVERFLOW
     assert C._scan(f, L, base, n=1, **kw) == lmc.LMC_ERR_OVERFLOW
     assert launches(fake) == []
+
+
+@pytest.mark.parametrize("H", [1, 4, 5, 8, 64, 153])
+def test_a_workspace_for_the_largest_call_serves_smaller_ones(lmc, H):
+    """Segments are of whole tiles, so calls of fewer tokens may have more of them."""
+    L = lmc.lmc_layout_build([W.kda(64, 1, H, 8)], 64, False, 1 << 24)
+    sizes = [lmc.lmc_linear_scan_workspace(L, 0, 3, n, H) for n in [0, 1, *range(500, 200_000, 333), 1 << 20, (1 << 31) - 1]]
+    assert sizes == sorted(sizes)
+
+
+def test_a_call_takes_the_workspace_of_a_larger_one(lmc, fake, env):
+    L, base, _ = env
+    need = ctypes.c_int64(0)
+    assert fake.lmc_linear_scan_workspace(L.handle, 0, 8, 131072, 4, ctypes.byref(need)) == lmc.LMC_OK
+    for n in range(64, 131072, 1000):
+        assert C._scan(Fake(lmc, fake), L, base, n=n, ws_bytes=need.value, out=base + (1 << 60)) == lmc.LMC_OK
