@@ -388,8 +388,10 @@ __device__ __forceinline__ void put(const RotatePlan &P, uint8_t *at, const Two 
 // normalised and turned: 90 us, 88 % of the copy rate, 112 with the angles one after
 // another; 374000 ragged rows of 8 key heads of 64 and as many values: 280 us, 81 %;
 // what is left are waits for loads, five CTAs a SM are better than four there.)
+constexpr int eights_ctas(int items) { return items == 1 ? 5 : 5 - items; }  // an SM's: 48, 80, 128 registers
+
 template <typename T2, int kItems, bool kPairs, Result kTo>
-__global__ void __launch_bounds__(kThreads, kItems == 1 ? 5 : 5 - kItems) lmc_rotate_eights_kernel(const __grid_constant__ RotatePlan P) {
+__global__ void __launch_bounds__(kThreads, eights_ctas(kItems)) lmc_rotate_eights_kernel(const __grid_constant__ RotatePlan P) {
     extern __shared__ __align__(16) float2 cs[];  // [rows][half], the steps [half], the weights [head_dim]
     __shared__ uint8_t *dst[kMaxRows];
     constexpr int kBytes = codes(kTo) ? 1 : 2;
