@@ -708,7 +708,9 @@ LMC_API int lmc_linear_step(const lmc_layout *layout, const lmc_linear *linear, 
  * same time each need their own. Status as lmc_linear_step (BAD_JOB also where
  * starts decreases or leaves [0, num_rows]; NO_SNAPSHOT for the page before
  * the request's tokens and the last one); an entry in between that lies outside
- * the pool raises BLOCK_OOR and only that snapshot is left out; TIMEOUT.
+ * the pool raises BLOCK_OOR and only that snapshot is left out; TIMEOUT. Where
+ * starts decrease anywhere, long requests of ranges that are right may be left out
+ * too, whole, as BAD_JOB; a row of two requests holds the result of either.
  * Errors: INVALID_ARG, ALIGN, OVERLAP, OVERFLOW, CUDA. */
 LMC_API int lmc_linear_scan(const lmc_layout *layout, const lmc_linear *linear, const int32_t *starts,
                             int64_t num_rows, void *pool, void *workspace, int64_t workspace_bytes, uint32_t *status,

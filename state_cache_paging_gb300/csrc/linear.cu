@@ -241,6 +241,8 @@ struct ScanPlan {
     int64_t segment;     // a request of n of these tokens (n >= 2) is cut into n segments
     float *slots;        // [num_rows / segment][H][dk][dv]: the states before segments
     float *totals;       // [num_rows / segment][H]: the decay over the segment before
+    int32_t *owners;     // [cuts]: the request whose segment the states pass made, -1: none
+    int64_t cuts;        // num_rows / segment
     int32_t k_copies, v_copies, k_panels, v_panels;  // copies for all panels, panels
     int32_t wide_out;    // whole tiles of the result are written by TMA, others 16 bytes at a time
 };
@@ -467,14 +469,15 @@ __device__ __forceinline__ int lift_of(float x) {
     return x == 0.0f ? 0 : max(-112, min(126, 14 - e));
 }
 
-// Largest r in [0, R) with starts[r] / segment + (shift ? r : 0) <= v; -1: none.
-// A warp together: 32 places at a time.
-__device__ __forceinline__ int request_of(const ScanPlan &P, int64_t v, bool shift) {
+// The request whose segments v lies among: the largest r in [0, R) with starts[r] /
+// segment <= v; -1: none. A warp together: 32 places at a time. (Where starts
+// decrease it finds one of them or another, the same every time.)
+__device__ __forceinline__ int request_of(const ScanPlan &P, int64_t v) {
     const int lane = threadIdx.x & 31;
     int64_t lo = 0, hi = P.L.R;
     for (;;) {
         const int64_t step = (hi - lo + 31) / 32, i = lo + step * lane;
-        const bool below = i < hi && __ldca(P.L.starts + i) / P.segment + (shift ? i : 0) <= v;
+        const bool below = i < hi && __ldca(P.L.starts + i) / P.segment <= v;
         const int found = __popc(__ballot_sync(0xffffffffu, below));
         if (found == 0)
             return -1;
@@ -494,26 +497,44 @@ __device__ __forceinline__ int64_t cut(int64_t T, int64_t i, int64_t n, int64_t 
     return t - (before + t) % N % kTile;
 }
 
-// States only: all segments but a request's last.
+// Whether the states before all n segments of request r, in the slots from `slot`
+// on, are the states pass's own work for r, by a warp together. It is so wherever
+// starts do not decrease: a request's segments are then found one behind the other,
+// and others' slots lie apart from its own. Where starts decrease the search may miss
+// segments, and others' may be written to the same slots: the ones of v write slot v +
+// 1, a request's first one slot v, too.
+__device__ __forceinline__ bool made_whole(const ScanPlan &P, int r, int64_t slot, int64_t n) {
+    bool whole = true;
+    for (int64_t v = slot - 1 + (threadIdx.x & 31); v < slot + n; v += 32)
+        if (v >= 0 && v < P.cuts)
+            whole = whole && __ldca(P.owners + v) == (v >= slot && v < slot + n - 1 ? r : -1);
+    return __all_sync(0xffffffffu, whole);
+}
+
+// States only: all segments but a request's last, segment v of all. Results: a CTA
+// for each request (its first segment, or all of it), then one for segment v + 1.
 template <bool kStatesOnly>
 __device__ __forceinline__ void find_item(const ScanPlan &P, Item &I) {
     const int lane = threadIdx.x & 31;
-    const int64_t v = blockIdx.x / P.L.H;
-    const int r = request_of(P, v, !kStatesOnly);
+    const int64_t x = blockIdx.x / P.L.H;
+    const bool extra = kStatesOnly || x >= P.L.R;
+    const int64_t v = !kStatesOnly && extra ? x - P.L.R : x;
+    const int r = extra ? request_of(P, v) : (int)x;
     Item J = {};
     J.h = (int)(blockIdx.x % P.L.H);
     J.r = r;
-    if (!kStatesOnly && v < P.L.R && J.h == 0 && lane == 0) {  // every request is looked at once
-        const uint32_t bad = span_of(P.L, (int)v).bad;
-        if (bad != 0)
-            atomicOr(P.L.status, bad);
-    }
     if (r >= 0) {
         const Span S = span_of(P.L, r);
-        const int64_t slot = __ldca(P.L.starts + r) / P.segment, i = v - slot - (kStatesOnly ? 0 : r);
-        const int64_t n = max((int64_t)1, S.count / P.segment);
-        // (i < 0: starts that decrease, which the search does not expect)
-        if (S.count > 0 && i >= 0 && i < (kStatesOnly ? n - 1 : n)) {
+        uint32_t bad = S.bad;
+        const int64_t slot = __ldca(P.L.starts + r) / P.segment, n = max((int64_t)1, S.count / P.segment);
+        const int64_t i = !extra ? 0 : v - slot + (kStatesOnly ? 0 : 1);
+        // (a segment before the first: starts that decrease)
+        bool work = S.count > 0 && i >= 0 && i < (kStatesOnly ? n - 1 : n) && (kStatesOnly || !extra || i > 0);
+        if (!kStatesOnly && work && n > 1 && !made_whole(P, r, slot, n)) {
+            work = false;
+            bad = LMC_ST_BAD_JOB;
+        }
+        if (work) {
             const int64_t a = cut(S.count, i, n, S.before, P.L.block_size), b = cut(S.count, i + 1, n, S.before, P.L.block_size);
             J.row = (int)(S.row + a);
             J.page = (int)((S.before + a) / P.L.block_size);
@@ -528,7 +549,11 @@ __device__ __forceinline__ void find_item(const ScanPlan &P, Item &I) {
             auto tiles = [](int tokens) { return (tokens + kTile - 1) / kTile; };
             J.tiles = tiles(head) + rest / N * tiles(N) + tiles(rest % N);
         }
+        if (!extra && bad != 0 && J.h == 0 && lane == 0)  // every request is looked at once
+            atomicOr(P.L.status, bad);
     }
+    if (kStatesOnly && J.h == 0 && lane == 0)
+        P.owners[v] = J.work ? r : -1;
     if (lane == 0)
         I = J;
 }
@@ -1419,12 +1444,14 @@ __global__ void __launch_bounds__(kJoinThreads) lmc_linear_join_kernel(const __g
     wait_for_launch();
     let_next_start();
     if (threadIdx.x < 32) {
-        const int r = request_of(P, v, false);
+        const int r = request_of(P, v);
         int n = 0;
         int64_t slot = -1;
         if (r >= 0) {
             slot = __ldca(L.starts + r) / P.segment;
             n = (int)(span_of(L, r).count / P.segment);
+            if (slot == v && n > 2 && !made_whole(P, r, slot, n))
+                n = 0;
         }
         if (threadIdx.x == 0) {
             first = slot == v ? 1 : 0;
@@ -1565,7 +1592,7 @@ int64_t segment_of(int64_t num_rows, int64_t H) {
 }
 
 struct ScanWork {
-    int64_t segment, slots, totals, bytes;  // tokens; offsets
+    int64_t segment, slots, totals, owners, bytes;  // tokens; offsets
 };
 
 ScanWork scan_work(int64_t rec_bytes, int64_t H, int64_t num_rows) {
@@ -1576,7 +1603,8 @@ ScanWork scan_work(int64_t rec_bytes, int64_t H, int64_t num_rows) {
     const int64_t n = std::min(num_rows / kLeastSegment, kSms / H);
     W.slots = 0;
     W.totals = (n * rec_bytes + 255) / 256 * 256;
-    W.bytes = W.totals + (n * H * 4 + 255) / 256 * 256 + 256;
+    W.owners = W.totals + n * H * 4;
+    W.bytes = std::max<int64_t>(256, (W.owners + n * 4 + 255) / 256 * 256);
     return W;
 }
 
@@ -1642,6 +1670,7 @@ extern "C" int lmc_linear_scan(const lmc_layout *L, const lmc_linear *a, const i
     P.segment = W.segment;
     P.slots = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + W.slots);
     P.totals = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + W.totals);
+    P.owners = reinterpret_cast<int32_t *>(static_cast<uint8_t *>(workspace) + W.owners);
     P.k_panels = (P.L.dk + 63) / 64;
     P.v_panels = (P.L.dv + 63) / 64;
     const bool bf16 = P.L.bf16, whole_k = P.L.dk % 64 == 0, whole_v = P.L.dv % 64 == 0;
@@ -1651,7 +1680,7 @@ extern "C" int lmc_linear_scan(const lmc_layout *L, const lmc_linear *a, const i
     P.k_copies = whole_k ? 1 : P.k_panels;
     P.v_copies = whole_v ? 1 : P.v_panels;
     const int64_t H = a->num_heads, K = a->num_key_heads;
-    const int64_t cuts = num_rows / W.segment;
+    const int64_t cuts = P.cuts = num_rows / W.segment;
     const int64_t grid = (cuts + a->num_requests) * H, states = cuts * H;
     if (grid > INT32_MAX)
         return LMC_ERR_OVERFLOW;
