@@ -240,7 +240,7 @@ struct ScanPlan {
     LinearPlan L;
     int64_t segment;     // a request of n of these tokens (n >= 2) is cut into n segments
     float *slots;        // [num_rows / segment][H][dk][dv]: the states before segments
-    float *totals;       // [num_rows / segment][H]: the decay over the segment before
+    float2 *totals;      // [num_rows / segment][H]: the decay over the segment before, in units of log 2 (high, low)
     int32_t *owners;     // [cuts]: the request whose segment the states pass made, -1: none
     int64_t cuts;        // num_rows / segment
     int32_t k_copies, v_copies, k_panels, v_panels;  // copies for all panels, panels
@@ -1153,7 +1153,9 @@ __device__ __forceinline__ void carry(const ScanPlan &P, ScanControl &C) {
         read(from);
     if (first)
         write(slot);
-    float total = 0.0f;  // log2 of the decay over the item
+    // log2 of the decay over the item, as two numbers: one would round the same way
+    // tile after tile (some 2^-25 of it each, under one decay for all tokens)
+    Twice total = {0.0f, 0.0f};
     if (!kStatesOnly && I.count > 0)
         hand_over(0);
     while (T.next()) {
@@ -1167,7 +1169,7 @@ __device__ __forceinline__ void carry(const ScanPlan &P, ScanControl &C) {
         scan_wait(C, &C.decays_full[n % kRing], (n / kRing) & 1, looks);
         const float grow = D.grow;
         if (kStatesOnly)
-            total += D.log[kTile - 1].x + D.log[kTile - 1].y;
+            total = plus(total, D.log[kTile - 1].x, D.log[kTile - 1].y);
         if (!kBf16)
             scan_wait(C, &C.unit_full[n % kRing], (n / kRing) & 1, looks);
         const float unit = kBf16 ? 1.0f : D.unit[j];
@@ -1207,7 +1209,7 @@ __device__ __forceinline__ void carry(const ScanPlan &P, ScanControl &C) {
     if (kStatesOnly) {
         write(slot + slot_size);
         if (threadIdx.x == 0)
-            P.totals[((int64_t)I.slot + 1) * L.H + I.h] = total;
+            P.totals[((int64_t)I.slot + 1) * L.H + I.h] = make_float2(total.high, total.low);
     }
 }
 
@@ -1469,11 +1471,16 @@ __global__ void __launch_bounds__(kJoinThreads) lmc_linear_join_kernel(const __g
     for (int i = 2; i < cuts; i++) {
         at += stride;
         const float4 u = __ldcg(at);
-        const float a = exp2f(__ldca(P.totals + (v + i) * L.H + h));
-        s.x = fmaf(a, s.x, u.x);
-        s.y = fmaf(a, s.y, u.y);
-        s.z = fmaf(a, s.z, u.z);
-        s.w = fmaf(a, s.w, u.w);
+        const float2 total = __ldca(P.totals + (v + i) * L.H + h);
+        // a slow decay as s + (decay - 1) s, as in a step
+        const bool slow = total.x > -0.7f && total.x < 0.7f;
+        const float a = slow ? expm1f((total.x + total.y) * 0.693147180559945309417f)
+                             : exp2f(total.x) * fmaf(total.y, 0.693147180559945309417f, 1.0f);
+        const float keep = slow ? 1.0f : 0.0f;
+        s.x = fmaf(keep, s.x, fmaf(a, s.x, u.x));
+        s.y = fmaf(keep, s.y, fmaf(a, s.y, u.y));
+        s.z = fmaf(keep, s.z, fmaf(a, s.z, u.z));
+        s.w = fmaf(keep, s.w, fmaf(a, s.w, u.w));
         __stcg(at, s);
     }
 }
@@ -1603,7 +1610,7 @@ ScanWork scan_work(int64_t rec_bytes, int64_t H, int64_t num_rows) {
     const int64_t n = std::min(num_rows / kLeastSegment, kSms / H);
     W.slots = 0;
     W.totals = (n * rec_bytes + 255) / 256 * 256;
-    W.owners = W.totals + n * H * 4;
+    W.owners = W.totals + n * H * 8;
     W.bytes = std::max<int64_t>(256, (W.owners + n * 4 + 255) / 256 * 256);
     return W;
 }
@@ -1669,7 +1676,7 @@ extern "C" int lmc_linear_scan(const lmc_layout *L, const lmc_linear *a, const i
     P.L.starts = starts;
     P.segment = W.segment;
     P.slots = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + W.slots);
-    P.totals = reinterpret_cast<float *>(static_cast<uint8_t *>(workspace) + W.totals);
+    P.totals = reinterpret_cast<float2 *>(static_cast<uint8_t *>(workspace) + W.totals);
     P.owners = reinterpret_cast<int32_t *>(static_cast<uint8_t *>(workspace) + W.owners);
     P.k_panels = (P.L.dk + 63) / 64;
     P.v_panels = (P.L.dv + 63) / 64;
