@@ -106,3 +106,76 @@ def test_a_cut_request_of_slow_decays():
         S = pool[at:at + rec].view(torch.float32).view(H, d, d)
         off = _off(S, _by_weights(k[:, 0], v, decay, (b + 1) * N))
         assert float(off.max()) <= ((b + 1) * N / 64) ** 0.5 * 2.0 ** -24, (b, int(off.argmax()), float(off.max()))
+
+
+@pytest.mark.parametrize("op", ["scan", "step"])
+def test_states_of_slow_decays(op):
+    """Thousands of decays near 1, the same for all tokens of a head, as prompts and
+    as steps. One rounding of the state a tile or step, as above; a decay rounded to
+    binary32 would make it sum to 2^-25 a time, the same way every time."""
+    H, d = 152, 8
+    n = 25600 if op == "scan" else 4096
+    N, rec = n, H * d * d * 4
+    L = lmc.lmc_layout_build([{"kind": "KDA", "conv_bytes": 16, "rec_bytes": rec}], N, False, 2 * (rec + 16))
+    g = torch.Generator(device=DEV).manual_seed(7)
+    q, k = ((1 + torch.randn(n, 1, d, generator=g, device=DEV)).bfloat16() for _ in range(2))
+    v = torch.randn(n, H, d, generator=g, device=DEV, dtype=torch.bfloat16) + 1
+    decay = -2.0 ** torch.linspace(-15, -13, H) if op == "scan" else -2.0 ** torch.linspace(-13, -11, H)
+    far = decay.cuda()[None].expand(n, H)
+    pool, out, status = torch.zeros(L.pool_bytes, dtype=torch.uint8, device=DEV), torch.empty_like(v), flag()
+    if op == "scan":
+        ws = torch.empty(lmc.lmc_linear_scan_workspace(L, 0, 1, n, H), dtype=torch.uint8, device=DEV)
+        lmc.lmc_linear_scan(L, 0, pool, ints([[1]]), ints([0, n]), ints([0]), q, k, v, far, out, ws, status, scale=1e-4)
+    else:
+        lengths, table = torch.arange(n, dtype=torch.int32, device=DEV), ints([[1]])
+        for t in range(n):
+            s = slice(t, t + 1)
+            lmc.lmc_linear_step(L, 0, pool, table, lengths[s], q[s], k[s], v[s], far[s], out[s], status, scale=1e-4)
+    torch.cuda.synchronize()
+    assert int(status.item()) == 0
+    at = L.base[0] + L.stride[0] + 16
+    S = pool[at:at + rec].view(torch.float32).view(H, d, d)
+    off = _off(S, _by_weights(k[:, 0], v, decay, n))
+    assert float(off.max()) <= (n / 64 if op == "scan" else n) ** 0.5 * 2.0 ** -24, (int(off.argmax()), float(off.max()))
+
+
+@pytest.mark.parametrize("op", ["scan", "step"])
+@pytest.mark.parametrize("act", ["bf16", "f16"])
+@pytest.mark.parametrize("decay", ["token", "head", "resets"])
+@pytest.mark.parametrize("dims", [(64, 64), (128, 128), (24, 40)])
+def test_states_keep_binary32s_digits(dims, decay, act, op):
+    """One to three tiles behind a state, and a step.
+
+    A step's product, decay and sums are off by a few 2^-24, not alike: below 2^-21 of
+    the state in the 2-norm. A tile's products of 16 tokens are added up part by part,
+    4 times 4 in bf16 and 2 times 4 in f16, and the tensor cores cut each sum off below
+    binary32's last place, by up to 2^-23 of it, half of that on average, all of them
+    the same way: 16 or 8 times 2^-24, 2^-20 or 2^-21. (Three bf16 parts of a value
+    times its decay would be off by 2^-18.7.)"""
+    H, N = 3, 200
+    had, new = ([0, 30, 7, 190], [64, 170, 1, 10]) if op == "scan" else ([0, 30, 7, 190], [1, 1, 1, 1])
+    P = R.States(lmc, H, *dims, N, 6)
+    table = R.tables(had, new, N, 6, np.random.default_rng(0))
+    g = torch.Generator().manual_seed(3)
+    for r, h in enumerate(had):
+        if h:
+            P.pages()[int(table[r, (h - 1) // N])] = torch.randn(H, *dims, generator=g)
+    rows = sum(new)
+    q, k, v, dec, _ = G.inputs(rows, H, H, *dims, act, decay, 4)
+    start = np.concatenate([[0], np.cumsum(new)]).astype(np.int32)
+    pool, out, status = P.pool.cuda(), torch.zeros(rows, H, dims[1], dtype=R.TYPES[act], device=DEV), flag()
+    a = [x.cuda() for x in (q, k, v)] + [dec.contiguous().cuda()]
+    if op == "scan":
+        lmc.lmc_linear_scan(P.layout, P.layer, pool, table.cuda(), ints(start.tolist()), ints(had), *a, out,
+                            workspace(P, len(new), rows)[0], status, scale=0.1)
+    else:
+        lmc.lmc_linear_step(P.layout, P.layer, pool, table.cuda(), ints(had), *a, out, status, scale=0.1)
+    torch.cuda.synchronize()
+    assert int(status.item()) == 0
+    got = P.pages(pool.cpu())
+    for r, (h, t) in enumerate(zip(had, new)):
+        s = slice(int(start[r]), int(start[r]) + t)
+        S0 = P.pages()[int(table[r, (h - 1) // N])].double() if h else torch.zeros(H, *dims, dtype=torch.float64)
+        _, _, kept = R.linear(S0, q[s], k[s], v[s], dec[s], 0.1, (t,))
+        off = _off(got[int(table[r, (h + t - 1) // N])], kept[t][0])
+        assert float(off.max()) <= 2.0 ** (-20 if act == "bf16" and op == "scan" else -21), (r, off.tolist())
