@@ -698,7 +698,9 @@ LMC_API int lmc_linear_step(const lmc_layout *layout, const lmc_linear *linear, 
  * 16-bit parts as keep its digits (BF16: four; F16: two, off by 2^-22 of
  * themselves or 2^-38 of the largest of a chunk's tokens). For the result two factors are rounded to the
  * type once, half a step each as the result is: the state before a chunk, and the
- * weights inside it, (q_t . k_j) * exp(sum of decays). A token whose values or
+ * weights inside it, (q_t . k_j) * exp(sum of decays). (F16, which has not
+ * binary32's range: numbers below 2^-20 of a token's largest weight, or 2^-28 of the
+ * largest of a value's state, are off by up to 2^-31 or 2^-39 of that one.) A token whose values or
  * decay are not finite may make NaN of the results of up to 63 tokens before it
  * in its request's block, of the same head (a key head's: of all its heads);
  * other requests are not touched.

@@ -464,6 +464,7 @@ __device__ __forceinline__ float2 from_halves(uint32_t x) {
     return __half22float2(*reinterpret_cast<const __half2 *>(&x));
 }
 __device__ __forceinline__ float power(int e) { return __uint_as_float((uint32_t)(127 + e) << 23); }
+__device__ __forceinline__ float inverse_power(float p) { return __uint_as_float((254u << 23) - __float_as_uint(p)); }
 __device__ __forceinline__ int lift_of(float x) {
     const int e = (int)(__float_as_uint(x) >> 23 & 255u) - 127;  // x >= 0
     return x == 0.0f ? 0 : max(-112, min(126, 14 - e));
@@ -988,10 +989,11 @@ __device__ __forceinline__ void weigh(const ScanPlan &P, ScanControl &C, uint8_t
             }
         };
         float ua = 1.0f, ub = 1.0f;
+        bool some_a = false, some_b = false;  // f16: a product is not 0
         if constexpr (!kBf16) {
             // f16 has not binary32's range: a row's weights are brought below 2^15, by
-            // the largest of its products (decays are at most 1; a weight keeps f16's
-            // steps down to 2^-28 of that one)
+            // the largest of its products (decays are at most 1), which is far from the
+            // largest weight where that product's token has been forgotten: see below
             float ta = 0.0f, tb = 0.0f;
 #pragma unroll 1
             for (int u = 0; u <= quarter; u++) {
@@ -1015,23 +1017,50 @@ __device__ __forceinline__ void weigh(const ScanPlan &P, ScanControl &C, uint8_t
             const int ea = lift_of(ta * unit), eb = lift_of(tb * unit);
             ua = power(ea);
             ub = power(eb);
-            if ((lane & 3) == 0) {
-                D.lift[ra] = power(-ea);
-                D.lift[rb] = power(-eb);
-            }
+            some_a = ta != 0.0f;
+            some_b = tb != 0.0f;
         }
         if (n >= 1)
             scan_wait(C, &C.weight_free, (n - 1) & 1, looks);
+        float wa = 0.0f, wb = 0.0f;  // f16: the largest of this thread's weights
+        for (bool again = false;; again = true) {
 #pragma unroll 1
-        for (int u = 0; u <= quarter; u++) {
-            float p[2][4];
-            make(u, p);
+            for (int u = 0; u <= quarter; u++) {
+                float p[2][4];
+                make(u, p);
 #pragma unroll
-            for (int i = 0; i < 2; i++) {
-                const int at = ((2 * u + i) ^ (ra & 7)) << 4;  // rb & 7 is the same
-                *reinterpret_cast<uint32_t *>(pa + at) = pack<kBf16>(p[i][0] * ua, p[i][1] * ua);
-                *reinterpret_cast<uint32_t *>(pb + at) = pack<kBf16>(p[i][2] * ub, p[i][3] * ub);
+                for (int i = 0; i < 2; i++) {
+                    const int at = ((2 * u + i) ^ (ra & 7)) << 4;  // rb & 7 is the same
+                    *reinterpret_cast<uint32_t *>(pa + at) = pack<kBf16>(p[i][0] * ua, p[i][1] * ua);
+                    *reinterpret_cast<uint32_t *>(pb + at) = pack<kBf16>(p[i][2] * ub, p[i][3] * ub);
+                    if (!kBf16) {
+                        wa = greatest(wa, p[i][0], p[i][1]);
+                        wb = greatest(wb, p[i][2], p[i][3]);
+                    }
+                }
             }
+            if (kBf16 || again)
+                break;
+            // Rows whose largest weight was brought below 2^6 are made again, by that
+            // one: a weight keeps f16's steps down to 2^-20 of its row's largest. (A
+            // row's four lanes hold a quarter of its weights each. Looking costs 2 to 4 %
+            // of the call; finding the largest weight first 9 %.)
+            uint32_t fine = __ballot_sync(0xffffffffu, wa * ua >= 64.0f || !some_a || ra >= T.rows);
+            uint32_t both = __ballot_sync(0xffffffffu, wb * ub >= 64.0f || !some_b || rb >= T.rows);
+            fine |= fine >> 1, both |= both >> 1;
+            fine |= fine >> 2, both |= both >> 2;
+            if ((fine & both & 0x11111111u) == 0x11111111u)
+                break;
+            for (int o = 1; o < 4; o <<= 1) {
+                wa = fmaxf(wa, __shfl_xor_sync(0xffffffffu, wa, o));
+                wb = fmaxf(wb, __shfl_xor_sync(0xffffffffu, wb, o));
+            }
+            ua = power(lift_of(wa));
+            ub = power(lift_of(wb));
+        }
+        if (!kBf16 && (lane & 3) == 0) {
+            D.lift[ra] = inverse_power(ua);
+            D.lift[rb] = inverse_power(ub);
         }
         if (__builtin_expect(held || twice, false) && quarter < 2) {
 #pragma unroll 1

@@ -179,3 +179,28 @@ def test_states_keep_binary32s_digits(dims, decay, act, op):
         _, _, kept = R.linear(S0, q[s], k[s], v[s], dec[s], 0.1, (t,))
         off = _off(got[int(table[r, (h + t - 1) // N])], kept[t][0])
         assert float(off.max()) <= 2.0 ** (-20 if act == "bf16" and op == "scan" else -21), (r, off.tolist())
+
+
+# ---- f16 -----------------------------------------------------------------------------
+
+@pytest.mark.parametrize("n", [20, 64, 200])
+@pytest.mark.parametrize("forgotten", [-float("inf"), -60.0])
+def test_f16_weights_beside_a_forgotten_tokens(n, forgotten):
+    """A first token whose product with every query is 2^32 times the others', and is
+    forgotten by the second: the others' weights keep f16's digits. As many independent
+    roundings of half a step: their 2-norm stays below one."""
+    H, d, N = 2, 64, 256
+    q, k, v, dec, _ = G.inputs(n, H, H, d, d, "f16", "token", 12)
+    q, k = q * 16, (k.float() * 2.0 ** -16).half()  # (k: randn / 8)
+    k[0] = (torch.randn(H, d, generator=torch.Generator().manual_seed(1)) * 2.0 ** 13).half()
+    v[0] = (v[0].float() * 2.0 ** -22).half()
+    dec[1] = forgotten
+    P = R.States(lmc, H, d, d, N, 2)
+    pool, out, status = P.pool.cuda(), torch.full((n, H, d), float("nan"), dtype=torch.float16, device=DEV), flag()
+    lmc.lmc_linear_scan(P.layout, P.layer, pool, ints([[1]]), ints([0, n]), ints([0]), *[x.cuda() for x in (q, k, v, dec)],
+                        out, workspace(P, 1, n)[0], status, scale=2.0 ** 12)
+    torch.cuda.synchronize()
+    assert int(status.item()) == 0
+    o, _, _ = R.linear(torch.zeros(H, d, d, dtype=torch.float64), q, k, v, dec, 2.0 ** 12)
+    assert 1e-2 < float(o[1:].abs().mean()) and float(o.abs().max()) < 65504
+    assert float((out.cpu().double() - o)[1:].norm()) <= R.HALF_STEP["f16"] * float(o[1:].norm())
