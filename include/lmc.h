@@ -580,8 +580,9 @@ LMC_API int lmc_move_tokens(const lmc_layout *layout, int32_t kv_group, void *po
  *   (a, b) -> mscale * (a cos t - b sin t, a sin t + b cos t),
  *   t = position * frequencies[i] for pair i.
  * The two ranges may overlap; values in neither stay as they are. All of it is
- * done in binary32 and rounded once, to the result's type; t is reduced exactly
- * (a whole number of 2^-64 turns per position), so far positions lose nothing.
+ * done in binary32 and rounded once, to the result's type. Before that t is reduced
+ * to less than a turn, in whole numbers of 2^-64 turns per position, and is off by
+ * at most 2^-31 turns (3e-9) whatever the position and the frequency.
  * A head's sum of squares is taken in binary32: values whose squares overflow
  * it are outside the norm's domain. */
 typedef struct {

@@ -4,7 +4,7 @@
 // Mathematics. y = x / sqrt(mean(x^2) + eps) * w on a head's first values, then
 // pairs turned by t = position * frequency. The angle is kept as a whole number
 // of 2^-64 turns: a step F = frequency * 2^64 / (2 pi), from the frequency's
-// significand times a 64-bit constant, times the position modulo 2^64. Its upper
+// significand times a 128-bit constant, times the position modulo 2^64. Its upper
 // 32 bits are the angle to 2^-32 turns however far the position is, without
 // 64-bit floating point (which this GPU is slow at).
 //
@@ -73,22 +73,28 @@ struct RotatePlan {
     float eps, mscale, inverse_norm_dim;
 };
 
-// frequency * 2^64 / (2 pi) modulo 2^64: the significand times 2^64 / (2 pi)
-// = 2935890503282001226.5, shifted by the exponent.
+// frequency * 2^64 / (2 pi), the nearest whole number modulo 2^64: the significand
+// times 2^128 / (2 pi), three words, shifted by the exponent. (Off by half, which 2^31
+// positions make 2^-34 turns.)
 __device__ __forceinline__ uint64_t step_of(float frequency) {
     const uint32_t bits = __float_as_uint(frequency);
     const int exponent = (int)(bits >> 23 & 255u);
     const uint64_t m = (bits & 0x7fffffu) | (exponent > 0 ? 0x800000u : 0u);
-    const uint64_t c = 2935890503282001226ull;
+    const uint64_t c1 = 2935890503282001226ull, c0 = 9154082963658192752ull;
     const int down = 150 - max(exponent, 1);  // frequency = m * 2^-down
-    const uint64_t lo = m * c, hi = __umul64hi(m, c);
+    const uint64_t w0 = m * c0, carried = __umul64hi(m, c0), w1 = m * c1 + carried;
+    const uint64_t w2 = __umul64hi(m, c1) + (w1 < carried);
     uint64_t f = 0;
-    if (down <= 0)
-        f = down > -64 ? lo << -down : 0;
+    if (down < 0)
+        f = down > -64 ? w1 << -down | w0 >> (64 + down) : 0;
+    else if (down == 0)
+        f = w1 + (w0 >> 63);
     else if (down < 64)
-        f = lo >> down | hi << (64 - down);
+        f = (w1 >> down | w2 << (64 - down)) + (w1 >> (down - 1) & 1);
+    else if (down == 64)
+        f = w2 + (w1 >> 63);
     else if (down < 128)
-        f = hi >> (down - 64);
+        f = (w2 >> (down - 64)) + (w2 >> (down - 65) & 1);
     return bits >> 31 ? 0 - f : f;
 }
 
