@@ -36,7 +36,8 @@ constexpr int kMaxHeadDim = 4096;
 constexpr int kManyCtas = 152 * 16;   // waves of CTAs enough to even out
 
 // Activations; a page's entries, as they are or as fp8 codes (kDivided: of a scale that
-// has no inverse to multiply by; such calls are rare and take the slower kernel).
+// has no inverse to multiply by, or too large a one; such calls are rare and take the
+// slower kernel).
 enum Result { kRows, kEntries, kCodes, kDivided };
 __host__ __device__ constexpr bool codes(Result to) { return to == kCodes || to == kDivided; }
 
@@ -833,6 +834,14 @@ int launch(RotatePlan &P, int width, cudaStream_t stream) {
     return follow(kern, dim3((unsigned)grid), kThreads, smem, stream, P) ? LMC_OK : LMC_ERR_CUDA;
 }
 
+// Whether 1 / scale fits into the factors that values are multiplied by anyway, mscale
+// and the norm's (at most 2^75, of a sum of squares that is not 0): an infinite factor
+// would make NaN of zeros.
+bool inverse_fits(const lmc_rotation *r, float inverse) {
+    const double norm = r->norm_dim > 0 ? std::min(1.0 / std::sqrt((double)r->eps), 0x1p75) : 0.0;
+    return inverse != 0.0f && (double)inverse * std::max(norm, std::fabs((double)r->mscale)) <= 0x1p127;
+}
+
 // Whether every piece of eight values lies on a multiple of its size.
 bool eights(const lmc_rotation *r, std::initializer_list<int64_t> bytes16) {
     int64_t all = (int64_t)(uintptr_t)r->norm_weight;
@@ -941,7 +950,7 @@ extern "C" int lmc_append_rotated(const lmc_layout *L, const lmc_entries *e, con
     plan_heads(P, r, width);
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     const bool bf16 = rows_dtype == LMC_E_BF16;
-    if (e->dtype == LMC_E_E4M3 && P.code_inverse == 0.0f)
+    if (e->dtype == LMC_E_E4M3 && !inverse_fits(r, P.code_inverse))
         return bf16 ? launch<__nv_bfloat162, kDivided>(P, width, s) : launch<__half2, kDivided>(P, width, s);
     if (e->dtype == LMC_E_E4M3)
         return bf16 ? launch<__nv_bfloat162, kCodes>(P, width, s) : launch<__half2, kCodes>(P, width, s);
