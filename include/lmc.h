@@ -644,7 +644,9 @@ LMC_API int lmc_append_rotated(const lmc_layout *layout, const lmc_entries *entr
  * that it completes and whose table entry is not -1 ([KL] snapshots at block
  * boundaries): what lmc_store moves. The page that was read is left as it was
  * unless it is also the one to be written. Pages that the requests of one call
- * write must differ from one another and from those that others read.
+ * write must differ from one another and from those that others read. A request's
+ * last page may stand at any of its positions (one page that rolls on): it is
+ * written once, last; other pages may not repeat among a request's positions.
  *
  * decay is a log, at most 0 (-inf forgets everything before the token). Values
  * below -1000 count as -1000, whose exponential is 0 in binary32. Sums, states and

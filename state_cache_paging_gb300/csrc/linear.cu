@@ -255,6 +255,7 @@ struct Item {
     int32_t count;       // tokens
     int32_t r, h;
     int32_t first;       // block of the state before them, -1: none
+    int32_t last;        // block of the state after the request's
     int32_t slot;        // of the segment; -1: the request is not cut
     int32_t ends;        // the request ends with it
     int32_t work;
@@ -542,6 +543,7 @@ __device__ __forceinline__ void find_item(const ScanPlan &P, Item &I) {
             J.phase = (int)((S.before + a) % P.L.block_size);
             J.count = (int)(b - a);
             J.first = S.first;
+            J.last = S.last;
             J.slot = n > 1 ? (int)(slot + i) : -1;
             J.ends = i == n - 1;
             J.work = 1;
@@ -1192,8 +1194,13 @@ __device__ __forceinline__ void carry(const ScanPlan &P, ScanControl &C) {
         const Decays &D = C.decays[n % kRing];
         // the block that is written to, asked for early
         int32_t block = -1;
-        if (!kStatesOnly && (T.block_ends || (I.ends && T.last())))
+        if (!kStatesOnly && (T.block_ends || (I.ends && T.last()))) {
             block = __ldca(L.table + I.r * L.row_stride + T.page);
+            // (a page that stands at several positions is written by the last one
+            // alone: segments do not take turns)
+            if (block == I.last && !(I.ends && T.last()))
+                block = -1;
+        }
 
         scan_wait(C, &C.decays_full[n % kRing], (n / kRing) & 1, looks);
         const float grow = D.grow;

@@ -63,6 +63,33 @@ def test_a_request_is_done_from_its_own_tokens_or_left_out(case):
             assert min(float((x - y).norm() / y.norm()) for y in o) <= 4 * half, i
 
 
+@pytest.mark.parametrize("n,N,H", [(6000, 144, 1), (5900, 64, 1), (6000, 16, 1), (4000, 100, 2), (8000, 200, 1), (900, 64, 2)])
+def test_one_page_at_every_position(n, N, H):
+    """Requests that keep one state each: the page is read and ends with the state after
+    the last token, whatever positions and segments lie between."""
+    d, had, new = 64, [70, 0, N], [n, 33, 0]
+    blocks = max(-(-(h + t) // N) for h, t in zip(had, new))
+    P = R.States(lmc, H, d, d, N, 4)
+    P.pages()[2] = torch.randn(H, d, d, generator=torch.Generator().manual_seed(2))
+    table = torch.tensor([[2], [0], [1]], dtype=torch.int32).expand(3, blocks).contiguous()
+    rows = sum(new)
+    q, k, v, dec, _ = G.inputs(rows, H, H, d, d, "bf16", "token", 14)
+    start = np.concatenate([[0], np.cumsum(new)]).astype(np.int32)
+    a = [x.cuda() for x in (q, k, v, dec)]
+    kept = [R.linear(P.pages()[2].double(), q[:n], k[:n], v[:n], dec[:n], 0.1, (n,))[2][n][0],
+            R.linear(torch.zeros(H, d, d, dtype=torch.float64), q[n:], k[n:], v[n:], dec[n:], 0.1, (33,))[2][33][0]]
+    for _ in range(20):
+        pool, out, status = P.pool.cuda(), torch.zeros(rows, H, d, dtype=torch.bfloat16, device=DEV), flag()
+        lmc.lmc_linear_scan(P.layout, P.layer, pool, table.cuda(), ints(start.tolist()), ints(had), *a, out,
+                            workspace(P, 3, rows)[0], status, scale=0.1)
+        torch.cuda.synchronize()
+        assert int(status.item()) == 0
+        got = P.pages(pool.cpu())
+        for b, S in ((2, kept[0]), (0, kept[1])):
+            assert float((got[b].double() - S).norm()) <= 2.0 ** -18 * float(S.norm()), b
+        assert bool(torch.isnan(got[[1, 3]]).all())
+
+
 # ---- digits of the states ------------------------------------------------------------
 
 def _by_weights(k, v, g, n):
