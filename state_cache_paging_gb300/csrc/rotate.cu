@@ -805,7 +805,7 @@ int launch(RotatePlan &P, int width, cudaStream_t stream) {
     P.rows_per_cta = (int32_t)rows;
     int64_t grid = (P.num_rows + rows - 1) / rows;
     if (grid > INT32_MAX)
-        return LMC_ERR_INVALID_ARG;
+        return kTo == kRows ? LMC_ERR_OVERFLOW : LMC_ERR_INVALID_ARG;  // (lmc_append's own)
     P.angle_rows = P.half > 0 ? kThreads / P.half : 0;
     P.angle_step = P.half > 0 ? kThreads % P.half : 0;
     P.row_step = at_once / P.units;
