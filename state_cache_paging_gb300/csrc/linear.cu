@@ -265,7 +265,7 @@ struct Item {
 // What a tile's tokens' decays give.
 struct alignas(16) Decays {
     float2 log[kTile];      // sum up to and with the token, in units of log 2 (high, low)
-    uint4 left[kTile / 2];  // from the token to the tile's end, two tokens: three bf16 parts, the first with a 0 behind it; or (f16) as it is
+    uint4 left[kTile / 2];  // from the token to the tile's end, two tokens: three bf16 parts f2, f3, f1 with a 0 behind it; or (f16) as it is
     float since[kTile];     // from the tile's start up to the token, times the call's scale
     float lift[kTile];      // f16: what the token's weights were divided by
     float unit[kMaxDim];    // f16: what a value's row of v times its decay was divided by
@@ -279,7 +279,7 @@ struct ScanControl {
     uint64_t unit_full[kRing], lift_full[2], down_full[2];  // f16
     uint64_t score_full, score_free;
     uint64_t weight_full, weight_free;
-    uint64_t parts_full[2], parts_free[2];  // the upper and the lower parts
+    uint64_t parts_full[2], parts_free[2];  // the lower and the upper parts
     uint64_t update_full[2], update_free[2];  // (one, but where only states are made)
     uint64_t state_full, state_free, out_full, out_free;
     uint64_t ended[2];
@@ -605,7 +605,7 @@ __device__ __forceinline__ void sum_decays(Decays &D, float g0, float g1, int ro
         const uint32_t p = pack<true>(f0, f1);
         const float r0 = f0 - from_q(p & 0xffff, true), r1 = f1 - from_q(p >> 16, true);
         const uint32_t q = pack<true>(r0, r1);
-        left = make_uint4(p, 0, q, pack<true>(r0 - from_q(q & 0xffff, true), r1 - from_q(q >> 16, true)));
+        left = make_uint4(q, pack<true>(r0 - from_q(q & 0xffff, true), r1 - from_q(q >> 16, true)), p, 0);
     } else {
         left = make_uint4(__float_as_uint(f0), __float_as_uint(f1), 0, 0);
     }
@@ -740,7 +740,8 @@ __device__ __forceinline__ void multiply_forward(const ScanPlan &P, ScanControl 
                         q + ((2 * kPanel >> 4) + (s >> 2) * (kPanel >> 4) + (s & 3) * 2), scores, s > 0);
             commit(&C.score_full);
         }
-        // as the parts come: the upper one or two, then the lower
+        // as the parts come: the lower one or two, then the upper. (A sum is cut off
+        // below its last place by each product: of the large part there are four.)
         const int b = kStatesOnly ? n & 1 : 0, use = kStatesOnly ? n >> 1 : n;
         const uint32_t to = tmem + (b ? kOtherUpdate : kUpdate);
         if (use >= 1)
@@ -838,14 +839,14 @@ __device__ __forceinline__ void split(const ScanPlan &P, ScanControl &C, uint8_t
             fence_async();
         }
         const uint32_t from = values + st * kStageBytes + ((chunk ^ (lane & 7)) << 4);
-        // Upper parts first: their products run while the lower are made, and the
-        // next tile's upper parts are made while the lower's run. (f16's two parts
-        // are made together, and go into one half each.)
+        // Lower parts first (the state is off by 1e-7, not 5e-7): their products run
+        // while the upper are made, and the next tile's lower parts are made while the
+        // upper's run. (f16's two parts are made together, and go into one half each.)
         if constexpr (kBf16) {
 #pragma unroll 1
-            for (int lower = 0; lower < 2; lower++) {
+            for (int upper = 0; upper < 2; upper++) {
                 if (n >= 1)
-                    scan_wait(C, &C.parts_free[lower], (n - 1) & 1, looks);
+                    scan_wait(C, &C.parts_free[upper], (n - 1) & 1, looks);
                 fence_after();
 #pragma unroll 1
                 for (int half = 0; half < 2; half++) {  // 32 tokens
@@ -858,18 +859,18 @@ __device__ __forceinline__ void split(const ScanPlan &P, ScanControl &C, uint8_t
                     // x = rn(v f) and y = v f - x + v g, g: f3, and 0 in the upper parts
 #pragma unroll
                     for (int k = 0; k < 8; k++) {
-                        const uint2 f = reinterpret_cast<const uint2 *>(&D.left[16 * half + 4 * (k >> 1) + (lane & 3)])[lower];
+                        const uint2 f = reinterpret_cast<const uint2 *>(&D.left[16 * half + 4 * (k >> 1) + (lane & 3)])[upper];
                         a[k] = times(v[k], f.x);
                         b[k] = plus_product(v[k], f.y, plus_product(v[k], f.x, minus(a[k])));
                     }
-                    store_part(to + 2 * kPartColumns * lower + 16 * half, a);
-                    store_part(to + 2 * kPartColumns * lower + kPartColumns + 16 * half, b);
+                    store_part(to + 2 * kPartColumns * upper + 16 * half, b);
+                    store_part(to + 2 * kPartColumns * upper + kPartColumns + 16 * half, a);
                 }
                 wait_st();
                 fence_before();
                 __syncwarp();
                 if (lane == 0)
-                    bar_arrive(&C.parts_full[lower]);
+                    bar_arrive(&C.parts_full[upper]);
             }
         } else {
             // two rounded parts of the product, whose row (a value's, of 64 tokens:
@@ -921,8 +922,8 @@ __device__ __forceinline__ void split(const ScanPlan &P, ScanControl &C, uint8_t
                     x = less(x, from_halves(a[k]));
                     b[k] = pack<false>(x.x, x.y);
                 }
-                store_part(to + 16 * half, a);
-                store_part(to + kPartColumns + 16 * half, b);
+                store_part(to + 16 * half, b);
+                store_part(to + kPartColumns + 16 * half, a);
             }
             wait_st();
             fence_before();
