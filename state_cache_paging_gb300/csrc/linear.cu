@@ -1473,9 +1473,11 @@ __global__ void __launch_bounds__(kScanThreads, 1) lmc_linear_scan_kernel(const 
 // i + 1 holds the state after segment 0 (i = 0), or what segment i adds, and
 // gets the state after it.
 constexpr int kJoinThreads = 256;
+static_assert(kJoinThreads >= kSms, "a thread for each segment of a request");
 
 __global__ void __launch_bounds__(kJoinThreads) lmc_linear_join_kernel(const __grid_constant__ ScanPlan P) {
     __shared__ int32_t first, cuts;
+    __shared__ float2 decays[kSms];  // of segments: (a, keep), the state before becomes keep s + a s
     const LinearPlan &L = P.L;
     const int parts = (L.dk * L.dv / 4 + kJoinThreads - 1) / kJoinThreads;
     const int part = blockIdx.x % parts, h = blockIdx.x / parts % L.H;
@@ -1498,8 +1500,18 @@ __global__ void __launch_bounds__(kJoinThreads) lmc_linear_join_kernel(const __g
         }
     }
     __syncthreads();
+    if (!first || cuts < 3)
+        return;
+    if ((int)threadIdx.x < cuts) {
+        const float2 total = __ldca(P.totals + (v + threadIdx.x) * L.H + h);
+        // a slow decay as s + (decay - 1) s, as in a step
+        const bool slow = total.x > -0.7f && total.x < 0.7f;
+        decays[threadIdx.x] = slow ? make_float2(expm1f((total.x + total.y) * 0.693147180559945309417f), 1.0f)
+                                   : make_float2(exp2f(total.x) * fmaf(total.y, 0.693147180559945309417f, 1.0f), 0.0f);
+    }
+    __syncthreads();
     const int e = part * kJoinThreads + threadIdx.x;
-    if (!first || cuts < 3 || e >= L.dk * L.dv / 4)
+    if (e >= L.dk * L.dv / 4)
         return;
     const int64_t stride = (int64_t)L.H * L.dk * L.dv / 4;
     float4 *at = reinterpret_cast<float4 *>(P.slots) + (v + 1) * stride + (int64_t)h * (L.dk * L.dv / 4) + e;
@@ -1508,12 +1520,7 @@ __global__ void __launch_bounds__(kJoinThreads) lmc_linear_join_kernel(const __g
     for (int i = 2; i < cuts; i++) {
         at += stride;
         const float4 u = __ldcg(at);
-        const float2 total = __ldca(P.totals + (v + i) * L.H + h);
-        // a slow decay as s + (decay - 1) s, as in a step
-        const bool slow = total.x > -0.7f && total.x < 0.7f;
-        const float a = slow ? expm1f((total.x + total.y) * 0.693147180559945309417f)
-                             : exp2f(total.x) * fmaf(total.y, 0.693147180559945309417f, 1.0f);
-        const float keep = slow ? 1.0f : 0.0f;
+        const float a = decays[i].x, keep = decays[i].y;
         s.x = fmaf(keep, s.x, fmaf(a, s.x, u.x));
         s.y = fmaf(keep, s.y, fmaf(a, s.y, u.y));
         s.z = fmaf(keep, s.z, fmaf(a, s.z, u.z));
