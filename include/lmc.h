@@ -579,7 +579,8 @@ LMC_API int lmc_move_tokens(const lmc_layout *layout, int32_t kv_group, void *po
  * and then rot_dim of its values, from rot_first on, are turned pair by pair,
  *   (a, b) -> mscale * (a cos t - b sin t, a sin t + b cos t),
  *   t = position * frequencies[i] for pair i.
- * The two ranges may overlap; values in neither stay as they are. All of it is
+ * The two ranges may overlap; values in neither stay as they are (a NaN stays one,
+ * perhaps of other bits). All of it is
  * done in binary32 and rounded once, to the result's type. Before that t is reduced
  * to less than a turn, in whole numbers of 2^-64 turns per position, and is off by
  * at most 2^-31 turns (3e-9) whatever the position and the frequency.
@@ -616,12 +617,13 @@ LMC_API int lmc_rotate(const lmc_rotation *rotation, int32_t dtype, const void *
  * status bits and errors, where a row's first num_heads * head_dim values (at
  * most entry_dim) are the heads of `rotation` and the others are taken as they
  * are. A latent entry is one head of entry_dim values (its first 512
- * normalised, its last 64 turned); an entry of keys and values is the keys'
+ * normalised, its last 64 turned, or none: rot_dim 0); an entry of keys and values is the keys'
  * heads with the values behind them. rotation->positions may be NULL: the angles
  * are then those of the cache positions; they are given apart where the two
  * differ (a cache that was cut to the tokens a request keeps). LMC_E_E4M3
  * entries: values that are neither normalised nor turned become the codes that
- * lmc_append makes; of the others 1 / scale, in binary32, is one more factor. */
+ * lmc_append makes; of the others 1 / scale, in binary32, is one more factor (a
+ * pair of values that it brings past binary32's range may become NaN). */
 LMC_API int lmc_append_rotated(const lmc_layout *layout, const lmc_entries *entries, const lmc_rotation *rotation,
                                void *pool, const int32_t *requests, const int32_t *positions, const void *rows,
                                int32_t rows_dtype, int64_t row_stride, int64_t num_rows, uint32_t *status,
@@ -629,12 +631,15 @@ LMC_API int lmc_append_rotated(const lmc_layout *layout, const lmc_entries *entr
 
 /* ---- linear attention over state pages ------------------------------------------- */
 
-/* The calls below compute with the states that a KDA layer's pages hold:
- * linear attention with a decay for each head. Head h of a request has a state
- * S of key_dim x value_dim binary32 numbers; token t changes it and reads it,
+/* Linear attention with one decay for each head, whose states lie in pages of the
+ * layout's state (KDA) layers. Head h of a request has a state S of key_dim x
+ * value_dim binary32 numbers; token t changes it and reads it,
  *   S_t = exp(decay[t][h]) S_(t-1) + k_t v_t^T,   out[t][h] = scale * S_t^T q_t,
  * S_(-1) = 0, where k_t and q_t are those of key head h / (num_heads /
- * num_key_heads). A page holds conv_bytes that these calls leave as they are,
+ * num_key_heads). (Kimi Delta Attention itself is another recurrence: it decays
+ * each key channel by a gate of its own and corrects the state by a delta rule.
+ * Its states are paged here like any, but these calls do not advance them.)
+ * A page holds conv_bytes that these calls leave as they are,
  * then the states [num_heads][key_dim][value_dim] (rec_bytes in all).
  *
  * Where states lie: the state after a request's first n tokens is held by the
@@ -648,12 +653,13 @@ LMC_API int lmc_append_rotated(const lmc_layout *layout, const lmc_entries *entr
  * last page may stand at any of its positions (one page that rolls on): it is
  * written once, last; other pages may not repeat among a request's positions.
  *
- * decay is a log, at most 0 (-inf forgets everything before the token). Values
- * below -1000 count as -1000, whose exponential is 0 in binary32. Sums, states and
- * products with them are binary32 (lmc_linear_scan's products run on the tensor
+ * decay is a log, at most 0 (-inf forgets everything finite before the token: 0
+ * times an infinity or NaN is NaN, and a state that holds an infinity may become
+ * NaN at any decay). Values below -1000 count as -1000, whose exponential is 0 in
+ * binary32. Sums, states and products with them are binary32 (lmc_linear_scan's products run on the tensor
  * cores; see there); the result is rounded once to `dtype`. */
 typedef struct {
-    int32_t layer;          /* a KDA layer of the layout */
+    int32_t layer;          /* a state (KDA) layer of the layout */
     int32_t dtype;          /* LMC_E_BF16 or LMC_E_F16: q, k, v and out */
     int32_t num_requests;   /* rows of the block table, at most 2^20 */
     int32_t num_heads;      /* states of a page, 1 .. 65535 */
@@ -698,12 +704,14 @@ LMC_API int lmc_linear_step(const lmc_layout *layout, const lmc_linear *linear, 
  *
  * Rounding: the tensor cores multiply 16-bit numbers of q's type, with binary32
  * sums. States are binary32, and what is added to them is multiplied in as many
- * 16-bit parts as keep its digits (BF16: four; F16: two, off by 2^-22 of
- * themselves or 2^-38 of the largest of a chunk's tokens). For the result two factors are rounded to the
- * type once, half a step each as the result is: the state before a chunk, and the
- * weights inside it, (q_t . k_j) * exp(sum of decays). (F16, which has not
- * binary32's range: numbers below 2^-20 of a token's largest weight, or 2^-28 of the
- * largest of a value's state, are off by up to 2^-31 or 2^-39 of that one.) A token whose values or
+ * 16-bit parts as keep its digits (BF16: four, of values times decays from 2^-100
+ * on; F16: two, off by 2^-22 of themselves or 2^-38 of the largest of a chunk's
+ * tokens); the tensor cores cut their sums off, 2^-22 of what a chunk adds at most
+ * in the mean. For the result two factors are rounded to the type once, half a
+ * step each as the result is: the state before a chunk, and the weights inside it,
+ * (q_t . k_j) * exp(sum of decays). (F16, which has not binary32's range: numbers
+ * below 2^-20 of a token's largest weight, or 2^-28 of the largest of a value's
+ * state, are off by up to 2^-31 or 2^-39 of that one.) A token whose values or
  * decay are not finite may make NaN of the results of up to 63 tokens before it
  * in its request's block, of the same head (a key head's: of all its heads);
  * other requests are not touched.

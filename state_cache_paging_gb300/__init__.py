@@ -881,7 +881,8 @@ def _linear(layout: Layout, layer: int, table, home: int, lengths, q, k, v, deca
 
 def lmc_linear_step(layout: Layout, layer: int, pool, table, lengths, q, k, v, decay, out, status, scale: float = 1.0,
                     stream=None) -> None:
-    """One token per request of linear attention over a KDA layer's states: q, k
+    """One token per request of linear attention with a decay for each head, whose
+    states lie in a state (KDA) layer's pages (not KDA's own recurrence): q, k
     [requests, key heads, key_dim], v, out [requests, heads, value_dim]
     (bfloat16 or float16), decay float32 [requests, heads] (logs, any strides,
     expanded ones too), lengths int32 [requests]: the tokens before (-1: the
@@ -908,8 +909,8 @@ def lmc_linear_scan_workspace(layout: Layout, layer: int, num_requests: int, num
 
 def lmc_linear_scan(layout: Layout, layer: int, pool, table, starts, lengths, q, k, v, decay, out, workspace, status,
                     scale: float = 1.0, stream=None) -> None:
-    """Linear attention of whole prompts (or of a step's share of them) over a
-    KDA layer's states: request r's tokens are rows starts[r] .. starts[r + 1]
+    """Linear attention of whole prompts (or of a step's share of them), states in
+    a state layer's pages: request r's tokens are rows starts[r] .. starts[r + 1]
     (int32 [requests + 1]) and follow the lengths[r] that its state has seen.
     Every block that is completed on the way leaves its snapshot in its page,
     where the table has one. Other arguments as for lmc_linear_step."""

@@ -1,5 +1,5 @@
-// linear.cu -- linear attention with a decay for each head over the states that
-// KDA layers' pages hold, for sm_103a: a token per request, and prompts.
+// linear.cu -- linear attention with a decay for each head, its states in the pages
+// of state layers, for sm_103a: a token per request, and prompts.
 //
 // Mathematics. S_t = exp(g_t) S_(t-1) + k_t v_t^T, out_t = scale S_t^T q_t. One
 // token: as it stands. Prompts: for a tile of up to 64 tokens and G_t = g_1 + .. +
@@ -13,7 +13,7 @@
 // 128 x 128 take 166 us, 96 % of the measured copy rate. Prompts are bound by the
 // instructions between the products: 32 requests of 8192 tokens of 32 heads in bf16
 // take 1670 us, 82 % of what reading q, k and v and writing the results takes at the
-// copy rate (in f16 some 58 %: binary32's range is brought into f16's row by row).
+// copy rate (in f16 some 55 %: binary32's range is brought into f16's row by row).
 // What brought it there from 3245 us: one role per kind of work (a warp waits for
 // nothing that it does not need), four exact bf16 parts of v instead of three truncated
 // ones, loops that stay in the instruction cache, two binary32 operations an
@@ -21,9 +21,10 @@
 //
 // Long requests are cut where there are fewer heads than SMs: a first pass finds what
 // each segment adds to the state (updates taking turns in two places of tensor memory:
-// 347 us become 339), a second one joins them, and the third makes the results of all
-// segments at once (131072 tokens of one request, 8 heads: 339 us, the first two passes
-// some 145 of them).
+// 347 us became 339), a second one joins them, and the third makes the results of all
+// segments at once (131072 tokens of one request, 8 heads: 344 us, the first two passes
+// some 145 of them). The first writes down whose segment it made in each place: a
+// request is continued only from places that are all its own.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>

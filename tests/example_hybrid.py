@@ -1,6 +1,7 @@
 """The hybrid model example shown in the README, as a module the tests run.
 
-A Kimi-Linear layout; one request's prompt passes a linear-attention layer and
+Pages of Kimi-Linear's sizes, whose state layers decay by the head here (KDA's own
+recurrence is another one); one request's prompt passes a linear-attention layer and
 an attention layer, three decode steps follow, and its first chunk is stored,
 loaded into a fresh pool and continued from there. run() returns the tensors a
 test checks.
@@ -18,7 +19,7 @@ def run(device="cuda"):
     N, prompt, steps, heads = 944, 1200, 3, 32
     total = prompt + steps
     L = lmc.lmc_layout_build([kda, kda, kda, mla] * 6, N, packed=False, mem_bytes=16 * 6 * 2170880)
-    state, latent = 0, 3                                              # a KDA layer, an MLA layer
+    state, latent = 0, 3                                              # a state layer, an MLA layer
     ints = lambda x: torch.tensor(x, dtype=torch.int32, device=device)  # noqa: E731
     draw = lambda *s: torch.randn(*s, device=device).bfloat16()         # noqa: E731
     pool = torch.zeros(L.pool_bytes, dtype=torch.uint8, device=device)
