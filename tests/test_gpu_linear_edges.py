@@ -232,3 +232,29 @@ def test_f16_weights_beside_a_forgotten_tokens(n, forgotten):
     o, _, _ = R.linear(torch.zeros(H, d, d, dtype=torch.float64), q, k, v, dec, 2.0 ** 12)
     assert 1e-2 < float(o[1:].abs().mean()) and float(o.abs().max()) < 65504
     assert float((out.cpu().double() - o)[1:].norm()) <= R.HALF_STEP["f16"] * float(o[1:].norm())
+
+
+@pytest.mark.parametrize("n", [1, 20, 37, 64])
+def test_f16_rows_of_other_requests_do_not_leak(n):
+    """NaN, infinities and the largest values in the next request's rows, which lie in the
+    same tile's boxes, change no bit of a request's results and states."""
+    H, d, N, new = 2, 64, 48, [n, 70, 41]
+    rows = sum(new)
+    q, k, v, dec, _ = G.inputs(rows, H, H, d, d, "f16", "resets", 2)
+    start, got = np.concatenate([[0], np.cumsum(new)]).astype(np.int32), []
+    for bad in (None, 65504.0, float("inf"), float("nan")):
+        if bad is not None:
+            for x in (q, k, v):
+                x[n:n + 70] = bad
+            dec[n:n + 70] = -1e30 if bad == 65504.0 else bad
+        P = R.States(lmc, H, d, d, N, 8)
+        pool, out, status = P.pool.cuda(), torch.zeros(rows, H, d, dtype=torch.float16, device=DEV), flag()
+        lmc.lmc_linear_scan(P.layout, P.layer, pool, ints([[0, 7, -1], [1, 2, 3], [4, 5, 6]]), ints(start.tolist()),
+                            ints([0, 0, 0]), *[x.cuda() for x in (q, k, v, dec)], out, workspace(P, 3, rows)[0], status, scale=0.1)
+        torch.cuda.synchronize()
+        assert int(status.item()) == 0
+        got.append((out.cpu(), P.pages(pool.cpu()).clone()))
+    for out, pages in got[1:]:
+        for s in (slice(0, n), slice(n + 70, rows)):
+            assert torch.equal(got[0][0][s], out[s])
+        assert torch.equal(got[0][1][[0, 4]], pages[[0, 4]])
